@@ -75,8 +75,11 @@ typedef enum attn_status {
     ATTN_ERR_TIMEOUT = 4,            /* a kernel's bounded wait expired (see attn_check_status) */
     ATTN_ERR_CUDA = 5,               /* another CUDA runtime/driver error */
     ATTN_ERR_SCRATCH_LIMIT = 6,      /* attn_fwd_splitkv_noalloc: problem exceeds its fixed scratch */
-    ATTN_ERR_BOUNDS = 7              /* bounds-checking build only: an index check failed and the
+    ATTN_ERR_BOUNDS = 7,             /* bounds-checking build only: an index check failed and the
                                         access was skipped (see attn_check_status) */
+    ATTN_ERR_TABLE = 8               /* a kernel read a block table or page list entry, a length or
+                                        a count out of range; what it stands for was skipped (see
+                                        attn_check_status) */
 } attn_status;
 
 typedef enum attn_dtype {
@@ -265,6 +268,145 @@ ATTN_API int attn_merge(const float *o_parts, const float *lse_parts, int n_part
                void *o, float *lse, int out_dtype, void *stream);
 
 /*
+ * Paged 8-bit key/value cache
+ * ---------------------------
+ * The cache a decode step reads: a pool of pages that the caller owns.  A page
+ * holds `page` consecutive tokens of one sequence, for every kv head, as 8-bit
+ * codes; each (page, kv head) block of keys and of values has one scale, and
+ * the value a code stands for is code * scale.  Not on the source pages; the
+ * attention over it is the operation above on those values, computed tile by
+ * tile (deepnotes "flash-attention-implemented-verified-and-measured",
+ * tiled_attention_online_softmax), with a partial state per key range joined
+ * as attn_merge does.
+ *
+ * Layout (all contiguous, device memory; codes and bounds 16-byte aligned):
+ *   k, v            [n_pages][H_kv][page][d], 1 byte each
+ *   k_scale, v_scale [n_pages][H_kv] fp32
+ *   k_bounds        [n_pages][H_kv][2][d], 1 byte each: the smallest and the
+ *                   largest key code of each channel.  May be NULL: then
+ *                   attn_cache_append keeps none and attn_cache_select refuses.
+ *   page in {16, 32, 64, 128}; d in {64, 128}; format one of attn_cache_format;
+ *   n_pages * H_kv * page / 16 < 2^31.
+ * Nothing in the pool needs to be initialised.
+ *
+ * Sequences  table [B][max_pages] int32 names the pages of each sequence in
+ *   order: token j is row j % page of page table[b][j / page].  lens [B] (pos
+ *   for append) is the number of tokens held; counts [B] (NULL: all rows) the
+ *   rows of this call that are the sequence's, the first ones of its S (Sq)
+ *   rows.  These arrays are device memory and only read, so a captured call
+ *   follows them.  Entries of a row behind its last page are not read.
+ *   A kernel that reads a needed page number outside 0 .. n_pages - 1, a
+ *   length outside 0 .. max_pages * page or a count outside 0 .. S skips what
+ *   it stands for (the length is clamped, the keys of a bad page count as
+ *   absent, append writes nothing of a sequence with a bad count) and
+ *   attn_check_status reports ATTN_ERR_TABLE.
+ *
+ * Scales  the smallest power of two s >= 2^-126 with amax <= top * s, amax the
+ *   block's largest magnitude and top = 448 (e4m3) or 127 (int8); 0 for
+ *   amax = 0.  Division by it is exact, so codes are x / s rounded once, to
+ *   nearest, ties to even.  A NaN or an infinity makes the scale of its block
+ *   NaN: everything read from that block and head is NaN until the page is
+ *   started again at its first row.  attn_cache_read and attn_fwd_cache take
+ *   any scale; pages that append continues must hold such powers of two.
+ */
+typedef enum attn_cache_format {
+    ATTN_CACHE_E4M3 = 0, /* 4-bit exponent, 3-bit mantissa, no infinities; largest 448 */
+    ATTN_CACHE_I8 = 1    /* -127 .. 127 */
+} attn_cache_format;
+
+typedef struct attn_cache {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    void *k_bounds;
+    int n_pages, H_kv, page, d, format;
+} attn_cache;
+
+/*
+ * attn_cache_append -- quantises counts[b] new tokens of each sequence behind
+ * the pos[b] it holds.
+ *
+ *   k, v   [B][H_kv][S][d] of dtype ATTN_F32, ATTN_BF16 or ATTN_F16
+ * A block that already holds rows of the sequence keeps them: its scale
+ * becomes the larger of its own and the new rows', and when that grows the
+ * older codes are rounded again under it.  pos[b] may lie before tokens
+ * written earlier (they are overwritten; scale and bounds of a page that is
+ * continued keep covering them).  Rows of a page behind the last new token are
+ * left as they were.  No page may be written for two sequences, or for one
+ * twice, in one call (its contents are then undefined).  One kernel.
+ */
+ATTN_API int attn_cache_append(const attn_cache *cache, const void *k, const void *v,
+                      const int32_t *table, int max_pages, const int32_t *pos,
+                      const int32_t *counts, int B, int S, int dtype, void *stream);
+
+/*
+ * attn_cache_read -- the first S tokens of each sequence as k, v
+ * [B][H_kv][S][d] of dtype ATTN_F32, ATTN_BF16 or ATTN_F16, for example for
+ * attn_fwd.  Rows from lens[b] on are zero.  Values beyond the type's range
+ * become its largest finite number.  One kernel.
+ */
+ATTN_API int attn_cache_read(const attn_cache *cache, const int32_t *table, int max_pages,
+                    const int32_t *lens, void *k, void *v, int B, int S, int dtype, void *stream);
+
+/*
+ * attn_cache_select -- the pages each query attends to: for query row i and
+ * kv head h, the page that holds the row's last visible key and the
+ * n_select - 1 others with the highest
+ *   score(p) = k_scale[p] * max over the query heads g of h of
+ *              sum_c max(q_gc * lo_pc, q_gc * hi_pc)
+ * (lo and hi from k_bounds), an upper bound of q . k over the page; equal
+ * scores go to the lower page, a NaN scores highest.
+ *
+ *   q      [B][H][Sq][d] of an attn_dtype's input type; H a multiple of H_kv,
+ *          at most 128 query heads per kv head
+ *   pages  [B][H_kv][Sq][n_select] int32: page indices within the sequence (0
+ *          its first page), ascending, then -1 where fewer are visible
+ *   causal, counts as attn_fwd_cache;  max_pages and n_select <= 28672
+ *   workspace  16-byte aligned scratch of attn_cache_select_workspace_size
+ *          bytes, not overlapping any other argument
+ * The choice is that of exact sums (fp64 decides where fp32 does not).
+ * Two kernels.
+ */
+ATTN_API int attn_cache_select_workspace_size(int B, int H_kv, int Sq, int max_pages, size_t *bytes);
+ATTN_API int attn_cache_select(const attn_cache *cache, const void *q, const int32_t *table,
+                      int max_pages, const int32_t *lens, const int32_t *counts, int32_t *pages,
+                      int n_select, int B, int H, int Sq, int causal, int dtype, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * attn_fwd_cache -- attention of Sq query rows per sequence over its tokens in
+ * the cache.
+ *
+ *   q, o   [B][H][Sq][d], lse [B][H][Sq] (NULL: not written), types as attn_fwd
+ *          (every attn_dtype); H a multiple of H_kv, query heads
+ *          h * H / H_kv .. of kv head h; B <= 4096; B * H * Sq < 2^31
+ *   counts the last counts[b] of the lens[b] tokens are the queries' own:
+ *          query i sits at position lens[b] - counts[b] + i.  Rows from
+ *          counts[b] on see no key.
+ *   causal key j is visible to query i iff j <= lens[b] - counts[b] + i (else
+ *          every held token is); a row that sees no key gets o = 0, lse = -inf
+ *   pages  NULL: all pages (n_select = 0).  Else [B][H_kv][Sq][n_select] with
+ *          n_select <= 28672: query
+ *          i of kv head h attends only to tokens of the listed pages (page
+ *          indices within the sequence, as attn_cache_select gives them; -1 is
+ *          skipped; a page listed twice counts twice).
+ *   workspace  16-byte aligned scratch of attn_fwd_cache_workspace_size bytes
+ *          (0 or n_select for its last argument), not overlapping any other
+ *          argument.  Calls that may overlap on the GPU, replays of graphs
+ *          among them, need workspaces of their own.
+ * Arithmetic: exact products of codes and q, fp32 sums; the weights keep 22
+ * bits, or 11 for a bf16 output with more than 8 query rows per kv head.
+ * Results do not depend on other sequences' contents, but the grouping of sums
+ * (not their terms) follows all lengths of the call.  Two kernels.
+ */
+ATTN_API int attn_fwd_cache_workspace_size(int B, int H, int H_kv, int Sq, int d, int dtype,
+                                  int n_select, size_t *bytes);
+ATTN_API int attn_fwd_cache(const attn_cache *cache, const void *q, void *o, float *lse,
+                   const int32_t *table, int max_pages, const int32_t *lens,
+                   const int32_t *counts, const int32_t *pages, int n_select, int B, int H,
+                   int Sq, int causal, float scale, int dtype, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
  * attn_check_status -- synchronises `stream`, then reads and clears the
  * library's device status word on the current device.  Returns
  * ATTN_ERR_BOUNDS if, in the bounds-checking build (libattn_checked.so,
@@ -272,8 +414,9 @@ ATTN_API int attn_merge(const float *o_parts, const float *lse_parts, int n_part
  * a global-memory index or TMA coordinate outside its buffer (the access was
  * skipped, so the output is incomplete); ATTN_ERR_TIMEOUT if any tensor-core
  * kernel since the last check gave up a bounded wait (its output is then
- * incomplete); ATTN_ERR_CUDA if the stream reports an error; ATTN_OK
- * otherwise.  The normal build never sets ATTN_ERR_BOUNDS.
+ * incomplete); ATTN_ERR_TABLE if a cache kernel read a page number, length
+ * or count out of range; ATTN_ERR_CUDA if the stream reports an error;
+ * ATTN_OK otherwise.  The normal build never sets ATTN_ERR_BOUNDS.
  */
 ATTN_API int attn_check_status(void *stream);
 

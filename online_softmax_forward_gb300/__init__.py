@@ -17,6 +17,7 @@ import os
 __all__ = [
     "ATTN_OK", "ATTN_ERR_INVALID_ARG", "ATTN_ERR_UNSUPPORTED_DEVICE", "ATTN_ERR_LAUNCH",
     "ATTN_ERR_TIMEOUT", "ATTN_ERR_CUDA", "ATTN_ERR_SCRATCH_LIMIT", "ATTN_ERR_BOUNDS",
+    "ATTN_ERR_TABLE", "ATTN_CACHE_E4M3", "ATTN_CACHE_I8",
     "NOALLOC_SCRATCH_BYTES",
     "ATTN_F32", "ATTN_BF16", "ATTN_F16", "ATTN_BF16_OUT_F32", "ATTN_F16_OUT_F32",
     "AttnError", "library_path", "load_library", "exported_symbols",
@@ -26,7 +27,10 @@ __all__ = [
     "attn_check_status", "attn_strerror", "attn_abi_version", "attn_test_set_hook",
     "attn_splitkv_workspace_size", "attn_splitkv_plan", "attn_fwd_splitkv", "attn_merge",
     "attn_fwd_splitkv_noalloc", "attn_shutdown",
+    "attn_cache_append", "attn_cache_read", "attn_cache_select_workspace_size",
+    "attn_cache_select", "attn_fwd_cache_workspace_size", "attn_fwd_cache",
     "attention", "attention_f32_blocked", "attention_splitkv", "merge", "dtype_code",
+    "KVCache", "cache_append", "cache_read", "cache_select", "attention_cache",
 ]
 
 ATTN_OK = 0
@@ -37,6 +41,7 @@ ATTN_ERR_TIMEOUT = 4
 ATTN_ERR_CUDA = 5
 ATTN_ERR_SCRATCH_LIMIT = 6
 ATTN_ERR_BOUNDS = 7  # the bounds-checking build (libattn_checked.so) only
+ATTN_ERR_TABLE = 8
 NOALLOC_SCRATCH_BYTES = 8 << 20  # the fixed scratch of attn_fwd_splitkv_noalloc
 
 ATTN_F32 = 0
@@ -44,6 +49,9 @@ ATTN_BF16 = 1
 ATTN_F16 = 2
 ATTN_BF16_OUT_F32 = 3
 ATTN_F16_OUT_F32 = 4
+
+ATTN_CACHE_E4M3 = 0
+ATTN_CACHE_I8 = 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -55,6 +63,15 @@ _checked_lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_Z = ctypes.c_size_t
+
+
+class _Cache(ctypes.Structure):  # attn_cache of include/attn.h
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("k_bounds", _P),
+                ("n_pages", _I), ("H_kv", _I), ("page", _I), ("d", _I), ("format", _I)]
+
+
+_C = ctypes.POINTER(_Cache)
 _SIGS = [
     ("attn_fwd", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     ("attn_validate", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I]),
@@ -72,6 +89,13 @@ _SIGS = [
     ("attn_fwd_splitkv_noalloc", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I,
                                       _P]),
     ("attn_shutdown", _I, []),
+    ("attn_cache_append", _I, [_C, _P, _P, _P, _I, _P, _P, _I, _I, _I, _P]),
+    ("attn_cache_read", _I, [_C, _P, _I, _P, _P, _P, _I, _I, _I, _P]),
+    ("attn_cache_select_workspace_size", _I, [_I, _I, _I, _I, ctypes.POINTER(_Z)]),
+    ("attn_cache_select", _I, [_C, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _Z, _P]),
+    ("attn_fwd_cache_workspace_size", _I, [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_Z)]),
+    ("attn_fwd_cache", _I, [_C, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _Z,
+                            _P]),
 ]
 _TEST_SIGS = [
     ("attn_fwd_f32_blocked", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P]),
@@ -244,6 +268,45 @@ def attn_merge(o_parts, lse_parts, n_parts, rows, d, o, lse, out_dtype, stream):
                                      lse, int(out_dtype), stream)
 
 
+def attn_cache_append(cache, k, v, table, max_pages, pos, counts, B, S, dtype, stream):
+    """``cache`` is a _Cache structure (KVCache.c)."""
+    return load_library().attn_cache_append(cache, k, v, table, max_pages, pos, counts, B, S,
+                                            dtype, stream)
+
+
+def attn_cache_read(cache, table, max_pages, lens, k, v, B, S, dtype, stream):
+    return load_library().attn_cache_read(cache, table, max_pages, lens, k, v, B, S, dtype, stream)
+
+
+def attn_cache_select_workspace_size(B, H_kv, Sq, max_pages):
+    """Returns (status, bytes)."""
+    n = _Z(0)
+    st = load_library().attn_cache_select_workspace_size(B, H_kv, Sq, max_pages, ctypes.byref(n))
+    return st, n.value
+
+
+def attn_cache_select(cache, q, table, max_pages, lens, counts, pages, n_select, B, H, Sq, causal,
+                      dtype, workspace, workspace_bytes, stream):
+    return load_library().attn_cache_select(cache, q, table, max_pages, lens, counts, pages,
+                                            n_select, B, H, Sq, int(causal), dtype, workspace,
+                                            int(workspace_bytes), stream)
+
+
+def attn_fwd_cache_workspace_size(B, H, H_kv, Sq, d, dtype, n_select=0):
+    """Returns (status, bytes)."""
+    n = _Z(0)
+    st = load_library().attn_fwd_cache_workspace_size(B, H, H_kv, Sq, d, dtype, n_select,
+                                                      ctypes.byref(n))
+    return st, n.value
+
+
+def attn_fwd_cache(cache, q, o, lse, table, max_pages, lens, counts, pages, n_select, B, H, Sq,
+                   causal, scale, dtype, workspace, workspace_bytes, stream):
+    return load_library().attn_fwd_cache(cache, q, o, lse, table, max_pages, lens, counts, pages,
+                                         n_select, B, H, Sq, int(causal), float(scale), dtype,
+                                         workspace, int(workspace_bytes), stream)
+
+
 # ------------------------------------------------------------------ torch helpers
 def dtype_code(in_dtype, out_dtype=None) -> int:
     """attn_dtype for torch input/output dtypes."""
@@ -413,4 +476,209 @@ def merge(o_parts, lse_parts, out_dtype=None, stream=None):
         st = attn_merge(o_parts.data_ptr(), lse_parts.data_ptr(), n, rows, d, out.data_ptr(),
                         lse.data_ptr(), code, _stream_handle(stream))
     _check(st, "attn_merge")
+    return out, lse
+
+
+# ------------------------------------------------------------------ paged 8-bit cache
+class KVCache:
+    """The pool of a paged 8-bit key/value cache (include/attn.h): five
+    contiguous CUDA tensors the caller owns,
+
+    ``k``, ``v`` [n_pages, H_kv, page, d] of torch.float8_e4m3fn or torch.int8,
+    ``k_scale``, ``v_scale`` [n_pages, H_kv] fp32 and, for ``cache_select``,
+    ``k_bounds`` [n_pages, H_kv, 2, d] of the codes' type.  The tensors may be
+    read at any time; nothing in them needs to be initialised."""
+
+    def __init__(self, k, v, k_scale, v_scale, k_bounds=None):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [n_pages, H_kv, page, d] of one dtype")
+        formats = {torch.float8_e4m3fn: ATTN_CACHE_E4M3, torch.int8: ATTN_CACHE_I8}
+        if k.dtype not in formats:
+            raise ValueError("codes must be float8_e4m3fn or int8, got %s" % k.dtype)
+        n, h, page, d = k.shape
+        if page not in (16, 32, 64, 128) or d not in (64, 128):
+            raise ValueError("page must be 16, 32, 64 or 128 and d 64 or 128, got %d and %d" % (page, d))
+        dev = _device_of(k, v)
+        for t, name in ((k, "k"), (v, "v")):
+            _check_out(t, (n, h, page, d), k.dtype, dev, name)
+        _check_out(k_scale, (n, h), torch.float32, dev, "k_scale")
+        _check_out(v_scale, (n, h), torch.float32, dev, "v_scale")
+        if k_bounds is not None:
+            _check_out(k_bounds, (n, h, 2, d), k.dtype, dev, "k_bounds")
+        self.k, self.v, self.k_scale, self.v_scale, self.k_bounds = k, v, k_scale, v_scale, k_bounds
+        self.n_pages, self.H_kv, self.page, self.d = n, h, page, d
+        self.device = k.device
+        self.c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                        k_bounds.data_ptr() if k_bounds is not None else None, n, h, page, d,
+                        formats[k.dtype])
+
+    @classmethod
+    def empty(cls, n_pages, H_kv, page, d, dtype=None, device="cuda", bounds=True):
+        """A pool allocated with torch; ``dtype`` float8_e4m3fn (default) or int8."""
+        import torch
+        dtype = torch.float8_e4m3fn if dtype is None else dtype
+        new = lambda *s, t=dtype: torch.empty(s, dtype=t, device=device)  # noqa: E731
+        return cls(new(n_pages, H_kv, page, d), new(n_pages, H_kv, page, d),
+                   new(n_pages, H_kv, t=torch.float32), new(n_pages, H_kv, t=torch.float32),
+                   new(n_pages, H_kv, 2, d) if bounds else None)
+
+
+def _sequence_args(cache, table, lens, counts, B):
+    """Checks the arrays of the call's sequences; returns (table width, counts pointer)."""
+    import torch
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("table must be [B, max_pages] with B = %d" % B)
+    dev = cache.device
+    for t, shape, name in ((table, table.shape, "table"), (lens, (B,), "lens"), (counts, (B,), "counts")):
+        if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
+                              or t.device != dev):
+            raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s"
+                             % (name, tuple(shape), dev))
+    return table.shape[1], counts.data_ptr() if counts is not None else None
+
+
+class _on:
+    """Makes the cache's device current for a call; nothing to do when it is."""
+
+    def __init__(self, device):
+        import torch
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _cache_rows(cache, k, v):
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must be [B, H_kv, S, d] of one dtype")
+    if k.shape[1] != cache.H_kv or k.shape[3] != cache.d:
+        raise ValueError("k has %d heads of width %d, the cache %d of %d"
+                         % (k.shape[1], k.shape[3], cache.H_kv, cache.d))
+    for t in (k, v):
+        if not t.is_contiguous() or t.device != cache.device:
+            raise ValueError("k and v must be contiguous tensors on %s" % cache.device)
+
+
+def cache_append(cache, k, v, table, pos, counts=None, stream=None):
+    """Quantises the first ``counts[b]`` (default: all S) rows of k, v
+    [B, H_kv, S, d] into the cache behind the ``pos[b]`` tokens sequence b
+    holds.  ``table`` [B, max_pages], ``pos`` and ``counts`` [B] are int32 CUDA
+    tensors, read on the device."""
+    _cache_rows(cache, k, v)
+    B, _, S, _ = k.shape
+    width, cnt = _sequence_args(cache, table, pos, counts, B)
+    code = dtype_code(k.dtype)
+    with _on(cache.device):
+        st = load_library().attn_cache_append(cache.c, k.data_ptr(), v.data_ptr(), table.data_ptr(),
+                                              width, pos.data_ptr(), cnt, B, S, code,
+                                              _stream_handle(stream))
+    _check(st, "attn_cache_append")
+
+
+def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
+    """The first S tokens of each sequence as (k, v) [B, H_kv, S, d] of
+    ``dtype`` (fp32, bf16 or fp16; default bf16); rows from lens[b] on are
+    zero.  ``out`` is a pair of tensors to write instead of new ones."""
+    import torch
+    B = table.shape[0]
+    width, _ = _sequence_args(cache, table, lens, None, B)
+    dtype = torch.bfloat16 if dtype is None else dtype
+    code = dtype_code(dtype)
+    shape = (B, cache.H_kv, S, cache.d)
+    if out is None:
+        out = (torch.empty(shape, dtype=dtype, device=cache.device),
+               torch.empty(shape, dtype=dtype, device=cache.device))
+    else:
+        for t, name in zip(out, ("out[0]", "out[1]")):
+            _check_out(t, shape, dtype, cache.device, name)
+    k, v = out
+    with _on(cache.device):
+        st = load_library().attn_cache_read(cache.c, table.data_ptr(), width, lens.data_ptr(),
+                                            k.data_ptr(), v.data_ptr(), B, S, code,
+                                            _stream_handle(stream))
+    _check(st, "attn_cache_read")
+    return k, v
+
+
+def _cache_q(cache, q):
+    if q.dim() != 4 or q.shape[3] != cache.d or q.shape[1] % cache.H_kv != 0 or q.shape[1] == 0:
+        raise ValueError("q must be [B, H, Sq, %d] with H a multiple of %d, got %s"
+                         % (cache.d, cache.H_kv, tuple(q.shape)))
+    if not q.is_contiguous() or q.device != cache.device:
+        raise ValueError("q must be a contiguous tensor on %s" % cache.device)
+
+
+def _workspace(workspace, need, device):
+    import torch
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if not workspace.is_contiguous() or _device_of(workspace) != device:
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return workspace
+
+
+def cache_select(q, cache, table, lens, n_select, counts=None, causal: bool = True, workspace=None,
+                 stream=None):
+    """The ``n_select`` pages each query attends to (attn_cache_select): int32
+    [B, H_kv, Sq, n_select], ascending, -1 where fewer are visible."""
+    import torch
+    _cache_q(cache, q)
+    if cache.k_bounds is None:
+        raise ValueError("the cache keeps no k_bounds")
+    B, H, Sq, _ = q.shape
+    width, cnt = _sequence_args(cache, table, lens, counts, B)
+    code = dtype_code(q.dtype)
+    st, need = attn_cache_select_workspace_size(B, cache.H_kv, Sq, width)
+    _check(st, "attn_cache_select_workspace_size")
+    workspace = _workspace(workspace, need, cache.device)
+    if n_select < 1:
+        raise ValueError("n_select must be at least 1, got %d" % n_select)
+    pages = torch.empty((B, cache.H_kv, Sq, n_select), dtype=torch.int32, device=cache.device)
+    with _on(cache.device):
+        st = load_library().attn_cache_select(
+            cache.c, q.data_ptr(), table.data_ptr(), width, lens.data_ptr(), cnt, pages.data_ptr(),
+            n_select, B, H, Sq, int(causal), code, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check(st, "attn_cache_select")
+    return pages
+
+
+def attention_cache(q, cache, table, lens, counts=None, causal: bool = True,
+                    scale: float | None = None, out_dtype=None, pages=None, workspace=None,
+                    stream=None):
+    """Attention of q [B, H, Sq, d] over the cached tokens of each sequence, or
+    over the pages of ``pages`` [B, H_kv, Sq, n] (``cache_select``).  The last
+    ``counts[b]`` (default Sq) of the ``lens[b]`` tokens are the queries' own.
+    The workspace is allocated here unless given.  Returns (o, lse)."""
+    import torch
+    _cache_q(cache, q)
+    B, H, Sq, d = q.shape
+    width, cnt = _sequence_args(cache, table, lens, counts, B)
+    code = dtype_code(q.dtype, out_dtype)
+    n = 0
+    if pages is not None:
+        n = pages.shape[-1]
+        if (tuple(pages.shape) != (B, cache.H_kv, Sq, n) or n < 1 or pages.dtype != torch.int32
+                or not pages.is_contiguous() or pages.device != cache.device):
+            raise ValueError("pages must be a contiguous int32 tensor [%d, %d, %d, n] on %s"
+                             % (B, cache.H_kv, Sq, cache.device))
+    st, need = attn_fwd_cache_workspace_size(B, H, cache.H_kv, Sq, d, code, n)
+    _check(st, "attn_fwd_cache_workspace_size")
+    workspace = _workspace(workspace, need, cache.device)
+    out = torch.empty((B, H, Sq, d), dtype=q.dtype if out_dtype is None else out_dtype,
+                      device=cache.device)
+    lse = torch.empty((B, H, Sq), dtype=torch.float32, device=cache.device)
+    with _on(cache.device):
+        st = load_library().attn_fwd_cache(
+            cache.c, q.data_ptr(), out.data_ptr(), lse.data_ptr(), table.data_ptr(), width,
+            lens.data_ptr(), cnt, pages.data_ptr() if pages is not None else None, n, B, H, Sq,
+            int(causal), 0.0 if scale is None else float(scale), code, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check(st, "attn_fwd_cache")
     return out, lse

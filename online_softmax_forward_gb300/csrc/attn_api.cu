@@ -9,6 +9,7 @@
 
 #include "attn.h"
 #include "attn_internal.h"
+#include "cache_index.h"
 #ifdef ATTN_TEST_EXPORTS
 #include "attn_test.h"  // the test library's build of this file
 #endif
@@ -230,6 +231,46 @@ static int validate(const void *q, const void *k, const void *v, const void *o,
     return ATTN_OK;
 }
 
+// Host check of a cache descriptor.
+static bool cache_ok(const attn_cache *c) {
+    if (!c) return false;
+    if (c->format != ATTN_CACHE_E4M3 && c->format != ATTN_CACHE_I8) return false;
+    if (c->d != 64 && c->d != 128) return false;
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return false;
+    if (c->n_pages < 1 || c->H_kv < 1) return false;
+    // the kernels number the 16-token pieces of the pool in 31 bits
+    if ((double)c->n_pages * c->H_kv * (c->page / 16) > (double)INT32_MAX) return false;
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale) return false;
+    return aligned(c->k, 16) && aligned(c->v, 16) && aligned(c->k_bounds, 16) &&
+           aligned(c->k_scale, 4) && aligned(c->v_scale, 4);
+}
+static size_t cache_code_bytes(const attn_cache &c) {
+    return (size_t)c.n_pages * c.H_kv * c.page * c.d;
+}
+// Does [p, p + n) overlap any array of the cache?
+static bool cache_overlap(const attn_cache &c, const void *p, size_t n) {
+    const size_t blocks = (size_t)c.n_pages * c.H_kv;
+    return overlap(p, n, c.k, cache_code_bytes(c)) || overlap(p, n, c.v, cache_code_bytes(c)) ||
+           overlap(p, n, c.k_scale, blocks * 4) || overlap(p, n, c.v_scale, blocks * 4) ||
+           overlap(p, n, c.k_bounds, blocks * 2 * c.d);
+}
+// The arrays of one call's sequences: table and lens (or pos), counts may be null.
+static bool sequences_ok(const int32_t *table, int max_pages, const int32_t *lens,
+                         const int32_t *counts, int B) {
+    if (B < 0 || max_pages < 1) return false;
+    if (B == 0) return true;
+    return table && lens && aligned(table, 4) && aligned(lens, 4) && aligned(counts, 4);
+}
+static bool overlap_sequences(const void *p, size_t n, const int32_t *table, int max_pages,
+                              const int32_t *lens, const int32_t *counts, int B) {
+    return overlap(p, n, table, (size_t)B * max_pages * 4) || overlap(p, n, lens, (size_t)B * 4) ||
+           overlap(p, n, counts, (size_t)B * 4);
+}
+// attn_dtype of plain 32- and 16-bit tensors as the cache kernels number them, or -1
+static int plain_dtype(int dtype) {
+    return dtype == ATTN_F32 ? 0 : dtype == ATTN_BF16 ? 1 : dtype == ATTN_F16 ? 2 : -1;
+}
+
 // Bytes of the split-KV workspace: partial outputs [n][B*H][Sq][d] and
 // partial lse [n][B*H][Sq], fp32.  Returns false on overflow.
 static bool splitkv_bytes(int64_t bh, int Sq, int d, int n_splits, size_t *bytes) {
@@ -296,6 +337,7 @@ const char *attn_strerror(int status) {
     case ATTN_ERR_CUDA: return "CUDA error";
     case ATTN_ERR_SCRATCH_LIMIT: return "the problem needs more scratch than the fixed device array of attn_fwd_splitkv_noalloc holds";
     case ATTN_ERR_BOUNDS: return "bounds-checking build: a kernel computed an index outside its buffer (the access was skipped)";
+    case ATTN_ERR_TABLE: return "a kernel read a block table or page list entry, a length or a count out of range (what it stands for was skipped)";
     default: return "unknown status";
     }
 }
@@ -530,6 +572,133 @@ int attn_merge(const float *o_parts, const float *lse_parts, int n_parts, int64_
                         (cudaStream_t)stream);
 }
 
+int attn_cache_append(const attn_cache *cache, const void *k, const void *v, const int32_t *table,
+                      int max_pages, const int32_t *pos, const int32_t *counts, int B, int S,
+                      int dtype, void *stream) {
+    const int dt = plain_dtype(dtype);
+    if (!cache_ok(cache) || dt < 0 || S < 0 || !sequences_ok(table, max_pages, pos, counts, B))
+        return ATTN_ERR_INVALID_ARG;
+    if (B == 0 || S == 0) return ATTN_OK;
+    // one CTA per touched page, kv head and tensor
+    if ((double)B * cache->H_kv * touched_pages(S, cache->page) * 2 > (double)INT32_MAX)
+        return ATTN_ERR_INVALID_ARG;
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_INVALID_ARG;
+    const size_t n = (size_t)B * cache->H_kv * S * cache->d * (dt == 0 ? 4 : 2);
+    if (cache_overlap(*cache, k, n) || cache_overlap(*cache, v, n) ||
+        cache_overlap(*cache, table, (size_t)B * max_pages * 4) ||
+        cache_overlap(*cache, pos, (size_t)B * 4) || cache_overlap(*cache, counts, counts ? (size_t)B * 4 : 0))
+        return ATTN_ERR_INVALID_ARG;
+    const int st = check_device();
+    if (st != ATTN_OK) return st;
+    return launch_cache_append(*cache, k, v, table, max_pages, pos, counts, B, S, dt,
+                               (cudaStream_t)stream);
+}
+
+int attn_cache_read(const attn_cache *cache, const int32_t *table, int max_pages,
+                    const int32_t *lens, void *k, void *v, int B, int S, int dtype, void *stream) {
+    const int dt = plain_dtype(dtype);
+    if (!cache_ok(cache) || dt < 0 || S < 0 || !sequences_ok(table, max_pages, lens, nullptr, B))
+        return ATTN_ERR_INVALID_ARG;
+    if (B == 0 || S == 0) return ATTN_OK;
+    if ((double)B * cache->H_kv * (S / cache->page + 1.0) * 2 > (double)INT32_MAX)
+        return ATTN_ERR_INVALID_ARG;
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_INVALID_ARG;
+    const size_t n = (size_t)B * cache->H_kv * S * cache->d * (dt == 0 ? 4 : 2);
+    if (cache_overlap(*cache, k, n) || cache_overlap(*cache, v, n) || overlap(k, n, v, n) ||
+        overlap_sequences(k, n, table, max_pages, lens, nullptr, B) ||
+        overlap_sequences(v, n, table, max_pages, lens, nullptr, B))
+        return ATTN_ERR_INVALID_ARG;
+    const int st = check_device();
+    if (st != ATTN_OK) return st;
+    return launch_cache_read(*cache, table, max_pages, lens, k, v, B, S, dt, (cudaStream_t)stream);
+}
+
+int attn_cache_select_workspace_size(int B, int H_kv, int Sq, int max_pages, size_t *bytes) {
+    if (!bytes || B < 0 || H_kv < 1 || Sq < 0 || max_pages < 1 || max_pages > kMaxSelectPages)
+        return ATTN_ERR_INVALID_ARG;
+    const double est = (double)B * H_kv * Sq * (12.0 * max_pages + 4.0);
+    if (est > 9.0e18) return ATTN_ERR_INVALID_ARG;
+    *bytes = (size_t)B * H_kv * Sq * ((size_t)12 * max_pages + 4);
+    return ATTN_OK;
+}
+
+int attn_cache_select(const attn_cache *cache, const void *q, const int32_t *table, int max_pages,
+                      const int32_t *lens, const int32_t *counts, int32_t *pages, int n_select,
+                      int B, int H, int Sq, int causal, int dtype, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    if (!cache_ok(cache) || !cache->k_bounds || !dtype_known(dtype) || Sq < 0 || H < 1 ||
+        H % cache->H_kv != 0 || H / cache->H_kv > kMaxSelectGroup || n_select < 1 || n_select > kMaxSelectPages ||
+        (causal != 0 && causal != 1) || !sequences_ok(table, max_pages, lens, counts, B))
+        return ATTN_ERR_INVALID_ARG;
+    size_t need = 0;
+    if (attn_cache_select_workspace_size(B, cache->H_kv, Sq, max_pages, &need) != ATTN_OK)
+        return ATTN_ERR_INVALID_ARG;
+    if (B == 0 || Sq == 0) return ATTN_OK;
+    const int64_t units = (int64_t)B * cache->H_kv * Sq;
+    if (units > INT32_MAX) return ATTN_ERR_INVALID_ARG;
+    if (!q || !aligned(q, 16) || !pages || !aligned(pages, 4) || !workspace ||
+        !aligned(workspace, 16) || workspace_bytes < need)
+        return ATTN_ERR_INVALID_ARG;
+    const size_t qn = (size_t)units * (H / cache->H_kv) * cache->d * elem_bytes_in(dtype);
+    const size_t pn = (size_t)units * n_select * 4;
+    if (cache_overlap(*cache, pages, pn) || cache_overlap(*cache, workspace, need) ||
+        overlap(pages, pn, q, qn) || overlap(workspace, need, q, qn) ||
+        overlap(pages, pn, workspace, need) ||
+        overlap_sequences(pages, pn, table, max_pages, lens, counts, B) ||
+        overlap_sequences(workspace, need, table, max_pages, lens, counts, B))
+        return ATTN_ERR_INVALID_ARG;
+    const int st = check_device();
+    if (st != ATTN_OK) return st;
+    return launch_cache_select(*cache, q, table, max_pages, lens, counts, pages, n_select, B, H, Sq,
+                               causal, dtype, workspace, (cudaStream_t)stream);
+}
+
+int attn_fwd_cache_workspace_size(int B, int H, int H_kv, int Sq, int d, int dtype, int n_select,
+                                  size_t *bytes) {
+    if (!bytes || B < 0 || B > kMaxCacheBatch || H < 1 || H_kv < 1 || H % H_kv != 0 || Sq < 0 ||
+        (d != 64 && d != 128) || !dtype_known(dtype) || n_select < 0 || n_select > kMaxSelectPages ||
+        (double)(H / H_kv) * Sq > (double)INT32_MAX || (double)B * H * Sq > (double)INT32_MAX)
+        return ATTN_ERR_INVALID_ARG;
+    *bytes = cache_fwd_workspace(B, H, H_kv, Sq, d, dtype, n_select > 0);
+    return ATTN_OK;
+}
+
+int attn_fwd_cache(const attn_cache *cache, const void *q, void *o, float *lse,
+                   const int32_t *table, int max_pages, const int32_t *lens, const int32_t *counts,
+                   const int32_t *pages, int n_select, int B, int H, int Sq, int causal,
+                   float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!cache_ok(cache) || !sequences_ok(table, max_pages, lens, counts, B) ||
+        (causal != 0 && causal != 1) || (pages ? n_select < 1 : n_select != 0) || !aligned(pages, 4))
+        return ATTN_ERR_INVALID_ARG;
+    size_t need = 0;
+    if (attn_fwd_cache_workspace_size(B, H, cache->H_kv, Sq, cache->d, dtype, n_select, &need) != ATTN_OK)
+        return ATTN_ERR_INVALID_ARG;
+    float sc = 0.f;
+    if (resolve_scale(scale, cache->d, &sc) != ATTN_OK) return ATTN_ERR_INVALID_ARG;
+    if (B == 0 || Sq == 0) return ATTN_OK;
+    if (!q || !o || !aligned(q, 16) || !aligned(o, 16) || (lse && !aligned(lse, 4)) || !workspace ||
+        !aligned(workspace, 16) || workspace_bytes < need)
+        return ATTN_ERR_INVALID_ARG;
+    const size_t rows = (size_t)B * H * Sq;
+    const size_t qn = rows * cache->d * elem_bytes_in(dtype), on = rows * cache->d * elem_bytes_out(dtype);
+    const size_t ln = lse ? rows * 4 : 0;
+    const size_t pn = pages ? (size_t)B * cache->H_kv * Sq * n_select * 4 : 0;
+    const void *outs[3] = {o, lse, workspace};
+    const size_t outn[3] = {on, ln, need};
+    for (int i = 0; i < 3; ++i) {
+        if (cache_overlap(*cache, outs[i], outn[i]) || overlap(outs[i], outn[i], q, qn) ||
+            overlap(outs[i], outn[i], pages, pn) ||
+            overlap_sequences(outs[i], outn[i], table, max_pages, lens, counts, B))
+            return ATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outn[i], outs[j], outn[j])) return ATTN_ERR_INVALID_ARG;
+    }
+    const int st = check_device();
+    if (st != ATTN_OK) return st;
+    return launch_cache_fwd(*cache, q, o, lse, table, max_pages, lens, counts, pages, n_select, B, H,
+                            Sq, causal, sc, dtype, workspace, (cudaStream_t)stream);
+}
+
 int attn_check_status(void *stream) {
     cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_to_status(e);
@@ -545,6 +714,7 @@ int attn_check_status(void *stream) {
     }
     if (word & kStatusBounds) return ATTN_ERR_BOUNDS;
     if (word & kStatusTimeout) return ATTN_ERR_TIMEOUT;
+    if (word & kStatusTable) return ATTN_ERR_TABLE;
     return ATTN_OK;
 }
 

@@ -1,0 +1,323 @@
+// attn_cache.cu -- the paged 8-bit cache: quantising new keys and values into
+// it (append) and reading them back (read).
+//
+// Layout: codes [n_pages][H_kv][page][d], one scale per (page, kv head), and
+// for the keys the smallest and largest code of each channel per (page, kv
+// head) as [2][d] codes.  A (page, head) block is one contiguous piece, so one
+// CTA owns it: it alone decides the block's scale and no atomics are needed.
+//
+// Append, per block and tensor, with x the rows that land in it:
+//     s  = max(s_old if the block holds older rows, pow2 scale of amax |x|)
+//     codes of x = rn(x / s);  older codes = rn(code * s_old / s) when s grew
+//     bounds = min / max (older bounds rounded the same way, codes of x)
+// Rounding is monotone, so the bounds are exactly the smallest and largest
+// code without reading the older rows again.  Older rows are read only when
+// the scale grows.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_internal.h"
+#include "cache_codec.cuh"
+#include "cache_index.h"
+
+namespace attn {
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+// Maximum over the block (NaN wins); every thread gets it.
+__device__ __forceinline__ float block_max_nan(float x, float *red) {
+    // magnitudes as integers: x >= 0 or NaN, and a NaN's bits exceed infinity's
+    uint32_t u = __float_as_uint(x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, o));
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) red[warp] = __uint_as_float(u);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) u = max(u, __float_as_uint(red[w]));
+    return __uint_as_float(u);
+}
+
+struct AppendArgs {
+    const void *x[2];   // new keys, values [B][Hkv][S][d]
+    uint8_t *codes[2];  // [n_pages][Hkv][page][d]
+    float *scale[2];    // [n_pages][Hkv]
+    uint8_t *bounds;    // [n_pages][Hkv][2][d], keys only
+    const int32_t *table, *pos, *counts;
+    int B, S, Hkv, page, n_pages, max_pages, touched;
+    int *status;
+};
+
+// One CTA per (touched page of a sequence, kv head, keys or values).
+template <int D, int FMT, int DT>
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
+    constexpr int G = D / 8;                      // 8-element groups per row
+    constexpr int RL = kAppendThreads / G;        // rows in parallel
+    __shared__ float red[kAppendThreads / 32];
+    __shared__ float edge[2][RL][D];
+    int64_t blk = blockIdx.x;
+    const int which = (int)(blk & 1);
+    blk >>= 1;
+    const int hk = (int)(blk % a.Hkv);
+    blk /= a.Hkv;
+    const int tp = (int)(blk % a.touched);
+    const int b = (int)(blk / a.touched);
+    const int pos = a.pos[b];
+    int cnt = a.counts ? a.counts[b] : a.S;
+    if (cnt < 0 || cnt > a.S || pos < 0) {  // nothing of this sequence is written
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusTable);
+        return;
+    }
+    const int64_t end = (int64_t)pos + cnt;
+    const int64_t lp = pos / a.page + tp;           // logical page
+    const int64_t first = lp * a.page;              // its first position
+    if (first >= end) return;
+    const int phys = lp < a.max_pages ? a.table[(int64_t)b * a.max_pages + lp] : -1;
+    if (phys < 0 || phys >= a.n_pages) {  // the rows have no page: skipped and reported
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusTable);
+        return;
+    }
+    const int r0 = pos > first ? (int)(pos - first) : 0;                  // first new row
+    const int r1 = end - first < a.page ? (int)(end - first) : a.page;    // past the last
+    const int64_t ph = (int64_t)phys * a.Hkv + hk;
+    uint8_t *codes = (which ? a.codes[1] : a.codes[0]) + ph * a.page * D;
+    float *scale = (which ? a.scale[1] : a.scale[0]) + ph;
+    const void *xs = which ? a.x[1] : a.x[0];
+    const float before = r0 > 0 ? *scale : 0.f;
+    // source row of page row r: s = first + r - pos
+    const size_t src = (((size_t)b * a.Hkv + hk) * a.S) * D;
+    const int64_t shift = first - pos;
+    const int g = threadIdx.x % G, rl = threadIdx.x / G;
+
+    float amax = 0.f;
+    for (int r = r0 + rl; r < r1; r += RL) {
+        float f[8];
+        const size_t i = src + (size_t)(shift + r) * D + g * 8;
+        if (!in_bounds(i + 8 <= (size_t)a.B * a.Hkv * a.S * D, a.status)) continue;
+        codec::load8<DT>(xs, i, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t u = __float_as_uint(f[e]) & 0x7fffffffu;
+            amax = __uint_as_float(max(u, __float_as_uint(amax)));
+        }
+    }
+    amax = block_max_nan(amax, red);
+    const float mine = codec::scale_for<FMT>(amax);
+    const float now = (before != before || mine != mine) ? __int_as_float(0x7fc00000)
+                                                         : fmaxf(before, mine);
+    const float inv = codec::inverse_scale(now);
+
+    float lo[8], hi[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        lo[e] = INFINITY;
+        hi[e] = -INFINITY;
+    }
+    for (int r = r0 + rl; r < r1; r += RL) {
+        float f[8];
+        const size_t i = src + (size_t)(shift + r) * D + g * 8;
+        if (!in_bounds(i + 8 <= (size_t)a.B * a.Hkv * a.S * D, a.status)) continue;
+        codec::load8<DT>(xs, i, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = inv > 0.f ? f[e] * inv : 0.f;
+        uint2 c;
+        c.x = codec::encode4<FMT>(f[0], f[1], f[2], f[3]);
+        c.y = codec::encode4<FMT>(f[4], f[5], f[6], f[7]);
+        *reinterpret_cast<uint2 *>(codes + (size_t)r * D + g * 8) = c;
+        codec::decode4<FMT>(c.x, f);
+        codec::decode4<FMT>(c.y, f + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            lo[e] = fminf(lo[e], f[e]);
+            hi[e] = fmaxf(hi[e], f[e]);
+        }
+    }
+    const bool grew = r0 > 0 && !(now == before);  // also when the block turned NaN
+    const float ratio = now > 0.f ? before * inv : 0.f;
+    if (grew) {  // the older rows under the larger scale
+        for (int i = threadIdx.x; i < r0 * (D / 8); i += kAppendThreads) {
+            uint2 *p = reinterpret_cast<uint2 *>(codes) + i;
+            uint2 c = *p;
+            float f[8];
+            codec::decode4<FMT>(c.x, f);
+            codec::decode4<FMT>(c.y, f + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = ratio > 0.f ? f[e] * ratio : 0.f;
+            c.x = codec::encode4<FMT>(f[0], f[1], f[2], f[3]);
+            c.y = codec::encode4<FMT>(f[4], f[5], f[6], f[7]);
+            *p = c;
+        }
+    }
+    if (threadIdx.x == 0) *scale = now;
+    if (which == 1 || !a.bounds) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        edge[0][rl][g * 8 + e] = lo[e];
+        edge[1][rl][g * 8 + e] = hi[e];
+    }
+    __syncthreads();
+    // thread t: side t / (D / 4), four channels
+    if (threadIdx.x < 2 * (D / 4)) {
+        const int side = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
+        uint32_t *p = reinterpret_cast<uint32_t *>(a.bounds + ((size_t)ph * 2 + side) * D) + c4;
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float x = edge[side][0][c4 * 4 + e];
+            for (int w = 1; w < RL; ++w) {
+                const float y = edge[side][w][c4 * 4 + e];
+                x = side ? fmaxf(x, y) : fminf(x, y);
+            }
+            f[e] = x;
+        }
+        if (r0 > 0) {
+            float o[4];
+            codec::decode4<FMT>(*p, o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = grew ? (ratio > 0.f ? o[e] * ratio : 0.f) : o[e];
+            codec::decode4<FMT>(codec::encode4<FMT>(o[0], o[1], o[2], o[3]), o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = side ? fmaxf(f[e], o[e]) : fminf(f[e], o[e]);
+        }
+        *p = codec::encode4<FMT>(f[0], f[1], f[2], f[3]);
+    }
+}
+
+struct ReadArgs {
+    const uint8_t *codes[2];
+    const float *scale[2];
+    void *out[2];  // [B][Hkv][S][d]
+    const int32_t *table, *lens;
+    int B, S, Hkv, page, n_pages, max_pages, tiles;
+    int *status;
+};
+
+constexpr int kReadThreads = 256;
+
+// One CTA per (page of a sequence, kv head, keys or values): 16 codes per
+// thread and step, 16-byte loads and stores.
+template <int D, int FMT, int DT>
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadArgs a) {
+    constexpr int G = D / 16;
+    int64_t blk = blockIdx.x;
+    const int which = (int)(blk & 1);
+    blk >>= 1;
+    const int lp = (int)(blk % a.tiles);
+    blk /= a.tiles;
+    const int hk = (int)(blk % a.Hkv);
+    const int b = (int)(blk / a.Hkv);
+    const int len0 = a.lens[b];
+    const int len = clamp_len(len0, a.max_pages, a.page);
+    if (len != len0 && threadIdx.x == 0) atomicOr(a.status, kStatusTable);
+    const int64_t first = (int64_t)lp * a.page;
+    const int rows = a.S - first < a.page ? (int)(a.S - first) : a.page;
+    int held = (int64_t)len - first < rows ? (int)((int64_t)len - first) : rows;
+    if (held < 0) held = 0;
+    const uint8_t *codes = nullptr;
+    float s = 0.f;
+    if (held > 0) {
+        const int phys = a.table[(int64_t)b * a.max_pages + lp];
+        if (phys < 0 || phys >= a.n_pages) {  // rows without a page read as zero, reported
+            if (threadIdx.x == 0) atomicOr(a.status, kStatusTable);
+            held = 0;
+        } else {
+            const int64_t ph = (int64_t)phys * a.Hkv + hk;
+            codes = (which ? a.codes[1] : a.codes[0]) + ph * a.page * D;
+            s = (which ? a.scale[1] : a.scale[0])[ph];
+        }
+    }
+    const size_t dst = (((size_t)b * a.Hkv + hk) * a.S + first) * D;
+    void *out = which ? a.out[1] : a.out[0];
+    for (int i = threadIdx.x; i < rows * G; i += kReadThreads) {
+        const int r = i / G;
+        float f[16];
+        if (r < held) {
+            const uint4 c = *reinterpret_cast<const uint4 *>(codes + (size_t)i * 16);
+            codec::decode4<FMT>(c.x, f);
+            codec::decode4<FMT>(c.y, f + 4);
+            codec::decode4<FMT>(c.z, f + 8);
+            codec::decode4<FMT>(c.w, f + 12);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] *= s;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] = 0.f;
+        }
+        const size_t at = dst + (size_t)i * 16;
+        if (!in_bounds(at + 16 <= (size_t)a.B * a.Hkv * a.S * D, a.status)) continue;
+        if constexpr (DT == 0) {
+            float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + at);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] = codec::clamped(f[e], 3.402823466e38f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+        } else {
+            uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + at);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                p[e] = make_uint4(codec::pack2_clamped<DT>(f[8 * e], f[8 * e + 1]),
+                                  codec::pack2_clamped<DT>(f[8 * e + 2], f[8 * e + 3]),
+                                  codec::pack2_clamped<DT>(f[8 * e + 4], f[8 * e + 5]),
+                                  codec::pack2_clamped<DT>(f[8 * e + 6], f[8 * e + 7]));
+        }
+    }
+}
+
+// f(integral constants D, FMT, DT) for the runtime values
+template <template <int, int, int> class F, typename... A>
+int dispatch(int d, int format, int dt, A... args) {
+#define ATTN_CASE(DD, FF, TT) \
+    if (d == DD && format == FF && dt == TT) return F<DD, FF, TT>::run(args...);
+#define ATTN_CASES(FF) \
+    ATTN_CASE(64, FF, 0) ATTN_CASE(64, FF, 1) ATTN_CASE(64, FF, 2) \
+    ATTN_CASE(128, FF, 0) ATTN_CASE(128, FF, 1) ATTN_CASE(128, FF, 2)
+    ATTN_CASES(ATTN_CACHE_E4M3)
+    ATTN_CASES(ATTN_CACHE_I8)
+#undef ATTN_CASES
+#undef ATTN_CASE
+    return ATTN_ERR_INVALID_ARG;
+}
+
+template <int D, int FMT, int DT>
+struct RunAppend {
+    static int run(const AppendArgs *a, unsigned grid, cudaStream_t s) {
+        cache_append_kernel<D, FMT, DT><<<grid, kAppendThreads, 0, s>>>(*a);
+        return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+    }
+};
+template <int D, int FMT, int DT>
+struct RunRead {
+    static int run(const ReadArgs *a, unsigned grid, cudaStream_t s) {
+        cache_read_kernel<D, FMT, DT><<<grid, kReadThreads, 0, s>>>(*a);
+        return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+    }
+};
+
+}  // namespace
+
+int launch_cache_append(const attn_cache &c, const void *k, const void *v, const int32_t *table,
+                        int max_pages, const int32_t *pos, const int32_t *counts, int B, int S,
+                        int dtype, cudaStream_t stream) {
+    const int64_t touched = touched_pages(S, c.page);
+    const int64_t grid = (int64_t)B * c.H_kv * touched * 2;  // the caller checked it
+    AppendArgs a = {{k, v}, {(uint8_t *)c.k, (uint8_t *)c.v}, {c.k_scale, c.v_scale},
+                    (uint8_t *)c.k_bounds, table, pos, counts, B, S, c.H_kv, c.page, c.n_pages,
+                    max_pages, (int)touched, status_word_device_ptr()};
+    if (!a.status) return ATTN_ERR_CUDA;
+    return dispatch<RunAppend>(c.d, c.format, dtype, (const AppendArgs *)&a, (unsigned)grid, stream);
+}
+
+int launch_cache_read(const attn_cache &c, const int32_t *table, int max_pages, const int32_t *lens,
+                      void *k, void *v, int B, int S, int dtype, cudaStream_t stream) {
+    const int64_t tiles = ((int64_t)S + c.page - 1) / c.page;
+    const int64_t grid = (int64_t)B * c.H_kv * tiles * 2;
+    ReadArgs a = {{(const uint8_t *)c.k, (const uint8_t *)c.v}, {c.k_scale, c.v_scale}, {k, v},
+                  table, lens, B, S, c.H_kv, c.page, c.n_pages, max_pages, (int)tiles,
+                  status_word_device_ptr()};
+    if (!a.status) return ATTN_ERR_CUDA;
+    return dispatch<RunRead>(c.d, c.format, dtype, (const ReadArgs *)&a, (unsigned)grid, stream);
+}
+
+}  // namespace attn

@@ -1,0 +1,770 @@
+// attn_cache_fwd.cu -- attention of a few query rows per sequence over the
+// paged 8-bit cache, over all pages or over a list of pages per query.
+//
+//     s_j = scale * k_scale[page(j)] * (q . kcode_j)
+//     o   = sum_j softmax_j(s) * v_scale[page(j)] * vcode_j
+//
+// Work.  A unit is (sequence, kv head, block of query rows): the G query heads
+// of a kv head share its keys, so the rows of a block are (query, head of the
+// group).  Its keys are walked in tiles of KT keys.  All tiles of a call are
+// numbered through and cut into equal contiguous ranges, one per warp
+// (cache_index.h): ragged lengths and few sequences fill the GPU alike.  A
+// warp writes the units it covers alone, and leaves a partial state (o, lse)
+// for the at most two it shares; a second kernel joins those with the online
+// softmax's merge of states.
+//
+// Products.  The 8-bit codes are exact in fp16, so both products run on
+// mma.m16n8k16 with fp32 accumulation and no dequantised tile exists
+// anywhere: the page's scales multiply the scores and the page's share of o.
+// A decode step is bound by reading the codes; of the 16 rows of the MMA few
+// carry queries, which costs nothing that is scarce here.
+//   8-row form: rows 0-7 are query rows, rows 8-15 the same rows' rounding
+//     remainders: q = hi + lo (lo = 0 unless q is fp32) and p = hi + lo, so the
+//     products are those of 22-bit numbers and fp32 outputs keep their digits.
+//   16-row form (bf16 output, more than 8 rows): p is rounded once to fp16
+//     (2^-12, against the output's 2^-9).
+// q rows are first multiplied by a power of two that puts the row's largest
+// magnitude in [2^14, 2^15): any fp32 or bf16 exponent then fits fp16.
+//
+// Fragments are loaded straight from global memory: the MMA's k index may name
+// the channels in any order that q and k share, and its n index any channel
+// of v.  Lane (g, t) = (lane / 4, lane % 4) reads D/4 consecutive bytes of key
+// row g (a whole row per 4 lanes), and D/8 consecutive bytes of value rows
+// 2t, 2t+1, 2t+8, 2t+9 (a whole row per 8 lanes), with 16-byte loads.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_internal.h"
+#include "cache_codec.cuh"
+#include "cache_index.h"
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMinTiles = 1;  // tiles per worker when there are few
+
+struct FwdArgs {
+    const void *q;
+    void *o;
+    float *lse;
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    const int32_t *table, *lens, *counts, *pages;
+    int64_t *prefix;  // [B + 1] tiles before each sequence (all pages)
+    float *po, *pl;   // partial states by slot: [slot][R][D], [slot][R] (log2)
+    int B, Hkv, G, Sq, page, n_pages, max_pages, n_sel, causal;
+    int nseg, rows, nrb;  // row groups of a (sequence, kv head), rows of one, row blocks of one
+    int dtype, workers;
+    float sl2;  // scale * log2(e)
+    int *status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint4 ldg16(const uint8_t *p) {
+    uint4 u;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+    return u;
+}
+__device__ __forceinline__ uint2 ldg8(const uint8_t *p) {
+    uint2 u;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(u.x), "=r"(u.y) : "l"(p));
+    return u;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Codes as fp16 pairs, exact.  e4m3: sign and the seven other bits moved into
+// place give code * 2^-8 (the exponent biases differ by 8; subnormals stay
+// right), so kUnit is 2^8, and no code becomes an fp16 NaN: what a page holds
+// behind its last token cannot disturb a product with 0.  int8: 0x6400 + u is
+// the fp16 1024 + u, u = code + 128.
+template <int FMT>
+struct Unpack;
+template <>
+struct Unpack<ATTN_CACHE_E4M3> {
+    static constexpr float kUnit = 256.f;
+    // bytes 1 and 3 of w, as (low, high)
+    __device__ __forceinline__ static uint32_t odd(uint32_t w) {
+        return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+    }
+    // channels (0, 2) and (1, 3) of four consecutive codes
+    __device__ __forceinline__ static void quad(uint32_t w, uint32_t &b0, uint32_t &b1) {
+        b0 = odd(w << 8);
+        b1 = odd(w);
+    }
+    // byte j of x and byte j of y
+    template <int J>
+    __device__ __forceinline__ static uint32_t pair(uint32_t x, uint32_t y) {
+        return odd(__byte_perm(x, y, (J + 4) * 0x1100 + J * 0x11));
+    }
+};
+template <>
+struct Unpack<ATTN_CACHE_I8> {
+    static constexpr float kUnit = 1.f;
+    __device__ __forceinline__ static uint32_t bias(uint32_t w) {  // 1024 + u -> u - 128
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&w),
+                                  __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    __device__ __forceinline__ static void quad(uint32_t w, uint32_t &b0, uint32_t &b1) {
+        const uint32_t u = w ^ 0x80808080u;
+        b0 = bias(__byte_perm(u, 0x64646464u, 0x4240));
+        b1 = bias(__byte_perm(u, 0x64646464u, 0x4341));
+    }
+    template <int J>
+    __device__ __forceinline__ static uint32_t pair(uint32_t x, uint32_t y) {
+        return bias((__byte_perm(x, y, (J + 4) * 0x1100 + J * 0x11) & 0x00ff00ffu) ^ 0x64806480u);
+    }
+};
+
+// Where a tile's unit lies.
+struct Unit {
+    int b, hk, seg, rb;
+    int64_t begin, end;  // its tiles
+};
+
+// Sequence lengths as tile counts, summed: prefix[b] tiles before sequence b.
+__device__ void scan_lengths(const FwdArgs &a, int kt, int64_t *prefix, int64_t *warp_sums) {
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
+    auto tiles = [&](int b) {
+        const int len0 = a.lens[b], cnt = a.counts ? a.counts[b] : a.Sq;
+        const int len = clamp_len(len0, a.max_pages, a.page);
+        if ((len != len0 || cnt < 0 || cnt > a.Sq) && blockIdx.x == 0)
+            atomicOr(a.status, kStatusTable);
+        return ((int64_t)len + kt - 1) / kt;
+    };
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) sum += tiles(b);
+    int64_t incl = sum;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    int64_t at = incl - sum;
+    for (int w = 0; w < warp; ++w) at += warp_sums[w];
+    for (int b = b0; b < b1; ++b) {
+        prefix[b] = at;
+        at += tiles(b);
+    }
+    if (b0 < a.B && b1 == a.B) prefix[a.B] = at;
+}
+
+// The unit that tile x belongs to.
+__device__ __forceinline__ Unit unit_of(const FwdArgs &a, const int64_t *prefix, int64_t tpu, int64_t x) {
+    Unit u;
+    const int per = a.nseg * a.nrb;
+    int64_t idx, first, len;  // unit within the sequence, the sequence's first tile, tiles per unit
+    if (a.pages) {
+        const int64_t n = x / tpu, units = (int64_t)a.Hkv * per;
+        u.b = (int)(n / units);
+        idx = n % units;
+        first = u.b * units * tpu;
+        len = tpu;
+    } else {
+        const int64_t units = (int64_t)a.Hkv * per, y = x / units;
+        int lo = 0, hi = a.B - 1;  // the last b with prefix[b] <= y
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= y) lo = mid; else hi = mid - 1;
+        }
+        u.b = lo;
+        first = prefix[lo] * units;
+        len = prefix[lo + 1] - prefix[lo];
+        idx = (x - first) / len;
+    }
+    u.begin = first + idx * len;
+    u.end = u.begin + len;
+    u.hk = (int)(idx / per);
+    u.seg = (int)(idx % per / a.nrb);
+    u.rb = (int)(idx % a.nrb);
+    return u;
+}
+
+// Query and head of row r of a unit; false past the group's rows.
+template <int R>
+__device__ __forceinline__ bool row_of(const FwdArgs &a, const Unit &u, int r, int &i, int &h) {
+    const int row = u.rb * R + r;
+    if (row >= a.rows) return false;
+    const int g = a.pages ? row : row % a.G;
+    i = a.pages ? u.seg : row / a.G;
+    h = u.hk * a.G + g;
+    return true;
+}
+
+struct Tile {  // one key tile, held by one lane
+    int at;    // tile of KT keys in the pool, -1: nothing to read
+    int key0;  // its first key's position in the sequence
+    float ks, vs;
+};
+
+template <int R, int KT>
+__device__ __forceinline__ Tile find_tile(const FwdArgs &a, const int64_t *prefix, int64_t tpu, int64_t x) {
+    Tile d;
+    d.at = -1;
+    d.key0 = 0;
+    d.ks = d.vs = 0.f;
+    const Unit u = unit_of(a, prefix, tpu, x);
+    const int in_page = a.page / KT;
+    const int64_t t = x - u.begin;
+    const int len = clamp_len(a.lens[u.b], a.max_pages, a.page);
+    const int cnt = a.counts ? min(max(a.counts[u.b], 0), a.Sq) : a.Sq;
+    int lp = (int)(t / in_page);
+    const int sub = (int)(t % in_page);
+    if (a.pages) {
+        const int64_t list = ((int64_t)u.b * a.Hkv + u.hk) * a.nseg + u.seg;
+        lp = a.pages[list * a.n_sel + lp];
+        if (lp < -1 || lp >= a.max_pages) atomicOr(a.status, kStatusTable);
+        if (lp < 0 || lp >= a.max_pages) return d;
+    }
+    // the block's last query that is one of the sequence's sees the most keys
+    int first, last, h;
+    row_of<R>(a, u, 0, first, h);
+    row_of<R>(a, u, min(a.rows - u.rb * R, R) - 1, last, h);
+    last = min(last, cnt - 1);
+    const int seen = last < first ? 0 : visible_keys(len, cnt, last, a.causal);
+    const int64_t key0 = (int64_t)lp * a.page + sub * KT;
+    if (key0 >= seen) return d;
+    d.key0 = (int)key0;
+    const int phys = a.table[(int64_t)u.b * a.max_pages + lp];
+    if (phys < 0 || phys >= a.n_pages) {
+        atomicOr(a.status, kStatusTable);
+        return d;
+    }
+    const int64_t ph = (int64_t)phys * a.Hkv + u.hk;
+    d.at = (int)(ph * in_page + sub);
+    d.ks = a.ks[ph];
+    d.vs = a.vs[ph];
+    return d;
+}
+
+__device__ __forceinline__ void load_q8(const FwdArgs &a, size_t i, float *f) {
+    if (a.dtype == ATTN_F32) codec::load8<0>(a.q, i, f);
+    else if (a.dtype == ATTN_BF16 || a.dtype == ATTN_BF16_OUT_F32) codec::load8<1>(a.q, i, f);
+    else codec::load8<2>(a.q, i, f);
+}
+
+// Eight consecutive outputs.
+__device__ __forceinline__ void store_o8(const FwdArgs &a, size_t i, const float *f) {
+    if (a.dtype == ATTN_BF16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.o) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if (a.dtype == ATTN_F16) {
+        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.o) + i) =
+            make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
+    } else {
+        float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + i);
+        p[0] = make_float4(f[0], f[1], f[2], f[3]);
+        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+
+// WIDE = 0: the 8-row form, 1: the 16-row form.
+template <int D, int FMT, int WIDE, int KT>
+__global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a) {
+    using U = Unpack<FMT>;
+    constexpr int R = WIDE ? 16 : 8;
+    constexpr int H = WIDE ? 2 : 1;    // query rows per lane: g, and g + 8 in the 16-row form
+    constexpr int NT = KT / 8;         // score tiles of 8 keys
+    constexpr int KS = KT / 16;        // k steps of P.V
+    constexpr int QS = D / 16;         // k steps of Q.K
+    constexpr int VT = D / 8;          // output tiles of 8 channels
+    constexpr int VW = D / 32;         // words of a lane's value row
+    extern __shared__ int64_t prefix[];  // [B + 1]
+    __shared__ int64_t warp_sums[kWarps];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int64_t tpu = a.pages ? (int64_t)a.n_sel * (a.page / KT) : 0;
+    const int64_t units = (int64_t)a.Hkv * a.nseg * a.nrb;  // of one sequence
+    int64_t total;
+    if (a.pages) {
+        total = a.B * units * tpu;
+        // lengths and counts out of range are reported here for a page list
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b < a.B; b += kThreads) {
+                const int len = a.lens[b], cnt = a.counts ? a.counts[b] : a.Sq;
+                if (len != clamp_len(len, a.max_pages, a.page) || cnt < 0 || cnt > a.Sq)
+                    atomicOr(a.status, kStatusTable);
+            }
+    } else {
+        scan_lengths(a, KT, prefix, warp_sums);
+        __syncthreads();
+        total = prefix[a.B] * units;
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b <= a.B; b += kThreads) a.prefix[b] = prefix[b];
+    }
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t workers = worker_count(total, a.workers, kMinTiles);
+    // neighbouring ranges on different SMs, so that few tiles spread widely
+    const int64_t w = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+    if (w >= workers) return;
+    const int64_t x0 = worker_begin(w, total, workers), x1 = worker_begin(w + 1, total, workers);
+    if (x0 >= x1) return;
+
+    // tiles x0 + 32 n + lane, and the next 32
+    Tile cur = {-1, 0, 0.f, 0.f}, nxt = cur;
+    if (x0 + lane < x1) cur = find_tile<R, KT>(a, prefix, tpu, x0 + lane);
+
+    uint4 kr[KT * D / 512];
+    constexpr int VN = KS * 4;
+    uint32_t vr[VN][VW];
+    auto load_k = [&](int at) {
+        const uint8_t *p = a.k + (size_t)at * KT * D + g * D + t * (D / 4);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) kr[n * (D / 64) + c] = ldg16(p + n * 8 * D + c * 16);
+    };
+    auto load_v = [&](int at) {
+        const uint8_t *p = a.v + (size_t)at * KT * D + g * (D / 8);
+#pragma unroll
+        for (int n = 0; n < VN; ++n) {
+            const int row = (n / 4) * 16 + 2 * t + (n & 1) + ((n & 2) ? 8 : 0);
+            if constexpr (VW == 4) {
+                const uint4 u = ldg16(p + row * D);
+                vr[n][0] = u.x; vr[n][1] = u.y; vr[n][2] = u.z; vr[n][3] = u.w;
+            } else {
+                const uint2 u = ldg8(p + row * D);
+                vr[n][0] = u.x; vr[n][1] = u.y;
+            }
+        }
+    };
+    {
+        const int at = __shfl_sync(0xffffffffu, cur.at, 0);
+        if (at >= 0) {
+            load_k(at);
+            load_v(at);
+        }
+    }
+
+    int64_t x = x0;
+    while (x < x1) {
+        const Unit u = unit_of(a, prefix, tpu, x);
+        const int64_t xe = u.end < x1 ? u.end : x1;
+        const int len = clamp_len(a.lens[u.b], a.max_pages, a.page);
+        const int cnt = a.counts ? min(max(a.counts[u.b], 0), a.Sq) : a.Sq;
+
+        // query fragments: k step w pairs channels (4w, 4w + 2) and (4w + 1, 4w + 3) of the
+        // lane's D/4 channels, as Unpack::quad does
+        uint32_t qa[QS][4];
+        float cq[H];
+        int lim[H];
+        int low = 0x7fffffff;  // fewest keys any row of the block sees
+#pragma unroll
+        for (int hh = 0; hh < H; ++hh) {
+            float f[D / 4];
+            int i, h;
+            const bool real = row_of<R>(a, u, g + 8 * hh, i, h);
+            lim[hh] = real ? visible_keys(len, cnt, i, a.causal) : 0;
+            if (real) {
+                const size_t at = (((size_t)u.b * a.Hkv * a.G + h) * a.Sq + i) * D + t * (D / 4);
+#pragma unroll
+                for (int e = 0; e < D / 4; e += 8) load_q8(a, at + e, f + e);
+            } else {
+#pragma unroll
+                for (int e = 0; e < D / 4; ++e) f[e] = 0.f;
+            }
+            float amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < D / 4; ++e) amax = fmaxf(amax, fabsf(f[e]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^up puts amax in [2^14, 2^15); 0 and infinity stay as they are
+            int up = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
+            up = up > 126 ? 126 : up;
+            if (amax == 0.f || !(amax <= 3.402823466e38f)) up = 0;
+            const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+            cq[hh] = a.sl2 * __uint_as_float((uint32_t)(127 - up) << 23) * U::kUnit;
+#pragma unroll
+            for (int s = 0; s < QS; ++s) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = f[4 * s + e] * mul;
+                qa[s][hh] = pack_f16(y[0], y[2]);
+                qa[s][hh + 2] = pack_f16(y[1], y[3]);
+                if constexpr (!WIDE) {
+                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&qa[s][0]));
+                    const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&qa[s][2]));
+                    qa[s][1] = pack_f16(y[0] - p.x, y[2] - p.y);
+                    qa[s][3] = pack_f16(y[1] - r.x, y[3] - r.y);
+                }
+            }
+            if (real) low = min(low, lim[hh]);
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
+
+        float m[H], l[H], acc[VT][2 * H];
+#pragma unroll
+        for (int hh = 0; hh < H; ++hh) {
+            m[hh] = -INFINITY;
+            l[hh] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < VT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2 * H; ++e) acc[n][e] = 0.f;
+
+        for (; x < xe; ++x) {
+            const int i = (int)(x - x0);
+            if ((i & 31) == 0) {
+                if (i > 0) cur = nxt;
+                nxt.at = -1;
+                if (x + 32 + lane < x1) nxt = find_tile<R, KT>(a, prefix, tpu, x + 32 + lane);
+            }
+            const int at = __shfl_sync(0xffffffffu, cur.at, i & 31);
+            const int key0 = __shfl_sync(0xffffffffu, cur.key0, i & 31);
+            const float ks = __shfl_sync(0xffffffffu, cur.ks, i & 31);
+            const float vs = __shfl_sync(0xffffffffu, cur.vs, i & 31);
+            const int ahead = ((i + 1) & 31) ? __shfl_sync(0xffffffffu, cur.at, (i + 1) & 31)
+                                             : __shfl_sync(0xffffffffu, nxt.at, 0);
+            const int next = x + 1 < x1 ? ahead : -1;
+            if (at < 0) {
+                if (next >= 0) {
+                    load_k(next);
+                    load_v(next);
+                }
+                continue;
+            }
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 u4 = kr[n * (D / 64) + c];
+                    const uint32_t words[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t b0, b1;
+                        U::quad(words[e], b0, b1);
+                        const int st = c * 4 + e;
+                        mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b0, b1);
+                    }
+                }
+            }
+            if (next >= 0) load_k(next);
+
+            uint32_t pa[KS][4];
+            float alpha[H], sv[H];
+#pragma unroll
+            for (int hh = 0; hh < H; ++hh) {
+                float y[NT][2];
+                const float f = ks * cq[hh];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        // hi and lo parts of q in the 8-row form
+                        y[n][c] = (WIDE ? s[n][2 * hh + c] : s[n][c] + s[n][2 + c]) * f;
+                        if (key0 + KT > low && key0 + 8 * n + 2 * t + c >= lim[hh]) y[n][c] = -INFINITY;
+                        mx = fmaxf(mx, y[n][c]);
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = fmaxf(m[hh], mx);
+                const float base = mn == -INFINITY ? 0.f : mn;
+                alpha[hh] = ex2(m[hh] - base);  // 0 while nothing has been seen
+                m[hh] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float p0 = ex2(y[n][0] - base), p1 = ex2(y[n][1] - base);
+                    sum += p0 + p1;
+                    // 2^15: small weights stay above fp16's subnormals
+                    const uint32_t hi = pack_f16(p0 * 32768.f, p1 * 32768.f);
+                    if constexpr (WIDE) {
+                        pa[n / 2][(n & 1) * 2 + hh] = hi;
+                    } else {
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                        pa[n / 2][(n & 1) * 2] = hi;
+                        pa[n / 2][(n & 1) * 2 + 1] = pack_f16(fmaf(p0, 32768.f, -b.x), fmaf(p1, 32768.f, -b.y));
+                    }
+                }
+                l[hh] = l[hh] * alpha[hh] + sum;
+                // a page no key of which the row sees adds nothing, not even its scale's NaN
+                sv[hh] = key0 < lim[hh] ? vs * (U::kUnit / 32768.f) : 0.f;
+            }
+            // o, four channel tiles (one word of each value row) at a time
+#pragma unroll
+            for (int wd = 0; wd < VW; ++wd) {
+                float c[4][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[e][0] = c[e][1] = c[e][2] = c[e][3] = 0.f;
+#pragma unroll
+                for (int st = 0; st < KS; ++st) {
+                    const uint32_t r0 = vr[4 * st][wd], r1 = vr[4 * st + 1][wd];
+                    const uint32_t r2 = vr[4 * st + 2][wd], r3 = vr[4 * st + 3][wd];
+                    mma16816(c[0], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<0>(r0, r1), U::template pair<0>(r2, r3));
+                    mma16816(c[1], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<1>(r0, r1), U::template pair<1>(r2, r3));
+                    mma16816(c[2], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<2>(r0, r1), U::template pair<2>(r2, r3));
+                    mma16816(c[3], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<3>(r0, r1), U::template pair<3>(r2, r3));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float *o = acc[4 * wd + e];
+                    if constexpr (WIDE) {
+                        o[0] = fmaf(sv[0], c[e][0], o[0] * alpha[0]);
+                        o[1] = fmaf(sv[0], c[e][1], o[1] * alpha[0]);
+                        o[2] = fmaf(sv[1], c[e][2], o[2] * alpha[1]);
+                        o[3] = fmaf(sv[1], c[e][3], o[3] * alpha[1]);
+                    } else {
+                        o[0] = fmaf(sv[0], c[e][0] + c[e][2], o[0] * alpha[0]);
+                        o[1] = fmaf(sv[0], c[e][1] + c[e][3], o[1] * alpha[0]);
+                    }
+                }
+            }
+            if (next >= 0) load_v(next);
+        }
+
+        // the unit's state so far: written if it is whole, else left for the merge
+        const bool whole = u.begin >= x0 && u.end <= x1;
+        const int64_t slot = partial_slot(w, u.begin < x0);
+#pragma unroll
+        for (int hh = 0; hh < H; ++hh) {
+            float sum = l[hh];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: no key was visible
+            const float base = m[hh] == -INFINITY ? 0.f : m[hh];
+            const float lse2 = sum == 0.f ? -INFINITY : base + log2f(sum);
+            const int r = g + 8 * hh;
+            float f[D / 4];
+#pragma unroll
+            for (int n = 0; n < VT; ++n) {
+                f[n] = acc[n][2 * hh] * inv;
+                f[VT + n] = acc[n][2 * hh + 1] * inv;
+            }
+            if (whole) {
+                int i, h;
+                if (!row_of<R>(a, u, r, i, h)) continue;
+                const size_t row = ((size_t)u.b * a.Hkv * a.G + h) * a.Sq + i;
+                if (!in_bounds(i < a.Sq && h < a.Hkv * a.G, a.status)) continue;
+#pragma unroll
+                for (int e = 0; e < D / 4; e += 8) store_o8(a, row * D + t * (D / 4) + e, f + e);
+                if (a.lse && t == 0) a.lse[row] = lse2 * 0.69314718055994530942f;
+            } else if (in_bounds(slot < 2 * (int64_t)a.workers, a.status)) {
+                float4 *p = reinterpret_cast<float4 *>(a.po + (slot * R + r) * D + t * (D / 4));
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                if (t == 0) a.pl[slot * R + r] = lse2;
+            }
+        }
+    }
+}
+
+// Joins the partial states of one row: one CTA per (unit, row of the block).
+// A unit that one warp covered has been written; a sequence without keys gets
+// o = 0, lse = -inf here.
+template <int D, int R, int KT>
+__global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) {
+    extern __shared__ float wts[];  // [workers]
+    __shared__ float red[kWarps];
+    __shared__ float part[kWarps][D];
+    const int64_t per = (int64_t)a.Hkv * a.nseg * a.nrb;
+    const int64_t unit = blockIdx.x;
+    Unit u;
+    u.b = (int)(unit / per);
+    const int64_t idx = unit % per;
+    u.hk = (int)(idx / (a.nseg * a.nrb));
+    u.seg = (int)(idx % (a.nseg * a.nrb) / a.nrb);
+    u.rb = (int)(idx % a.nrb);
+    const int r = blockIdx.y;
+    int i, h;
+    const bool real = row_of<R>(a, u, r, i, h);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!real) return;
+    int64_t total;
+    if (a.pages) {
+        const int64_t tpu = (int64_t)a.n_sel * (a.page / KT);
+        total = a.B * per * tpu;
+        u.begin = unit * tpu;
+        u.end = u.begin + tpu;
+    } else {
+        const int64_t p0 = a.prefix[u.b], p1 = a.prefix[u.b + 1];
+        total = a.prefix[a.B] * per;
+        u.begin = p0 * per + idx * (p1 - p0);
+        u.end = u.begin + (p1 - p0);
+    }
+    const size_t row = ((size_t)u.b * a.Hkv * a.G + h) * a.Sq + i;
+    if (!in_bounds(i < a.Sq && h < a.Hkv * a.G, a.status)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (u.begin == u.end) {
+        if (threadIdx.x < D / 8) {
+            const float z[8] = {};
+            store_o8(a, row * D + threadIdx.x * 8, z);
+        }
+        if (a.lse && threadIdx.x == 0) a.lse[row] = -INFINITY;
+        return;
+    }
+    const int64_t workers = worker_count(total, a.workers, kMinTiles);
+    const int64_t w0 = worker_of(u.begin, total, workers), w1 = worker_of(u.end - 1, total, workers);
+    if (w0 == w1) return;
+    const int n = (int)(w1 - w0 + 1);
+    auto slot = [&](int p) { return partial_slot(w0 + p, p > 0); };
+    float M = -INFINITY;
+    for (int p = threadIdx.x; p < n; p += kThreads) {
+        wts[p] = a.pl[slot(p) * R + r];
+        M = fmaxf(M, wts[p]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) red[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) M = fmaxf(M, red[k]);
+    const float base = M == -INFINITY ? 0.f : M;
+    // every warp sums all weights in the same order, and its own parts' o
+    float L = 0.f;
+    for (int p = lane; p < n; p += 32) L += ex2(wts[p] - base);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    constexpr int C = D / 32;
+    float acc[C] = {};
+#pragma unroll 4
+    for (int p = warp; p < n; p += kWarps) {
+        const float wt = ex2(wts[p] - base);
+        const float *src = a.po + (slot(p) * R + r) * D + lane * C;
+        float v[C];
+        if constexpr (C == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(src);
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2 *>(src);
+            v[0] = x.x; v[1] = x.y;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = fmaf(wt, v[c], acc[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) part[warp][lane * C + c] = acc[c];
+    __syncthreads();
+    if (threadIdx.x < D / 8) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) sum += part[k][threadIdx.x * 8 + e];
+            f[e] = sum * inv;
+        }
+        store_o8(a, row * D + threadIdx.x * 8, f);
+        if (a.lse && threadIdx.x == 0)
+            a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * 0.69314718055994530942f;
+    }
+}
+
+template <int D, int FMT, int WIDE, int KT>
+int launch_fwd_t(FwdArgs &a, unsigned grid, cudaStream_t stream) {
+    constexpr int R = WIDE ? 16 : 8;
+    auto fwd = cache_fwd_kernel<D, FMT, WIDE, KT>;
+    const size_t smem = a.pages ? 0 : (size_t)(a.B + 1) * 8;
+    fwd<<<grid, kThreads, smem, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    const int64_t units = (int64_t)a.B * a.Hkv * a.nseg * a.nrb;
+    cfg.gridDim = dim3((unsigned)units, (unsigned)(a.rows < R ? a.rows : R));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)a.workers * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, R, KT>, (const FwdArgs)a);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+template <int D, int FMT>
+int launch_fwd_w(FwdArgs &a, bool wide, int kt, unsigned grid, cudaStream_t s) {
+    if (wide) return kt == 16 ? launch_fwd_t<D, FMT, 1, 16>(a, grid, s) : launch_fwd_t<D, FMT, 1, 32>(a, grid, s);
+    return kt == 16 ? launch_fwd_t<D, FMT, 0, 16>(a, grid, s) : launch_fwd_t<D, FMT, 0, 32>(a, grid, s);
+}
+
+}  // namespace
+
+// The 16-row form where the output's own rounding hides the weights' and the
+// rows do not fit eight.
+static bool cache_wide(int rows, int dtype) { return dtype == ATTN_BF16 && rows > 8; }
+
+// Workspace: the tile counts [B + 1], then two partial states per worker.
+size_t cache_fwd_workspace(int B, int H, int H_kv, int Sq, int d, int dtype, bool listed) {
+    const int64_t rows = (int64_t)(H / H_kv) * (listed ? 1 : Sq);
+    const size_t R = cache_wide((int)(rows > 16 ? 16 : rows), dtype) ? 16 : 8;
+    const size_t prefix = (((size_t)B + 1) * 8 + 15) / 16 * 16;
+    return prefix + (size_t)2 * kCacheMaxCtas * kWarps * R * (d + 1) * 4;
+}
+
+int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, const int32_t *table,
+                     int max_pages, const int32_t *lens, const int32_t *counts, const int32_t *pages,
+                     int n_select, int B, int H, int Sq, int causal, float scale, int dtype,
+                     void *workspace, cudaStream_t stream) {
+    FwdArgs a = {};
+    a.q = q; a.o = o; a.lse = lse;
+    a.k = (const uint8_t *)c.k; a.v = (const uint8_t *)c.v;
+    a.ks = c.k_scale; a.vs = c.v_scale;
+    a.table = table; a.lens = lens; a.counts = counts; a.pages = pages;
+    a.B = B; a.Hkv = c.H_kv; a.G = H / c.H_kv; a.Sq = Sq;
+    a.page = c.page; a.n_pages = c.n_pages; a.max_pages = max_pages; a.n_sel = n_select;
+    a.causal = causal; a.dtype = dtype;
+    a.sl2 = scale * 1.4426950408889634f;
+    a.nseg = pages ? Sq : 1;
+    a.rows = pages ? a.G : a.G * Sq;
+    const bool wide = cache_wide(a.rows, dtype);
+    const int R = wide ? 16 : 8;
+    a.nrb = (a.rows + R - 1) / R;
+    const int64_t units = (int64_t)B * a.Hkv * a.nseg * a.nrb;  // at most B * H * Sq < 2^31
+    a.status = status_word_device_ptr();
+    if (!a.status) return ATTN_ERR_CUDA;
+    const int kt = c.page == 16 ? 16 : 32;
+    const int sms = device_sm_count();
+    if (sms <= 0) return ATTN_ERR_CUDA;
+    // as many CTAs as the longest possible lengths can give every warp a tile
+    const double most = (double)units * (pages ? (double)n_select * c.page : (double)max_pages * c.page) / kt;
+    int64_t ctas = most / kWarps < sms ? (int64_t)(most / kWarps) + 1 : sms;
+    if (ctas > kCacheMaxCtas) ctas = kCacheMaxCtas;
+    if (ctas > sms) ctas = sms;
+    a.workers = (int)ctas * kWarps;
+    a.prefix = reinterpret_cast<int64_t *>(workspace);
+    a.po = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + (((size_t)B + 1) * 8 + 15) / 16 * 16);
+    a.pl = a.po + (size_t)2 * a.workers * R * c.d;
+    if (c.d == 64)
+        return c.format == ATTN_CACHE_E4M3 ? launch_fwd_w<64, ATTN_CACHE_E4M3>(a, wide, kt, (unsigned)ctas, stream)
+                                           : launch_fwd_w<64, ATTN_CACHE_I8>(a, wide, kt, (unsigned)ctas, stream);
+    return c.format == ATTN_CACHE_E4M3 ? launch_fwd_w<128, ATTN_CACHE_E4M3>(a, wide, kt, (unsigned)ctas, stream)
+                                       : launch_fwd_w<128, ATTN_CACHE_I8>(a, wide, kt, (unsigned)ctas, stream);
+}
+
+}  // namespace attn

@@ -12,6 +12,9 @@ namespace attn {
 constexpr int kStatusTimeout = 1;
 // Bit set by the bounds-checking build when an index check failed.
 constexpr int kStatusBounds = 2;
+// Bit set when a block table entry, page list entry, length or count that a
+// kernel read was out of range (the keys or rows concerned were skipped).
+constexpr int kStatusTable = 4;
 
 // The bounds-checking build (compiled with ATTN_BOUNDS_CHECK; the library
 // libattn_checked.so) tests every global-memory index and every TMA
@@ -87,6 +90,27 @@ int launch_merge(const float *po, const float *pl, int n_parts, int64_t rows, in
 constexpr size_t kNoAllocScratchBytes = (size_t)8 << 20;
 int noalloc_scratch_ptr(void **ptr);
 void forget_noalloc_scratch(int dev);  // attn_shutdown: look the address up again next time
+
+// Paged 8-bit cache (attn_cache.cu, attn_cache_select.cu, attn_cache_fwd.cu).
+constexpr int kMaxCacheBatch = 4096;       // sequences of one attention call
+constexpr int kMaxSelectPages = 28672;     // table width attn_cache_select takes, and n_select
+constexpr int kMaxSelectGroup = 128;       // query heads per kv head it takes
+constexpr int kCacheMaxCtas = 160;         // CTAs of the attention kernel at most (one per SM)
+// in the input and output type: 0 fp32, 1 bf16, 2 fp16
+int launch_cache_append(const attn_cache &c, const void *k, const void *v, const int32_t *table,
+                        int max_pages, const int32_t *pos, const int32_t *counts, int B, int S,
+                        int dtype, cudaStream_t stream);
+int launch_cache_read(const attn_cache &c, const int32_t *table, int max_pages, const int32_t *lens,
+                      void *k, void *v, int B, int S, int dtype, cudaStream_t stream);
+int launch_cache_select(const attn_cache &c, const void *q, const int32_t *table, int max_pages,
+                        const int32_t *lens, const int32_t *counts, int32_t *pages, int n_select,
+                        int B, int H, int Sq, int causal, int dtype, void *workspace,
+                        cudaStream_t stream);
+size_t cache_fwd_workspace(int B, int H, int H_kv, int Sq, int d, int dtype, bool listed);
+int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, const int32_t *table,
+                     int max_pages, const int32_t *lens, const int32_t *counts, const int32_t *pages,
+                     int n_select, int B, int H, int Sq, int causal, float scale, int dtype,
+                     void *workspace, cudaStream_t stream);
 
 // Writes o = 0 and lse = -inf (Skv == 0).
 int launch_empty_keys(void *o, float *lse, const Problem &p, cudaStream_t stream);
