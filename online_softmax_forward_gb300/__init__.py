@@ -11,6 +11,7 @@ computing anything another way.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -524,45 +525,54 @@ class KVCache:
                    new(n_pages, H_kv, 2, d) if bounds else None)
 
 
-def _sequence_args(cache, table, lens, counts, B):
-    """Checks the arrays of the call's sequences; returns (table width, counts pointer)."""
+def _int32_on(t, shape, device, name):
     import torch
+    if (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device):
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s"
+                         % (name, tuple(shape), device))
+    return t.data_ptr()
+
+
+def _sequence_args(cache, table, lens, counts, B):
+    """Checks the arrays of the call's sequences; returns the table's pointer and width, and the
+    pointers of lens and counts."""
     if table.dim() != 2 or table.shape[0] != B:
         raise ValueError("table must be [B, max_pages] with B = %d" % B)
     dev = cache.device
-    for t, shape, name in ((table, table.shape, "table"), (lens, (B,), "lens"), (counts, (B,), "counts")):
-        if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
-                              or t.device != dev):
-            raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s"
-                             % (name, tuple(shape), dev))
-    return table.shape[1], counts.data_ptr() if counts is not None else None
+    width = table.shape[1]
+    return (_int32_on(table, (B, width), dev, "table"), width, _int32_on(lens, (B,), dev, "lens"),
+            None if counts is None else _int32_on(counts, (B,), dev, "counts"))
 
 
-class _on:
-    """Makes the cache's device current for a call; nothing to do when it is."""
-
-    def __init__(self, device):
-        import torch
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call_on(device, fn, args, stream):
+    """fn(*args, stream handle) with ``device`` current; raises for a status other than ATTN_OK.
+    A decode step's calls are short: the device guard is taken only when it changes something,
+    and the current stream's handle is asked for without making a Stream object."""
+    import torch
+    if stream is not None:
+        handle = stream.cuda_stream
+    else:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch._C._cuda_getDevice() == device.index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != ATTN_OK:
+        raise AttnError(st, fn.__name__)
 
 
 def _cache_rows(cache, k, v):
+    """(B, S, attn_dtype) of new rows."""
     if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must be [B, H_kv, S, d] of one dtype")
-    if k.shape[1] != cache.H_kv or k.shape[3] != cache.d:
-        raise ValueError("k has %d heads of width %d, the cache %d of %d"
-                         % (k.shape[1], k.shape[3], cache.H_kv, cache.d))
+    B, H, S, d = k.shape
+    if H != cache.H_kv or d != cache.d:
+        raise ValueError("k has %d heads of width %d, the cache %d of %d" % (H, d, cache.H_kv, cache.d))
     for t in (k, v):
         if not t.is_contiguous() or t.device != cache.device:
             raise ValueError("k and v must be contiguous tensors on %s" % cache.device)
+    return B, S, dtype_code(k.dtype)
 
 
 def cache_append(cache, k, v, table, pos, counts=None, stream=None):
@@ -570,15 +580,10 @@ def cache_append(cache, k, v, table, pos, counts=None, stream=None):
     [B, H_kv, S, d] into the cache behind the ``pos[b]`` tokens sequence b
     holds.  ``table`` [B, max_pages], ``pos`` and ``counts`` [B] are int32 CUDA
     tensors, read on the device."""
-    _cache_rows(cache, k, v)
-    B, _, S, _ = k.shape
-    width, cnt = _sequence_args(cache, table, pos, counts, B)
-    code = dtype_code(k.dtype)
-    with _on(cache.device):
-        st = load_library().attn_cache_append(cache.c, k.data_ptr(), v.data_ptr(), table.data_ptr(),
-                                              width, pos.data_ptr(), cnt, B, S, code,
-                                              _stream_handle(stream))
-    _check(st, "attn_cache_append")
+    B, S, code = _cache_rows(cache, k, v)
+    t, width, p, n = _sequence_args(cache, table, pos, counts, B)
+    _call_on(cache.device, load_library().attn_cache_append,
+             (cache.c, k.data_ptr(), v.data_ptr(), t, width, p, n, B, S, code), stream)
 
 
 def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
@@ -587,40 +592,49 @@ def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
     zero.  ``out`` is a pair of tensors to write instead of new ones."""
     import torch
     B = table.shape[0]
-    width, _ = _sequence_args(cache, table, lens, None, B)
+    t, width, n, _ = _sequence_args(cache, table, lens, None, B)
     dtype = torch.bfloat16 if dtype is None else dtype
     code = dtype_code(dtype)
     shape = (B, cache.H_kv, S, cache.d)
     if out is None:
-        out = (torch.empty(shape, dtype=dtype, device=cache.device),
-               torch.empty(shape, dtype=dtype, device=cache.device))
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
     else:
-        for t, name in zip(out, ("out[0]", "out[1]")):
-            _check_out(t, shape, dtype, cache.device, name)
-    k, v = out
-    with _on(cache.device):
-        st = load_library().attn_cache_read(cache.c, table.data_ptr(), width, lens.data_ptr(),
-                                            k.data_ptr(), v.data_ptr(), B, S, code,
-                                            _stream_handle(stream))
-    _check(st, "attn_cache_read")
+        k, v = out
+        _check_out(k, shape, dtype, cache.device, "out[0]")
+        _check_out(v, shape, dtype, cache.device, "out[1]")
+    _call_on(cache.device, load_library().attn_cache_read,
+             (cache.c, t, width, n, k.data_ptr(), v.data_ptr(), B, S, code), stream)
     return k, v
 
 
 def _cache_q(cache, q):
+    """(B, H, Sq) of queries."""
     if q.dim() != 4 or q.shape[3] != cache.d or q.shape[1] % cache.H_kv != 0 or q.shape[1] == 0:
         raise ValueError("q must be [B, H, Sq, %d] with H a multiple of %d, got %s"
                          % (cache.d, cache.H_kv, tuple(q.shape)))
     if not q.is_contiguous() or q.device != cache.device:
         raise ValueError("q must be a contiguous tensor on %s" % cache.device)
+    return q.shape[:3]
+
+
+@functools.lru_cache(maxsize=None)
+def _need(size, *args):
+    """Bytes of a workspace: ``size`` depends on its arguments alone."""
+    st, need = size(*args)
+    _check(st, size.__name__)
+    return need
 
 
 def _workspace(workspace, need, device):
+    """(tensor, pointer, bytes) of the scratch of one call."""
     import torch
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
     if not workspace.is_contiguous() or _device_of(workspace) != device:
         raise ValueError("workspace must be a contiguous tensor on %s" % device)
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def cache_select(q, cache, table, lens, n_select, counts=None, causal: bool = True, workspace=None,
@@ -628,24 +642,19 @@ def cache_select(q, cache, table, lens, n_select, counts=None, causal: bool = Tr
     """The ``n_select`` pages each query attends to (attn_cache_select): int32
     [B, H_kv, Sq, n_select], ascending, -1 where fewer are visible."""
     import torch
-    _cache_q(cache, q)
+    B, H, Sq = _cache_q(cache, q)
     if cache.k_bounds is None:
         raise ValueError("the cache keeps no k_bounds")
-    B, H, Sq, _ = q.shape
-    width, cnt = _sequence_args(cache, table, lens, counts, B)
-    code = dtype_code(q.dtype)
-    st, need = attn_cache_select_workspace_size(B, cache.H_kv, Sq, width)
-    _check(st, "attn_cache_select_workspace_size")
-    workspace = _workspace(workspace, need, cache.device)
     if n_select < 1:
         raise ValueError("n_select must be at least 1, got %d" % n_select)
+    t, width, p, n = _sequence_args(cache, table, lens, counts, B)
+    code = dtype_code(q.dtype)
+    ws, wp, wn = _workspace(workspace, _need(attn_cache_select_workspace_size, B, cache.H_kv, Sq, width),
+                            cache.device)
     pages = torch.empty((B, cache.H_kv, Sq, n_select), dtype=torch.int32, device=cache.device)
-    with _on(cache.device):
-        st = load_library().attn_cache_select(
-            cache.c, q.data_ptr(), table.data_ptr(), width, lens.data_ptr(), cnt, pages.data_ptr(),
-            n_select, B, H, Sq, int(causal), code, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    _check(st, "attn_cache_select")
+    _call_on(cache.device, load_library().attn_cache_select,
+             (cache.c, q.data_ptr(), t, width, p, n, pages.data_ptr(), n_select, B, H, Sq,
+              1 if causal else 0, code, wp, wn), stream)
     return pages
 
 
@@ -657,28 +666,20 @@ def attention_cache(q, cache, table, lens, counts=None, causal: bool = True,
     ``counts[b]`` (default Sq) of the ``lens[b]`` tokens are the queries' own.
     The workspace is allocated here unless given.  Returns (o, lse)."""
     import torch
-    _cache_q(cache, q)
-    B, H, Sq, d = q.shape
-    width, cnt = _sequence_args(cache, table, lens, counts, B)
+    B, H, Sq = _cache_q(cache, q)
+    t, width, p, n = _sequence_args(cache, table, lens, counts, B)
     code = dtype_code(q.dtype, out_dtype)
-    n = 0
+    listed, n_select = None, 0
     if pages is not None:
-        n = pages.shape[-1]
-        if (tuple(pages.shape) != (B, cache.H_kv, Sq, n) or n < 1 or pages.dtype != torch.int32
-                or not pages.is_contiguous() or pages.device != cache.device):
-            raise ValueError("pages must be a contiguous int32 tensor [%d, %d, %d, n] on %s"
-                             % (B, cache.H_kv, Sq, cache.device))
-    st, need = attn_fwd_cache_workspace_size(B, H, cache.H_kv, Sq, d, code, n)
-    _check(st, "attn_fwd_cache_workspace_size")
-    workspace = _workspace(workspace, need, cache.device)
-    out = torch.empty((B, H, Sq, d), dtype=q.dtype if out_dtype is None else out_dtype,
-                      device=cache.device)
+        n_select = pages.shape[-1]
+        if n_select < 1:
+            raise ValueError("pages must list at least one page")
+        listed = _int32_on(pages, (B, cache.H_kv, Sq, n_select), cache.device, "pages")
+    ws, wp, wn = _workspace(workspace, _need(attn_fwd_cache_workspace_size, B, H, cache.H_kv, Sq,
+                                             cache.d, code, n_select), cache.device)
+    out = torch.empty_like(q) if out_dtype is None else torch.empty_like(q, dtype=out_dtype)
     lse = torch.empty((B, H, Sq), dtype=torch.float32, device=cache.device)
-    with _on(cache.device):
-        st = load_library().attn_fwd_cache(
-            cache.c, q.data_ptr(), out.data_ptr(), lse.data_ptr(), table.data_ptr(), width,
-            lens.data_ptr(), cnt, pages.data_ptr() if pages is not None else None, n, B, H, Sq,
-            int(causal), 0.0 if scale is None else float(scale), code, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    _check(st, "attn_fwd_cache")
+    _call_on(cache.device, load_library().attn_fwd_cache,
+             (cache.c, q.data_ptr(), out.data_ptr(), lse.data_ptr(), t, width, p, n, listed, n_select,
+              B, H, Sq, 1 if causal else 0, 0.0 if scale is None else float(scale), code, wp, wn), stream)
     return out, lse
