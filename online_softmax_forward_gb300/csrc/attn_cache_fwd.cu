@@ -6,12 +6,13 @@
 //
 // Work.  A unit is (sequence, kv head, block of query rows): the G query heads
 // of a kv head share its keys, so the rows of a block are (query, head of the
-// group).  Its keys are walked in tiles of KT keys.  All tiles of a call are
-// numbered through and cut into equal contiguous ranges, one per warp
-// (cache_index.h): ragged lengths and few sequences fill the GPU alike.  A
-// warp writes the units it covers alone, and leaves a partial state (o, lse)
-// for the at most two it shares; a second kernel joins those with the online
-// softmax's merge of states.
+// group).  Its keys are walked in tiles of KT keys (a page, or 64 of its 128).
+// All tiles of a call are numbered through and cut into equal contiguous
+// ranges, one per warp (cache_index.h): ragged lengths and few sequences fill
+// the GPU alike.  A warp writes the units it covers alone.  Of the units that
+// several warps of a CTA share the states are joined in shared memory, and a
+// second kernel joins the at most one unit that runs over the end of each CTA's
+// range, with the online softmax's merge of states.
 //
 // Products.  The 8-bit codes are exact in fp16, so both products run on
 // mma.m16n8k16 with fp32 accumulation and no dequantised tile exists
@@ -26,11 +27,14 @@
 // q rows are first multiplied by a power of two that puts the row's largest
 // magnitude in [2^14, 2^15): any fp32 or bf16 exponent then fits fp16.
 //
-// Fragments are loaded straight from global memory: the MMA's k index may name
-// the channels in any order that q and k share, and its n index any channel
-// of v.  Lane (g, t) = (lane / 4, lane % 4) reads D/4 consecutive bytes of key
-// row g (a whole row per 4 lanes), and D/8 consecutive bytes of value rows
-// 2t, 2t+1, 2t+8, 2t+9 (a whole row per 8 lanes), with 16-byte loads.
+// Loads.  Each warp copies its own tiles into a ring of shared memory slots with
+// 16-byte cp.async (a slot holds the codes of one tile's keys or values), all
+// slots but the one in use in flight, and waits for nobody else.  The MMA's k
+// index may name the channels in any order that q and k share, and its n index
+// any channel of v: lane (g, t) = (lane / 4, lane % 4) reads D/4 consecutive
+// bytes of key row g, and D/8 consecutive bytes of value rows 2t, 2t+1, 2t+8,
+// 2t+9.  The 16-byte pieces of a row are swizzled so that both reads are free of
+// bank conflicts.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -45,6 +49,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kRing = 24 * 1024;  // shared memory of each warp's tiles, later of its states
 constexpr int kMinTiles = 1;  // tiles per worker when there are few
 
 struct FwdArgs {
@@ -54,8 +59,9 @@ struct FwdArgs {
     const uint8_t *k, *v;
     const float *ks, *vs;
     const int32_t *table, *lens, *counts, *pages;
-    int64_t *prefix;  // [B + 1] tiles before each sequence (all pages)
-    float *po, *pl;   // partial states by slot: [slot][R][D], [slot][R] (log2)
+    float *hold;      // [warp][R][D]: state of the unit a warp's range begins inside of, if more follows
+    float *po, *pl;   // states of the CTAs' shared units by slot: [slot][R][D], [slot][R] (log2)
+    int4 *tail;       // [2 * CTA]: the unit that runs over the end of a CTA's range
     int B, Hkv, G, Sq, page, n_pages, max_pages, n_sel, causal;
     int nseg, rows, nrb;  // row groups of a (sequence, kv head), rows of one, row blocks of one
     int dtype, workers;
@@ -68,17 +74,32 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint4 ldg16(const uint8_t *p) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
     uint4 u;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(p));
     return u;
 }
-__device__ __forceinline__ uint2 ldg8(const uint8_t *p) {
+__device__ __forceinline__ uint2 lds8(uint32_t p) {
     uint2 u;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(u.x), "=r"(u.y) : "l"(p));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(p));
     return u;
+}
+// Byte offset of 16-byte piece c of row r in a slot.  D = 128: pieces are
+// exchanged within a row by r & 7; D = 64: within a pair of rows (128 bytes) by
+// the pair's number.
+template <int D>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+    if constexpr (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+    else return (uint32_t)((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ ((r >> 1 & 3) * 2)) << 4));
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -288,6 +309,23 @@ __device__ __forceinline__ void store_o8(const FwdArgs &a, size_t i, const float
     }
 }
 
+// Row of o and lse that row r of a unit is; false past the group's rows.
+template <int R>
+__device__ __forceinline__ bool out_row(const FwdArgs &a, const Unit &u, int r, size_t &row) {
+    int i, h;
+    if (!row_of<R>(a, u, r, i, h)) return false;
+    row = ((size_t)u.b * a.Hkv * a.G + h) * a.Sq + i;
+    return in_bounds(i < a.Sq && h < a.Hkv * a.G && u.b < a.B, a.status);
+}
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// One output.
+__device__ __forceinline__ void store_o(const FwdArgs &a, size_t i, float x) {
+    if (a.dtype == ATTN_BF16) reinterpret_cast<__nv_bfloat16 *>(a.o)[i] = __float2bfloat16_rn(x);
+    else if (a.dtype == ATTN_F16) reinterpret_cast<__half *>(a.o)[i] = __float2half_rn(x);
+    else reinterpret_cast<float *>(a.o)[i] = x;
+}
+
 // WIDE = 0: the 8-row form, 1: the 16-row form.
 template <int D, int FMT, int WIDE, int KT>
 __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a) {
@@ -298,13 +336,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
     constexpr int KS = KT / 16;        // k steps of P.V
     constexpr int QS = D / 16;         // k steps of Q.K
     constexpr int VT = D / 8;          // output tiles of 8 channels
-    constexpr int VW = D / 32;         // words of a lane's value row
-    extern __shared__ int64_t prefix[];  // [B + 1]
+    constexpr int SLOT = KT * D;       // bytes of a tile's keys or values
+    constexpr int NS = kRing / SLOT < 8 ? kRing / SLOT : 8;
+    static_assert(NS >= 3 && R * D * 4 <= kRing, "a warp's ring later holds a state");
+    extern __shared__ __align__(128) uint8_t sm[];
+    int64_t *prefix = reinterpret_cast<int64_t *>(sm + kWarps * kRing);  // [B + 1]
     __shared__ int64_t warp_sums[kWarps];
+    __shared__ float s_lse[kWarps][2][R];
+    __shared__ Unit s_unit[kWarps][2];
+    __shared__ const float *s_keep[kWarps][2];
+    __shared__ int64_t s_end[kWarps];   // past the warp's last tile
+    __shared__ int s_has[kWarps];       // bit 0: a state of a unit begun before, bit 1: of one that goes on
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int64_t tpu = a.pages ? (int64_t)a.n_sel * (a.page / KT) : 0;
     const int64_t units = (int64_t)a.Hkv * a.nseg * a.nrb;  // of one sequence
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     int64_t total;
     if (a.pages) {
         total = a.B * units * tpu;
@@ -319,51 +366,56 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
         scan_lengths(a, KT, prefix, warp_sums);
         __syncthreads();
         total = prefix[a.B] * units;
-        if (blockIdx.x == 0)
-            for (int b = threadIdx.x; b <= a.B; b += kThreads) a.prefix[b] = prefix[b];
+        // sequences without a token have no tile: o = 0, lse = -inf
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            if (prefix[b] != prefix[b + 1]) continue;
+            const size_t row0 = (size_t)b * a.Hkv * a.G * a.Sq, n = (size_t)a.Hkv * a.G * a.Sq;
+            const float z[8] = {};
+            for (size_t e = threadIdx.x; e < n * (D / 8); e += kThreads) store_o8(a, row0 * D + e * 8, z);
+            if (a.lse)
+                for (size_t e = threadIdx.x; e < n; e += kThreads) a.lse[row0 + e] = -INFINITY;
+        }
     }
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int64_t workers = worker_count(total, a.workers, kMinTiles);
-    // neighbouring ranges on different SMs, so that few tiles spread widely
-    const int64_t w = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-    if (w >= workers) return;
-    const int64_t x0 = worker_begin(w, total, workers), x1 = worker_begin(w + 1, total, workers);
-    if (x0 >= x1) return;
+    const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+    int64_t x0 = 0, x1 = 0;
+    if (w < workers && total > 0) {
+        x0 = worker_begin(w, total, workers);
+        x1 = worker_begin(w + 1, total, workers);
+    }
+    if (lane == 0) {
+        s_has[warp] = 0;
+        s_end[warp] = x1;
+    }
 
     // tiles x0 + 32 n + lane, and the next 32
     Tile cur = {-1, 0, 0.f, 0.f}, nxt = cur;
     if (x0 + lane < x1) cur = find_tile<R, KT>(a, prefix, tpu, x0 + lane);
 
-    uint4 kr[KT * D / 512];
-    constexpr int VN = KS * 4;
-    uint32_t vr[VN][VW];
-    auto load_k = [&](int at) {
-        const uint8_t *p = a.k + (size_t)at * KT * D + g * D + t * (D / 4);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + warp * kRing);
+    // slot s: keys (even s) or values (odd s) of the range's tile s / 2; `from` is
+    // the lane's register that holds tile s / 2's place in the pool
+    auto issue = [&](int s, int buf, int n_tiles, int base) {
+        const int j = s >> 1;
+        const int held = j - base;  // < 64
+        const int at = __shfl_sync(0xffffffffu, held < 32 ? cur.at : nxt.at, held & 31);
+        if (j < n_tiles && at >= 0) {
+            const uint8_t *src = ((s & 1) ? a.v : a.k) + (size_t)at * SLOT;
+            const uint32_t dst = ring + buf * SLOT;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) kr[n * (D / 64) + c] = ldg16(p + n * 8 * D + c * 16);
-    };
-    auto load_v = [&](int at) {
-        const uint8_t *p = a.v + (size_t)at * KT * D + g * (D / 8);
-#pragma unroll
-        for (int n = 0; n < VN; ++n) {
-            const int row = (n / 4) * 16 + 2 * t + (n & 1) + ((n & 2) ? 8 : 0);
-            if constexpr (VW == 4) {
-                const uint4 u = ldg16(p + row * D);
-                vr[n][0] = u.x; vr[n][1] = u.y; vr[n][2] = u.z; vr[n][3] = u.w;
-            } else {
-                const uint2 u = ldg8(p + row * D);
-                vr[n][0] = u.x; vr[n][1] = u.y;
+            for (int e = 0; e < SLOT / 512; ++e) {
+                const int c = e * 32 + lane;
+                cp_async16(dst + swizzled<D>(c / (D / 16), c % (D / 16)), src + c * 16);
             }
         }
+        cp_async_commit();
     };
-    {
-        const int at = __shfl_sync(0xffffffffu, cur.at, 0);
-        if (at >= 0) {
-            load_k(at);
-            load_v(at);
-        }
+    const int n_tiles = (int)(x1 - x0);
+    int put = 0, get = 0;  // ring buffers: next to fill, next to read
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+        issue(s, s, n_tiles, 0);
+        put = s + 1;
     }
 
     int64_t x = x0;
@@ -441,38 +493,45 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                 nxt.at = -1;
                 if (x + 32 + lane < x1) nxt = find_tile<R, KT>(a, prefix, tpu, x + 32 + lane);
             }
+            const int base = i & ~31;
             const int at = __shfl_sync(0xffffffffu, cur.at, i & 31);
             const int key0 = __shfl_sync(0xffffffffu, cur.key0, i & 31);
             const float ks = __shfl_sync(0xffffffffu, cur.ks, i & 31);
             const float vs = __shfl_sync(0xffffffffu, cur.vs, i & 31);
-            const int ahead = ((i + 1) & 31) ? __shfl_sync(0xffffffffu, cur.at, (i + 1) & 31)
-                                             : __shfl_sync(0xffffffffu, nxt.at, 0);
-            const int next = x + 1 < x1 ? ahead : -1;
-            if (at < 0) {
-                if (next >= 0) {
-                    load_k(next);
-                    load_v(next);
-                }
-                continue;
-            }
+
+            // keys: the buffer read last is free again, every lane has passed its __syncwarp
+            issue(2 * i + NS - 1, put, n_tiles, base);
+            put = put + 1 == NS ? 0 : put + 1;
+            cp_async_wait<NS - 1>();
+            __syncwarp();
             float s[NT][4];
+            if (at >= 0) {
+                const uint32_t kb = ring + get * SLOT;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+                for (int n = 0; n < NT; ++n) {
+                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const uint4 u4 = kr[n * (D / 64) + c];
-                    const uint32_t words[4] = {u4.x, u4.y, u4.z, u4.w};
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint4 u4 = lds16(kb + swizzled<D>(n * 8 + g, t * (D / 64) + c));
+                        const uint32_t words[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t b0, b1;
-                        U::quad(words[e], b0, b1);
-                        const int st = c * 4 + e;
-                        mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b0, b1);
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t b0, b1;
+                            U::quad(words[e], b0, b1);
+                            const int st = c * 4 + e;
+                            mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b0, b1);
+                        }
                     }
                 }
             }
-            if (next >= 0) load_k(next);
+            get = get + 1 == NS ? 0 : get + 1;
+            __syncwarp();
+            issue(2 * i + NS, put, n_tiles, base);
+            put = put + 1 == NS ? 0 : put + 1;
+            if (at < 0) {
+                get = get + 1 == NS ? 0 : get + 1;
+                continue;
+            }
 
             uint32_t pa[KS][4];
             float alpha[H], sv[H];
@@ -493,13 +552,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float mn = fmaxf(m[hh], mx);
-                const float base = mn == -INFINITY ? 0.f : mn;
-                alpha[hh] = ex2(m[hh] - base);  // 0 while nothing has been seen
+                const float top = mn == -INFINITY ? 0.f : mn;
+                alpha[hh] = ex2(m[hh] - top);  // 0 while nothing has been seen
                 m[hh] = mn;
                 float sum = 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float p0 = ex2(y[n][0] - base), p1 = ex2(y[n][1] - base);
+                    const float p0 = ex2(y[n][0] - top), p1 = ex2(y[n][1] - top);
                     sum += p0 + p1;
                     // 2^15: small weights stay above fp16's subnormals
                     const uint32_t hi = pack_f16(p0 * 32768.f, p1 * 32768.f);
@@ -515,49 +574,73 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                 // a page no key of which the row sees adds nothing, not even its scale's NaN
                 sv[hh] = key0 < lim[hh] ? vs * (U::kUnit / 32768.f) : 0.f;
             }
-            // o, four channel tiles (one word of each value row) at a time
+            cp_async_wait<NS - 1>();
+            __syncwarp();
+            {
+                const uint32_t vb = ring + get * SLOT;
+                float c[VT][4];
 #pragma unroll
-            for (int wd = 0; wd < VW; ++wd) {
-                float c[4][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c[e][0] = c[e][1] = c[e][2] = c[e][3] = 0.f;
+                for (int n = 0; n < VT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
 #pragma unroll
                 for (int st = 0; st < KS; ++st) {
-                    const uint32_t r0 = vr[4 * st][wd], r1 = vr[4 * st + 1][wd];
-                    const uint32_t r2 = vr[4 * st + 2][wd], r3 = vr[4 * st + 3][wd];
-                    mma16816(c[0], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<0>(r0, r1), U::template pair<0>(r2, r3));
-                    mma16816(c[1], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<1>(r0, r1), U::template pair<1>(r2, r3));
-                    mma16816(c[2], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<2>(r0, r1), U::template pair<2>(r2, r3));
-                    mma16816(c[3], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<3>(r0, r1), U::template pair<3>(r2, r3));
+                    uint32_t r[4][D / 32];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = st * 16 + 2 * t + (e & 1) + ((e & 2) ? 8 : 0);
+                        if constexpr (D == 128) {
+                            const uint4 u4 = lds16(vb + swizzled<D>(row, g));
+                            r[e][0] = u4.x; r[e][1] = u4.y; r[e][2] = u4.z; r[e][3] = u4.w;
+                        } else {
+                            const uint2 u2 = lds8(vb + swizzled<D>(row, g >> 1) + (g & 1) * 8);
+                            r[e][0] = u2.x; r[e][1] = u2.y;
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        const uint32_t r0 = r[0][q], r1 = r[1][q], r2 = r[2][q], r3 = r[3][q];
+                        mma16816(c[4 * q], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<0>(r0, r1), U::template pair<0>(r2, r3));
+                        mma16816(c[4 * q + 1], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<1>(r0, r1), U::template pair<1>(r2, r3));
+                        mma16816(c[4 * q + 2], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<2>(r0, r1), U::template pair<2>(r2, r3));
+                        mma16816(c[4 * q + 3], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<3>(r0, r1), U::template pair<3>(r2, r3));
+                    }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float *o = acc[4 * wd + e];
+                for (int n = 0; n < VT; ++n) {
+                    float *o = acc[n];
                     if constexpr (WIDE) {
-                        o[0] = fmaf(sv[0], c[e][0], o[0] * alpha[0]);
-                        o[1] = fmaf(sv[0], c[e][1], o[1] * alpha[0]);
-                        o[2] = fmaf(sv[1], c[e][2], o[2] * alpha[1]);
-                        o[3] = fmaf(sv[1], c[e][3], o[3] * alpha[1]);
+                        o[0] = fmaf(sv[0], c[n][0], o[0] * alpha[0]);
+                        o[1] = fmaf(sv[0], c[n][1], o[1] * alpha[0]);
+                        o[2] = fmaf(sv[1], c[n][2], o[2] * alpha[1]);
+                        o[3] = fmaf(sv[1], c[n][3], o[3] * alpha[1]);
                     } else {
-                        o[0] = fmaf(sv[0], c[e][0] + c[e][2], o[0] * alpha[0]);
-                        o[1] = fmaf(sv[0], c[e][1] + c[e][3], o[1] * alpha[0]);
+                        o[0] = fmaf(sv[0], c[n][0] + c[n][2], o[0] * alpha[0]);
+                        o[1] = fmaf(sv[0], c[n][1] + c[n][3], o[1] * alpha[0]);
                     }
                 }
             }
-            if (next >= 0) load_v(next);
+            get = get + 1 == NS ? 0 : get + 1;
+            __syncwarp();  // the buffer may be filled again
         }
 
-        // the unit's state so far: written if it is whole, else left for the merge
+        // the unit's state: written if it is whole, else kept for the join.  The range's last unit
+        // leaves it in the ring, which is not needed any more; a first unit that more follow, in
+        // global memory.
         const bool whole = u.begin >= x0 && u.end <= x1;
-        const int64_t slot = partial_slot(w, u.begin < x0);
+        const bool before = u.begin < x0;
+        float *keep = xe < x1 ? a.hold + w * R * D : reinterpret_cast<float *>(sm + warp * kRing);
+        if (!in_bounds(w < (int64_t)gridDim.x * kWarps, a.status)) break;
+        if (xe == x1) {
+            cp_async_wait<0>();
+            __syncwarp();
+        }
 #pragma unroll
         for (int hh = 0; hh < H; ++hh) {
             float sum = l[hh];
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: no key was visible
-            const float base = m[hh] == -INFINITY ? 0.f : m[hh];
-            const float lse2 = sum == 0.f ? -INFINITY : base + log2f(sum);
+            const float top = m[hh] == -INFINITY ? 0.f : m[hh];
+            const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
             const int r = g + 8 * hh;
             float f[D / 4];
 #pragma unroll
@@ -566,72 +649,110 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                 f[VT + n] = acc[n][2 * hh + 1] * inv;
             }
             if (whole) {
-                int i, h;
-                if (!row_of<R>(a, u, r, i, h)) continue;
-                const size_t row = ((size_t)u.b * a.Hkv * a.G + h) * a.Sq + i;
-                if (!in_bounds(i < a.Sq && h < a.Hkv * a.G, a.status)) continue;
+                size_t row;
+                if (!out_row<R>(a, u, r, row)) continue;
 #pragma unroll
                 for (int e = 0; e < D / 4; e += 8) store_o8(a, row * D + t * (D / 4) + e, f + e);
-                if (a.lse && t == 0) a.lse[row] = lse2 * 0.69314718055994530942f;
-            } else if (in_bounds(slot < 2 * (int64_t)a.workers, a.status)) {
-                float4 *p = reinterpret_cast<float4 *>(a.po + (slot * R + r) * D + t * (D / 4));
+                if (a.lse && t == 0) a.lse[row] = lse2 * kLn2;
+            } else {
+                float4 *p = reinterpret_cast<float4 *>(keep + r * D + t * (D / 4));
 #pragma unroll
                 for (int e = 0; e < D / 16; ++e) p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                if (t == 0) a.pl[slot * R + r] = lse2;
+                if (t == 0) s_lse[warp][before ? 0 : 1][r] = lse2;
+            }
+        }
+        if (!whole && lane == 0) {
+            s_unit[warp][before ? 0 : 1] = u;
+            s_keep[warp][before ? 0 : 1] = keep;
+            s_has[warp] |= before ? 1 : 2;
+        }
+    }
+    __syncthreads();
+
+    // Join the states of the CTA's shared units.  A group is a unit's pieces: a
+    // state that goes on (or, from warp 0, one begun in an earlier CTA) and the
+    // following warps' states of the same unit.  Each warp takes rows warp, warp + 8.
+    int64_t X1 = 0;  // past the CTA's last tile
+    for (int k = 0; k < kWarps; ++k) X1 = s_end[k] > X1 ? s_end[k] : X1;
+    bool over = false;
+    for (int first = 0; first < kWarps; ++first) {
+#pragma unroll 1
+        for (int side = first == 0 ? 0 : 1; side < 2; ++side) {
+            if (!(s_has[first] & (1 << side))) continue;
+            const Unit u = s_unit[first][side];
+            int n = 1;  // pieces
+            if (u.end > s_end[first])
+                while (first + n < kWarps && (s_has[first + n] & 1) && s_unit[first + n][0].begin == u.begin) {
+                    ++n;
+                    if (u.end <= s_end[first + n - 1]) break;
+                }
+            const bool earlier = side == 0, later = u.end > X1;
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (earlier ? 0 : 1);
+            over = over || (later && !earlier);
+            if (later && !earlier && threadIdx.x == 0) {
+                const int last = (int)(worker_of(u.end - 1, total, workers) / kWarps);
+                a.tail[2 * blockIdx.x] = make_int4(1, last, u.b, u.hk);
+                a.tail[2 * blockIdx.x + 1] = make_int4(u.seg, u.rb, 0, 0);
+            }
+#pragma unroll 1
+            for (int r = warp; r < R; r += kWarps) {
+                float M = -INFINITY;
+                for (int k = 0; k < n; ++k) M = fmaxf(M, s_lse[first + k][k == 0 ? side : 0][r]);
+                const float top = M == -INFINITY ? 0.f : M;
+                float L = 0.f, o[D / 32] = {};
+                for (int k = 0; k < n; ++k) {
+                    const int sd = k == 0 ? side : 0;
+                    const float wt = ex2(s_lse[first + k][sd][r] - top);
+                    const float *src = s_keep[first + k][sd] + r * D + lane;
+                    L += wt;
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(wt, src[32 * e], o[e]);
+                }
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                const float lse2 = L == 0.f ? -INFINITY : top + log2f(L);
+                if (earlier || later) {
+                    if (!in_bounds(slot < 2 * (int64_t)gridDim.x, a.status)) continue;
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) a.po[(slot * R + r) * D + lane + 32 * e] = o[e] * inv;
+                    if (lane == 0) a.pl[slot * R + r] = lse2;
+                } else {
+                    size_t row;
+                    if (!out_row<R>(a, u, r, row)) continue;
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) store_o(a, row * D + lane + 32 * e, o[e] * inv);
+                    if (a.lse && lane == 0) a.lse[row] = lse2 * kLn2;
+                }
             }
         }
     }
+    if (!over && threadIdx.x == 0) a.tail[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
 }
 
-// Joins the partial states of one row: one CTA per (unit, row of the block).
-// A unit that one warp covered has been written; a sequence without keys gets
-// o = 0, lse = -inf here.
-template <int D, int R, int KT>
+// Joins the states of the unit that runs over the end of CTA blockIdx.x's
+// range: the CTA's own and those of the CTAs up to the one that holds the
+// unit's end.  One CTA per (range end, row of the block).
+template <int D, int R>
 __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) {
-    extern __shared__ float wts[];  // [workers]
+    __shared__ float wts[kCacheMaxCtas];
     __shared__ float red[kWarps];
     __shared__ float part[kWarps][D];
-    const int64_t per = (int64_t)a.Hkv * a.nseg * a.nrb;
-    const int64_t unit = blockIdx.x;
-    Unit u;
-    u.b = (int)(unit / per);
-    const int64_t idx = unit % per;
-    u.hk = (int)(idx / (a.nseg * a.nrb));
-    u.seg = (int)(idx % (a.nseg * a.nrb) / a.nrb);
-    u.rb = (int)(idx % a.nrb);
-    const int r = blockIdx.y;
-    int i, h;
-    const bool real = row_of<R>(a, u, r, i, h);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!real) return;
-    int64_t total;
-    if (a.pages) {
-        const int64_t tpu = (int64_t)a.n_sel * (a.page / KT);
-        total = a.B * per * tpu;
-        u.begin = unit * tpu;
-        u.end = u.begin + tpu;
-    } else {
-        const int64_t p0 = a.prefix[u.b], p1 = a.prefix[u.b + 1];
-        total = a.prefix[a.B] * per;
-        u.begin = p0 * per + idx * (p1 - p0);
-        u.end = u.begin + (p1 - p0);
-    }
-    const size_t row = ((size_t)u.b * a.Hkv * a.G + h) * a.Sq + i;
-    if (!in_bounds(i < a.Sq && h < a.Hkv * a.G, a.status)) return;
+    const int4 d0 = a.tail[2 * blockIdx.x];
+    if (!d0.x) return;
+    const int4 d1 = a.tail[2 * blockIdx.x + 1];
+    Unit u;
+    u.b = d0.z;
+    u.hk = d0.w;
+    u.seg = d1.x;
+    u.rb = d1.y;
+    const int r = blockIdx.y;
+    size_t row;
+    if (!out_row<R>(a, u, r, row)) return;
+    const int n = d0.y - (int)blockIdx.x + 1;
+    if (!in_bounds(n <= kCacheMaxCtas, a.status)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (u.begin == u.end) {
-        if (threadIdx.x < D / 8) {
-            const float z[8] = {};
-            store_o8(a, row * D + threadIdx.x * 8, z);
-        }
-        if (a.lse && threadIdx.x == 0) a.lse[row] = -INFINITY;
-        return;
-    }
-    const int64_t workers = worker_count(total, a.workers, kMinTiles);
-    const int64_t w0 = worker_of(u.begin, total, workers), w1 = worker_of(u.end - 1, total, workers);
-    if (w0 == w1) return;
-    const int n = (int)(w1 - w0 + 1);
-    auto slot = [&](int p) { return partial_slot(w0 + p, p > 0); };
+    // the owner's state lies in its second slot, the others' in their first
+    auto slot = [&](int p) { return 2 * (int64_t)(blockIdx.x + p) + (p == 0 ? 1 : 0); };
     float M = -INFINITY;
     for (int p = threadIdx.x; p < n; p += kThreads) {
         wts[p] = a.pl[slot(p) * R + r];
@@ -643,74 +764,68 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) 
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) M = fmaxf(M, red[k]);
-    const float base = M == -INFINITY ? 0.f : M;
+    const float top = M == -INFINITY ? 0.f : M;
     // every warp sums all weights in the same order, and its own parts' o
     float L = 0.f;
-    for (int p = lane; p < n; p += 32) L += ex2(wts[p] - base);
+    for (int p = lane; p < n; p += 32) L += ex2(wts[p] - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     constexpr int C = D / 32;
     float acc[C] = {};
 #pragma unroll 4
     for (int p = warp; p < n; p += kWarps) {
-        const float wt = ex2(wts[p] - base);
-        const float *src = a.po + (slot(p) * R + r) * D + lane * C;
-        float v[C];
-        if constexpr (C == 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(src);
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        } else {
-            const float2 x = *reinterpret_cast<const float2 *>(src);
-            v[0] = x.x; v[1] = x.y;
-        }
+        const float wt = ex2(wts[p] - top);
+        const float *src = a.po + (slot(p) * R + r) * D + lane;
 #pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] = fmaf(wt, v[c], acc[c]);
+        for (int c = 0; c < C; ++c) acc[c] = fmaf(wt, src[32 * c], acc[c]);
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) part[warp][lane * C + c] = acc[c];
+    for (int c = 0; c < C; ++c) part[warp][lane + 32 * c] = acc[c];
     __syncthreads();
-    if (threadIdx.x < D / 8) {
+    if (threadIdx.x < D) {
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        float f[8];
+        float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) sum += part[k][threadIdx.x * 8 + e];
-            f[e] = sum * inv;
-        }
-        store_o8(a, row * D + threadIdx.x * 8, f);
-        if (a.lse && threadIdx.x == 0)
-            a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * 0.69314718055994530942f;
+        for (int k = 0; k < kWarps; ++k) sum += part[k][threadIdx.x];
+        store_o(a, row * D + threadIdx.x, sum * inv);
+        if (a.lse && threadIdx.x == 0) a.lse[row] = L == 0.f ? -INFINITY : (top + log2f(L)) * kLn2;
     }
 }
 
 template <int D, int FMT, int WIDE, int KT>
-int launch_fwd_t(FwdArgs &a, unsigned grid, cudaStream_t stream) {
+int launch_fwd_t(const FwdArgs &a, unsigned grid, cudaStream_t stream) {
     constexpr int R = WIDE ? 16 : 8;
     auto fwd = cache_fwd_kernel<D, FMT, WIDE, KT>;
-    const size_t smem = a.pages ? 0 : (size_t)(a.B + 1) * 8;
-    fwd<<<grid, kThreads, smem, stream>>>(a);
+    constexpr size_t ring = (size_t)kWarps * kRing;
+    if (!set_smem_limit_once(reinterpret_cast<const void *>(fwd), (int)(ring + (kMaxCacheBatch + 1) * 8)))
+        return ATTN_ERR_LAUNCH;
+    fwd<<<grid, kThreads, ring + (a.pages ? 0 : ((size_t)a.B + 1) * 8), stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
-    const int64_t units = (int64_t)a.B * a.Hkv * a.nseg * a.nrb;
-    cfg.gridDim = dim3((unsigned)units, (unsigned)(a.rows < R ? a.rows : R));
+    cfg.gridDim = dim3(grid, (unsigned)(a.rows < R ? a.rows : R));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)a.workers * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, R, KT>, (const FwdArgs)a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, R>, a);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
+// Keys of a tile: a page, at most 64 (the work per tile beside its keys is
+// then spread over twice as many as with 32), or 32 for the 16-row form at
+// d = 128, whose 64 keys do not fit the registers.
+constexpr int tile_keys(int d, bool wide, int page) {
+    return page < 64 ? page : (wide && d == 128 ? 32 : 64);
+}
+
 template <int D, int FMT>
-int launch_fwd_w(FwdArgs &a, bool wide, int kt, unsigned grid, cudaStream_t s) {
-    if (wide) return kt == 16 ? launch_fwd_t<D, FMT, 1, 16>(a, grid, s) : launch_fwd_t<D, FMT, 1, 32>(a, grid, s);
-    return kt == 16 ? launch_fwd_t<D, FMT, 0, 16>(a, grid, s) : launch_fwd_t<D, FMT, 0, 32>(a, grid, s);
+int launch_fwd_w(const FwdArgs &a, bool wide, int kt, unsigned grid, cudaStream_t s) {
+#define ATTN_KT(W)                                                    (kt == 16   ? launch_fwd_t<D, FMT, W, 16>(a, grid, s)              : kt == 32 ? launch_fwd_t<D, FMT, W, 32>(a, grid, s)                         : launch_fwd_t<D, FMT, W, 64>(a, grid, s))
+    return wide ? ATTN_KT(1) : ATTN_KT(0);
+#undef ATTN_KT
 }
 
 }  // namespace
@@ -719,12 +834,11 @@ int launch_fwd_w(FwdArgs &a, bool wide, int kt, unsigned grid, cudaStream_t s) {
 // rows do not fit eight.
 static bool cache_wide(int rows, int dtype) { return dtype == ATTN_BF16 && rows > 8; }
 
-// Workspace: the tile counts [B + 1], then two partial states per worker.
+// Workspace: the tails [2 * CTA], a state per warp, two per CTA and their lse.
 size_t cache_fwd_workspace(int B, int H, int H_kv, int Sq, int d, int dtype, bool listed) {
     const int64_t rows = (int64_t)(H / H_kv) * (listed ? 1 : Sq);
     const size_t R = cache_wide((int)(rows > 16 ? 16 : rows), dtype) ? 16 : 8;
-    const size_t prefix = (((size_t)B + 1) * 8 + 15) / 16 * 16;
-    return prefix + (size_t)2 * kCacheMaxCtas * kWarps * R * (d + 1) * 4;
+    return (size_t)kCacheMaxCtas * (32 + (kWarps + 2) * R * d * 4 + 2 * R * 4);
 }
 
 int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, const int32_t *table,
@@ -748,7 +862,7 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     const int64_t units = (int64_t)B * a.Hkv * a.nseg * a.nrb;  // at most B * H * Sq < 2^31
     a.status = status_word_device_ptr();
     if (!a.status) return ATTN_ERR_CUDA;
-    const int kt = c.page == 16 ? 16 : 32;
+    const int kt = tile_keys(c.d, wide, c.page);
     const int sms = device_sm_count();
     if (sms <= 0) return ATTN_ERR_CUDA;
     // as many CTAs as the longest possible lengths can give every warp a tile
@@ -757,9 +871,10 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     if (ctas > kCacheMaxCtas) ctas = kCacheMaxCtas;
     if (ctas > sms) ctas = sms;
     a.workers = (int)ctas * kWarps;
-    a.prefix = reinterpret_cast<int64_t *>(workspace);
-    a.po = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + (((size_t)B + 1) * 8 + 15) / 16 * 16);
-    a.pl = a.po + (size_t)2 * a.workers * R * c.d;
+    a.tail = reinterpret_cast<int4 *>(workspace);
+    a.hold = reinterpret_cast<float *>(a.tail + 2 * ctas);
+    a.po = a.hold + (size_t)a.workers * R * c.d;
+    a.pl = a.po + (size_t)2 * ctas * R * c.d;
     if (c.d == 64)
         return c.format == ATTN_CACHE_E4M3 ? launch_fwd_w<64, ATTN_CACHE_E4M3>(a, wide, kt, (unsigned)ctas, stream)
                                            : launch_fwd_w<64, ATTN_CACHE_I8>(a, wide, kt, (unsigned)ctas, stream);

@@ -15,28 +15,23 @@
 namespace attn {
 
 // The total key tiles of a call, numbered 0 .. total - 1 in the order of the
-// units they belong to, are cut into `workers` contiguous ranges whose
-// lengths differ by at most one tile.  worker_begin(w) is the first tile of
-// worker w; worker_begin(workers) == total.  total * workers stays below
-// 2^63 (workers <= 2^11, total <= 2^51).
+// units they belong to, are cut into `workers` contiguous ranges: total / workers
+// tiles each, the first total % workers of them one more.  worker_begin(w) is the
+// first tile of worker w; worker_begin(workers) == total.
 ATTN_HD int64_t worker_begin(int64_t w, int64_t total, int64_t workers) {
-    return w * total / workers;
+    const int64_t q = total / workers, r = total - q * workers;
+    return w * q + (w < r ? w : r);
 }
-// The worker whose range holds tile x (0 <= x < total): the largest w with
-// w * total / workers < x + 1.
+// The worker whose range holds tile x (0 <= x < total; total >= workers).
 ATTN_HD int64_t worker_of(int64_t x, int64_t total, int64_t workers) {
-    return ((x + 1) * workers - 1) / total;
+    const int64_t q = total / workers, r = total - q * workers, longer = r * (q + 1);
+    return x < longer ? x / (q + 1) : r + (x - longer) / q;
 }
 // Workers that share `total` tiles: at least min_tiles each, at most `most`.
 ATTN_HD int64_t worker_count(int64_t total, int64_t most, int64_t min_tiles) {
     const int64_t n = (total + min_tiles - 1) / min_tiles;
     return n < 1 ? 1 : (n < most ? n : most);
 }
-// A worker has at most two units that it shares with other workers: the one
-// its range begins inside of (slot 2w) and the one its range ends inside of
-// (slot 2w + 1); a unit that does both uses slot 2w.
-ATTN_HD int64_t partial_slot(int64_t w, bool begins_before) { return 2 * w + (begins_before ? 0 : 1); }
-
 // Tokens a sequence's table row can address, and its length clamped to them.
 ATTN_HD int64_t cache_capacity(int max_pages, int page) { return (int64_t)max_pages * page; }
 ATTN_HD int clamp_len(int len, int max_pages, int page) {

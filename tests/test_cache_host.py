@@ -19,7 +19,6 @@ extern "C" {
 int64_t begin_(int64_t w, int64_t t, int64_t n) { return worker_begin(w, t, n); }
 int64_t of_(int64_t x, int64_t t, int64_t n) { return worker_of(x, t, n); }
 int64_t count_(int64_t t, int64_t most, int64_t least) { return worker_count(t, most, least); }
-int64_t slot_(int64_t w, int b) { return partial_slot(w, b != 0); }
 int clamp_(int len, int pages, int page) { return clamp_len(len, pages, page); }
 int visible_(int len, int cnt, int i, int causal) { return visible_keys(len, cnt, i, causal); }
 int64_t touched_(int64_t s, int page) { return touched_pages(s, page); }
@@ -39,7 +38,7 @@ def idx(tmp_path_factory):
                    check=True)
     lib = ctypes.CDLL(so)
     for name, res, args in (("begin_", 8, (8, 8, 8)), ("of_", 8, (8, 8, 8)), ("count_", 8, (8, 8, 8)),
-                            ("slot_", 8, (8, 4)), ("clamp_", 4, (4, 4, 4)), ("visible_", 4, (4, 4, 4, 4)),
+                            ("clamp_", 4, (4, 4, 4)), ("visible_", 4, (4, 4, 4, 4)),
                             ("touched_", 8, (8, 4))):
         t = {8: ctypes.c_int64, 4: ctypes.c_int}
         fn = getattr(lib, name)
@@ -76,28 +75,6 @@ def test_worker_count_keeps_the_least_range(idx):
     assert idx.count_(0, 1216, 1) == 1
     assert idx.count_(10, 1216, 4) == 3
     assert idx.count_(10 ** 6, 1216, 4) == 1216
-
-
-@pytest.mark.parametrize("lens", [[3], [1, 1, 1], [5, 0, 17, 2], [40, 1, 1, 60], [1] * 30])
-@pytest.mark.parametrize("workers", [1, 3, 8, 40])
-def test_shared_units_never_meet_in_a_slot(idx, lens, workers):
-    """Every unit's tiles are cut at the range edges; each piece of a unit that several workers
-    hold has a slot of its own, below 2 * workers."""
-    total = sum(lens)
-    n = idx.count_(total, workers, 1)
-    taken = set()
-    at = 0
-    for length in lens:
-        if length:
-            w0, w1 = idx.of_(at, total, n), idx.of_(at + length - 1, total, n)
-            if w0 != w1:
-                for w in range(w0, w1 + 1):
-                    before = at < idx.begin_(w, total, n)
-                    assert before == (w > w0)
-                    slot = idx.slot_(w, before)
-                    assert 0 <= slot < 2 * n and slot not in taken
-                    taken.add(slot)
-        at += length
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
