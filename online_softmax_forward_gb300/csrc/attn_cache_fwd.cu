@@ -27,6 +27,12 @@
 // q rows are first multiplied by a power of two that puts the row's largest
 // magnitude in [2^14, 2^15): any fp32 or bf16 exponent then fits fp16.
 //
+// Softmax.  The sums l and o are kept relative to a reference `top` of the
+// scores and, o, to a reference 2^11 / rv of the page scales, so the weight that
+// enters the second product is p * v_scale * rv.  Both references move only when
+// a step of 16 keys would pass fp16's range or a weight 2^4: one vote a step, no
+// maximum across lanes and no rescaling in the others.
+//
 // Loads.  Each warp copies its own tiles into a ring of shared memory slots with
 // 16-byte cp.async (a slot holds the codes of one tile's keys or values), all
 // slots but the one in use in flight, and waits for nobody else.  The MMA's k
@@ -88,6 +94,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t p) {
                  : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(p));
     return u;
 }
+__device__ __forceinline__ void sts16_zero(uint32_t p) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
+}
 __device__ __forceinline__ uint2 lds8(uint32_t p) {
     uint2 u;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(p));
@@ -114,47 +123,30 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Codes as fp16 pairs, exact.  e4m3: sign and the seven other bits moved into
-// place give code * 2^-8 (the exponent biases differ by 8; subnormals stay
-// right), so kUnit is 2^8, and no code becomes an fp16 NaN: what a page holds
-// behind its last token cannot disturb a product with 0.  int8: 0x6400 + u is
-// the fp16 1024 + u, u = code + 128.
+// Codes as fp16 pairs, exact.  e4m3: one conversion a pair, as cheap as any
+// integer instruction (2 clocks a warp and SM quarter; moving the bits into place
+// by hand takes four).  int8: 0x6400 + u is the fp16 1024 + u, u = code + 128.
 template <int FMT>
 struct Unpack;
 template <>
 struct Unpack<ATTN_CACHE_E4M3> {
-    static constexpr float kUnit = 256.f;
-    // bytes 1 and 3 of w, as (low, high)
-    __device__ __forceinline__ static uint32_t odd(uint32_t w) {
-        return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
-    }
-    // channels (0, 2) and (1, 3) of four consecutive codes
-    __device__ __forceinline__ static void quad(uint32_t w, uint32_t &b0, uint32_t &b1) {
-        b0 = odd(w << 8);
-        b1 = odd(w);
-    }
-    // byte j of x and byte j of y
-    template <int J>
-    __device__ __forceinline__ static uint32_t pair(uint32_t x, uint32_t y) {
-        return odd(__byte_perm(x, y, (J + 4) * 0x1100 + J * 0x11));
+    // bytes (0, 1) and (2, 3) of w
+    __device__ __forceinline__ static void quad(uint32_t w, uint32_t &lo, uint32_t &hi) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
     }
 };
 template <>
 struct Unpack<ATTN_CACHE_I8> {
-    static constexpr float kUnit = 1.f;
-    __device__ __forceinline__ static uint32_t bias(uint32_t w) {  // 1024 + u -> u - 128
+    __device__ __forceinline__ static uint32_t less1152(uint32_t w) {  // 1024 + u -> u - 128
         const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&w),
                                   __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
         return *reinterpret_cast<const uint32_t *>(&h);
     }
-    __device__ __forceinline__ static void quad(uint32_t w, uint32_t &b0, uint32_t &b1) {
+    __device__ __forceinline__ static void quad(uint32_t w, uint32_t &lo, uint32_t &hi) {
         const uint32_t u = w ^ 0x80808080u;
-        b0 = bias(__byte_perm(u, 0x64646464u, 0x4240));
-        b1 = bias(__byte_perm(u, 0x64646464u, 0x4341));
-    }
-    template <int J>
-    __device__ __forceinline__ static uint32_t pair(uint32_t x, uint32_t y) {
-        return bias((__byte_perm(x, y, (J + 4) * 0x1100 + J * 0x11) & 0x00ff00ffu) ^ 0x64806480u);
+        lo = less1152(__byte_perm(u, 0x64646464u, 0x4140));
+        hi = less1152(__byte_perm(u, 0x64646464u, 0x4342));
     }
 };
 
@@ -319,6 +311,10 @@ __device__ __forceinline__ bool out_row(const FwdArgs &a, const Unit &u, int r, 
 }
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// `top` before the first key: any visible score is above it by more than the
+// range of exp2, so that its weight comes out infinite and sets the references.
+constexpr float kUnset = -3.0e38f;
+
 // One output.
 __device__ __forceinline__ void store_o(const FwdArgs &a, size_t i, float x) {
     if (a.dtype == ATTN_BF16) reinterpret_cast<__nv_bfloat16 *>(a.o)[i] = __float2bfloat16_rn(x);
@@ -332,11 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
     using U = Unpack<FMT>;
     constexpr int R = WIDE ? 16 : 8;
     constexpr int H = WIDE ? 2 : 1;    // query rows per lane: g, and g + 8 in the 16-row form
-    constexpr int NT = KT / 8;         // score tiles of 8 keys
-    constexpr int KS = KT / 16;        // k steps of P.V
     constexpr int QS = D / 16;         // k steps of Q.K
     constexpr int VT = D / 8;          // output tiles of 8 channels
-    constexpr int SLOT = KT * D;       // bytes of a tile's keys or values
+    constexpr int HALF = KT * D;       // bytes of a tile's keys, then its values
+    constexpr int SLOT = 2 * HALF;
     constexpr int NS = kRing / SLOT < 8 ? kRing / SLOT : 8;
     static_assert(NS >= 3 && R * D * 4 <= kRing, "a warp's ring later holds a state");
     extern __shared__ __align__(128) uint8_t sm[];
@@ -393,30 +388,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
     if (x0 + lane < x1) cur = find_tile<R, KT>(a, prefix, tpu, x0 + lane);
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + warp * kRing);
-    // slot s: keys (even s) or values (odd s) of the range's tile s / 2; `from` is
-    // the lane's register that holds tile s / 2's place in the pool
-    auto issue = [&](int s, int buf, int n_tiles, int base) {
-        const int j = s >> 1;
+    // tile j of the range into ring buffer `buf`; cur holds the tiles base .. base + 31
+    auto issue = [&](int j, int buf, int n_tiles, int base) {
         const int held = j - base;  // < 64
         const int at = __shfl_sync(0xffffffffu, held < 32 ? cur.at : nxt.at, held & 31);
         if (j < n_tiles && at >= 0) {
-            const uint8_t *src = ((s & 1) ? a.v : a.k) + (size_t)at * SLOT;
+            const size_t src = (size_t)at * HALF + lane * 16;
             const uint32_t dst = ring + buf * SLOT;
 #pragma unroll
-            for (int e = 0; e < SLOT / 512; ++e) {
+            for (int e = 0; e < HALF / 512; ++e) {
                 const int c = e * 32 + lane;
-                cp_async16(dst + swizzled<D>(c / (D / 16), c % (D / 16)), src + c * 16);
+                const uint32_t to = dst + swizzled<D>(c / (D / 16), c % (D / 16));
+                cp_async16(to, a.k + src + e * 512);
+                cp_async16(to + HALF, a.v + src + e * 512);
             }
         }
         cp_async_commit();
     };
     const int n_tiles = (int)(x1 - x0);
-    int put = 0, get = 0;  // ring buffers: next to fill, next to read
-#pragma unroll
-    for (int s = 0; s < NS - 1; ++s) {
-        issue(s, s, n_tiles, 0);
-        put = s + 1;
-    }
+    int put = NS - 1, get = 0;  // ring buffers: next to fill, next to read
+#pragma unroll 1
+    for (int j = 0; j < NS - 1; ++j) issue(j, j, n_tiles, 0);
 
     int64_t x = x0;
     while (x < x1) {
@@ -425,8 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
         const int len = clamp_len(a.lens[u.b], a.max_pages, a.page);
         const int cnt = a.counts ? min(max(a.counts[u.b], 0), a.Sq) : a.Sq;
 
-        // query fragments: k step w pairs channels (4w, 4w + 2) and (4w + 1, 4w + 3) of the
-        // lane's D/4 channels, as Unpack::quad does
+        // query fragments: k step w holds channels 4w .. 4w + 3 of the lane's D/4 channels
         uint32_t qa[QS][4];
         float cq[H];
         int lim[H];
@@ -455,19 +446,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
             up = up > 126 ? 126 : up;
             if (amax == 0.f || !(amax <= 3.402823466e38f)) up = 0;
             const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-            cq[hh] = a.sl2 * __uint_as_float((uint32_t)(127 - up) << 23) * U::kUnit;
+            cq[hh] = a.sl2 * __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
             for (int s = 0; s < QS; ++s) {
                 float y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = f[4 * s + e] * mul;
-                qa[s][hh] = pack_f16(y[0], y[2]);
-                qa[s][hh + 2] = pack_f16(y[1], y[3]);
+                qa[s][hh] = pack_f16(y[0], y[1]);
+                qa[s][hh + 2] = pack_f16(y[2], y[3]);
                 if constexpr (!WIDE) {
                     const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&qa[s][0]));
                     const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&qa[s][2]));
-                    qa[s][1] = pack_f16(y[0] - p.x, y[2] - p.y);
-                    qa[s][3] = pack_f16(y[1] - r.x, y[3] - r.y);
+                    qa[s][1] = pack_f16(y[0] - p.x, y[1] - p.y);
+                    qa[s][3] = pack_f16(y[2] - r.x, y[3] - r.y);
                 }
             }
             if (real) low = min(low, lim[hh]);
@@ -475,17 +466,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
 
-        float m[H], l[H], acc[VT][2 * H];
+        // l and acc relative to `top` and rv; the first key seen sets both
+        float top[H], rv[H], l[H], acc[VT][4];
 #pragma unroll
         for (int hh = 0; hh < H; ++hh) {
-            m[hh] = -INFINITY;
+            top[hh] = kUnset;
+            rv[hh] = 0x1p111f;
             l[hh] = 0.f;
         }
 #pragma unroll
-        for (int n = 0; n < VT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2 * H; ++e) acc[n][e] = 0.f;
+        for (int n = 0; n < VT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 
+#pragma unroll 1
         for (; x < xe; ++x) {
             const int i = (int)(x - x0);
             if ((i & 31) == 0) {
@@ -493,132 +485,142 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                 nxt.at = -1;
                 if (x + 32 + lane < x1) nxt = find_tile<R, KT>(a, prefix, tpu, x + 32 + lane);
             }
-            const int base = i & ~31;
+            // the buffer read last is free again: every lane has passed its __syncwarp
+            issue(i + NS - 1, put, n_tiles, i & ~31);
+            put = put + 1 == NS ? 0 : put + 1;
             const int at = __shfl_sync(0xffffffffu, cur.at, i & 31);
             const int key0 = __shfl_sync(0xffffffffu, cur.key0, i & 31);
             const float ks = __shfl_sync(0xffffffffu, cur.ks, i & 31);
             const float vs = __shfl_sync(0xffffffffu, cur.vs, i & 31);
-
-            // keys: the buffer read last is free again, every lane has passed its __syncwarp
-            issue(2 * i + NS - 1, put, n_tiles, base);
-            put = put + 1 == NS ? 0 : put + 1;
+            const uint32_t kb = ring + get * SLOT, vb = kb + HALF;
+            get = get + 1 == NS ? 0 : get + 1;
+            if (at < 0) continue;
             cp_async_wait<NS - 1>();
             __syncwarp();
-            float s[NT][4];
-            if (at >= 0) {
-                const uint32_t kb = ring + get * SLOT;
+            if (FMT == ATTN_CACHE_E4M3 && key0 + KT > len) {
+                // behind the sequence's last token a page may hold any code, NaN among
+                // them, which a weight of 0 would not remove
+                for (int c = lane; c < HALF / 16; c += 32)
+                    if (key0 + c / (D / 16) >= len)
+                        sts16_zero(vb + swizzled<D>(c / (D / 16), c % (D / 16)));
+                __syncwarp();
+            }
+            float f[H], sv[H];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            for (int hh = 0; hh < H; ++hh) {
+                f[hh] = ks * cq[hh];
+                // a page no key of which the row sees adds nothing, not even its scale's NaN
+                sv[hh] = key0 < lim[hh] ? vs : 0.f;
+            }
+#pragma unroll 1
+            for (int k16 = 0; k16 < KT; k16 += 16) {
+                float s[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    float e0[4] = {}, e1[4] = {};  // two chains, for the latency
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
-                        const uint4 u4 = lds16(kb + swizzled<D>(n * 8 + g, t * (D / 64) + c));
+                        const uint4 u4 = lds16(kb + k16 * D + swizzled<D>(n * 8 + g, t * (D / 64) + c));
                         const uint32_t words[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t b0, b1;
                             U::quad(words[e], b0, b1);
                             const int st = c * 4 + e;
-                            mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b0, b1);
+                            mma16816((e & 1) ? e1 : e0, qa[st][0], qa[st][1], qa[st][2], qa[st][3], b0, b1);
                         }
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][e] = e0[e] + e1[e];
                 }
-            }
-            get = get + 1 == NS ? 0 : get + 1;
-            __syncwarp();
-            issue(2 * i + NS, put, n_tiles, base);
-            put = put + 1 == NS ? 0 : put + 1;
-            if (at < 0) {
-                get = get + 1 == NS ? 0 : get + 1;
-                continue;
-            }
-
-            uint32_t pa[KS][4];
-            float alpha[H], sv[H];
+                float y[H][4], p[H][4], c[H];
+                bool far = false;
 #pragma unroll
-            for (int hh = 0; hh < H; ++hh) {
-                float y[NT][2];
-                const float f = ks * cq[hh];
-                float mx = -INFINITY;
+                for (int hh = 0; hh < H; ++hh) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int e = 0; e < 4; ++e)  // hi and lo parts of q in the 8-row form
+                        y[hh][e] = (WIDE ? s[e >> 1][2 * hh + (e & 1)] : s[e >> 1][e & 1] + s[e >> 1][2 + (e & 1)]) * f[hh];
+                    if (key0 + k16 + 16 > low) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        // hi and lo parts of q in the 8-row form
-                        y[n][c] = (WIDE ? s[n][2 * hh + c] : s[n][c] + s[n][2 + c]) * f;
-                        if (key0 + KT > low && key0 + 8 * n + 2 * t + c >= lim[hh]) y[n][c] = -INFINITY;
-                        mx = fmaxf(mx, y[n][c]);
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + k16 + 8 * (e >> 1) + 2 * t + (e & 1) >= lim[hh]) y[hh][e] = -INFINITY;
                     }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[hh], mx);
-                const float top = mn == -INFINITY ? 0.f : mn;
-                alpha[hh] = ex2(m[hh] - top);  // 0 while nothing has been seen
-                m[hh] = mn;
-                float sum = 0.f;
+                    c[hh] = sv[hh] * rv[hh];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float p0 = ex2(y[n][0] - top), p1 = ex2(y[n][1] - top);
-                    sum += p0 + p1;
-                    // 2^15: small weights stay above fp16's subnormals
-                    const uint32_t hi = pack_f16(p0 * 32768.f, p1 * 32768.f);
-                    if constexpr (WIDE) {
-                        pa[n / 2][(n & 1) * 2 + hh] = hi;
-                    } else {
-                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                        pa[n / 2][(n & 1) * 2] = hi;
-                        pa[n / 2][(n & 1) * 2 + 1] = pack_f16(fmaf(p0, 32768.f, -b.x), fmaf(p1, 32768.f, -b.y));
+                    for (int e = 0; e < 4; ++e) p[hh][e] = ex2(y[hh][e] - top[hh]);
+                    const float most = fmaxf(fmaxf(p[hh][0], p[hh][1]), fmaxf(p[hh][2], p[hh][3]));
+                    far = far || most > 16.f || most * c[hh] > 32768.f;
+                }
+                if (__any_sync(0xffffffffu, far)) {
+                    // new references: the scores' maximum, and the page scale unless what o
+                    // holds is larger by now
+#pragma unroll
+                    for (int hh = 0; hh < H; ++hh) {
+                        float mx = fmaxf(fmaxf(y[hh][0], y[hh][1]), fmaxf(y[hh][2], y[hh][3]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        const float nt = fmaxf(top[hh], mx);
+                        const float alpha = ex2(top[hh] - nt);  // 0 from kUnset
+                        const float was = alpha * 2048.f / rv[hh];
+                        const float nv = mx == -INFINITY ? rv[hh] : 2048.f / fmaxf(fmaxf(was, sv[hh]), 0x1p-100f);
+                        const float to = alpha * (nv / rv[hh]);
+                        l[hh] *= alpha;
+#pragma unroll
+                        for (int n = 0; n < VT; ++n) {
+                            if constexpr (WIDE) {
+                                acc[n][2 * hh] *= to;
+                                acc[n][2 * hh + 1] *= to;
+                            } else {
+                                acc[n][0] *= to; acc[n][1] *= to; acc[n][2] *= to; acc[n][3] *= to;
+                            }
+                        }
+                        top[hh] = nt;
+                        rv[hh] = nv;
+                        c[hh] = sv[hh] * nv;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[hh][e] = ex2(y[hh][e] - nt);
                     }
                 }
-                l[hh] = l[hh] * alpha[hh] + sum;
-                // a page no key of which the row sees adds nothing, not even its scale's NaN
-                sv[hh] = key0 < lim[hh] ? vs * (U::kUnit / 32768.f) : 0.f;
-            }
-            cp_async_wait<NS - 1>();
-            __syncwarp();
-            {
-                const uint32_t vb = ring + get * SLOT;
-                float c[VT][4];
+                uint32_t pa[4];
 #pragma unroll
-                for (int n = 0; n < VT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+                for (int hh = 0; hh < H; ++hh) {
+                    l[hh] += (p[hh][0] + p[hh][1]) + (p[hh][2] + p[hh][3]);
 #pragma unroll
-                for (int st = 0; st < KS; ++st) {
-                    uint32_t r[4][D / 32];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int row = st * 16 + 2 * t + (e & 1) + ((e & 2) ? 8 : 0);
-                        if constexpr (D == 128) {
-                            const uint4 u4 = lds16(vb + swizzled<D>(row, g));
-                            r[e][0] = u4.x; r[e][1] = u4.y; r[e][2] = u4.z; r[e][3] = u4.w;
+                    for (int n = 0; n < 2; ++n) {
+                        const float w0 = p[hh][2 * n] * c[hh], w1 = p[hh][2 * n + 1] * c[hh];
+                        const uint32_t hi = pack_f16(w0, w1);
+                        if constexpr (WIDE) {
+                            pa[2 * n + hh] = hi;
                         } else {
-                            const uint2 u2 = lds8(vb + swizzled<D>(row, g >> 1) + (g & 1) * 8);
-                            r[e][0] = u2.x; r[e][1] = u2.y;
+                            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                            pa[2 * n] = hi;
+                            pa[2 * n + 1] = pack_f16(w0 - b.x, w1 - b.y);
                         }
                     }
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        const uint32_t r0 = r[0][q], r1 = r[1][q], r2 = r[2][q], r3 = r[3][q];
-                        mma16816(c[4 * q], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<0>(r0, r1), U::template pair<0>(r2, r3));
-                        mma16816(c[4 * q + 1], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<1>(r0, r1), U::template pair<1>(r2, r3));
-                        mma16816(c[4 * q + 2], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<2>(r0, r1), U::template pair<2>(r2, r3));
-                        mma16816(c[4 * q + 3], pa[st][0], pa[st][1], pa[st][2], pa[st][3], U::template pair<3>(r0, r1), U::template pair<3>(r2, r3));
-                    }
                 }
+                uint32_t r[4][D / 32];
 #pragma unroll
-                for (int n = 0; n < VT; ++n) {
-                    float *o = acc[n];
-                    if constexpr (WIDE) {
-                        o[0] = fmaf(sv[0], c[n][0], o[0] * alpha[0]);
-                        o[1] = fmaf(sv[0], c[n][1], o[1] * alpha[0]);
-                        o[2] = fmaf(sv[1], c[n][2], o[2] * alpha[1]);
-                        o[3] = fmaf(sv[1], c[n][3], o[3] * alpha[1]);
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 2 * t + (e & 1) + ((e & 2) ? 8 : 0);
+                    if constexpr (D == 128) {
+                        const uint4 u4 = lds16(vb + k16 * D + swizzled<D>(row, g));
+                        r[e][0] = u4.x; r[e][1] = u4.y; r[e][2] = u4.z; r[e][3] = u4.w;
                     } else {
-                        o[0] = fmaf(sv[0], c[n][0] + c[n][2], o[0] * alpha[0]);
-                        o[1] = fmaf(sv[0], c[n][1] + c[n][3], o[1] * alpha[0]);
+                        const uint2 u2 = lds8(vb + k16 * D + swizzled<D>(row, g >> 1) + (g & 1) * 8);
+                        r[e][0] = u2.x; r[e][1] = u2.y;
                     }
                 }
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {  // bytes 2 hf and 2 hf + 1 of the four rows' words
+                        uint32_t a0, a1, b0, b1;
+                        U::quad(__byte_perm(r[0][q], r[1][q], hf ? 0x7362 : 0x5140), a0, a1);
+                        U::quad(__byte_perm(r[2][q], r[3][q], hf ? 0x7362 : 0x5140), b0, b1);
+                        mma16816(acc[4 * q + 2 * hf], pa[0], pa[1], pa[2], pa[3], a0, b0);
+                        mma16816(acc[4 * q + 2 * hf + 1], pa[0], pa[1], pa[2], pa[3], a1, b1);
+                    }
             }
-            get = get + 1 == NS ? 0 : get + 1;
             __syncwarp();  // the buffer may be filled again
         }
 
@@ -638,15 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
             float sum = l[hh];
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: no key was visible
-            const float top = m[hh] == -INFINITY ? 0.f : m[hh];
-            const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+            // 0: no key was visible.  NaN scores alone leave `top` unset
+            const float inv = sum == 0.f ? 0.f : 1.f / sum, unit = 1.f / rv[hh];
+            const float lse2 = sum == 0.f ? -INFINITY : top[hh] + log2f(sum);
             const int r = g + 8 * hh;
             float f[D / 4];
 #pragma unroll
             for (int n = 0; n < VT; ++n) {
-                f[n] = acc[n][2 * hh] * inv;
-                f[VT + n] = acc[n][2 * hh + 1] * inv;
+                f[n] = (WIDE ? acc[n][2 * hh] : acc[n][0] + acc[n][2]) * inv * unit;
+                f[VT + n] = (WIDE ? acc[n][2 * hh + 1] : acc[n][1] + acc[n][3]) * inv * unit;
             }
             if (whole) {
                 size_t row;
@@ -814,18 +816,22 @@ int launch_fwd_t(const FwdArgs &a, unsigned grid, cudaStream_t stream) {
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
-// Keys of a tile: a page, at most 64 (the work per tile beside its keys is
-// then spread over twice as many as with 32), or 32 for the 16-row form at
-// d = 128, whose 64 keys do not fit the registers.
-constexpr int tile_keys(int d, bool wide, int page) {
-    return page < 64 ? page : (wide && d == 128 ? 32 : 64);
+// Keys of a tile: at most 8 KB of keys and values, three of which a warp's ring
+// holds, and no more than a page.
+constexpr int tile_keys(int d, int page) {
+    const int most = d == 128 ? 32 : 64;
+    return page < most ? page : most;
 }
 
+template <int D, int FMT, int WIDE>
+int launch_fwd_k(const FwdArgs &a, int kt, unsigned grid, cudaStream_t s) {
+    if (kt == 16) return launch_fwd_t<D, FMT, WIDE, 16>(a, grid, s);
+    if (kt == 32) return launch_fwd_t<D, FMT, WIDE, 32>(a, grid, s);
+    return launch_fwd_t<D, FMT, WIDE, tile_keys(D, 64)>(a, grid, s);
+}
 template <int D, int FMT>
 int launch_fwd_w(const FwdArgs &a, bool wide, int kt, unsigned grid, cudaStream_t s) {
-#define ATTN_KT(W)                                                    (kt == 16   ? launch_fwd_t<D, FMT, W, 16>(a, grid, s)              : kt == 32 ? launch_fwd_t<D, FMT, W, 32>(a, grid, s)                         : launch_fwd_t<D, FMT, W, 64>(a, grid, s))
-    return wide ? ATTN_KT(1) : ATTN_KT(0);
-#undef ATTN_KT
+    return wide ? launch_fwd_k<D, FMT, 1>(a, kt, grid, s) : launch_fwd_k<D, FMT, 0>(a, kt, grid, s);
 }
 
 }  // namespace
@@ -862,7 +868,7 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     const int64_t units = (int64_t)B * a.Hkv * a.nseg * a.nrb;  // at most B * H * Sq < 2^31
     a.status = status_word_device_ptr();
     if (!a.status) return ATTN_ERR_CUDA;
-    const int kt = tile_keys(c.d, wide, c.page);
+    const int kt = tile_keys(c.d, c.page);
     const int sms = device_sm_count();
     if (sms <= 0) return ATTN_ERR_CUDA;
     // as many CTAs as the longest possible lengths can give every warp a tile
