@@ -378,7 +378,8 @@ ATTN_API int attn_cache_select(const attn_cache *cache, const void *q, const int
  *
  *   q, o   [B][H][Sq][d], lse [B][H][Sq] (NULL: not written), types as attn_fwd
  *          (every attn_dtype); H a multiple of H_kv, query heads
- *          h * H / H_kv .. of kv head h; B <= 4096; B * H * Sq < 2^31
+ *          h * H / H_kv .. of kv head h; B <= 4096; B * H * Sq < 2^31;
+ *          B * max_pages * page / 16 < 2^31
  *   counts the last counts[b] of the lens[b] tokens are the queries' own:
  *          query i sits at position lens[b] - counts[b] + i.  Rows from
  *          counts[b] on see no key.

@@ -675,6 +675,8 @@ int attn_fwd_cache(const attn_cache *cache, const void *q, void *o, float *lse,
         return ATTN_ERR_INVALID_ARG;
     float sc = 0.f;
     if (resolve_scale(scale, cache->d, &sc) != ATTN_OK) return ATTN_ERR_INVALID_ARG;
+    // the kernel counts a call's 16-token pieces per kv head, and a list's, in 31 bits
+    if ((double)B * max_pages * (cache->page / 16) > (double)INT32_MAX) return ATTN_ERR_INVALID_ARG;
     if (B == 0 || Sq == 0) return ATTN_OK;
     if (!q || !o || !aligned(q, 16) || !aligned(o, 16) || (lse && !aligned(lse, 4)) || !workspace ||
         !aligned(workspace, 16) || workspace_bytes < need)

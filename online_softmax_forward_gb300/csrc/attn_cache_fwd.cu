@@ -67,10 +67,12 @@ struct FwdArgs {
     const int32_t *table, *lens, *counts, *pages;
     float *hold;      // [warp][R][D]: state of the unit a warp's range begins inside of, if more follows
     float *po, *pl;   // states of the CTAs' shared units by slot: [slot][R][D], [slot][R] (log2)
-    int4 *tail;       // [2 * CTA]: the unit that runs over the end of a CTA's range
+    int4 *tail;       // [CTA]: the unit that runs over the end of a CTA's range
     int B, Hkv, G, Sq, page, n_pages, max_pages, n_sel, causal;
     int nseg, rows, nrb;  // row groups of a (sequence, kv head), rows of one, row blocks of one
+    int units;            // of a sequence: Hkv * nseg * nrb
     int dtype, workers;
+    FastDiv by_units, by_per, by_nrb, by_group;  // per = nseg * nrb
     float sl2;  // scale * log2(e)
     int *status;
 };
@@ -150,71 +152,72 @@ struct Unpack<ATTN_CACHE_I8> {
     }
 };
 
-// Where a tile's unit lies.
-struct Unit {
-    int b, hk, seg, rb;
-    int64_t begin, end;  // its tiles
-};
-
 // Sequence lengths as tile counts, summed: prefix[b] tiles before sequence b.
-__device__ void scan_lengths(const FwdArgs &a, int kt, int64_t *prefix, int64_t *warp_sums) {
+__device__ __forceinline__ void scan_lengths(const FwdArgs &a, int kt, int *prefix, int *warp_sums) {
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
-    auto tiles = [&](int b) {
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
         const int len0 = a.lens[b], cnt = a.counts ? a.counts[b] : a.Sq;
         const int len = clamp_len(len0, a.max_pages, a.page);
         if ((len != len0 || cnt < 0 || cnt > a.Sq) && blockIdx.x == 0)
             atomicOr(a.status, kStatusTable);
-        return ((int64_t)len + kt - 1) / kt;
-    };
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += tiles(b);
-    int64_t incl = sum;
+        const int n = (int)(((int64_t)len + kt - 1) / kt);
+        prefix[b + 1] = n;  // turned into a sum below
+        sum += n;
+    }
+    int incl = sum;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
-    int64_t at = incl - sum;
-    for (int w = 0; w < warp; ++w) at += warp_sums[w];
-    for (int b = b0; b < b1; ++b) {
-        prefix[b] = at;
-        at += tiles(b);
-    }
-    if (b0 < a.B && b1 == a.B) prefix[a.B] = at;
+    int at = incl - sum;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) at += w < warp ? warp_sums[w] : 0;
+    for (int b = b0; b < b1; ++b) prefix[b + 1] = at += prefix[b + 1];
+    if (threadIdx.x == 0) prefix[0] = 0;
+    __syncthreads();
 }
 
-// The unit that tile x belongs to.
-__device__ __forceinline__ Unit unit_of(const FwdArgs &a, const int64_t *prefix, int64_t tpu, int64_t x) {
-    Unit u;
-    const int per = a.nseg * a.nrb;
-    int64_t idx, first, len;  // unit within the sequence, the sequence's first tile, tiles per unit
+// Where tile x lies.
+__device__ __forceinline__ Place place_of(const FwdArgs &a, const int *prefix, int tpu, int64_t x) {
+    Place p;
     if (a.pages) {
-        const int64_t n = x / tpu, units = (int64_t)a.Hkv * per;
-        u.b = (int)(n / units);
-        idx = n % units;
-        first = u.b * units * tpu;
-        len = tpu;
-    } else {
-        const int64_t units = (int64_t)a.Hkv * per, y = x / units;
-        int lo = 0, hi = a.B - 1;  // the last b with prefix[b] <= y
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (prefix[mid] <= y) lo = mid; else hi = mid - 1;
-        }
-        u.b = lo;
-        first = prefix[lo] * units;
-        len = prefix[lo + 1] - prefix[lo];
-        idx = (x - first) / len;
+        const int64_t n = quotient(x, tpu);
+        p.b = (int)quotient(n, a.units);
+        p.unit = (int)(n - (int64_t)p.b * a.units);
+        p.n = tpu;
+        p.t = (int)(x - n * tpu);
+        return p;
     }
-    u.begin = first + idx * len;
-    u.end = u.begin + len;
-    u.hk = (int)(idx / per);
-    u.seg = (int)(idx % per / a.nrb);
-    u.rb = (int)(idx % a.nrb);
+    const int y = (uint64_t)x >> 31 ? (int)(x / a.units) : (int)((uint32_t)x / a.by_units);
+    int lo = 0, hi = a.B - 1;  // the last b with prefix[b] <= y
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= y) lo = mid; else hi = mid - 1;
+    }
+    const int64_t in = x - (int64_t)prefix[lo] * a.units;
+    p.b = lo;
+    p.n = prefix[lo + 1] - prefix[lo];
+    p.unit = (int)quotient(in, p.n);
+    p.t = (int)(in - (int64_t)p.unit * p.n);
+    return p;
+}
+
+struct Unit {
+    int b, hk, seg, rb;
+};
+__device__ __forceinline__ Unit unit_at(const FwdArgs &a, int b, int unit) {
+    Unit u;
+    u.b = b;
+    u.hk = (int)((uint32_t)unit / a.by_per);
+    const int in = unit - u.hk * a.nseg * a.nrb;
+    u.seg = (int)((uint32_t)in / a.by_nrb);
+    u.rb = in - u.seg * a.nrb;
     return u;
 }
 
@@ -222,11 +225,10 @@ __device__ __forceinline__ Unit unit_of(const FwdArgs &a, const int64_t *prefix,
 template <int R>
 __device__ __forceinline__ bool row_of(const FwdArgs &a, const Unit &u, int r, int &i, int &h) {
     const int row = u.rb * R + r;
-    if (row >= a.rows) return false;
-    const int g = a.pages ? row : row % a.G;
-    i = a.pages ? u.seg : row / a.G;
-    h = u.hk * a.G + g;
-    return true;
+    const int q = a.pages ? u.seg : (int)((uint32_t)row / a.by_group);
+    i = q;
+    h = u.hk * a.G + (a.pages ? row : row - q * a.G);
+    return row < a.rows;
 }
 
 struct Tile {  // one key tile, held by one lane
@@ -236,24 +238,24 @@ struct Tile {  // one key tile, held by one lane
 };
 
 template <int R, int KT>
-__device__ __forceinline__ Tile find_tile(const FwdArgs &a, const int64_t *prefix, int64_t tpu, int64_t x) {
+__device__ __forceinline__ Tile find_tile(const FwdArgs &a, const Place &p) {
     Tile d;
     d.at = -1;
     d.key0 = 0;
     d.ks = d.vs = 0.f;
-    const Unit u = unit_of(a, prefix, tpu, x);
-    const int in_page = a.page / KT;
-    const int64_t t = x - u.begin;
-    const int len = clamp_len(a.lens[u.b], a.max_pages, a.page);
-    const int cnt = a.counts ? min(max(a.counts[u.b], 0), a.Sq) : a.Sq;
-    int lp = (int)(t / in_page);
-    const int sub = (int)(t % in_page);
+    const int shift = 31 - __clz(a.page / KT);  // tiles of a page: a power of two
+    int lp = p.t >> shift;
+    const int sub = p.t & ((1 << shift) - 1);
+    const Unit u = unit_at(a, p.b, p.unit);
     if (a.pages) {
         const int64_t list = ((int64_t)u.b * a.Hkv + u.hk) * a.nseg + u.seg;
         lp = a.pages[list * a.n_sel + lp];
         if (lp < -1 || lp >= a.max_pages) atomicOr(a.status, kStatusTable);
         if (lp < 0 || lp >= a.max_pages) return d;
     }
+    const int phys = a.table[(int64_t)u.b * a.max_pages + lp];
+    const int len = clamp_len(a.lens[u.b], a.max_pages, a.page);
+    const int cnt = a.counts ? min(max(a.counts[u.b], 0), a.Sq) : a.Sq;
     // the block's last query that is one of the sequence's sees the most keys
     int first, last, h;
     row_of<R>(a, u, 0, first, h);
@@ -263,22 +265,30 @@ __device__ __forceinline__ Tile find_tile(const FwdArgs &a, const int64_t *prefi
     const int64_t key0 = (int64_t)lp * a.page + sub * KT;
     if (key0 >= seen) return d;
     d.key0 = (int)key0;
-    const int phys = a.table[(int64_t)u.b * a.max_pages + lp];
     if (phys < 0 || phys >= a.n_pages) {
         atomicOr(a.status, kStatusTable);
         return d;
     }
     const int64_t ph = (int64_t)phys * a.Hkv + u.hk;
-    d.at = (int)(ph * in_page + sub);
+    d.at = (int)((ph << shift) + sub);
     d.ks = a.ks[ph];
     d.vs = a.vs[ph];
     return d;
 }
 
-__device__ __forceinline__ void load_q8(const FwdArgs &a, size_t i, float *f) {
-    if (a.dtype == ATTN_F32) codec::load8<0>(a.q, i, f);
-    else if (a.dtype == ATTN_BF16 || a.dtype == ATTN_BF16_OUT_F32) codec::load8<1>(a.q, i, f);
-    else codec::load8<2>(a.q, i, f);
+// Elements [i, i + N) of q as fp32.
+template <int N>
+__device__ __forceinline__ void load_q(const FwdArgs &a, size_t i, float *f) {
+    if (a.dtype == ATTN_F32) {
+#pragma unroll
+        for (int e = 0; e < N; e += 8) codec::load8<0>(a.q, i + e, f + e);
+    } else if (a.dtype == ATTN_BF16 || a.dtype == ATTN_BF16_OUT_F32) {
+#pragma unroll
+        for (int e = 0; e < N; e += 8) codec::load8<1>(a.q, i + e, f + e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; e += 8) codec::load8<2>(a.q, i + e, f + e);
+    }
 }
 
 // Eight consecutive outputs.
@@ -334,22 +344,24 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
     constexpr int SLOT = 2 * HALF;
     constexpr int NS = kRing / SLOT < 8 ? kRing / SLOT : 8;
     static_assert(NS >= 3 && R * D * 4 <= kRing, "a warp's ring later holds a state");
+    constexpr int STEP = KT < 32 ? KT : 32;  // keys of one softmax step
+    constexpr int NT = STEP / 8;             // score tiles of 8 keys
+    constexpr int KS = STEP / 16;            // k steps of P.V
     extern __shared__ __align__(128) uint8_t sm[];
-    int64_t *prefix = reinterpret_cast<int64_t *>(sm + kWarps * kRing);  // [B + 1]
-    __shared__ int64_t warp_sums[kWarps];
+    int *prefix = reinterpret_cast<int *>(sm + kWarps * kRing);  // [B + 1]
+    __shared__ int warp_sums[kWarps];
     __shared__ float s_lse[kWarps][2][R];
-    __shared__ Unit s_unit[kWarps][2];
     __shared__ const float *s_keep[kWarps][2];
-    __shared__ int64_t s_end[kWarps];   // past the warp's last tile
-    __shared__ int s_has[kWarps];       // bit 0: a state of a unit begun before, bit 1: of one that goes on
+    __shared__ int s_b[kWarps][2], s_unit[kWarps][2];  // the units of the warps' kept states
+    __shared__ int s_has[kWarps];  // bit 0: a state of a unit begun before, 1: that unit goes on,
+                                   // 2: a state of a unit begun here that goes on
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const int64_t tpu = a.pages ? (int64_t)a.n_sel * (a.page / KT) : 0;
-    const int64_t units = (int64_t)a.Hkv * a.nseg * a.nrb;  // of one sequence
+    const int tpu = a.pages ? a.n_sel * (a.page / KT) : 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     int64_t total;
     if (a.pages) {
-        total = a.B * units * tpu;
+        total = (int64_t)a.B * a.units * tpu;
         // lengths and counts out of range are reported here for a page list
         if (blockIdx.x == 0)
             for (int b = threadIdx.x; b < a.B; b += kThreads) {
@@ -359,8 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
             }
     } else {
         scan_lengths(a, KT, prefix, warp_sums);
-        __syncthreads();
-        total = prefix[a.B] * units;
+        total = (int64_t)prefix[a.B] * a.units;
         // sequences without a token have no tile: o = 0, lse = -inf
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
             if (prefix[b] != prefix[b + 1]) continue;
@@ -372,24 +383,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
         }
     }
     const int64_t workers = worker_count(total, a.workers, kMinTiles);
-    const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
-    int64_t x0 = 0, x1 = 0;
+    const int w = blockIdx.x * kWarps + warp;
+    int64_t x0 = 0;
+    int n_tiles = 0;  // of this warp's range
     if (w < workers && total > 0) {
         x0 = worker_begin(w, total, workers);
-        x1 = worker_begin(w + 1, total, workers);
+        n_tiles = (int)(worker_begin(w + 1, total, workers) - x0);
     }
-    if (lane == 0) {
-        s_has[warp] = 0;
-        s_end[warp] = x1;
-    }
+    if (lane == 0) s_has[warp] = 0;
+    auto tiles = [&](int b) { return a.pages ? tpu : prefix[b + 1] - prefix[b]; };
 
-    // tiles x0 + 32 n + lane, and the next 32
+    Place here = {0, 0, 0, 1};
+    if (n_tiles > 0) here = place_of(a, prefix, tpu, x0);
+    // lane: tile 32 k + lane of the range, and the one 32 further
+    Place mine = here;
     Tile cur = {-1, 0, 0.f, 0.f}, nxt = cur;
-    if (x0 + lane < x1) cur = find_tile<R, KT>(a, prefix, tpu, x0 + lane);
+    if (lane < n_tiles) {
+        advance(mine, lane, a.units, tiles);
+        cur = find_tile<R, KT>(a, mine);
+    }
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + warp * kRing);
     // tile j of the range into ring buffer `buf`; cur holds the tiles base .. base + 31
-    auto issue = [&](int j, int buf, int n_tiles, int base) {
+    auto issue = [&](int j, int buf, int base) {
         const int held = j - base;  // < 64
         const int at = __shfl_sync(0xffffffffu, held < 32 ? cur.at : nxt.at, held & 31);
         if (j < n_tiles && at >= 0) {
@@ -405,15 +421,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
         }
         cp_async_commit();
     };
-    const int n_tiles = (int)(x1 - x0);
     int put = NS - 1, get = 0;  // ring buffers: next to fill, next to read
 #pragma unroll 1
-    for (int j = 0; j < NS - 1; ++j) issue(j, j, n_tiles, 0);
+    for (int j = 0; j < NS - 1; ++j) issue(j, j, 0);
 
-    int64_t x = x0;
-    while (x < x1) {
-        const Unit u = unit_of(a, prefix, tpu, x);
-        const int64_t xe = u.end < x1 ? u.end : x1;
+    int i = 0;  // tile of the range
+    while (i < n_tiles) {
+        const Unit u = unit_at(a, here.b, here.unit);
+        const int left = min(here.n - here.t, n_tiles - i);  // tiles of this unit in the range
         const int len = clamp_len(a.lens[u.b], a.max_pages, a.page);
         const int cnt = a.counts ? min(max(a.counts[u.b], 0), a.Sq) : a.Sq;
 
@@ -425,13 +440,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
 #pragma unroll
         for (int hh = 0; hh < H; ++hh) {
             float f[D / 4];
-            int i, h;
-            const bool real = row_of<R>(a, u, g + 8 * hh, i, h);
-            lim[hh] = real ? visible_keys(len, cnt, i, a.causal) : 0;
+            int qi, h;
+            const bool real = row_of<R>(a, u, g + 8 * hh, qi, h);
+            lim[hh] = real ? visible_keys(len, cnt, qi, a.causal) : 0;
             if (real) {
-                const size_t at = (((size_t)u.b * a.Hkv * a.G + h) * a.Sq + i) * D + t * (D / 4);
-#pragma unroll
-                for (int e = 0; e < D / 4; e += 8) load_q8(a, at + e, f + e);
+                load_q<D / 4>(a, (((size_t)u.b * a.Hkv * a.G + h) * a.Sq + qi) * D + t * (D / 4), f);
+                low = min(low, lim[hh]);
             } else {
 #pragma unroll
                 for (int e = 0; e < D / 4; ++e) f[e] = 0.f;
@@ -461,7 +475,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                     qa[s][3] = pack_f16(y[2] - r.x, y[3] - r.y);
                 }
             }
-            if (real) low = min(low, lim[hh]);
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
@@ -477,16 +490,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
 #pragma unroll
         for (int n = 0; n < VT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 
+        const int stop = i + left;
 #pragma unroll 1
-        for (; x < xe; ++x) {
-            const int i = (int)(x - x0);
+        for (; i < stop; ++i) {
             if ((i & 31) == 0) {
                 if (i > 0) cur = nxt;
                 nxt.at = -1;
-                if (x + 32 + lane < x1) nxt = find_tile<R, KT>(a, prefix, tpu, x + 32 + lane);
+                if (i + 32 + lane < n_tiles) {
+                    advance(mine, 32, a.units, tiles);
+                    nxt = find_tile<R, KT>(a, mine);
+                }
             }
             // the buffer read last is free again: every lane has passed its __syncwarp
-            issue(i + NS - 1, put, n_tiles, i & ~31);
+            issue(i + NS - 1, put, i & ~31);
             put = put + 1 == NS ? 0 : put + 1;
             const int at = __shfl_sync(0xffffffffu, cur.at, i & 31);
             const int key0 = __shfl_sync(0xffffffffu, cur.key0, i & 31);
@@ -500,55 +516,54 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
             if (FMT == ATTN_CACHE_E4M3 && key0 + KT > len) {
                 // behind the sequence's last token a page may hold any code, NaN among
                 // them, which a weight of 0 would not remove
+#pragma unroll 1
                 for (int c = lane; c < HALF / 16; c += 32)
                     if (key0 + c / (D / 16) >= len)
                         sts16_zero(vb + swizzled<D>(c / (D / 16), c % (D / 16)));
                 __syncwarp();
             }
-            float f[H], sv[H];
-#pragma unroll
-            for (int hh = 0; hh < H; ++hh) {
-                f[hh] = ks * cq[hh];
-                // a page no key of which the row sees adds nothing, not even its scale's NaN
-                sv[hh] = key0 < lim[hh] ? vs : 0.f;
-            }
 #pragma unroll 1
-            for (int k16 = 0; k16 < KT; k16 += 16) {
-                float s[2][4];
+            for (int step = 0; step < KT; step += STEP) {
+                float s[NT][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    float e0[4] = {}, e1[4] = {};  // two chains, for the latency
+                for (int n = 0; n < NT; ++n) {
+                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
-                        const uint4 u4 = lds16(kb + k16 * D + swizzled<D>(n * 8 + g, t * (D / 64) + c));
+                        const uint4 u4 = lds16(kb + step * D + swizzled<D>(n * 8 + g, t * (D / 64) + c));
                         const uint32_t words[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t b0, b1;
                             U::quad(words[e], b0, b1);
                             const int st = c * 4 + e;
-                            mma16816((e & 1) ? e1 : e0, qa[st][0], qa[st][1], qa[st][2], qa[st][3], b0, b1);
+                            mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b0, b1);
                         }
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[n][e] = e0[e] + e1[e];
                 }
-                float y[H][4], p[H][4], c[H];
+                if constexpr (!WIDE) {  // hi and lo parts of q
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        s[n][0] += s[n][2];
+                        s[n][1] += s[n][3];
+                    }
+                }
+                const bool edge = key0 + step + STEP > low;  // some row does not see every key
+                float p[H][2 * NT], c[H];
                 bool far = false;
 #pragma unroll
                 for (int hh = 0; hh < H; ++hh) {
+                    const float f = ks * cq[hh];
+                    // a page no key of which the row sees adds nothing, not even its scale's NaN
+                    c[hh] = key0 < lim[hh] ? vs * rv[hh] : 0.f;
+                    float most = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)  // hi and lo parts of q in the 8-row form
-                        y[hh][e] = (WIDE ? s[e >> 1][2 * hh + (e & 1)] : s[e >> 1][e & 1] + s[e >> 1][2 + (e & 1)]) * f[hh];
-                    if (key0 + k16 + 16 > low) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (key0 + k16 + 8 * (e >> 1) + 2 * t + (e & 1) >= lim[hh]) y[hh][e] = -INFINITY;
+                    for (int e = 0; e < 2 * NT; ++e) {
+                        float z = fmaf(s[e >> 1][2 * hh + (e & 1)], f, -top[hh]);
+                        if (edge && key0 + step + 8 * (e >> 1) + 2 * t + (e & 1) >= lim[hh]) z = -INFINITY;
+                        p[hh][e] = ex2(z);
+                        most = fmaxf(most, p[hh][e]);
                     }
-                    c[hh] = sv[hh] * rv[hh];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[hh][e] = ex2(y[hh][e] - top[hh]);
-                    const float most = fmaxf(fmaxf(p[hh][0], p[hh][1]), fmaxf(p[hh][2], p[hh][3]));
                     far = far || most > 16.f || most * c[hh] > 32768.f;
                 }
                 if (__any_sync(0xffffffffu, far)) {
@@ -556,13 +571,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                     // holds is larger by now
 #pragma unroll
                     for (int hh = 0; hh < H; ++hh) {
-                        float mx = fmaxf(fmaxf(y[hh][0], y[hh][1]), fmaxf(y[hh][2], y[hh][3]));
+                        const float f = ks * cq[hh], sv = key0 < lim[hh] ? vs : 0.f;
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 2 * NT; ++e) {
+                            float &y = p[hh][e];
+                            y = s[e >> 1][2 * hh + (e & 1)] * f;
+                            if (edge && key0 + step + 8 * (e >> 1) + 2 * t + (e & 1) >= lim[hh]) y = -INFINITY;
+                            mx = fmaxf(mx, y);
+                        }
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                         const float nt = fmaxf(top[hh], mx);
                         const float alpha = ex2(top[hh] - nt);  // 0 from kUnset
                         const float was = alpha * 2048.f / rv[hh];
-                        const float nv = mx == -INFINITY ? rv[hh] : 2048.f / fmaxf(fmaxf(was, sv[hh]), 0x1p-100f);
+                        const float nv = mx == -INFINITY ? rv[hh] : 2048.f / fmaxf(fmaxf(was, sv), 0x1p-100f);
                         const float to = alpha * (nv / rv[hh]);
                         l[hh] *= alpha;
 #pragma unroll
@@ -576,50 +599,55 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                         }
                         top[hh] = nt;
                         rv[hh] = nv;
-                        c[hh] = sv[hh] * nv;
+                        c[hh] = sv * nv;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) p[hh][e] = ex2(y[hh][e] - nt);
+                        for (int e = 0; e < 2 * NT; ++e) p[hh][e] = ex2(p[hh][e] - nt);
                     }
                 }
-                uint32_t pa[4];
+                uint32_t pa[KS][4];
 #pragma unroll
                 for (int hh = 0; hh < H; ++hh) {
-                    l[hh] += (p[hh][0] + p[hh][1]) + (p[hh][2] + p[hh][3]);
+                    float sum = 0.f;
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
+                    for (int n = 0; n < NT; ++n) {
+                        sum += p[hh][2 * n] + p[hh][2 * n + 1];
                         const float w0 = p[hh][2 * n] * c[hh], w1 = p[hh][2 * n + 1] * c[hh];
                         const uint32_t hi = pack_f16(w0, w1);
                         if constexpr (WIDE) {
-                            pa[2 * n + hh] = hi;
+                            pa[n / 2][(n & 1) * 2 + hh] = hi;
                         } else {
                             const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                            pa[2 * n] = hi;
-                            pa[2 * n + 1] = pack_f16(w0 - b.x, w1 - b.y);
+                            pa[n / 2][(n & 1) * 2] = hi;
+                            pa[n / 2][(n & 1) * 2 + 1] = pack_f16(w0 - b.x, w1 - b.y);
                         }
                     }
-                }
-                uint32_t r[4][D / 32];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 2 * t + (e & 1) + ((e & 2) ? 8 : 0);
-                    if constexpr (D == 128) {
-                        const uint4 u4 = lds16(vb + k16 * D + swizzled<D>(row, g));
-                        r[e][0] = u4.x; r[e][1] = u4.y; r[e][2] = u4.z; r[e][3] = u4.w;
-                    } else {
-                        const uint2 u2 = lds8(vb + k16 * D + swizzled<D>(row, g >> 1) + (g & 1) * 8);
-                        r[e][0] = u2.x; r[e][1] = u2.y;
-                    }
+                    l[hh] += sum;
                 }
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q)
+                for (int st = 0; st < KS; ++st) {
+                    uint32_t r[4][D / 32];
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {  // bytes 2 hf and 2 hf + 1 of the four rows' words
-                        uint32_t a0, a1, b0, b1;
-                        U::quad(__byte_perm(r[0][q], r[1][q], hf ? 0x7362 : 0x5140), a0, a1);
-                        U::quad(__byte_perm(r[2][q], r[3][q], hf ? 0x7362 : 0x5140), b0, b1);
-                        mma16816(acc[4 * q + 2 * hf], pa[0], pa[1], pa[2], pa[3], a0, b0);
-                        mma16816(acc[4 * q + 2 * hf + 1], pa[0], pa[1], pa[2], pa[3], a1, b1);
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = st * 16 + 2 * t + (e & 1) + ((e & 2) ? 8 : 0);
+                        if constexpr (D == 128) {
+                            const uint4 u4 = lds16(vb + step * D + swizzled<D>(row, g));
+                            r[e][0] = u4.x; r[e][1] = u4.y; r[e][2] = u4.z; r[e][3] = u4.w;
+                        } else {
+                            const uint2 u2 = lds8(vb + step * D + swizzled<D>(row, g >> 1) + (g & 1) * 8);
+                            r[e][0] = u2.x; r[e][1] = u2.y;
+                        }
                     }
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {  // bytes 2 hf and 2 hf + 1 of the four rows' words
+                            uint32_t a0, a1, b0, b1;
+                            U::quad(__byte_perm(r[0][q], r[1][q], hf ? 0x7362 : 0x5140), a0, a1);
+                            U::quad(__byte_perm(r[2][q], r[3][q], hf ? 0x7362 : 0x5140), b0, b1);
+                            mma16816(acc[4 * q + 2 * hf], pa[st][0], pa[st][1], pa[st][2], pa[st][3], a0, b0);
+                            mma16816(acc[4 * q + 2 * hf + 1], pa[st][0], pa[st][1], pa[st][2], pa[st][3], a1, b1);
+                        }
+                }
             }
             __syncwarp();  // the buffer may be filled again
         }
@@ -627,11 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
         // the unit's state: written if it is whole, else kept for the join.  The range's last unit
         // leaves it in the ring, which is not needed any more; a first unit that more follow, in
         // global memory.
-        const bool whole = u.begin >= x0 && u.end <= x1;
-        const bool before = u.begin < x0;
-        float *keep = xe < x1 ? a.hold + w * R * D : reinterpret_cast<float *>(sm + warp * kRing);
-        if (!in_bounds(w < (int64_t)gridDim.x * kWarps, a.status)) break;
-        if (xe == x1) {
+        const bool before = i == left && here.t > 0, after = here.t + left < here.n;
+        float *keep = i < n_tiles ? a.hold + (size_t)w * R * D : reinterpret_cast<float *>(sm + warp * kRing);
+        if (i == n_tiles) {
             cp_async_wait<0>();
             __syncwarp();
         }
@@ -650,84 +676,111 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                 f[n] = (WIDE ? acc[n][2 * hh] : acc[n][0] + acc[n][2]) * inv * unit;
                 f[VT + n] = (WIDE ? acc[n][2 * hh + 1] : acc[n][1] + acc[n][3]) * inv * unit;
             }
-            if (whole) {
+            if (!before && !after) {
                 size_t row;
                 if (!out_row<R>(a, u, r, row)) continue;
 #pragma unroll
                 for (int e = 0; e < D / 4; e += 8) store_o8(a, row * D + t * (D / 4) + e, f + e);
                 if (a.lse && t == 0) a.lse[row] = lse2 * kLn2;
-            } else {
+            } else if (in_bounds(w < (int)gridDim.x * kWarps, a.status)) {
                 float4 *p = reinterpret_cast<float4 *>(keep + r * D + t * (D / 4));
 #pragma unroll
                 for (int e = 0; e < D / 16; ++e) p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                 if (t == 0) s_lse[warp][before ? 0 : 1][r] = lse2;
             }
         }
-        if (!whole && lane == 0) {
-            s_unit[warp][before ? 0 : 1] = u;
-            s_keep[warp][before ? 0 : 1] = keep;
-            s_has[warp] |= before ? 1 : 2;
+        if ((before || after) && lane == 0) {
+            const int side = before ? 0 : 1;
+            s_b[warp][side] = here.b;
+            s_unit[warp][side] = here.unit;
+            s_keep[warp][side] = keep;
+            s_has[warp] |= before ? (after ? 3 : 1) : 4;
         }
+        if (i < n_tiles) advance(here, left, a.units, tiles);
     }
     __syncthreads();
 
-    // Join the states of the CTA's shared units.  A group is a unit's pieces: a
-    // state that goes on (or, from warp 0, one begun in an earlier CTA) and the
-    // following warps' states of the same unit.  Each warp takes rows warp, warp + 8.
-    int64_t X1 = 0;  // past the CTA's last tile
-    for (int k = 0; k < kWarps; ++k) X1 = s_end[k] > X1 ? s_end[k] : X1;
+    // Join the states of the CTA's shared units.  A unit's pieces are a state
+    // that goes on (or, from warp 0, one begun in an earlier CTA) and the
+    // following warps' states of units begun before, up to one that ends.  Each
+    // warp takes rows warp, warp + 8; lane k holds piece k's weight.
+    uint32_t heads = 0, goes = 0, tails = 0;  // by warp, from s_has
+    {
+        const int has = lane < kWarps ? s_has[lane] : 0;
+        heads = __ballot_sync(0xffffffffu, has & 1);
+        goes = __ballot_sync(0xffffffffu, has & 2);
+        tails = __ballot_sync(0xffffffffu, has & 4);
+    }
+    if (!(tails | (heads & 1))) {  // nothing shared
+        if (threadIdx.x == 0) a.tail[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
     bool over = false;
-    for (int first = 0; first < kWarps; ++first) {
 #pragma unroll 1
-        for (int side = first == 0 ? 0 : 1; side < 2; ++side) {
-            if (!(s_has[first] & (1 << side))) continue;
-            const Unit u = s_unit[first][side];
-            int n = 1;  // pieces
-            if (u.end > s_end[first])
-                while (first + n < kWarps && (s_has[first + n] & 1) && s_unit[first + n][0].begin == u.begin) {
-                    ++n;
-                    if (u.end <= s_end[first + n - 1]) break;
-                }
-            const bool earlier = side == 0, later = u.end > X1;
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (earlier ? 0 : 1);
-            over = over || (later && !earlier);
-            if (later && !earlier && threadIdx.x == 0) {
-                const int last = (int)(worker_of(u.end - 1, total, workers) / kWarps);
-                a.tail[2 * blockIdx.x] = make_int4(1, last, u.b, u.hk);
-                a.tail[2 * blockIdx.x + 1] = make_int4(u.seg, u.rb, 0, 0);
-            }
-#pragma unroll 1
-            for (int r = warp; r < R; r += kWarps) {
-                float M = -INFINITY;
-                for (int k = 0; k < n; ++k) M = fmaxf(M, s_lse[first + k][k == 0 ? side : 0][r]);
-                const float top = M == -INFINITY ? 0.f : M;
-                float L = 0.f, o[D / 32] = {};
-                for (int k = 0; k < n; ++k) {
-                    const int sd = k == 0 ? side : 0;
-                    const float wt = ex2(s_lse[first + k][sd][r] - top);
-                    const float *src = s_keep[first + k][sd] + r * D + lane;
-                    L += wt;
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(wt, src[32 * e], o[e]);
-                }
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-                const float lse2 = L == 0.f ? -INFINITY : top + log2f(L);
-                if (earlier || later) {
-                    if (!in_bounds(slot < 2 * (int64_t)gridDim.x, a.status)) continue;
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) a.po[(slot * R + r) * D + lane + 32 * e] = o[e] * inv;
-                    if (lane == 0) a.pl[slot * R + r] = lse2;
-                } else {
-                    size_t row;
-                    if (!out_row<R>(a, u, r, row)) continue;
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) store_o(a, row * D + lane + 32 * e, o[e] * inv);
-                    if (a.lse && lane == 0) a.lse[row] = lse2 * kLn2;
-                }
+    for (int g0 = heads & 1 ? -1 : __ffs(tails) - 1; g0 < kWarps;) {
+        const int first = g0 < 0 ? 0 : g0, side = g0 < 0 ? 0 : 1;
+        int n = 1;
+        bool open = side ? true : (goes & 1);  // the unit goes on behind the pieces so far
+        while (open && first + n < kWarps && (heads >> (first + n) & 1)) {
+            open = goes >> (first + n) & 1;
+            ++n;
+        }
+        const bool earlier = side == 0;
+        const Unit u = unit_at(a, s_b[first][side], s_unit[first][side]);
+        const int slot = 2 * blockIdx.x + (earlier ? 0 : 1);
+        if (open && !earlier) {
+            over = true;
+            if (threadIdx.x == 0) {
+                const int nt = tiles(u.b);
+                const int64_t end = (a.pages ? (int64_t)u.b * a.units * nt : (int64_t)prefix[u.b] * a.units) +
+                                    (int64_t)(s_unit[first][side] + 1) * nt;
+                a.tail[blockIdx.x] = make_int4(1, (int)(worker_of(end - 1, total, workers) / kWarps), u.b,
+                                               s_unit[first][side]);
             }
         }
+#pragma unroll
+        for (int r = warp; r < R; r += kWarps) {
+            const float ls = lane < n ? s_lse[first + lane][lane == 0 ? side : 0][r] : -INFINITY;
+            float M = ls;
+#pragma unroll
+            for (int o = 1; o < kWarps; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float base = M == -INFINITY ? 0.f : M;
+            const float wt = ex2(ls - base);
+            float L = wt;
+#pragma unroll
+            for (int o = 1; o < kWarps; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            M = __shfl_sync(0xffffffffu, M, 0);
+            L = __shfl_sync(0xffffffffu, L, 0);
+            float o[D / 32] = {};
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, wt, k);
+                if (k >= n) continue;
+                const float *src = s_keep[first + k][k == 0 ? side : 0] + r * D + lane;
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) o[e] = fmaf(wk, src[32 * e], o[e]);
+            }
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const float lse2 = L == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(L);
+            if (earlier || open) {
+                if (!in_bounds(slot < 2 * (int)gridDim.x, a.status)) continue;
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) a.po[((size_t)slot * R + r) * D + lane + 32 * e] = o[e] * inv;
+                if (lane == 0) a.pl[slot * R + r] = lse2;
+            } else {
+                size_t row;
+                if (!out_row<R>(a, u, r, row)) continue;
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) store_o(a, row * D + lane + 32 * e, o[e] * inv);
+                if (a.lse && lane == 0) a.lse[row] = lse2 * kLn2;
+            }
+        }
+        // the next state that goes on (this group's own is `first` or none)
+        const uint32_t rest = tails >> first >> (side ? 1 : 0);
+        if (!rest) break;
+        g0 = first + (side ? 1 : 0) + __ffs(rest) - 1;
     }
-    if (!over && threadIdx.x == 0) a.tail[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!over && threadIdx.x == 0) a.tail[blockIdx.x] = make_int4(0, 0, 0, 0);
 }
 
 // Joins the states of the unit that runs over the end of CTA blockIdx.x's
@@ -739,14 +792,9 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) 
     __shared__ float red[kWarps];
     __shared__ float part[kWarps][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 d0 = a.tail[2 * blockIdx.x];
+    const int4 d0 = a.tail[blockIdx.x];
     if (!d0.x) return;
-    const int4 d1 = a.tail[2 * blockIdx.x + 1];
-    Unit u;
-    u.b = d0.z;
-    u.hk = d0.w;
-    u.seg = d1.x;
-    u.rb = d1.y;
+    const Unit u = unit_at(a, d0.z, d0.w);
     const int r = blockIdx.y;
     size_t row;
     if (!out_row<R>(a, u, r, row)) return;
@@ -799,9 +847,9 @@ int launch_fwd_t(const FwdArgs &a, unsigned grid, cudaStream_t stream) {
     constexpr int R = WIDE ? 16 : 8;
     auto fwd = cache_fwd_kernel<D, FMT, WIDE, KT>;
     constexpr size_t ring = (size_t)kWarps * kRing;
-    if (!set_smem_limit_once(reinterpret_cast<const void *>(fwd), (int)(ring + (kMaxCacheBatch + 1) * 8)))
+    if (!set_smem_limit_once(reinterpret_cast<const void *>(fwd), (int)(ring + (kMaxCacheBatch + 1) * 4)))
         return ATTN_ERR_LAUNCH;
-    fwd<<<grid, kThreads, ring + (a.pages ? 0 : ((size_t)a.B + 1) * 8), stream>>>(a);
+    fwd<<<grid, kThreads, ring + (a.pages ? 0 : ((size_t)a.B + 1) * 4), stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, (unsigned)(a.rows < R ? a.rows : R));
@@ -840,11 +888,11 @@ int launch_fwd_w(const FwdArgs &a, bool wide, int kt, unsigned grid, cudaStream_
 // rows do not fit eight.
 static bool cache_wide(int rows, int dtype) { return dtype == ATTN_BF16 && rows > 8; }
 
-// Workspace: the tails [2 * CTA], a state per warp, two per CTA and their lse.
+// Workspace: the tails [CTA], a state per warp, two per CTA and their lse.
 size_t cache_fwd_workspace(int B, int H, int H_kv, int Sq, int d, int dtype, bool listed) {
     const int64_t rows = (int64_t)(H / H_kv) * (listed ? 1 : Sq);
     const size_t R = cache_wide((int)(rows > 16 ? 16 : rows), dtype) ? 16 : 8;
-    return (size_t)kCacheMaxCtas * (32 + (kWarps + 2) * R * d * 4 + 2 * R * 4);
+    return (size_t)kCacheMaxCtas * (16 + (kWarps + 2) * R * d * 4 + 2 * R * 4);
 }
 
 int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, const int32_t *table,
@@ -865,7 +913,12 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     const bool wide = cache_wide(a.rows, dtype);
     const int R = wide ? 16 : 8;
     a.nrb = (a.rows + R - 1) / R;
-    const int64_t units = (int64_t)B * a.Hkv * a.nseg * a.nrb;  // at most B * H * Sq < 2^31
+    a.units = a.Hkv * a.nseg * a.nrb;
+    const int64_t units = (int64_t)B * a.units;  // at most B * H * Sq < 2^31
+    a.by_units = fast_div((uint32_t)a.units);
+    a.by_per = fast_div((uint32_t)(a.nseg * a.nrb));
+    a.by_nrb = fast_div((uint32_t)a.nrb);
+    a.by_group = fast_div((uint32_t)a.G);
     a.status = status_word_device_ptr();
     if (!a.status) return ATTN_ERR_CUDA;
     const int kt = tile_keys(c.d, c.page);
@@ -878,7 +931,7 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     if (ctas > sms) ctas = sms;
     a.workers = (int)ctas * kWarps;
     a.tail = reinterpret_cast<int4 *>(workspace);
-    a.hold = reinterpret_cast<float *>(a.tail + 2 * ctas);
+    a.hold = reinterpret_cast<float *>(a.tail + ctas);
     a.po = a.hold + (size_t)a.workers * R * c.d;
     a.pl = a.po + (size_t)2 * ctas * R * c.d;
     if (c.d == 64)

@@ -21,6 +21,12 @@ int64_t of_(int64_t x, int64_t t, int64_t n) { return worker_of(x, t, n); }
 int64_t count_(int64_t t, int64_t most, int64_t least) { return worker_count(t, most, least); }
 int clamp_(int len, int pages, int page) { return clamp_len(len, pages, page); }
 int visible_(int len, int cnt, int i, int causal) { return visible_keys(len, cnt, i, causal); }
+uint32_t div_(uint32_t n, uint32_t d) { return n / fast_div(d); }
+void advance_(int *p, int by, int units, const int *tiles) {
+    Place q = {p[0], p[1], p[2], p[3]};
+    advance(q, by, units, [&](int b) { return tiles[b]; });
+    p[0] = q.b; p[1] = q.unit; p[2] = q.t; p[3] = q.n;
+}
 int64_t touched_(int64_t s, int page) { return touched_pages(s, page); }
 }
 """
@@ -43,7 +49,32 @@ def idx(tmp_path_factory):
         t = {8: ctypes.c_int64, 4: ctypes.c_int}
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = t[res], [t[a] for a in args]
+    lib.div_.restype, lib.div_.argtypes = ctypes.c_uint32, [ctypes.c_uint32] * 2
+    ints = ctypes.POINTER(ctypes.c_int)
+    lib.advance_.restype, lib.advance_.argtypes = None, [ints, ctypes.c_int, ctypes.c_int, ints]
     return lib
+
+
+def test_division_by_multiplication(idx):
+    top = 2 ** 31 - 1
+    for d in (1, 2, 3, 5, 7, 8, 9, 127, 128, 129, 1000, 65535, 65536, 99991, 2 ** 30, 2 ** 30 + 1, top):
+        for k in (0, 1, 2, 3, top // d // 2, top // d):
+            for n in (k * d - 1, k * d, k * d + 1, k * d + d - 1, top):
+                if 0 <= n <= top:
+                    assert idx.div_(n, d) == n // d, (n, d)
+
+
+@pytest.mark.parametrize("tiles", [[3], [1, 0, 2], [0, 5, 0, 0, 1, 7], [1] * 9])
+@pytest.mark.parametrize("units", [1, 2, 5])
+@pytest.mark.parametrize("by", [1, 4, 32])
+def test_advance_steps_through_the_units(idx, tiles, units, by):
+    order = [(b, u, t, n) for b, n in enumerate(tiles) for u in range(units) for t in range(n)]
+    c = (ctypes.c_int * len(tiles))(*tiles)
+    for start in range(len(order)):
+        if start + by < len(order):
+            p = (ctypes.c_int * 4)(*order[start])
+            idx.advance_(p, by, units, c)
+            assert tuple(p) == order[start + by]
 
 
 @pytest.mark.parametrize("workers", [1, 2, 7, 1216, 1280])
@@ -190,7 +221,7 @@ def test_bad_caches_are_refused(lib, name, kw):
     ("select", dict(ws=WS + 8)), ("select", dict(bytes=2 * 2 * (12 * 4 + 4) - 1)), ("select", dict(ws=K)),
     ("select", dict(ws=PAGES)), ("select", dict(max_pages=28673)), ("select", dict(lens=None)),
     ("attend", dict(q=None)), ("attend", dict(o=None)), ("attend", dict(o=O + 8)), ("attend", dict(lse=L + 2)),
-    ("attend", dict(H=5)), ("attend", dict(H=-2)), ("attend", dict(Sq=-1)), ("attend", dict(B=4097)),
+    ("attend", dict(H=5)), ("attend", dict(H=-2)), ("attend", dict(max_pages=1 << 30)), ("attend", dict(Sq=-1)), ("attend", dict(B=4097)),
     ("attend", dict(causal=3)), ("attend", dict(scale=float("nan"))), ("attend", dict(scale=float("inf"))),
     ("attend", dict(dtype=-1)), ("attend", dict(n=2)), ("attend", dict(pages=PAGES, n=0)),
     ("attend", dict(pages=PAGES + 1, n=2)), ("attend", dict(ws=None)), ("attend", dict(ws=WS + 4)),
