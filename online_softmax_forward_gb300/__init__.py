@@ -510,6 +510,7 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale, self.k_bounds = k, v, k_scale, v_scale, k_bounds
         self.n_pages, self.H_kv, self.page, self.d = n, h, page, d
         self.device = k.device
+        self._scratch = {}  # stream handle -> workspace of the calls on that stream
         self.c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                         k_bounds.data_ptr() if k_bounds is not None else None, n, h, page, d,
                         formats[k.dtype])
@@ -526,8 +527,8 @@ class KVCache:
 
 
 def _int32_on(t, shape, device, name):
-    import torch
-    if (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device):
+    """Pointer of an int32 array of the call."""
+    if t.dtype is not _int32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s"
                          % (name, tuple(shape), device))
     return t.data_ptr()
@@ -536,37 +537,47 @@ def _int32_on(t, shape, device, name):
 def _sequence_args(cache, table, lens, counts, B):
     """Checks the arrays of the call's sequences; returns the table's pointer and width, and the
     pointers of lens and counts."""
-    if table.dim() != 2 or table.shape[0] != B:
+    global _int32
+    if _int32 is None:
+        import torch
+        _int32 = torch.int32
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != B:
         raise ValueError("table must be [B, max_pages] with B = %d" % B)
     dev = cache.device
-    width = table.shape[1]
-    return (_int32_on(table, (B, width), dev, "table"), width, _int32_on(lens, (B,), dev, "lens"),
-            None if counts is None else _int32_on(counts, (B,), dev, "counts"))
+    one = (B,)
+    return (_int32_on(table, shape, dev, "table"), shape[1], _int32_on(lens, one, dev, "lens"),
+            None if counts is None else _int32_on(counts, one, dev, "counts"))
 
 
-def _call_on(device, fn, args, stream):
-    """fn(*args, stream handle) with ``device`` current; raises for a status other than ATTN_OK.
-    A decode step's calls are short: the device guard is taken only when it changes something,
-    and the current stream's handle is asked for without making a Stream object."""
+_int32 = None  # torch.int32 once a call has needed it
+
+
+def _call_on(device, fn, *args):
+    """fn(*args) with ``device`` current; raises for a status other than ATTN_OK."""
     import torch
-    if stream is not None:
-        handle = stream.cuda_stream
-    else:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
     if torch._C._cuda_getDevice() == device.index:
-        st = fn(*args, handle)
+        st = fn(*args)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, handle)
+            st = fn(*args)
     if st != ATTN_OK:
         raise AttnError(st, fn.__name__)
 
 
+def _handle(device, stream):
+    """The cudaStream_t of ``stream``, or of the device's current stream: asked for without
+    making a Stream object, which takes longer than a launch."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
 def _cache_rows(cache, k, v):
     """(B, S, attn_dtype) of new rows."""
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+    shape = k.shape
+    if len(shape) != 4 or shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must be [B, H_kv, S, d] of one dtype")
-    B, H, S, d = k.shape
+    B, H, S, d = shape
     if H != cache.H_kv or d != cache.d:
         raise ValueError("k has %d heads of width %d, the cache %d of %d" % (H, d, cache.H_kv, cache.d))
     for t in (k, v):
@@ -582,8 +593,8 @@ def cache_append(cache, k, v, table, pos, counts=None, stream=None):
     tensors, read on the device."""
     B, S, code = _cache_rows(cache, k, v)
     t, width, p, n = _sequence_args(cache, table, pos, counts, B)
-    _call_on(cache.device, load_library().attn_cache_append,
-             (cache.c, k.data_ptr(), v.data_ptr(), t, width, p, n, B, S, code), stream)
+    _call_on(cache.device, load_library().attn_cache_append, cache.c, k.data_ptr(), v.data_ptr(), t,
+             width, p, n, B, S, code, _handle(cache.device, stream))
 
 
 def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
@@ -603,22 +614,23 @@ def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
         k, v = out
         _check_out(k, shape, dtype, cache.device, "out[0]")
         _check_out(v, shape, dtype, cache.device, "out[1]")
-    _call_on(cache.device, load_library().attn_cache_read,
-             (cache.c, t, width, n, k.data_ptr(), v.data_ptr(), B, S, code), stream)
+    _call_on(cache.device, load_library().attn_cache_read, cache.c, t, width, n, k.data_ptr(),
+             v.data_ptr(), B, S, code, _handle(cache.device, stream))
     return k, v
 
 
 def _cache_q(cache, q):
     """(B, H, Sq) of queries."""
-    if q.dim() != 4 or q.shape[3] != cache.d or q.shape[1] % cache.H_kv != 0 or q.shape[1] == 0:
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != cache.d or shape[1] % cache.H_kv != 0 or shape[1] == 0:
         raise ValueError("q must be [B, H, Sq, %d] with H a multiple of %d, got %s"
-                         % (cache.d, cache.H_kv, tuple(q.shape)))
+                         % (cache.d, cache.H_kv, tuple(shape)))
     if not q.is_contiguous() or q.device != cache.device:
         raise ValueError("q must be a contiguous tensor on %s" % cache.device)
-    return q.shape[:3]
+    return shape[0], shape[1], shape[2]
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _need(size, *args):
     """Bytes of a workspace: ``size`` depends on its arguments alone."""
     st, need = size(*args)
@@ -626,15 +638,28 @@ def _need(size, *args):
     return need
 
 
-def _workspace(workspace, need, device):
-    """(tensor, pointer, bytes) of the scratch of one call."""
+def _workspace(workspace, need, cache, stream, handle):
+    """(pointer, bytes, tensor) of the scratch of one call; the tensor has to outlive the launch.
+    Calls on one stream follow one another, so the cache keeps a workspace for each stream; a
+    call that is being captured gets one of its own from the graph's memory, and a call on a
+    stream that is not the current one one that lives until that stream is done with it."""
     import torch
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-        return workspace, workspace.data_ptr(), need
-    if not workspace.is_contiguous() or _device_of(workspace) != device:
-        raise ValueError("workspace must be a contiguous tensor on %s" % device)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace is not None:
+        if not workspace.is_contiguous() or _device_of(workspace) != cache.device:
+            raise ValueError("workspace must be a contiguous tensor on %s" % cache.device)
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    keep = stream is None and not torch._C._cuda_isCurrentStreamCapturing()
+    if keep:
+        kept = cache._scratch.get(handle)
+        if kept is not None and kept[1] >= need:
+            return kept
+    workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
+    new = (workspace.data_ptr(), max(need, 16), workspace)
+    if keep:
+        cache._scratch[handle] = new
+    elif stream is not None:
+        workspace.record_stream(stream)
+    return new
 
 
 def cache_select(q, cache, table, lens, n_select, counts=None, causal: bool = True, workspace=None,
@@ -649,12 +674,12 @@ def cache_select(q, cache, table, lens, n_select, counts=None, causal: bool = Tr
         raise ValueError("n_select must be at least 1, got %d" % n_select)
     t, width, p, n = _sequence_args(cache, table, lens, counts, B)
     code = dtype_code(q.dtype)
-    ws, wp, wn = _workspace(workspace, _need(attn_cache_select_workspace_size, B, cache.H_kv, Sq, width),
-                            cache.device)
+    handle = _handle(cache.device, stream)
+    need = _need(attn_cache_select_workspace_size, B, cache.H_kv, Sq, width)
+    wp, wn, held = _workspace(workspace, need, cache, stream, handle)
     pages = torch.empty((B, cache.H_kv, Sq, n_select), dtype=torch.int32, device=cache.device)
-    _call_on(cache.device, load_library().attn_cache_select,
-             (cache.c, q.data_ptr(), t, width, p, n, pages.data_ptr(), n_select, B, H, Sq,
-              1 if causal else 0, code, wp, wn), stream)
+    _call_on(cache.device, load_library().attn_cache_select, cache.c, q.data_ptr(), t, width, p, n,
+             pages.data_ptr(), n_select, B, H, Sq, 1 if causal else 0, code, wp, wn, handle)
     return pages
 
 
@@ -675,11 +700,12 @@ def attention_cache(q, cache, table, lens, counts=None, causal: bool = True,
         if n_select < 1:
             raise ValueError("pages must list at least one page")
         listed = _int32_on(pages, (B, cache.H_kv, Sq, n_select), cache.device, "pages")
-    ws, wp, wn = _workspace(workspace, _need(attn_fwd_cache_workspace_size, B, H, cache.H_kv, Sq,
-                                             cache.d, code, n_select), cache.device)
+    handle = _handle(cache.device, stream)
+    need = _need(attn_fwd_cache_workspace_size, B, H, cache.H_kv, Sq, cache.d, code, n_select)
+    wp, wn, held = _workspace(workspace, need, cache, stream, handle)
     out = torch.empty_like(q) if out_dtype is None else torch.empty_like(q, dtype=out_dtype)
     lse = torch.empty((B, H, Sq), dtype=torch.float32, device=cache.device)
-    _call_on(cache.device, load_library().attn_fwd_cache,
-             (cache.c, q.data_ptr(), out.data_ptr(), lse.data_ptr(), t, width, p, n, listed, n_select,
-              B, H, Sq, 1 if causal else 0, 0.0 if scale is None else float(scale), code, wp, wn), stream)
+    _call_on(cache.device, load_library().attn_fwd_cache, cache.c, q.data_ptr(), out.data_ptr(),
+             lse.data_ptr(), t, width, p, n, listed, n_select, B, H, Sq, 1 if causal else 0,
+             0.0 if scale is None else float(scale), code, wp, wn, handle)
     return out, lse
