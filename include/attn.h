@@ -363,8 +363,9 @@ ATTN_API int attn_cache_read(const attn_cache *cache, const int32_t *table, int 
  *   causal, counts as attn_fwd_cache;  max_pages and n_select <= 28672
  *   workspace  16-byte aligned scratch of attn_cache_select_workspace_size
  *          bytes, not overlapping any other argument
+ *   B * H_kv * Sq < 2^28
  * The choice is that of exact sums (fp64 decides where fp32 does not).
- * Two kernels.
+ * One kernel.
  */
 ATTN_API int attn_cache_select_workspace_size(int B, int H_kv, int Sq, int max_pages, size_t *bytes);
 ATTN_API int attn_cache_select(const attn_cache *cache, const void *q, const int32_t *table,

@@ -41,7 +41,8 @@ CHECKED_SOURCES = [(src, src.replace(".cu", "_checked.o"),
                     ["-DATTN_BOUNDS_CHECK"] + (["-DATTN_TEST_EXPORTS"] if src == "attn_api.cu"
                                                else []))
                    for src in SOURCES]
-HEADERS = ["attn_internal.h", "cache_codec.cuh", "cache_index.h", "sm100_ptx.cuh"]
+HEADERS = ["attn_internal.h", "cache_codec.cuh", "cache_index.h", "cache_mma.cuh",
+           "sm100_ptx.cuh"]
 PUBLIC_HEADERS = ["attn.h", "attn_test.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -616,9 +616,9 @@ int attn_cache_read(const attn_cache *cache, const int32_t *table, int max_pages
 int attn_cache_select_workspace_size(int B, int H_kv, int Sq, int max_pages, size_t *bytes) {
     if (!bytes || B < 0 || H_kv < 1 || Sq < 0 || max_pages < 1 || max_pages > kMaxSelectPages)
         return ATTN_ERR_INVALID_ARG;
-    const double est = (double)B * H_kv * Sq * (12.0 * max_pages + 4.0);
+    const double est = (double)B * H_kv * Sq * 8.0 * max_pages;
     if (est > 9.0e18) return ATTN_ERR_INVALID_ARG;
-    *bytes = (size_t)B * H_kv * Sq * ((size_t)12 * max_pages + 4);
+    *bytes = (size_t)B * H_kv * Sq * 8 * max_pages;
     return ATTN_OK;
 }
 
@@ -635,7 +635,7 @@ int attn_cache_select(const attn_cache *cache, const void *q, const int32_t *tab
         return ATTN_ERR_INVALID_ARG;
     if (B == 0 || Sq == 0) return ATTN_OK;
     const int64_t units = (int64_t)B * cache->H_kv * Sq;
-    if (units > INT32_MAX) return ATTN_ERR_INVALID_ARG;
+    if (units > INT32_MAX / 8) return ATTN_ERR_INVALID_ARG;
     if (!q || !aligned(q, 16) || !pages || !aligned(pages, 4) || !workspace ||
         !aligned(workspace, 16) || workspace_bytes < need)
         return ATTN_ERR_INVALID_ARG;

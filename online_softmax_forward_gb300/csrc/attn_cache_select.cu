@@ -7,12 +7,20 @@
 // page * d.  The page of the query's last visible key is always taken, then
 // the highest scores, ties to the lowest page.
 //
-// Scores are summed in fp32 with a bound on their error.  A page whose score
-// is further from the cut than that is decided by it; the few others are
-// summed again in fp64, where the products of a 16-bit q and an 8-bit code
-// (at most 19 bits) add up exactly unless they span more than 2^27, so the
-// choice does not depend on the order of a sum.  (fp64 for every page would
-// cost more than the reading: this GPU has 1/64 the fp64 rate.)
+// With q split into its positive and negative part the sum is one product of
+// length 2 d, [q+ q-] . [hi lo]: eight heads and eight pages at a time on
+// mma.m16n8k16, in the fp16 form of attn_cache_fwd.cu (a power of two per row of
+// q, codes exact).  A cluster of CTAs shares the pages of one (sequence, kv
+// head, query) and writes its scores into the first CTA's shared memory, which
+// finds the cut by bisection and writes the list.
+//
+// The fp32 scores carry a bound on their error.  A page whose score is further
+// from the cut than that is decided by it; the few others are summed again in
+// fp64, where the products of a 16-bit q and an 8-bit code (at most 19 bits) add
+// up exactly unless they span more than 2^27, so the choice does not depend on
+// the order of a sum.  (fp64 for every page would cost more than the reading:
+// this GPU has 1/64 the fp64 rate.)
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -20,9 +28,15 @@
 #include "attn_internal.h"
 #include "cache_codec.cuh"
 #include "cache_index.h"
+#include "cache_mma.cuh"
 
 namespace attn {
 namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kGroups = 4;  // groups of eight pages a warp loads at once
 
 struct SelectArgs {
     const void *q;  // [B][Hkv * G][Sq][d]
@@ -30,121 +44,10 @@ struct SelectArgs {
     const float *k_scale;
     const int32_t *table, *lens, *counts;
     int32_t *pages;  // [B][Hkv][Sq][n]
-    float *scores;   // [B][Hkv][Sq][max_pages]
-    float *mass;     // [B][Hkv][Sq]: max over the group of sum |q|
     double *exact;   // [B][Hkv][Sq][max_pages]: fp64 scores of the pages near the cut
-    int B, Hkv, G, Sq, page, n_pages, max_pages, n, causal;
+    int B, Hkv, G, Sq, page, n_pages, max_pages, n, causal, cluster;
     int *status;
 };
-
-constexpr int kScoreThreads = 256;
-constexpr int kScorePages = 128;   // pages per CTA of the score kernel
-constexpr int kSelectThreads = 256;
-
-__device__ __forceinline__ float warp_sum_f(float x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-// Pages visible to query i of sequence b.
-__device__ __forceinline__ int visible_pages(const SelectArgs &a, int b, int i) {
-    const int len0 = a.lens[b], cnt0 = a.counts ? a.counts[b] : a.Sq;
-    const int len = clamp_len(len0, a.max_pages, a.page);
-    const int cnt = min(max(cnt0, 0), a.Sq);
-    if ((len != len0 || cnt != cnt0) && threadIdx.x == 0) atomicOr(a.status, kStatusTable);
-    const int keys = visible_keys(len, cnt, i, a.causal);
-    return (int)(((int64_t)keys + a.page - 1) / a.page);
-}
-
-// Physical page, or -1 (reported) for an entry outside the pool.
-__device__ __forceinline__ int page_of(const SelectArgs &a, int b, int lp) {
-    const int phys = a.table[(int64_t)b * a.max_pages + lp];
-    if (phys < 0 || phys >= a.n_pages) {
-        atomicOr(a.status, kStatusTable);
-        return -1;
-    }
-    return phys;
-}
-
-// grid (units, page chunks); 16 channels per lane, D / 16 lanes per page.
-template <int D, int FMT, int DT>
-__global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const SelectArgs a) {
-    constexpr int L = D / 16;       // lanes per page
-    constexpr int PPW = 32 / L;     // pages per warp step
-    extern __shared__ float sq[];   // [G][D] positive parts, then [G][D] negative parts
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t unit = blockIdx.x;  // (b, hk, i)
-    const int i = (int)(unit % a.Sq);
-    const int hk = (int)(unit / a.Sq % a.Hkv);
-    const int b = (int)(unit / a.Sq / a.Hkv);
-    const int vis = visible_pages(a, b, i);
-    const int p0 = blockIdx.y * kScorePages;
-    if (vis <= a.n || p0 >= vis - 1) return;  // every page is taken, or none of these is scored
-    float *pos = sq, *neg = sq + a.G * D;
-    for (int t = threadIdx.x; t < a.G * (D / 8); t += kScoreThreads) {
-        const int g = t / (D / 8), c = t % (D / 8) * 8;
-        float f[8];
-        codec::load8<DT>(a.q, (((size_t)b * a.Hkv * a.G + hk * a.G + g) * a.Sq + i) * D + c, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {  // written so that a NaN stays in both parts
-            pos[g * D + c + e] = f[e] < 0.f ? 0.f : f[e];
-            neg[g * D + c + e] = f[e] > 0.f ? 0.f : f[e];
-        }
-    }
-    __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = lane / L, l = lane % L;
-    if (blockIdx.y == 0 && warp == 0) {
-        float most = 0.f;
-        for (int g = 0; g < a.G; ++g) {
-            float s = 0.f;
-            for (int c = lane; c < D; c += 32) s += pos[g * D + c] - neg[g * D + c];
-            s = warp_sum_f(s);
-            most = (s > most || s != s) ? s : most;
-        }
-        if (lane == 0) a.mass[unit] = most;
-    }
-    const int p1 = min(p0 + kScorePages, vis - 1);
-    for (int base = p0 + warp * PPW; base < p1; base += kScoreThreads / 32 * PPW) {
-        const int lp = base + sub;
-        float best = -INFINITY, s = 0.f;
-        int phys = -1;
-        if (lp < p1) phys = page_of(a, b, lp);
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-        if (phys >= 0) {
-            const int64_t ph = (int64_t)phys * a.Hkv + hk;
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.bounds + (size_t)ph * 2 * D) + l;
-            lo = src[0];
-            hi = src[L];
-            s = a.k_scale[ph];
-        }
-        float fl[16], fh[16];
-        codec::decode4<FMT>(lo.x, fl); codec::decode4<FMT>(lo.y, fl + 4);
-        codec::decode4<FMT>(lo.z, fl + 8); codec::decode4<FMT>(lo.w, fl + 12);
-        codec::decode4<FMT>(hi.x, fh); codec::decode4<FMT>(hi.y, fh + 4);
-        codec::decode4<FMT>(hi.z, fh + 8); codec::decode4<FMT>(hi.w, fh + 12);
-        for (int g = 0; g < a.G; ++g) {
-            const float4 *qp = reinterpret_cast<const float4 *>(pos + g * D + l * 16);
-            const float4 *qn = reinterpret_cast<const float4 *>(neg + g * D + l * 16);
-            float x = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 u = qp[e], w = qn[e];
-                x = fmaf(u.x, fh[4 * e], fmaf(w.x, fl[4 * e], x));
-                x = fmaf(u.y, fh[4 * e + 1], fmaf(w.y, fl[4 * e + 1], x));
-                x = fmaf(u.z, fh[4 * e + 2], fmaf(w.z, fl[4 * e + 2], x));
-                x = fmaf(u.w, fh[4 * e + 3], fmaf(w.w, fl[4 * e + 3], x));
-            }
-#pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            best = (x > best || x != x) ? x : best;
-        }
-        // a page outside the pool scores lowest
-        if (lp < p1 && l == 0 && in_bounds(lp < a.max_pages, a.status))
-            a.scores[unit * a.max_pages + lp] = phys >= 0 ? best * s : -INFINITY;
-    }
-}
 
 // fp32 value as an integer of the same order.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -153,6 +56,22 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 __device__ __forceinline__ float unordered(uint32_t u) {
     return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u);
+}
+
+// `local` (a shared memory address) in the cluster's first CTA.
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t local) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(local));
+    return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Exclusive prefix sum of one flag per thread; *total gets the block's sum.
@@ -164,7 +83,7 @@ __device__ __forceinline__ int block_scan(int x, int *warps, int *total) {
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += warps[w];
         all += warps[w];
     }
@@ -172,101 +91,228 @@ __device__ __forceinline__ int block_scan(int x, int *warps, int *total) {
     return before + __popc(m & ((1u << lane) - 1));
 }
 
-// One CTA per (b, hk, i).  Shared memory: keys [max_pages], then the list of
-// pages near the cut [max_pages].
+// One cluster per (b, hk, i).  Dynamic shared memory: keys [max_pages], then
+// the list of pages near the cut [max_pages].
 template <int D, int FMT, int DT>
-__global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const SelectArgs a) {
-    extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int hist[256], wsum[kSelectThreads / 32];
-    __shared__ int s_bin, s_left, s_near;
-    __shared__ uint32_t s_top;
-    const int64_t unit = blockIdx.x;
+__global__ void __launch_bounds__(kThreads) cache_select_kernel(const SelectArgs a) {
+    using U = Unpack<FMT>;
+    constexpr int QS = D / 16;
+    extern __shared__ __align__(16) uint32_t key[];
+    __shared__ int wsum[2][kWarps], s_near;
+    __shared__ uint32_t wmin[2][kWarps], s_top[kMaxCluster];
+    const int64_t unit = blockIdx.x / a.cluster;
+    const int rank = (int)(blockIdx.x - unit * a.cluster);
     const int i = (int)(unit % a.Sq);
     const int hk = (int)(unit / a.Sq % a.Hkv);
     const int b = (int)(unit / a.Sq / a.Hkv);
-    const int vis = visible_pages(a, b, i);
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, t4 = lane & 3;
+    const int len0 = a.lens[b], cnt0 = a.counts ? a.counts[b] : a.Sq;
+    const int len = clamp_len(len0, a.max_pages, a.page);
+    const int cnt = min(max(cnt0, 0), a.Sq);
+    if ((len != len0 || cnt != cnt0) && t == 0) atomicOr(a.status, kStatusTable);
+    const int vis = (int)(((int64_t)visible_keys(len, cnt, i, a.causal) + a.page - 1) / a.page);
     int32_t *out = a.pages + unit * a.n;
-    const int t = threadIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (vis <= a.n) {
-        for (int j = t; j < a.n; j += kSelectThreads) out[j] = j < vis ? j : -1;
+    if (vis <= a.n) {  // every page, for the whole cluster
+        if (rank == 0)
+            for (int j = t; j < a.n; j += kThreads) out[j] = j < vis ? j : -1;
         return;
     }
-    double *exact = a.exact + unit * a.max_pages;                         // [max_pages]
-    uint32_t *key = reinterpret_cast<uint32_t *>(sm);                     // [max_pages]
-    int *near = reinterpret_cast<int *>(key + a.max_pages);               // [max_pages]
+    cluster_arrive();  // all CTAs of the cluster run before anyone writes to the first
     const int m = vis - 1;       // pages that compete
     const int k = a.n - 1;       // places for them
-    if (t == 0) {
-        s_near = 0;
-        s_top = 0;
-    }
-    __syncthreads();
-    const float *sc = a.scores + unit * a.max_pages;
-    // the largest scale bounds every page's error; a score that is not
-    // finite leaves the whole decision to fp64
-    float scale_top = 0.f;
-    bool odd = false;
-    for (int p = t; p < m; p += kSelectThreads) {
-        const float x = sc[p];
-        key[p] = ordered(x);
-        const int phys = a.table[(int64_t)b * a.max_pages + p];
-        if (phys >= 0 && phys < a.n_pages) {
-            const float s = a.k_scale[(int64_t)phys * a.Hkv + hk];
-            if (!(fabsf(x) <= 3.402823466e38f) || s != s) odd = true;
-            scale_top = fmaxf(scale_top, s);
-        }
-    }
-    atomicMax(&s_top, odd ? 0x7f800000u : __float_as_uint(scale_top));
-    __syncthreads();
-    // |error| <= 2^-24 * (16 + 4 additions) * sum |q| * top * scale, and the
-    // rounding of the last product; 24 covers both
-    constexpr float kTop = FMT == ATTN_CACHE_E4M3 ? 448.f : 128.f;
-    const float eps = 24.f * 5.9604645e-8f * kTop * a.mass[unit] * __uint_as_float(s_top);
+    const int32_t *table = a.table + (int64_t)b * a.max_pages;
 
-    float cut_lo = -INFINITY, cut_hi = INFINITY;  // decided above cut_hi: in; below cut_lo: out
-    if (k == 0) {
-        cut_lo = INFINITY;
-    } else if (eps <= 3.402823466e38f) {
-        // the k-th largest key, 8 bits at a time
-        uint32_t prefix = 0, mask = 0;
-        int left = k;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int h = t; h < 256; h += kSelectThreads) hist[h] = 0;
-            __syncthreads();
-            for (int p = t; p < m; p += kSelectThreads)
-                if ((key[p] & mask) == prefix) atomicAdd(&hist[(key[p] >> shift) & 255], 1);
-            __syncthreads();
-            if (t < 32) {  // lane t: bins 255 - 8 t down to 248 - 8 t
-                int c[8], sum = 0;
+    // ---- scores of this CTA's pages
+    const int slice = ((m + a.cluster - 1) / a.cluster + 7) / 8 * 8;
+    const int p0 = rank * slice, p1 = min(m, p0 + slice);
+    const uint32_t first_key = in_first_cta((uint32_t)__cvta_generic_to_shared(key));
+    float mass = 0.f, scale_top = 0.f;
+    bool odd = false;
+    for (int g0 = 0; g0 < a.G; g0 += 8) {
+        // rows: heads g0 + g.  k steps 0 .. QS - 1 hold the positive parts of channels
+        // 4s .. 4s + 3 of the lane's D/4, the others the negative ones
+        uint32_t qa[2][QS][4];
+        float back, sum = 0.f;
+        {
+            float f[D / 4];
+            if (g0 + g < a.G) {
+                const size_t at = (((size_t)b * a.Hkv * a.G + hk * a.G + g0 + g) * a.Sq + i) * D + t4 * (D / 4);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum += c[e] = hist[255 - 8 * t - e];
-                int incl = sum;
+                for (int e = 0; e < D / 4; e += 8) codec::load8<DT>(a.q, at + e, f + e);
+            } else {
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (t >= o) incl += y;
+                for (int e = 0; e < D / 4; ++e) f[e] = 0.f;
+            }
+            float amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < D / 4; ++e) {
+                amax = fmaxf(amax, fabsf(f[e]));
+                sum += fabsf(f[e]);
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            float mul;
+            row_power(amax, mul, back);
+#pragma unroll
+            for (int s = 0; s < QS; ++s)
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    float y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // a NaN stays in both parts
+                        const float v = f[4 * s + e];
+                        y[e] = ((side ? v > 0.f : v < 0.f) ? 0.f : v) * mul;
+                    }
+                    uint32_t *x = qa[side][s];
+                    x[0] = pack_f16(y[0], y[1]);
+                    x[2] = pack_f16(y[2], y[3]);
+                    x[1] = x[3] = 0;
+                    if constexpr (DT == 0) {  // rows 8 .. 15: what fp16 leaves of an fp32 q
+                        const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&x[0]));
+                        const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&x[2]));
+                        x[1] = pack_f16(y[0] - u.x, y[1] - u.y);
+                        x[3] = pack_f16(y[2] - w.x, y[3] - w.y);
+                    }
                 }
-                int above = incl - sum;
-                if (above < left && left <= incl) {
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        mass = (sum > mass || sum != sum) ? sum : mass;
+        if (g0 == 0) cluster_wait();
+#pragma unroll 1
+        for (int base = p0 + warp * 8 * kGroups; base < p1; base += kThreads / 4 * kGroups) {
+            uint4 lo[kGroups][D / 64], hi[kGroups][D / 64];
+            float sc[kGroups];
+            int phys[kGroups];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (above < left && left <= above + c[e]) {
-                            s_bin = 255 - 8 * t - e;
-                            s_left = left - above;
-                            above = 1 << 30;
-                        } else {
-                            above += c[e];
-                        }
+            for (int j = 0; j < kGroups; ++j) {
+                const int p = base + 8 * j + g;
+                phys[j] = p < p1 ? table[p] : -1;
+            }
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+                const bool in = phys[j] >= 0 && phys[j] < a.n_pages;
+                if (base + 8 * j + g < p1 && !in && t4 == 0) atomicOr(a.status, kStatusTable);
+                const int64_t ph = in ? (int64_t)phys[j] * a.Hkv + hk : 0;
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.bounds + (size_t)ph * 2 * D + t4 * (D / 4));
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    lo[j][c] = in ? src[c] : make_uint4(0, 0, 0, 0);
+                    hi[j][c] = in ? src[D / 16 + c] : make_uint4(0, 0, 0, 0);
+                }
+                sc[j] = in ? a.k_scale[ph] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+                float s0[4] = {}, s1[4] = {};
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint32_t hw[4] = {hi[j][c].x, hi[j][c].y, hi[j][c].z, hi[j][c].w};
+                    const uint32_t lw[4] = {lo[j][c].x, lo[j][c].y, lo[j][c].z, lo[j][c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t b0, b1;
+                        const uint32_t *x = qa[0][c * 4 + e], *y = qa[1][c * 4 + e];
+                        U::quad(hw[e], b0, b1);
+                        mma16816(s0, x[0], x[1], x[2], x[3], b0, b1);
+                        U::quad(lw[e], b0, b1);
+                        mma16816(s1, y[0], y[1], y[2], y[3], b0, b1);
+                    }
+                }
+                scale_top = fmaxf(scale_top, sc[j]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {  // page 2 t4 + c of the group, head g0 + g
+                    float x = (s0[c] + s1[c]) + (s0[2 + c] + s1[2 + c]);
+                    x = x != x ? INFINITY : x * back;
+                    if (g0 + g >= a.G) x = -INFINITY;
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                    const int from = (2 * t4 + c) * 4;
+                    const float s = __shfl_sync(0xffffffffu, sc[j], from);
+                    const int ok = __shfl_sync(0xffffffffu, phys[j], from);
+                    const int p = base + 8 * j + 2 * t4 + c;
+                    if (g == 0 && p < p1 && in_bounds(p < a.max_pages, a.status)) {
+                        x *= s;
+                        // what is not finite leaves the decision to fp64; a page outside the
+                        // pool scores lowest
+                        if (!(fabsf(x) <= 3.402823466e38f)) odd = true;
+                        if (ok < 0 || ok >= a.n_pages) x = -INFINITY;
+                        const uint32_t at = first_key + p * 4;
+                        if (g0 == 0) st_cluster(at, ordered(x));
+                        else asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(at), "r"(ordered(x)) : "memory");
                     }
                 }
             }
-            __syncthreads();
-            prefix |= (uint32_t)s_bin << shift;
-            mask |= 255u << shift;
-            left = s_left;
         }
-        const float T = unordered(prefix);
+    }
+    // the largest scale bounds every page's error
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        scale_top = fmaxf(scale_top, __shfl_xor_sync(0xffffffffu, scale_top, o));
+        const float y = __shfl_xor_sync(0xffffffffu, mass, o);
+        mass = (y > mass || y != y) ? y : mass;
+    }
+    odd = __any_sync(0xffffffffu, odd);
+    if (lane == 0) wmin[0][warp] = odd ? 0x7f800000u : __float_as_uint(scale_top);
+    __syncthreads();
+    if (t == 0) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = max(top, wmin[0][w]);
+        st_cluster(in_first_cta((uint32_t)__cvta_generic_to_shared(&s_top[rank])), top);
+        if (rank == 0) s_near = 0;
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (rank != 0) return;
+
+    // ---- the cut, in the first CTA
+    uint32_t top = 0;
+    for (int r = 0; r < a.cluster; ++r) top = max(top, s_top[r]);
+    // |error| of a score: 2 QS + 2 <= 18 additions of partial sums, each off by at
+    // most 2^-22 of sum |q| * code, two fp32 products and q's 22 bits: below
+    // 2^-17 * sum |q| * largest code * scale
+    constexpr float kTop = FMT == ATTN_CACHE_E4M3 ? 448.f : 128.f;
+    const float eps = 0x1p-17f * kTop * mass * __uint_as_float(top);
+    float cut_lo = -INFINITY, cut_hi = INFINITY;  // decided above cut_hi: in; below cut_lo: out
+    if (k > 0 && eps <= 3.402823466e38f) {
+        // the k-th largest key: the largest v that at least k keys reach, by bisection;
+        // done as soon as exactly k do, v then being the smallest of them
+        uint32_t v = 0, most = 0xffffffffu;  // at least k keys >= v; fewer than k > most
+        int buf = 0;
+        while (v < most) {
+            const uint32_t mid = v + ((most - v) >> 1) + 1;
+            int n = 0;
+            uint32_t low = 0xffffffffu;
+            for (int p = t; p < m; p += kThreads) {
+                const uint32_t x = key[p];
+                if (x >= mid) {
+                    ++n;
+                    low = min(low, x);
+                }
+            }
+            n = __reduce_add_sync(0xffffffffu, n);
+            low = __reduce_min_sync(0xffffffffu, low);
+            if (lane == 0) {
+                wsum[buf][warp] = n;
+                wmin[buf][warp] = low;
+            }
+            __syncthreads();
+            n = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                n += wsum[buf][w];
+                low = min(low, wmin[buf][w]);
+            }
+            buf ^= 1;
+            if (n >= k) {
+                v = low;  // the smallest key that reaches mid
+                if (n == k) break;
+            } else {
+                most = mid - 1;
+            }
+        }
+        const float T = unordered(v);
         cut_lo = T - 2.f * eps;
         cut_hi = T + 2.f * eps;
         // a bound that rounds back to T would decide equal scores
@@ -274,37 +320,38 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Sele
         if (!(cut_hi > T)) cut_hi = T;
     }
     // pages above the cut are in, those near it are listed
-    int sure = 0;
-    for (int base = 0; base < m; base += kSelectThreads) {
-        const int p = base + t;
-        const float x = p < m ? unordered(key[p]) : 0.f;
-        const bool in = p < m && k > 0 && x > cut_hi;
-        const bool close = p < m && k > 0 && !in && !(x < cut_lo);
-        if (close) {
-            const int at = atomicAdd(&s_near, 1);
-            near[at] = p;
-        }
-        int n;
-        block_scan(in, wsum, &n);
-        sure += n;
-        __syncthreads();
-        if (p < m) key[p] = in ? 1 : 0;
+    int *near = reinterpret_cast<int *>(key + a.max_pages);
+    int n_in = 0;
+    for (int p = t; p < m; p += kThreads) {
+        const float x = unordered(key[p]);
+        const bool in = k > 0 && x > cut_hi;
+        if (k > 0 && !in && !(x < cut_lo)) near[atomicAdd(&s_near, 1)] = p;
+        key[p] = in ? 1 : 0;
+        n_in += in;
     }
+    n_in = __reduce_add_sync(0xffffffffu, n_in);
     __syncthreads();
+    if (lane == 0) wsum[0][warp] = n_in;
+    __syncthreads();
+    int sure = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sure += wsum[0][w];
     const int near_n = s_near, places = k - sure;
     if (near_n <= places) {
-        for (int j = t; j < near_n; j += kSelectThreads) key[near[j]] = 1;
+        for (int j = t; j < near_n; j += kThreads) key[near[j]] = 1;
     } else {
-        const int warp = t >> 5, lane = t & 31;
-        for (int j = warp; j < near_n; j += kSelectThreads / 32) {
-            const int phys = a.table[(int64_t)b * a.max_pages + near[j]];
+        double *exact = a.exact + unit * a.max_pages;
+#pragma unroll 1
+        for (int j = warp; j < near_n; j += kWarps) {
+            const int phys = table[near[j]];
             double best = -INFINITY;
             if (phys >= 0 && phys < a.n_pages) {
                 const int64_t ph = (int64_t)phys * a.Hkv + hk;
                 const uint8_t *lo = a.bounds + (size_t)ph * 2 * D, *hi = lo + D;
                 const double s = a.k_scale[ph];
-                for (int g = 0; g < a.G; ++g) {
-                    const size_t qi = (((size_t)b * a.Hkv * a.G + hk * a.G + g) * a.Sq + i) * D;
+#pragma unroll 1
+                for (int h = 0; h < a.G; ++h) {
+                    const size_t qi = (((size_t)b * a.Hkv * a.G + hk * a.G + h) * a.Sq + i) * D;
                     double x = 0.0;
                     for (int c = lane * 8; c < D; c += 256) {
                         float q8[8], l8[8], h8[8];
@@ -327,23 +374,23 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Sele
             if (lane == 0) exact[j] = best;
         }
         __syncthreads();
-        for (int j = t; j < near_n; j += kSelectThreads) {
+        for (int j = t; j < near_n; j += kThreads) {
             const double x = exact[j];
             const int p = near[j];
-            int rank = 0;
+            int place = 0;
             for (int o = 0; o < near_n; ++o)
-                rank += exact[o] > x || (exact[o] == x && near[o] < p);
-            if (rank < places) key[p] = 1;
+                place += exact[o] > x || (exact[o] == x && near[o] < p);
+            if (place < places) key[p] = 1;
         }
     }
     __syncthreads();
     // ascending order; the last visible page closes the list
     int done = 0;
-    for (int base = 0; base < m; base += kSelectThreads) {
+    for (int base = 0; base < m; base += kThreads) {
         const int p = base + t;
         const int in = p < m ? (int)key[p] : 0;
         int n;
-        const int at = done + block_scan(in, wsum, &n);
+        const int at = done + block_scan(in, wsum[0], &n);
         if (in && in_bounds(at < k, a.status)) out[at] = p;
         done += n;
     }
@@ -351,37 +398,34 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Sele
 }
 
 template <int D, int FMT, int DT>
-int launch_select_t(const SelectArgs &a, cudaStream_t stream) {
+int launch_select_t(SelectArgs &a, int sms, cudaStream_t stream) {
     const int64_t units = (int64_t)a.B * a.Hkv * a.Sq;
-    const int chunks = (a.max_pages + kScorePages - 1) / kScorePages;
-    auto score = cache_score_kernel<D, FMT, DT>;
-    auto select = cache_select_kernel<D, FMT, DT>;
-    const int smem1 = 2 * a.G * D * 4;
-    const int smem2 = a.max_pages * 8;
-    if (!set_smem_limit_once(reinterpret_cast<const void *>(score), 2 * kMaxSelectGroup * D * 4) ||
-        !set_smem_limit_once(reinterpret_cast<const void *>(select), kMaxSelectPages * 8))
-        return ATTN_ERR_LAUNCH;
-    score<<<dim3((unsigned)units, (unsigned)chunks), kScoreThreads, smem1, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
+    // CTAs per unit: up to eight while they fit the GPU at two an SM and have 64 pages each
+    a.cluster = 1;
+    while (a.cluster < kMaxCluster && units * a.cluster * 2 <= 2 * sms && a.cluster * 2 * 64 <= a.max_pages)
+        a.cluster *= 2;
+    auto kern = cache_select_kernel<D, FMT, DT>;
+    if (!set_smem_limit_once(reinterpret_cast<const void *>(kern), kMaxSelectPages * 8)) return ATTN_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)units);
-    cfg.blockDim = dim3(kSelectThreads);
-    cfg.dynamicSmemBytes = (size_t)smem2;
+    cfg.gridDim = dim3((unsigned)(units * a.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)a.max_pages * 8;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, select, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, (const SelectArgs)a);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 template <int D, int FMT>
-int launch_select_q(const SelectArgs &a, int dtype, cudaStream_t stream) {
-    if (dtype == ATTN_F32) return launch_select_t<D, FMT, 0>(a, stream);
-    if (dtype == ATTN_BF16 || dtype == ATTN_BF16_OUT_F32) return launch_select_t<D, FMT, 1>(a, stream);
-    return launch_select_t<D, FMT, 2>(a, stream);
+int launch_select_q(SelectArgs &a, int dtype, int sms, cudaStream_t stream) {
+    if (dtype == ATTN_F32) return launch_select_t<D, FMT, 0>(a, sms, stream);
+    if (dtype == ATTN_BF16 || dtype == ATTN_BF16_OUT_F32) return launch_select_t<D, FMT, 1>(a, sms, stream);
+    return launch_select_t<D, FMT, 2>(a, sms, stream);
 }
 
 }  // namespace
@@ -390,18 +434,17 @@ int launch_cache_select(const attn_cache &c, const void *q, const int32_t *table
                         const int32_t *lens, const int32_t *counts, int32_t *pages, int n_select,
                         int B, int H, int Sq, int causal, int dtype, void *workspace,
                         cudaStream_t stream) {
-    const int64_t units = (int64_t)B * c.H_kv * Sq;
-    double *exact = reinterpret_cast<double *>(workspace);
-    float *scores = reinterpret_cast<float *>(exact + units * max_pages);
-    SelectArgs a = {q, (const uint8_t *)c.k_bounds, c.k_scale, table, lens, counts, pages, scores,
-                    scores + units * max_pages, exact, B, c.H_kv, H / c.H_kv, Sq, c.page, c.n_pages,
-                    max_pages, n_select, causal, status_word_device_ptr()};
+    SelectArgs a = {q, (const uint8_t *)c.k_bounds, c.k_scale, table, lens, counts, pages,
+                    reinterpret_cast<double *>(workspace), B, c.H_kv, H / c.H_kv, Sq, c.page,
+                    c.n_pages, max_pages, n_select, causal, 1, status_word_device_ptr()};
     if (!a.status) return ATTN_ERR_CUDA;
+    const int sms = device_sm_count();
+    if (sms <= 0) return ATTN_ERR_CUDA;
     if (c.d == 64)
-        return c.format == ATTN_CACHE_E4M3 ? launch_select_q<64, ATTN_CACHE_E4M3>(a, dtype, stream)
-                                           : launch_select_q<64, ATTN_CACHE_I8>(a, dtype, stream);
-    return c.format == ATTN_CACHE_E4M3 ? launch_select_q<128, ATTN_CACHE_E4M3>(a, dtype, stream)
-                                       : launch_select_q<128, ATTN_CACHE_I8>(a, dtype, stream);
+        return c.format == ATTN_CACHE_E4M3 ? launch_select_q<64, ATTN_CACHE_E4M3>(a, dtype, sms, stream)
+                                           : launch_select_q<64, ATTN_CACHE_I8>(a, dtype, sms, stream);
+    return c.format == ATTN_CACHE_E4M3 ? launch_select_q<128, ATTN_CACHE_E4M3>(a, dtype, sms, stream)
+                                       : launch_select_q<128, ATTN_CACHE_I8>(a, dtype, sms, stream);
 }
 
 }  // namespace attn
