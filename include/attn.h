@@ -360,7 +360,7 @@ ATTN_API int attn_cache_read(const attn_cache *cache, const int32_t *table, int 
  *          at most 128 query heads per kv head
  *   pages  [B][H_kv][Sq][n_select] int32: page indices within the sequence (0
  *          its first page), ascending, then -1 where fewer are visible
- *   causal, counts as attn_fwd_cache;  max_pages and n_select <= 28672
+ *   causal, counts as attn_fwd_cache;  max_pages and n_select <= 27648
  *   workspace  16-byte aligned scratch of attn_cache_select_workspace_size
  *          bytes, not overlapping any other argument
  *   B * H_kv * Sq < 2^28
@@ -387,7 +387,7 @@ ATTN_API int attn_cache_select(const attn_cache *cache, const void *q, const int
  *   causal key j is visible to query i iff j <= lens[b] - counts[b] + i (else
  *          every held token is); a row that sees no key gets o = 0, lse = -inf
  *   pages  NULL: all pages (n_select = 0).  Else [B][H_kv][Sq][n_select] with
- *          n_select <= 28672: query
+ *          n_select <= 27648: query
  *          i of kv head h attends only to tokens of the listed pages (page
  *          indices within the sequence, as attn_cache_select gives them; -1 is
  *          skipped; a page listed twice counts twice).

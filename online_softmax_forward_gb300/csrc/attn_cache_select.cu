@@ -36,7 +36,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kGroups = 4;  // groups of eight pages a warp loads at once
+constexpr int kBins = 1024;
+constexpr int kGroups = 2;  // groups of eight pages a warp loads at once
 
 struct SelectArgs {
     const void *q;  // [B][Hkv * G][Sq][d]
@@ -91,15 +92,56 @@ __device__ __forceinline__ int block_scan(int x, int *warps, int *total) {
     return before + __popc(m & ((1u << lane) - 1));
 }
 
-// One cluster per (b, hk, i).  Dynamic shared memory: keys [max_pages], then
+// Exact score of a page, in fp64: eight lanes per head, four heads at a time.
+template <int D, int FMT, int DT>
+__device__ double exact_score(const SelectArgs &a, int b, int hk, int i, int phys) {
+    const int lane = threadIdx.x & 31, sub = lane >> 3, c0 = (lane & 7) * (D / 8);
+    double best = -INFINITY;
+    if (phys < 0 || phys >= a.n_pages) return best;
+    const int64_t ph = (int64_t)phys * a.Hkv + hk;
+    const uint8_t *lo = a.bounds + (size_t)ph * 2 * D + c0, *hi = lo + D;
+#pragma unroll 1
+    for (int h0 = 0; h0 < a.G; h0 += 4) {
+        const int h = min(h0 + sub, a.G - 1);  // a head twice changes no maximum
+        const size_t qi = (((size_t)b * a.Hkv * a.G + hk * a.G + h) * a.Sq + i) * D + c0;
+        double x[4] = {};
+#pragma unroll
+        for (int c = 0; c < D / 8; c += 8) {
+            float q8[8], l8[8], h8[8];
+            codec::load8<DT>(a.q, qi + c, q8);
+            const uint2 lw = *reinterpret_cast<const uint2 *>(lo + c);
+            const uint2 hw = *reinterpret_cast<const uint2 *>(hi + c);
+            codec::decode4<FMT>(lw.x, l8); codec::decode4<FMT>(lw.y, l8 + 4);
+            codec::decode4<FMT>(hw.x, h8); codec::decode4<FMT>(hw.y, h8 + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e & 3] = fma((double)q8[e], (double)(q8[e] < 0.f ? l8[e] : h8[e]), x[e & 3]);
+        }
+        double y = (x[0] + x[1]) + (x[2] + x[3]);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        best = (y > best || y != y) ? y : best;
+    }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+        const double y = __shfl_xor_sync(0xffffffffu, best, o);
+        best = (y > best || y != y) ? y : best;
+    }
+    best *= a.k_scale[ph];
+    return best != best ? INFINITY : best;  // a NaN is attended to, so that it shows
+}
+
+// One cluster per (b, hk, i).  Dynamic shared memory: scores [max_pages], then
 // the list of pages near the cut [max_pages].
 template <int D, int FMT, int DT>
-__global__ void __launch_bounds__(kThreads) cache_select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectArgs a) {
     using U = Unpack<FMT>;
     constexpr int QS = D / 16;
-    extern __shared__ __align__(16) uint32_t key[];
-    __shared__ int wsum[2][kWarps], s_near;
-    __shared__ uint32_t wmin[2][kWarps], s_top[kMaxCluster];
+    extern __shared__ __align__(16) uint32_t key[];  // ordered scores, later 1 for a page that is in
+    __shared__ int wsum[kWarps], s_near, s_in, s_open, s_bin;
+    __shared__ int hist[kBins];
+    // largest scale (infinity: leave it to fp64), largest and smallest score, by warp and by CTA
+    __shared__ uint32_t w_top[3][kWarps], s_top[3][kMaxCluster];
     const int64_t unit = blockIdx.x / a.cluster;
     const int rank = (int)(blockIdx.x - unit * a.cluster);
     const int i = (int)(unit % a.Sq);
@@ -126,7 +168,10 @@ __global__ void __launch_bounds__(kThreads) cache_select_kernel(const SelectArgs
     const int slice = ((m + a.cluster - 1) / a.cluster + 7) / 8 * 8;
     const int p0 = rank * slice, p1 = min(m, p0 + slice);
     const uint32_t first_key = in_first_cta((uint32_t)__cvta_generic_to_shared(key));
+    for (int h = t; h < kBins; h += kThreads) hist[h] = 0;
+    if (t == 0) s_near = s_in = s_open = 0;
     float mass = 0.f, scale_top = 0.f;
+    uint32_t high = 0, low = 0xffffffffu;
     bool odd = false;
     for (int g0 = 0; g0 < a.G; g0 += 8) {
         // rows: heads g0 + g.  k steps 0 .. QS - 1 hold the positive parts of channels
@@ -236,8 +281,9 @@ __global__ void __launch_bounds__(kThreads) cache_select_kernel(const SelectArgs
                         // what is not finite leaves the decision to fp64; a page outside the
                         // pool scores lowest
                         if (!(fabsf(x) <= 3.402823466e38f)) odd = true;
+                        const uint32_t at = first_key + p * 4, y = ordered(x);
                         if (ok < 0 || ok >= a.n_pages) x = -INFINITY;
-                        const uint32_t at = first_key + p * 4;
+                        else high = max(high, y), low = min(low, y);
                         if (g0 == 0) st_cluster(at, ordered(x));
                         else asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(at), "r"(ordered(x)) : "memory");
                     }
@@ -253,14 +299,19 @@ __global__ void __launch_bounds__(kThreads) cache_select_kernel(const SelectArgs
         mass = (y > mass || y != y) ? y : mass;
     }
     odd = __any_sync(0xffffffffu, odd);
-    if (lane == 0) wmin[0][warp] = odd ? 0x7f800000u : __float_as_uint(scale_top);
+    high = __reduce_max_sync(0xffffffffu, high);
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) {
+        w_top[0][warp] = odd ? 0x7f800000u : __float_as_uint(scale_top);
+        w_top[1][warp] = high;
+        w_top[2][warp] = low;
+    }
     __syncthreads();
-    if (t == 0) {
-        uint32_t top = 0;
+    if (t < 3) {
+        uint32_t x = w_top[t][0];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = max(top, wmin[0][w]);
-        st_cluster(in_first_cta((uint32_t)__cvta_generic_to_shared(&s_top[rank])), top);
-        if (rank == 0) s_near = 0;
+        for (int w = 1; w < kWarps; ++w) x = t < 2 ? max(x, w_top[t][w]) : min(x, w_top[t][w]);
+        st_cluster(in_first_cta((uint32_t)__cvta_generic_to_shared(&s_top[t][rank])), x);
     }
     cluster_arrive();
     cluster_wait();
@@ -268,119 +319,117 @@ __global__ void __launch_bounds__(kThreads) cache_select_kernel(const SelectArgs
 
     // ---- the cut, in the first CTA
     uint32_t top = 0;
-    for (int r = 0; r < a.cluster; ++r) top = max(top, s_top[r]);
-    // |error| of a score: 2 QS + 2 <= 18 additions of partial sums, each off by at
-    // most 2^-22 of sum |q| * code, two fp32 products and q's 22 bits: below
-    // 2^-17 * sum |q| * largest code * scale
+    for (int r = 0; r < a.cluster; ++r) {
+        top = max(top, s_top[0][r]);
+        high = max(high, s_top[1][r]);
+        low = min(low, s_top[2][r]);
+    }
+    // |error| of a score: 2 QS <= 16 sums of 16 products and 3 of sums, each off by at
+    // most 2^-22 of what sum |q| * code has reached, two fp32 products and q's 22
+    // bits: below 2^-18 * sum |q| * largest code * scale
     constexpr float kTop = FMT == ATTN_CACHE_E4M3 ? 448.f : 128.f;
-    const float eps = 0x1p-17f * kTop * mass * __uint_as_float(top);
-    float cut_lo = -INFINITY, cut_hi = INFINITY;  // decided above cut_hi: in; below cut_lo: out
-    if (k > 0 && eps <= 3.402823466e38f) {
-        // the k-th largest key: the largest v that at least k keys reach, by bisection;
-        // done as soon as exactly k do, v then being the smallest of them
-        uint32_t v = 0, most = 0xffffffffu;  // at least k keys >= v; fewer than k > most
-        int buf = 0;
-        while (v < most) {
-            const uint32_t mid = v + ((most - v) >> 1) + 1;
-            int n = 0;
-            uint32_t low = 0xffffffffu;
-            for (int p = t; p < m; p += kThreads) {
-                const uint32_t x = key[p];
-                if (x >= mid) {
-                    ++n;
-                    low = min(low, x);
-                }
-            }
-            n = __reduce_add_sync(0xffffffffu, n);
-            low = __reduce_min_sync(0xffffffffu, low);
-            if (lane == 0) {
-                wsum[buf][warp] = n;
-                wmin[buf][warp] = low;
-            }
-            __syncthreads();
-            n = 0;
+    const float eps = 2.f * 0x1p-18f * kTop * mass * __uint_as_float(top);  // of a difference
+    const float least = unordered(low), per_bin = kBins / (unordered(high) - least);
+    // pages whose score may be that of the last place: every one, or those of the
+    // n-th score's bin and of the bins within eps of it
+    int bin_lo = 0, bin_hi = kBins - 1;
+    const bool binned = k > 0 && eps <= 1e37f && per_bin > 0.f && per_bin <= 1e37f;
+    // not decreasing with the score
+    auto bin_of = [&](float x) { return (int)fminf(fmaxf((x - least) * per_bin, 0.f), kBins - 1.f); };
+    if (binned) {
+        for (int p = t; p < m; p += kThreads) atomicAdd(&hist[bin_of(unordered(key[p]))], 1);
+        __syncthreads();
+        // thread t: bins kBins - 1 - 4 t down
+        int c[4], sum = 0;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                n += wsum[buf][w];
-                low = min(low, wmin[buf][w]);
-            }
-            buf ^= 1;
-            if (n >= k) {
-                v = low;  // the smallest key that reaches mid
-                if (n == k) break;
-            } else {
-                most = mid - 1;
+        for (int e = 0; e < 4; ++e) sum += c[e] = hist[kBins - 1 - 4 * t - e];
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) incl += w < warp ? wsum[w] : 0;
+        int above = incl - sum;
+        if (above < k && k <= incl) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (above < k && k <= above + c[e]) s_bin = kBins - 1 - 4 * t - e;
+                above += c[e];
             }
         }
-        const float T = unordered(v);
-        cut_lo = T - 2.f * eps;
-        cut_hi = T + 2.f * eps;
-        // a bound that rounds back to T would decide equal scores
-        if (!(cut_lo < T)) cut_lo = T;
-        if (!(cut_hi > T)) cut_hi = T;
+        __syncthreads();
+        const int bin = s_bin;
+        // one bin for the place in the bin, one for the rounding of (x - least) * per_bin
+        const float reach = eps * per_bin + 2.f;
+        bin_lo = (int)fmaxf(bin - reach, 0.f);
+        bin_hi = (int)fminf(bin + reach, kBins - 1.f);
     }
-    // pages above the cut are in, those near it are listed
+    static_assert(kBins == 4 * kThreads, "four bins a thread");
     int *near = reinterpret_cast<int *>(key + a.max_pages);
+    const bool equal = eps == 0.f;  // q or every scale is 0: all scores are
     int n_in = 0;
     for (int p = t; p < m; p += kThreads) {
-        const float x = unordered(key[p]);
-        const bool in = k > 0 && x > cut_hi;
-        if (k > 0 && !in && !(x < cut_lo)) near[atomicAdd(&s_near, 1)] = p;
-        key[p] = in ? 1 : 0;
+        const int bin = binned ? bin_of(unordered(key[p])) : bin_lo;
+        const bool in = equal ? p < k : bin > bin_hi && k > 0;
+        if (!in && !equal && k > 0 && bin >= bin_lo) near[atomicAdd(&s_near, 1)] = p;
+        else key[p] = in ? 1 : 0;
         n_in += in;
     }
     n_in = __reduce_add_sync(0xffffffffu, n_in);
+    if (lane == 0) atomicAdd(&s_in, n_in);
     __syncthreads();
-    if (lane == 0) wsum[0][warp] = n_in;
+    const int near_n = s_near, places = k - s_in;
+    // settle the near ones among themselves: `sure` beat a page whatever the errors,
+    // `may` might
+    double *exact = a.exact + unit * a.max_pages;
+    int settled = 0;
+    for (int base = 0; base < near_n; base += kThreads) {
+        const int j = base + t;
+        int sure = 0, may = 0;
+        if (j < near_n) {
+            const float x = unordered(key[near[j]]);
+            for (int o = 0; o < near_n; ++o) {
+                const float y = unordered(key[near[o]]);
+                sure += y > x + eps;
+                may += !(y < x - eps);  // itself among them
+            }
+        }
+        // 1: in, 0: out, 2: open.  The scores are still read by others: kept aside
+        const int fate = may - 1 < places ? 1 : (sure >= places ? 0 : 2);
+        if (j < near_n) exact[j] = fate;
+        settled += j < near_n && fate == 1;
+        if (j < near_n && fate == 2) s_open = 1;
+    }
+    settled = __reduce_add_sync(0xffffffffu, settled);
     __syncthreads();
-    int sure = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sure += wsum[0][w];
-    const int near_n = s_near, places = k - sure;
-    if (near_n <= places) {
-        for (int j = t; j < near_n; j += kThreads) key[near[j]] = 1;
-    } else {
-        double *exact = a.exact + unit * a.max_pages;
+    if (lane == 0) atomicAdd(&s_in, settled);
+    for (int j = t; j < near_n; j += kThreads) key[near[j]] = (uint32_t)exact[j];
+    __syncthreads();
+    if (s_open) {
+        const int left = k - s_in;
 #pragma unroll 1
         for (int j = warp; j < near_n; j += kWarps) {
-            const int phys = table[near[j]];
-            double best = -INFINITY;
-            if (phys >= 0 && phys < a.n_pages) {
-                const int64_t ph = (int64_t)phys * a.Hkv + hk;
-                const uint8_t *lo = a.bounds + (size_t)ph * 2 * D, *hi = lo + D;
-                const double s = a.k_scale[ph];
-#pragma unroll 1
-                for (int h = 0; h < a.G; ++h) {
-                    const size_t qi = (((size_t)b * a.Hkv * a.G + hk * a.G + h) * a.Sq + i) * D;
-                    double x = 0.0;
-                    for (int c = lane * 8; c < D; c += 256) {
-                        float q8[8], l8[8], h8[8];
-                        codec::load8<DT>(a.q, qi + c, q8);
-                        const uint2 lw = *reinterpret_cast<const uint2 *>(lo + c);
-                        const uint2 hw = *reinterpret_cast<const uint2 *>(hi + c);
-                        codec::decode4<FMT>(lw.x, l8); codec::decode4<FMT>(lw.y, l8 + 4);
-                        codec::decode4<FMT>(hw.x, h8); codec::decode4<FMT>(hw.y, h8 + 4);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            x = fma((double)q8[e], (double)(q8[e] < 0.f ? l8[e] : h8[e]), x);
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                    best = (x > best || x != x) ? x : best;
-                }
-                best *= s;
-                if (best != best) best = INFINITY;  // a NaN is attended to, so that it shows
-            }
-            if (lane == 0) exact[j] = best;
+            const int p = near[j];
+            if (key[p] != 2) continue;  // the same for the whole warp
+            const double x = exact_score<D, FMT, DT>(a, b, hk, i, table[p]);
+            if (lane == 0) exact[j] = x;
         }
         __syncthreads();
-        for (int j = t; j < near_n; j += kThreads) {
-            const double x = exact[j];
-            const int p = near[j];
-            int place = 0;
-            for (int o = 0; o < near_n; ++o)
-                place += exact[o] > x || (exact[o] == x && near[o] < p);
-            if (place < places) key[p] = 1;
+        for (int base = 0; base < near_n; base += kThreads) {
+            const int j = base + t;
+            bool in = false;
+            if (j < near_n && (key[near[j]] & 2)) {
+                const double x = exact[j];
+                int place = 0;
+                for (int o = 0; o < near_n; ++o)
+                    if (key[near[o]] & 2) place += exact[o] > x || (exact[o] == x && near[o] < near[j]);
+                in = place < left;
+            }
+            if (in) key[near[j]] = 3;
         }
     }
     __syncthreads();
@@ -388,9 +437,9 @@ __global__ void __launch_bounds__(kThreads) cache_select_kernel(const SelectArgs
     int done = 0;
     for (int base = 0; base < m; base += kThreads) {
         const int p = base + t;
-        const int in = p < m ? (int)key[p] : 0;
+        const int in = p < m ? (int)(key[p] & 1) : 0;
         int n;
-        const int at = done + block_scan(in, wsum[0], &n);
+        const int at = done + block_scan(in, wsum, &n);
         if (in && in_bounds(at < k, a.status)) out[at] = p;
         done += n;
     }

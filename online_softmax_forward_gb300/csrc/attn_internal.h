@@ -93,7 +93,7 @@ void forget_noalloc_scratch(int dev);  // attn_shutdown: look the address up aga
 
 // Paged 8-bit cache (attn_cache.cu, attn_cache_select.cu, attn_cache_fwd.cu).
 constexpr int kMaxCacheBatch = 4096;       // sequences of one attention call
-constexpr int kMaxSelectPages = 28672;     // table width attn_cache_select takes, and n_select
+constexpr int kMaxSelectPages = 27648;     // table width attn_cache_select takes, and n_select
 constexpr int kMaxSelectGroup = 128;       // query heads per kv head it takes
 constexpr int kCacheMaxCtas = 160;         // CTAs of the attention kernel at most (one per SM)
 // in the input and output type: 0 fp32, 1 bf16, 2 fp16

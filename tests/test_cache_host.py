@@ -214,12 +214,12 @@ def test_bad_caches_are_refused(lib, name, kw):
     ("read", dict(v=NV + 4)), ("read", dict(v=NK + 64)), ("read", dict(k=K)), ("read", dict(v=KS)),
     ("read", dict(k=TABLE)), ("read", dict(lens=None)), ("read", dict(max_pages=-3)),
     ("select", dict(q=None)), ("select", dict(q=Q + 8)), ("select", dict(n=0)), ("select", dict(n=-2)),
-    ("select", dict(n=28673)), ("attend", dict(pages=PAGES, n=28673)),
+    ("select", dict(n=27649)), ("attend", dict(pages=PAGES, n=27649)),
     ("select", dict(H=3)), ("select", dict(H=0)), ("select", dict(H=2 * 129)), ("select", dict(Sq=-1)),
     ("select", dict(causal=2)), ("select", dict(dtype=5)), ("select", dict(pages=None)),
     ("select", dict(pages=PAGES + 2)), ("select", dict(pages=Q)), ("select", dict(ws=None)),
     ("select", dict(ws=WS + 8)), ("select", dict(bytes=2 * 2 * 8 * 4 - 1)), ("select", dict(ws=K)),
-    ("select", dict(ws=PAGES)), ("select", dict(max_pages=28673)), ("select", dict(lens=None)),
+    ("select", dict(ws=PAGES)), ("select", dict(max_pages=27649)), ("select", dict(lens=None)),
     ("attend", dict(q=None)), ("attend", dict(o=None)), ("attend", dict(o=O + 8)), ("attend", dict(lse=L + 2)),
     ("attend", dict(H=5)), ("attend", dict(H=-2)), ("attend", dict(max_pages=1 << 30)), ("attend", dict(Sq=-1)), ("attend", dict(B=4097)),
     ("attend", dict(causal=3)), ("attend", dict(scale=float("nan"))), ("attend", dict(scale=float("inf"))),
@@ -249,7 +249,7 @@ def test_empty_calls_do_nothing(lib, name, kw):
 def test_workspace_sizes(lib):
     assert pkg.attn_cache_select_workspace_size(2, 3, 4, 10) == (pkg.ATTN_OK, 24 * 80)
     assert pkg.attn_cache_select_workspace_size(0, 3, 4, 10) == (pkg.ATTN_OK, 0)
-    for bad in ((-1, 1, 1, 1), (1, 0, 1, 1), (1, 1, -1, 1), (1, 1, 1, 0), (1, 1, 1, 28673)):
+    for bad in ((-1, 1, 1, 1), (1, 0, 1, 1), (1, 1, -1, 1), (1, 1, 1, 0), (1, 1, 1, 27649)):
         assert pkg.attn_cache_select_workspace_size(*bad)[0] == pkg.ATTN_ERR_INVALID_ARG
     for args in ((1, 8, 8, 1, 128, 1), (64, 32, 8, 5, 64, 0), (1, 32, 1, 1, 128, 1, 7)):
         st, n = pkg.attn_fwd_cache_workspace_size(*args)
