@@ -10,9 +10,10 @@
 //     s  = max(s_old if the block holds older rows, pow2 scale of amax |x|)
 //     codes of x = rn(x / s);  older codes = rn(code * s_old / s) when s grew
 //     bounds = min / max (older bounds rounded the same way, codes of x)
-// Rounding is monotone, so the bounds are exactly the smallest and largest
-// code without reading the older rows again.  Older rows are read only when
-// the scale grows.
+// Rounding is monotone, so the bounds are the codes of the smallest and largest
+// x of each channel, and no older row is read again for them.  Older rows are
+// read only when the scale grows.  The new rows are read once: they wait in
+// registers, as they lie in memory, until the block's scale is known.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -26,20 +27,6 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 
-// Maximum over the block (NaN wins); every thread gets it.
-__device__ __forceinline__ float block_max_nan(float x, float *red) {
-    // magnitudes as integers: x >= 0 or NaN, and a NaN's bits exceed infinity's
-    uint32_t u = __float_as_uint(x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, o));
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) red[warp] = __uint_as_float(u);
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) u = max(u, __float_as_uint(red[w]));
-    return __uint_as_float(u);
-}
-
 struct AppendArgs {
     const void *x[2];   // new keys, values [B][Hkv][S][d]
     uint8_t *codes[2];  // [n_pages][Hkv][page][d]
@@ -51,12 +38,15 @@ struct AppendArgs {
 };
 
 // One CTA per (touched page of a sequence, kv head, keys or values).
-template <int D, int FMT, int DT>
+// MOST: rows of the largest page that it takes, 64 or 128 (registers hold them).
+template <int D, int FMT, int DT, int MOST>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
-    constexpr int G = D / 8;                      // 8-element groups per row
-    constexpr int RL = kAppendThreads / G;        // rows in parallel
-    __shared__ float red[kAppendThreads / 32];
-    __shared__ float edge[2][RL][D];
+    constexpr int G = D / 8;               // 8-channel groups of a row: one per thread
+    constexpr int RL = kAppendThreads / G; // rows at a time
+    constexpr int N = MOST / RL;
+    constexpr int kW = kAppendThreads / 32;
+    __shared__ float red[kW];
+    __shared__ float edge[2][kW][D];       // smallest and largest by warp
     int64_t blk = blockIdx.x;
     const int which = (int)(blk & 1);
     blk >>= 1;
@@ -74,65 +64,80 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
     const int64_t lp = pos / a.page + tp;           // logical page
     const int64_t first = lp * a.page;              // its first position
     if (first >= end) return;
+    const int r0 = pos > first ? (int)(pos - first) : 0;                  // first new row
+    const int r1 = end - first < a.page ? (int)(end - first) : a.page;    // past the last
+    const void *xs = which ? a.x[1] : a.x[0];
+    const int g = threadIdx.x % G, rl = threadIdx.x / G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // row r of the page is row first + r - pos of x
+    const size_t src = (((size_t)b * a.Hkv + hk) * a.S) * D + g * 8;
+    const int64_t shift = first - pos;
+
+    // the rows are asked for before the page that they go to
+    codec::Raw8<DT> raw[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int r = rl + n * RL;
+        const size_t i = src + (size_t)(shift + r) * D;
+        if (r >= r0 && r < r1 && in_bounds(i + 8 <= (size_t)a.B * a.Hkv * a.S * D, a.status))
+            raw[n].load(xs, i);
+    }
     const int phys = lp < a.max_pages ? a.table[(int64_t)b * a.max_pages + lp] : -1;
     if (phys < 0 || phys >= a.n_pages) {  // the rows have no page: skipped and reported
         if (threadIdx.x == 0) atomicOr(a.status, kStatusTable);
         return;
     }
-    const int r0 = pos > first ? (int)(pos - first) : 0;                  // first new row
-    const int r1 = end - first < a.page ? (int)(end - first) : a.page;    // past the last
     const int64_t ph = (int64_t)phys * a.Hkv + hk;
     uint8_t *codes = (which ? a.codes[1] : a.codes[0]) + ph * a.page * D;
     float *scale = (which ? a.scale[1] : a.scale[0]) + ph;
-    const void *xs = which ? a.x[1] : a.x[0];
     const float before = r0 > 0 ? *scale : 0.f;
-    // source row of page row r: s = first + r - pos
-    const size_t src = (((size_t)b * a.Hkv + hk) * a.S) * D;
-    const int64_t shift = first - pos;
-    const int g = threadIdx.x % G, rl = threadIdx.x / G;
-
-    float amax = 0.f;
-    for (int r = r0 + rl; r < r1; r += RL) {
-        float f[8];
-        const size_t i = src + (size_t)(shift + r) * D + g * 8;
-        if (!in_bounds(i + 8 <= (size_t)a.B * a.Hkv * a.S * D, a.status)) continue;
-        codec::load8<DT>(xs, i, f);
+    codec::Range8<DT> range;
+    range.clear();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t u = __float_as_uint(f[e]) & 0x7fffffffu;
-            amax = __uint_as_float(max(u, __float_as_uint(amax)));
+    for (int n = 0; n < N; ++n) {
+        const int r = rl + n * RL;
+        if (r >= r0 && r < r1) range.add(raw[n]);
+    }
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1) range.join(o);  // the warp's rows
+    float lo[8], hi[8];
+    codec::Range8<DT>::widen(range.lo, lo);
+    codec::Range8<DT>::widen(range.hi, hi);
+    // magnitudes compared as integers: a NaN's bits exceed infinity's.  A warp without
+    // a row holds (inf, -inf) and counts as 0
+    uint32_t amax = 0;
+    if (!(lo[0] == INFINITY && hi[0] == -INFINITY)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            amax = max(amax, max(__float_as_uint(lo[e]) & 0x7fffffffu, __float_as_uint(hi[e]) & 0x7fffffffu));
+    }
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if (lane == 0) red[warp] = __uint_as_float(amax);
+    if (which == 0 && a.bounds && lane < G) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            *reinterpret_cast<float4 *>(&edge[0][warp][g * 8 + e]) = make_float4(lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
+            *reinterpret_cast<float4 *>(&edge[1][warp][g * 8 + e]) = make_float4(hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
         }
     }
-    amax = block_max_nan(amax, red);
-    const float mine = codec::scale_for<FMT>(amax);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kW; ++w) amax = max(amax, __float_as_uint(red[w]));
+    const float mine = codec::scale_for<FMT>(__uint_as_float(amax));
     const float now = (before != before || mine != mine) ? __int_as_float(0x7fc00000)
                                                          : fmaxf(before, mine);
     const float inv = codec::inverse_scale(now);
-
-    float lo[8], hi[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        lo[e] = INFINITY;
-        hi[e] = -INFINITY;
-    }
-    for (int r = r0 + rl; r < r1; r += RL) {
+    for (int n = 0; n < N; ++n) {
+        const int r = rl + n * RL;
+        if (r < r0 || r >= r1) continue;
         float f[8];
-        const size_t i = src + (size_t)(shift + r) * D + g * 8;
-        if (!in_bounds(i + 8 <= (size_t)a.B * a.Hkv * a.S * D, a.status)) continue;
-        codec::load8<DT>(xs, i, f);
+        raw[n].widen(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = inv > 0.f ? f[e] * inv : 0.f;
         uint2 c;
         c.x = codec::encode4<FMT>(f[0], f[1], f[2], f[3]);
         c.y = codec::encode4<FMT>(f[4], f[5], f[6], f[7]);
         *reinterpret_cast<uint2 *>(codes + (size_t)r * D + g * 8) = c;
-        codec::decode4<FMT>(c.x, f);
-        codec::decode4<FMT>(c.y, f + 4);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            lo[e] = fminf(lo[e], f[e]);
-            hi[e] = fmaxf(hi[e], f[e]);
-        }
     }
     const bool grew = r0 > 0 && !(now == before);  // also when the block turned NaN
     const float ratio = now > 0.f ? before * inv : 0.f;
@@ -151,35 +156,29 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
         }
     }
     if (threadIdx.x == 0) *scale = now;
-    if (which == 1 || !a.bounds) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        edge[0][rl][g * 8 + e] = lo[e];
-        edge[1][rl][g * 8 + e] = hi[e];
-    }
-    __syncthreads();
     // thread t: side t / (D / 4), four channels
-    if (threadIdx.x < 2 * (D / 4)) {
+    if (which == 0 && a.bounds && threadIdx.x < 2 * (D / 4)) {
         const int side = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
         uint32_t *p = reinterpret_cast<uint32_t *>(a.bounds + ((size_t)ph * 2 + side) * D) + c4;
         float f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float x = edge[side][0][c4 * 4 + e];
-            for (int w = 1; w < RL; ++w) {
+#pragma unroll
+            for (int w = 1; w < kW; ++w) {
                 const float y = edge[side][w][c4 * 4 + e];
                 x = side ? fmaxf(x, y) : fminf(x, y);
             }
-            f[e] = x;
+            f[e] = inv > 0.f ? x * inv : 0.f;
         }
         if (r0 > 0) {
             float o[4];
             codec::decode4<FMT>(*p, o);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = grew ? (ratio > 0.f ? o[e] * ratio : 0.f) : o[e];
-            codec::decode4<FMT>(codec::encode4<FMT>(o[0], o[1], o[2], o[3]), o);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = side ? fmaxf(f[e], o[e]) : fminf(f[e], o[e]);
+            for (int e = 0; e < 4; ++e) {
+                if (grew) o[e] = ratio > 0.f ? o[e] * ratio : 0.f;
+                f[e] = side ? fmaxf(f[e], o[e]) : fminf(f[e], o[e]);
+            }
         }
         *p = codec::encode4<FMT>(f[0], f[1], f[2], f[3]);
     }
@@ -283,7 +282,8 @@ int dispatch(int d, int format, int dt, A... args) {
 template <int D, int FMT, int DT>
 struct RunAppend {
     static int run(const AppendArgs *a, unsigned grid, cudaStream_t s) {
-        cache_append_kernel<D, FMT, DT><<<grid, kAppendThreads, 0, s>>>(*a);
+        if (a->page <= 64) cache_append_kernel<D, FMT, DT, 64><<<grid, kAppendThreads, 0, s>>>(*a);
+        else cache_append_kernel<D, FMT, DT, 128><<<grid, kAppendThreads, 0, s>>>(*a);
         return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
     }
 };

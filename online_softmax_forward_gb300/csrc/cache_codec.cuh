@@ -12,6 +12,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "attn.h"
 
@@ -67,20 +68,26 @@ __device__ __forceinline__ void decode4(uint32_t w, float *f) {
     }
 }
 
-// Eight consecutive values of the type `dtype` (0 fp32, 1 bf16, 2 fp16) as fp32.
+// Eight consecutive values of a type (DT: 0 fp32, 1 bf16, 2 fp16) as they lie in memory.
 template <int DT>
-__device__ __forceinline__ void load8(const void *p, size_t i, float *f) {
-    if constexpr (DT == 0) {
-        const float4 a = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
-        const float4 b = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i + 4);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
-        const uint4 u = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p) + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw8 {
+    uint4 u[DT == 0 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *p, size_t i) {
+        if constexpr (DT == 0) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(p) + i);
+            u[0] = q[0];
+            u[1] = q[1];
+        } else {
+            u[0] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p) + i);
+        }
+    }
+    __device__ __forceinline__ void widen(float *f) const {
+        const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == 1) {
+            if constexpr (DT == 0) {
+                f[j] = __uint_as_float(w[j]);
+            } else if constexpr (DT == 1) {
                 f[2 * j] = __uint_as_float(w[j] << 16);
                 f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
             } else {
@@ -89,8 +96,76 @@ __device__ __forceinline__ void load8(const void *p, size_t i, float *f) {
                 f[2 * j + 1] = x.y;
             }
         }
+        if constexpr (DT == 0) {
+            f[4] = __uint_as_float(u[1].x); f[5] = __uint_as_float(u[1].y);
+            f[6] = __uint_as_float(u[1].z); f[7] = __uint_as_float(u[1].w);
+        }
     }
+};
+template <int DT>
+__device__ __forceinline__ void load8(const void *p, size_t i, float *f) {
+    Raw8<DT> r;
+    r.load(p, i);
+    r.widen(f);
 }
+
+// Smallest and largest of eight channels over the rows that add() is given; a NaN
+// stays.  Pairs of 16-bit values are compared as pairs.
+template <int DT>
+struct Range8 {
+    using P = typename std::conditional<DT == 1, __nv_bfloat162, __half2>::type;
+    uint32_t lo[DT == 0 ? 8 : 4], hi[DT == 0 ? 8 : 4];
+    __device__ __forceinline__ static uint32_t least(uint32_t a, uint32_t b) {
+        if constexpr (DT == 0) {
+            const float x = __uint_as_float(a), y = __uint_as_float(b);
+            return __float_as_uint(x != x || y < x || y != y ? (x != x ? x : y) : x);
+        } else {
+            const P r = __hmin2_nan(*reinterpret_cast<const P *>(&a), *reinterpret_cast<const P *>(&b));
+            return *reinterpret_cast<const uint32_t *>(&r);
+        }
+    }
+    __device__ __forceinline__ static uint32_t most(uint32_t a, uint32_t b) {
+        if constexpr (DT == 0) {
+            const float x = __uint_as_float(a), y = __uint_as_float(b);
+            return __float_as_uint(x != x || y > x || y != y ? (x != x ? x : y) : x);
+        } else {
+            const P r = __hmax2_nan(*reinterpret_cast<const P *>(&a), *reinterpret_cast<const P *>(&b));
+            return *reinterpret_cast<const uint32_t *>(&r);
+        }
+    }
+    __device__ __forceinline__ void clear() {  // +infinity, -infinity
+        constexpr uint32_t up = DT == 0 ? 0x7f800000u : DT == 1 ? 0x7f807f80u : 0x7c007c00u;
+        constexpr uint32_t sign = DT == 0 ? 0x80000000u : 0x80008000u;
+#pragma unroll
+        for (int j = 0; j < (DT == 0 ? 8 : 4); ++j) {
+            lo[j] = up;
+            hi[j] = up | sign;
+        }
+    }
+    __device__ __forceinline__ void add(const Raw8<DT> &r) {
+        const uint32_t w[8] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w, r.u[DT == 0].x, r.u[DT == 0].y,
+                               r.u[DT == 0].z, r.u[DT == 0].w};
+#pragma unroll
+        for (int j = 0; j < (DT == 0 ? 8 : 4); ++j) {
+            lo[j] = least(lo[j], w[j]);
+            hi[j] = most(hi[j], w[j]);
+        }
+    }
+    // also over the lanes whose number differs in bit `o`
+    __device__ __forceinline__ void join(int o) {
+#pragma unroll
+        for (int j = 0; j < (DT == 0 ? 8 : 4); ++j) {
+            lo[j] = least(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
+            hi[j] = most(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
+        }
+    }
+    __device__ __forceinline__ static void widen(const uint32_t *w, float *f) {
+        Raw8<DT> r;
+        r.u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (DT == 0) r.u[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        r.widen(f);
+    }
+};
 
 // x within +-far, NaN kept: a value beyond the output type's range becomes
 // its largest finite one (the nearest code to 65504 may stand for 65536)
