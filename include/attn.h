@@ -307,7 +307,7 @@ ATTN_API int attn_merge(const float *o_parts, const float *lse_parts, int n_part
  *   nearest, ties to even.  A NaN or an infinity makes the scale of its block
  *   NaN: everything read from that block and head is NaN until the page is
  *   started again at its first row.  attn_cache_read and attn_fwd_cache take
- *   any scale; pages that append continues must hold such powers of two.
+ *   any finite scale or NaN; pages that append continues must hold such powers of two.
  */
 typedef enum attn_cache_format {
     ATTN_CACHE_E4M3 = 0, /* 4-bit exponent, 3-bit mantissa, no infinities; largest 448 */
@@ -396,7 +396,8 @@ ATTN_API int attn_cache_select(const attn_cache *cache, const void *q, const int
  *          argument.  Calls that may overlap on the GPU, replays of graphs
  *          among them, need workspaces of their own.
  * Arithmetic: exact products of codes and q, fp32 sums; the weights keep 22
- * bits, or 11 for a bf16 output with more than 8 query rows per kv head.
+ * bits, or 11 for a 16-bit output with more than 8 query rows per kv head
+ * (H / H_kv * Sq, or H / H_kv with a page list).
  * Results do not depend on other sequences' contents, but the grouping of sums
  * (not their terms) follows all lengths of the call.  Two kernels.
  */

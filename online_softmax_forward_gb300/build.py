@@ -32,8 +32,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn.so")
 TEST_LIB = os.path.join(HERE, "libattn_test.so")
 CHECKED_LIB = os.path.join(HERE, "libattn_checked.so")
-SOURCES = ["attn_api.cu", "attn_cache.cu", "attn_cache_fwd.cu", "attn_cache_select.cu", "attn_f32.cu",
-           "attn_splitkv.cu", "attn_tc.cu"]
+SOURCES = ["attn_api.cu", "attn_cache.cu", "attn_cache_fwd.cu", "attn_cache_select.cu",
+           "attn_cache_tc.cu", "attn_f32.cu", "attn_splitkv.cu", "attn_tc.cu"]
 # (source, object name, extra flags) of the test library's own objects
 TEST_SOURCES = [("attn_api.cu", "attn_api_test.o", ["-DATTN_TEST_EXPORTS"])]
 # ... and of the bounds-checking library's, one per source
@@ -41,8 +41,8 @@ CHECKED_SOURCES = [(src, src.replace(".cu", "_checked.o"),
                     ["-DATTN_BOUNDS_CHECK"] + (["-DATTN_TEST_EXPORTS"] if src == "attn_api.cu"
                                                else []))
                    for src in SOURCES]
-HEADERS = ["attn_internal.h", "cache_codec.cuh", "cache_index.h", "cache_mma.cuh",
-           "sm100_ptx.cuh"]
+HEADERS = ["attn_internal.h", "cache_codec.cuh", "cache_fwd.cuh", "cache_index.h", "cache_mma.cuh",
+           "sm100_ptx.cuh", "tc_common.cuh"]
 PUBLIC_HEADERS = ["attn.h", "attn_test.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -22,8 +22,8 @@
 //   8-row form: rows 0-7 are query rows, rows 8-15 the same rows' rounding
 //     remainders: q = hi + lo (lo = 0 unless q is fp32) and p = hi + lo, so the
 //     products are those of 22-bit numbers and fp32 outputs keep their digits.
-//   16-row form (bf16 output, more than 8 rows): p is rounded once to fp16
-//     (2^-12, against the output's 2^-9).
+//   16-row form (16-bit output, 9 to 16 rows; with a page list, any number above 8):
+//     p is rounded once to fp16 (2^-12, as an fp16 output is, or less than a bf16 one).
 // q rows are first multiplied by a power of two that puts the row's largest
 // magnitude in [2^14, 2^15): any fp32 or bf16 exponent then fits fp16.
 //
@@ -47,8 +47,7 @@
 #include <stdint.h>
 
 #include "attn_internal.h"
-#include "cache_codec.cuh"
-#include "cache_index.h"
+#include "cache_fwd.cuh"
 #include "cache_mma.cuh"
 
 namespace attn {
@@ -59,38 +58,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRing = 24 * 1024;  // shared memory of each warp's tiles, later of its states
 constexpr int kMinTiles = 1;  // tiles per worker when there are few
 
-struct FwdArgs {
-    const void *q;
-    void *o;
-    float *lse;
-    const uint8_t *k, *v;
-    const float *ks, *vs;
-    const int32_t *table, *lens, *counts, *pages;
-    float *hold;      // [warp][R][D]: state of the unit a warp's range begins inside of, if more follows
-    float *po, *pl;   // states of the CTAs' shared units by slot: [slot][R][D], [slot][R] (log2)
-    int4 *tail;       // [CTA]: the unit that runs over the end of a CTA's range
-    int B, Hkv, G, Sq, page, n_pages, max_pages, n_sel, causal;
-    int nseg, rows, nrb;  // row groups of a (sequence, kv head), rows of one, row blocks of one
-    int units;            // of a sequence: Hkv * nseg * nrb
-    int dtype, workers;
-    FastDiv by_units, by_per, by_nrb, by_group;  // per = nseg * nrb
-    float sl2;  // scale * log2(e)
-    int *status;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
     uint4 u;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -113,85 +80,6 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     if constexpr (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
     else return (uint32_t)((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ ((r >> 1 & 3) * 2)) << 4));
 }
-// Sequence lengths as tile counts, summed: prefix[b] tiles before sequence b.
-__device__ __forceinline__ void scan_lengths(const FwdArgs &a, int kt, int *prefix, int *warp_sums) {
-    const int per = (a.B + kThreads - 1) / kThreads;
-    const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int len0 = a.lens[b], cnt = a.counts ? a.counts[b] : a.Sq;
-        const int len = clamp_len(len0, a.max_pages, a.page);
-        if ((len != len0 || cnt < 0 || cnt > a.Sq) && blockIdx.x == 0)
-            atomicOr(a.status, kStatusTable);
-        const int n = (int)(((int64_t)len + kt - 1) / kt);
-        prefix[b + 1] = n;  // turned into a sum below
-        sum += n;
-    }
-    int incl = sum;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    int at = incl - sum;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) at += w < warp ? warp_sums[w] : 0;
-    for (int b = b0; b < b1; ++b) prefix[b + 1] = at += prefix[b + 1];
-    if (threadIdx.x == 0) prefix[0] = 0;
-    __syncthreads();
-}
-
-// Where tile x lies.
-__device__ __forceinline__ Place place_of(const FwdArgs &a, const int *prefix, int tpu, int64_t x) {
-    Place p;
-    if (a.pages) {
-        const int64_t n = quotient(x, tpu);
-        p.b = (int)quotient(n, a.units);
-        p.unit = (int)(n - (int64_t)p.b * a.units);
-        p.n = tpu;
-        p.t = (int)(x - n * tpu);
-        return p;
-    }
-    const int y = (uint64_t)x >> 31 ? (int)(x / a.units) : (int)((uint32_t)x / a.by_units);
-    int lo = 0, hi = a.B - 1;  // the last b with prefix[b] <= y
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= y) lo = mid; else hi = mid - 1;
-    }
-    const int64_t in = x - (int64_t)prefix[lo] * a.units;
-    p.b = lo;
-    p.n = prefix[lo + 1] - prefix[lo];
-    p.unit = (int)quotient(in, p.n);
-    p.t = (int)(in - (int64_t)p.unit * p.n);
-    return p;
-}
-
-struct Unit {
-    int b, hk, seg, rb;
-};
-__device__ __forceinline__ Unit unit_at(const FwdArgs &a, int b, int unit) {
-    Unit u;
-    u.b = b;
-    u.hk = (int)((uint32_t)unit / a.by_per);
-    const int in = unit - u.hk * a.nseg * a.nrb;
-    u.seg = (int)((uint32_t)in / a.by_nrb);
-    u.rb = in - u.seg * a.nrb;
-    return u;
-}
-
-// Query and head of row r of a unit; false past the group's rows.
-template <int R>
-__device__ __forceinline__ bool row_of(const FwdArgs &a, const Unit &u, int r, int &i, int &h) {
-    const int row = u.rb * R + r;
-    const int q = a.pages ? u.seg : (int)((uint32_t)row / a.by_group);
-    i = q;
-    h = u.hk * a.G + (a.pages ? row : row - q * a.G);
-    return row < a.rows;
-}
-
 struct Tile {  // one key tile, held by one lane
     int at;    // tile of KT keys in the pool, -1: nothing to read
     int key0;  // its first key's position in the sequence
@@ -237,62 +125,6 @@ __device__ __forceinline__ Tile find_tile(const FwdArgs &a, const Place &p) {
     return d;
 }
 
-// Elements [i, i + N) of q as fp32.
-template <int N>
-__device__ __forceinline__ void load_q(const FwdArgs &a, size_t i, float *f) {
-    if (a.dtype == ATTN_F32) {
-#pragma unroll
-        for (int e = 0; e < N; e += 8) codec::load8<0>(a.q, i + e, f + e);
-    } else if (a.dtype == ATTN_BF16 || a.dtype == ATTN_BF16_OUT_F32) {
-#pragma unroll
-        for (int e = 0; e < N; e += 8) codec::load8<1>(a.q, i + e, f + e);
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; e += 8) codec::load8<2>(a.q, i + e, f + e);
-    }
-}
-
-// Eight consecutive outputs.
-__device__ __forceinline__ void store_o8(const FwdArgs &a, size_t i, const float *f) {
-    if (a.dtype == ATTN_BF16) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.o) + i) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if (a.dtype == ATTN_F16) {
-        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.o) + i) =
-            make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
-    } else {
-        float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + i);
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-}
-
-// Row of o and lse that row r of a unit is; false past the group's rows.
-template <int R>
-__device__ __forceinline__ bool out_row(const FwdArgs &a, const Unit &u, int r, size_t &row) {
-    int i, h;
-    if (!row_of<R>(a, u, r, i, h)) return false;
-    row = ((size_t)u.b * a.Hkv * a.G + h) * a.Sq + i;
-    return in_bounds(i < a.Sq && h < a.Hkv * a.G && u.b < a.B, a.status);
-}
-constexpr float kLn2 = 0.69314718055994530942f;
-
-// `top` before the first key: any visible score is above it by more than the
-// range of exp2, so that its weight comes out infinite and sets the references.
-constexpr float kUnset = -3.0e38f;
-
-// One output.
-__device__ __forceinline__ void store_o(const FwdArgs &a, size_t i, float x) {
-    if (a.dtype == ATTN_BF16) reinterpret_cast<__nv_bfloat16 *>(a.o)[i] = __float2bfloat16_rn(x);
-    else if (a.dtype == ATTN_F16) reinterpret_cast<__half *>(a.o)[i] = __float2half_rn(x);
-    else reinterpret_cast<float *>(a.o)[i] = x;
-}
-
 // WIDE = 0: the 8-row form, 1: the 16-row form.
 template <int D, int FMT, int WIDE, int KT>
 __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a) {
@@ -331,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                     atomicOr(a.status, kStatusTable);
             }
     } else {
-        scan_lengths(a, KT, prefix, warp_sums);
+        scan_lengths<kThreads>(a, KT, prefix, warp_sums);
         total = (int64_t)prefix[a.B] * a.units;
         // sequences without a token have no tile: o = 0, lse = -inf
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -842,14 +674,25 @@ int launch_fwd_w(const FwdArgs &a, bool wide, int kt, unsigned grid, cudaStream_
 
 }  // namespace
 
+// Query rows per kv head from which the 128-row tcgen05 kernel runs (16-bit
+// outputs, all pages).
+constexpr int64_t kTcRows = 17;
+static bool cache_tc(int64_t rows, int dtype, bool listed) {
+    return !listed && (dtype == ATTN_BF16 || dtype == ATTN_F16) && rows >= kTcRows;
+}
 // The 16-row form where the output's own rounding hides the weights' and the
 // rows do not fit eight.
-static bool cache_wide(int rows, int dtype) { return dtype == ATTN_BF16 && rows > 8; }
+static bool cache_wide(int64_t rows, int dtype) {
+    return (dtype == ATTN_BF16 || dtype == ATTN_F16) && rows > 8;
+}
 
-// Workspace: the tails [CTA], a state per warp, two per CTA and their lse.
+// Workspace: the tails [CTA], a state per warp, two per CTA and their lse (the
+// tcgen05 kernel: without the warps').
 size_t cache_fwd_workspace(int B, int H, int H_kv, int Sq, int d, int dtype, bool listed) {
     const int64_t rows = (int64_t)(H / H_kv) * (listed ? 1 : Sq);
-    const size_t R = cache_wide((int)(rows > 16 ? 16 : rows), dtype) ? 16 : 8;
+    if (cache_tc(rows, dtype, listed))
+        return (size_t)kCacheMaxCtas * (16 + 2 * 128 * (size_t)d * 4 + 2 * 128 * 4);
+    const size_t R = cache_wide(rows, dtype) ? 16 : 8;
     return (size_t)kCacheMaxCtas * (16 + (kWarps + 2) * R * d * 4 + 2 * R * 4);
 }
 
@@ -868,6 +711,10 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     a.sl2 = scale * 1.4426950408889634f;
     a.nseg = pages ? Sq : 1;
     a.rows = pages ? a.G : a.G * Sq;
+    a.by_group = fast_div((uint32_t)a.G);
+    a.status = status_word_device_ptr();
+    if (!a.status) return ATTN_ERR_CUDA;
+    if (cache_tc(a.rows, dtype, pages != nullptr)) return launch_cache_tc(a, c.d, c.format, workspace, stream);
     const bool wide = cache_wide(a.rows, dtype);
     const int R = wide ? 16 : 8;
     a.nrb = (a.rows + R - 1) / R;
@@ -876,9 +723,6 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     a.by_units = fast_div((uint32_t)a.units);
     a.by_per = fast_div((uint32_t)(a.nseg * a.nrb));
     a.by_nrb = fast_div((uint32_t)a.nrb);
-    a.by_group = fast_div((uint32_t)a.G);
-    a.status = status_word_device_ptr();
-    if (!a.status) return ATTN_ERR_CUDA;
     const int kt = tile_keys(c.d, c.page);
     const int sms = device_sm_count();
     if (sms <= 0) return ATTN_ERR_CUDA;

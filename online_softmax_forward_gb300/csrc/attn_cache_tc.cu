@@ -1,0 +1,781 @@
+// attn_cache_tc.cu -- attention over the paged 8-bit cache for many query rows
+// per kv head (prompt chunks, draft tokens), on tcgen05.
+//
+// The operation and the numbering of the work are those of attn_cache_fwd.cu.  A
+// unit here is (sequence, kv head, block of 128 rows); its keys are walked in
+// tiles of 128, and each CTA (one per SM) takes one contiguous range of tiles.
+// With 128 rows the products are no longer free, and one conversion of the codes
+// to fp16 serves all of them:
+//
+//   warps 9-11  copy the codes with cp.async into private buffers, three items
+//               (a tile's keys or values) ahead, convert them to fp16, exact, and
+//               write the MMA's 128-byte-swizzled tiles into a ring of stages;
+//   warp 8      issues S_t = Q K_j^T and O_t += P_t V_j, t = j & 1;
+//   warps 0-3   softmax of the even tiles, 4-7 of the odd ones, a thread per row:
+//               S out of tensor memory, the pages' scales applied per 16 keys, P
+//               as fp16 over the first half of S_t.
+//
+// The two halves keep states of their own (top, rv, l and O_t, references moved
+// only when a tile would pass fp16's range, as in attn_cache_fwd.cu), so that one
+// exponentiates while the other's products run; they are joined when the unit
+// ends.  A warp without a real row (few drafts, few heads) only keeps step.  P in
+// fp16 is rounded by 2^-12, so this kernel serves the 16-bit outputs.
+//
+// Tensor memory (512 columns): S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 from
+// 256, O_1 from 256 + D.  S_t(j + 2) may be written once P_t(j) has been used: its
+// issue waits for that product.  Every wait is bounded, as in attn_tc.cu.
+#include <atomic>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_internal.h"
+#include "cache_fwd.cuh"
+#include "cache_mma.cuh"
+#include "sm100_ptx.cuh"
+#include "tc_common.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int R = 128;   // rows of a unit
+constexpr int KT = 128;  // keys of a tile
+constexpr int kMmaWarp = 8;
+constexpr int kThreads = 12 * 32;
+constexpr int kConverters = 3;      // warps 9 .. 11
+constexpr int kAhead = 3;           // items whose copies are in flight
+constexpr int kScaleRing = 8;       // tiles whose page scales are kept
+constexpr uint32_t kTmemCols = 512;
+// Register split (setmaxnreg): launched with kLaunchRegs each; the softmax
+// warpgroups grow, the third shrinks; the totals match exactly.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs == kThreads * kLaunchRegs, "register split");
+constexpr float kLargest = 1024.f;  // of a tile's sum of weights; 32 * 1024 fits fp16
+constexpr float kBase = 32.f;       // page scale times rv, at its largest after a move
+
+struct Bars {
+    uint64_t q_full, q_empty;
+    uint64_t kv_full[6], kv_empty[6];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t o_empty, joined, mma_done;
+    uint64_t sc_full[kScaleRing];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int kChunks = D / 64;
+    static constexpr int kChunkBytes = 128 * 128;             // 64 channels of 128 rows, fp16
+    static constexpr int kTile = kChunks * kChunkBytes;       // Q, K or V tile
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kIters = KT * D / 512;               // 512-byte pieces of an item
+    static constexpr int kMine = (kIters + kConverters - 1) / kConverters;
+    static constexpr int kRawWarp = (kAhead + 1) * kMine * 512;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffKV = kTile;
+    static constexpr int kOffRaw = kOffKV + kStages * kTile;
+    static constexpr int kOffScale = kOffRaw + kConverters * kRawWarp;   // [ring][2][8] fp32
+    static constexpr int kOffState = kOffScale + kScaleRing * 16 * 4;    // [2][2][3][128] fp32
+    static constexpr int kOffBar = kOffState + 2 * 2 * 3 * R * 4;
+    static constexpr int kOffPrefix = kOffBar + 512;
+    static constexpr int kSmem = kOffPrefix + (kMaxCacheBatch + 1) * 4 + 1024;  // + alignment
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(Cfg<128>::kSmem <= 227 * 1024 && Cfg<64>::kSmem <= 227 * 1024, "shared memory");
+
+// A piece of a unit inside the CTA's range, the same for every role.
+struct Piece {
+    Unit u;
+    int len, cnt;
+    int t0, left;  // first tile of the unit, tiles in the range
+    int live;      // of those, tiles that some row sees
+};
+
+struct TcArgs {
+    FwdArgs f;
+    unsigned long long timeout_ns;
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_constant__ TcArgs args) {
+    using C = Cfg<D>;
+    using U = Unpack<FMT>;
+    const FwdArgs &a = args.f;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars *bars = reinterpret_cast<Bars *>(sm + C::kOffBar);
+    int *prefix = reinterpret_cast<int *>(sm + C::kOffPrefix);
+    float *scales = reinterpret_cast<float *>(sm + C::kOffScale);
+    float *state = reinterpret_cast<float *>(sm + C::kOffState);
+    __shared__ int warp_sums[kThreads / 32];
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
+    const Watch watch{&bars->abort_flag, a.status, args.timeout_ns};
+    auto bar = [&](uint64_t &b) { return ptx::smem_addr(&b); };
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(bar(bars->q_full), 128);
+        ptx::mbar_init(bar(bars->q_empty), 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(bar(bars->kv_full[s]), kConverters * 32);
+            ptx::mbar_init(bar(bars->kv_empty[s]), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(bar(bars->s_full[t]), 1);
+            ptx::mbar_init(bar(bars->p_full[t]), 128);
+            ptx::mbar_init(bar(bars->pv_done[t]), 1);
+        }
+        ptx::mbar_init(bar(bars->o_empty), 256);
+        ptx::mbar_init(bar(bars->joined), 256);
+        ptx::mbar_init(bar(bars->mma_done), 1);
+        for (int s = 0; s < kScaleRing; ++s) ptx::mbar_init(bar(bars->sc_full[s]), 1);
+        bars->abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(ptx::smem_addr(&bars->tmem_base), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    scan_lengths<kThreads>(a, KT, prefix, warp_sums);
+    const int64_t total = (int64_t)prefix[a.B] * a.units;
+    // sequences without a token have no tile: o = 0, lse = -inf
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (prefix[b] != prefix[b + 1]) continue;
+        const size_t row0 = (size_t)b * a.Hkv * a.G * a.Sq, n = (size_t)a.Hkv * a.G * a.Sq;
+        const float z[8] = {};
+        for (size_t e = threadIdx.x; e < n * (D / 8); e += kThreads) store_o8(a, row0 * D + e * 8, z);
+        if (a.lse)
+            for (size_t e = threadIdx.x; e < n; e += kThreads) a.lse[row0 + e] = -INFINITY;
+    }
+    const int64_t workers = worker_count(total, a.workers, 1);
+    int64_t x0 = 0;
+    int n_tiles = 0;
+    if (blockIdx.x < workers && total > 0) {
+        x0 = worker_begin(blockIdx.x, total, workers);
+        n_tiles = (int)(worker_begin(blockIdx.x + 1, total, workers) - x0);
+    }
+    auto tiles = [&](int b) { return prefix[b + 1] - prefix[b]; };
+    Place start = {0, 0, 0, 1};
+    if (n_tiles > 0) start = place_of(a, prefix, 0, x0);
+    if (threadIdx.x == 0) {
+        // the unit that runs over the end of the range, if it began in it
+        int4 d = make_int4(0, 0, 0, 0);
+        if (n_tiles > 0) {
+            const int64_t x1 = x0 + n_tiles;
+            const Place p = place_of(a, prefix, 0, x1 - 1);
+            const int64_t end = x1 - 1 - p.t + p.n;
+            if (end > x1 && x1 - 1 - p.t >= x0)
+                d = make_int4(1, (int)worker_of(end - 1, total, workers), p.b, p.unit);
+        }
+        a.tail[blockIdx.x] = d;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
+    const uint32_t sQ = ptx::smem_addr(sm + C::kOffQ), sKV = ptx::smem_addr(sm + C::kOffKV);
+
+    // the piece at `here` when `done` tiles of the range lie before it
+    auto piece_at = [&](const Place &here, int done) {
+        Piece p;
+        p.u = unit_at(a, here.b, here.unit);
+        p.len = clamp_len(a.lens[here.b], a.max_pages, a.page);
+        p.cnt = a.counts ? min(max(a.counts[here.b], 0), a.Sq) : a.Sq;
+        p.t0 = here.t;
+        p.left = min(here.n - here.t, n_tiles - done);
+        // the block's last query that is one of the sequence's sees the most keys
+        int first, last, h;
+        row_of<R>(a, p.u, 0, first, h);
+        row_of<R>(a, p.u, min(a.rows - p.u.rb * R, R) - 1, last, h);
+        last = min(last, p.cnt - 1);
+        const int seen = last < first ? 0 : visible_keys(p.len, p.cnt, last, a.causal);
+        p.live = max(0, min(p.left, (int)(((int64_t)seen + KT - 1) / KT) - p.t0));
+        return p;
+    };
+    // item m of a piece with n live tiles, in the order of the products: K_0, K_1, V_0, K_2,
+    // V_1, ..., V_{n-2}, V_{n-1}
+    auto item = [](int m, int n, int &j) {
+        if (m == 0) {
+            j = 0;
+            return false;
+        }
+        j = (m + 1) / 2;
+        if ((m & 1) && j < n) return false;
+        j = (m & 1) ? n - 1 : (m - 2) / 2;
+        return true;
+    };
+
+    if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        ptx::setmaxnreg_dec<kOtherRegs>();
+        auto wait_all = [&](uint32_t b, uint32_t parity) {
+            return __all_sync(0xffffffffu, watch.wait(b, parity));
+        };
+        constexpr uint32_t kIdescS = idesc_f16(false, R, KT, false);
+        constexpr uint32_t kIdescO = idesc_f16(false, R, D, true);
+        const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(sKV, 16, 1024);
+        const uint64_t dv = sdesc(sKV, C::kChunkBytes, 1024);
+        uint32_t pos = 0, qn = 0, on = 0, pn[2] = {0, 0};
+        bool ok = true;
+        Place here = start;
+        for (int i = 0; i < n_tiles && ok;) {
+            const Piece p = piece_at(here, i);
+            auto issue_s = [&](int j) {
+                const int st = pos % C::kStages;
+                if (!wait_all(bar(bars->kv_full[st]), (pos / C::kStages) & 1)) return false;
+                ptx::tc_fence_after();
+                const uint64_t dkj = dk + (uint64_t)((st * C::kTile) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
+                    ptx::mma_ss_warp(tmem + (j & 1) * KT, dq + off, dkj + off, kIdescS, kk > 0 ? 1u : 0u);
+                }
+                ptx::mma_commit_warp(bar(bars->s_full[j & 1]));
+                ptx::mma_commit_warp(bar(bars->kv_empty[st]));
+                if (j == p.live - 1) ptx::mma_commit_warp(bar(bars->q_empty));
+                ++pos;
+                return true;
+            };
+            if (p.live > 0) {
+                ok = wait_all(bar(bars->q_full), qn & 1);
+                ++qn;
+                ok = ok && issue_s(0) && (p.live < 2 || issue_s(1));
+                // the epilogue of the last unit has read both O
+                ok = ok && wait_all(bar(bars->o_empty), (on & 1) ^ 1);
+                ++on;
+                for (int j = 0; j < p.live && ok; ++j) {
+                    const int t = j & 1, st = pos % C::kStages;
+                    ok = wait_all(bar(bars->p_full[t]), pn[t] & 1) &&
+                         wait_all(bar(bars->kv_full[st]), (pos / C::kStages) & 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint64_t dvj = dv + (uint64_t)((st * C::kTile) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < KT / 16; ++kk)
+                        ptx::mma_ts_warp(tmem + 256 + t * D, tmem + t * KT + kk * 8,
+                                         dvj + (uint64_t)((kk * 16 * 128) >> 4), kIdescO,
+                                         (j > 1 || kk > 0) ? 1u : 0u);
+                    ptx::mma_commit_warp(bar(bars->pv_done[t]));
+                    ptx::mma_commit_warp(bar(bars->kv_empty[st]));
+                    ++pos;
+                    if (j + 2 < p.live)  // S_t takes P_t's place
+                        ok = wait_all(bar(bars->pv_done[t]), pn[t] & 1) && issue_s(j + 2);
+                    ++pn[t];
+                }
+            }
+            i += p.left;
+            if (i < n_tiles) advance(here, p.left, a.units, tiles);
+        }
+        // every MMA issued by this warp has completed before tensor memory is freed
+        ptx::mma_commit_warp(bar(bars->mma_done));
+        watch.drain(bar(bars->mma_done), 0);
+        __syncwarp();
+    } else if (warp > kMmaWarp) {
+        // ------------------------------------------------------------ converters
+        ptx::setmaxnreg_dec<kOtherRegs>();
+        const int cw = warp - kMmaWarp - 1;
+        uint8_t *raw = sm + C::kOffRaw + cw * C::kRawWarp + lane * 16;
+        const uint32_t raw_at = ptx::smem_addr(raw);
+        const int page16 = a.page / 16;
+        // row and 16-byte piece of a lane in a 512-byte copy: for d = 128 the two
+        // halves of a row are not written in the same quarter of the warp, whose
+        // lanes would meet in the same banks
+        const int rl = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
+        const int ql = D == 128 ? (lane & 3) + ((lane >> 3) & 1) * 4 : lane & 3;
+        const int src_off = rl * D + ql * 16;
+        constexpr int kRowsIter = 512 / D;
+
+        // The items to copy run kAhead ahead of the ones to convert; both walk the pieces.
+        struct Cursor {
+            Place here;
+            int i, m, slot;  // tiles of the range before the piece, item of it, tiles before (mod ring)
+        };
+        Cursor in = {start, 0, 0, 0}, out = in;
+        Piece pi, po;
+        // to the first piece from the cursor on that has a live tile
+        auto settle = [&](Cursor &c, Piece &p) {
+            while (c.i < n_tiles) {
+                p = piece_at(c.here, c.i);
+                if (p.live > 0) return;
+                c.i += p.left;
+                if (c.i < n_tiles) advance(c.here, p.left, a.units, tiles);
+            }
+        };
+        auto step = [&](Cursor &c, Piece &p) {
+            if (++c.m < 2 * p.live) return;
+            c.m = 0;
+            c.slot = (c.slot + p.live) % kScaleRing;
+            c.i += p.left;
+            if (c.i < n_tiles) advance(c.here, p.left, a.units, tiles);
+            settle(c, p);
+        };
+        // lane s < 8: 16-key piece s of the item's tile as a 16-row piece of the pool, -1: none
+        auto find = [&](const Cursor &c, const Piece &p) {
+            int at = -1;
+            if (c.i < n_tiles && lane < 8) {
+                int j;
+                item(c.m, p.live, j);
+                const int key = (p.t0 + j) * KT + lane * 16;
+                if (key < p.len) {
+                    const int lp = key / a.page;
+                    const int phys = a.table[(int64_t)p.u.b * a.max_pages + lp];
+                    if (phys < 0 || phys >= a.n_pages) atomicOr(a.status, kStatusTable);
+                    else at = (phys * a.Hkv + p.u.hk) * page16 + (key - lp * a.page) / 16;
+                }
+            }
+            return at;
+        };
+        settle(in, pi);
+        settle(out, po);
+        int next_at = find(in, pi);
+        int buf_in = 0, buf_out = 0;
+        uint32_t missing = 0;  // 8 bits for each buffer: its item's pieces that are not there
+        // the copies of the item at `in`
+        auto issue = [&] {
+            if (in.i < n_tiles) {
+                const int at = next_at;
+                int j;
+                const bool is_v = item(in.m, pi.live, j);
+                missing = (missing & ~(0xffu << (8 * buf_in))) |
+                          (__ballot_sync(0xffffffffu, lane < 8 && at < 0) & 0xffu) << (8 * buf_in);
+                const uint8_t *src = (is_v ? a.v : a.k) + src_off;
+#pragma unroll
+                for (int e = 0; e < C::kMine; ++e) {
+                    const int it = cw + e * kConverters;
+                    const int row = it * kRowsIter;
+                    const int seg = __shfl_sync(0xffffffffu, at, (row >> 4) & 7);
+                    if (it < C::kIters && seg >= 0)
+                        cp_async16(raw_at + (buf_in * C::kMine + e) * 512,
+                                   src + (size_t)seg * 16 * D + (row & 15) * D);
+                }
+                if (!is_v && cw == 0) {
+                    // the tile's scales: lanes 0-7 of the keys, 8-15 of the values; an infinite
+                    // key scale marks a piece that is not there
+                    const int seg = __shfl_sync(0xffffffffu, at, lane & 7);
+                    float *dst = scales + ((in.slot + j) % kScaleRing) * 16 + lane;
+                    if (lane < 16) {
+                        if (seg >= 0) {
+                            const float *s = (lane < 8 ? a.ks : a.vs) + seg / page16;
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_addr(dst)), "l"(s) : "memory");
+                        } else {
+                            *dst = lane < 8 ? INFINITY : 0.f;
+                        }
+                    }
+                }
+                step(in, pi);
+                next_at = find(in, pi);
+                buf_in = buf_in == kAhead ? 0 : buf_in + 1;
+            }
+            cp_async_commit();
+        };
+#pragma unroll 1
+        for (int k = 0; k < kAhead; ++k) issue();
+        uint32_t pos = 0;
+        while (out.i < n_tiles) {
+            issue();
+            cp_async_wait<kAhead>();
+            int j;
+            const bool is_v = item(out.m, po.live, j);
+            const int key0 = (po.t0 + j) * KT;
+            if (!is_v && cw == 0) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(bars->sc_full[(out.slot + j) % kScaleRing]));
+            }
+            const int st = pos % C::kStages;
+            if (!__all_sync(0xffffffffu, watch.wait(bar(bars->kv_empty[st]), ((pos / C::kStages) & 1) ^ 1))) break;
+            const uint32_t dst = sKV + st * C::kTile;
+            // pieces of the tile that are not there hold no values (as behind the last token)
+            const int seen = is_v ? po.len - key0 : KT;
+            const uint32_t miss = missing >> (8 * buf_out);
+#pragma unroll
+            for (int e = 0; e < C::kMine; ++e) {
+                const int it = cw + e * kConverters;
+                if (it < C::kIters) {
+                    const int row = it * kRowsIter + rl;
+                    uint4 c = *reinterpret_cast<const uint4 *>(raw + (buf_out * C::kMine + e) * 512);
+                    const bool gone = is_v && (row >= seen || (miss >> (row >> 4 & 7) & 1));
+                    uint32_t h[8];
+                    U::quad(c.x, h[0], h[1]);
+                    U::quad(c.y, h[2], h[3]);
+                    U::quad(c.z, h[4], h[5]);
+                    U::quad(c.w, h[6], h[7]);
+                    if (gone) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) h[k] = 0;
+                    }
+                    const uint32_t line = dst + (ql >> 2) * C::kChunkBytes + row * 128;
+                    const uint32_t p0 = (ql & 3) * 2;
+                    ptx::st_shared_v4(line + ((p0 ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    ptx::st_shared_v4(line + (((p0 + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(bar(bars->kv_full[st]));
+            ++pos;
+            buf_out = buf_out == kAhead ? 0 : buf_out + 1;
+            step(out, po);
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        ptx::setmaxnreg_inc<kSoftmaxRegs>();
+        const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
+        const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+        const uint32_t tS = tmem + lanes + t * KT, tO = tmem + lanes + 256 + t * D;
+        uint32_t sn = 0, qn = 0, jn = 0;
+        int slot = 0;
+        bool ok = true;
+        Place here = start;
+        for (int i = 0; i < n_tiles && ok;) {
+            const Piece p = piece_at(here, i);
+            int qi, h;
+            const bool real = row_of<R>(a, p.u, r, qi, h);
+            const bool idle = !__any_sync(0xffffffffu, real);  // no row of this warp is one
+            // rows past the block's see everything, so that they never ask for a mask
+            const int lim = real ? visible_keys(p.len, p.cnt, qi, a.causal) : 0x7fffffff;
+            const size_t at = real ? (((size_t)p.u.b * a.Hkv * a.G + h) * a.Sq + qi) * D : 0;
+            float cq = 0.f;
+            if (p.live > 0) {
+                // the row's power of two; the first warpgroup writes the row as fp16
+                float amax = 0.f;
+                if (real) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float f[32];
+                        load_q<32>(a, at + c, f);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(f[e]));
+                    }
+                }
+                float mul, back;
+                row_power(amax, mul, back);
+                cq = a.sl2 * back;
+                if (t == 0) {
+                    if (!__all_sync(0xffffffffu, watch.wait(bar(bars->q_empty), (qn & 1) ^ 1))) break;
+                    ++qn;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float f[32];
+                        if (real) {
+                            load_q<32>(a, at + c, f);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = 0.f;
+                        }
+                        const uint32_t line = sQ + (c >> 6) * C::kChunkBytes + r * 128;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) w[k] = pack_f16(f[8 * e + 2 * k] * mul, f[8 * e + 2 * k + 1] * mul);
+                            ptx::st_shared_v4(line + ((uint32_t)((((c & 63) >> 3) + e) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    ptx::fence_proxy_async_smem();
+                    ptx::mbar_arrive(bar(bars->q_full));
+                }
+            }
+            float top = kUnset, rv = 0x1p100f, l = 0.f;
+            for (int j = t; j < p.live; j += 2) {
+                const int ring = (slot + j) % kScaleRing, lap = (slot + j) / kScaleRing;
+                bool got = watch.wait(bar(bars->sc_full[ring]), lap & 1);
+                got = got && watch.wait(bar(bars->s_full[t]), sn & 1);
+                ++sn;
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                if (!idle) {
+                    const float *ks = scales + ring * 16, *vs = ks + 8;
+                    const int key0 = (p.t0 + j) * KT;
+                    bool hole = false;
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) hole = hole || ks[s] == INFINITY;
+                    const bool edge = __any_sync(0xffffffffu, hole || key0 + KT > lim);
+                    uint32_t pk[64];
+                    float sum = 0.f;
+                    bool moved = false;
+                    while (true) {
+                        bool far = false;
+                        sum = 0.f;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {  // 32 keys
+                            uint32_t s32[32];
+                            ptx::tmem_ld32(tS + c * 32, s32);
+                            ptx::tmem_wait_ld();
+                            reg_fence(s32);
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {  // of one page
+                                const int seg = c * 2 + s;
+                                const float f = ks[seg] * cq;
+                                // a page no key of which the row sees adds nothing, not even its
+                                // scale's NaN
+                                const float cv = key0 + seg * 16 < lim ? vs[seg] * rv : 0.f;
+                                float part = 0.f;
+#pragma unroll
+                                for (int e = 0; e < 16; e += 2) {
+                                    float z0 = fmaf(__uint_as_float(s32[s * 16 + e]), f, -top);
+                                    float z1 = fmaf(__uint_as_float(s32[s * 16 + e + 1]), f, -top);
+                                    if (edge) {
+                                        const int key = key0 + seg * 16 + e;
+                                        const bool gone = ks[seg] == INFINITY;
+                                        if (gone || key >= lim) z0 = -INFINITY;
+                                        if (gone || key + 1 >= lim) z1 = -INFINITY;
+                                    }
+                                    const float p0 = ptx::ex2_approx(z0), p1 = ptx::ex2_approx(z1);
+                                    part += p0 + p1;
+                                    pk[seg * 8 + e / 2] = pack_f16(p0 * cv, p1 * cv);
+                                }
+                                far = far || part > kLargest || part * cv > kLargest * kBase;
+                                sum += part;
+                            }
+                        }
+                        if (moved || !__any_sync(0xffffffffu, far)) break;
+                        moved = true;
+                        // new references: the scores' maximum, and the page scales unless what O
+                        // holds is larger by now
+                        float mx = -INFINITY, most = 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t s32[32];
+                            __syncwarp();
+                            ptx::tmem_ld32(tS + c * 32, s32);
+                            ptx::tmem_wait_ld();
+                            reg_fence(s32);
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                const int seg = c * 2 + s;
+                                const bool gone = ks[seg] == INFINITY;
+                                const float f = ks[seg] * cq;
+                                if (!gone && key0 + seg * 16 < lim) most = fmaxf(most, vs[seg]);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (!gone && key0 + seg * 16 + e < lim)
+                                        mx = fmaxf(mx, __uint_as_float(s32[s * 16 + e]) * f);
+                            }
+                        }
+                        const float nt = fmaxf(top, mx);
+                        const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
+                        const float was = alpha * kBase / rv;
+                        const float nv = mx == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, most), 0x1p-95f);
+                        const float to = alpha * (nv / rv);
+                        l *= alpha;
+                        top = nt;
+                        rv = nv;
+                        if (j > 1) {  // O_t holds the tiles before: S(j) came after their products
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                ptx::tmem_ld32(tO + c * 32, o);
+                                ptx::tmem_wait_ld();
+                                reg_fence(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * to);
+                                ptx::tmem_st32(tO + c * 32, o);
+                                ptx::tmem_wait_st();
+                            }
+                        }
+                    }
+                    l += sum;
+                    // P over S_t's first columns, all of which this warp has read
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) w[e] = pk[e];
+                    ptx::tmem_st32(tS, w);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) w[e] = pk[32 + e];
+                    ptx::tmem_st32(tS + 32, w);
+                    ptx::tmem_wait_st();
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(bar(bars->p_full[t]));
+            }
+            if (!ok) break;
+
+            // ---- the unit's end: the two halves' states, each with half of the channels
+            const int mine = (p.live - t + 1) / 2;  // tiles of this half
+            if (mine > 0) {
+                const bool got = watch.wait(bar(bars->pv_done[t]), (sn - 1) & 1);
+                if (!__all_sync(0xffffffffu, got)) break;
+            }
+            float *own = state + ((jn & 1) * 2 + t) * 3 * R;
+            own[r] = top;
+            own[R + r] = rv;
+            own[2 * R + r] = l;
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(bars->joined));
+            const bool got = watch.wait(bar(bars->joined), jn & 1);
+            if (!__all_sync(0xffffffffu, got)) break;
+            ptx::tc_fence_after();
+            const float *other = state + ((jn & 1) * 2 + (t ^ 1)) * 3 * R;
+            ++jn;
+            const float top2 = other[r], l2 = other[2 * R + r];
+            const float base = fmaxf(top, top2);
+            const float w1 = ptx::ex2_approx(top - base), w2 = ptx::ex2_approx(top2 - base);
+            const float L = l * w1 + l2 * w2;  // 0: no key was visible
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const float lse2 = L == 0.f ? -INFINITY : base + log2f(L);
+            // of this half's O and the other's, weight times inverse unit
+            const float c1 = w1 * inv, u1 = 1.f / rv, c2 = w2 * inv, u2 = 1.f / other[R + r];
+            const bool before = i == 0 && here.t > 0, after = here.t + p.left < here.n;
+            const bool whole = !before && !after;
+            const int sl = 2 * blockIdx.x + (before ? 0 : 1);
+            const bool has2 = p.live - (t ^ 1) > 0;  // the other half had a tile
+            if (!idle) {
+#pragma unroll 1
+                for (int c = t * (D / 2); c < (t + 1) * (D / 2); c += 32) {
+                    float f[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = 0.f;
+                    if (mine > 0) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(tmem + lanes + 256 + t * D + c, o);
+                        ptx::tmem_wait_ld();
+                        reg_fence(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * u1 * c1;
+                    }
+                    if (has2) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(tmem + lanes + 256 + (t ^ 1) * D + c, o);
+                        ptx::tmem_wait_ld();
+                        reg_fence(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(o[e]) * u2 * c2;
+                    }
+                    if (real && whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            if (in_bounds(at + c + e + 8 <= (size_t)a.B * a.Hkv * a.G * a.Sq * D, a.status))
+                                store_o8(a, at + c + e, f + e);
+                    } else if (real && in_bounds(sl < 2 * (int)gridDim.x, a.status)) {
+                        float4 *d = reinterpret_cast<float4 *>(a.po + ((size_t)sl * R + r) * D + c);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) d[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    }
+                    __syncwarp();  // the loads above are the whole warp's
+                }
+                if (t == 0 && real) {
+                    if (!whole) a.pl[sl * R + r] = lse2;
+                    else if (a.lse) a.lse[at / D] = lse2 * kLn2;
+                }
+            }
+            if (p.live > 0) {
+                __syncwarp();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(bar(bars->o_empty));
+            }
+            slot += p.live;
+            i += p.left;
+            if (i < n_tiles) advance(here, p.left, a.units, tiles);
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the states of the units that run over the CTAs' ends, a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) cache_tc_merge_kernel(const FwdArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 d = a.tail[blockIdx.x];
+    if (!d.x) return;
+    const Unit u = unit_at(a, d.z, d.w);
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    size_t row;
+    if (!out_row<R>(a, u, r, row)) return;
+    const int n = d.y - (int)blockIdx.x + 1;
+    if (!in_bounds(n <= kCacheMaxCtas, a.status)) return;
+    auto slot = [&](int p) { return 2 * (size_t)(blockIdx.x + p) + (p == 0 ? 1 : 0); };
+    float M = -INFINITY;
+    for (int p = lane; p < n; p += 32) M = fmaxf(M, a.pl[slot(p) * R + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f, acc[D / 32] = {};
+    for (int p0 = 0; p0 < n; p0 += 32) {
+        const float wt = p0 + lane < n ? ptx::ex2_approx(a.pl[slot(p0 + lane) * R + r] - base) : 0.f;
+        L += wt;
+#pragma unroll 4
+        for (int p = 0; p < min(32, n - p0); ++p) {
+            const float w = __shfl_sync(0xffffffffu, wt, p);
+            const float *src = a.po + (slot(p0 + p) * R + r) * D + lane;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, src[32 * e], acc[e]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) store_o(a, row * D + lane + 32 * e, acc[e] * inv);
+    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * kLn2;
+}
+
+template <int D, int FMT>
+int launch_t(const FwdArgs &f, unsigned grid, cudaStream_t stream) {
+    using C = Cfg<D>;
+    auto kern = cache_tc_kernel<D, FMT>;
+    // setmaxnreg needs exactly the register pool the split was made for
+    static std::atomic<int> regs_ok{-1};
+    int ok = regs_ok.load(std::memory_order_relaxed);
+    if (ok < 0) {
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return ATTN_ERR_UNSUPPORTED_DEVICE;
+        ok = (fa.numRegs == kLaunchRegs && fa.maxThreadsPerBlock >= kThreads) ? 1 : 0;
+        regs_ok.store(ok, std::memory_order_relaxed);
+    }
+    if (!ok || !set_smem_limit_once(reinterpret_cast<const void *>(kern), C::kSmem)) return ATTN_ERR_LAUNCH;
+    TcArgs args;
+    args.f = f;
+    args.timeout_ns = watchdog_ns();
+    // the whole of shared memory for any batch, so that one CTA runs on an SM: tensor
+    // memory has no room for two
+    kern<<<grid, kThreads, C::kSmem, stream>>>(args);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, (unsigned)((f.rows < R ? f.rows : R) + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_tc_merge_kernel<D>, f);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+// a: every field but the workspace's and the row blocks'.
+int launch_cache_tc(FwdArgs &a, int d, int format, void *workspace, cudaStream_t stream) {
+    a.nrb = (a.rows + R - 1) / R;
+    a.units = a.Hkv * a.nrb;
+    a.by_units = fast_div((uint32_t)a.units);
+    a.by_per = fast_div((uint32_t)a.nrb);
+    a.by_nrb = a.by_per;
+    const int sms = device_sm_count();
+    const double most = (double)a.B * a.units * (((double)a.max_pages * a.page + KT - 1) / KT);
+    int ctas = sms < kCacheMaxCtas ? sms : kCacheMaxCtas;
+    if (most < ctas) ctas = (int)most;
+    a.workers = ctas;
+    a.tail = reinterpret_cast<int4 *>(workspace);
+    a.po = reinterpret_cast<float *>(a.tail + ctas);
+    a.pl = a.po + (size_t)2 * ctas * R * d;
+    if (d == 64)
+        return format == ATTN_CACHE_E4M3 ? launch_t<64, ATTN_CACHE_E4M3>(a, (unsigned)ctas, stream)
+                                         : launch_t<64, ATTN_CACHE_I8>(a, (unsigned)ctas, stream);
+    return format == ATTN_CACHE_E4M3 ? launch_t<128, ATTN_CACHE_E4M3>(a, (unsigned)ctas, stream)
+                                     : launch_t<128, ATTN_CACHE_I8>(a, (unsigned)ctas, stream);
+}
+
+}  // namespace attn

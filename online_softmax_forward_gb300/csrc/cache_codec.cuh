@@ -17,6 +17,12 @@
 #include "attn.h"
 
 namespace attn {
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 namespace codec {
 
 // smallest power of two s >= 2^-126 with amax <= top * s; 0 for amax = 0,

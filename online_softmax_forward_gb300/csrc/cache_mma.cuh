@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "attn.h"
+#include "cache_codec.cuh"
 
 namespace attn {
 
@@ -18,11 +19,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // Codes as fp16 pairs, exact.  e4m3: one conversion a pair, as cheap as any
 // integer instruction (2 clocks a warp and SM quarter; moving the bits into place
 // by hand takes four).  int8: 0x6400 + u is the fp16 1024 + u, u = code + 128.

@@ -10,8 +10,8 @@ for equality.  Attention is compared within bounds made of
         of at most 128 exact products, in at most 16 fp32 additions of the
         partial sums (each off by at most 2^-23 of the running magnitude, which
         is at most a), and three fp32 products: e_s = 20 * 2^-23 * a;
-  p     weights exp2 (2^-22) kept in 22 bits, or in 11 in the 16-row form
-        (bf16 output, more than 8 query rows per kv head): e_p = 2^-21 + 2^-12;
+  p     weights exp2 (2^-22) kept in 22 bits, or in 11 (16-bit output, more than 8
+        query rows per kv head): e_p = 2^-21 + 2^-12;
   o     an average of v with weights off by 2 e_s + e_p (numerator and sum) in
         fp32 sums: (2 e_s + 2 e_p + 2^-18) * max|v|, plus half a step of the
         output type times |o| (bf16 2^-9.., as finfo.eps / 2);
@@ -233,7 +233,7 @@ def check_attention(q, c, t, lens, counts, causal, scale=None, out_dtype=None, p
     assert status() == pkg.ATTN_OK
     o_, lse_, a, vmax = ref.attention(f64(q), ref.snapshot(c), t, lens, counts, causal, scale, pages)
     es = 20 * 2.0 ** -23 * a
-    wide = q.shape[1] // c.H_kv * (q.shape[2] if pages is None else 1) > 8 and o.dtype == torch.bfloat16
+    wide = q.shape[1] // c.H_kv * (q.shape[2] if pages is None else 1) > 8 and o.dtype != torch.float32
     ep = 2.0 ** -21 + (2.0 ** -12 if wide else 0.0)
     err = np.abs(f64(o) - o_)
     bound = (2 * es + 2 * ep + 2.0 ** -18) * vmax + HALF[o.dtype] * np.abs(o_) * 1.01 + 2.0 ** -24
@@ -258,6 +258,10 @@ ATTEND = [
     ([257], [17], 17, 16, 1, 128, 128),                      # many rows, blocks of them
     ([130, 131], [40, 13], 40, 5, 1, 64, 128),
     ([129], [1], 1, 40, 1, 128, 32),                         # 40 heads on one
+    ([700, 0, 128, 129], [33, 0, 33, 9], 33, 8, 2, 128, 64), # more than 128 rows, an empty sequence
+    ([1100, 64], [20, 20], 20, 4, 2, 64, 16),                # 80 rows: a warp without one
+    ([385], [260], 260, 2, 2, 128, 128),                     # causal blocks that end early
+    ([50], [60], 60, 3, 1, 64, 32),                          # more queries than tokens
     ([2500], [3], 3, 3, 3, 64, 16),
 ]
 
