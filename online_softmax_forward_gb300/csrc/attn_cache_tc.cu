@@ -7,28 +7,30 @@
 // With 128 rows the products are no longer free, and one conversion of the codes
 // to fp16 serves all of them:
 //
-//   warps 9-11  copy the codes with cp.async into private buffers, three items
-//               (a tile's keys or values) ahead, convert them to fp16, exact, and
-//               write the MMA's 128-byte-swizzled tiles into a ring of stages;
+//   warps 9-12  load the codes of the keys and 13-15 those of the values, a tile
+//               ahead in registers, convert them to fp16, exact, and write the
+//               MMA's 128-byte-swizzled tiles into two rings of stages;
 //   warp 8      issues S_t = Q K_j^T and O_t += P_t V_j, t = j & 1;
 //   warps 0-3   softmax of the even tiles, 4-7 of the odd ones, a thread per row:
 //               S out of tensor memory, the pages' scales applied per 16 keys, P
 //               as fp16 over the first half of S_t.
 //
 // The two halves keep states of their own (top, rv, l and O_t, references moved
-// only when a tile would pass fp16's range, as in attn_cache_fwd.cu), so that one
-// exponentiates while the other's products run; they are joined when the unit
-// ends.  A warp without a real row (few drafts, few heads) only keeps step.  P in
+// only when a weight would pass 2^10 or fp16's range, as in attn_cache_fwd.cu), so
+// that one exponentiates while the other's products run; they are joined when the
+// unit ends.  The largest scores come with a first load of S (tcgen05.ld.red), so
+// that P can replace S step by step: two registers' worth of 32 keys are live at
+// a time and 16 warps fit the SM.  A warp without a real row (few drafts, few heads) only keeps step.  P in
 // fp16 is rounded by 2^-12, so this kernel serves the 16-bit outputs.
 //
 // Tensor memory (512 columns): S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 from
 // 256, O_1 from 256 + D.  S_t(j + 2) may be written once P_t(j) has been used: its
 // issue waits for that product.  Every wait is bounded, as in attn_tc.cu.
-#include <atomic>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "cache_fwd.cuh"
@@ -39,24 +41,26 @@
 namespace attn {
 namespace {
 
+__device__ __forceinline__ uint4 ldg16(const uint8_t *p) {
+    uint4 u;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+    return u;
+}
+
 constexpr int R = 128;   // rows of a unit
 constexpr int KT = 128;  // keys of a tile
 constexpr int kMmaWarp = 8;
-constexpr int kThreads = 12 * 32;
-constexpr int kConverters = 3;      // warps 9 .. 11
-constexpr int kAhead = 3;           // items whose copies are in flight
+constexpr int kThreads = 16 * 32;
+constexpr int kKeyWarps = 4, kValueWarps = 3;  // 9 .. 12, 13 .. 15
 constexpr int kScaleRing = 8;       // tiles whose page scales are kept
 constexpr uint32_t kTmemCols = 512;
-// Register split (setmaxnreg): launched with kLaunchRegs each; the softmax
-// warpgroups grow, the third shrinks; the totals match exactly.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
-static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs == kThreads * kLaunchRegs, "register split");
-constexpr float kLargest = 1024.f;  // of a tile's sum of weights; 32 * 1024 fits fp16
+constexpr float kLargest = 10.f;    // log2 of the largest weight; 32 * 2^10 fits fp16
 constexpr float kBase = 32.f;       // page scale times rv, at its largest after a move
 
 struct Bars {
     uint64_t q_full, q_empty;
-    uint64_t kv_full[6], kv_empty[6];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t o_empty, joined, mma_done;
     uint64_t sc_full[kScaleRing];
@@ -69,15 +73,15 @@ struct Cfg {
     static constexpr int kChunks = D / 64;
     static constexpr int kChunkBytes = 128 * 128;             // 64 channels of 128 rows, fp16
     static constexpr int kTile = kChunks * kChunkBytes;       // Q, K or V tile
-    static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kIters = KT * D / 512;               // 512-byte pieces of an item
-    static constexpr int kMine = (kIters + kConverters - 1) / kConverters;
-    static constexpr int kRawWarp = (kAhead + 1) * kMine * 512;
+    static constexpr int kKeyStages = D == 128 ? 2 : 4;
+    static constexpr int kValueStages = D == 128 ? 3 : 4;
+    static constexpr int kIters = KT * D / 512;               // 512-byte pieces of a tile's codes
     static constexpr int kOffQ = 0;
-    static constexpr int kOffKV = kTile;
-    static constexpr int kOffRaw = kOffKV + kStages * kTile;
-    static constexpr int kOffScale = kOffRaw + kConverters * kRawWarp;   // [ring][2][8] fp32
-    static constexpr int kOffState = kOffScale + kScaleRing * 16 * 4;    // [2][2][3][128] fp32
+    static constexpr int kOffK = kTile;
+    static constexpr int kOffV = kOffK + kKeyStages * kTile;
+    static constexpr int kOffScale = kOffV + kValueStages * kTile;       // [ring][2][8] fp32
+    static constexpr int kOffBack = kOffScale + kScaleRing * 16 * 4;     // [2][128] fp32
+    static constexpr int kOffState = kOffBack + 2 * R * 4;               // [2][2][3][128] fp32
     static constexpr int kOffBar = kOffState + 2 * 2 * 3 * R * 4;
     static constexpr int kOffPrefix = kOffBar + 512;
     static constexpr int kSmem = kOffPrefix + (kMaxCacheBatch + 1) * 4 + 1024;  // + alignment
@@ -108,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     Bars *bars = reinterpret_cast<Bars *>(sm + C::kOffBar);
     int *prefix = reinterpret_cast<int *>(sm + C::kOffPrefix);
     float *scales = reinterpret_cast<float *>(sm + C::kOffScale);
+    float *backs = reinterpret_cast<float *>(sm + C::kOffBack);
     float *state = reinterpret_cast<float *>(sm + C::kOffState);
     __shared__ int warp_sums[kThreads / 32];
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
@@ -117,11 +122,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (threadIdx.x == 0) {
-        ptx::mbar_init(bar(bars->q_full), 128);
+        ptx::mbar_init(bar(bars->q_full), 256);
         ptx::mbar_init(bar(bars->q_empty), 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(bar(bars->kv_full[s]), kConverters * 32);
-            ptx::mbar_init(bar(bars->kv_empty[s]), 1);
+        for (int s = 0; s < 4; ++s) {
+            ptx::mbar_init(bar(bars->k_full[s]), kKeyWarps * 32);
+            ptx::mbar_init(bar(bars->k_empty[s]), 1);
+            ptx::mbar_init(bar(bars->v_full[s]), kValueWarps * 32);
+            ptx::mbar_init(bar(bars->v_empty[s]), 1);
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(bar(bars->s_full[t]), 1);
@@ -176,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
-    const uint32_t sQ = ptx::smem_addr(sm + C::kOffQ), sKV = ptx::smem_addr(sm + C::kOffKV);
+    const uint32_t sQ = ptx::smem_addr(sm + C::kOffQ), sK = ptx::smem_addr(sm + C::kOffK);
+    const uint32_t sV = ptx::smem_addr(sm + C::kOffV);
 
     // the piece at `here` when `done` tiles of the range lie before it
     auto piece_at = [&](const Place &here, int done) {
@@ -195,37 +203,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         p.live = max(0, min(p.left, (int)(((int64_t)seen + KT - 1) / KT) - p.t0));
         return p;
     };
-    // item m of a piece with n live tiles, in the order of the products: K_0, K_1, V_0, K_2,
-    // V_1, ..., V_{n-2}, V_{n-1}
-    auto item = [](int m, int n, int &j) {
-        if (m == 0) {
-            j = 0;
-            return false;
-        }
-        j = (m + 1) / 2;
-        if ((m & 1) && j < n) return false;
-        j = (m & 1) ? n - 1 : (m - 2) / 2;
-        return true;
-    };
-
     if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
-        ptx::setmaxnreg_dec<kOtherRegs>();
         auto wait_all = [&](uint32_t b, uint32_t parity) {
             return __all_sync(0xffffffffu, watch.wait(b, parity));
         };
         constexpr uint32_t kIdescS = idesc_f16(false, R, KT, false);
         constexpr uint32_t kIdescO = idesc_f16(false, R, D, true);
-        const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(sKV, 16, 1024);
-        const uint64_t dv = sdesc(sKV, C::kChunkBytes, 1024);
-        uint32_t pos = 0, qn = 0, on = 0, pn[2] = {0, 0};
+        const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(sK, 16, 1024);
+        const uint64_t dv = sdesc(sV, C::kChunkBytes, 1024);
+        uint32_t kn = 0, vn = 0, qn = 0, on = 0, pn[2] = {0, 0};
         bool ok = true;
         Place here = start;
         for (int i = 0; i < n_tiles && ok;) {
             const Piece p = piece_at(here, i);
             auto issue_s = [&](int j) {
-                const int st = pos % C::kStages;
-                if (!wait_all(bar(bars->kv_full[st]), (pos / C::kStages) & 1)) return false;
+                const int st = kn % C::kKeyStages;
+                if (!wait_all(bar(bars->k_full[st]), (kn / C::kKeyStages) & 1)) return false;
                 ptx::tc_fence_after();
                 const uint64_t dkj = dk + (uint64_t)((st * C::kTile) >> 4);
 #pragma unroll
@@ -234,9 +228,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                     ptx::mma_ss_warp(tmem + (j & 1) * KT, dq + off, dkj + off, kIdescS, kk > 0 ? 1u : 0u);
                 }
                 ptx::mma_commit_warp(bar(bars->s_full[j & 1]));
-                ptx::mma_commit_warp(bar(bars->kv_empty[st]));
+                ptx::mma_commit_warp(bar(bars->k_empty[st]));
                 if (j == p.live - 1) ptx::mma_commit_warp(bar(bars->q_empty));
-                ++pos;
+                ++kn;
                 return true;
             };
             if (p.live > 0) {
@@ -247,9 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                 ok = ok && wait_all(bar(bars->o_empty), (on & 1) ^ 1);
                 ++on;
                 for (int j = 0; j < p.live && ok; ++j) {
-                    const int t = j & 1, st = pos % C::kStages;
-                    ok = wait_all(bar(bars->p_full[t]), pn[t] & 1) &&
-                         wait_all(bar(bars->kv_full[st]), (pos / C::kStages) & 1);
+                    const int t = j & 1, st = vn % C::kValueStages;
+                    ok = wait_all(bar(bars->v_full[st]), (vn / C::kValueStages) & 1) &&
+                         wait_all(bar(bars->p_full[t]), pn[t] & 1);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint64_t dvj = dv + (uint64_t)((st * C::kTile) >> 4);
@@ -259,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                                          dvj + (uint64_t)((kk * 16 * 128) >> 4), kIdescO,
                                          (j > 1 || kk > 0) ? 1u : 0u);
                     ptx::mma_commit_warp(bar(bars->pv_done[t]));
-                    ptx::mma_commit_warp(bar(bars->kv_empty[st]));
-                    ++pos;
+                    ptx::mma_commit_warp(bar(bars->v_empty[st]));
+                    ++vn;
                     if (j + 2 < p.live)  // S_t takes P_t's place
                         ok = wait_all(bar(bars->pv_done[t]), pn[t] & 1) && issue_s(j + 2);
                     ++pn[t];
@@ -275,154 +269,129 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         __syncwarp();
     } else if (warp > kMmaWarp) {
         // ------------------------------------------------------------ converters
-        ptx::setmaxnreg_dec<kOtherRegs>();
-        const int cw = warp - kMmaWarp - 1;
-        uint8_t *raw = sm + C::kOffRaw + cw * C::kRawWarp + lane * 16;
-        const uint32_t raw_at = ptx::smem_addr(raw);
-        const int page16 = a.page / 16;
-        // row and 16-byte piece of a lane in a 512-byte copy: for d = 128 the two
+        const int page_shift = 31 - __clz(a.page);
+        // row and 16-byte piece of a lane in a 512-byte load: for d = 128 the two
         // halves of a row are not written in the same quarter of the warp, whose
         // lanes would meet in the same banks
         const int rl = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
         const int ql = D == 128 ? (lane & 3) + ((lane >> 3) & 1) * 4 : lane & 3;
-        const int src_off = rl * D + ql * 16;
         constexpr int kRowsIter = 512 / D;
+        const uint32_t p0 = (ql & 3) * 2;
 
-        // The items to copy run kAhead ahead of the ones to convert; both walk the pieces.
-        struct Cursor {
-            Place here;
-            int i, m, slot;  // tiles of the range before the piece, item of it, tiles before (mod ring)
-        };
-        Cursor in = {start, 0, 0, 0}, out = in;
-        Piece pi, po;
-        // to the first piece from the cursor on that has a live tile
-        auto settle = [&](Cursor &c, Piece &p) {
-            while (c.i < n_tiles) {
-                p = piece_at(c.here, c.i);
-                if (p.live > 0) return;
-                c.i += p.left;
-                if (c.i < n_tiles) advance(c.here, p.left, a.units, tiles);
-            }
-        };
-        auto step = [&](Cursor &c, Piece &p) {
-            if (++c.m < 2 * p.live) return;
-            c.m = 0;
-            c.slot = (c.slot + p.live) % kScaleRing;
-            c.i += p.left;
-            if (c.i < n_tiles) advance(c.here, p.left, a.units, tiles);
-            settle(c, p);
-        };
-        // lane s < 8: 16-key piece s of the item's tile as a 16-row piece of the pool, -1: none
-        auto find = [&](const Cursor &c, const Piece &p) {
-            int at = -1;
-            if (c.i < n_tiles && lane < 8) {
-                int j;
-                item(c.m, p.live, j);
+        // NW warps, this one cw, take every NW-th 512-byte piece of a tile
+        auto convert = [&](auto values, auto warps, int cw) {
+            constexpr bool V = decltype(values)::value;
+            constexpr int NW = decltype(warps)::value;
+            constexpr int N = (C::kIters + NW - 1) / NW;
+            constexpr int kStages = V ? C::kValueStages : C::kKeyStages;
+            const uint8_t *base = (V ? a.v : a.k) + rl * D + ql * 16;
+            const uint32_t to = (V ? sV : sK) + (ql >> 2) * C::kChunkBytes;
+            // the next tile to load: its piece and place in it
+            Place here = start;
+            Piece p;
+            int i = 0, j = 0, slot = 0;
+            auto settle = [&] {  // to the first piece from here on that has a live tile
+                while (i < n_tiles) {
+                    p = piece_at(here, i);
+                    if (p.live > 0) return;
+                    i += p.left;
+                    if (i < n_tiles) advance(here, p.left, a.units, tiles);
+                }
+            };
+            // lane s < 8: 16-key piece s of the tile as a 16-row piece of the pool, -1: none
+            auto find = [&] {
+                int at = -1;
                 const int key = (p.t0 + j) * KT + lane * 16;
-                if (key < p.len) {
-                    const int lp = key / a.page;
-                    const int phys = a.table[(int64_t)p.u.b * a.max_pages + lp];
+                if (i < n_tiles && lane < 8 && key < p.len) {
+                    const int phys = a.table[(int64_t)p.u.b * a.max_pages + (key >> page_shift)];
                     if (phys < 0 || phys >= a.n_pages) atomicOr(a.status, kStatusTable);
-                    else at = (phys * a.Hkv + p.u.hk) * page16 + (key - lp * a.page) / 16;
+                    else at = (((phys * a.Hkv + p.u.hk) << page_shift) + (key & (a.page - 1))) >> 4;
                 }
-            }
-            return at;
-        };
-        settle(in, pi);
-        settle(out, po);
-        int next_at = find(in, pi);
-        int buf_in = 0, buf_out = 0;
-        uint32_t missing = 0;  // 8 bits for each buffer: its item's pieces that are not there
-        // the copies of the item at `in`
-        auto issue = [&] {
-            if (in.i < n_tiles) {
-                const int at = next_at;
-                int j;
-                const bool is_v = item(in.m, pi.live, j);
-                missing = (missing & ~(0xffu << (8 * buf_in))) |
-                          (__ballot_sync(0xffffffffu, lane < 8 && at < 0) & 0xffu) << (8 * buf_in);
-                const uint8_t *src = (is_v ? a.v : a.k) + src_off;
-#pragma unroll
-                for (int e = 0; e < C::kMine; ++e) {
-                    const int it = cw + e * kConverters;
-                    const int row = it * kRowsIter;
-                    const int seg = __shfl_sync(0xffffffffu, at, (row >> 4) & 7);
-                    if (it < C::kIters && seg >= 0)
-                        cp_async16(raw_at + (buf_in * C::kMine + e) * 512,
-                                   src + (size_t)seg * 16 * D + (row & 15) * D);
-                }
-                if (!is_v && cw == 0) {
-                    // the tile's scales: lanes 0-7 of the keys, 8-15 of the values; an infinite
-                    // key scale marks a piece that is not there
+                return at;
+            };
+            settle();
+            int at = find();
+            uint4 raw[N];
+            float scale = 0.f;   // lanes 0-7: of the tile's keys, 8-15: of its values
+            uint32_t miss = 0;   // pieces of the tile that are not there
+            int key0 = 0, len = 0, ring = 0;
+            bool have = false;
+            uint32_t n = 0;
+            // loads what belongs to the tile at (p, j), piece e of it
+            auto load = [&](int e) {
+                const int it = cw + e * NW, row = it * kRowsIter;
+                const int seg = __shfl_sync(0xffffffffu, at, (row >> 4) & 7);
+                if (it < C::kIters && seg >= 0)
+                    raw[e] = ldg16(base + (size_t)seg * 16 * D + (row & 15) * D);
+            };
+            // moves on: what was just loaded becomes the tile to convert
+            auto take = [&] {
+                have = i < n_tiles;
+                miss = __ballot_sync(0xffffffffu, lane < 8 && at < 0) & 0xffu;
+                if (!V && cw == 0) {
                     const int seg = __shfl_sync(0xffffffffu, at, lane & 7);
-                    float *dst = scales + ((in.slot + j) % kScaleRing) * 16 + lane;
-                    if (lane < 16) {
-                        if (seg >= 0) {
-                            const float *s = (lane < 8 ? a.ks : a.vs) + seg / page16;
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_addr(dst)), "l"(s) : "memory");
-                        } else {
-                            *dst = lane < 8 ? INFINITY : 0.f;
-                        }
-                    }
+                    // an infinite key scale marks a piece that is not there
+                    scale = lane < 8 ? INFINITY : 0.f;
+                    if (have && lane < 16 && seg >= 0) scale = (lane < 8 ? a.ks : a.vs)[seg >> (page_shift - 4)];
                 }
-                step(in, pi);
-                next_at = find(in, pi);
-                buf_in = buf_in == kAhead ? 0 : buf_in + 1;
-            }
-            cp_async_commit();
-        };
-#pragma unroll 1
-        for (int k = 0; k < kAhead; ++k) issue();
-        uint32_t pos = 0;
-        while (out.i < n_tiles) {
-            issue();
-            cp_async_wait<kAhead>();
-            int j;
-            const bool is_v = item(out.m, po.live, j);
-            const int key0 = (po.t0 + j) * KT;
-            if (!is_v && cw == 0) {
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(bars->sc_full[(out.slot + j) % kScaleRing]));
-            }
-            const int st = pos % C::kStages;
-            if (!__all_sync(0xffffffffu, watch.wait(bar(bars->kv_empty[st]), ((pos / C::kStages) & 1) ^ 1))) break;
-            const uint32_t dst = sKV + st * C::kTile;
-            // pieces of the tile that are not there hold no values (as behind the last token)
-            const int seen = is_v ? po.len - key0 : KT;
-            const uint32_t miss = missing >> (8 * buf_out);
+                if (!have) return;
+                key0 = (p.t0 + j) * KT;
+                len = p.len;
+                ring = (slot + j) % kScaleRing;
+                if (++j == p.live) {
+                    slot = (slot + p.live) % kScaleRing;
+                    j = 0;
+                    i += p.left;
+                    if (i < n_tiles) advance(here, p.left, a.units, tiles);
+                    settle();
+                }
+                at = find();
+            };
 #pragma unroll
-            for (int e = 0; e < C::kMine; ++e) {
-                const int it = cw + e * kConverters;
-                if (it < C::kIters) {
-                    const int row = it * kRowsIter + rl;
-                    uint4 c = *reinterpret_cast<const uint4 *>(raw + (buf_out * C::kMine + e) * 512);
-                    const bool gone = is_v && (row >= seen || (miss >> (row >> 4 & 7) & 1));
+            for (int e = 0; e < N; ++e) load(e);
+            take();
+            while (have) {
+                const int st = n % kStages;
+                if (!__all_sync(0xffffffffu, watch.wait(bar(V ? bars->v_empty[st] : bars->k_empty[st]), ((n / kStages) & 1) ^ 1))) break;
+                if (!V && cw == 0) {
+                    if (lane < 16) scales[ring * 16 + lane] = scale;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(bars->sc_full[ring]));
+                }
+                const int held = len - key0;
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const int it = cw + e * NW, row = it * kRowsIter + rl;
                     uint32_t h[8];
-                    U::quad(c.x, h[0], h[1]);
-                    U::quad(c.y, h[2], h[3]);
-                    U::quad(c.z, h[4], h[5]);
-                    U::quad(c.w, h[6], h[7]);
-                    if (gone) {
+                    U::quad(raw[e].x, h[0], h[1]);
+                    U::quad(raw[e].y, h[2], h[3]);
+                    U::quad(raw[e].z, h[4], h[5]);
+                    U::quad(raw[e].w, h[6], h[7]);
+                    load(e);
+                    // behind the last token, or without a page: no values
+                    if (V && (row >= held || (miss >> (row >> 4 & 7) & 1))) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k) h[k] = 0;
                     }
-                    const uint32_t line = dst + (ql >> 2) * C::kChunkBytes + row * 128;
-                    const uint32_t p0 = (ql & 3) * 2;
-                    ptx::st_shared_v4(line + ((p0 ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-                    ptx::st_shared_v4(line + (((p0 + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
+                    if (it < C::kIters) {
+                        const uint32_t line = to + st * C::kTile + row * 128;
+                        ptx::st_shared_v4(line + ((p0 ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                        ptx::st_shared_v4(line + (((p0 + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
+                    }
                 }
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive(bar(V ? bars->v_full[st] : bars->k_full[st]));
+                ++n;
+                take();
             }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(bar(bars->kv_full[st]));
-            ++pos;
-            buf_out = buf_out == kAhead ? 0 : buf_out + 1;
-            step(out, po);
-        }
-        cp_async_wait<0>();
+        };
+        if (warp <= kMmaWarp + kKeyWarps)
+            convert(std::false_type{}, std::integral_constant<int, kKeyWarps>{}, warp - kMmaWarp - 1);
+        else
+            convert(std::true_type{}, std::integral_constant<int, kValueWarps>{}, warp - kMmaWarp - kKeyWarps - 1);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        ptx::setmaxnreg_inc<kSoftmaxRegs>();
         const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
         const uint32_t tS = tmem + lanes + t * KT, tO = tmem + lanes + 256 + t * D;
@@ -440,44 +409,49 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             const size_t at = real ? (((size_t)p.u.b * a.Hkv * a.G + h) * a.Sq + qi) * D : 0;
             float cq = 0.f;
             if (p.live > 0) {
-                // the row's power of two; the first warpgroup writes the row as fp16
-                float amax = 0.f;
-                if (real) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float f[32];
-                        load_q<32>(a, at + c, f);
+                // Q: warp w of the eight takes rows 16 w .. 16 w + 15, D / 8 lanes a row, all
+                // loaded before the first is used
+                constexpr int LR = D / 8, PW = 32 / LR;  // lanes of a row, rows of a load
+                float *back = backs + (qn & 1) * R;
+                codec::Raw8<1> q[16 / PW];  // 16-bit of either type
+                const int sub = lane / LR, piece = lane % LR;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(f[e]));
-                    }
+                for (int e = 0; e < 16 / PW; ++e) {
+                    int ri, rh;
+                    q[e].u[0] = make_uint4(0, 0, 0, 0);
+                    if (row_of<R>(a, p.u, warp * 16 + e * PW + sub, ri, rh))
+                        q[e].load(a.q, (((size_t)p.u.b * a.Hkv * a.G + rh) * a.Sq + ri) * D + piece * 8);
                 }
-                float mul, back;
-                row_power(amax, mul, back);
-                cq = a.sl2 * back;
-                if (t == 0) {
-                    if (!__all_sync(0xffffffffu, watch.wait(bar(bars->q_empty), (qn & 1) ^ 1))) break;
-                    ++qn;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float f[32];
-                        if (real) {
-                            load_q<32>(a, at + c, f);
-                        } else {
+                if (!__all_sync(0xffffffffu, watch.wait(bar(bars->q_empty), (qn & 1) ^ 1))) break;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) f[e] = 0.f;
-                        }
-                        const uint32_t line = sQ + (c >> 6) * C::kChunkBytes + r * 128;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) w[k] = pack_f16(f[8 * e + 2 * k] * mul, f[8 * e + 2 * k + 1] * mul);
-                            ptx::st_shared_v4(line + ((uint32_t)((((c & 63) >> 3) + e) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-                        }
+                for (int e = 0; e < 16 / PW; ++e) {
+                    float f[8];
+                    if (a.dtype == ATTN_BF16) {
+                        q[e].widen(f);
+                    } else {
+                        codec::Raw8<2> x;
+                        x.u[0] = q[e].u[0];
+                        x.widen(f);
                     }
-                    ptx::fence_proxy_async_smem();
-                    ptx::mbar_arrive(bar(bars->q_full));
+                    float amax = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+#pragma unroll
+                    for (int o = 1; o < LR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    float mul, inv;
+                    row_power(amax, mul, inv);
+                    const int row = warp * 16 + e * PW + sub;
+                    if (piece == 0) back[row] = inv;
+                    ptx::st_shared_v4(sQ + (piece >> 3) * C::kChunkBytes + row * 128 +
+                                          ((uint32_t)((piece & 7) ^ (row & 7)) << 4),
+                                      pack_f16(f[0] * mul, f[1] * mul), pack_f16(f[2] * mul, f[3] * mul),
+                                      pack_f16(f[4] * mul, f[5] * mul), pack_f16(f[6] * mul, f[7] * mul));
                 }
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive(bar(bars->q_full));
+                if (!__all_sync(0xffffffffu, watch.wait(bar(bars->q_full), qn & 1))) break;
+                ++qn;
+                cq = a.sl2 * back[r];
             }
             float top = kUnset, rv = 0x1p100f, l = 0.f;
             for (int j = t; j < p.live; j += 2) {
@@ -497,49 +471,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
 #pragma unroll
                     for (int s = 0; s < 8; ++s) hole = hole || ks[s] == INFINITY;
                     const bool edge = __any_sync(0xffffffffu, hole || key0 + KT > lim);
-                    uint32_t pk[64];
-                    float sum = 0.f;
-                    bool moved = false;
-                    while (true) {
-                        bool far = false;
-                        sum = 0.f;
+                    // the largest score of each 16 keys, from the load that reduces, and of the
+                    // visible ones in software where some are not
+                    float high = -INFINITY, most = 0.f;
+                    bool far = false;
+                    auto look = [&](int seg, float m) {
+                        if (m == -INFINITY) return;  // nothing visible
+                        const float v = vs[seg];
+                        m *= ks[seg] * cq;
+                        high = fmaxf(high, m);
+                        most = fmaxf(most, v);
+                        far = far || m - top > kLargest || ptx::ex2_approx(m - top) * (v * rv) > kBase * 1024.f;
+                    };
+                    if (!edge) {
+#pragma unroll 1
+                        for (int c = 0; c < 8; c += 4) {
+                            uint32_t d[4][16];
+                            float mx[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {  // 32 keys
-                            uint32_t s32[32];
-                            ptx::tmem_ld32(tS + c * 32, s32);
+                            for (int s = 0; s < 4; ++s) ptx::tmem_ld16_max(tS + (c + s) * 16, d[s], mx[s]);
                             ptx::tmem_wait_ld();
-                            reg_fence(s32);
 #pragma unroll
-                            for (int s = 0; s < 2; ++s) {  // of one page
-                                const int seg = c * 2 + s;
-                                const float f = ks[seg] * cq;
-                                // a page no key of which the row sees adds nothing, not even its
-                                // scale's NaN
-                                const float cv = key0 + seg * 16 < lim ? vs[seg] * rv : 0.f;
-                                float part = 0.f;
+                            for (int s = 0; s < 4; ++s) asm volatile("" : "+f"(mx[s]));
 #pragma unroll
-                                for (int e = 0; e < 16; e += 2) {
-                                    float z0 = fmaf(__uint_as_float(s32[s * 16 + e]), f, -top);
-                                    float z1 = fmaf(__uint_as_float(s32[s * 16 + e + 1]), f, -top);
-                                    if (edge) {
-                                        const int key = key0 + seg * 16 + e;
-                                        const bool gone = ks[seg] == INFINITY;
-                                        if (gone || key >= lim) z0 = -INFINITY;
-                                        if (gone || key + 1 >= lim) z1 = -INFINITY;
-                                    }
-                                    const float p0 = ptx::ex2_approx(z0), p1 = ptx::ex2_approx(z1);
-                                    part += p0 + p1;
-                                    pk[seg * 8 + e / 2] = pack_f16(p0 * cv, p1 * cv);
-                                }
-                                far = far || part > kLargest || part * cv > kLargest * kBase;
-                                sum += part;
-                            }
+                            for (int s = 0; s < 4; ++s) look(c + s, mx[s]);
                         }
-                        if (moved || !__any_sync(0xffffffffu, far)) break;
-                        moved = true;
-                        // new references: the scores' maximum, and the page scales unless what O
-                        // holds is larger by now
-                        float mx = -INFINITY, most = 0.f;
+                    } else {
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t s32[32];
@@ -549,24 +506,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                             reg_fence(s32);
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
-                                const int seg = c * 2 + s;
-                                const bool gone = ks[seg] == INFINITY;
-                                const float f = ks[seg] * cq;
-                                if (!gone && key0 + seg * 16 < lim) most = fmaxf(most, vs[seg]);
+                                const int n = ks[c * 2 + s] == INFINITY ? 0 : lim - (key0 + (c * 2 + s) * 16);
+                                float m = -INFINITY;
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
-                                    if (!gone && key0 + seg * 16 + e < lim)
-                                        mx = fmaxf(mx, __uint_as_float(s32[s * 16 + e]) * f);
+                                    if (e < n) m = fmaxf(m, __uint_as_float(s32[s * 16 + e]));
+                                look(c * 2 + s, m);
                             }
                         }
-                        const float nt = fmaxf(top, mx);
+                    }
+                    __syncwarp();
+                    if (__any_sync(0xffffffffu, far)) {
+                        // new references: the scores' maximum, and the page scales unless what O
+                        // holds is larger by now
+                        const float nt = fmaxf(top, high);
                         const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
                         const float was = alpha * kBase / rv;
-                        const float nv = mx == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, most), 0x1p-95f);
+                        const float nv = high == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, most), 0x1p-95f);
                         const float to = alpha * (nv / rv);
                         l *= alpha;
                         top = nt;
                         rv = nv;
+                        __syncwarp();
                         if (j > 1) {  // O_t holds the tiles before: S(j) came after their products
 #pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
@@ -581,15 +542,38 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                             }
                         }
                     }
+                    // P of 32 keys takes 16 columns of S_t, all of them read before
+                    float sum = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t s32[32], pk[16];
+                        ptx::tmem_ld32(tS + c * 32, s32);
+                        ptx::tmem_wait_ld();
+                        reg_fence(s32);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {  // of one page
+                            const int seg = c * 2 + s;
+                            const float f = ks[seg] * cq;
+                            const int n = edge ? (ks[seg] == INFINITY ? 0 : lim - (key0 + seg * 16)) : 16;
+                            // a page no key of which the row sees adds nothing, not even its
+                            // scale's NaN
+                            const float cv = n > 0 ? vs[seg] * rv : 0.f;
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                float z0 = fmaf(__uint_as_float(s32[s * 16 + e]), f, -top);
+                                float z1 = fmaf(__uint_as_float(s32[s * 16 + e + 1]), f, -top);
+                                if (edge) {
+                                    if (e >= n) z0 = -INFINITY;
+                                    if (e + 1 >= n) z1 = -INFINITY;
+                                }
+                                const float w0 = ptx::ex2_approx(z0), w1 = ptx::ex2_approx(z1);
+                                sum += w0 + w1;
+                                pk[s * 8 + e / 2] = pack_f16(w0 * cv, w1 * cv);
+                            }
+                        }
+                        ptx::tmem_st16(tS + c * 16, pk);
+                    }
                     l += sum;
-                    // P over S_t's first columns, all of which this warp has read
-                    uint32_t w[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) w[e] = pk[e];
-                    ptx::tmem_st32(tS, w);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) w[e] = pk[32 + e];
-                    ptx::tmem_st32(tS + 32, w);
                     ptx::tmem_wait_st();
                 }
                 ptx::tc_fence_before();
@@ -724,16 +708,7 @@ template <int D, int FMT>
 int launch_t(const FwdArgs &f, unsigned grid, cudaStream_t stream) {
     using C = Cfg<D>;
     auto kern = cache_tc_kernel<D, FMT>;
-    // setmaxnreg needs exactly the register pool the split was made for
-    static std::atomic<int> regs_ok{-1};
-    int ok = regs_ok.load(std::memory_order_relaxed);
-    if (ok < 0) {
-        cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return ATTN_ERR_UNSUPPORTED_DEVICE;
-        ok = (fa.numRegs == kLaunchRegs && fa.maxThreadsPerBlock >= kThreads) ? 1 : 0;
-        regs_ok.store(ok, std::memory_order_relaxed);
-    }
-    if (!ok || !set_smem_limit_once(reinterpret_cast<const void *>(kern), C::kSmem)) return ATTN_ERR_LAUNCH;
+    if (!set_smem_limit_once(reinterpret_cast<const void *>(kern), C::kSmem)) return ATTN_ERR_LAUNCH;
     TcArgs args;
     args.f = f;
     args.timeout_ns = watchdog_ns();
