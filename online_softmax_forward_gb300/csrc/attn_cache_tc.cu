@@ -7,13 +7,16 @@
 // With 128 rows the products are no longer free, and one conversion of the codes
 // to fp16 serves all of them:
 //
-//   warps 9-12  load the codes of the keys and 13-15 those of the values, a tile
+//   warps 8-11  load the codes of the keys and 12-15 those of the values, a tile
 //               ahead in registers, convert them to fp16, exact, and write the
-//               MMA's 128-byte-swizzled tiles into two rings of stages;
-//   warp 8      issues S_t = Q K_j^T and O_t += P_t V_j, t = j & 1;
-//   warps 0-3   softmax of the even tiles, 4-7 of the odd ones, a thread per row:
-//               S out of tensor memory, the pages' scales applied per 16 keys, P
-//               as fp16 over the first half of S_t.
+//               MMA's 128-byte-swizzled tiles into two rings of stages (four warps
+//               each: a lane's rows are then 16 apart, and every address of a tile
+//               is one base and a constant);
+//   warps 0-3   softmax of the even tiles (t = 0), 4-7 of the odd ones (t = 1), a
+//               thread per row: S_t out of tensor memory, the pages' scales
+//               applied per 16 keys, P_t as fp16 over the first half of S_t.  The
+//               first warp of each four issues its half's products, S_t = Q K_j^T
+//               and O_t += P_t V_j.
 //
 // The two halves keep states of their own (top, rv, l and O_t, references moved
 // only when a weight would pass 2^10 or fp16's range, as in attn_cache_fwd.cu), so
@@ -30,7 +33,6 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
-#include <type_traits>
 
 #include "attn_internal.h"
 #include "cache_fwd.cuh"
@@ -50,9 +52,8 @@ __device__ __forceinline__ uint4 ldg16(const uint8_t *p) {
 
 constexpr int R = 128;   // rows of a unit
 constexpr int KT = 128;  // keys of a tile
-constexpr int kMmaWarp = 8;
+constexpr int kConvertWarp0 = 8;  // 8 .. 11 keys, 12 .. 15 values
 constexpr int kThreads = 16 * 32;
-constexpr int kKeyWarps = 4, kValueWarps = 3;  // 9 .. 12, 13 .. 15
 constexpr int kScaleRing = 8;       // tiles whose page scales are kept
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLargest = 10.f;    // log2 of the largest weight; 32 * 2^10 fits fp16
@@ -62,7 +63,7 @@ struct Bars {
     uint64_t q_full, q_empty;
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
     uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t o_empty, joined, mma_done;
+    uint64_t o_empty, joined, mma_done[2];
     uint64_t sc_full[kScaleRing];
     uint32_t tmem_base;
     int abort_flag;
@@ -75,7 +76,6 @@ struct Cfg {
     static constexpr int kTile = kChunks * kChunkBytes;       // Q, K or V tile
     static constexpr int kKeyStages = D == 128 ? 2 : 4;
     static constexpr int kValueStages = D == 128 ? 3 : 4;
-    static constexpr int kIters = KT * D / 512;               // 512-byte pieces of a tile's codes
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kTile;
     static constexpr int kOffV = kOffK + kKeyStages * kTile;
@@ -123,26 +123,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(bars->q_full), 256);
-        ptx::mbar_init(bar(bars->q_empty), 1);
+        ptx::mbar_init(bar(bars->q_empty), 2);
         for (int s = 0; s < 4; ++s) {
-            ptx::mbar_init(bar(bars->k_full[s]), kKeyWarps * 32);
+            ptx::mbar_init(bar(bars->k_full[s]), 128);
             ptx::mbar_init(bar(bars->k_empty[s]), 1);
-            ptx::mbar_init(bar(bars->v_full[s]), kValueWarps * 32);
+            ptx::mbar_init(bar(bars->v_full[s]), 128);
             ptx::mbar_init(bar(bars->v_empty[s]), 1);
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(bar(bars->s_full[t]), 1);
             ptx::mbar_init(bar(bars->p_full[t]), 128);
             ptx::mbar_init(bar(bars->pv_done[t]), 1);
+            ptx::mbar_init(bar(bars->mma_done[t]), 1);
         }
         ptx::mbar_init(bar(bars->o_empty), 256);
         ptx::mbar_init(bar(bars->joined), 256);
-        ptx::mbar_init(bar(bars->mma_done), 1);
         for (int s = 0; s < kScaleRing; ++s) ptx::mbar_init(bar(bars->sc_full[s]), 1);
         bars->abort_flag = 0;
         ptx::fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == 0) {
         ptx::tmem_alloc(ptx::smem_addr(&bars->tmem_base), kTmemCols);
         ptx::tmem_relinquish();
     }
@@ -203,192 +203,124 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         p.live = max(0, min(p.left, (int)(((int64_t)seen + KT - 1) / KT) - p.t0));
         return p;
     };
-    if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issuer
-        auto wait_all = [&](uint32_t b, uint32_t parity) {
-            return __all_sync(0xffffffffu, watch.wait(b, parity));
-        };
-        constexpr uint32_t kIdescS = idesc_f16(false, R, KT, false);
-        constexpr uint32_t kIdescO = idesc_f16(false, R, D, true);
-        const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(sK, 16, 1024);
-        const uint64_t dv = sdesc(sV, C::kChunkBytes, 1024);
-        uint32_t kn = 0, vn = 0, qn = 0, on = 0, pn[2] = {0, 0};
-        bool ok = true;
-        Place here = start;
-        for (int i = 0; i < n_tiles && ok;) {
-            const Piece p = piece_at(here, i);
-            auto issue_s = [&](int j) {
-                const int st = kn % C::kKeyStages;
-                if (!wait_all(bar(bars->k_full[st]), (kn / C::kKeyStages) & 1)) return false;
-                ptx::tc_fence_after();
-                const uint64_t dkj = dk + (uint64_t)((st * C::kTile) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
-                    ptx::mma_ss_warp(tmem + (j & 1) * KT, dq + off, dkj + off, kIdescS, kk > 0 ? 1u : 0u);
-                }
-                ptx::mma_commit_warp(bar(bars->s_full[j & 1]));
-                ptx::mma_commit_warp(bar(bars->k_empty[st]));
-                if (j == p.live - 1) ptx::mma_commit_warp(bar(bars->q_empty));
-                ++kn;
-                return true;
-            };
-            if (p.live > 0) {
-                ok = wait_all(bar(bars->q_full), qn & 1);
-                ++qn;
-                ok = ok && issue_s(0) && (p.live < 2 || issue_s(1));
-                // the epilogue of the last unit has read both O
-                ok = ok && wait_all(bar(bars->o_empty), (on & 1) ^ 1);
-                ++on;
-                for (int j = 0; j < p.live && ok; ++j) {
-                    const int t = j & 1, st = vn % C::kValueStages;
-                    ok = wait_all(bar(bars->v_full[st]), (vn / C::kValueStages) & 1) &&
-                         wait_all(bar(bars->p_full[t]), pn[t] & 1);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint64_t dvj = dv + (uint64_t)((st * C::kTile) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < KT / 16; ++kk)
-                        ptx::mma_ts_warp(tmem + 256 + t * D, tmem + t * KT + kk * 8,
-                                         dvj + (uint64_t)((kk * 16 * 128) >> 4), kIdescO,
-                                         (j > 1 || kk > 0) ? 1u : 0u);
-                    ptx::mma_commit_warp(bar(bars->pv_done[t]));
-                    ptx::mma_commit_warp(bar(bars->v_empty[st]));
-                    ++vn;
-                    if (j + 2 < p.live)  // S_t takes P_t's place
-                        ok = wait_all(bar(bars->pv_done[t]), pn[t] & 1) && issue_s(j + 2);
-                    ++pn[t];
-                }
-            }
-            i += p.left;
-            if (i < n_tiles) advance(here, p.left, a.units, tiles);
-        }
-        // every MMA issued by this warp has completed before tensor memory is freed
-        ptx::mma_commit_warp(bar(bars->mma_done));
-        watch.drain(bar(bars->mma_done), 0);
-        __syncwarp();
-    } else if (warp > kMmaWarp) {
+    if (warp >= kConvertWarp0) {
         // ------------------------------------------------------------ converters
+        const bool values = warp >= kConvertWarp0 + 4;
+        const int cw = warp & 3;
         const int page_shift = 31 - __clz(a.page);
-        // row and 16-byte piece of a lane in a 512-byte load: for d = 128 the two
-        // halves of a row are not written in the same quarter of the warp, whose
-        // lanes would meet in the same banks
-        const int rl = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
+        // A warp's load covers 512 bytes: kRows rows of the tile, rows 4 kRows apart from load to
+        // load.  Row and 16-byte piece of a lane: for d = 128 the two halves of a row are not
+        // written in the same quarter of the warp, whose lanes would meet in the same banks
+        constexpr int kRows = 512 / D, N = KT / (4 * kRows);
+        const int rl = (D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2) + cw * kRows;
         const int ql = D == 128 ? (lane & 3) + ((lane >> 3) & 1) * 4 : lane & 3;
-        constexpr int kRowsIter = 512 / D;
-        const uint32_t p0 = (ql & 3) * 2;
+        const uint8_t *src = (values ? a.v : a.k) + (rl & 15) * D + ql * 16;
+        const uint32_t line = (values ? sV : sK) + (ql >> 2) * C::kChunkBytes + rl * 128;
+        const uint32_t to0 = line + (((ql & 3) * 2 ^ (rl & 7)) << 4);
+        const uint32_t to1 = line + (((ql & 3) * 2 + 1 ^ (rl & 7)) << 4);
+        uint64_t *full = values ? bars->v_full : bars->k_full;
+        uint64_t *empty = values ? bars->v_empty : bars->k_empty;
+        const uint32_t stages = values ? C::kValueStages : C::kKeyStages;
 
-        // NW warps, this one cw, take every NW-th 512-byte piece of a tile
-        auto convert = [&](auto values, auto warps, int cw) {
-            constexpr bool V = decltype(values)::value;
-            constexpr int NW = decltype(warps)::value;
-            constexpr int N = (C::kIters + NW - 1) / NW;
-            constexpr int kStages = V ? C::kValueStages : C::kKeyStages;
-            const uint8_t *base = (V ? a.v : a.k) + rl * D + ql * 16;
-            const uint32_t to = (V ? sV : sK) + (ql >> 2) * C::kChunkBytes;
-            // the next tile to load: its piece and place in it
-            Place here = start;
-            Piece p;
-            int i = 0, j = 0, slot = 0;
-            auto settle = [&] {  // to the first piece from here on that has a live tile
-                while (i < n_tiles) {
-                    p = piece_at(here, i);
-                    if (p.live > 0) return;
-                    i += p.left;
-                    if (i < n_tiles) advance(here, p.left, a.units, tiles);
-                }
-            };
-            // lane s < 8: 16-key piece s of the tile as a 16-row piece of the pool, -1: none
-            auto find = [&] {
-                int at = -1;
-                const int key = (p.t0 + j) * KT + lane * 16;
-                if (i < n_tiles && lane < 8 && key < p.len) {
-                    const int phys = a.table[(int64_t)p.u.b * a.max_pages + (key >> page_shift)];
-                    if (phys < 0 || phys >= a.n_pages) atomicOr(a.status, kStatusTable);
-                    else at = (((phys * a.Hkv + p.u.hk) << page_shift) + (key & (a.page - 1))) >> 4;
-                }
-                return at;
-            };
-            settle();
-            int at = find();
-            uint4 raw[N];
-            float scale = 0.f;   // lanes 0-7: of the tile's keys, 8-15: of its values
-            uint32_t miss = 0;   // pieces of the tile that are not there
-            int key0 = 0, len = 0, ring = 0;
-            bool have = false;
-            uint32_t n = 0;
-            // loads what belongs to the tile at (p, j), piece e of it
-            auto load = [&](int e) {
-                const int it = cw + e * NW, row = it * kRowsIter;
-                const int seg = __shfl_sync(0xffffffffu, at, (row >> 4) & 7);
-                if (it < C::kIters && seg >= 0)
-                    raw[e] = ldg16(base + (size_t)seg * 16 * D + (row & 15) * D);
-            };
-            // moves on: what was just loaded becomes the tile to convert
-            auto take = [&] {
-                have = i < n_tiles;
-                miss = __ballot_sync(0xffffffffu, lane < 8 && at < 0) & 0xffu;
-                if (!V && cw == 0) {
-                    const int seg = __shfl_sync(0xffffffffu, at, lane & 7);
-                    // an infinite key scale marks a piece that is not there
-                    scale = lane < 8 ? INFINITY : 0.f;
-                    if (have && lane < 16 && seg >= 0) scale = (lane < 8 ? a.ks : a.vs)[seg >> (page_shift - 4)];
-                }
-                if (!have) return;
-                key0 = (p.t0 + j) * KT;
-                len = p.len;
-                ring = (slot + j) % kScaleRing;
-                if (++j == p.live) {
-                    slot = (slot + p.live) % kScaleRing;
-                    j = 0;
-                    i += p.left;
-                    if (i < n_tiles) advance(here, p.left, a.units, tiles);
-                    settle();
-                }
-                at = find();
-            };
+        // the next tile to load: its piece and place in it
+        Place here = start;
+        Piece p;
+        int i = 0, j = 0, slot = 0;
+        auto settle = [&] {  // to the first piece from here on that has a live tile
+            while (i < n_tiles) {
+                p = piece_at(here, i);
+                if (p.live > 0) return;
+                i += p.left;
+                if (i < n_tiles) advance(here, p.left, a.units, tiles);
+            }
+        };
+        // lane s < 8: 16-key piece s of the tile as a 16-row piece of the pool, -1: none
+        auto find = [&] {
+            int at = -1;
+            const int key = (p.t0 + j) * KT + lane * 16;
+            if (i < n_tiles && lane < 8 && key < p.len) {
+                const int phys = a.table[(int64_t)p.u.b * a.max_pages + (key >> page_shift)];
+                if (phys < 0 || phys >= a.n_pages) atomicOr(a.status, kStatusTable);
+                else at = (((phys * a.Hkv + p.u.hk) << page_shift) + (key & (a.page - 1))) >> 4;
+            }
+            return at;
+        };
+        settle();
+        int at = find();
+        uint4 raw[N];
+        float scale = 0.f;   // lanes 0-7: of the tile's keys, 8-15: of its values
+        uint32_t miss = 0;   // pieces of the tile that are not there
+        int key0 = 0, len = 0, ring = 0;
+        bool have = false;
+        // load e of the tile at (p, j): rows rl + 4 kRows e
+        auto load = [&](int e) {
+            const int seg = __shfl_sync(0xffffffffu, at, (4 * kRows * e + cw * kRows) >> 4);
+            if (seg >= 0) raw[e] = ldg16(src + (size_t)seg * (16 * D));
+        };
+        // what was just loaded becomes the tile to convert; on to the next
+        auto take = [&] {
+            have = i < n_tiles;
+            miss = __ballot_sync(0xffffffffu, lane < 8 && at < 0) & 0xffu;
+            if (!have) return;
+            if (warp == kConvertWarp0) {
+                const int seg = __shfl_sync(0xffffffffu, at, lane & 7);
+                // an infinite key scale marks a piece that is not there
+                scale = lane < 8 ? INFINITY : 0.f;
+                if (lane < 16 && seg >= 0) scale = (lane < 8 ? a.ks : a.vs)[seg >> (page_shift - 4)];
+            }
+            key0 = (p.t0 + j) * KT;
+            len = p.len;
+            ring = (slot + j) % kScaleRing;
+            if (++j == p.live) {
+                slot = (slot + p.live) % kScaleRing;
+                j = 0;
+                i += p.left;
+                if (i < n_tiles) advance(here, p.left, a.units, tiles);
+                settle();
+            }
+            at = find();
+        };
 #pragma unroll
-            for (int e = 0; e < N; ++e) load(e);
-            take();
-            while (have) {
-                const int st = n % kStages;
-                if (!__all_sync(0xffffffffu, watch.wait(bar(V ? bars->v_empty[st] : bars->k_empty[st]), ((n / kStages) & 1) ^ 1))) break;
-                if (!V && cw == 0) {
-                    if (lane < 16) scales[ring * 16 + lane] = scale;
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar(bars->sc_full[ring]));
-                }
-                const int held = len - key0;
+        for (int e = 0; e < N; ++e) load(e);
+        take();
+        uint32_t st = 0, lap = 0;
+        while (have) {
+            if (!__all_sync(0xffffffffu, watch.wait(bar(empty[st]), (lap & 1) ^ 1))) break;
+            if (warp == kConvertWarp0) {
+                if (lane < 16) scales[ring * 16 + lane] = scale;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(bars->sc_full[ring]));
+            }
+            // behind the last token, or without a page, there are no values
+            const int held = len - key0;
+            const bool part = values && (held < KT || miss != 0);
+            const uint32_t off = st * C::kTile;
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const int it = cw + e * NW, row = it * kRowsIter + rl;
-                    uint32_t h[8];
-                    U::quad(raw[e].x, h[0], h[1]);
-                    U::quad(raw[e].y, h[2], h[3]);
-                    U::quad(raw[e].z, h[4], h[5]);
-                    U::quad(raw[e].w, h[6], h[7]);
-                    load(e);
-                    // behind the last token, or without a page: no values
-                    if (V && (row >= held || (miss >> (row >> 4 & 7) & 1))) {
+            for (int e = 0; e < N; ++e) {
+                uint32_t h[8];
+                U::quad(raw[e].x, h[0], h[1]);
+                U::quad(raw[e].y, h[2], h[3]);
+                U::quad(raw[e].z, h[4], h[5]);
+                U::quad(raw[e].w, h[6], h[7]);
+                load(e);
+                if (part) {
+                    const int row = rl + 4 * kRows * e;
+                    if (row >= held || (miss >> (row >> 4) & 1)) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k) h[k] = 0;
                     }
-                    if (it < C::kIters) {
-                        const uint32_t line = to + st * C::kTile + row * 128;
-                        ptx::st_shared_v4(line + ((p0 ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-                        ptx::st_shared_v4(line + (((p0 + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
-                    }
                 }
-                ptx::fence_proxy_async_smem();
-                ptx::mbar_arrive(bar(V ? bars->v_full[st] : bars->k_full[st]));
-                ++n;
-                take();
+                ptx::st_shared_v4(to0 + off + e * (4 * kRows * 128), h[0], h[1], h[2], h[3]);
+                ptx::st_shared_v4(to1 + off + e * (4 * kRows * 128), h[4], h[5], h[6], h[7]);
             }
-        };
-        if (warp <= kMmaWarp + kKeyWarps)
-            convert(std::false_type{}, std::integral_constant<int, kKeyWarps>{}, warp - kMmaWarp - 1);
-        else
-            convert(std::true_type{}, std::integral_constant<int, kValueWarps>{}, warp - kMmaWarp - kKeyWarps - 1);
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(bar(full[st]));
+            if (++st == stages) {
+                st = 0;
+                ++lap;
+            }
+            take();
+        }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
@@ -396,9 +328,47 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
         const uint32_t tS = tmem + lanes + t * KT, tO = tmem + lanes + 256 + t * D;
         uint32_t sn = 0, qn = 0, jn = 0;
-        int slot = 0;
+        uint32_t slot = 0;  // live tiles before the unit
         bool ok = true;
         Place here = start;
+        // ---- this half's products, issued by its first warp
+        auto wait_all = [&](uint32_t b, uint32_t parity) {
+            return __all_sync(0xffffffffu, watch.wait(b, parity));
+        };
+        // S_t of tile j of the unit, the tile-th live one of the range
+        auto issue_s = [&](int j, uint32_t tile, int live) {
+            const uint32_t st = tile % C::kKeyStages;
+            if (!wait_all(bar(bars->k_full[st]), (tile / C::kKeyStages) & 1)) return false;
+            ptx::tc_fence_after();
+            const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(sK + st * C::kTile, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
+                ptx::mma_ss_warp(tmem + t * KT, dq + off, dk + off, idesc_f16(false, R, KT, false), kk > 0 ? 1u : 0u);
+            }
+            ptx::mma_commit_warp(bar(bars->s_full[t]));
+            ptx::mma_commit_warp(bar(bars->k_empty[st]));
+            if (j + 2 >= live) ptx::mma_commit_warp(bar(bars->q_empty));
+            return true;
+        };
+        // O_t += P_t V_j; `first`: O_t is set, once the last unit's epilogue has read it
+        auto issue_pv = [&](uint32_t tile, bool first, uint32_t n, uint32_t units_done) {
+            const uint32_t st = tile % C::kValueStages;
+            if (!wait_all(bar(bars->v_full[st]), (tile / C::kValueStages) & 1) ||
+                !wait_all(bar(bars->p_full[t]), n & 1) ||
+                (first && !wait_all(bar(bars->o_empty), (units_done & 1) ^ 1)))
+                return false;
+            ptx::tc_fence_after();
+            const uint64_t dv = sdesc(sV + st * C::kTile, C::kChunkBytes, 1024);
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+                ptx::mma_ts_warp(tmem + 256 + t * D, tmem + t * KT + kk * 8,
+                                 dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_f16(false, R, D, true),
+                                 (!first || kk > 0) ? 1u : 0u);
+            ptx::mma_commit_warp(bar(bars->pv_done[t]));
+            ptx::mma_commit_warp(bar(bars->v_empty[st]));
+            return true;
+        };
         for (int i = 0; i < n_tiles && ok;) {
             const Piece p = piece_at(here, i);
             int qi, h;
@@ -452,10 +422,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                 if (!__all_sync(0xffffffffu, watch.wait(bar(bars->q_full), qn & 1))) break;
                 ++qn;
                 cq = a.sl2 * back[r];
+                if (wq == 0) {
+                    if (t >= p.live) ptx::mbar_arrive_warp(bar(bars->q_empty));  // a unit of one tile
+                    else if (!issue_s(t, slot + t, p.live)) break;
+                }
             }
             float top = kUnset, rv = 0x1p100f, l = 0.f;
             for (int j = t; j < p.live; j += 2) {
-                const int ring = (slot + j) % kScaleRing, lap = (slot + j) / kScaleRing;
+                const uint32_t ring = (slot + j) % kScaleRing, lap = (slot + j) / kScaleRing;
                 bool got = watch.wait(bar(bars->sc_full[ring]), lap & 1);
                 got = got && watch.wait(bar(bars->s_full[t]), sn & 1);
                 ++sn;
@@ -578,6 +552,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                 }
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(bar(bars->p_full[t]));
+                if (wq == 0) {
+                    __syncwarp();
+                    ok = issue_pv(slot + j, j < 2, sn - 1, qn - 1);
+                    if (ok && j + 2 < p.live)  // S_t takes P_t's place
+                        ok = wait_all(bar(bars->pv_done[t]), (sn - 1) & 1) && issue_s(j + 2, slot + j + 2, p.live);
+                    if (!ok) break;
+                }
             }
             if (!ok) break;
 
@@ -658,12 +639,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             i += p.left;
             if (i < n_tiles) advance(here, p.left, a.units, tiles);
         }
+        // every MMA issued by this warp has completed before tensor memory is freed
+        __syncwarp();
+        if (wq == 0) {
+            ptx::mma_commit_warp(bar(bars->mma_done[t]));
+            watch.drain(bar(bars->mma_done[t]), 0);
+        }
+        __syncwarp();
     }
 
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+    if (warp == 0) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
 // Joins the states of the units that run over the CTAs' ends, a warp per row.
