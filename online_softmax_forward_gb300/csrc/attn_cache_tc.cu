@@ -19,11 +19,11 @@
 //               and O_t += P_t V_j.
 //
 // The two halves keep states of their own (top, rv, l and O_t, references moved
-// only when a weight would pass 2^10 or fp16's range, as in attn_cache_fwd.cu), so
-// that one exponentiates while the other's products run; they are joined when the
-// unit ends.  The largest scores come with a first load of S (tcgen05.ld.red), so
-// that P can replace S step by step: two registers' worth of 32 keys are live at
-// a time and 16 warps fit the SM.  A warp without a real row (few drafts, few heads) only keeps step.  P in
+// only when 16 weights would pass 2^10 or fp16's range, as in attn_cache_fwd.cu),
+// so that one exponentiates while the other's products run; they are joined when
+// the unit ends.  S is taken and P put in its place 16 keys at a time, the next
+// 16 on their way, so that 16 warps fit the SM; a move of the references also
+// scales what the tile has put there.  A warp without a real row (few drafts, few heads) only keeps step.  P in
 // fp16 is rounded by 2^-12, so this kernel serves the 16-bit outputs.
 //
 // Tensor memory (512 columns): S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 from
@@ -56,7 +56,7 @@ constexpr int kConvertWarp0 = 8;  // 8 .. 11 keys, 12 .. 15 values
 constexpr int kThreads = 16 * 32;
 constexpr int kScaleRing = 8;       // tiles whose page scales are kept
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLargest = 10.f;    // log2 of the largest weight; 32 * 2^10 fits fp16
+constexpr float kLargest = 1024.f;  // of 16 keys' sum of weights; 32 * 1024 fits fp16
 constexpr float kBase = 32.f;       // page scale times rv, at its largest after a move
 
 struct Bars {
@@ -445,107 +445,99 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
 #pragma unroll
                     for (int s = 0; s < 8; ++s) hole = hole || ks[s] == INFINITY;
                     const bool edge = __any_sync(0xffffffffu, hole || key0 + KT > lim);
-                    // the largest score of each 16 keys, from the load that reduces, and of the
-                    // visible ones in software where some are not
-                    float high = -INFINITY, most = 0.f;
-                    bool far = false;
-                    auto look = [&](int seg, float m) {
-                        if (m == -INFINITY) return;  // nothing visible
-                        const float v = vs[seg];
-                        m *= ks[seg] * cq;
-                        high = fmaxf(high, m);
-                        most = fmaxf(most, v);
-                        far = far || m - top > kLargest || ptx::ex2_approx(m - top) * (v * rv) > kBase * 1024.f;
-                    };
-                    if (!edge) {
+                    float sum = 0.f;
+                    uint32_t s[16];
+                    ptx::tmem_ld16(tS, s);
+                    ptx::tmem_wait_ld();
+                    reg_fence(s);
 #pragma unroll 1
-                        for (int c = 0; c < 8; c += 4) {
-                            uint32_t d[4][16];
-                            float mx[4];
+                    for (int seg = 0; seg < 8; ++seg) {  // 16 keys of one page
+                        // the next ones on their way (the last step's are not used); they arrive
+                        // before the step ends, so that no copy of them is made too early
+                        uint32_t next[16];
+                        ptx::tmem_ld16(tS + (seg < 7 ? seg + 1 : 7) * 16, next);
+                        const float kscale = ks[seg], f = kscale * cq;
+                        const int n = edge ? (kscale == INFINITY ? 0 : lim - (key0 + seg * 16)) : 16;
+                        // a page no key of which the row sees adds nothing, not even its scale's NaN
+                        const float sv = n > 0 ? vs[seg] : 0.f;
+                        float cv = sv * rv, part[4] = {}, w[16];
 #pragma unroll
-                            for (int s = 0; s < 4; ++s) ptx::tmem_ld16_max(tS + (c + s) * 16, d[s], mx[s]);
-                            ptx::tmem_wait_ld();
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) asm volatile("" : "+f"(mx[s]));
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) look(c + s, mx[s]);
+                        for (int e = 0; e < 16; ++e) {
+                            float z = fmaf(__uint_as_float(s[e]), f, -top);
+                            if (edge && e >= n) z = -INFINITY;
+                            w[e] = ptx::ex2_approx(z);
+                            part[e & 3] += w[e];
                         }
-                    } else {
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t s32[32];
+                        float all = (part[0] + part[1]) + (part[2] + part[3]);
+                        if (__any_sync(0xffffffffu, all > kLargest || all * cv > kLargest * kBase)) {
+                            // new references: the scores' maximum, and the page's scale unless
+                            // what O holds is larger by now
+                            float mx = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (e < n) mx = fmaxf(mx, __uint_as_float(s[e]) * f);
+                            const float nt = fmaxf(top, mx);
+                            const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
+                            const float was = alpha * kBase / rv;
+                            const float nv = mx == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, sv), 0x1p-95f);
+                            const float to = alpha * (nv / rv);
+                            l *= alpha;
+                            sum *= alpha;
+                            top = nt;
+                            rv = nv;
+                            cv = sv * rv;
                             __syncwarp();
-                            ptx::tmem_ld32(tS + c * 32, s32);
-                            ptx::tmem_wait_ld();
-                            reg_fence(s32);
-#pragma unroll
-                            for (int s = 0; s < 2; ++s) {
-                                const int n = ks[c * 2 + s] == INFINITY ? 0 : lim - (key0 + (c * 2 + s) * 16);
-                                float m = -INFINITY;
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (e < n) m = fmaxf(m, __uint_as_float(s32[s * 16 + e]));
-                                look(c * 2 + s, m);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                    if (__any_sync(0xffffffffu, far)) {
-                        // new references: the scores' maximum, and the page scales unless what O
-                        // holds is larger by now
-                        const float nt = fmaxf(top, high);
-                        const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
-                        const float was = alpha * kBase / rv;
-                        const float nv = high == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, most), 0x1p-95f);
-                        const float to = alpha * (nv / rv);
-                        l *= alpha;
-                        top = nt;
-                        rv = nv;
-                        __syncwarp();
-                        if (j > 1) {  // O_t holds the tiles before: S(j) came after their products
+                            ptx::tmem_wait_ld();  // `next`, before more is loaded
+                            reg_fence(next);
+                            ptx::tmem_wait_st();
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                ptx::tmem_ld32(tO + c * 32, o);
+                            for (int c = 0; c < seg; ++c) {  // the tile's earlier P
+                                uint32_t o[8];
+                                ptx::tmem_ld8(tS + c * 8, o);
                                 ptx::tmem_wait_ld();
                                 reg_fence(o);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * to);
-                                ptx::tmem_st32(tO + c * 32, o);
-                                ptx::tmem_wait_st();
-                            }
-                        }
-                    }
-                    // P of 32 keys takes 16 columns of S_t, all of them read before
-                    float sum = 0.f;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t s32[32], pk[16];
-                        ptx::tmem_ld32(tS + c * 32, s32);
-                        ptx::tmem_wait_ld();
-                        reg_fence(s32);
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {  // of one page
-                            const int seg = c * 2 + s;
-                            const float f = ks[seg] * cq;
-                            const int n = edge ? (ks[seg] == INFINITY ? 0 : lim - (key0 + seg * 16)) : 16;
-                            // a page no key of which the row sees adds nothing, not even its
-                            // scale's NaN
-                            const float cv = n > 0 ? vs[seg] * rv : 0.f;
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                float z0 = fmaf(__uint_as_float(s32[s * 16 + e]), f, -top);
-                                float z1 = fmaf(__uint_as_float(s32[s * 16 + e + 1]), f, -top);
-                                if (edge) {
-                                    if (e >= n) z0 = -INFINITY;
-                                    if (e + 1 >= n) z1 = -INFINITY;
+                                for (int e = 0; e < 8; ++e) {
+                                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&o[e]));
+                                    o[e] = pack_f16(x.x * to, x.y * to);
                                 }
-                                const float w0 = ptx::ex2_approx(z0), w1 = ptx::ex2_approx(z1);
-                                sum += w0 + w1;
-                                pk[s * 8 + e / 2] = pack_f16(w0 * cv, w1 * cv);
+                                ptx::tmem_st8(tS + c * 8, o);
+                            }
+                            if (j > 1) {  // O_t holds the tiles before: S(j) came after their products
+#pragma unroll 1
+                                for (int c = 0; c < D / 16; ++c) {
+                                    uint32_t o[16];
+                                    ptx::tmem_ld16(tO + c * 16, o);
+                                    ptx::tmem_wait_ld();
+                                    reg_fence(o);
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 8) {
+                                        uint32_t x[8];
+#pragma unroll
+                                        for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(__uint_as_float(o[e + k]) * to);
+                                        ptx::tmem_st8(tO + c * 16 + e, x);
+                                    }
+                                }
+                            }
+                            ptx::tmem_wait_st();
+                            all = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float z = fmaf(__uint_as_float(s[e]), f, -top);
+                                if (e >= n) z = -INFINITY;
+                                w[e] = ptx::ex2_approx(z);
+                                all += w[e];
                             }
                         }
-                        ptx::tmem_st16(tS + c * 16, pk);
+                        sum += all;
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) pk[e] = pack_f16(w[2 * e] * cv, w[2 * e + 1] * cv);
+                        ptx::tmem_wait_ld();
+                        reg_fence(next);
+                        ptx::tmem_st8(tS + seg * 8, pk);  // columns all read before
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) s[e] = next[e];
                     }
                     l += sum;
                     ptx::tmem_wait_st();
@@ -619,9 +611,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                             if (in_bounds(at + c + e + 8 <= (size_t)a.B * a.Hkv * a.G * a.Sq * D, a.status))
                                 store_o8(a, at + c + e, f + e);
                     } else if (real && in_bounds(sl < 2 * (int)gridDim.x, a.status)) {
-                        float4 *d = reinterpret_cast<float4 *>(a.po + ((size_t)sl * R + r) * D + c);
+                        // [D / 4][R][4]: a warp's store is one piece
+                        float4 *d = reinterpret_cast<float4 *>(a.po + (size_t)sl * R * D) + (c / 4) * R + r;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) d[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e) d[e * R] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                     }
                     __syncwarp();  // the loads above are the whole warp's
                 }
@@ -654,42 +647,39 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
     if (warp == 0) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the states of the units that run over the CTAs' ends, a warp per row.
+// Joins the states of the units that run over the CTAs' ends: eight rows a CTA,
+// thread t four channels of row t % 8, so that a warp reads whole 128-byte lines
+// of the states' [D / 4][R][4].
 template <int D>
-__global__ void __launch_bounds__(256) cache_tc_merge_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(8 * D / 4) cache_tc_merge_kernel(const FwdArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 d = a.tail[blockIdx.x];
     if (!d.x) return;
     const Unit u = unit_at(a, d.z, d.w);
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int r = blockIdx.y * 8 + (threadIdx.x & 7), c4 = threadIdx.x >> 3;
     size_t row;
     if (!out_row<R>(a, u, r, row)) return;
     const int n = d.y - (int)blockIdx.x + 1;
     if (!in_bounds(n <= kCacheMaxCtas, a.status)) return;
     auto slot = [&](int p) { return 2 * (size_t)(blockIdx.x + p) + (p == 0 ? 1 : 0); };
     float M = -INFINITY;
-    for (int p = lane; p < n; p += 32) M = fmaxf(M, a.pl[slot(p) * R + r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int p = 0; p < n; ++p) M = fmaxf(M, a.pl[slot(p) * R + r]);
     const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[D / 32] = {};
-    for (int p0 = 0; p0 < n; p0 += 32) {
-        const float wt = p0 + lane < n ? ptx::ex2_approx(a.pl[slot(p0 + lane) * R + r] - base) : 0.f;
-        L += wt;
+    float L = 0.f, acc[4] = {};
 #pragma unroll 4
-        for (int p = 0; p < min(32, n - p0); ++p) {
-            const float w = __shfl_sync(0xffffffffu, wt, p);
-            const float *src = a.po + (slot(p0 + p) * R + r) * D + lane;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, src[32 * e], acc[e]);
-        }
+    for (int p = 0; p < n; ++p) {
+        const float w = ptx::ex2_approx(a.pl[slot(p) * R + r] - base);
+        const float4 x = reinterpret_cast<const float4 *>(a.po + slot(p) * R * D)[c4 * R + r];
+        L += w;
+        acc[0] = fmaf(w, x.x, acc[0]);
+        acc[1] = fmaf(w, x.y, acc[1]);
+        acc[2] = fmaf(w, x.z, acc[2]);
+        acc[3] = fmaf(w, x.w, acc[3]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) store_o(a, row * D + lane + 32 * e, acc[e] * inv);
-    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * kLn2;
+    for (int e = 0; e < 4; ++e) store_o(a, row * D + c4 * 4 + e, acc[e] * inv);
+    if (a.lse && c4 == 0) a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * kLn2;
 }
 
 template <int D, int FMT>
@@ -706,7 +696,7 @@ int launch_t(const FwdArgs &f, unsigned grid, cudaStream_t stream) {
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, (unsigned)((f.rows < R ? f.rows : R) + 7) / 8);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(8 * D / 4);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
