@@ -18,17 +18,19 @@
 //               first warp of each four issues its half's products, S_t = Q K_j^T
 //               and O_t += P_t V_j.
 //
-// The two halves keep states of their own (top, rv, l and O_t, references moved
-// only when 16 weights would pass 2^10 or fp16's range, as in attn_cache_fwd.cu),
+// The two warpgroups keep states of their own (top, rv, l and O_t, references moved
+// only when 32 weights would pass 2^10 or fp16's range, as in attn_cache_fwd.cu),
 // so that one exponentiates while the other's products run; they are joined when
-// the unit ends.  S is taken and P put in its place 16 keys at a time, the next
-// 16 on their way, so that 16 warps fit the SM; a move of the references also
-// scales what the tile has put there.  A warp without a real row (few drafts, few heads) only keeps step.  P in
-// fp16 is rounded by 2^-12, so this kernel serves the 16-bit outputs.
+// the unit ends.  P in fp16 is rounded by 2^-12, so this kernel serves the 16-bit
+// outputs.  A warp without a real row (few drafts, few heads) only keeps step.
 //
-// Tensor memory (512 columns): S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 from
-// 256, O_1 from 256 + D.  S_t(j + 2) may be written once P_t(j) has been used: its
-// issue waits for that product.  Every wait is bounded, as in attn_tc.cu.
+// A tile's S, P and products go in halves of 64 keys.  Tensor memory (512 columns)
+// is full with S_0 [0, 128), S_1 [128, 256), O_0 from 256 and O_1 from 256 + D, so
+// P of a half lies over the first half of its S, and S_t(j + 2) of a half waits for
+// the product that reads it; the other half keeps the tensor cores and the warps
+// busy meanwhile.  S is taken and P put in its place 32 keys at a time, the next 32
+// on their way, so that 16 warps fit the SM's registers.  Every wait is bounded, as
+// in attn_tc.cu.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -56,13 +58,13 @@ constexpr int kConvertWarp0 = 8;  // 8 .. 11 keys, 12 .. 15 values
 constexpr int kThreads = 16 * 32;
 constexpr int kScaleRing = 8;       // tiles whose page scales are kept
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLargest = 1024.f;  // of 16 keys' sum of weights; 32 * 1024 fits fp16
+constexpr float kLargest = 1024.f;  // of 32 keys' sum of weights; 32 * 1024 fits fp16
 constexpr float kBase = 32.f;       // page scale times rv, at its largest after a move
 
 struct Bars {
     uint64_t q_full, q_empty;
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [warpgroup][half of the tile]
     uint64_t o_empty, joined, mma_done[2];
     uint64_t sc_full[kScaleRing];
     uint32_t tmem_base;
@@ -131,9 +133,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             ptx::mbar_init(bar(bars->v_empty[s]), 1);
         }
         for (int t = 0; t < 2; ++t) {
-            ptx::mbar_init(bar(bars->s_full[t]), 1);
-            ptx::mbar_init(bar(bars->p_full[t]), 128);
-            ptx::mbar_init(bar(bars->pv_done[t]), 1);
+            for (int h = 0; h < 2; ++h) {
+                ptx::mbar_init(bar(bars->s_full[t][h]), 1);
+                ptx::mbar_init(bar(bars->p_full[t][h]), 128);
+                ptx::mbar_init(bar(bars->pv_done[t][h]), 1);
+            }
             ptx::mbar_init(bar(bars->mma_done[t]), 1);
         }
         ptx::mbar_init(bar(bars->o_empty), 256);
@@ -335,38 +339,41 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         auto wait_all = [&](uint32_t b, uint32_t parity) {
             return __all_sync(0xffffffffu, watch.wait(b, parity));
         };
-        // S_t of tile j of the unit, the tile-th live one of the range
-        auto issue_s = [&](int j, uint32_t tile, int live) {
+        // half h of S_t of a tile, the tile-th live one of the range; `last` of the unit's for t
+        auto issue_s = [&](int h, uint32_t tile, bool last) {
             const uint32_t st = tile % C::kKeyStages;
             if (!wait_all(bar(bars->k_full[st]), (tile / C::kKeyStages) & 1)) return false;
             ptx::tc_fence_after();
-            const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(sK + st * C::kTile, 16, 1024);
+            const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(sK + st * C::kTile + h * 64 * 128, 16, 1024);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
-                ptx::mma_ss_warp(tmem + t * KT, dq + off, dk + off, idesc_f16(false, R, KT, false), kk > 0 ? 1u : 0u);
+                ptx::mma_ss_warp(tmem + t * KT + h * 64, dq + off, dk + off, idesc_f16(false, R, 64, false), kk > 0 ? 1u : 0u);
             }
-            ptx::mma_commit_warp(bar(bars->s_full[t]));
-            ptx::mma_commit_warp(bar(bars->k_empty[st]));
-            if (j + 2 >= live) ptx::mma_commit_warp(bar(bars->q_empty));
+            ptx::mma_commit_warp(bar(bars->s_full[t][h]));
+            if (h == 1) {
+                ptx::mma_commit_warp(bar(bars->k_empty[st]));
+                if (last) ptx::mma_commit_warp(bar(bars->q_empty));
+            }
             return true;
         };
-        // O_t += P_t V_j; `first`: O_t is set, once the last unit's epilogue has read it
-        auto issue_pv = [&](uint32_t tile, bool first, uint32_t n, uint32_t units_done) {
+        // O_t += P_t V_j for half h; `first` tile: O_t is set, once the last unit's epilogue has
+        // read it.  n: this warpgroup's tiles before
+        auto issue_pv = [&](int h, uint32_t tile, bool first, uint32_t n, uint32_t units_done) {
             const uint32_t st = tile % C::kValueStages;
             if (!wait_all(bar(bars->v_full[st]), (tile / C::kValueStages) & 1) ||
-                !wait_all(bar(bars->p_full[t]), n & 1) ||
-                (first && !wait_all(bar(bars->o_empty), (units_done & 1) ^ 1)))
+                !wait_all(bar(bars->p_full[t][h]), n & 1) ||
+                (first && h == 0 && !wait_all(bar(bars->o_empty), (units_done & 1) ^ 1)))
                 return false;
             ptx::tc_fence_after();
-            const uint64_t dv = sdesc(sV + st * C::kTile, C::kChunkBytes, 1024);
+            const uint64_t dv = sdesc(sV + st * C::kTile + h * 64 * 128, C::kChunkBytes, 1024);
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-                ptx::mma_ts_warp(tmem + 256 + t * D, tmem + t * KT + kk * 8,
+            for (int kk = 0; kk < 4; ++kk)
+                ptx::mma_ts_warp(tmem + 256 + t * D, tmem + t * KT + h * 64 + kk * 8,
                                  dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_f16(false, R, D, true),
-                                 (!first || kk > 0) ? 1u : 0u);
-            ptx::mma_commit_warp(bar(bars->pv_done[t]));
-            ptx::mma_commit_warp(bar(bars->v_empty[st]));
+                                 (!first || h > 0 || kk > 0) ? 1u : 0u);
+            ptx::mma_commit_warp(bar(bars->pv_done[t][h]));
+            if (h == 1) ptx::mma_commit_warp(bar(bars->v_empty[st]));
             return true;
         };
         for (int i = 0; i < n_tiles && ok;) {
@@ -424,141 +431,196 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                 cq = a.sl2 * back[r];
                 if (wq == 0) {
                     if (t >= p.live) ptx::mbar_arrive_warp(bar(bars->q_empty));  // a unit of one tile
-                    else if (!issue_s(t, slot + t, p.live)) break;
+                    else if (!issue_s(0, slot + t, t + 2 >= p.live) || !issue_s(1, slot + t, t + 2 >= p.live)) break;
                 }
             }
             float top = kUnset, rv = 0x1p100f, l = 0.f;
             for (int j = t; j < p.live; j += 2) {
                 const uint32_t ring = (slot + j) % kScaleRing, lap = (slot + j) / kScaleRing;
-                bool got = watch.wait(bar(bars->sc_full[ring]), lap & 1);
-                got = got && watch.wait(bar(bars->s_full[t]), sn & 1);
-                ++sn;
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                if (!idle) {
-                    const float *ks = scales + ring * 16, *vs = ks + 8;
-                    const int key0 = (p.t0 + j) * KT;
+                ok = wait_all(bar(bars->sc_full[ring]), lap & 1);
+                const float *ks = scales + ring * 16, *vs = ks + 8;
+                const int key0 = (p.t0 + j) * KT;
+                bool edge = false;
+                if (ok && !idle) {
                     bool hole = false;
 #pragma unroll
                     for (int s = 0; s < 8; ++s) hole = hole || ks[s] == INFINITY;
-                    const bool edge = __any_sync(0xffffffffu, hole || key0 + KT > lim);
-                    float sum = 0.f;
-                    uint32_t s[16];
-                    ptx::tmem_ld16(tS, s);
-                    ptx::tmem_wait_ld();
-                    reg_fence(s);
+                    edge = __any_sync(0xffffffffu, hole || key0 + KT > lim);
+                }
 #pragma unroll 1
-                    for (int seg = 0; seg < 8; ++seg) {  // 16 keys of one page
-                        // the next ones on their way (the last step's are not used); they arrive
-                        // before the step ends, so that no copy of them is made too early
-                        uint32_t next[16];
-                        ptx::tmem_ld16(tS + (seg < 7 ? seg + 1 : 7) * 16, next);
-                        const float kscale = ks[seg], f = kscale * cq;
-                        const int n = edge ? (kscale == INFINITY ? 0 : lim - (key0 + seg * 16)) : 16;
-                        // a page no key of which the row sees adds nothing, not even its scale's NaN
-                        const float sv = n > 0 ? vs[seg] : 0.f;
-                        float cv = sv * rv, part[4] = {}, w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float z = fmaf(__uint_as_float(s[e]), f, -top);
-                            if (edge && e >= n) z = -INFINITY;
-                            w[e] = ptx::ex2_approx(z);
-                            part[e & 3] += w[e];
-                        }
-                        float all = (part[0] + part[1]) + (part[2] + part[3]);
-                        if (__any_sync(0xffffffffu, all > kLargest || all * cv > kLargest * kBase)) {
-                            // new references: the scores' maximum, and the page's scale unless
-                            // what O holds is larger by now
-                            float mx = -INFINITY;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (e < n) mx = fmaxf(mx, __uint_as_float(s[e]) * f);
-                            const float nt = fmaxf(top, mx);
-                            const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
-                            const float was = alpha * kBase / rv;
-                            const float nv = mx == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, sv), 0x1p-95f);
-                            const float to = alpha * (nv / rv);
-                            l *= alpha;
-                            sum *= alpha;
-                            top = nt;
-                            rv = nv;
-                            cv = sv * rv;
-                            __syncwarp();
-                            ptx::tmem_wait_ld();  // `next`, before more is loaded
-                            reg_fence(next);
-                            ptx::tmem_wait_st();
+                for (int half = 0; half < 2 && ok; ++half) {
+                    ok = wait_all(bar(bars->s_full[t][half]), sn & 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (!idle) {
+                        const uint32_t tH = tS + half * 64;
+                        float sum = 0.f;
+                        uint32_t s[32];
+                        ptx::tmem_ld32(tH, s);
+                        ptx::tmem_wait_ld();
+                        reg_fence(s);
 #pragma unroll 1
-                            for (int c = 0; c < seg; ++c) {  // the tile's earlier P
-                                uint32_t o[8];
-                                ptx::tmem_ld8(tS + c * 8, o);
-                                ptx::tmem_wait_ld();
-                                reg_fence(o);
+                        for (int step = 0; step < 2; ++step) {  // 32 keys, 16 of one page and 16
+                            // the next 32 on their way (the second step's are not used); they are
+                            // waited for before the step ends, so that no copy is made too early
+                            uint32_t next[32];
+                            ptx::tmem_ld32(tH + 32, next);
+                            const int seg = half * 4 + step * 2;
+                            float f[2], sv[2], cv[2];
+                            int n[2];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&o[e]));
-                                    o[e] = pack_f16(x.x * to, x.y * to);
-                                }
-                                ptx::tmem_st8(tS + c * 8, o);
+                            for (int g = 0; g < 2; ++g) {
+                                const float kscale = ks[seg + g];
+                                f[g] = kscale * cq;
+                                n[g] = edge ? (kscale == INFINITY ? 0 : lim - (key0 + (seg + g) * 16)) : 16;
+                                // a page no key of which the row sees adds nothing, not even its
+                                // scale's NaN
+                                sv[g] = n[g] > 0 ? vs[seg + g] : 0.f;
+                                cv[g] = sv[g] * rv;
                             }
-                            if (j > 1) {  // O_t holds the tiles before: S(j) came after their products
+                            float2 part[2][2];
+                            auto weights = [&] {  // of s, in place; their sums of each 16
+#pragma unroll
+                                for (int g = 0; g < 2; ++g) {
+                                    const float2 f2 = make_float2(f[g], f[g]), t2 = make_float2(-top, -top);
+                                    part[g][0] = part[g][1] = make_float2(0.f, 0.f);
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) {
+                                        uint32_t &s0 = s[g * 16 + e], &s1 = s[g * 16 + e + 1];
+                                        float2 z = __ffma2_rn(make_float2(__uint_as_float(s0), __uint_as_float(s1)), f2, t2);
+                                        z = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
+                                        part[g][(e >> 1) & 1] = __fadd2_rn(part[g][(e >> 1) & 1], z);
+                                        s0 = __float_as_uint(z.x);
+                                        s1 = __float_as_uint(z.y);
+                                    }
+                                }
+                                if (!edge) return;
+#pragma unroll
+                                for (int g = 0; g < 2; ++g) {  // again without what is not seen
+                                    part[g][0] = part[g][1] = make_float2(0.f, 0.f);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        if (e >= n[g]) s[g * 16 + e] = 0;
+                                        part[g][0].x += __uint_as_float(s[g * 16 + e]);
+                                    }
+                                }
+                            };
+                            weights();
+                            float all[2];
+                            auto add = [&] {
+#pragma unroll
+                                for (int g = 0; g < 2; ++g) {
+                                    const float2 x = __fadd2_rn(part[g][0], part[g][1]);
+                                    all[g] = x.x + x.y;
+                                }
+                            };
+                            add();
+                            if (__any_sync(0xffffffffu, fmaxf(all[0], all[1]) > kLargest ||
+                                                            fmaxf(all[0] * cv[0], all[1] * cv[1]) > kLargest * kBase)) {
+                                // new references: the scores' maximum, and the pages' scale unless
+                                // what O holds is larger by now.  S of the step is still there
+                                __syncwarp();
+                                ptx::tmem_wait_ld();
+                                reg_fence(next);
+                                ptx::tmem_wait_st();
+                                ptx::tmem_ld32(tH + step * 32, s);
+                                ptx::tmem_wait_ld();
+                                reg_fence(s);
+                                float mx = -INFINITY, most = 0.f;
+#pragma unroll
+                                for (int g = 0; g < 2; ++g) {
+                                    most = fmaxf(most, sv[g]);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        if (e < n[g]) mx = fmaxf(mx, __uint_as_float(s[g * 16 + e]) * f[g]);
+                                }
+                                const float nt = fmaxf(top, mx);
+                                const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
+                                const float was = alpha * kBase / rv;
+                                const float nv = mx == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, most), 0x1p-95f);
+                                const float to = alpha * (nv / rv);
+                                l *= alpha;
+                                sum *= alpha;
+                                top = nt;
+                                rv = nv;
+                                // O_t holds the tiles before (S(j) came after their products), and
+                                // this tile's first half
+                                if (half == 1) {
+                                    ok = wait_all(bar(bars->pv_done[t][0]), sn & 1);
+                                    ptx::tc_fence_after();
+                                }
+                                if (j > 1 || half == 1) {
 #pragma unroll 1
-                                for (int c = 0; c < D / 16; ++c) {
+                                    for (int c = 0; c < D / 16; ++c) {
+                                        uint32_t o[16];
+                                        __syncwarp();
+                                        ptx::tmem_ld16(tO + c * 16, o);
+                                        ptx::tmem_wait_ld();
+                                        reg_fence(o);
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * to);
+                                        ptx::tmem_st16(tO + c * 16, o);
+                                    }
+                                }
+                                if (step == 1) {  // the half's first 32 weights
                                     uint32_t o[16];
-                                    ptx::tmem_ld16(tO + c * 16, o);
+                                    ptx::tmem_ld16(tH, o);
                                     ptx::tmem_wait_ld();
                                     reg_fence(o);
 #pragma unroll
-                                    for (int e = 0; e < 16; e += 8) {
-                                        uint32_t x[8];
-#pragma unroll
-                                        for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(__uint_as_float(o[e + k]) * to);
-                                        ptx::tmem_st8(tO + c * 16 + e, x);
+                                    for (int e = 0; e < 16; ++e) {
+                                        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&o[e]));
+                                        o[e] = pack_f16(x.x * to, x.y * to);
                                     }
+                                    ptx::tmem_st16(tH, o);
                                 }
-                            }
-                            ptx::tmem_wait_st();
-                            all = 0.f;
+                                ptx::tmem_wait_st();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float z = fmaf(__uint_as_float(s[e]), f, -top);
-                                if (e >= n) z = -INFINITY;
-                                w[e] = ptx::ex2_approx(z);
-                                all += w[e];
+                                for (int g = 0; g < 2; ++g) cv[g] = sv[g] * rv;
+                                weights();
+                                add();
                             }
+                            sum += all[0] + all[1];
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float2 x = __fmul2_rn(
+                                        make_float2(__uint_as_float(s[g * 16 + 2 * e]), __uint_as_float(s[g * 16 + 2 * e + 1])),
+                                        make_float2(cv[g], cv[g]));
+                                    pk[g * 8 + e] = pack_f16(x.x, x.y);
+                                }
+                            ptx::tmem_wait_ld();
+                            reg_fence(next);
+                            ptx::tmem_st16(tH + step * 16, pk);  // over columns already taken
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[e] = next[e];
                         }
-                        sum += all;
-                        uint32_t pk[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) pk[e] = pack_f16(w[2 * e] * cv, w[2 * e + 1] * cv);
-                        ptx::tmem_wait_ld();
-                        reg_fence(next);
-                        ptx::tmem_st8(tS + seg * 8, pk);  // columns all read before
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) s[e] = next[e];
+                        l += sum;
+                        ptx::tmem_wait_st();
                     }
-                    l += sum;
-                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(bar(bars->p_full[t][half]));
+                    if (wq == 0) {
+                        __syncwarp();
+                        ok = ok && issue_pv(half, slot + j, j < 2, sn, qn - 1);
+                    }
                 }
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(bar(bars->p_full[t]));
-                if (wq == 0) {
-                    __syncwarp();
-                    ok = issue_pv(slot + j, j < 2, sn - 1, qn - 1);
-                    if (ok && j + 2 < p.live)  // S_t takes P_t's place
-                        ok = wait_all(bar(bars->pv_done[t]), (sn - 1) & 1) && issue_s(j + 2, slot + j + 2, p.live);
-                    if (!ok) break;
-                }
+                if (ok && wq == 0 && j + 2 < p.live)  // S_t takes the place of P_t, half by half
+                    ok = wait_all(bar(bars->pv_done[t][0]), sn & 1) && issue_s(0, slot + j + 2, j + 4 >= p.live) &&
+                         wait_all(bar(bars->pv_done[t][1]), sn & 1) && issue_s(1, slot + j + 2, j + 4 >= p.live);
+                ++sn;
+                if (!ok) break;
             }
             if (!ok) break;
 
             // ---- the unit's end: the two halves' states, each with half of the channels
             const int mine = (p.live - t + 1) / 2;  // tiles of this half
             if (mine > 0) {
-                const bool got = watch.wait(bar(bars->pv_done[t]), (sn - 1) & 1);
-                if (!__all_sync(0xffffffffu, got)) break;
+                if (!wait_all(bar(bars->pv_done[t][0]), (sn - 1) & 1) ||
+                    !wait_all(bar(bars->pv_done[t][1]), (sn - 1) & 1))
+                    break;
             }
             float *own = state + ((jn & 1) * 2 + t) * 3 * R;
             own[r] = top;
