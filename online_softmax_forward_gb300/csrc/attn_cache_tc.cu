@@ -7,16 +7,13 @@
 // With 128 rows the products are no longer free, and one conversion of the codes
 // to fp16 serves all of them:
 //
-//   warps 8-11  load the codes of the keys and 12-15 those of the values, a tile
+//   warps 8-10  load the codes of the keys and 11-13 those of the values, a tile
 //               ahead in registers, convert them to fp16, exact, and write the
-//               MMA's 128-byte-swizzled tiles into two rings of stages (four warps
-//               each: a lane's rows are then 16 apart, and every address of a tile
-//               is one base and a constant);
+//               MMA's 128-byte-swizzled tiles into two rings of stages;
 //   warps 0-3   softmax of the even tiles (t = 0), 4-7 of the odd ones (t = 1), a
 //               thread per row: S_t out of tensor memory, the pages' scales
-//               applied per 16 keys, P_t as fp16 over the first half of S_t.  The
-//               first warp of each four issues its half's products, S_t = Q K_j^T
-//               and O_t += P_t V_j.
+//               applied per 16 keys, P_t as fp16 over the first half of S_t;
+//   warps 14-15 issue the products of t = 0 and 1, S_t = Q K_j^T and O_t += P_t V_j.
 //
 // The two warpgroups keep states of their own (top, rv, l and O_t, references moved
 // only when 32 weights would pass 2^10 or fp16's range, as in attn_cache_fwd.cu),
@@ -54,7 +51,9 @@ __device__ __forceinline__ uint4 ldg16(const uint8_t *p) {
 
 constexpr int R = 128;   // rows of a unit
 constexpr int KT = 128;  // keys of a tile
-constexpr int kConvertWarp0 = 8;  // 8 .. 11 keys, 12 .. 15 values
+constexpr int kConvertWarp0 = 8;  // 8 .. 10 keys, 11 .. 13 values
+constexpr int kConverters = 3;
+constexpr int kIssueWarp0 = 14;   // 14, 15
 constexpr int kThreads = 16 * 32;
 constexpr int kScaleRing = 8;       // tiles whose page scales are kept
 constexpr uint32_t kTmemCols = 512;
@@ -127,9 +126,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         ptx::mbar_init(bar(bars->q_full), 256);
         ptx::mbar_init(bar(bars->q_empty), 2);
         for (int s = 0; s < 4; ++s) {
-            ptx::mbar_init(bar(bars->k_full[s]), 128);
+            ptx::mbar_init(bar(bars->k_full[s]), kConverters * 32);
             ptx::mbar_init(bar(bars->k_empty[s]), 1);
-            ptx::mbar_init(bar(bars->v_full[s]), 128);
+            ptx::mbar_init(bar(bars->v_full[s]), kConverters * 32);
             ptx::mbar_init(bar(bars->v_empty[s]), 1);
         }
         for (int t = 0; t < 2; ++t) {
@@ -207,21 +206,95 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         p.live = max(0, min(p.left, (int)(((int64_t)seen + KT - 1) / KT) - p.t0));
         return p;
     };
-    if (warp >= kConvertWarp0) {
+    auto wait_all = [&](uint32_t b, uint32_t parity) {
+        return __all_sync(0xffffffffu, watch.wait(b, parity));
+    };
+    if (warp >= kIssueWarp0) {
+        // ------------------------------------------------------------ issuer of t's products
+        const int t = warp - kIssueWarp0;
+        uint32_t n = 0, qn = 0;   // tiles of t and units so far
+        uint32_t slot = 0;        // live tiles before the unit
+        bool ok = true;
+        // half h of S_t of the tile-th live one of the range; `last`: of t's in the unit
+        auto issue_s = [&](int h, uint32_t tile, bool last) {
+            const uint32_t st = tile % C::kKeyStages;
+            if (!wait_all(bar(bars->k_full[st]), (tile / C::kKeyStages) & 1)) return false;
+            ptx::tc_fence_after();
+            const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(sK + st * C::kTile + h * 64 * 128, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
+                ptx::mma_ss_warp(tmem + t * KT + h * 64, dq + off, dk + off, idesc_f16(false, R, 64, false), kk > 0 ? 1u : 0u);
+            }
+            ptx::mma_commit_warp(bar(bars->s_full[t][h]));
+            if (h == 1) {
+                ptx::mma_commit_warp(bar(bars->k_empty[st]));
+                if (last) ptx::mma_commit_warp(bar(bars->q_empty));
+            }
+            return true;
+        };
+        // O_t += P_t V_j for half h; `first` tile: O_t is set, once the last unit's epilogue has
+        // read it
+        auto issue_pv = [&](int h, uint32_t tile, bool first) {
+            const uint32_t st = tile % C::kValueStages;
+            if (!wait_all(bar(bars->v_full[st]), (tile / C::kValueStages) & 1) ||
+                !wait_all(bar(bars->p_full[t][h]), n & 1) ||
+                (first && h == 0 && !wait_all(bar(bars->o_empty), (qn & 1) ^ 1)))
+                return false;
+            ptx::tc_fence_after();
+            const uint64_t dv = sdesc(sV + st * C::kTile + h * 64 * 128, C::kChunkBytes, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                ptx::mma_ts_warp(tmem + 256 + t * D, tmem + t * KT + h * 64 + kk * 8,
+                                 dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_f16(false, R, D, true),
+                                 (!first || h > 0 || kk > 0) ? 1u : 0u);
+            ptx::mma_commit_warp(bar(bars->pv_done[t][h]));
+            if (h == 1) ptx::mma_commit_warp(bar(bars->v_empty[st]));
+            return true;
+        };
+        Place here = start;
+        for (int i = 0; i < n_tiles && ok;) {
+            const Piece p = piece_at(here, i);
+            if (p.live > 0) {
+                ok = wait_all(bar(bars->q_full), qn & 1);
+                if (ok && t >= p.live) ptx::mbar_arrive_warp(bar(bars->q_empty));  // a unit of one tile
+                if (ok && t < p.live)
+                    ok = issue_s(0, slot + t, t + 2 >= p.live) && issue_s(1, slot + t, t + 2 >= p.live);
+                for (int j = t; j < p.live && ok; j += 2) {
+                    // S_t of the next tile takes the place of P_t, half by half
+                    const bool more = j + 2 < p.live, last = j + 4 >= p.live;
+                    ok = issue_pv(0, slot + j, j < 2);
+                    if (ok && more) ok = wait_all(bar(bars->pv_done[t][0]), n & 1) && issue_s(0, slot + j + 2, last);
+                    ok = ok && issue_pv(1, slot + j, j < 2);
+                    if (ok && more) ok = wait_all(bar(bars->pv_done[t][1]), n & 1) && issue_s(1, slot + j + 2, last);
+                    ++n;
+                }
+                ++qn;
+            }
+            slot += p.live;
+            i += p.left;
+            if (i < n_tiles) advance(here, p.left, a.units, tiles);
+        }
+        // every MMA issued by this warp has completed before tensor memory is freed
+        ptx::mma_commit_warp(bar(bars->mma_done[t]));
+        watch.drain(bar(bars->mma_done[t]), 0);
+        __syncwarp();
+    } else if (warp >= kConvertWarp0) {
         // ------------------------------------------------------------ converters
-        const bool values = warp >= kConvertWarp0 + 4;
-        const int cw = warp & 3;
+        const bool values = warp >= kConvertWarp0 + kConverters;
+        const int cw = warp - kConvertWarp0 - (values ? kConverters : 0);
         const int page_shift = 31 - __clz(a.page);
-        // A warp's load covers 512 bytes: kRows rows of the tile, rows 4 kRows apart from load to
-        // load.  Row and 16-byte piece of a lane: for d = 128 the two halves of a row are not
-        // written in the same quarter of the warp, whose lanes would meet in the same banks
-        constexpr int kRows = 512 / D, N = KT / (4 * kRows);
-        const int rl = (D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2) + cw * kRows;
+        // A warp's load covers 512 bytes, kRows rows of the tile: load e rows
+        // (cw + 3 e) kRows on.  Row and 16-byte piece of a lane: for d = 128 the two halves of a
+        // row are not written in the same quarter of the warp, whose lanes would meet in the same
+        // banks
+        constexpr int kRows = 512 / D, kIters = KT / kRows, N = (kIters + kConverters - 1) / kConverters;
+        const int rl = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
         const int ql = D == 128 ? (lane & 3) + ((lane >> 3) & 1) * 4 : lane & 3;
-        const uint8_t *src = (values ? a.v : a.k) + (rl & 15) * D + ql * 16;
-        const uint32_t line = (values ? sV : sK) + (ql >> 2) * C::kChunkBytes + rl * 128;
-        const uint32_t to0 = line + (((ql & 3) * 2 ^ (rl & 7)) << 4);
-        const uint32_t to1 = line + (((ql & 3) * 2 + 1 ^ (rl & 7)) << 4);
+        const uint8_t *src = (values ? a.v : a.k) + rl * D + ql * 16;
+        const uint32_t line = (values ? sV : sK) + (ql >> 2) * C::kChunkBytes + (cw * kRows + rl) * 128;
+        // 16-byte places in the swizzled line: the row's bit 2 changes from load to load at d = 128
+        const uint32_t in_line = (uint32_t)((ql & 3) * 2) ^ (uint32_t)((cw * kRows + rl) & 7);
         uint64_t *full = values ? bars->v_full : bars->k_full;
         uint64_t *empty = values ? bars->v_empty : bars->k_empty;
         const uint32_t stages = values ? C::kValueStages : C::kKeyStages;
@@ -256,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         uint32_t miss = 0;   // pieces of the tile that are not there
         int key0 = 0, len = 0, ring = 0;
         bool have = false;
-        // load e of the tile at (p, j): rows rl + 4 kRows e
-        auto load = [&](int e) {
-            const int seg = __shfl_sync(0xffffffffu, at, (4 * kRows * e + cw * kRows) >> 4);
-            if (seg >= 0) raw[e] = ldg16(src + (size_t)seg * (16 * D));
+        auto load = [&](int e) {  // of the tile at (p, j)
+            const int row = (cw + kConverters * e) * kRows;
+            const int seg = __shfl_sync(0xffffffffu, at, (row >> 4) & 7);
+            if (row < KT && seg >= 0) raw[e] = ldg16(src + (size_t)seg * (16 * D) + (row & 15) * D);
         };
         // what was just loaded becomes the tile to convert; on to the next
         auto take = [&] {
@@ -307,15 +380,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                 U::quad(raw[e].z, h[4], h[5]);
                 U::quad(raw[e].w, h[6], h[7]);
                 load(e);
-                if (part) {
-                    const int row = rl + 4 * kRows * e;
-                    if (row >= held || (miss >> (row >> 4) & 1)) {
+                const int row = (cw + kConverters * e) * kRows + rl;
+                if (part && (row >= held || (miss >> (row >> 4 & 7) & 1))) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) h[k] = 0;
-                    }
+                    for (int k = 0; k < 8; ++k) h[k] = 0;
                 }
-                ptx::st_shared_v4(to0 + off + e * (4 * kRows * 128), h[0], h[1], h[2], h[3]);
-                ptx::st_shared_v4(to1 + off + e * (4 * kRows * 128), h[4], h[5], h[6], h[7]);
+                if (e < N - 1 || row < KT) {
+                    const uint32_t to = line + off + e * (kConverters * kRows * 128);
+                    const uint32_t in = in_line ^ (uint32_t)((e * kConverters * kRows) & 7);
+                    ptx::st_shared_v4(to + (in << 4), h[0], h[1], h[2], h[3]);
+                    ptx::st_shared_v4(to + ((in ^ 1) << 4), h[4], h[5], h[6], h[7]);
+                }
             }
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(bar(full[st]));
@@ -335,47 +410,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         uint32_t slot = 0;  // live tiles before the unit
         bool ok = true;
         Place here = start;
-        // ---- this half's products, issued by its first warp
-        auto wait_all = [&](uint32_t b, uint32_t parity) {
-            return __all_sync(0xffffffffu, watch.wait(b, parity));
-        };
-        // half h of S_t of a tile, the tile-th live one of the range; `last` of the unit's for t
-        auto issue_s = [&](int h, uint32_t tile, bool last) {
-            const uint32_t st = tile % C::kKeyStages;
-            if (!wait_all(bar(bars->k_full[st]), (tile / C::kKeyStages) & 1)) return false;
-            ptx::tc_fence_after();
-            const uint64_t dq = sdesc(sQ, 16, 1024), dk = sdesc(sK + st * C::kTile + h * 64 * 128, 16, 1024);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
-                ptx::mma_ss_warp(tmem + t * KT + h * 64, dq + off, dk + off, idesc_f16(false, R, 64, false), kk > 0 ? 1u : 0u);
-            }
-            ptx::mma_commit_warp(bar(bars->s_full[t][h]));
-            if (h == 1) {
-                ptx::mma_commit_warp(bar(bars->k_empty[st]));
-                if (last) ptx::mma_commit_warp(bar(bars->q_empty));
-            }
-            return true;
-        };
-        // O_t += P_t V_j for half h; `first` tile: O_t is set, once the last unit's epilogue has
-        // read it.  n: this warpgroup's tiles before
-        auto issue_pv = [&](int h, uint32_t tile, bool first, uint32_t n, uint32_t units_done) {
-            const uint32_t st = tile % C::kValueStages;
-            if (!wait_all(bar(bars->v_full[st]), (tile / C::kValueStages) & 1) ||
-                !wait_all(bar(bars->p_full[t][h]), n & 1) ||
-                (first && h == 0 && !wait_all(bar(bars->o_empty), (units_done & 1) ^ 1)))
-                return false;
-            ptx::tc_fence_after();
-            const uint64_t dv = sdesc(sV + st * C::kTile + h * 64 * 128, C::kChunkBytes, 1024);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                ptx::mma_ts_warp(tmem + 256 + t * D, tmem + t * KT + h * 64 + kk * 8,
-                                 dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_f16(false, R, D, true),
-                                 (!first || h > 0 || kk > 0) ? 1u : 0u);
-            ptx::mma_commit_warp(bar(bars->pv_done[t][h]));
-            if (h == 1) ptx::mma_commit_warp(bar(bars->v_empty[st]));
-            return true;
-        };
         for (int i = 0; i < n_tiles && ok;) {
             const Piece p = piece_at(here, i);
             int qi, h;
@@ -429,10 +463,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                 if (!__all_sync(0xffffffffu, watch.wait(bar(bars->q_full), qn & 1))) break;
                 ++qn;
                 cq = a.sl2 * back[r];
-                if (wq == 0) {
-                    if (t >= p.live) ptx::mbar_arrive_warp(bar(bars->q_empty));  // a unit of one tile
-                    else if (!issue_s(0, slot + t, t + 2 >= p.live) || !issue_s(1, slot + t, t + 2 >= p.live)) break;
-                }
             }
             float top = kUnset, rv = 0x1p100f, l = 0.f;
             for (int j = t; j < p.live; j += 2) {
@@ -543,13 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                                 sum *= alpha;
                                 top = nt;
                                 rv = nv;
-                                // O_t holds the tiles before (S(j) came after their products), and
-                                // this tile's first half
-                                if (half == 1) {
-                                    ok = wait_all(bar(bars->pv_done[t][0]), sn & 1);
-                                    ptx::tc_fence_after();
-                                }
+                                // O_t holds the tiles before and this one's first half
                                 if (j > 1 || half == 1) {
+                                    ok = half == 1 ? wait_all(bar(bars->pv_done[t][0]), sn & 1)
+                                                   : wait_all(bar(bars->pv_done[t][1]), (sn - 1) & 1);
+                                    ptx::tc_fence_after();
 #pragma unroll 1
                                     for (int c = 0; c < D / 16; ++c) {
                                         uint32_t o[16];
@@ -602,14 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                     }
                     ptx::tc_fence_before();
                     ptx::mbar_arrive(bar(bars->p_full[t][half]));
-                    if (wq == 0) {
-                        __syncwarp();
-                        ok = ok && issue_pv(half, slot + j, j < 2, sn, qn - 1);
-                    }
                 }
-                if (ok && wq == 0 && j + 2 < p.live)  // S_t takes the place of P_t, half by half
-                    ok = wait_all(bar(bars->pv_done[t][0]), sn & 1) && issue_s(0, slot + j + 2, j + 4 >= p.live) &&
-                         wait_all(bar(bars->pv_done[t][1]), sn & 1) && issue_s(1, slot + j + 2, j + 4 >= p.live);
                 ++sn;
                 if (!ok) break;
             }
@@ -694,13 +715,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             i += p.left;
             if (i < n_tiles) advance(here, p.left, a.units, tiles);
         }
-        // every MMA issued by this warp has completed before tensor memory is freed
-        __syncwarp();
-        if (wq == 0) {
-            ptx::mma_commit_warp(bar(bars->mma_done[t]));
-            watch.drain(bar(bars->mma_done[t]), 0);
-        }
-        __syncwarp();
     }
 
     ptx::tc_fence_before();
