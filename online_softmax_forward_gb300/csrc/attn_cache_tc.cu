@@ -16,7 +16,7 @@
 //   warps 14-15 issue the products of t = 0 and 1, S_t = Q K_j^T and O_t += P_t V_j.
 //
 // The two warpgroups keep states of their own (top, rv, l and O_t, references moved
-// only when 32 weights would pass 2^10 or fp16's range, as in attn_cache_fwd.cu),
+// only when 16 weights would pass 2^10 or fp16's range, as in attn_cache_fwd.cu),
 // so that one exponentiates while the other's products run; they are joined when
 // the unit ends.  P in fp16 is rounded by 2^-12, so this kernel serves the 16-bit
 // outputs.  A warp without a real row (few drafts, few heads) only keeps step.
@@ -25,9 +25,8 @@
 // is full with S_0 [0, 128), S_1 [128, 256), O_0 from 256 and O_1 from 256 + D, so
 // P of a half lies over the first half of its S, and S_t(j + 2) of a half waits for
 // the product that reads it; the other half keeps the tensor cores and the warps
-// busy meanwhile.  S is taken and P put in its place 32 keys at a time, the next 32
-// on their way, so that 16 warps fit the SM's registers.  Every wait is bounded, as
-// in attn_tc.cu.
+// busy meanwhile, and 64 weights are what the registers of 16 warps hold.  Every
+// wait is bounded, as in attn_tc.cu.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -56,8 +55,9 @@ constexpr int kConverters = 3;
 constexpr int kIssueWarp0 = 14;   // 14, 15
 constexpr int kThreads = 16 * 32;
 constexpr int kScaleRing = 8;       // tiles whose page scales are kept
+constexpr int kScaleWords = 20;     // 8 of keys, 8 of values, the pieces that are missing; 16-byte steps
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLargest = 1024.f;  // of 32 keys' sum of weights; 32 * 1024 fits fp16
+constexpr float kLargest = 1024.f;  // of 16 keys' sum of weights; 32 * 1024 fits fp16
 constexpr float kBase = 32.f;       // page scale times rv, at its largest after a move
 
 struct Bars {
@@ -80,8 +80,8 @@ struct Cfg {
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kTile;
     static constexpr int kOffV = kOffK + kKeyStages * kTile;
-    static constexpr int kOffScale = kOffV + kValueStages * kTile;       // [ring][2][8] fp32
-    static constexpr int kOffBack = kOffScale + kScaleRing * 16 * 4;     // [2][128] fp32
+    static constexpr int kOffScale = kOffV + kValueStages * kTile;       // [ring][words]
+    static constexpr int kOffBack = kOffScale + kScaleRing * kScaleWords * 4;     // [2][128] fp32
     static constexpr int kOffState = kOffBack + 2 * R * 4;               // [2][2][3][128] fp32
     static constexpr int kOffBar = kOffState + 2 * 2 * 3 * R * 4;
     static constexpr int kOffPrefix = kOffBar + 512;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         settle();
         int at = find();
         uint4 raw[N];
-        float scale = 0.f;   // lanes 0-7: of the tile's keys, 8-15: of its values
+        float scale = 0.f;   // lanes 0-7: of the tile's keys, 8-15: of its values, 16: `miss`
         uint32_t miss = 0;   // pieces of the tile that are not there
         int key0 = 0, len = 0, ring = 0;
         bool have = false;
@@ -341,8 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             if (!have) return;
             if (warp == kConvertWarp0) {
                 const int seg = __shfl_sync(0xffffffffu, at, lane & 7);
-                // an infinite key scale marks a piece that is not there
-                scale = lane < 8 ? INFINITY : 0.f;
+                scale = lane == 16 ? __uint_as_float(miss) : 0.f;
                 if (lane < 16 && seg >= 0) scale = (lane < 8 ? a.ks : a.vs)[seg >> (page_shift - 4)];
             }
             key0 = (p.t0 + j) * KT;
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         while (have) {
             if (!__all_sync(0xffffffffu, watch.wait(bar(empty[st]), (lap & 1) ^ 1))) break;
             if (warp == kConvertWarp0) {
-                if (lane < 16) scales[ring * 16 + lane] = scale;
+                if (lane < 17) scales[ring * kScaleWords + lane] = scale;
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(bars->sc_full[ring]));
             }
@@ -468,14 +467,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             for (int j = t; j < p.live; j += 2) {
                 const uint32_t ring = (slot + j) % kScaleRing, lap = (slot + j) / kScaleRing;
                 ok = wait_all(bar(bars->sc_full[ring]), lap & 1);
-                const float *ks = scales + ring * 16, *vs = ks + 8;
+                const float *ks = scales + ring * kScaleWords, *vs = ks + 8;
                 const int key0 = (p.t0 + j) * KT;
-                bool edge = false;
+                uint32_t miss = 0;
+                bool edge = false;  // a row of this warp does not see every key
                 if (ok && !idle) {
-                    bool hole = false;
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) hole = hole || ks[s] == INFINITY;
-                    edge = __any_sync(0xffffffffu, hole || key0 + KT > lim);
+                    miss = __float_as_uint(ks[16]);
+                    edge = __any_sync(0xffffffffu, miss != 0 || key0 + KT > lim);
                 }
 #pragma unroll 1
                 for (int half = 0; half < 2 && ok; ++half) {
@@ -484,148 +482,120 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                     ptx::tc_fence_after();
                     if (!idle) {
                         const uint32_t tH = tS + half * 64;
-                        float sum = 0.f;
-                        uint32_t s[32];
-                        ptx::tmem_ld32(tH, s);
-                        ptx::tmem_wait_ld();
-                        reg_fence(s);
-#pragma unroll 1
-                        for (int step = 0; step < 2; ++step) {  // 32 keys, 16 of one page and 16
-                            // the next 32 on their way (the second step's are not used); they are
-                            // waited for before the step ends, so that no copy is made too early
-                            uint32_t next[32];
-                            ptx::tmem_ld32(tH + 32, next);
-                            const int seg = half * 4 + step * 2;
-                            float f[2], sv[2], cv[2];
-                            int n[2];
+                        uint32_t s0[32], s1[32];
+                        ptx::tmem_ld32(tH, s0);
+                        ptx::tmem_ld32(tH + 32, s1);
+                        // four pieces of 16 keys, each of one page: the first key that the row does
+                        // not see, and the values' scale.  A page no key of which the row sees adds
+                        // nothing, not even its scale's NaN
+                        int n[4];
+                        float f[4], sv[4];
+                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + half * 4);
+                        const float4 v4 = *reinterpret_cast<const float4 *>(vs + half * 4);
+                        f[0] = k4.x * cq; f[1] = k4.y * cq; f[2] = k4.z * cq; f[3] = k4.w * cq;
+                        sv[0] = v4.x; sv[1] = v4.y; sv[2] = v4.z; sv[3] = v4.w;
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                const float kscale = ks[seg + g];
-                                f[g] = kscale * cq;
-                                n[g] = edge ? (kscale == INFINITY ? 0 : lim - (key0 + (seg + g) * 16)) : 16;
-                                // a page no key of which the row sees adds nothing, not even its
-                                // scale's NaN
-                                sv[g] = n[g] > 0 ? vs[seg + g] : 0.f;
-                                cv[g] = sv[g] * rv;
+                        for (int g = 0; g < 4; ++g) {
+                            n[g] = 16;
+                            if (edge) {
+                                n[g] = (miss >> (half * 4 + g) & 1) ? 0 : lim - (key0 + half * 64 + g * 16);
+                                if (n[g] <= 0) sv[g] = 0.f;
                             }
-                            float2 part[2][2];
-                            auto weights = [&] {  // of s, in place; their sums of each 16
+                        }
+                        float all[4];  // sums of the weights of each 16
+                        auto weights = [&] {  // of s0 and s1, in place
 #pragma unroll
-                                for (int g = 0; g < 2; ++g) {
-                                    const float2 f2 = make_float2(f[g], f[g]), t2 = make_float2(-top, -top);
-                                    part[g][0] = part[g][1] = make_float2(0.f, 0.f);
+                            for (int g = 0; g < 4; ++g) {
+                                const float2 f2 = make_float2(f[g], f[g]), t2 = make_float2(-top, -top);
+                                float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                                uint32_t *s = (g < 2 ? s0 : s1) + (g & 1) * 16;
 #pragma unroll
-                                    for (int e = 0; e < 16; e += 2) {
-                                        uint32_t &s0 = s[g * 16 + e], &s1 = s[g * 16 + e + 1];
-                                        float2 z = __ffma2_rn(make_float2(__uint_as_float(s0), __uint_as_float(s1)), f2, t2);
-                                        z = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
-                                        part[g][(e >> 1) & 1] = __fadd2_rn(part[g][(e >> 1) & 1], z);
-                                        s0 = __float_as_uint(z.x);
-                                        s1 = __float_as_uint(z.y);
-                                    }
+                                for (int e = 0; e < 16; e += 2) {
+                                    float2 z = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f2, t2);
+                                    z = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
+                                    part[(e >> 1) & 1] = __fadd2_rn(part[(e >> 1) & 1], z);
+                                    s[e] = __float_as_uint(z.x);
+                                    s[e + 1] = __float_as_uint(z.y);
                                 }
-                                if (!edge) return;
+                                part[0] = __fadd2_rn(part[0], part[1]);
+                                all[g] = part[0].x + part[0].y;
+                            }
+                            if (!edge) return;
 #pragma unroll
-                                for (int g = 0; g < 2; ++g) {  // again without what is not seen
-                                    part[g][0] = part[g][1] = make_float2(0.f, 0.f);
+                            for (int g = 0; g < 4; ++g) {  // again without what is not seen
+                                uint32_t *s = (g < 2 ? s0 : s1) + (g & 1) * 16;
+                                all[g] = 0.f;
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        if (e >= n[g]) s[g * 16 + e] = 0;
-                                        part[g][0].x += __uint_as_float(s[g * 16 + e]);
-                                    }
+                                for (int e = 0; e < 16; ++e) {
+                                    if (e >= n[g]) s[e] = 0;
+                                    all[g] += __uint_as_float(s[e]);
                                 }
-                            };
+                            }
+                        };
+                        ptx::tmem_wait_ld();
+                        reg_fence(s0);
+                        reg_fence(s1);
+                        weights();
+                        const float most = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+                        const float heavy = fmaxf(fmaxf(all[0] * sv[0], all[1] * sv[1]), fmaxf(all[2] * sv[2], all[3] * sv[3]));
+                        if (__any_sync(0xffffffffu, most > kLargest || heavy * rv > kLargest * kBase)) {
+                            // new references: the scores' maximum, and the pages' scale unless what
+                            // O holds is larger by now
+                            ptx::tmem_ld32(tH, s0);
+                            ptx::tmem_ld32(tH + 32, s1);
+                            ptx::tmem_wait_ld();
+                            reg_fence(s0);
+                            reg_fence(s1);
+                            float mx = -INFINITY, scale = 0.f;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const uint32_t *s = (g < 2 ? s0 : s1) + (g & 1) * 16;
+                                scale = fmaxf(scale, sv[g]);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (e < n[g]) mx = fmaxf(mx, __uint_as_float(s[e]) * f[g]);
+                            }
+                            const float nt = fmaxf(top, mx);
+                            const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
+                            const float was = alpha * kBase / rv;
+                            const float nv = mx == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, scale), 0x1p-95f);
+                            const float to = alpha * (nv / rv);
+                            l *= alpha;
+                            top = nt;
+                            rv = nv;
                             weights();
-                            float all[2];
-                            auto add = [&] {
-#pragma unroll
-                                for (int g = 0; g < 2; ++g) {
-                                    const float2 x = __fadd2_rn(part[g][0], part[g][1]);
-                                    all[g] = x.x + x.y;
-                                }
-                            };
-                            add();
-                            if (__any_sync(0xffffffffu, fmaxf(all[0], all[1]) > kLargest ||
-                                                            fmaxf(all[0] * cv[0], all[1] * cv[1]) > kLargest * kBase)) {
-                                // new references: the scores' maximum, and the pages' scale unless
-                                // what O holds is larger by now.  S of the step is still there
-                                __syncwarp();
-                                ptx::tmem_wait_ld();
-                                reg_fence(next);
-                                ptx::tmem_wait_st();
-                                ptx::tmem_ld32(tH + step * 32, s);
-                                ptx::tmem_wait_ld();
-                                reg_fence(s);
-                                float mx = -INFINITY, most = 0.f;
-#pragma unroll
-                                for (int g = 0; g < 2; ++g) {
-                                    most = fmaxf(most, sv[g]);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        if (e < n[g]) mx = fmaxf(mx, __uint_as_float(s[g * 16 + e]) * f[g]);
-                                }
-                                const float nt = fmaxf(top, mx);
-                                const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
-                                const float was = alpha * kBase / rv;
-                                const float nv = mx == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, most), 0x1p-95f);
-                                const float to = alpha * (nv / rv);
-                                l *= alpha;
-                                sum *= alpha;
-                                top = nt;
-                                rv = nv;
-                                // O_t holds the tiles before and this one's first half
-                                if (j > 1 || half == 1) {
-                                    ok = half == 1 ? wait_all(bar(bars->pv_done[t][0]), sn & 1)
-                                                   : wait_all(bar(bars->pv_done[t][1]), (sn - 1) & 1);
-                                    ptx::tc_fence_after();
+                            // O_t holds the tiles before and this one's first half
+                            if (j > 1 || half == 1) {
+                                ok = half == 1 ? wait_all(bar(bars->pv_done[t][0]), sn & 1)
+                                               : wait_all(bar(bars->pv_done[t][1]), (sn - 1) & 1);
+                                ptx::tc_fence_after();
 #pragma unroll 1
-                                    for (int c = 0; c < D / 16; ++c) {
-                                        uint32_t o[16];
-                                        __syncwarp();
-                                        ptx::tmem_ld16(tO + c * 16, o);
-                                        ptx::tmem_wait_ld();
-                                        reg_fence(o);
-#pragma unroll
-                                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * to);
-                                        ptx::tmem_st16(tO + c * 16, o);
-                                    }
-                                }
-                                if (step == 1) {  // the half's first 32 weights
+                                for (int c = 0; c < D / 16; ++c) {
                                     uint32_t o[16];
-                                    ptx::tmem_ld16(tH, o);
+                                    __syncwarp();
+                                    ptx::tmem_ld16(tO + c * 16, o);
                                     ptx::tmem_wait_ld();
                                     reg_fence(o);
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&o[e]));
-                                        o[e] = pack_f16(x.x * to, x.y * to);
-                                    }
-                                    ptx::tmem_st16(tH, o);
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * to);
+                                    ptx::tmem_st16(tO + c * 16, o);
                                 }
-                                ptx::tmem_wait_st();
-#pragma unroll
-                                for (int g = 0; g < 2; ++g) cv[g] = sv[g] * rv;
-                                weights();
-                                add();
                             }
-                            sum += all[0] + all[1];
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int g = 0; g < 2; ++g)
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float2 x = __fmul2_rn(
-                                        make_float2(__uint_as_float(s[g * 16 + 2 * e]), __uint_as_float(s[g * 16 + 2 * e + 1])),
-                                        make_float2(cv[g], cv[g]));
-                                    pk[g * 8 + e] = pack_f16(x.x, x.y);
-                                }
-                            ptx::tmem_wait_ld();
-                            reg_fence(next);
-                            ptx::tmem_st16(tH + step * 16, pk);  // over columns already taken
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) s[e] = next[e];
                         }
-                        l += sum;
+                        l += (all[0] + all[1]) + (all[2] + all[3]);
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const uint32_t *s = (g < 2 ? s0 : s1) + (g & 1) * 16;
+                            const float2 c2 = make_float2(sv[g] * rv, sv[g] * rv);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 x = __fmul2_rn(
+                                    make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2);
+                                pk[g * 8 + e] = pack_f16(x.x, x.y);
+                            }
+                        }
+                        ptx::tmem_st32(tH, pk);  // over columns already taken
                         ptx::tmem_wait_st();
                     }
                     ptx::tc_fence_before();
