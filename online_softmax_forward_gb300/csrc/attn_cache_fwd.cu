@@ -676,7 +676,7 @@ int launch_fwd_w(const FwdArgs &a, bool wide, int kt, unsigned grid, cudaStream_
 
 // Query rows per kv head from which the 128-row tcgen05 kernel runs (16-bit
 // outputs, all pages).
-constexpr int64_t kTcRows = 17;
+constexpr int64_t kTcRows = 33;
 static bool cache_tc(int64_t rows, int dtype, bool listed) {
     return !listed && (dtype == ATTN_BF16 || dtype == ATTN_F16) && rows >= kTcRows;
 }

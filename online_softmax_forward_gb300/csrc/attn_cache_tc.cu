@@ -57,6 +57,9 @@ constexpr int kThreads = 16 * 32;
 constexpr int kScaleRing = 8;       // tiles whose page scales are kept
 constexpr int kScaleWords = 20;     // 8 of keys, 8 of values, the pieces that are missing; 16-byte steps
 constexpr uint32_t kTmemCols = 512;
+// What a second unit costs a CTA (its queries, the first scores, the join), in tiles:
+// about 20 000 clocks against 3 000 a tile.
+constexpr int kSwitch = 6;
 constexpr float kLargest = 1024.f;  // of 16 keys' sum of weights; 32 * 1024 fits fp16
 constexpr float kBase = 32.f;       // page scale times rv, at its largest after a move
 
@@ -160,28 +163,39 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         if (a.lse)
             for (size_t e = threadIdx.x; e < n; e += kThreads) a.lse[row0 + e] = -INFINITY;
     }
+    auto tiles = [&](int b) { return prefix[b + 1] - prefix[b]; };
     const int64_t workers = worker_count(total, a.workers, 1);
     int64_t x0 = 0;
     int n_tiles = 0;
-    if (blockIdx.x < workers && total > 0) {
+    Place start = {0, 0, 0, 1};
+    // Equal ranges, or a unit each where that is no longer for the longest one
+    int longest = 0;
+    for (int b = threadIdx.x; b < a.B; b += kThreads) longest = max(longest, tiles(b));
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) warp_sums[threadIdx.x >> 5] = longest;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) longest = max(longest, warp_sums[w]);
+    const int64_t all_units = (int64_t)a.B * a.units;
+    const bool one_each = all_units <= gridDim.x && longest <= (total + workers - 1) / workers + kSwitch;
+    int4 tail = make_int4(0, 0, 0, 0);  // the unit that runs over the end of the range, if it began in it
+    if (one_each) {
+        if (blockIdx.x < all_units) {
+            start.b = blockIdx.x / a.units;
+            start.unit = blockIdx.x - start.b * a.units;
+            start.n = n_tiles = tiles(start.b);
+        }
+    } else if (blockIdx.x < workers && total > 0) {
         x0 = worker_begin(blockIdx.x, total, workers);
         n_tiles = (int)(worker_begin(blockIdx.x + 1, total, workers) - x0);
+        start = place_of(a, prefix, 0, x0);
+        const int64_t x1 = x0 + n_tiles;
+        const Place p = place_of(a, prefix, 0, x1 - 1);
+        const int64_t end = x1 - 1 - p.t + p.n;
+        if (end > x1 && x1 - 1 - p.t >= x0)
+            tail = make_int4(1, (int)worker_of(end - 1, total, workers), p.b, p.unit);
     }
-    auto tiles = [&](int b) { return prefix[b + 1] - prefix[b]; };
-    Place start = {0, 0, 0, 1};
-    if (n_tiles > 0) start = place_of(a, prefix, 0, x0);
-    if (threadIdx.x == 0) {
-        // the unit that runs over the end of the range, if it began in it
-        int4 d = make_int4(0, 0, 0, 0);
-        if (n_tiles > 0) {
-            const int64_t x1 = x0 + n_tiles;
-            const Place p = place_of(a, prefix, 0, x1 - 1);
-            const int64_t end = x1 - 1 - p.t + p.n;
-            if (end > x1 && x1 - 1 - p.t >= x0)
-                d = make_int4(1, (int)worker_of(end - 1, total, workers), p.b, p.unit);
-        }
-        a.tail[blockIdx.x] = d;
-    }
+    if (threadIdx.x == 0) a.tail[blockIdx.x] = tail;
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -443,9 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                         x.u[0] = q[e].u[0];
                         x.widen(f);
                     }
-                    float amax = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+                    float amax = fmaxf(ptx::max3(fabsf(f[0]), fabsf(f[1]), fabsf(f[2])),
+                                       ptx::max3(fabsf(f[3]), fabsf(f[4]), ptx::max3(fabsf(f[5]), fabsf(f[6]), fabsf(f[7]))));
 #pragma unroll
                     for (int o = 1; o < LR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                     float mul, inv;
@@ -535,6 +548,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                         ptx::tmem_wait_ld();
                         reg_fence(s0);
                         reg_fence(s1);
+                        float mx, scale;
+                        auto largest = [&] {  // visible score, and the pages' largest scale
+                            mx = -INFINITY;
+                            scale = 0.f;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const uint32_t *s = (g < 2 ? s0 : s1) + (g & 1) * 16;
+                                float m = -INFINITY;
+                                if (!edge) {
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2)
+                                        m = ptx::max3(m, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        if (e < n[g]) m = fmaxf(m, __uint_as_float(s[e]));
+                                }
+                                if (m != -INFINITY) mx = fmaxf(mx, m * f[g]);
+                                scale = fmaxf(scale, sv[g]);
+                            }
+                        };
+                        if (j < 2 && half == 0) {  // the unit's first references
+                            largest();
+                            top = fmaxf(top, mx);
+                            if (mx != -INFINITY) rv = kBase / fmaxf(scale, 0x1p-95f);
+                        }
                         weights();
                         const float most = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
                         const float heavy = fmaxf(fmaxf(all[0] * sv[0], all[1] * sv[1]), fmaxf(all[2] * sv[2], all[3] * sv[3]));
@@ -546,15 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                             ptx::tmem_wait_ld();
                             reg_fence(s0);
                             reg_fence(s1);
-                            float mx = -INFINITY, scale = 0.f;
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const uint32_t *s = (g < 2 ? s0 : s1) + (g & 1) * 16;
-                                scale = fmaxf(scale, sv[g]);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (e < n[g]) mx = fmaxf(mx, __uint_as_float(s[e]) * f[g]);
-                            }
+                            largest();
                             const float nt = fmaxf(top, mx);
                             const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
                             const float was = alpha * kBase / rv;
