@@ -609,7 +609,7 @@ def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
     shape = (B, cache.H_kv, S, cache.d)
     if out is None:
         k = torch.empty(shape, dtype=dtype, device=cache.device)
-        v = torch.empty_like(k)
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
     else:
         k, v = out
         _check_out(k, shape, dtype, cache.device, "out[0]")
@@ -703,8 +703,9 @@ def attention_cache(q, cache, table, lens, counts=None, causal: bool = True,
     handle = _handle(cache.device, stream)
     need = _need(attn_fwd_cache_workspace_size, B, H, cache.H_kv, Sq, cache.d, code, n_select)
     wp, wn, held = _workspace(workspace, need, cache, stream, handle)
-    out = torch.empty_like(q) if out_dtype is None else torch.empty_like(q, dtype=out_dtype)
-    lse = torch.empty((B, H, Sq), dtype=torch.float32, device=cache.device)
+    dev = cache.device
+    out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=dev)
+    lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
     _call_on(cache.device, load_library().attn_fwd_cache, cache.c, q.data_ptr(), out.data_ptr(),
              lse.data_ptr(), t, width, p, n, listed, n_select, B, H, Sq, 1 if causal else 0,
              0.0 if scale is None else float(scale), code, wp, wn, handle)

@@ -57,6 +57,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRing = 24 * 1024;  // shared memory of each warp's tiles, later of its states
 constexpr int kMinTiles = 1;  // tiles per worker when there are few
+constexpr int kOneEachTiles = 4 * kWarps;  // of a unit that one CTA takes
 
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
     uint4 u;
@@ -152,42 +153,64 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
 
     const int tpu = a.pages ? a.n_sel * (a.page / KT) : 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    int64_t total;
-    if (a.pages) {
-        total = (int64_t)a.B * a.units * tpu;
-        // lengths and counts out of range are reported here for a page list
-        if (blockIdx.x == 0)
-            for (int b = threadIdx.x; b < a.B; b += kThreads) {
-                const int len = a.lens[b], cnt = a.counts ? a.counts[b] : a.Sq;
-                if (len != clamp_len(len, a.max_pages, a.page) || cnt < 0 || cnt > a.Sq)
-                    atomicOr(a.status, kStatusTable);
-            }
-    } else {
-        scan_lengths<kThreads>(a, KT, prefix, warp_sums);
-        total = (int64_t)prefix[a.B] * a.units;
-        // sequences without a token have no tile: o = 0, lse = -inf
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-            if (prefix[b] != prefix[b + 1]) continue;
-            const size_t row0 = (size_t)b * a.Hkv * a.G * a.Sq, n = (size_t)a.Hkv * a.G * a.Sq;
+    int64_t total = 0, workers = kWarps;
+    int64_t x0 = 0;
+    int w = warp, n_tiles = 0;  // this warp's range
+    Place here = {0, 0, 0, 1};
+    auto tiles = [&](int b) { return a.pages ? tpu : prefix[b + 1] - prefix[b]; };
+    auto report = [&](int b) {  // a length or count out of range
+        const int len = a.lens[b], cnt = a.counts ? a.counts[b] : a.Sq;
+        if (len != clamp_len(len, a.max_pages, a.page) || cnt < 0 || cnt > a.Sq)
+            atomicOr(a.status, kStatusTable);
+    };
+    if (lane == 0) s_has[warp] = 0;
+    if (a.one_each) {
+        here.b = (int)((uint32_t)blockIdx.x / a.by_units);
+        here.unit = blockIdx.x - here.b * a.units;
+        if (here.unit == 0 && threadIdx.x == 0) report(here.b);
+        here.n = a.pages ? tpu : (clamp_len(a.lens[here.b], a.max_pages, a.page) + KT - 1) / KT;
+        const int64_t share = worker_count(here.n, kWarps, 1);
+        if (warp < share) {
+            here.t = (int)worker_begin(warp, here.n, share);
+            n_tiles = (int)worker_begin(warp + 1, here.n, share) - here.t;
+        }
+        if (here.n == 0) {  // no token: o = 0, lse = -inf
+            const Unit u = unit_at(a, here.b, here.unit);
             const float z[8] = {};
-            for (size_t e = threadIdx.x; e < n * (D / 8); e += kThreads) store_o8(a, row0 * D + e * 8, z);
-            if (a.lse)
-                for (size_t e = threadIdx.x; e < n; e += kThreads) a.lse[row0 + e] = -INFINITY;
+            for (int e = threadIdx.x; e < R * (D / 8); e += kThreads) {
+                size_t row;
+                if (!out_row<R>(a, u, e / (D / 8), row)) continue;
+                store_o8(a, row * D + e % (D / 8) * 8, z);
+                if (a.lse && e % (D / 8) == 0) a.lse[row] = -INFINITY;
+            }
+            return;
+        }
+    } else {
+        if (a.pages) {
+            total = (int64_t)a.B * a.units * tpu;
+            if (blockIdx.x == 0)
+                for (int b = threadIdx.x; b < a.B; b += kThreads) report(b);
+        } else {
+            scan_lengths<kThreads>(a, KT, prefix, warp_sums);
+            total = (int64_t)prefix[a.B] * a.units;
+            // sequences without a token have no tile: o = 0, lse = -inf
+            for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+                if (prefix[b] != prefix[b + 1]) continue;
+                const size_t row0 = (size_t)b * a.Hkv * a.G * a.Sq, n = (size_t)a.Hkv * a.G * a.Sq;
+                const float z[8] = {};
+                for (size_t e = threadIdx.x; e < n * (D / 8); e += kThreads) store_o8(a, row0 * D + e * 8, z);
+                if (a.lse)
+                    for (size_t e = threadIdx.x; e < n; e += kThreads) a.lse[row0 + e] = -INFINITY;
+            }
+        }
+        workers = worker_count(total, a.workers, kMinTiles);
+        w += blockIdx.x * kWarps;
+        if (w < workers && total > 0) {
+            x0 = worker_begin(w, total, workers);
+            n_tiles = (int)(worker_begin(w + 1, total, workers) - x0);
+            here = place_of(a, prefix, tpu, x0);
         }
     }
-    const int64_t workers = worker_count(total, a.workers, kMinTiles);
-    const int w = blockIdx.x * kWarps + warp;
-    int64_t x0 = 0;
-    int n_tiles = 0;  // of this warp's range
-    if (w < workers && total > 0) {
-        x0 = worker_begin(w, total, workers);
-        n_tiles = (int)(worker_begin(w + 1, total, workers) - x0);
-    }
-    if (lane == 0) s_has[warp] = 0;
-    auto tiles = [&](int b) { return a.pages ? tpu : prefix[b + 1] - prefix[b]; };
-
-    Place here = {0, 0, 0, 1};
-    if (n_tiles > 0) here = place_of(a, prefix, tpu, x0);
     // lane: tile 32 k + lane of the range, and the one 32 further
     Place mine = here;
     Tile cur = {-1, 0, 0.f, 0.f}, nxt = cur;
@@ -641,6 +664,7 @@ int launch_fwd_t(const FwdArgs &a, unsigned grid, cudaStream_t stream) {
         return ATTN_ERR_LAUNCH;
     fwd<<<grid, kThreads, ring + (a.pages ? 0 : ((size_t)a.B + 1) * 4), stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
+    if (a.one_each) return ATTN_OK;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, (unsigned)(a.rows < R ? a.rows : R));
     cfg.blockDim = dim3(kThreads);
@@ -731,6 +755,12 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     int64_t ctas = most / kWarps < sms ? (int64_t)(most / kWarps) + 1 : sms;
     if (ctas > kCacheMaxCtas) ctas = kCacheMaxCtas;
     if (ctas > sms) ctas = sms;
+    // Few units of few tiles, by the longest possible lengths: a CTA each.  Four tiles a warp
+    // take as long as one and the second kernel, which is then not launched (one sequence of
+    // 1000 tokens, 8 kv heads: 11.1 us either way on the device, 17.1 and 14.5 us a call)
+    const int longest = pages ? n_select * (c.page / kt) : (int)(((int64_t)max_pages * c.page + kt - 1) / kt);
+    a.one_each = units <= ctas && longest <= kOneEachTiles;
+    if (a.one_each) ctas = units;
     a.workers = (int)ctas * kWarps;
     a.tail = reinterpret_cast<int4 *>(workspace);
     a.hold = reinterpret_cast<float *>(a.tail + ctas);

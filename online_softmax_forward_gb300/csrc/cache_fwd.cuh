@@ -27,6 +27,7 @@ struct FwdArgs {
     int nseg, rows, nrb;  // row groups of a (sequence, kv head), rows of one, row blocks of one
     int units;            // of a sequence: Hkv * nseg * nrb
     int dtype, workers;
+    int one_each;         // a CTA per unit, and no state left for a second kernel
     FastDiv by_units, by_per, by_nrb, by_group;  // per = nseg * nrb
     float sl2;  // scale * log2(e)
     int *status;
