@@ -49,6 +49,7 @@
 #include "attn_internal.h"
 #include "cache_fwd.cuh"
 #include "cache_mma.cuh"
+#include "sm100_ptx.cuh"
 
 namespace attn {
 namespace {
@@ -357,26 +358,40 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                 if constexpr (!WIDE) {  // hi and lo parts of q
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        s[n][0] += s[n][2];
-                        s[n][1] += s[n][3];
+                        const float2 x = __fadd2_rn(make_float2(s[n][0], s[n][1]), make_float2(s[n][2], s[n][3]));
+                        s[n][0] = x.x;
+                        s[n][1] = x.y;
                     }
                 }
                 const bool edge = key0 + step + STEP > low;  // some row does not see every key
-                float p[H][2 * NT], c[H];
+                float2 p[H][NT];  // weights of keys 8 n + 2 t and the next
+                float c[H];
+                auto weights = [&](int hh) {
+                    const float f = ks * cq[hh];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float2 z = __ffma2_rn(make_float2(s[n][2 * hh], s[n][2 * hh + 1]), make_float2(f, f),
+                                                    make_float2(-top[hh], -top[hh]));
+                        p[hh][n] = make_float2(ex2(z.x), ex2(z.y));
+                    }
+                    if (edge) {
+                        const int seen = lim[hh] - (key0 + step + 2 * t);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            if (8 * n >= seen) p[hh][n].x = 0.f;
+                            if (8 * n + 1 >= seen) p[hh][n].y = 0.f;
+                        }
+                    }
+                };
                 bool far = false;
 #pragma unroll
                 for (int hh = 0; hh < H; ++hh) {
-                    const float f = ks * cq[hh];
                     // a page no key of which the row sees adds nothing, not even its scale's NaN
                     c[hh] = key0 < lim[hh] ? vs * rv[hh] : 0.f;
+                    weights(hh);
                     float most = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 2 * NT; ++e) {
-                        float z = fmaf(s[e >> 1][2 * hh + (e & 1)], f, -top[hh]);
-                        if (edge && key0 + step + 8 * (e >> 1) + 2 * t + (e & 1) >= lim[hh]) z = -INFINITY;
-                        p[hh][e] = ex2(z);
-                        most = fmaxf(most, p[hh][e]);
-                    }
+                    for (int n = 0; n < NT; ++n) most = ptx::max3(most, p[hh][n].x, p[hh][n].y);
                     far = far || most > 16.f || most * c[hh] > 32768.f;
                 }
                 if (__any_sync(0xffffffffu, far)) {
@@ -385,14 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
 #pragma unroll
                     for (int hh = 0; hh < H; ++hh) {
                         const float f = ks * cq[hh], sv = key0 < lim[hh] ? vs : 0.f;
+                        const int seen = lim[hh] - (key0 + step + 2 * t);
                         float mx = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 2 * NT; ++e) {
-                            float &y = p[hh][e];
-                            y = s[e >> 1][2 * hh + (e & 1)] * f;
-                            if (edge && key0 + step + 8 * (e >> 1) + 2 * t + (e & 1) >= lim[hh]) y = -INFINITY;
-                            mx = fmaxf(mx, y);
-                        }
+                        for (int e = 0; e < 2 * NT; ++e)
+                            if (!edge || 8 * (e >> 1) + (e & 1) < seen) mx = fmaxf(mx, s[e >> 1][2 * hh + (e & 1)] * f);
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                         const float nt = fmaxf(top[hh], mx);
@@ -413,28 +425,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                         top[hh] = nt;
                         rv[hh] = nv;
                         c[hh] = sv * nv;
-#pragma unroll
-                        for (int e = 0; e < 2 * NT; ++e) p[hh][e] = ex2(p[hh][e] - nt);
+                        weights(hh);
                     }
                 }
                 uint32_t pa[KS][4];
 #pragma unroll
                 for (int hh = 0; hh < H; ++hh) {
-                    float sum = 0.f;
+                    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        sum += p[hh][2 * n] + p[hh][2 * n + 1];
-                        const float w0 = p[hh][2 * n] * c[hh], w1 = p[hh][2 * n + 1] * c[hh];
-                        const uint32_t hi = pack_f16(w0, w1);
+                        sum = __fadd2_rn(sum, p[hh][n]);
+                        const float2 w = __fmul2_rn(p[hh][n], make_float2(c[hh], c[hh]));
+                        const uint32_t hi = pack_f16(w.x, w.y);
                         if constexpr (WIDE) {
                             pa[n / 2][(n & 1) * 2 + hh] = hi;
                         } else {
                             const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
                             pa[n / 2][(n & 1) * 2] = hi;
-                            pa[n / 2][(n & 1) * 2 + 1] = pack_f16(w0 - b.x, w1 - b.y);
+                            pa[n / 2][(n & 1) * 2 + 1] = pack_f16(w.x - b.x, w.y - b.y);
                         }
                     }
-                    l[hh] += sum;
+                    l[hh] += sum.x + sum.y;
                 }
 #pragma unroll
                 for (int st = 0; st < KS; ++st) {
