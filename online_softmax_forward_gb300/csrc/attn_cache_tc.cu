@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             if (i < n_tiles && lane < 8 && key < p.len) {
                 const int phys = a.table[(int64_t)p.u.b * a.max_pages + (key >> page_shift)];
                 if (phys < 0 || phys >= a.n_pages) atomicOr(a.status, kStatusTable);
-                else at = (((phys * a.Hkv + p.u.hk) << page_shift) + (key & (a.page - 1))) >> 4;
+                else at = ((phys * a.Hkv + p.u.hk) << (page_shift - 4)) + ((key & (a.page - 1)) >> 4);
             }
             return at;
         };
