@@ -286,7 +286,7 @@ ATTN_API int attn_merge(const float *o_parts, const float *lse_parts, int n_part
  *                   largest key code of each channel.  May be NULL: then
  *                   attn_cache_append keeps none and attn_cache_select refuses.
  *   page in {16, 32, 64, 128}; d in {64, 128}; format one of attn_cache_format;
- *   n_pages * H_kv * page / 16 < 2^31.
+ *   n_pages * H_kv * page / 16 < 2^31; max_pages * page <= 2^31 - 1025.
  * Nothing in the pool needs to be initialised.
  *
  * Sequences  table [B][max_pages] int32 names the pages of each sequence in
@@ -306,8 +306,8 @@ ATTN_API int attn_merge(const float *o_parts, const float *lse_parts, int n_part
  *   amax = 0.  Division by it is exact, so codes are x / s rounded once, to
  *   nearest, ties to even.  A NaN or an infinity makes the scale of its block
  *   NaN: everything read from that block and head is NaN until the page is
- *   started again at its first row.  attn_cache_read and attn_fwd_cache take
- *   any finite scale or NaN; pages that append continues must hold such powers of two.
+ *   started again at its first row.  attn_cache_read takes any scale, the
+ *   others any finite scale >= 0 or NaN; pages that append continues must hold such powers of two.
  */
 typedef enum attn_cache_format {
     ATTN_CACHE_E4M3 = 0, /* 4-bit exponent, 3-bit mantissa, no infinities; largest 448 */

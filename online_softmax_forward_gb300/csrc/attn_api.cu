@@ -255,9 +255,11 @@ static bool cache_overlap(const attn_cache &c, const void *p, size_t n) {
            overlap(p, n, c.k_bounds, blocks * 2 * c.d);
 }
 // The arrays of one call's sequences: table and lens (or pos), counts may be null.
-static bool sequences_ok(const int32_t *table, int max_pages, const int32_t *lens,
-                         const int32_t *counts, int B) {
+static bool sequences_ok(const attn_cache &c, const int32_t *table, int max_pages,
+                         const int32_t *lens, const int32_t *counts, int B) {
     if (B < 0 || max_pages < 1) return false;
+    // token positions, and the ends of tiles they lie in, fit 31 bits
+    if ((double)max_pages * c.page > (double)(INT32_MAX - 1024)) return false;
     if (B == 0) return true;
     return table && lens && aligned(table, 4) && aligned(lens, 4) && aligned(counts, 4);
 }
@@ -576,7 +578,7 @@ int attn_cache_append(const attn_cache *cache, const void *k, const void *v, con
                       int max_pages, const int32_t *pos, const int32_t *counts, int B, int S,
                       int dtype, void *stream) {
     const int dt = plain_dtype(dtype);
-    if (!cache_ok(cache) || dt < 0 || S < 0 || !sequences_ok(table, max_pages, pos, counts, B))
+    if (!cache_ok(cache) || dt < 0 || S < 0 || !sequences_ok(*cache, table, max_pages, pos, counts, B))
         return ATTN_ERR_INVALID_ARG;
     if (B == 0 || S == 0) return ATTN_OK;
     // one CTA per touched page, kv head and tensor
@@ -597,7 +599,7 @@ int attn_cache_append(const attn_cache *cache, const void *k, const void *v, con
 int attn_cache_read(const attn_cache *cache, const int32_t *table, int max_pages,
                     const int32_t *lens, void *k, void *v, int B, int S, int dtype, void *stream) {
     const int dt = plain_dtype(dtype);
-    if (!cache_ok(cache) || dt < 0 || S < 0 || !sequences_ok(table, max_pages, lens, nullptr, B))
+    if (!cache_ok(cache) || dt < 0 || S < 0 || !sequences_ok(*cache, table, max_pages, lens, nullptr, B))
         return ATTN_ERR_INVALID_ARG;
     if (B == 0 || S == 0) return ATTN_OK;
     if ((double)B * cache->H_kv * (S / cache->page + 1.0) * 2 > (double)INT32_MAX)
@@ -628,7 +630,7 @@ int attn_cache_select(const attn_cache *cache, const void *q, const int32_t *tab
                       size_t workspace_bytes, void *stream) {
     if (!cache_ok(cache) || !cache->k_bounds || !dtype_known(dtype) || Sq < 0 || H < 1 ||
         H % cache->H_kv != 0 || H / cache->H_kv > kMaxSelectGroup || n_select < 1 || n_select > kMaxSelectPages ||
-        (causal != 0 && causal != 1) || !sequences_ok(table, max_pages, lens, counts, B))
+        (causal != 0 && causal != 1) || !sequences_ok(*cache, table, max_pages, lens, counts, B))
         return ATTN_ERR_INVALID_ARG;
     size_t need = 0;
     if (attn_cache_select_workspace_size(B, cache->H_kv, Sq, max_pages, &need) != ATTN_OK)
@@ -667,7 +669,7 @@ int attn_fwd_cache(const attn_cache *cache, const void *q, void *o, float *lse,
                    const int32_t *table, int max_pages, const int32_t *lens, const int32_t *counts,
                    const int32_t *pages, int n_select, int B, int H, int Sq, int causal,
                    float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
-    if (!cache_ok(cache) || !sequences_ok(table, max_pages, lens, counts, B) ||
+    if (!cache_ok(cache) || !sequences_ok(*cache, table, max_pages, lens, counts, B) ||
         (causal != 0 && causal != 1) || (pages ? n_select < 1 : n_select != 0) || !aligned(pages, 4))
         return ATTN_ERR_INVALID_ARG;
     size_t need = 0;

@@ -208,7 +208,7 @@ def test_bad_caches_are_refused(lib, name, kw):
     ("append", dict(dtype=pkg.ATTN_BF16_OUT_F32)), ("append", dict(dtype=9)), ("append", dict(S=-1)),
     ("append", dict(B=-1)), ("append", dict(k=None)), ("append", dict(v=NV + 8)), ("append", dict(table=None)),
     ("append", dict(table=TABLE + 2)), ("append", dict(pos=None)), ("append", dict(counts=COUNTS + 1)),
-    ("append", dict(max_pages=0)), ("append", dict(k=K)), ("append", dict(v=KB)), ("append", dict(table=VS)),
+    ("append", dict(max_pages=0)), ("append", dict(max_pages=(2 ** 31 - 1024) // 16)), ("append", dict(k=K)), ("append", dict(v=KB)), ("append", dict(table=VS)),
     ("append", dict(counts=K + 64)), ("append", dict(B=1 << 20, S=1 << 20)),
     ("read", dict(dtype=pkg.ATTN_F16_OUT_F32)), ("read", dict(S=-1)), ("read", dict(k=None)),
     ("read", dict(v=NV + 4)), ("read", dict(v=NK + 64)), ("read", dict(k=K)), ("read", dict(v=KS)),
