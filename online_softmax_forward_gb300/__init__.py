@@ -14,6 +14,7 @@ import ctypes
 import functools
 import math
 import os
+import threading
 
 __all__ = [
     "ATTN_OK", "ATTN_ERR_INVALID_ARG", "ATTN_ERR_UNSUPPORTED_DEVICE", "ATTN_ERR_LAUNCH",
@@ -510,7 +511,7 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale, self.k_bounds = k, v, k_scale, v_scale, k_bounds
         self.n_pages, self.H_kv, self.page, self.d = n, h, page, d
         self.device = k.device
-        self._scratch = {}  # stream handle -> workspace of the calls on that stream
+        self._scratch = {}  # (thread, stream handle) -> workspace of its calls
         self.c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                         k_bounds.data_ptr() if k_bounds is not None else None, n, h, page, d,
                         formats[k.dtype])
@@ -640,9 +641,11 @@ def _need(size, *args):
 
 def _workspace(workspace, need, cache, stream, handle):
     """(pointer, bytes, tensor) of the scratch of one call; the tensor has to outlive the launch.
-    Calls on one stream follow one another, so the cache keeps a workspace for each stream; a
-    call that is being captured gets one of its own from the graph's memory, and a call on a
-    stream that is not the current one one that lives until that stream is done with it."""
+    A thread's calls on one stream follow one another, so the cache keeps a workspace for each
+    thread and stream (a call's two kernels need not be adjacent when two threads share a
+    stream); a call that is being captured gets one of its own from the graph's memory, and a
+    call on a stream that is not the current one one that lives until that stream is done with
+    it."""
     import torch
     if workspace is not None:
         if not workspace.is_contiguous() or _device_of(workspace) != cache.device:
@@ -650,13 +653,14 @@ def _workspace(workspace, need, cache, stream, handle):
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     keep = stream is None and not torch._C._cuda_isCurrentStreamCapturing()
     if keep:
-        kept = cache._scratch.get(handle)
+        who = (threading.get_ident(), handle)
+        kept = cache._scratch.get(who)
         if kept is not None and kept[1] >= need:
             return kept
     workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
     new = (workspace.data_ptr(), max(need, 16), workspace)
     if keep:
-        cache._scratch[handle] = new
+        cache._scratch[who] = new
     elif stream is not None:
         workspace.record_stream(stream)
     return new

@@ -328,6 +328,78 @@ def test_a_marked_page_shows_in_the_rows_that_see_it_and_in_no_other():
     assert status() == pkg.ATTN_OK
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Sq", [1, 4, 40])  # the 8-, 16- and 128-row kernels
+def test_references_that_have_to_move(fmt, Sq):
+    """Scores that keep growing along the sequence (each stretch far above the last), values whose
+    pages grow and shrink by many powers of two, and pages between that nobody weighs: what was
+    accumulated has to be carried from one reference to the next."""
+    page, d, n = 16, 64, 900
+    c = new_cache(60, 1, page, d, fmt, junk=True)
+    t = tables([n], page, 60, 60, seed=2)
+    k, v = rows((1, 1, n, d), 1, torch.float32, 0.05), rows((1, 1, n, d), 2, torch.float32)
+    q = rows((1, 4, Sq, d), 4, torch.float32, 0.1)
+    q[..., 0] = 8.0
+    k[0, 0, :, 0] = torch.arange(n) // 150 * 20.0  # scores rise by 20 every 150 keys
+    v *= torch.exp2(torch.tensor([0, 9, -12, 3, 14, -6, 1])[torch.arange(n) // 48 % 7])[:, None]
+    v[0, 0, 200:210] *= 2.0 ** 25  # large, but outweighed
+    pkg.cache_append(c, k.cuda(), v.cuda(), dev(t), dev([0]))
+    for causal in (True, False):
+        check_attention(q.to(torch.bfloat16), c, t, [n], [Sq], causal, scale=1.0 / 8)
+        # falling scores: the first reference is the last
+        check_attention(-q.to(torch.bfloat16), c, t, [n], [Sq], causal, scale=1.0 / 8)
+
+
+def test_marked_pages_with_many_rows():
+    """As above in the 128-row kernel: a page's NaN reaches the rows that see it only."""
+    page, d, n = 32, 128, 300
+    c = new_cache(12, 1, page, d, "e4m3")
+    t = tables([n], page, 12, 12, seed=5)
+    k, v = rows((1, 1, n, d), 1, torch.float32), rows((1, 1, n, d), 2, torch.float32)
+    v[0, 0, 290, 3] = math.nan  # page 9
+    pkg.cache_append(c, k.cuda(), v.cuda(), dev(t), dev([0]))
+    q = rows((1, 2, 40, d), 3, torch.bfloat16).cuda()  # positions 260 .. 299; page 9 begins at 288
+    o, lse = pkg.attention_cache(q, c, dev(t), dev([n]))
+    assert status() == pkg.ATTN_OK
+    assert torch.isfinite(o[:, :, :28]).all() and torch.isnan(o[:, :, 28:]).all()
+    assert torch.isfinite(lse).all()
+    bad = t.copy()
+    bad[0, 2] = 99
+    pkg.attention_cache(q, c, dev(bad), dev([n]))
+    assert status() == pkg.ATTN_ERR_TABLE
+
+
+def _random_case(rng):
+    d, page = rng.choice([64, 128]), rng.choice([16, 32, 64, 128])
+    Hkv, G = rng.choice([1, 2, 3, 5]), rng.choice([1, 2, 3, 4, 7, 8, 9, 16, 33])
+    Sq = rng.choice([1, 1, 2, 3, 5, 9, 17, 40])
+    B = rng.randint(1, 4)
+    most = rng.choice([3, 40, 150, 600])
+    lens = [rng.choice([0, 1, rng.randint(1, most), rng.randint(1, most)]) for _ in range(B)]
+    counts = [rng.randint(0, Sq) if rng.random() < 0.4 else Sq for _ in range(B)]
+    return d, page, Hkv, G, Sq, lens, counts
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_shapes(seed):
+    """Head groups, lengths, counts, page sizes and types at random, all pages and selected ones."""
+    import random
+    rng = random.Random(seed)
+    d, page, Hkv, G, Sq, lens, counts = _random_case(rng)
+    while G * Hkv * Sq * sum(lens) > 400000:  # the reference is a loop over rows
+        d, page, Hkv, G, Sq, lens, counts = _random_case(rng)
+    fmt, causal = rng.choice(["e4m3", "int8"]), rng.random() < 0.6
+    dtype = rng.choice([torch.bfloat16, torch.float16, torch.float32])
+    out = torch.float32 if rng.random() < 0.3 else None
+    c, t = filled(lens, Hkv, page, d, fmt, seed=seed, width=-(-max(max(lens), 1) // page) + rng.randint(0, 40))
+    q = rows((len(lens), G * Hkv, Sq, d), seed + 9, dtype)
+    check_attention(q, c, t, lens, counts, causal, out_dtype=out)
+    n = rng.randint(1, 6)
+    pages = pkg.cache_select(q.cuda(), c, dev(t), dev(lens), n, counts=dev(counts), causal=causal).cpu().numpy()
+    assert np.array_equal(pages, ref.select(f64(q), ref.snapshot(c), t, lens, counts, n, causal))
+    check_attention(q, c, t, lens, counts, causal, out_dtype=out, pages=pages)
+
+
 def test_every_key_of_a_large_split_call_counts():
     """Long sequences: many partial states per row.  q = 0 gives equal weights, so o is the mean
     of v and lse the logarithm of the number of keys."""
@@ -386,6 +458,8 @@ SELECT = [
     ([3000], [3], 3, 8, 1, 128, 16, 40),
     ([520, 260], [1, 1], 1, 16, 8, 64, 64, 3),
     ([700], [1], 1, 2, 2, 64, 16, 1),
+    ([900, 300], [1, 1], 1, 40, 2, 128, 32, 7),           # 20 heads on one: three blocks of eight
+    ([5000], [1], 1, 2, 1, 64, 16, 9),                    # pages for a whole cluster
 ]
 
 
@@ -576,11 +650,65 @@ def test_a_captured_step_follows_the_lengths_on_the_device():
     check_pool(caches[0], ref.snapshot(caches[1]))
 
 
-def test_calls_on_two_streams_at_once():
+def test_calls_of_two_threads_on_one_stream():
+    """Two threads decode with one cache on the default stream: a call's second kernel may come
+    behind the other thread's first."""
+    import threading
+    lens, d = [2500, 900], 64
+    c, t = filled(lens, 2, 32, d, "int8", seed=3)
+    tt, ll = dev(t), dev(lens)
+    qs = [[rows((2, 4, 1, d), 10 * k + i, torch.bfloat16).cuda() for i in range(20)] for k in range(2)]
+    want = [[pkg.attention_cache(q, c, tt, ll) for q in x] for x in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(k):
+        for q in qs[k]:
+            got[k].append(pkg.attention_cache(q, c, tt, ll))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    for k in range(2):
+        for (a, la), (b, lb) in zip(want[k], got[k]):
+            assert torch.equal(a, b) and torch.equal(la, lb)
+    assert status() == pkg.ATTN_OK
+
+
+def test_two_graphs_replayed_at_once():
+    """Each captured call has a workspace of its own."""
+    lens, d = [3000, 700], 64
+    c, t = filled(lens, 2, 32, d, "e4m3", seed=3)
+    tt, ll = dev(t), dev(lens)
+    qs = [rows((2, 4, n, d), n, torch.bfloat16).cuda() for n in (1, 30)]
+    want = [pkg.attention_cache(q, c, tt, ll) for q in qs]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(pkg.attention_cache(q, c, tt, ll))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (a, la), (b, lb) in zip(want, got):
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    assert status() == pkg.ATTN_OK
+
+
+@pytest.mark.parametrize("Sq", [1, 30])
+def test_calls_on_two_streams_at_once(Sq):
     lens, d = [3000, 1200], 128
     c, t = filled(lens, 4, 64, d, "e4m3", seed=1)
     tt, ll = dev(t), dev(lens)
-    qs = [rows((2, 8, 1, d), i, torch.bfloat16).cuda() for i in range(8)]
+    qs = [rows((2, 8, Sq, d), i, torch.bfloat16).cuda() for i in range(8)]
     want = [pkg.attention_cache(q, c, tt, ll) for q in qs]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -592,7 +720,7 @@ def test_calls_on_two_streams_at_once():
     for (a, la), (b, lb) in zip(want, got):
         assert torch.equal(a, b) and torch.equal(la, lb)
     # the stream argument, with a workspace of the caller's
-    st, need = pkg.attn_fwd_cache_workspace_size(2, 8, 4, 1, d, pkg.ATTN_BF16)
+    st, need = pkg.attn_fwd_cache_workspace_size(2, 8, 4, Sq, d, pkg.ATTN_BF16)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     o, _ = pkg.attention_cache(qs[0], c, tt, ll, workspace=ws, stream=streams[0])
