@@ -380,6 +380,45 @@ def _random_case(rng):
     return d, page, Hkv, G, Sq, lens, counts
 
 
+@pytest.mark.parametrize("case", ATTEND, ids=lambda c: "L%s_q%d_H%dx%d_d%d_p%d" % (c[0], c[2], *c[3:]))
+def test_a_wide_table_gives_the_same_results(case):
+    """A table with room for long sequences has the work cut into ranges that cross the
+    sequences; a narrow one gives each unit a CTA where units are few."""
+    lens, counts, Sq, H, Hkv, d, page = case
+    for fmt, dtype, out in (("e4m3", torch.bfloat16, None), ("int8", torch.float32, None),
+                            ("e4m3", torch.float16, torch.float32)):
+        c, t = filled(lens, Hkv, page, d, fmt, seed=len(lens) + d, width=8192 // page)
+        q = rows((len(lens), H, Sq, d), 78, dtype)
+        check_attention(q, c, t, lens, counts, True, out_dtype=out)
+        pages = np.full((len(lens), Hkv, Sq, 80), -1)  # every page of the sequence, from the last
+        for b, n in enumerate(lens):
+            held = min(-(-n // page), 80)
+            pages[b, ..., :held] = np.arange(held)[::-1]
+        check_attention(q, c, t, lens, counts, False, out_dtype=out, pages=pages)
+
+
+@pytest.mark.parametrize("d,fmt", [(64, "e4m3"), (64, "int8"), (128, "e4m3"), (128, "int8")])
+def test_many_rows_of_many_sequences(d, fmt):
+    """The 128-row kernel with more units than SMs, of uneven lengths, some without a token or a
+    query: ranges hold several units, and units several ranges."""
+    import random
+    rng = random.Random(d)
+    lens = [rng.choice([0, 1, 16, 127, 128, 129, rng.randint(1, 400)]) for _ in range(60)] + [1500]
+    counts = [rng.choice([34, 34, 0, 1, 20]) for _ in lens]
+    c, t = filled(lens, 3, 32, d, fmt, seed=d)
+    q = rows((len(lens), 3, 34, d), 5, torch.bfloat16)
+    for causal in (True, False):
+        check_attention(q, c, t, lens, counts, causal)
+
+
+def test_scratch_grows_with_the_calls():
+    """The workspace that a cache keeps serves small calls, larger ones and small ones again."""
+    c, t = filled([900, 40], 2, 32, 64, "int8", seed=6)
+    for Sq in (1, 40, 1, 6, 150, 1):
+        q = rows((2, 4, Sq, 64), Sq, torch.float16)
+        check_attention(q, c, t, [900, 40], [Sq, min(Sq, 3)], True)
+
+
 @pytest.mark.parametrize("seed", range(40))
 def test_random_shapes(seed):
     """Head groups, lengths, counts, page sizes and types at random, all pages and selected ones."""
