@@ -411,6 +411,58 @@ def test_many_rows_of_many_sequences(d, fmt):
         check_attention(q, c, t, lens, counts, causal)
 
 
+def test_offsets_past_32_bits():
+    """One sequence of 2^25 + 100 tokens: codes and rows lie past 2^32 bytes and elements.  All
+    tokens but the last 200 are zeros, whose part of the softmax is a count."""
+    page, d, n, m = 128, 128, 2 ** 25 + 100, 200
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    width = -(-n // page)
+    c = new_cache(width + 1, 1, page, d, "e4m3")
+    t = torch.arange(width, dtype=torch.int32, device="cuda")[None].contiguous()
+    t[0, 7], t[0, -2] = width, 7  # the last three pages: near the pool's end, its start, its end
+    t[0, -3], t[0, -1] = width - 1, width - 3
+    last = [width - 1, 7, width - 3]
+    k, v = rows((1, 1, m, d), 1, torch.bfloat16, 0.5), rows((1, 1, m, d), 2, torch.bfloat16)
+    pkg.cache_append(c, k.cuda(), v.cuda(), t, dev([n - m]))
+    assert status() == pkg.ATTN_OK
+
+    def part(at):  # these pages in a pool of their own
+        return pkg.KVCache(*(x[at] for x in (c.k, c.v, c.k_scale, c.v_scale, c.k_bounds)))
+
+    small, own = part(last), [[0, 1, 2]]
+    held = n - (width - 3) * page  # tokens in the last three pages
+    want = ref.read(ref.snapshot(small), own, [held], held)
+    assert abs(want[0]).max() > 1
+    for dtype in (torch.bfloat16, torch.float16):
+        for g, w in zip(pkg.cache_read(c, t, dev([n]), n, dtype=dtype), want):
+            same(f64(g[:, :, n - held:]), f64(torch.from_numpy(w).to(dtype)))
+            assert not g[:, :, : n - held: 4099].any()
+    mixed = False
+    for Sq, dtype in ((1, torch.float32), (1, torch.bfloat16), (5, torch.bfloat16), (40, torch.float16)):
+        q = rows((1, 2, Sq, d), Sq, dtype)
+        o, lse = pkg.attention_cache(q.cuda(), c, t, dev([n]), scale=0.12)
+        assert status() == pkg.ATTN_OK
+        o_, lse_, a, vmax = ref.attention(f64(q), ref.snapshot(small), own, [held], [Sq], True, 0.12)
+        all_ = np.logaddexp(lse_, math.log(n - held))  # the other tokens' scores are 0
+        share = np.exp(lse_ - all_)[..., None]
+        mixed = mixed or np.any((share > 0.05) & (share < 0.95))
+        # as check_attention, and two joins by lse, rounded by 2^-20 (below 32) each
+        tol = 2 * 20 * 2.0 ** -23 * a + 2 * (2.0 ** -21 + 2.0 ** -12) + 2.0 ** -18 + 2.0 ** -17
+        assert np.all(np.abs(f64(o) - o_ * share) <= tol * vmax + HALF[o.dtype] * np.abs(o_ * share) * 1.01)
+        assert np.all(np.abs(f64(lse) - all_) <= tol)
+    assert mixed
+    near = t[:, -40:].contiguous()
+    tokens, small = 39 * page + n % page, part(near[0].long())
+    q, own = rows((1, 2, 1, d), 9, torch.float32), [list(range(40))]
+    pages = pkg.cache_select(q.cuda(), c, near, dev([tokens]), 3).cpu().numpy()
+    assert np.array_equal(pages, ref.select(f64(q), ref.snapshot(small), own, [tokens], [1], 3, True))
+    o, _ = pkg.attention_cache(q.cuda(), c, near, dev([tokens]), pages=dev(pages))
+    o_ = check_attention(q, small, np.array(own), [tokens], [1], True, pages=pages)[0]
+    assert torch.equal(o, o_)
+    assert status() == pkg.ATTN_OK
+
+
 def test_scratch_grows_with_the_calls():
     """The workspace that a cache keeps serves small calls, larger ones and small ones again."""
     c, t = filled([900, 40], 2, 32, 64, "int8", seed=6)
