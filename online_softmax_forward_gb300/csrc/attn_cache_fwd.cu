@@ -88,6 +88,11 @@ struct Tile {  // one key tile, held by one lane
     float ks, vs;
 };
 
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {  // an 8 x 8 tile of 16-bit numbers
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 template <int R, int KT>
 __device__ __forceinline__ Tile find_tile(const FwdArgs &a, const Place &p) {
     Tile d;
@@ -127,21 +132,20 @@ __device__ __forceinline__ Tile find_tile(const FwdArgs &a, const Place &p) {
     return d;
 }
 
-// WIDE = 0: the 8-row form, 1: the 16-row form.
-template <int D, int FMT, int WIDE, int KT>
+// NB blocks of 8 query rows; FINE: q and the weights in 22 bits (NB = 1).
+template <int D, int FMT, int NB, int FINE, int KT>
 __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a) {
     using U = Unpack<FMT>;
-    constexpr int R = WIDE ? 16 : 8;
-    constexpr int H = WIDE ? 2 : 1;    // query rows per lane: g, and g + 8 in the 16-row form
-    constexpr int QS = D / 16;         // k steps of Q.K
-    constexpr int VT = D / 8;          // output tiles of 8 channels
+    constexpr int R = NB * 8;
+    constexpr int QS = D / 16;         // k steps of K.Q
+    constexpr int VT = D / 16;         // output tiles of 16 channels
+    static_assert(!FINE || NB == 1, "one block");
     constexpr int HALF = KT * D;       // bytes of a tile's keys, then its values
     constexpr int SLOT = 2 * HALF;
     constexpr int NS = kRing / SLOT < 8 ? kRing / SLOT : 8;
     static_assert(NS >= 3 && R * D * 4 <= kRing, "a warp's ring later holds a state");
     constexpr int STEP = KT < 32 ? KT : 32;  // keys of one softmax step
-    constexpr int NT = STEP / 8;             // score tiles of 8 keys
-    constexpr int KS = STEP / 16;            // k steps of P.V
+    constexpr int MT = STEP / 16;            // score tiles of 16 keys
     extern __shared__ __align__(128) uint8_t sm[];
     int *prefix = reinterpret_cast<int *>(sm + kWarps * kRing);  // [B + 1]
     __shared__ int warp_sums[kWarps];
@@ -249,20 +253,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
         const int len = clamp_len(a.lens[u.b], a.max_pages, a.page);
         const int cnt = a.counts ? min(max(a.counts[u.b], 0), a.Sq) : a.Sq;
 
-        // query fragments: k step w holds channels 4w .. 4w + 3 of the lane's D/4 channels
-        uint32_t qa[QS][4];
-        float cq[H];
-        int lim[H];
+        // query fragments: k step w holds channels 4w .. 4w + 3 of the lane's D/4 channels of
+        // row g of each block; the lane's scores, weights and sums are those of rows 2t, 2t + 1
+        uint32_t qb[NB][QS][2], ql[FINE ? QS : 1][2];
+        float2 cq[NB];
+        int lim[NB][2];
         int low = 0x7fffffff;  // fewest keys any row of the block sees
 #pragma unroll
-        for (int hh = 0; hh < H; ++hh) {
+        for (int nb = 0; nb < NB; ++nb) {
             float f[D / 4];
             int qi, h;
-            const bool real = row_of<R>(a, u, g + 8 * hh, qi, h);
-            lim[hh] = real ? visible_keys(len, cnt, qi, a.causal) : 0;
+            const bool real = row_of<R>(a, u, nb * 8 + g, qi, h);
+            const int sees = real ? visible_keys(len, cnt, qi, a.causal) : 0;
             if (real) {
                 load_q<D / 4>(a, (((size_t)u.b * a.Hkv * a.G + h) * a.Sq + qi) * D + t * (D / 4), f);
-                low = min(low, lim[hh]);
+                low = min(low, sees);
             } else {
 #pragma unroll
                 for (int e = 0; e < D / 4; ++e) f[e] = 0.f;
@@ -274,35 +279,36 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             float mul, back;
             row_power(amax, mul, back);
-            cq[hh] = a.sl2 * back;
+            back *= a.sl2;
+            cq[nb] = make_float2(__shfl_sync(0xffffffffu, back, t * 8), __shfl_sync(0xffffffffu, back, t * 8 + 4));
+            lim[nb][0] = __shfl_sync(0xffffffffu, sees, t * 8);
+            lim[nb][1] = __shfl_sync(0xffffffffu, sees, t * 8 + 4);
 #pragma unroll
-            for (int s = 0; s < QS; ++s) {
-                float y[4];
+            for (int w4 = 0; w4 < QS; ++w4)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = f[4 * s + e] * mul;
-                qa[s][hh] = pack_f16(y[0], y[1]);
-                qa[s][hh + 2] = pack_f16(y[2], y[3]);
-                if constexpr (!WIDE) {
-                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&qa[s][0]));
-                    const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&qa[s][2]));
-                    qa[s][1] = pack_f16(y[0] - p.x, y[1] - p.y);
-                    qa[s][3] = pack_f16(y[2] - r.x, y[3] - r.y);
+                for (int e = 0; e < 2; ++e) {
+                    const float y0 = f[4 * w4 + 2 * e] * mul, y1 = f[4 * w4 + 2 * e + 1] * mul;
+                    qb[nb][w4][e] = pack_f16(y0, y1);
+                    if constexpr (FINE) {
+                        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&qb[nb][w4][e]));
+                        ql[w4][e] = pack_f16(y0 - p.x, y1 - p.y);
+                    }
                 }
-            }
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
 
         // l and acc relative to `top` and rv; the first key seen sets both
-        float top[H], rv[H], l[H], acc[VT][4];
+        float2 top[NB], rv[NB], l[NB];
+        float acc[NB][VT][4];
 #pragma unroll
-        for (int hh = 0; hh < H; ++hh) {
-            top[hh] = kUnset;
-            rv[hh] = 0x1p111f;
-            l[hh] = 0.f;
+        for (int nb = 0; nb < NB; ++nb) {
+            top[nb] = make_float2(kUnset, kUnset);
+            rv[nb] = make_float2(0x1p111f, 0x1p111f);
+            l[nb] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int n = 0; n < VT; ++n) acc[nb][n][0] = acc[nb][n][1] = acc[nb][n][2] = acc[nb][n][3] = 0.f;
         }
-#pragma unroll
-        for (int n = 0; n < VT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 
         const int stop = i + left;
 #pragma unroll 1
@@ -338,117 +344,139 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
             }
 #pragma unroll 1
             for (int step = 0; step < KT; step += STEP) {
-                float s[NT][4];
+                // two chains of products where one block alone would leave the MMAs waiting for
+                // one another: halves of the channels, or q's parts
+                constexpr int CH = NB == 1 ? 2 : 1;
+                float s[NB * CH][MT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+                for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                    for (int n = 0; n < NB * CH; ++n) s[n][m][0] = s[n][m][1] = s[n][m][2] = s[n][m][3] = 0.f;
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
-                        const uint4 u4 = lds16(kb + step * D + swizzled<D>(n * 8 + g, t * (D / 64) + c));
-                        const uint32_t words[4] = {u4.x, u4.y, u4.z, u4.w};
+                        const uint4 x = lds16(kb + step * D + swizzled<D>(m * 16 + g, t * (D / 64) + c));
+                        const uint4 y = lds16(kb + step * D + swizzled<D>(m * 16 + 8 + g, t * (D / 64) + c));
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            uint32_t b0, b1;
-                            U::quad(words[e], b0, b1);
+                            uint32_t a0, a1, a2, a3;
+                            U::quad(xs[e], a0, a2);
+                            U::quad(ys[e], a1, a3);
                             const int st = c * 4 + e;
-                            mma16816(s[n], qa[st][0], qa[st][1], qa[st][2], qa[st][3], b0, b1);
+                            if constexpr (FINE) {
+                                mma16816(s[0][m], a0, a1, a2, a3, qb[0][st][0], qb[0][st][1]);
+                                mma16816(s[1][m], a0, a1, a2, a3, ql[st][0], ql[st][1]);
+                            } else {
+#pragma unroll
+                                for (int n = 0; n < NB; ++n)
+                                    mma16816(s[n + (CH - 1) * (e & 1)][m], a0, a1, a2, a3, qb[n][st][0], qb[n][st][1]);
+                            }
                         }
                     }
-                }
-                if constexpr (!WIDE) {  // hi and lo parts of q
+                    if constexpr (CH == 2) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float2 x = __fadd2_rn(make_float2(s[n][0], s[n][1]), make_float2(s[n][2], s[n][3]));
-                        s[n][0] = x.x;
-                        s[n][1] = x.y;
+                        for (int e = 0; e < 4; ++e) s[0][m][e] += s[1][m][e];
                     }
                 }
                 const bool edge = key0 + step + STEP > low;  // some row does not see every key
-                float2 p[H][NT];  // weights of keys 8 n + 2 t and the next
-                float c[H];
-                auto weights = [&](int hh) {
-                    const float f = ks * cq[hh];
+                float2 p[NB][MT][2];  // weights of keys 16 m + g and 8 more, for both rows
+                float2 c[NB];
+                auto weights = [&](int nb) {
+                    const float2 f = __fmul2_rn(cq[nb], make_float2(ks, ks));
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float2 z = __ffma2_rn(make_float2(s[n][2 * hh], s[n][2 * hh + 1]), make_float2(f, f),
-                                                    make_float2(-top[hh], -top[hh]));
-                        p[hh][n] = make_float2(ex2(z.x), ex2(z.y));
-                    }
-                    if (edge) {
-                        const int seen = lim[hh] - (key0 + step + 2 * t);
+                    for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if (8 * n >= seen) p[hh][n].x = 0.f;
-                            if (8 * n + 1 >= seen) p[hh][n].y = 0.f;
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const float2 z = __ffma2_rn(make_float2(s[nb][m][2 * hf], s[nb][m][2 * hf + 1]), f,
+                                                        make_float2(-top[nb].x, -top[nb].y));
+                            p[nb][m][hf] = make_float2(ex2(z.x), ex2(z.y));
                         }
+                    if (edge) {
+                        const int at = key0 + step + g;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                if (m * 16 + hf * 8 >= lim[nb][0] - at) p[nb][m][hf].x = 0.f;
+                                if (m * 16 + hf * 8 >= lim[nb][1] - at) p[nb][m][hf].y = 0.f;
+                            }
                     }
                 };
                 bool far = false;
 #pragma unroll
-                for (int hh = 0; hh < H; ++hh) {
+                for (int nb = 0; nb < NB; ++nb) {
                     // a page no key of which the row sees adds nothing, not even its scale's NaN
-                    c[hh] = key0 < lim[hh] ? vs * rv[hh] : 0.f;
-                    weights(hh);
-                    float most = 0.f;
+                    c[nb] = __fmul2_rn(rv[nb], make_float2(key0 < lim[nb][0] ? vs : 0.f, key0 < lim[nb][1] ? vs : 0.f));
+                    weights(nb);
+                    float2 most = p[nb][0][0];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) most = ptx::max3(most, p[hh][n].x, p[hh][n].y);
-                    far = far || most > 16.f || most * c[hh] > 32768.f;
+                    for (int e = 1; e < 2 * MT; ++e) {
+                        most.x = fmaxf(most.x, p[nb][e >> 1][e & 1].x);
+                        most.y = fmaxf(most.y, p[nb][e >> 1][e & 1].y);
+                    }
+                    far = far || fmaxf(most.x, most.y) > 16.f || fmaxf(most.x * c[nb].x, most.y * c[nb].y) > 32768.f;
                 }
                 if (__any_sync(0xffffffffu, far)) {
                     // new references: the scores' maximum, and the page scale unless what o
                     // holds is larger by now
-#pragma unroll
-                    for (int hh = 0; hh < H; ++hh) {
-                        const float f = ks * cq[hh], sv = key0 < lim[hh] ? vs : 0.f;
-                        const int seen = lim[hh] - (key0 + step + 2 * t);
+                    auto moved = [&](float f, float sv, int seen, const float (&x)[2 * MT], float &top, float &rv,
+                                     float &l, float &c) {
                         float mx = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 2 * NT; ++e)
-                            if (!edge || 8 * (e >> 1) + (e & 1) < seen) mx = fmaxf(mx, s[e >> 1][2 * hh + (e & 1)] * f);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        const float nt = fmaxf(top[hh], mx);
-                        const float alpha = ex2(top[hh] - nt);  // 0 from kUnset
-                        const float was = alpha * 2048.f / rv[hh];
-                        const float nv = mx == -INFINITY ? rv[hh] : 2048.f / fmaxf(fmaxf(was, sv), 0x1p-100f);
-                        const float to = alpha * (nv / rv[hh]);
-                        l[hh] *= alpha;
+                        for (int e = 0; e < 2 * MT; ++e)
+                            if (!edge || 8 * e < seen) mx = fmaxf(mx, x[e] * f);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        const float nt = fmaxf(top, mx);
+                        const float alpha = ex2(top - nt);  // 0 from kUnset
+                        const float was = alpha * 2048.f / rv;
+                        const float nv = mx == -INFINITY ? rv : 2048.f / fmaxf(fmaxf(was, sv), 0x1p-100f);
+                        const float to = alpha * (nv / rv);
+                        l *= alpha;
+                        top = nt;
+                        rv = nv;
+                        c = sv * nv;
+                        return to;
+                    };
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float x[2][2 * MT];
+#pragma unroll
+                        for (int e = 0; e < 4 * MT; ++e) x[e & 1][e >> 1] = s[nb][e >> 2][e & 3];
+                        const int at = key0 + step + g;
+                        float2 to;
+                        to.x = moved(ks * cq[nb].x, key0 < lim[nb][0] ? vs : 0.f, lim[nb][0] - at, x[0], top[nb].x,
+                                     rv[nb].x, l[nb].x, c[nb].x);
+                        to.y = moved(ks * cq[nb].y, key0 < lim[nb][1] ? vs : 0.f, lim[nb][1] - at, x[1], top[nb].y,
+                                     rv[nb].y, l[nb].y, c[nb].y);
 #pragma unroll
                         for (int n = 0; n < VT; ++n) {
-                            if constexpr (WIDE) {
-                                acc[n][2 * hh] *= to;
-                                acc[n][2 * hh + 1] *= to;
-                            } else {
-                                acc[n][0] *= to; acc[n][1] *= to; acc[n][2] *= to; acc[n][3] *= to;
+                            acc[nb][n][0] *= to.x;
+                            acc[nb][n][1] *= to.y;
+                            acc[nb][n][2] *= to.x;
+                            acc[nb][n][3] *= to.y;
+                        }
+                        weights(nb);
+                    }
+                }
+                uint32_t pb[NB][MT][2], pl[FINE ? MT : 1][2];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            l[nb] = __fadd2_rn(l[nb], p[nb][m][hf]);
+                            const float2 w2 = __fmul2_rn(p[nb][m][hf], c[nb]);
+                            const uint32_t hi = pack_f16(w2.x, w2.y);
+                            pb[nb][m][hf] = transposed(hi);
+                            if constexpr (FINE) {
+                                const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                                pl[m][hf] = transposed(pack_f16(w2.x - b.x, w2.y - b.y));
                             }
                         }
-                        top[hh] = nt;
-                        rv[hh] = nv;
-                        c[hh] = sv * nv;
-                        weights(hh);
-                    }
-                }
-                uint32_t pa[KS][4];
 #pragma unroll
-                for (int hh = 0; hh < H; ++hh) {
-                    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        sum = __fadd2_rn(sum, p[hh][n]);
-                        const float2 w = __fmul2_rn(p[hh][n], make_float2(c[hh], c[hh]));
-                        const uint32_t hi = pack_f16(w.x, w.y);
-                        if constexpr (WIDE) {
-                            pa[n / 2][(n & 1) * 2 + hh] = hi;
-                        } else {
-                            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                            pa[n / 2][(n & 1) * 2] = hi;
-                            pa[n / 2][(n & 1) * 2 + 1] = pack_f16(w.x - b.x, w.y - b.y);
-                        }
-                    }
-                    l[hh] += sum.x + sum.y;
-                }
-#pragma unroll
-                for (int st = 0; st < KS; ++st) {
+                for (int st = 0; st < MT; ++st) {
                     uint32_t r[4][D / 32];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -465,11 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                     for (int q = 0; q < D / 32; ++q)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {  // bytes 2 hf and 2 hf + 1 of the four rows' words
-                            uint32_t a0, a1, b0, b1;
+                            uint32_t a0, a1, a2, a3;
                             U::quad(__byte_perm(r[0][q], r[1][q], hf ? 0x7362 : 0x5140), a0, a1);
-                            U::quad(__byte_perm(r[2][q], r[3][q], hf ? 0x7362 : 0x5140), b0, b1);
-                            mma16816(acc[4 * q + 2 * hf], pa[st][0], pa[st][1], pa[st][2], pa[st][3], a0, b0);
-                            mma16816(acc[4 * q + 2 * hf + 1], pa[st][0], pa[st][1], pa[st][2], pa[st][3], a1, b1);
+                            U::quad(__byte_perm(r[2][q], r[3][q], hf ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                float(&o4)[4] = acc[nb][2 * q + hf];
+                                mma16816(o4, a0, a1, a2, a3, pb[nb][st][0], pb[nb][st][1]);
+                                if constexpr (FINE) mma16816(o4, a0, a1, a2, a3, pl[st][0], pl[st][1]);
+                            }
                         }
                 }
             }
@@ -486,33 +518,35 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
             __syncwarp();
         }
 #pragma unroll
-        for (int hh = 0; hh < H; ++hh) {
-            float sum = l[hh];
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            // 0: no key was visible.  NaN scores alone leave `top` unset
-            const float inv = sum == 0.f ? 0.f : 1.f / sum, unit = 1.f / rv[hh];
-            const float lse2 = sum == 0.f ? -INFINITY : top[hh] + log2f(sum);
-            const int r = g + 8 * hh;
-            float f[D / 4];
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int n = 0; n < VT; ++n) {
-                f[n] = (WIDE ? acc[n][2 * hh] : acc[n][0] + acc[n][2]) * inv * unit;
-                f[VT + n] = (WIDE ? acc[n][2 * hh + 1] : acc[n][1] + acc[n][3]) * inv * unit;
+            for (int x = 0; x < 2; ++x) {
+                float sum = x ? l[nb].y : l[nb].x;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                // 0: no key was visible.  NaN scores alone leave `top` unset
+                const float inv = sum == 0.f ? 0.f : 1.f / sum, unit = 1.f / (x ? rv[nb].y : rv[nb].x);
+                const float lse2 = sum == 0.f ? -INFINITY : (x ? top[nb].y : top[nb].x) + log2f(sum);
+                const int r = nb * 8 + 2 * t + x;
+                float f[D / 8];  // channels g * D / 8 ...
+#pragma unroll
+                for (int n = 0; n < VT; ++n) {
+                    f[2 * n] = acc[nb][n][x] * inv * unit;
+                    f[2 * n + 1] = acc[nb][n][2 + x] * inv * unit;
+                }
+                if (!before && !after) {
+                    size_t row;
+                    if (!out_row<R>(a, u, r, row)) continue;
+#pragma unroll
+                    for (int e = 0; e < D / 8; e += 8) store_o8(a, row * D + g * (D / 8) + e, f + e);
+                    if (a.lse && g == 0) a.lse[row] = lse2 * kLn2;
+                } else if (in_bounds(w < (int)gridDim.x * kWarps, a.status)) {
+                    float4 *p = reinterpret_cast<float4 *>(keep + r * D + g * (D / 8));
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    if (g == 0) s_lse[warp][before ? 0 : 1][r] = lse2;
+                }
             }
-            if (!before && !after) {
-                size_t row;
-                if (!out_row<R>(a, u, r, row)) continue;
-#pragma unroll
-                for (int e = 0; e < D / 4; e += 8) store_o8(a, row * D + t * (D / 4) + e, f + e);
-                if (a.lse && t == 0) a.lse[row] = lse2 * kLn2;
-            } else if (in_bounds(w < (int)gridDim.x * kWarps, a.status)) {
-                float4 *p = reinterpret_cast<float4 *>(keep + r * D + t * (D / 4));
-#pragma unroll
-                for (int e = 0; e < D / 16; ++e) p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                if (t == 0) s_lse[warp][before ? 0 : 1][r] = lse2;
-            }
-        }
         if ((before || after) && lane == 0) {
             const int side = before ? 0 : 1;
             s_b[warp][side] = here.b;
@@ -562,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                                                s_unit[first][side]);
             }
         }
-#pragma unroll
+#pragma unroll 1
         for (int r = warp; r < R; r += kWarps) {
             const float ls = lane < n ? s_lse[first + lane][lane == 0 ? side : 0][r] : -INFINITY;
             float M = ls;
@@ -666,10 +700,10 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) 
     }
 }
 
-template <int D, int FMT, int WIDE, int KT>
+template <int D, int FMT, int NB, int FINE, int KT>
 int launch_fwd_t(const FwdArgs &a, unsigned grid, cudaStream_t stream) {
-    constexpr int R = WIDE ? 16 : 8;
-    auto fwd = cache_fwd_kernel<D, FMT, WIDE, KT>;
+    constexpr int R = NB * 8;
+    auto fwd = cache_fwd_kernel<D, FMT, NB, FINE, KT>;
     constexpr size_t ring = (size_t)kWarps * kRing;
     if (!set_smem_limit_once(reinterpret_cast<const void *>(fwd), (int)(ring + (kMaxCacheBatch + 1) * 4)))
         return ATTN_ERR_LAUNCH;
@@ -691,20 +725,20 @@ int launch_fwd_t(const FwdArgs &a, unsigned grid, cudaStream_t stream) {
 
 // Keys of a tile: at most 8 KB of keys and values, three of which a warp's ring
 // holds, and no more than a page.
-constexpr int tile_keys(int d, int page) {
-    const int most = d == 128 ? 32 : 64;
-    return page < most ? page : most;
-}
+constexpr int tile_keys(int page) { return page < 32 ? page : 32; }
 
-template <int D, int FMT, int WIDE>
+template <int D, int FMT, int NB, int FINE>
 int launch_fwd_k(const FwdArgs &a, int kt, unsigned grid, cudaStream_t s) {
-    if (kt == 16) return launch_fwd_t<D, FMT, WIDE, 16>(a, grid, s);
-    if (kt == 32) return launch_fwd_t<D, FMT, WIDE, 32>(a, grid, s);
-    return launch_fwd_t<D, FMT, WIDE, tile_keys(D, 64)>(a, grid, s);
+    return kt == 16 ? launch_fwd_t<D, FMT, NB, FINE, 16>(a, grid, s) : launch_fwd_t<D, FMT, NB, FINE, 32>(a, grid, s);
 }
+template <int D>
+constexpr int kMostBlocks = D == 64 ? 3 : 2;  // of 8 rows, in the registers of a warp
 template <int D, int FMT>
-int launch_fwd_w(const FwdArgs &a, bool wide, int kt, unsigned grid, cudaStream_t s) {
-    return wide ? launch_fwd_k<D, FMT, 1>(a, kt, grid, s) : launch_fwd_k<D, FMT, 0>(a, kt, grid, s);
+int launch_fwd_n(const FwdArgs &a, int nb, bool fine, int kt, unsigned grid, cudaStream_t s) {
+    if (fine) return launch_fwd_k<D, FMT, 1, 1>(a, kt, grid, s);
+    if constexpr (kMostBlocks<D> == 3)
+        if (nb == 3) return launch_fwd_k<D, FMT, 3, 0>(a, kt, grid, s);
+    return nb == 2 ? launch_fwd_k<D, FMT, 2, 0>(a, kt, grid, s) : launch_fwd_k<D, FMT, 1, 0>(a, kt, grid, s);
 }
 
 }  // namespace
@@ -715,10 +749,14 @@ constexpr int64_t kTcRows = 33;
 static bool cache_tc(int64_t rows, int dtype, bool listed) {
     return !listed && (dtype == ATTN_BF16 || dtype == ATTN_F16) && rows >= kTcRows;
 }
-// The 16-row form where the output's own rounding hides the weights' and the
-// rows do not fit eight.
-static bool cache_wide(int64_t rows, int dtype) {
-    return (dtype == ATTN_BF16 || dtype == ATTN_F16) && rows > 8;
+// fp32 outputs keep q and the weights in 22 bits.
+static bool cache_fine(int dtype) { return dtype != ATTN_BF16 && dtype != ATTN_F16; }
+// Blocks of 8 rows that a warp takes at once, which share the loads and conversions
+// of the codes: as few units as the registers allow, of as few rows as cover them.
+static int cache_blocks(int64_t rows, int dtype, int d) {
+    const int64_t most = cache_fine(dtype) ? 1 : d == 64 ? kMostBlocks<64> : kMostBlocks<128>;
+    const int64_t blocks = (rows + 7) / 8, units = (blocks + most - 1) / most;
+    return (int)((blocks + units - 1) / units);
 }
 
 // Workspace: the tails [CTA], a state per warp, two per CTA and their lse (the
@@ -727,7 +765,7 @@ size_t cache_fwd_workspace(int B, int H, int H_kv, int Sq, int d, int dtype, boo
     const int64_t rows = (int64_t)(H / H_kv) * (listed ? 1 : Sq);
     if (cache_tc(rows, dtype, listed))
         return (size_t)kCacheMaxCtas * (16 + 2 * 128 * (size_t)d * 4 + 2 * 128 * 4);
-    const size_t R = cache_wide(rows, dtype) ? 16 : 8;
+    const size_t R = cache_blocks(rows, dtype, d) * 8;
     return (size_t)kCacheMaxCtas * (16 + (kWarps + 2) * R * d * 4 + 2 * R * 4);
 }
 
@@ -750,15 +788,15 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     a.status = status_word_device_ptr();
     if (!a.status) return ATTN_ERR_CUDA;
     if (cache_tc(a.rows, dtype, pages != nullptr)) return launch_cache_tc(a, c.d, c.format, workspace, stream);
-    const bool wide = cache_wide(a.rows, dtype);
-    const int R = wide ? 16 : 8;
+    const int nb = cache_blocks(a.rows, dtype, c.d), R = nb * 8;
+    const bool fine = cache_fine(dtype);
     a.nrb = (a.rows + R - 1) / R;
     a.units = a.Hkv * a.nseg * a.nrb;
     const int64_t units = (int64_t)B * a.units;  // at most B * H * Sq < 2^31
     a.by_units = fast_div((uint32_t)a.units);
     a.by_per = fast_div((uint32_t)(a.nseg * a.nrb));
     a.by_nrb = fast_div((uint32_t)a.nrb);
-    const int kt = tile_keys(c.d, c.page);
+    const int kt = tile_keys(c.page);
     const int sms = device_sm_count();
     if (sms <= 0) return ATTN_ERR_CUDA;
     // as many CTAs as the longest possible lengths can give every warp a tile
@@ -778,10 +816,10 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     a.po = a.hold + (size_t)a.workers * R * c.d;
     a.pl = a.po + (size_t)2 * ctas * R * c.d;
     if (c.d == 64)
-        return c.format == ATTN_CACHE_E4M3 ? launch_fwd_w<64, ATTN_CACHE_E4M3>(a, wide, kt, (unsigned)ctas, stream)
-                                           : launch_fwd_w<64, ATTN_CACHE_I8>(a, wide, kt, (unsigned)ctas, stream);
-    return c.format == ATTN_CACHE_E4M3 ? launch_fwd_w<128, ATTN_CACHE_E4M3>(a, wide, kt, (unsigned)ctas, stream)
-                                       : launch_fwd_w<128, ATTN_CACHE_I8>(a, wide, kt, (unsigned)ctas, stream);
+        return c.format == ATTN_CACHE_E4M3 ? launch_fwd_n<64, ATTN_CACHE_E4M3>(a, nb, fine, kt, (unsigned)ctas, stream)
+                                           : launch_fwd_n<64, ATTN_CACHE_I8>(a, nb, fine, kt, (unsigned)ctas, stream);
+    return c.format == ATTN_CACHE_E4M3 ? launch_fwd_n<128, ATTN_CACHE_E4M3>(a, nb, fine, kt, (unsigned)ctas, stream)
+                                       : launch_fwd_n<128, ATTN_CACHE_I8>(a, nb, fine, kt, (unsigned)ctas, stream);
 }
 
 }  // namespace attn
