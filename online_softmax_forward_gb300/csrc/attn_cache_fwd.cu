@@ -58,7 +58,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRing = 24 * 1024;  // shared memory of each warp's tiles, later of its states
 constexpr int kMinTiles = 1;  // tiles per worker when there are few
-constexpr int kOneEachTiles = 4 * kWarps;  // of a unit that one CTA takes
+constexpr int kSwitch = 8;   // tiles that a second unit, and a second kernel, cost a warp
 
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
     uint4 u;
@@ -88,6 +88,8 @@ struct Tile {  // one key tile, held by one lane
     float ks, vs;
 };
 
+// Quotients of normal numbers below 2^126, to 2^-22.
+__device__ __forceinline__ float ratio(float a, float b) { return __fdividef(a, b); }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {  // an 8 x 8 tile of 16-bit numbers
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -168,17 +170,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
         if (len != clamp_len(len, a.max_pages, a.page) || cnt < 0 || cnt > a.Sq)
             atomicOr(a.status, kStatusTable);
     };
+    auto share_unit = [&] {  // the warps' parts of the unit at `here`
+        const int64_t share = worker_count(here.n, kWarps, 1);
+        if (warp < share) {
+            here.t = (int)worker_begin(warp, here.n, share);
+            n_tiles = (int)worker_begin(warp + 1, here.n, share) - here.t;
+        }
+    };
     if (lane == 0) s_has[warp] = 0;
     if (a.one_each) {
         here.b = (int)((uint32_t)blockIdx.x / a.by_units);
         here.unit = blockIdx.x - here.b * a.units;
         if (here.unit == 0 && threadIdx.x == 0) report(here.b);
         here.n = a.pages ? tpu : (clamp_len(a.lens[here.b], a.max_pages, a.page) + KT - 1) / KT;
-        const int64_t share = worker_count(here.n, kWarps, 1);
-        if (warp < share) {
-            here.t = (int)worker_begin(warp, here.n, share);
-            n_tiles = (int)worker_begin(warp + 1, here.n, share) - here.t;
-        }
+        share_unit();
         if (here.n == 0) {  // no token: o = 0, lse = -inf
             const Unit u = unit_at(a, here.b, here.unit);
             const float z[8] = {};
@@ -210,7 +215,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
         }
         workers = worker_count(total, a.workers, kMinTiles);
         w += blockIdx.x * kWarps;
-        if (w < workers && total > 0) {
+        const int64_t all = (int64_t)a.B * a.units;
+        bool alone = false;  // a CTA takes one unit
+        if (!a.pages && all <= gridDim.x) {
+            int longest = 0;
+            for (int b = threadIdx.x; b < a.B; b += kThreads) longest = max(longest, tiles(b));
+            alone = !__syncthreads_or(longest > ((total + workers - 1) / workers + kSwitch) * kWarps);
+        }
+        if (alone) {
+            if (blockIdx.x < all) {
+                here.b = (int)((uint32_t)blockIdx.x / a.by_units);
+                here.unit = blockIdx.x - here.b * a.units;
+                here.n = tiles(here.b);
+                share_unit();
+            }
+        } else if (w < workers && total > 0) {
             x0 = worker_begin(w, total, workers);
             n_tiles = (int)(worker_begin(w + 1, total, workers) - x0);
             here = place_of(a, prefix, tpu, x0);
@@ -259,18 +278,47 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
         float2 cq[NB];
         int lim[NB][2];
         int low = 0x7fffffff;  // fewest keys any row of the block sees
+        float fine[FINE ? D / 4 : 1];
+        codec::Raw8<1> raw[FINE ? 1 : NB][D / 32];  // 16-bit q, loaded together
+        int sees_all[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            int qi, h;
+            const bool real = row_of<R>(a, u, nb * 8 + g, qi, h);
+            sees_all[nb] = real ? visible_keys(len, cnt, qi, a.causal) : 0;
+            if (real) low = min(low, sees_all[nb]);
+            const size_t at = real ? (((size_t)u.b * a.Hkv * a.G + h) * a.Sq + qi) * D + t * (D / 4) : 0;
+            if constexpr (FINE) {
+                float *f = fine;
+#pragma unroll
+                for (int e = 0; e < D / 4; ++e) f[e] = 0.f;
+                if (real) load_q<D / 4>(a, at, f);
+            } else {
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) {
+                    raw[nb][e].u[0] = make_uint4(0, 0, 0, 0);
+                    if (real) raw[nb][e].load(a.q, at + 8 * e);
+                }
+            }
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             float f[D / 4];
-            int qi, h;
-            const bool real = row_of<R>(a, u, nb * 8 + g, qi, h);
-            const int sees = real ? visible_keys(len, cnt, qi, a.causal) : 0;
-            if (real) {
-                load_q<D / 4>(a, (((size_t)u.b * a.Hkv * a.G + h) * a.Sq + qi) * D + t * (D / 4), f);
-                low = min(low, sees);
+            const int sees = sees_all[nb];
+            if constexpr (FINE) {
+#pragma unroll
+                for (int e = 0; e < D / 4; ++e) f[e] = fine[e];
             } else {
 #pragma unroll
-                for (int e = 0; e < D / 4; ++e) f[e] = 0.f;
+                for (int e = 0; e < D / 32; ++e) {
+                    if (a.dtype == ATTN_BF16) {
+                        raw[nb][e].widen(f + 8 * e);
+                    } else {
+                        codec::Raw8<2> x;
+                        x.u[0] = raw[nb][e].u[0];
+                        x.widen(f + 8 * e);
+                    }
+                }
             }
             float amax = 0.f;
 #pragma unroll
@@ -429,9 +477,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                         const float nt = fmaxf(top, mx);
                         const float alpha = ex2(top - nt);  // 0 from kUnset
-                        const float was = alpha * 2048.f / rv;
-                        const float nv = mx == -INFINITY ? rv : 2048.f / fmaxf(fmaxf(was, sv), 0x1p-100f);
-                        const float to = alpha * (nv / rv);
+                        const float was = ratio(alpha * 2048.f, rv);
+                        const float nv = mx == -INFINITY ? rv : ratio(2048.f, fmaxf(fmaxf(was, sv), 0x1p-100f));
+                        const float to = alpha * ratio(nv, rv);
                         l *= alpha;
                         top = nt;
                         rv = nv;
@@ -525,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 // 0: no key was visible.  NaN scores alone leave `top` unset
-                const float inv = sum == 0.f ? 0.f : 1.f / sum, unit = 1.f / (x ? rv[nb].y : rv[nb].x);
+                const float inv = sum == 0.f ? 0.f : ratio(1.f, sum), unit = ratio(1.f, x ? rv[nb].y : rv[nb].x);
                 const float lse2 = sum == 0.f ? -INFINITY : (x ? top[nb].y : top[nb].x) + log2f(sum);
                 const int r = nb * 8 + 2 * t + x;
                 float f[D / 8];  // channels g * D / 8 ...
@@ -618,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
 #pragma unroll
                 for (int e = 0; e < D / 32; ++e) o[e] = fmaf(wk, src[32 * e], o[e]);
             }
-            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const float inv = L == 0.f ? 0.f : ratio(1.f, L);
             const float lse2 = L == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(L);
             if (earlier || open) {
                 if (!in_bounds(slot < 2 * (int)gridDim.x, a.status)) continue;
@@ -691,7 +739,7 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) 
     for (int c = 0; c < C; ++c) part[warp][lane + 32 * c] = acc[c];
     __syncthreads();
     if (threadIdx.x < D) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = L == 0.f ? 0.f : ratio(1.f, L);
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) sum += part[k][threadIdx.x];
@@ -804,11 +852,12 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     int64_t ctas = most / kWarps < sms ? (int64_t)(most / kWarps) + 1 : sms;
     if (ctas > kCacheMaxCtas) ctas = kCacheMaxCtas;
     if (ctas > sms) ctas = sms;
-    // Few units of few tiles, by the longest possible lengths: a CTA each.  Four tiles a warp
-    // take as long as one and the second kernel, which is then not launched (one sequence of
-    // 1000 tokens, 8 kv heads: 11.1 us either way on the device, 17.1 and 14.5 us a call)
-    const int longest = pages ? n_select * (c.page / kt) : (int)(((int64_t)max_pages * c.page + kt - 1) / kt);
-    a.one_each = units <= ctas && longest <= kOneEachTiles;
+    // A CTA for each unit, if that is not longer for a warp than its share of all the work by
+    // more than what sharing a unit costs: by the number of listed pages or the longest possible
+    // lengths, and then without the second kernel, or, in the kernel, by the lengths
+    const int64_t longest = pages ? (int64_t)n_select * (c.page / kt) : ((int64_t)max_pages * c.page + kt - 1) / kt;
+    const double share = pages ? (double)units * longest / ((double)sms * kWarps) : 1;
+    a.one_each = units <= sms && longest <= (share + kSwitch) * kWarps;
     if (a.one_each) ctas = units;
     a.workers = (int)ctas * kWarps;
     a.tail = reinterpret_cast<int4 *>(workspace);
