@@ -33,7 +33,8 @@ struct AppendArgs {
     float *scale[2];    // [n_pages][Hkv]
     uint8_t *bounds;    // [n_pages][Hkv][2][d], keys only
     const int32_t *table, *pos, *counts;
-    int B, S, Hkv, page, n_pages, max_pages, touched;
+    int B, S, Hkv, page, page_shift, n_pages, max_pages, touched;
+    FastDiv by_heads, by_touched;
     int *status;
 };
 
@@ -48,15 +49,15 @@ __global__ void __launch_bounds__(kAppendThreads, DT == 0 || MOST == 128 ? 1 : 8
     constexpr int RL = kAppendThreads / G; // rows at a time
     constexpr int N = MOST / RL;
     constexpr int kW = kAppendThreads / 32;
-    __shared__ float red[kW];
-    __shared__ float edge[2][kW][D];       // smallest and largest by warp
-    int64_t blk = blockIdx.x;
-    const int which = (int)(blk & 1);
-    blk >>= 1;
-    const int hk = (int)(blk % a.Hkv);
-    blk /= a.Hkv;
-    const int tp = (int)(blk % a.touched);
-    const int b = (int)(blk / a.touched);
+    using Range = codec::Range8<DT>;
+    using Edge = typename std::conditional<DT == 0, float, uint16_t>::type;
+    __shared__ uint32_t red[kW];
+    __shared__ __align__(16) Edge edge[2][kW][D];  // smallest and largest by warp
+    const int which = blockIdx.x & 1;
+    const uint32_t page_of = (blockIdx.x >> 1) / a.by_heads;
+    const int hk = (int)((blockIdx.x >> 1) - page_of * a.Hkv);
+    const int b = (int)(page_of / a.by_touched);
+    const int tp = (int)(page_of - (uint32_t)b * a.touched);
     const int pos = a.pos[b];
     int cnt = a.counts ? a.counts[b] : a.S;
     if (cnt < 0 || cnt > a.S || pos < 0) {  // nothing of this sequence is written
@@ -64,23 +65,22 @@ __global__ void __launch_bounds__(kAppendThreads, DT == 0 || MOST == 128 ? 1 : 8
         return;
     }
     const int64_t end = (int64_t)pos + cnt;
-    const int64_t lp = pos / a.page + tp;           // logical page
-    const int64_t first = lp * a.page;              // its first position
+    const int64_t lp = (pos >> a.page_shift) + (int64_t)tp;  // logical page
+    const int64_t first = lp << a.page_shift;                // its first position
     if (first >= end) return;
     const int r0 = pos > first ? (int)(pos - first) : 0;                  // first new row
     const int r1 = end - first < a.page ? (int)(end - first) : a.page;    // past the last
     const void *xs = which ? a.x[1] : a.x[0];
     const int g = threadIdx.x % G, rl = threadIdx.x / G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // row r of the page is row first + r - pos of x
-    const size_t src = (((size_t)b * a.Hkv + hk) * a.S) * D + g * 8;
-    const int64_t shift = first - pos;
+    const size_t src = (((size_t)b * a.Hkv + hk) * a.S + (size_t)(first - pos + rl)) * D + g * 8;
 
     // the rows are asked for before the page that they go to
     codec::Raw8<DT> raw[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int r = rl + n * RL;
-        const size_t i = src + (size_t)(shift + r) * D;
+        const size_t i = src + n * (RL * D);
         if (r >= r0 && r < r1 && in_bounds(i + 8 <= (size_t)a.B * a.Hkv * a.S * D, a.status))
             raw[n].load(xs, i);
     }
@@ -90,41 +90,44 @@ __global__ void __launch_bounds__(kAppendThreads, DT == 0 || MOST == 128 ? 1 : 8
         return;
     }
     const int64_t ph = (int64_t)phys * a.Hkv + hk;
-    uint8_t *codes = (which ? a.codes[1] : a.codes[0]) + ph * a.page * D;
+    uint8_t *codes = (which ? a.codes[1] : a.codes[0]) + (ph << a.page_shift) * D;
     float *scale = (which ? a.scale[1] : a.scale[0]) + ph;
     const float before = r0 > 0 ? *scale : 0.f;
-    codec::Range8<DT> range;
-    range.clear();
+    uint32_t amax;  // as bits: a NaN's exceed infinity's
+    if (which == 0 && a.bounds) {
+        Range range;
+        range.clear();
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int r = rl + n * RL;
-        if (r >= r0 && r < r1) range.add(raw[n]);
-    }
+        for (int n = 0; n < N; ++n) {
+            const int r = rl + n * RL;
+            if (r >= r0 && r < r1) range.add(raw[n]);
+        }
 #pragma unroll
-    for (int o = G; o < 32; o <<= 1) range.join(o);  // the warp's rows
-    float lo[8], hi[8];
-    codec::Range8<DT>::widen(range.lo, lo);
-    codec::Range8<DT>::widen(range.hi, hi);
-    // magnitudes compared as integers: a NaN's bits exceed infinity's.  A warp without
-    // a row holds (inf, -inf) and counts as 0
-    uint32_t amax = 0;
-    if (!(lo[0] == INFINITY && hi[0] == -INFINITY)) {
+        for (int o = G; o < 32; o <<= 1) range.join(o);  // the warp's rows
+        amax = range.largest();
+        if (lane < G) {
+            constexpr int kE = 16 / sizeof(Edge);  // channels of a 16-byte store
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            amax = max(amax, max(__float_as_uint(lo[e]) & 0x7fffffffu, __float_as_uint(hi[e]) & 0x7fffffffu));
+            for (int e = 0; e < 8 / kE; ++e) {
+                const uint32_t *l = range.lo + 4 * e, *h = range.hi + 4 * e;
+                *reinterpret_cast<uint4 *>(&edge[0][warp][g * 8 + e * kE]) = make_uint4(l[0], l[1], l[2], l[3]);
+                *reinterpret_cast<uint4 *>(&edge[1][warp][g * 8 + e * kE]) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
+    } else {
+        uint32_t m[Range::kN] = {};
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int r = rl + n * RL;
+            if (r >= r0 && r < r1) Range::add_magnitudes(m, raw[n]);
+        }
+        amax = Range::largest(m);
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
-    if (lane == 0) red[warp] = __uint_as_float(amax);
-    if (which == 0 && a.bounds && lane < G) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-            *reinterpret_cast<float4 *>(&edge[0][warp][g * 8 + e]) = make_float4(lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
-            *reinterpret_cast<float4 *>(&edge[1][warp][g * 8 + e]) = make_float4(hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
-        }
-    }
+    if (lane == 0) red[warp] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kW; ++w) amax = max(amax, __float_as_uint(red[w]));
+    for (int w = 0; w < kW; ++w) amax = max(amax, red[w]);
     const float mine = codec::scale_for<FMT>(__uint_as_float(amax));
     const float now = (before != before || mine != mine) ? __int_as_float(0x7fc00000)
                                                          : fmaxf(before, mine);
@@ -133,14 +136,20 @@ __global__ void __launch_bounds__(kAppendThreads, DT == 0 || MOST == 128 ? 1 : 8
     for (int n = 0; n < N; ++n) {
         const int r = rl + n * RL;
         if (r < r0 || r >= r1) continue;
-        float f[8];
-        raw[n].widen(f);
+        uint2 c = make_uint2(0, 0);
+        if (inv > 0.f) {
+            float f[8];
+            raw[n].widen(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = inv > 0.f ? f[e] * inv : 0.f;
-        uint2 c;
-        c.x = codec::encode4<FMT>(f[0], f[1], f[2], f[3]);
-        c.y = codec::encode4<FMT>(f[4], f[5], f[6], f[7]);
-        *reinterpret_cast<uint2 *>(codes + (size_t)r * D + g * 8) = c;
+            for (int e = 0; e < 8; e += 2) {
+                const float2 y = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(inv, inv));
+                f[e] = y.x;
+                f[e + 1] = y.y;
+            }
+            c.x = codec::encode4<FMT>(f[0], f[1], f[2], f[3]);
+            c.y = codec::encode4<FMT>(f[4], f[5], f[6], f[7]);
+        }
+        *reinterpret_cast<uint2 *>(codes + (rl * D + g * 8) + n * (RL * D)) = c;
     }
     const bool grew = r0 > 0 && !(now == before);  // also when the block turned NaN
     const float ratio = now > 0.f ? before * inv : 0.f;
@@ -163,17 +172,20 @@ __global__ void __launch_bounds__(kAppendThreads, DT == 0 || MOST == 128 ? 1 : 8
     if (which == 0 && a.bounds && threadIdx.x < 2 * (D / 4)) {
         const int side = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
         uint32_t *p = reinterpret_cast<uint32_t *>(a.bounds + ((size_t)ph * 2 + side) * D) + c4;
-        float f[4];
+        constexpr int kV = DT == 0 ? 4 : 2;  // words of four channels
+        uint32_t x[kV];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float x = edge[side][0][c4 * 4 + e];
+        for (int w = 0; w < kW; ++w) {
+            const uint32_t *y = reinterpret_cast<const uint32_t *>(&edge[side][w][c4 * 4]);
 #pragma unroll
-            for (int w = 1; w < kW; ++w) {
-                const float y = edge[side][w][c4 * 4 + e];
-                x = side ? fmaxf(x, y) : fminf(x, y);
-            }
-            f[e] = inv > 0.f ? x * inv : 0.f;
+            for (int e = 0; e < kV; ++e)
+                x[e] = w == 0 ? y[e] : side ? Range::most(x[e], y[e]) : Range::least(x[e], y[e]);
         }
+        const uint32_t all[8] = {x[0], x[1], x[kV - 2], x[kV - 1], 0, 0, 0, 0};
+        float f[8];
+        Range::widen(all, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = inv > 0.f ? f[e] * inv : 0.f;
         if (r0 > 0) {
             float o[4];
             codec::decode4<FMT>(*p, o);
@@ -192,7 +204,8 @@ struct ReadArgs {
     const float *scale[2];
     void *out[2];  // [B][Hkv][S][d]
     const int32_t *table, *lens;
-    int B, S, Hkv, page, n_pages, max_pages, tiles;
+    int B, S, Hkv, page, page_shift, n_pages, max_pages, tiles;
+    FastDiv by_heads, by_tiles;
     int *status;
 };
 
@@ -203,17 +216,15 @@ constexpr int kReadThreads = 256;
 template <int D, int FMT, int DT>
 __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadArgs a) {
     constexpr int G = D / 16;
-    int64_t blk = blockIdx.x;
-    const int which = (int)(blk & 1);
-    blk >>= 1;
-    const int lp = (int)(blk % a.tiles);
-    blk /= a.tiles;
-    const int hk = (int)(blk % a.Hkv);
-    const int b = (int)(blk / a.Hkv);
+    const int which = blockIdx.x & 1;
+    const uint32_t block_of = (blockIdx.x >> 1) / a.by_tiles;
+    const int lp = (int)((blockIdx.x >> 1) - block_of * a.tiles);
+    const int b = (int)(block_of / a.by_heads);
+    const int hk = (int)(block_of - (uint32_t)b * a.Hkv);
     const int len0 = a.lens[b];
     const int len = clamp_len(len0, a.max_pages, a.page);
     if (len != len0 && threadIdx.x == 0) atomicOr(a.status, kStatusTable);
-    const int64_t first = (int64_t)lp * a.page;
+    const int64_t first = (int64_t)lp << a.page_shift;
     const int rows = a.S - first < a.page ? (int)(a.S - first) : a.page;
     int held = (int64_t)len - first < rows ? (int)((int64_t)len - first) : rows;
     if (held < 0) held = 0;
@@ -226,7 +237,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadArgs
             held = 0;
         } else {
             const int64_t ph = (int64_t)phys * a.Hkv + hk;
-            codes = (which ? a.codes[1] : a.codes[0]) + ph * a.page * D;
+            codes = (which ? a.codes[1] : a.codes[0]) + (ph << a.page_shift) * D;
             s = (which ? a.scale[1] : a.scale[0])[ph];
         }
     }
@@ -267,6 +278,8 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadArgs
     }
 }
 
+int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
 // f(integral constants D, FMT, DT) for the runtime values
 template <template <int, int, int> class F, typename... A>
 int dispatch(int d, int format, int dt, A... args) {
@@ -306,8 +319,9 @@ int launch_cache_append(const attn_cache &c, const void *k, const void *v, const
     const int64_t touched = touched_pages(S, c.page);
     const int64_t grid = (int64_t)B * c.H_kv * touched * 2;  // the caller checked it
     AppendArgs a = {{k, v}, {(uint8_t *)c.k, (uint8_t *)c.v}, {c.k_scale, c.v_scale},
-                    (uint8_t *)c.k_bounds, table, pos, counts, B, S, c.H_kv, c.page, c.n_pages,
-                    max_pages, (int)touched, status_word_device_ptr()};
+                    (uint8_t *)c.k_bounds, table, pos, counts, B, S, c.H_kv, c.page, log2_of(c.page), c.n_pages,
+                    max_pages, (int)touched, fast_div((uint32_t)c.H_kv), fast_div((uint32_t)touched),
+                    status_word_device_ptr()};
     if (!a.status) return ATTN_ERR_CUDA;
     return dispatch<RunAppend>(c.d, c.format, dtype, (const AppendArgs *)&a, (unsigned)grid, stream);
 }
@@ -317,8 +331,8 @@ int launch_cache_read(const attn_cache &c, const int32_t *table, int max_pages, 
     const int64_t tiles = ((int64_t)S + c.page - 1) / c.page;
     const int64_t grid = (int64_t)B * c.H_kv * tiles * 2;
     ReadArgs a = {{(const uint8_t *)c.k, (const uint8_t *)c.v}, {c.k_scale, c.v_scale}, {k, v},
-                  table, lens, B, S, c.H_kv, c.page, c.n_pages, max_pages, (int)tiles,
-                  status_word_device_ptr()};
+                  table, lens, B, S, c.H_kv, c.page, log2_of(c.page), c.n_pages, max_pages, (int)tiles,
+                  fast_div((uint32_t)c.H_kv), fast_div((uint32_t)tiles), status_word_device_ptr()};
     if (!a.status) return ATTN_ERR_CUDA;
     return dispatch<RunRead>(c.d, c.format, dtype, (const ReadArgs *)&a, (unsigned)grid, stream);
 }

@@ -139,28 +139,54 @@ struct Range8 {
             return *reinterpret_cast<const uint32_t *>(&r);
         }
     }
+    static constexpr uint32_t kUp = DT == 0 ? 0x7f800000u : DT == 1 ? 0x7f807f80u : 0x7c007c00u;
+    static constexpr uint32_t kSign = DT == 0 ? 0x80000000u : 0x80008000u;
+    static constexpr int kN = DT == 0 ? 8 : 4;
     __device__ __forceinline__ void clear() {  // +infinity, -infinity
-        constexpr uint32_t up = DT == 0 ? 0x7f800000u : DT == 1 ? 0x7f807f80u : 0x7c007c00u;
-        constexpr uint32_t sign = DT == 0 ? 0x80000000u : 0x80008000u;
 #pragma unroll
-        for (int j = 0; j < (DT == 0 ? 8 : 4); ++j) {
-            lo[j] = up;
-            hi[j] = up | sign;
+        for (int j = 0; j < kN; ++j) {
+            lo[j] = kUp;
+            hi[j] = kUp | kSign;
         }
+    }
+    // The largest magnitude of w as the bits of a float; a NaN's exceed infinity's.
+    __device__ __forceinline__ static uint32_t largest(const uint32_t (&w)[kN]) {
+        uint32_t m = w[0] & ~kSign;
+#pragma unroll
+        for (int j = 1; j < kN; ++j) m = most(m, w[j] & ~kSign);
+        if constexpr (DT == 0) return m;
+        float f[8];
+        const uint32_t pair[4] = {m, 0, 0, 0};
+        widen(pair, f);
+        return max(__float_as_uint(f[0]), __float_as_uint(f[1]));
+    }
+    __device__ __forceinline__ uint32_t largest() const {  // 0 if no row was added
+        if (lo[0] == kUp && hi[0] == (kUp | kSign)) return 0;
+        uint32_t m[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) m[j] = most(lo[j] & ~kSign, hi[j] & ~kSign);
+        return largest(m);
     }
     __device__ __forceinline__ void add(const Raw8<DT> &r) {
         const uint32_t w[8] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w, r.u[DT == 0].x, r.u[DT == 0].y,
                                r.u[DT == 0].z, r.u[DT == 0].w};
 #pragma unroll
-        for (int j = 0; j < (DT == 0 ? 8 : 4); ++j) {
+        for (int j = 0; j < kN; ++j) {
             lo[j] = least(lo[j], w[j]);
             hi[j] = most(hi[j], w[j]);
         }
     }
+    // |values| into `m`, which starts at 0
+    __device__ __forceinline__ static void add_magnitudes(uint32_t (&m)[kN], const Raw8<DT> &r) {
+        const uint32_t w[8] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w, r.u[DT == 0].x, r.u[DT == 0].y,
+                               r.u[DT == 0].z, r.u[DT == 0].w};
+#pragma unroll
+        for (int j = 0; j < kN; ++j) m[j] = most(m[j], w[j] & ~kSign);
+    }
     // also over the lanes whose number differs in bit `o`
     __device__ __forceinline__ void join(int o) {
 #pragma unroll
-        for (int j = 0; j < (DT == 0 ? 8 : 4); ++j) {
+        for (int j = 0; j < kN; ++j) {
             lo[j] = least(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
             hi[j] = most(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
         }
