@@ -38,13 +38,21 @@ struct AppendArgs {
     int *status;
 };
 
+// CTAs of an SM.  A CTA is a chain of waits (positions, rows, the block's maximum),
+// which others hide: as many as leave each thread the registers for its rows.  Two
+// 8k prompts of 32 heads, d = 128: bf16 52 us with eight of 32 registers (five: 71,
+// before the instructions were fewer); fp32 83 us with four (five spill: 92, three:
+// 112); fp32 with pages of 128 85 us with two, 94 with three.
+template <int D, int DT, int MOST>
+constexpr int kAppendCtas = DT != 0 ? (MOST == 128 ? 4 : 8) : D == 128 ? (MOST == 128 ? 2 : 4) : (MOST == 128 ? 4 : 6);
+
 // One CTA per (touched page of a sequence, kv head, keys or values).
 // MOST: rows of the largest page that it takes, 64 or 128 (registers hold them).
-// A CTA is a chain of waits (positions, rows, the block's maximum), so as many as
-// fit hide each other's: eight of 32 registers a thread, 65 us for two 8k prompts
-// of 32 heads, against 71 us with five.
+// Bound by memory: 95 % of the copy rate in the case above.  It is also near the
+// issue rate, so a page is found without divisions, and keys' ranges and values'
+// magnitudes are kept as packed pairs of 16 bits until a warp's rows are joined.
 template <int D, int FMT, int DT, int MOST>
-__global__ void __launch_bounds__(kAppendThreads, DT == 0 || MOST == 128 ? 1 : 8) cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, (kAppendCtas<D, DT, MOST>)) cache_append_kernel(const AppendArgs a) {
     constexpr int G = D / 8;               // 8-channel groups of a row: one per thread
     constexpr int RL = kAppendThreads / G; // rows at a time
     constexpr int N = MOST / RL;

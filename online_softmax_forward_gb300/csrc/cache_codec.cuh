@@ -123,8 +123,9 @@ struct Range8 {
     uint32_t lo[DT == 0 ? 8 : 4], hi[DT == 0 ? 8 : 4];
     __device__ __forceinline__ static uint32_t least(uint32_t a, uint32_t b) {
         if constexpr (DT == 0) {
-            const float x = __uint_as_float(a), y = __uint_as_float(b);
-            return __float_as_uint(x != x || y < x || y != y ? (x != x ? x : y) : x);
+            float r;
+            asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+            return __float_as_uint(r);
         } else {
             const P r = __hmin2_nan(*reinterpret_cast<const P *>(&a), *reinterpret_cast<const P *>(&b));
             return *reinterpret_cast<const uint32_t *>(&r);
@@ -132,8 +133,9 @@ struct Range8 {
     }
     __device__ __forceinline__ static uint32_t most(uint32_t a, uint32_t b) {
         if constexpr (DT == 0) {
-            const float x = __uint_as_float(a), y = __uint_as_float(b);
-            return __float_as_uint(x != x || y > x || y != y ? (x != x ? x : y) : x);
+            float r;
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+            return __float_as_uint(r);
         } else {
             const P r = __hmax2_nan(*reinterpret_cast<const P *>(&a), *reinterpret_cast<const P *>(&b));
             return *reinterpret_cast<const uint32_t *>(&r);
