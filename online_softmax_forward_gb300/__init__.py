@@ -570,7 +570,21 @@ def _handle(device, stream):
     """The cudaStream_t of ``stream``, or of the device's current stream: asked for without
     making a Stream object, which takes longer than a launch."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError("the cache is on %s, the stream on %s" % (device, stream.device))
+    return stream.cuda_stream
+
+
+def _on(stream, make):
+    """make(), whose tensors belong to ``stream`` if one is given: memory that the current
+    stream's work still uses is then not handed to another stream's."""
+    if stream is None:
+        return make()
+    import torch
+    with torch.cuda.stream(stream):
+        return make()
 
 
 def _cache_rows(cache, k, v):
@@ -608,15 +622,16 @@ def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
     dtype = torch.bfloat16 if dtype is None else dtype
     code = dtype_code(dtype)
     shape = (B, cache.H_kv, S, cache.d)
+    handle = _handle(cache.device, stream)
     if out is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        k, v = _on(stream, lambda: (torch.empty(shape, dtype=dtype, device=cache.device),
+                                    torch.empty(shape, dtype=dtype, device=cache.device)))
     else:
         k, v = out
         _check_out(k, shape, dtype, cache.device, "out[0]")
         _check_out(v, shape, dtype, cache.device, "out[1]")
     _call_on(cache.device, load_library().attn_cache_read, cache.c, t, width, n, k.data_ptr(),
-             v.data_ptr(), B, S, code, _handle(cache.device, stream))
+             v.data_ptr(), B, S, code, handle)
     return k, v
 
 
@@ -643,9 +658,8 @@ def _workspace(workspace, need, cache, stream, handle):
     """(pointer, bytes, tensor) of the scratch of one call; the tensor has to outlive the launch.
     A thread's calls on one stream follow one another, so the cache keeps a workspace for each
     thread and stream (a call's two kernels need not be adjacent when two threads share a
-    stream); a call that is being captured gets one of its own from the graph's memory, and a
-    call on a stream that is not the current one one that lives until that stream is done with
-    it."""
+    stream); a call that is being captured, or on a stream that it names, gets one of its own,
+    which belongs to the graph or to that stream."""
     import torch
     if workspace is not None:
         if not workspace.is_contiguous() or _device_of(workspace) != cache.device:
@@ -657,12 +671,10 @@ def _workspace(workspace, need, cache, stream, handle):
         kept = cache._scratch.get(who)
         if kept is not None and kept[1] >= need:
             return kept
-    workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
+    workspace = _on(stream, lambda: torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device))
     new = (workspace.data_ptr(), max(need, 16), workspace)
     if keep:
         cache._scratch[who] = new
-    elif stream is not None:
-        workspace.record_stream(stream)
     return new
 
 
@@ -681,7 +693,8 @@ def cache_select(q, cache, table, lens, n_select, counts=None, causal: bool = Tr
     handle = _handle(cache.device, stream)
     need = _need(attn_cache_select_workspace_size, B, cache.H_kv, Sq, width)
     wp, wn, held = _workspace(workspace, need, cache, stream, handle)
-    pages = torch.empty((B, cache.H_kv, Sq, n_select), dtype=torch.int32, device=cache.device)
+    pages = _on(stream, lambda: torch.empty((B, cache.H_kv, Sq, n_select), dtype=torch.int32,
+                                            device=cache.device))
     _call_on(cache.device, load_library().attn_cache_select, cache.c, q.data_ptr(), t, width, p, n,
              pages.data_ptr(), n_select, B, H, Sq, 1 if causal else 0, code, wp, wn, handle)
     return pages
@@ -708,8 +721,9 @@ def attention_cache(q, cache, table, lens, counts=None, causal: bool = True,
     need = _need(attn_fwd_cache_workspace_size, B, H, cache.H_kv, Sq, cache.d, code, n_select)
     wp, wn, held = _workspace(workspace, need, cache, stream, handle)
     dev = cache.device
-    out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=dev)
-    lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
+    out, lse = _on(stream, lambda: (
+        torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=dev),
+        torch.empty((B, H, Sq), dtype=torch.float32, device=dev)))
     _call_on(cache.device, load_library().attn_fwd_cache, cache.c, q.data_ptr(), out.data_ptr(),
              lse.data_ptr(), t, width, p, n, listed, n_select, B, H, Sq, 1 if causal else 0,
              0.0 if scale is None else float(scale), code, wp, wn, handle)

@@ -803,7 +803,7 @@ static bool cache_fine(int dtype) { return dtype != ATTN_BF16 && dtype != ATTN_F
 // of the codes: as few units as the registers allow, of as few rows as cover them.
 static int cache_blocks(int64_t rows, int dtype, int d) {
     const int64_t most = cache_fine(dtype) ? 1 : d == 64 ? kMostBlocks<64> : kMostBlocks<128>;
-    const int64_t blocks = (rows + 7) / 8, units = (blocks + most - 1) / most;
+    const int64_t blocks = rows > 8 ? (rows + 7) / 8 : 1, units = (blocks + most - 1) / most;
     return (int)((blocks + units - 1) / units);
 }
 

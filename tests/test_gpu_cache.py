@@ -818,6 +818,29 @@ def test_calls_on_two_streams_at_once(Sq):
     assert torch.equal(o, want[0][0]) and status() == pkg.ATTN_OK
 
 
+def test_results_on_a_named_stream_share_no_memory_with_the_current_one():
+    """Memory freed on the current stream may still be written by what is queued there; a call
+    that names another stream gets its tensors from that one's."""
+    lens, d = [900, 300], 64
+    c, t = filled(lens, 2, 32, d, "e4m3", seed=1)
+    tt, ll = dev(t), dev(lens)
+    q = rows((2, 4, 1, d), 3, torch.bfloat16).cuda()
+    side = torch.cuda.Stream()
+    calls = [lambda s: pkg.attention_cache(q, c, tt, ll, stream=s), lambda s: pkg.cache_read(c, tt, ll, 300, stream=s),
+             lambda s: (pkg.cache_select(q, c, tt, ll, 3, stream=s),)]
+    for f in calls:
+        want = [x.clone() for x in f(None)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        late = [torch.empty_like(x).fill_(7) for x in want for _ in range(4)]
+        del late  # freed, and written once the wait is over
+        got = f(side)
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+    assert status() == pkg.ATTN_OK
+
+
 def test_wrappers_refuse_before_launching():
     c, t = filled([40], 2, 16, 64, "e4m3")
     t, lens = dev(t), dev([40])
