@@ -493,6 +493,7 @@ class KVCache:
 
     def __init__(self, k, v, k_scale, v_scale, k_bounds=None):
         import torch
+        _bind(torch)
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must be [n_pages, H_kv, page, d] of one dtype")
         formats = {torch.float8_e4m3fn: ATTN_CACHE_E4M3, torch.int8: ATTN_CACHE_I8}
@@ -538,10 +539,6 @@ def _int32_on(t, shape, device, name):
 def _sequence_args(cache, table, lens, counts, B):
     """Checks the arrays of the call's sequences; returns the table's pointer and width, and the
     pointers of lens and counts."""
-    global _int32
-    if _int32 is None:
-        import torch
-        _int32 = torch.int32
     shape = table.shape
     if len(shape) != 2 or shape[0] != B:
         raise ValueError("table must be [B, max_pages] with B = %d" % B)
@@ -551,16 +548,25 @@ def _sequence_args(cache, table, lens, counts, B):
             None if counts is None else _int32_on(counts, one, dev, "counts"))
 
 
-_int32 = None  # torch.int32 once a call has needed it
+# What every call on a cache needs of torch, bound once a KVCache exists: looking it up in each
+# call takes as long as a small kernel.
+_torch = _int32 = _raw_stream = _current_device = _capturing = None
+
+
+def _bind(torch):
+    global _torch, _int32, _raw_stream, _current_device, _capturing
+    _torch, _int32 = torch, torch.int32
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _current_device = torch._C._cuda_getDevice
+    _capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _call_on(device, fn, *args):
     """fn(*args) with ``device`` current; raises for a status other than ATTN_OK."""
-    import torch
-    if torch._C._cuda_getDevice() == device.index:
+    if _current_device() == device.index:
         st = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with _torch.cuda.device(device):
             st = fn(*args)
     if st != ATTN_OK:
         raise AttnError(st, fn.__name__)
@@ -569,22 +575,20 @@ def _call_on(device, fn, *args):
 def _handle(device, stream):
     """The cudaStream_t of ``stream``, or of the device's current stream: asked for without
     making a Stream object, which takes longer than a launch."""
-    import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _raw_stream(device.index)
     if stream.device != device:
         raise ValueError("the cache is on %s, the stream on %s" % (device, stream.device))
     return stream.cuda_stream
 
 
-def _on(stream, make):
-    """make(), whose tensors belong to ``stream`` if one is given: memory that the current
-    stream's work still uses is then not handed to another stream's."""
+def _new(stream, shape, dtype, device):
+    """An uninitialised tensor that belongs to ``stream`` if one is given: memory that the
+    current stream's work still uses is then not handed to another stream's."""
     if stream is None:
-        return make()
-    import torch
-    with torch.cuda.stream(stream):
-        return make()
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 def _cache_rows(cache, k, v):
@@ -616,16 +620,15 @@ def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
     """The first S tokens of each sequence as (k, v) [B, H_kv, S, d] of
     ``dtype`` (fp32, bf16 or fp16; default bf16); rows from lens[b] on are
     zero.  ``out`` is a pair of tensors to write instead of new ones."""
-    import torch
     B = table.shape[0]
     t, width, n, _ = _sequence_args(cache, table, lens, None, B)
-    dtype = torch.bfloat16 if dtype is None else dtype
+    dtype = _torch.bfloat16 if dtype is None else dtype
     code = dtype_code(dtype)
     shape = (B, cache.H_kv, S, cache.d)
     handle = _handle(cache.device, stream)
     if out is None:
-        k, v = _on(stream, lambda: (torch.empty(shape, dtype=dtype, device=cache.device),
-                                    torch.empty(shape, dtype=dtype, device=cache.device)))
+        k = _new(stream, shape, dtype, cache.device)
+        v = _new(stream, shape, dtype, cache.device)
     else:
         k, v = out
         _check_out(k, shape, dtype, cache.device, "out[0]")
@@ -660,18 +663,17 @@ def _workspace(workspace, need, cache, stream, handle):
     thread and stream (a call's two kernels need not be adjacent when two threads share a
     stream); a call that is being captured, or on a stream that it names, gets one of its own,
     which belongs to the graph or to that stream."""
-    import torch
     if workspace is not None:
         if not workspace.is_contiguous() or _device_of(workspace) != cache.device:
             raise ValueError("workspace must be a contiguous tensor on %s" % cache.device)
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    keep = stream is None and not torch._C._cuda_isCurrentStreamCapturing()
+    keep = stream is None and not _capturing()
     if keep:
         who = (threading.get_ident(), handle)
         kept = cache._scratch.get(who)
         if kept is not None and kept[1] >= need:
             return kept
-    workspace = _on(stream, lambda: torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device))
+    workspace = _new(stream, max(need, 16), _torch.uint8, cache.device)
     new = (workspace.data_ptr(), max(need, 16), workspace)
     if keep:
         cache._scratch[who] = new
@@ -682,7 +684,6 @@ def cache_select(q, cache, table, lens, n_select, counts=None, causal: bool = Tr
                  stream=None):
     """The ``n_select`` pages each query attends to (attn_cache_select): int32
     [B, H_kv, Sq, n_select], ascending, -1 where fewer are visible."""
-    import torch
     B, H, Sq = _cache_q(cache, q)
     if cache.k_bounds is None:
         raise ValueError("the cache keeps no k_bounds")
@@ -693,8 +694,7 @@ def cache_select(q, cache, table, lens, n_select, counts=None, causal: bool = Tr
     handle = _handle(cache.device, stream)
     need = _need(attn_cache_select_workspace_size, B, cache.H_kv, Sq, width)
     wp, wn, held = _workspace(workspace, need, cache, stream, handle)
-    pages = _on(stream, lambda: torch.empty((B, cache.H_kv, Sq, n_select), dtype=torch.int32,
-                                            device=cache.device))
+    pages = _new(stream, (B, cache.H_kv, Sq, n_select), _int32, cache.device)
     _call_on(cache.device, load_library().attn_cache_select, cache.c, q.data_ptr(), t, width, p, n,
              pages.data_ptr(), n_select, B, H, Sq, 1 if causal else 0, code, wp, wn, handle)
     return pages
@@ -707,7 +707,6 @@ def attention_cache(q, cache, table, lens, counts=None, causal: bool = True,
     over the pages of ``pages`` [B, H_kv, Sq, n] (``cache_select``).  The last
     ``counts[b]`` (default Sq) of the ``lens[b]`` tokens are the queries' own.
     The workspace is allocated here unless given.  Returns (o, lse)."""
-    import torch
     B, H, Sq = _cache_q(cache, q)
     t, width, p, n = _sequence_args(cache, table, lens, counts, B)
     code = dtype_code(q.dtype, out_dtype)
@@ -721,9 +720,8 @@ def attention_cache(q, cache, table, lens, counts=None, causal: bool = True,
     need = _need(attn_fwd_cache_workspace_size, B, H, cache.H_kv, Sq, cache.d, code, n_select)
     wp, wn, held = _workspace(workspace, need, cache, stream, handle)
     dev = cache.device
-    out, lse = _on(stream, lambda: (
-        torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=dev),
-        torch.empty((B, H, Sq), dtype=torch.float32, device=dev)))
+    out = _new(stream, q.shape, q.dtype if out_dtype is None else out_dtype, dev)
+    lse = _new(stream, (B, H, Sq), _torch.float32, dev)
     _call_on(cache.device, load_library().attn_fwd_cache, cache.c, q.data_ptr(), out.data_ptr(),
              lse.data_ptr(), t, width, p, n, listed, n_select, B, H, Sq, 1 if causal else 0,
              0.0 if scale is None else float(scale), code, wp, wn, handle)
