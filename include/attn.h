@@ -307,7 +307,8 @@ ATTN_API int attn_merge(const float *o_parts, const float *lse_parts, int n_part
  *   nearest, ties to even.  A NaN or an infinity makes the scale of its block
  *   NaN: everything read from that block and head is NaN until the page is
  *   started again at its first row.  attn_cache_read takes any scale, the
- *   others any finite scale >= 0 or NaN; pages that append continues must hold such powers of two.
+ *   others any finite scale >= 0 or NaN; pages that append continues must hold
+ *   such powers of two.
  */
 typedef enum attn_cache_format {
     ATTN_CACHE_E4M3 = 0, /* 4-bit exponent, 3-bit mantissa, no infinities; largest 448 */
@@ -395,11 +396,11 @@ ATTN_API int attn_cache_select(const attn_cache *cache, const void *q, const int
  *          (0 or n_select for its last argument), not overlapping any other
  *          argument.  Calls that may overlap on the GPU, replays of graphs
  *          among them, need workspaces of their own.
- * Arithmetic: exact products of codes and q, fp32 sums; the weights keep 22
- * bits, or 11 for a 16-bit output with more than 8 query rows per kv head
- * (H / H_kv * Sq, or H / H_kv with a page list).
+ * Arithmetic: exact products of codes and q (fp32 q: 22 bits of each row's
+ * range), fp32 sums; the weights keep 22 bits for fp32 outputs, 11 for 16-bit
+ * ones.
  * Results do not depend on other sequences' contents, but the grouping of sums
- * (not their terms) follows all lengths of the call.  Two kernels.
+ * (not their terms) follows all lengths of the call.  One or two kernels.
  */
 ATTN_API int attn_fwd_cache_workspace_size(int B, int H, int H_kv, int Sq, int d, int dtype,
                                   int n_select, size_t *bytes);

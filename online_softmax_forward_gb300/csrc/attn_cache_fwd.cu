@@ -6,24 +6,29 @@
 //
 // Work.  A unit is (sequence, kv head, block of query rows): the G query heads
 // of a kv head share its keys, so the rows of a block are (query, head of the
-// group).  Its keys are walked in tiles of KT keys (a page, or 64 of its 128).
+// group).  Its keys are walked in tiles of KT keys (32, or a page of 16).
 // All tiles of a call are numbered through and cut into equal contiguous
 // ranges, one per warp (cache_index.h): ragged lengths and few sequences fill
 // the GPU alike.  A warp writes the units it covers alone.  Of the units that
 // several warps of a CTA share the states are joined in shared memory, and a
 // second kernel joins the at most one unit that runs over the end of each CTA's
-// range, with the online softmax's merge of states.
+// range, with the online softmax's merge of states.  Where units are few and of
+// like length a CTA takes one each, and nothing is left to join (kSwitch).
 //
 // Products.  The 8-bit codes are exact in fp16, so both products run on
 // mma.m16n8k16 with fp32 accumulation and no dequantised tile exists
 // anywhere: the page's scales multiply the scores and the page's share of o.
-// A decode step is bound by reading the codes; of the 16 rows of the MMA few
-// carry queries, which costs nothing that is scarce here.
-//   8-row form: rows 0-7 are query rows, rows 8-15 the same rows' rounding
-//     remainders: q = hi + lo (lo = 0 unless q is fp32) and p = hi + lo, so the
-//     products are those of 22-bit numbers and fp32 outputs keep their digits.
-//   16-row form (16-bit output, 9 to 16 rows; with a page list, any number above 8):
-//     p is rounded once to fp16 (2^-12, as an fp16 output is, or less than a bf16 one).
+// Keys and channels lie on the MMA's 16 rows and 8 query rows on its columns,
+// S^T = K Q^T and O^T = V^T P^T, since a decode step has few queries: with the
+// queries on the rows it takes twice the MMAs and twice the registers for o (4 x 32
+// heads, 32k keys: 174 -> 171 us; one 1k sequence 11.1 -> 10.2 us).  P leaves
+// the first product key by key and enters the second query by query: movmatrix
+// turns it.  A warp takes up to two blocks of 8 rows, three at d = 64, which share
+// the loads and conversions of the codes.
+//   16-bit outputs: q is exact in fp16, p is rounded once to it (2^-12, as an
+//     fp16 output is, or less than a bf16 one).
+//   fp32 outputs: q = hi + lo and p = hi + lo in two products each, those of
+//     22-bit numbers.
 // q rows are first multiplied by a power of two that puts the row's largest
 // magnitude in [2^14, 2^15): any fp32 or bf16 exponent then fits fp16.
 //
@@ -34,13 +39,22 @@
 // maximum across lanes and no rescaling in the others.
 //
 // Loads.  Each warp copies its own tiles into a ring of shared memory slots with
-// 16-byte cp.async (a slot holds the codes of one tile's keys or values), all
-// slots but the one in use in flight, and waits for nobody else.  The MMA's k
-// index may name the channels in any order that q and k share, and its n index
-// any channel of v: lane (g, t) = (lane / 4, lane % 4) reads D/4 consecutive
-// bytes of key row g, and D/8 consecutive bytes of value rows 2t, 2t+1, 2t+8,
-// 2t+9.  The 16-byte pieces of a row are swizzled so that both reads are free of
-// bank conflicts.
+// 16-byte cp.async (a slot holds the codes of one tile's keys and values), all
+// slots but the one in use in flight, and waits for nobody else.  (Tiles by TMA,
+// with the swizzle in the tensor map, measured the same for 4 x 32 x 32k keys and
+// cost the short calls a microsecond on the host.)  The MMA's k index may name the
+// channels in any order that q and k share, and its row any channel of v: lane
+// (g, t) = (lane / 4, lane % 4) reads D/4 consecutive bytes of key rows g and
+// g + 8, and D/8 consecutive bytes of value rows 2t, 2t+1, 2t+8, 2t+9.  The 16-byte
+// pieces of a row are swizzled so that both reads are free of bank conflicts.
+//
+// Bound: by the reading of the codes where they are many (4 x 32 heads, 32k keys,
+// d = 128: 172 us, 6.2 TB/s, 92 % of the copy rate; the SMs do not get equal shares
+// of the memory and the last ends 14 % after the mean), by waits in short calls
+// (one sequence of 1000 tokens, 8 kv heads: 9.7 us, of which 3 for eight steps of
+// keys; the rest finds the tiles, loads q, joins, each a chain of cold loads and
+// code).  8 warps of up to 240 registers; 12 warps, which one block's registers
+// allow, measured 169 us and 9.9 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -57,8 +71,11 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRing = 24 * 1024;  // shared memory of each warp's tiles, later of its states
-constexpr int kMinTiles = 1;  // tiles per worker when there are few
-constexpr int kSwitch = 8;   // tiles that a second unit, and a second kernel, cost a warp
+// Tiles that a second unit and a second kernel cost a warp.  With 2, 5, 8, 12, 16 in us: five
+// drafts of 16 sequences of up to 4096 tokens 35.2, 35.2, 32.9, 32.8, 30.1; one sequence of 1000
+// tokens 10.6, 9.6, 9.6, 9.6, 9.6; selection and attention over 96 pages of 32 for 16 units
+// 34.2, 34.2, 34.2, 42.2, 42.1
+constexpr int kSwitch = 8;
 
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
     uint4 u;
@@ -213,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                     for (size_t e = threadIdx.x; e < n; e += kThreads) a.lse[row0 + e] = -INFINITY;
             }
         }
-        workers = worker_count(total, a.workers, kMinTiles);
+        workers = worker_count(total, a.workers, 1);
         w += blockIdx.x * kWarps;
         const int64_t all = (int64_t)a.B * a.units;
         bool alone = false;  // a CTA takes one unit
@@ -791,12 +808,6 @@ int launch_fwd_n(const FwdArgs &a, int nb, bool fine, int kt, unsigned grid, cud
 
 }  // namespace
 
-// Query rows per kv head from which the 128-row tcgen05 kernel runs (16-bit
-// outputs, all pages).
-constexpr int64_t kTcRows = 33;
-static bool cache_tc(int64_t rows, int dtype, bool listed) {
-    return !listed && (dtype == ATTN_BF16 || dtype == ATTN_F16) && rows >= kTcRows;
-}
 // fp32 outputs keep q and the weights in 22 bits.
 static bool cache_fine(int dtype) { return dtype != ATTN_BF16 && dtype != ATTN_F16; }
 // Blocks of 8 rows that a warp takes at once, which share the loads and conversions
@@ -807,14 +818,29 @@ static int cache_blocks(int64_t rows, int dtype, int d) {
     return (int)((blocks + units - 1) / units);
 }
 
+// Which kernel takes a call of 16-bit output over all pages.  The 128-row tcgen05
+// kernel takes the same time for 9 rows as for 128; the one of this file is faster
+// as long as its units leave SMs over or are small.  Times in us here and there,
+// 8 kv heads, d = 128 (d = 64):
+//      rows   2 x 4096 keys           16 x 4096               1 x 32768
+//      32     20.6, 26.7 (17.4, 22.2) 56.9, 57.9 (44.1, 41.3) 36.3, 49.0 (27.1, 37.0)
+//      48     24.0, 26.8 (22.1, 22.4) 74.3, 59.9 (58.4, 41.7) 43.7, 49.6 (35.0, 37.6)
+//      64     26.5, 27.4 (25.8, 22.7) 92.1, 60.1 (72.3, 42.0) 50.7, 50.0 (42.0, 38.4)
+//      96     30.8, 28.3 (28.5, 23.3) 126.9, 61.6 (90.7, 43.7) 67.3, 50.5 (49.4, 39.0)
+constexpr int64_t kTcRows = 33, kTcAlways = 65;
+static bool cache_tc(int64_t rows, int64_t units, int sms, int dtype, bool listed) {
+    return !listed && !cache_fine(dtype) && (rows >= kTcAlways || (rows >= kTcRows && units > sms));
+}
+
 // Workspace: the tails [CTA], a state per warp, two per CTA and their lse (the
-// tcgen05 kernel: without the warps').
+// tcgen05 kernel: without the warps').  For any number of SMs.
 size_t cache_fwd_workspace(int B, int H, int H_kv, int Sq, int d, int dtype, bool listed) {
     const int64_t rows = (int64_t)(H / H_kv) * (listed ? 1 : Sq);
-    if (cache_tc(rows, dtype, listed))
-        return (size_t)kCacheMaxCtas * (16 + 2 * 128 * (size_t)d * 4 + 2 * 128 * 4);
     const size_t R = cache_blocks(rows, dtype, d) * 8;
-    return (size_t)kCacheMaxCtas * (16 + (kWarps + 2) * R * d * 4 + 2 * R * 4);
+    const size_t mma = (size_t)kCacheMaxCtas * (16 + (kWarps + 2) * R * d * 4 + 2 * R * 4);
+    const size_t tc = (size_t)kCacheMaxCtas * (16 + 2 * 128 * (size_t)d * 4 + 2 * 128 * 4);
+    if (cache_tc(rows, INT64_MAX, 0, dtype, listed)) return rows >= kTcAlways || tc > mma ? tc : mma;
+    return mma;
 }
 
 int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, const int32_t *table,
@@ -835,29 +861,29 @@ int launch_cache_fwd(const attn_cache &c, const void *q, void *o, float *lse, co
     a.by_group = fast_div((uint32_t)a.G);
     a.status = status_word_device_ptr();
     if (!a.status) return ATTN_ERR_CUDA;
-    if (cache_tc(a.rows, dtype, pages != nullptr)) return launch_cache_tc(a, c.d, c.format, workspace, stream);
+    const int sms = device_sm_count();
+    if (sms <= 0) return ATTN_ERR_CUDA;
     const int nb = cache_blocks(a.rows, dtype, c.d), R = nb * 8;
     const bool fine = cache_fine(dtype);
     a.nrb = (a.rows + R - 1) / R;
     a.units = a.Hkv * a.nseg * a.nrb;
     const int64_t units = (int64_t)B * a.units;  // at most B * H * Sq < 2^31
+    if (cache_tc(a.rows, units, sms, dtype, pages != nullptr)) return launch_cache_tc(a, c.d, c.format, workspace, stream);
     a.by_units = fast_div((uint32_t)a.units);
     a.by_per = fast_div((uint32_t)(a.nseg * a.nrb));
     a.by_nrb = fast_div((uint32_t)a.nrb);
     const int kt = tile_keys(c.page);
-    const int sms = device_sm_count();
-    if (sms <= 0) return ATTN_ERR_CUDA;
     // as many CTAs as the longest possible lengths can give every warp a tile
+    const int room = sms < kCacheMaxCtas ? sms : kCacheMaxCtas;
     const double most = (double)units * (pages ? (double)n_select * c.page : (double)max_pages * c.page) / kt;
-    int64_t ctas = most / kWarps < sms ? (int64_t)(most / kWarps) + 1 : sms;
-    if (ctas > kCacheMaxCtas) ctas = kCacheMaxCtas;
-    if (ctas > sms) ctas = sms;
+    int64_t ctas = most / kWarps < room ? (int64_t)(most / kWarps) + 1 : room;
+    if (ctas > room) ctas = room;
     // A CTA for each unit, if that is not longer for a warp than its share of all the work by
     // more than what sharing a unit costs: by the number of listed pages or the longest possible
     // lengths, and then without the second kernel, or, in the kernel, by the lengths
     const int64_t longest = pages ? (int64_t)n_select * (c.page / kt) : ((int64_t)max_pages * c.page + kt - 1) / kt;
-    const double share = pages ? (double)units * longest / ((double)sms * kWarps) : 1;
-    a.one_each = units <= sms && longest <= (share + kSwitch) * kWarps;
+    const double share = pages ? (double)units * longest / ((double)room * kWarps) : 1;
+    a.one_each = units <= room && longest <= (share + kSwitch) * kWarps;
     if (a.one_each) ctas = units;
     a.workers = (int)ctas * kWarps;
     a.tail = reinterpret_cast<int4 *>(workspace);
