@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
         Place here = start;
         Piece p;
         int i = 0, j = 0, slot = 0;
+        int held0 = -4;  // `at` holds the places of the piece's tiles from this one on
         auto settle = [&] {  // to the first piece from here on that has a live tile
             while (i < n_tiles) {
                 p = piece_at(here, i);
@@ -325,38 +326,48 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                 if (i < n_tiles) advance(here, p.left, a.units, tiles);
             }
         };
-        // lane s < 8: 16-key piece s of the tile as a 16-row piece of the pool, -1: none
+        // lane 8 k + s: 16-key piece s of tile held0 + k as a 16-row piece of the pool, -1: none.
+        // Looked up for four tiles at a time, since each look waits for the table
+        int at = -1;
         auto find = [&] {
-            int at = -1;
-            const int key = (p.t0 + j) * KT + lane * 16;
-            if (i < n_tiles && lane < 8 && key < p.len) {
+            if (i < n_tiles && j < held0 + 4) return;
+            held0 = j;
+            at = -1;
+            if (i >= n_tiles) return;
+            const int tile = j + (lane >> 3), key = (p.t0 + tile) * KT + (lane & 7) * 16;
+            if (tile < p.live && key < p.len) {
                 const int phys = a.table[(int64_t)p.u.b * a.max_pages + (key >> page_shift)];
                 if (phys < 0 || phys >= a.n_pages) atomicOr(a.status, kStatusTable);
                 else at = ((phys * a.Hkv + p.u.hk) << (page_shift - 4)) + ((key & (a.page - 1)) >> 4);
             }
-            return at;
         };
         settle();
-        int at = find();
+        find();
         uint4 raw[N];
         float scale = 0.f;   // lanes 0-7: of the tile's keys, 8-15: of its values, 16: `miss`
         uint32_t miss = 0;   // pieces of the tile that are not there
         int key0 = 0, len = 0, ring = 0;
         bool have = false;
-        auto load = [&](int e) {  // of the tile at (p, j)
+        int seg[N];  // of the tile at (p, j): the pieces that this warp loads from
+        auto places = [&] {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                seg[e] = __shfl_sync(0xffffffffu, at, (j - held0) * 8 + ((cw + kConverters * e) * kRows >> 4 & 7));
+        };
+        auto load = [&](int e) {
             const int row = (cw + kConverters * e) * kRows;
-            const int seg = __shfl_sync(0xffffffffu, at, (row >> 4) & 7);
-            if (row < KT && seg >= 0) raw[e] = ldg16(src + (size_t)seg * (16 * D) + (row & 15) * D);
+            if (row < KT && seg[e] >= 0) raw[e] = ldg16(src + (size_t)seg[e] * (16 * D) + (row & 15) * D);
         };
         // what was just loaded becomes the tile to convert; on to the next
         auto take = [&] {
             have = i < n_tiles;
-            miss = __ballot_sync(0xffffffffu, lane < 8 && at < 0) & 0xffu;
             if (!have) return;
+            const int first = (j - held0) * 8;
+            miss = __ballot_sync(0xffffffffu, at < 0) >> first & 0xffu;
             if (warp == kConvertWarp0) {
-                const int seg = __shfl_sync(0xffffffffu, at, lane & 7);
+                const int piece = __shfl_sync(0xffffffffu, at, first + (lane & 7));
                 scale = lane == 16 ? __uint_as_float(miss) : 0.f;
-                if (lane < 16 && seg >= 0) scale = (lane < 8 ? a.ks : a.vs)[seg >> (page_shift - 4)];
+                if (lane < 16 && piece >= 0) scale = (lane < 8 ? a.ks : a.vs)[piece >> (page_shift - 4)];
             }
             key0 = (p.t0 + j) * KT;
             len = p.len;
@@ -364,23 +375,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             if (++j == p.live) {
                 slot = (slot + p.live) % kScaleRing;
                 j = 0;
+                held0 = -4;
                 i += p.left;
                 if (i < n_tiles) advance(here, p.left, a.units, tiles);
                 settle();
             }
-            at = find();
+            find();
         };
+        places();
 #pragma unroll
         for (int e = 0; e < N; ++e) load(e);
         take();
         uint32_t st = 0, lap = 0;
         while (have) {
+            places();
             if (!__all_sync(0xffffffffu, watch.wait(bar(empty[st]), (lap & 1) ^ 1))) break;
-            if (warp == kConvertWarp0) {
-                if (lane < 17) scales[ring * kScaleWords + lane] = scale;
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(bars->sc_full[ring]));
-            }
             // behind the last token, or without a page, there are no values
             const int held = len - key0;
             const bool part = values && (held < KT || miss != 0);
@@ -404,6 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                     ptx::st_shared_v4(to + (in << 4), h[0], h[1], h[2], h[3]);
                     ptx::st_shared_v4(to + ((in ^ 1) << 4), h[4], h[5], h[6], h[7]);
                 }
+            }
+            if (warp == kConvertWarp0) {
+                if (lane < 17) scales[ring * kScaleWords + lane] = scale;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(bars->sc_full[ring]));
             }
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(bar(full[st]));
