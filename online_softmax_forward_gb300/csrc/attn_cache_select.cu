@@ -12,7 +12,8 @@
 // mma.m16n8k16, in the fp16 form of attn_cache_fwd.cu (a power of two per row of
 // q, codes exact).  A cluster of CTAs shares the pages of one (sequence, kv
 // head, query) and writes its scores into the first CTA's shared memory, which
-// finds the cut by bisection and writes the list.
+// finds the cut by a histogram of 1024 bins, then among the pages of the cut's bin,
+// and writes the list.
 //
 // The fp32 scores carry a bound on their error.  A page whose score is further
 // from the cut than that is decided by it; the few others are summed again in
@@ -20,6 +21,12 @@
 // up exactly unless they span more than 2^27, so the choice does not depend on
 // the order of a sum.  (fp64 for every page would cost more than the reading:
 // this GPU has 1/64 the fp64 rate.)
+//
+// Bound: by waits.  With the attention over the choice, 32 of 512 pages for 64 units
+// take 27 us and 96 of 4096 for 16 units 34 us, 12 and 23 us of it here, where the
+// bounds alone would be read in 1 to 3 us: lengths, table, bounds, scores, histogram
+// and list follow one another.  Three kernels in its place (scores, cut, list) took 50
+// and 75 us for the pair, a bisection in place of the histogram 49.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
