@@ -53,7 +53,8 @@ struct SelectArgs {
     const int32_t *table, *lens, *counts;
     int32_t *pages;  // [B][Hkv][Sq][n]
     double *exact;   // [B][Hkv][Sq][max_pages]: fp64 scores of the pages near the cut
-    int B, Hkv, G, Sq, page, n_pages, max_pages, n, causal, cluster;
+    int B, Hkv, G, Sq, page, n_pages, max_pages, n, causal, cluster, cluster_shift;
+    FastDiv by_queries, by_heads;
     int *status;
 };
 
@@ -82,21 +83,20 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Exclusive prefix sum of one flag per thread; *total gets the block's sum.
-__device__ __forceinline__ int block_scan(int x, int *warps, int *total) {
+// Sum of the threads' numbers before this one's; `warps` is not in use.
+__device__ __forceinline__ int block_scan(int x, int *warps) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t m = __ballot_sync(0xffffffffu, x != 0);
-    __syncthreads();  // `warps` may still be read from the last call
-    if (lane == 0) warps[warp] = __popc(m);
-    __syncthreads();
-    int before = 0, all = 0;
+    int incl = x;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += warps[w];
-        all += warps[w];
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
     }
-    *total = all;
-    return before + __popc(m & ((1u << lane) - 1));
+    if (lane == 31) warps[warp] = incl;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) incl += w < warp ? warps[w] : 0;
+    return incl - x;
 }
 
 // Exact score of a page, in fp64: eight lanes per head, four heads at a time.
@@ -147,13 +147,15 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     extern __shared__ __align__(16) uint32_t key[];  // ordered scores, later 1 for a page that is in
     __shared__ int wsum[kWarps], s_near, s_in, s_open, s_bin;
     __shared__ int hist[kBins];
+    __shared__ double s_exact[kThreads];
     // largest scale (infinity: leave it to fp64), largest and smallest score, by warp and by CTA
     __shared__ uint32_t w_top[3][kWarps], s_top[3][kMaxCluster];
-    const int64_t unit = blockIdx.x / a.cluster;
-    const int rank = (int)(blockIdx.x - unit * a.cluster);
-    const int i = (int)(unit % a.Sq);
-    const int hk = (int)(unit / a.Sq % a.Hkv);
-    const int b = (int)(unit / a.Sq / a.Hkv);
+    const int64_t unit = blockIdx.x >> a.cluster_shift;
+    const int rank = (int)(blockIdx.x & (a.cluster - 1));
+    const uint32_t head_of = (uint32_t)unit / a.by_queries;
+    const int i = (int)((uint32_t)unit - head_of * a.Sq);
+    const int b = (int)(head_of / a.by_heads);
+    const int hk = (int)(head_of - (uint32_t)b * a.Hkv);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, t4 = lane & 3;
     const int len0 = a.lens[b], cnt0 = a.counts ? a.counts[b] : a.Sq;
     const int len = clamp_len(len0, a.max_pages, a.page);
@@ -231,16 +233,23 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         mass = (sum > mass || sum != sum) ? sum : mass;
         if (g0 == 0) cluster_wait();
+        int next[kGroups];  // pages of the table, asked for a step ahead
+        auto look = [&](int base) {
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+                const int p = base + 8 * j + g;
+                next[j] = p < p1 ? table[p] : -1;
+            }
+        };
+        constexpr int kStride = kThreads / 4 * kGroups;
+        look(p0 + warp * 8 * kGroups);
 #pragma unroll 1
-        for (int base = p0 + warp * 8 * kGroups; base < p1; base += kThreads / 4 * kGroups) {
+        for (int base = p0 + warp * 8 * kGroups; base < p1; base += kStride) {
             uint4 lo[kGroups][D / 64], hi[kGroups][D / 64];
             float sc[kGroups];
             int phys[kGroups];
 #pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                const int p = base + 8 * j + g;
-                phys[j] = p < p1 ? table[p] : -1;
-            }
+            for (int j = 0; j < kGroups; ++j) phys[j] = next[j];
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 const bool in = phys[j] >= 0 && phys[j] < a.n_pages;
@@ -254,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
                 }
                 sc[j] = in ? a.k_scale[ph] : 0.f;
             }
+            look(base + kStride);
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 float s0[4] = {}, s1[4] = {};
@@ -344,24 +354,15 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     // not decreasing with the score
     auto bin_of = [&](float x) { return (int)fminf(fmaxf((x - least) * per_bin, 0.f), kBins - 1.f); };
     if (binned) {
+#pragma unroll 4
         for (int p = t; p < m; p += kThreads) atomicAdd(&hist[bin_of(unordered(key[p]))], 1);
         __syncthreads();
         // thread t: bins kBins - 1 - 4 t down
         int c[4], sum = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum += c[e] = hist[kBins - 1 - 4 * t - e];
-        int incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) wsum[warp] = incl;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) incl += w < warp ? wsum[w] : 0;
-        int above = incl - sum;
-        if (above < k && k <= incl) {
+        int above = block_scan(sum, wsum);
+        if (above < k && k <= above + sum) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (above < k && k <= above + c[e]) s_bin = kBins - 1 - 4 * t - e;
@@ -379,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     int *near = reinterpret_cast<int *>(key + a.max_pages);
     const bool equal = eps == 0.f;  // q or every scale is 0: all scores are
     int n_in = 0;
+#pragma unroll 4
     for (int p = t; p < m; p += kThreads) {
         const int bin = binned ? bin_of(unordered(key[p])) : bin_lo;
         const bool in = equal ? p < k : bin > bin_hi && k > 0;
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     const int near_n = s_near, places = k - s_in;
     // settle the near ones among themselves: `sure` beat a page whatever the errors,
     // `may` might
-    double *exact = a.exact + unit * a.max_pages;
+    double *exact = near_n <= kThreads ? s_exact : a.exact + unit * a.max_pages;
     int settled = 0;
     for (int base = 0; base < near_n; base += kThreads) {
         const int j = base + t;
@@ -440,16 +442,18 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
         }
     }
     __syncthreads();
-    // ascending order; the last visible page closes the list
-    int done = 0;
-    for (int base = 0; base < m; base += kThreads) {
-        const int p = base + t;
-        const int in = p < m ? (int)(key[p] & 1) : 0;
-        int n;
-        const int at = done + block_scan(in, wsum, &n);
-        if (in && in_bounds(at < k, a.status)) out[at] = p;
-        done += n;
-    }
+    // ascending order; the last visible page closes the list.  A thread takes a stretch of
+    // pages, of odd length so that the threads' reads fall into different banks
+    const int per = (m + kThreads - 1) / kThreads | 1;
+    const int p_end = min(m, (t + 1) * per);
+    int mine = 0;
+    for (int p = t * per; p < p_end; ++p) mine += (int)(key[p] & 1);
+    int at = block_scan(mine, wsum);
+    for (int p = t * per; p < p_end; ++p)
+        if (key[p] & 1) {
+            if (in_bounds(at < k, a.status)) out[at] = p;
+            ++at;
+        }
     if (t == 0) out[k] = m;
 }
 
@@ -457,9 +461,13 @@ template <int D, int FMT, int DT>
 int launch_select_t(SelectArgs &a, int sms, cudaStream_t stream) {
     const int64_t units = (int64_t)a.B * a.Hkv * a.Sq;
     // CTAs per unit: up to eight while they fit the GPU at two an SM and have 64 pages each
-    a.cluster = 1;
-    while (a.cluster < kMaxCluster && units * a.cluster * 2 <= 2 * sms && a.cluster * 2 * 64 <= a.max_pages)
-        a.cluster *= 2;
+    a.cluster_shift = 0;
+    while (1 << a.cluster_shift < kMaxCluster && units << (a.cluster_shift + 1) <= 2 * sms &&
+           128 << a.cluster_shift <= a.max_pages)
+        ++a.cluster_shift;
+    a.cluster = 1 << a.cluster_shift;
+    a.by_queries = fast_div((uint32_t)a.Sq);
+    a.by_heads = fast_div((uint32_t)a.Hkv);
     auto kern = cache_select_kernel<D, FMT, DT>;
     if (!set_smem_limit_once(reinterpret_cast<const void *>(kern), kMaxSelectPages * 8)) return ATTN_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
@@ -492,7 +500,7 @@ int launch_cache_select(const attn_cache &c, const void *q, const int32_t *table
                         cudaStream_t stream) {
     SelectArgs a = {q, (const uint8_t *)c.k_bounds, c.k_scale, table, lens, counts, pages,
                     reinterpret_cast<double *>(workspace), B, c.H_kv, H / c.H_kv, Sq, c.page,
-                    c.n_pages, max_pages, n_select, causal, 1, status_word_device_ptr()};
+                    c.n_pages, max_pages, n_select, causal, 1, 0, {}, {}, status_word_device_ptr()};
     if (!a.status) return ATTN_ERR_CUDA;
     const int sms = device_sm_count();
     if (sms <= 0) return ATTN_ERR_CUDA;
