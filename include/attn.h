@@ -333,7 +333,8 @@ typedef struct attn_cache {
  * written earlier (they are overwritten; scale and bounds of a page that is
  * continued keep covering them).  Rows of a page behind the last new token are
  * left as they were.  No page may be written for two sequences, or for one
- * twice, in one call (its contents are then undefined).  One kernel.
+ * twice, in one call (its contents are then undefined).  The cache's arrays
+ * must not overlap.  One kernel.
  */
 ATTN_API int attn_cache_append(const attn_cache *cache, const void *k, const void *v,
                       const int32_t *table, int max_pages, const int32_t *pos,

@@ -620,7 +620,9 @@ def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
     """The first S tokens of each sequence as (k, v) [B, H_kv, S, d] of
     ``dtype`` (fp32, bf16 or fp16; default bf16); rows from lens[b] on are
     zero.  ``out`` is a pair of tensors to write instead of new ones."""
-    B = table.shape[0]
+    B = table.shape[0] if table.dim() == 2 else -1
+    if S < 0:
+        raise ValueError("S must not be negative, got %d" % S)
     t, width, n, _ = _sequence_args(cache, table, lens, None, B)
     dtype = _torch.bfloat16 if dtype is None else dtype
     code = dtype_code(dtype)
@@ -712,9 +714,9 @@ def attention_cache(q, cache, table, lens, counts=None, causal: bool = True,
     code = dtype_code(q.dtype, out_dtype)
     listed, n_select = None, 0
     if pages is not None:
-        n_select = pages.shape[-1]
+        n_select = pages.shape[-1] if pages.dim() == 4 else 0
         if n_select < 1:
-            raise ValueError("pages must list at least one page")
+            raise ValueError("pages must be [B, H_kv, Sq, n] and list at least one page")
         listed = _int32_on(pages, (B, cache.H_kv, Sq, n_select), cache.device, "pages")
     handle = _handle(cache.device, stream)
     need = _need(attn_fwd_cache_workspace_size, B, H, cache.H_kv, Sq, cache.d, code, n_select)

@@ -254,6 +254,16 @@ static bool cache_overlap(const attn_cache &c, const void *p, size_t n) {
            overlap(p, n, c.k_scale, blocks * 4) || overlap(p, n, c.v_scale, blocks * 4) ||
            overlap(p, n, c.k_bounds, blocks * 2 * c.d);
 }
+// Do two arrays of the cache overlap?  What is written to one would change the other.
+static bool cache_shared(const attn_cache &c) {
+    const size_t blocks = (size_t)c.n_pages * c.H_kv, codes = cache_code_bytes(c);
+    const void *p[5] = {c.k, c.v, c.k_scale, c.v_scale, c.k_bounds};
+    const size_t n[5] = {codes, codes, blocks * 4, blocks * 4, blocks * 2 * c.d};
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(p[i], n[i], p[j], n[j])) return true;
+    return false;
+}
 // The arrays of one call's sequences: table and lens (or pos), counts may be null.
 static bool sequences_ok(const attn_cache &c, const int32_t *table, int max_pages,
                          const int32_t *lens, const int32_t *counts, int B) {
@@ -586,7 +596,7 @@ int attn_cache_append(const attn_cache *cache, const void *k, const void *v, con
         return ATTN_ERR_INVALID_ARG;
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_INVALID_ARG;
     const size_t n = (size_t)B * cache->H_kv * S * cache->d * (dt == 0 ? 4 : 2);
-    if (cache_overlap(*cache, k, n) || cache_overlap(*cache, v, n) ||
+    if (cache_shared(*cache) || cache_overlap(*cache, k, n) || cache_overlap(*cache, v, n) ||
         cache_overlap(*cache, table, (size_t)B * max_pages * 4) ||
         cache_overlap(*cache, pos, (size_t)B * 4) || cache_overlap(*cache, counts, counts ? (size_t)B * 4 : 0))
         return ATTN_ERR_INVALID_ARG;

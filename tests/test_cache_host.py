@@ -208,8 +208,8 @@ def test_bad_caches_are_refused(lib, name, kw):
     ("append", dict(dtype=pkg.ATTN_BF16_OUT_F32)), ("append", dict(dtype=9)), ("append", dict(S=-1)),
     ("append", dict(B=-1)), ("append", dict(k=None)), ("append", dict(v=NV + 8)), ("append", dict(table=None)),
     ("append", dict(table=TABLE + 2)), ("append", dict(pos=None)), ("append", dict(counts=COUNTS + 1)),
-    ("append", dict(max_pages=0)), ("append", dict(max_pages=(2 ** 31 - 1024) // 16)), ("append", dict(k=K)), ("append", dict(v=KB)), ("append", dict(table=VS)),
-    ("append", dict(counts=K + 64)), ("append", dict(B=1 << 20, S=1 << 20)),
+    ("append", dict(max_pages=0)), ("append", dict(max_pages=(2 ** 31 - 1024) // 16)), ("append", dict(k=K)),
+    ("append", dict(v=KB)), ("append", dict(table=VS)), ("append", dict(counts=K + 64)), ("append", dict(B=1 << 20, S=1 << 20)),
     ("read", dict(dtype=pkg.ATTN_F16_OUT_F32)), ("read", dict(S=-1)), ("read", dict(k=None)),
     ("read", dict(v=NV + 4)), ("read", dict(v=NK + 64)), ("read", dict(k=K)), ("read", dict(v=KS)),
     ("read", dict(k=TABLE)), ("read", dict(lens=None)), ("read", dict(max_pages=-3)),
@@ -231,6 +231,12 @@ def test_bad_caches_are_refused(lib, name, kw):
 ], ids=lambda x: x if isinstance(x, str) else ",".join("%s=%s" % i for i in x.items()))
 def test_bad_arguments_are_refused(lib, name, kw):
     assert CALLS[name](lib, **kw) == pkg.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(v=K), dict(v=K + 16), dict(k_scale=V), dict(v_scale=KS), dict(v_scale=KS + 4),
+                                dict(k_bounds=K), dict(k_bounds=VS)], ids=str)
+def test_append_refuses_a_cache_whose_arrays_overlap(lib, kw):
+    assert append(lib, cache(**kw)) == pkg.ATTN_ERR_INVALID_ARG
 
 
 def test_select_needs_bounds(lib):

@@ -858,6 +858,9 @@ def test_wrappers_refuse_before_launching():
         lambda: pkg.cache_append(c, x.expand(1, 2, 5, 64), x.expand(1, 2, 5, 64), t, lens),
         lambda: pkg.cache_read(c, t, lens, 40, dtype=torch.float64),
         lambda: pkg.cache_read(c, t, lens, 40, out=(x, x)),
+        lambda: pkg.cache_read(c, t, lens, -1),
+        lambda: pkg.cache_read(c, lens[0], lens, 40),
+        lambda: pkg.attention_cache(q, c, t, lens, pages=lens[0]),
         lambda: pkg.cache_select(q, c, t, lens, 0),
         lambda: pkg.cache_select(q[:, :3], c, t, lens, 1),
         lambda: pkg.attention_cache(q[..., :32], c, t, lens),
