@@ -591,6 +591,13 @@ def _new(stream, shape, dtype, device):
         return _torch.empty(shape, dtype=dtype, device=device)
 
 
+def _new_like(stream, t):
+    """The same for a tensor of a contiguous one's shape, type and device, in less time."""
+    if stream is None:
+        return _torch.empty_like(t)
+    return _new(stream, t.shape, t.dtype, t.device)
+
+
 def _cache_rows(cache, k, v):
     """(B, S, attn_dtype) of new rows."""
     shape = k.shape
@@ -630,7 +637,7 @@ def cache_read(cache, table, lens, S, dtype=None, out=None, stream=None):
     handle = _handle(cache.device, stream)
     if out is None:
         k = _new(stream, shape, dtype, cache.device)
-        v = _new(stream, shape, dtype, cache.device)
+        v = _new_like(stream, k)
     else:
         k, v = out
         _check_out(k, shape, dtype, cache.device, "out[0]")
@@ -722,7 +729,7 @@ def attention_cache(q, cache, table, lens, counts=None, causal: bool = True,
     need = _need(attn_fwd_cache_workspace_size, B, H, cache.H_kv, Sq, cache.d, code, n_select)
     wp, wn, held = _workspace(workspace, need, cache, stream, handle)
     dev = cache.device
-    out = _new(stream, q.shape, q.dtype if out_dtype is None else out_dtype, dev)
+    out = _new_like(stream, q) if out_dtype is None else _new(stream, q.shape, out_dtype, dev)
     lse = _new(stream, (B, H, Sq), _torch.float32, dev)
     _call_on(cache.device, load_library().attn_fwd_cache, cache.c, q.data_ptr(), out.data_ptr(),
              lse.data_ptr(), t, width, p, n, listed, n_select, B, H, Sq, 1 if causal else 0,
