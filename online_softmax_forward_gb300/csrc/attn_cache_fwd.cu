@@ -76,6 +76,11 @@ constexpr int kRing = 24 * 1024;  // shared memory of each warp's tiles, later o
 // tokens 10.6, 9.6, 9.6, 9.6, 9.6; selection and attention over 96 pages of 32 for 16 units
 // 34.2, 34.2, 34.2, 42.2, 42.1
 constexpr int kSwitch = 8;
+// CTAs to a unit, on average, up to which the second kernel takes a row per warp.  A row per warp
+// and a row per CTA: five drafts (20 rows) of 32 sequences of 2000 to 4096 tokens, 8 kv heads,
+// 48.2 and 50.9 us; 64 ragged sequences 102.7 and 103.6; 4 of 32k (about five CTAs a unit) 42.9 and 42.0; one
+// of 32k and one kv head 44.1 and 13.4
+constexpr int kFewShares = 3;
 
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
     uint4 u;
@@ -765,6 +770,40 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) 
     }
 }
 
+// The same with a row per warp, for units that few CTAs share.
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) cache_merge_rows_kernel(const FwdArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 d0 = a.tail[blockIdx.x];
+    if (!d0.x) return;
+    const Unit u = unit_at(a, d0.z, d0.w);
+    const int lane = threadIdx.x & 31, r = blockIdx.y * kWarps + (threadIdx.x >> 5);
+    size_t row;
+    if (r >= R || !out_row<R>(a, u, r, row)) return;
+    const int n = d0.y - (int)blockIdx.x + 1;
+    if (!in_bounds(n <= kCacheMaxCtas, a.status)) return;
+    auto slot = [&](int p) { return 2 * (int64_t)(blockIdx.x + p) + (p == 0 ? 1 : 0); };
+    float M = -INFINITY;
+    for (int p = lane; p < n; p += 32) M = fmaxf(M, a.pl[slot(p) * R + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float top = M == -INFINITY ? 0.f : M;
+    constexpr int C = D / 32;
+    float L = 0.f, acc[C] = {};
+#pragma unroll 4
+    for (int p = 0; p < n; ++p) {
+        const float wt = ex2(a.pl[slot(p) * R + r] - top);
+        const float *src = a.po + (slot(p) * R + r) * D + lane;
+        L += wt;
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = fmaf(wt, src[32 * c], acc[c]);
+    }
+    const float inv = L == 0.f ? 0.f : ratio(1.f, L);
+#pragma unroll
+    for (int c = 0; c < C; ++c) store_o(a, row * D + lane + 32 * c, acc[c] * inv);
+    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (top + log2f(L)) * kLn2;
+}
+
 template <int D, int FMT, int NB, int FINE, int KT>
 int launch_fwd_t(const FwdArgs &a, unsigned grid, cudaStream_t stream) {
     constexpr int R = NB * 8;
@@ -776,7 +815,9 @@ int launch_fwd_t(const FwdArgs &a, unsigned grid, cudaStream_t stream) {
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
     if (a.one_each) return ATTN_OK;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, (unsigned)(a.rows < R ? a.rows : R));
+    const int rows = a.rows < R ? a.rows : R;
+    const bool by_warp = (int64_t)a.B * a.units * kFewShares >= grid;
+    cfg.gridDim = dim3(grid, by_warp ? (unsigned)(rows + kWarps - 1) / kWarps : (unsigned)rows);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -784,7 +825,7 @@ int launch_fwd_t(const FwdArgs &a, unsigned grid, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, R>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, by_warp ? cache_merge_rows_kernel<D, R> : cache_merge_kernel<D, R>, a);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
