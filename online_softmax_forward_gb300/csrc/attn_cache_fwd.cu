@@ -35,7 +35,7 @@
 // Softmax.  The sums l and o are kept relative to a reference `top` of the
 // scores and, o, to a reference 2^11 / rv of the page scales, so the weight that
 // enters the second product is p * v_scale * rv.  Both references move only when
-// a step of 16 keys would pass fp16's range or a weight 2^4: one vote a step, no
+// a step of 32 keys (a page of 16) would pass fp16's range or a weight 2^4: one vote, no
 // maximum across lanes and no rescaling in the others.
 //
 // Loads.  Each warp copies its own tiles into a ring of shared memory slots with
@@ -72,14 +72,14 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRing = 24 * 1024;  // shared memory of each warp's tiles, later of its states
 // Tiles that a second unit and a second kernel cost a warp.  With 2, 5, 8, 12, 16 in us: five
-// drafts of 16 sequences of up to 4096 tokens 35.2, 35.2, 32.9, 32.8, 30.1; one sequence of 1000
+// drafts of 16 sequences of up to 4096 tokens 33.5, 33.5, 31.9, 32.0, 29.8; one sequence of 1000
 // tokens 10.6, 9.6, 9.6, 9.6, 9.6; selection and attention over 96 pages of 32 for 16 units
-// 34.2, 34.2, 34.2, 42.2, 42.1
+// 33.6, 33.4, 33.4, 40.9, 40.9
 constexpr int kSwitch = 8;
 // CTAs to a unit, on average, up to which the second kernel takes a row per warp.  A row per warp
 // and a row per CTA: five drafts (20 rows) of 32 sequences of 2000 to 4096 tokens, 8 kv heads,
-// 48.2 and 50.9 us; 64 ragged sequences 102.7 and 103.6; 4 of 32k (about five CTAs a unit) 42.9 and 42.0; one
-// of 32k and one kv head 44.1 and 13.4
+// 48.2 and 50.9 us; 64 ragged sequences 102.7 and 103.6; 4 of 32k (about five CTAs a unit) 42.9
+// and 42.0; one of 32k and one kv head 44.1 and 13.4
 constexpr int kFewShares = 3;
 
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
