@@ -25,7 +25,6 @@
 namespace attn {
 namespace {
 
-constexpr int kAppendThreads = 256;
 
 struct AppendArgs {
     const void *x[2];   // new keys, values [B][Hkv][S][d]
@@ -38,25 +37,34 @@ struct AppendArgs {
     int *status;
 };
 
+// Threads of a CTA, by the rows of the largest page that it takes: as many rows a
+// thread for pages of 16, 32 and 64 (with 256 threads for all, two 8k prompts of 32
+// heads take 142 us in pages of 16, so 56; 80 and 53 in pages of 32).
+template <int MOST>
+constexpr int kAppendThreads = MOST < 64 ? MOST * 4 : 256;
+
 // CTAs of an SM.  A CTA is a chain of waits (positions, rows, the block's maximum),
 // which others hide: as many as leave each thread the registers for its rows.  Two
 // 8k prompts of 32 heads, d = 128: bf16 52 us with eight of 32 registers (five: 71,
 // before the instructions were fewer); fp32 83 us with four (five spill: 92, three:
 // 112); fp32 with pages of 128 85 us with two, 94 with three.
 template <int D, int DT, int MOST>
-constexpr int kAppendCtas = DT != 0 ? (MOST == 128 ? 4 : 8) : D == 128 ? (MOST == 128 ? 2 : 4) : (MOST == 128 ? 4 : 6);
+constexpr int kAppendCtas = (DT != 0 ? (MOST == 128 ? 4 : 8) : D == 128 ? (MOST == 128 ? 2 : 4) : (MOST == 128 ? 4 : 6)) *
+                            (256 / kAppendThreads<MOST>);
 
 // One CTA per (touched page of a sequence, kv head, keys or values).
-// MOST: rows of the largest page that it takes, 64 or 128 (registers hold them).
+// MOST: rows of the page, which registers hold.
 // Bound by memory: 95 % of the copy rate in the case above.  It is also near the
 // issue rate, so a page is found without divisions, and keys' ranges and values'
 // magnitudes are kept as packed pairs of 16 bits until a warp's rows are joined.
 template <int D, int FMT, int DT, int MOST>
-__global__ void __launch_bounds__(kAppendThreads, (kAppendCtas<D, DT, MOST>)) cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads<MOST>, (kAppendCtas<D, DT, MOST>)) cache_append_kernel(const AppendArgs a) {
     constexpr int G = D / 8;               // 8-channel groups of a row: one per thread
-    constexpr int RL = kAppendThreads / G; // rows at a time
+    constexpr int T = kAppendThreads<MOST>;
+    constexpr int RL = T / G;              // rows at a time
     constexpr int N = MOST / RL;
-    constexpr int kW = kAppendThreads / 32;
+    constexpr int kW = T / 32;
+    static_assert(T >= 2 * (D / 4), "the bounds' threads");
     using Range = codec::Range8<DT>;
     using Edge = typename std::conditional<DT == 0, float, uint16_t>::type;
     __shared__ uint32_t red[kW];
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(kAppendThreads, (kAppendCtas<D, DT, MOST>)) ca
     const bool grew = r0 > 0 && !(now == before);  // also when the block turned NaN
     const float ratio = now > 0.f ? before * inv : 0.f;
     if (grew) {  // the older rows under the larger scale
-        for (int i = threadIdx.x; i < r0 * (D / 8); i += kAppendThreads) {
+        for (int i = threadIdx.x; i < r0 * (D / 8); i += T) {
             uint2 *p = reinterpret_cast<uint2 *>(codes) + i;
             uint2 c = *p;
             float f[8];
@@ -212,69 +220,79 @@ struct ReadArgs {
     const float *scale[2];
     void *out[2];  // [B][Hkv][S][d]
     const int32_t *table, *lens;
-    int B, S, Hkv, page, page_shift, n_pages, max_pages, tiles;
+    int B, S, Hkv, page, page_shift, tile_shift, n_pages, max_pages, tiles;
     FastDiv by_heads, by_tiles;
     int *status;
 };
 
 constexpr int kReadThreads = 256;
 
-// One CTA per (page of a sequence, kv head, keys or values): 16 codes per
-// thread and step, 16-byte loads and stores.  Bound by memory: four contexts of 32k
-// tokens, 8 kv heads, d = 128, to bf16 122 us, 97 % of the copy rate.
+// One CTA per (tile of a sequence, kv head, keys or values), a tile being 128 rows, or
+// fewer, but a page at least, where that leaves SMs without work (a few short
+// sequences: 4.3 us a page each, 6.5 us in tiles of 128).  16 codes a thread and step,
+// 16-byte loads and stores; 4 codes for fp32, whose stores then lie side by side.
+// Bound by memory: four contexts of 32k tokens, 8 kv heads, d = 128, to bf16 122 us,
+// 97 % of the copy rate, with pages of 16 123 us (194 with a page to a CTA).
 template <int D, int FMT, int DT>
 __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadArgs a) {
-    constexpr int G = D / 16;
+    constexpr int E = DT == 0 ? 4 : 16;  // codes of a step
+    constexpr int G = D / E;
+    __shared__ int64_t s_block[8];  // (page, kv head) blocks of the tile, -1: rows read as zero
+    __shared__ float s_scale[8];
     const int which = blockIdx.x & 1;
     const uint32_t block_of = (blockIdx.x >> 1) / a.by_tiles;
-    const int lp = (int)((blockIdx.x >> 1) - block_of * a.tiles);
+    const int tile = (int)((blockIdx.x >> 1) - block_of * a.tiles);
     const int b = (int)(block_of / a.by_heads);
     const int hk = (int)(block_of - (uint32_t)b * a.Hkv);
     const int len0 = a.lens[b];
     const int len = clamp_len(len0, a.max_pages, a.page);
     if (len != len0 && threadIdx.x == 0) atomicOr(a.status, kStatusTable);
-    const int64_t first = (int64_t)lp << a.page_shift;
-    const int rows = a.S - first < a.page ? (int)(a.S - first) : a.page;
-    int held = (int64_t)len - first < rows ? (int)((int64_t)len - first) : rows;
-    if (held < 0) held = 0;
-    const uint8_t *codes = nullptr;
-    float s = 0.f;
-    if (held > 0) {
-        const int phys = a.table[(int64_t)b * a.max_pages + lp];
-        if (phys < 0 || phys >= a.n_pages) {  // rows without a page read as zero, reported
-            if (threadIdx.x == 0) atomicOr(a.status, kStatusTable);
-            held = 0;
-        } else {
-            const int64_t ph = (int64_t)phys * a.Hkv + hk;
-            codes = (which ? a.codes[1] : a.codes[0]) + (ph << a.page_shift) * D;
-            s = (which ? a.scale[1] : a.scale[0])[ph];
+    const int64_t first = (int64_t)tile << a.tile_shift;
+    const int rows = a.S - first < 1 << a.tile_shift ? (int)(a.S - first) : 1 << a.tile_shift;
+    const int held = (int)max((int64_t)0, min((int64_t)rows, (int64_t)len - first));
+    if (threadIdx.x < 1u << (a.tile_shift - a.page_shift)) {
+        int64_t block = -1;
+        const int64_t lp = (first >> a.page_shift) + threadIdx.x;
+        if (((int)threadIdx.x << a.page_shift) < held) {
+            const int phys = a.table[(int64_t)b * a.max_pages + lp];
+            if (phys < 0 || phys >= a.n_pages) atomicOr(a.status, kStatusTable);  // read as zero, reported
+            else block = (int64_t)phys * a.Hkv + hk;
         }
+        s_block[threadIdx.x] = block;
+        s_scale[threadIdx.x] = block < 0 ? 0.f : (which ? a.scale[1] : a.scale[0])[block];
     }
+    __syncthreads();
+    const uint8_t *codes = which ? a.codes[1] : a.codes[0];
     const size_t dst = (((size_t)b * a.Hkv + hk) * a.S + first) * D;
     void *out = which ? a.out[1] : a.out[0];
     for (int i = threadIdx.x; i < rows * G; i += kReadThreads) {
-        const int r = i / G;
-        float f[16];
-        if (r < held) {
-            const uint4 c = *reinterpret_cast<const uint4 *>(codes + (size_t)i * 16);
-            codec::decode4<FMT>(c.x, f);
-            codec::decode4<FMT>(c.y, f + 4);
-            codec::decode4<FMT>(c.z, f + 8);
-            codec::decode4<FMT>(c.w, f + 12);
+        const int r = i / G, in_page = r & (a.page - 1);
+        const int64_t block = s_block[r >> a.page_shift];
+        float f[E];
+        if (r < held && block >= 0) {
+            const float s = s_scale[r >> a.page_shift];
+            const uint8_t *c = codes + ((block << a.page_shift) + in_page) * D + i % G * E;
+            if constexpr (DT == 0) {
+                codec::decode4<FMT>(*reinterpret_cast<const uint32_t *>(c), f);
+            } else {
+                const uint4 w = *reinterpret_cast<const uint4 *>(c);
+                codec::decode4<FMT>(w.x, f);
+                codec::decode4<FMT>(w.y, f + 4);
+                codec::decode4<FMT>(w.z, f + 8);
+                codec::decode4<FMT>(w.w, f + 12);
+            }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] *= s;
+            for (int e = 0; e < E; ++e) f[e] *= s;
         } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] = 0.f;
+            for (int e = 0; e < E; ++e) f[e] = 0.f;
         }
-        const size_t at = dst + (size_t)i * 16;
-        if (!in_bounds(at + 16 <= (size_t)a.B * a.Hkv * a.S * D, a.status)) continue;
+        const size_t at = dst + (size_t)i * E;
+        if (!in_bounds(at + E <= (size_t)a.B * a.Hkv * a.S * D, a.status)) continue;
         if constexpr (DT == 0) {
-            float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + at);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] = codec::clamped(f[e], 3.402823466e38f);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+            for (int e = 0; e < E; ++e) f[e] = codec::clamped(f[e], 3.402823466e38f);
+            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + at) = make_float4(f[0], f[1], f[2], f[3]);
         } else {
             uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + at);
 #pragma unroll
@@ -307,8 +325,10 @@ int dispatch(int d, int format, int dt, A... args) {
 template <int D, int FMT, int DT>
 struct RunAppend {
     static int run(const AppendArgs *a, unsigned grid, cudaStream_t s) {
-        if (a->page <= 64) cache_append_kernel<D, FMT, DT, 64><<<grid, kAppendThreads, 0, s>>>(*a);
-        else cache_append_kernel<D, FMT, DT, 128><<<grid, kAppendThreads, 0, s>>>(*a);
+        if (a->page == 16) cache_append_kernel<D, FMT, DT, 16><<<grid, kAppendThreads<16>, 0, s>>>(*a);
+        else if (a->page == 32) cache_append_kernel<D, FMT, DT, 32><<<grid, kAppendThreads<32>, 0, s>>>(*a);
+        else if (a->page == 64) cache_append_kernel<D, FMT, DT, 64><<<grid, kAppendThreads<64>, 0, s>>>(*a);
+        else cache_append_kernel<D, FMT, DT, 128><<<grid, kAppendThreads<128>, 0, s>>>(*a);
         return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
     }
 };
@@ -337,10 +357,15 @@ int launch_cache_append(const attn_cache &c, const void *k, const void *v, const
 
 int launch_cache_read(const attn_cache &c, const int32_t *table, int max_pages, const int32_t *lens,
                       void *k, void *v, int B, int S, int dtype, cudaStream_t stream) {
-    const int64_t tiles = ((int64_t)S + c.page - 1) / c.page;
+    const int sms = device_sm_count();
+    if (sms <= 0) return ATTN_ERR_CUDA;
+    int shift = 7;
+    auto tiles_of = [&](int sh) { return ((int64_t)S + (1 << sh) - 1) >> sh; };
+    while (shift > log2_of(c.page) && (int64_t)B * c.H_kv * tiles_of(shift) * 2 < 8 * (int64_t)sms) --shift;
+    const int64_t tiles = tiles_of(shift);
     const int64_t grid = (int64_t)B * c.H_kv * tiles * 2;
     ReadArgs a = {{(const uint8_t *)c.k, (const uint8_t *)c.v}, {c.k_scale, c.v_scale}, {k, v},
-                  table, lens, B, S, c.H_kv, c.page, log2_of(c.page), c.n_pages, max_pages, (int)tiles,
+                  table, lens, B, S, c.H_kv, c.page, log2_of(c.page), shift, c.n_pages, max_pages, (int)tiles,
                   fast_div((uint32_t)c.H_kv), fast_div((uint32_t)tiles), status_word_device_ptr()};
     if (!a.status) return ATTN_ERR_CUDA;
     return dispatch<RunRead>(c.d, c.format, dtype, (const ReadArgs *)&a, (unsigned)grid, stream);
