@@ -37,11 +37,11 @@ struct AppendArgs {
     int *status;
 };
 
-// Threads of a CTA, by the rows of the largest page that it takes: as many rows a
-// thread for pages of 16, 32 and 64 (with 256 threads for all, two 8k prompts of 32
-// heads take 142 us in pages of 16, so 56; 80 and 53 in pages of 32).
-template <int MOST>
-constexpr int kAppendThreads = MOST < 64 ? MOST * 4 : 256;
+// Threads of a CTA: four rows each for pages up to 64.  With 256 threads for all, two
+// 8k prompts of 32 heads take 142 us in pages of 16 (so 56) and 80 in pages of 32 (53),
+// with d = 64 and int8 40 in pages of 64 (29).
+template <int D, int MOST>
+constexpr int kAppendThreads = MOST <= 64 ? MOST * D / 32 : 256;
 
 // CTAs of an SM.  A CTA is a chain of waits (positions, rows, the block's maximum),
 // which others hide: as many as leave each thread the registers for its rows.  Two
@@ -49,8 +49,11 @@ constexpr int kAppendThreads = MOST < 64 ? MOST * 4 : 256;
 // before the instructions were fewer); fp32 83 us with four (five spill: 92, three:
 // 112); fp32 with pages of 128 85 us with two, 94 with three.
 template <int D, int DT, int MOST>
-constexpr int kAppendCtas = (DT != 0 ? (MOST == 128 ? 4 : 8) : D == 128 ? (MOST == 128 ? 2 : 4) : (MOST == 128 ? 4 : 6)) *
-                            (256 / kAppendThreads<MOST>);
+constexpr int kAppendCtasOf256 = DT != 0 ? (MOST == 128 ? 4 : 8) : D == 128 ? (MOST == 128 ? 2 : 4) : 4;
+template <int D, int DT, int MOST>
+constexpr int kAppendCtas = kAppendCtasOf256<D, DT, MOST> * (256 / kAppendThreads<D, MOST>) > 32
+                                ? 32  // of an SM at most
+                                : kAppendCtasOf256<D, DT, MOST> * (256 / kAppendThreads<D, MOST>);
 
 // One CTA per (touched page of a sequence, kv head, keys or values).
 // MOST: rows of the page, which registers hold.
@@ -58,9 +61,9 @@ constexpr int kAppendCtas = (DT != 0 ? (MOST == 128 ? 4 : 8) : D == 128 ? (MOST 
 // issue rate, so a page is found without divisions, and keys' ranges and values'
 // magnitudes are kept as packed pairs of 16 bits until a warp's rows are joined.
 template <int D, int FMT, int DT, int MOST>
-__global__ void __launch_bounds__(kAppendThreads<MOST>, (kAppendCtas<D, DT, MOST>)) cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__((kAppendThreads<D, MOST>), (kAppendCtas<D, DT, MOST>)) cache_append_kernel(const AppendArgs a) {
     constexpr int G = D / 8;               // 8-channel groups of a row: one per thread
-    constexpr int T = kAppendThreads<MOST>;
+    constexpr int T = kAppendThreads<D, MOST>;
     constexpr int RL = T / G;              // rows at a time
     constexpr int N = MOST / RL;
     constexpr int kW = T / 32;
@@ -325,10 +328,10 @@ int dispatch(int d, int format, int dt, A... args) {
 template <int D, int FMT, int DT>
 struct RunAppend {
     static int run(const AppendArgs *a, unsigned grid, cudaStream_t s) {
-        if (a->page == 16) cache_append_kernel<D, FMT, DT, 16><<<grid, kAppendThreads<16>, 0, s>>>(*a);
-        else if (a->page == 32) cache_append_kernel<D, FMT, DT, 32><<<grid, kAppendThreads<32>, 0, s>>>(*a);
-        else if (a->page == 64) cache_append_kernel<D, FMT, DT, 64><<<grid, kAppendThreads<64>, 0, s>>>(*a);
-        else cache_append_kernel<D, FMT, DT, 128><<<grid, kAppendThreads<128>, 0, s>>>(*a);
+        if (a->page == 16) cache_append_kernel<D, FMT, DT, 16><<<grid, kAppendThreads<D, 16>, 0, s>>>(*a);
+        else if (a->page == 32) cache_append_kernel<D, FMT, DT, 32><<<grid, kAppendThreads<D, 32>, 0, s>>>(*a);
+        else if (a->page == 64) cache_append_kernel<D, FMT, DT, 64><<<grid, kAppendThreads<D, 64>, 0, s>>>(*a);
+        else cache_append_kernel<D, FMT, DT, 128><<<grid, kAppendThreads<D, 128>, 0, s>>>(*a);
         return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
     }
 };
