@@ -332,7 +332,8 @@ typedef struct attn_cache {
  * older codes are rounded again under it.  pos[b] may lie before tokens
  * written earlier (they are overwritten; scale and bounds of a page that is
  * continued keep covering them).  Rows of a page behind the last new token are
- * left as they were.  No page may be written for two sequences, or for one
+ * left as they were.  A sequence with a count of 0 touches no page, and its
+ * table row is not read.  No page may be written for two sequences, or for one
  * twice, in one call (its contents are then undefined).  The cache's arrays
  * must not overlap.  One kernel.
  */

@@ -83,6 +83,8 @@ __global__ void __launch_bounds__((kAppendThreads<D, MOST>), (kAppendCtas<D, DT,
         if (threadIdx.x == 0) atomicOr(a.status, kStatusTable);
         return;
     }
+    // Without rows the page at `pos` is not looked at either: it may be another's by now.
+    if (cnt == 0) return;
     const int64_t end = (int64_t)pos + cnt;
     const int64_t lp = (pos >> a.page_shift) + (int64_t)tp;  // logical page
     const int64_t first = lp << a.page_shift;                // its first position
