@@ -484,11 +484,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                         most.x = fmaxf(most.x, p[nb][e >> 1][e & 1].x);
                         most.y = fmaxf(most.y, p[nb][e >> 1][e & 1].y);
                     }
-                    far = far || fmaxf(most.x, most.y) > 16.f || fmaxf(most.x * c[nb].x, most.y * c[nb].y) > 32768.f;
+                    // not <=: where c has overflowed beside weights of 0 the product is a NaN
+                    far = far || fmaxf(most.x, most.y) > 16.f ||
+                          !(most.x * c[nb].x <= 32768.f && most.y * c[nb].y <= 32768.f);
                 }
                 if (__any_sync(0xffffffffu, far)) {
                     // new references: the scores' maximum, and the page scale unless what o
-                    // holds is larger by now
+                    // holds is larger by now.  Returned: what o is to be multiplied by
                     auto moved = [&](float f, float sv, int seen, const float (&x)[2 * MT], float &top, float &rv,
                                      float &l, float &c) {
                         float mx = -INFINITY;
@@ -500,12 +502,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                         const float nt = fmaxf(top, mx);
                         const float alpha = ex2(top - nt);  // 0 from kUnset
                         const float was = ratio(alpha * 2048.f, rv);
-                        const float nv = mx == -INFINITY ? rv : ratio(2048.f, fmaxf(fmaxf(was, sv), 0x1p-100f));
-                        const float to = alpha * ratio(nv, rv);
+                        // a page whose weights are all 0 by now says nothing of the reference, and its
+                        // share of o is 0 (or its scale's NaN)
+                        const bool weighs = mx - nt >= -126.f;
+                        const float nv = mx == -INFINITY ? rv : ratio(2048.f, fmaxf(fmaxf(was, weighs ? sv : 0.f), 0x1p-100f));
+                        const float to = alpha == 0.f ? 0.f : alpha * ratio(nv, rv);
                         l *= alpha;
                         top = nt;
                         rv = nv;
-                        c = sv * nv;
+                        c = weighs || sv != sv ? sv * nv : 0.f;
                         return to;
                     };
 #pragma unroll

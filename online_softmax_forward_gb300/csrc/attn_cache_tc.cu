@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             int qi, h;
             const bool real = row_of<R>(a, p.u, r, qi, h);
             const bool idle = !__any_sync(0xffffffffu, real);  // no row of this warp is one
-            // rows past the block's see everything, so that they never ask for a mask
-            const int lim = real ? visible_keys(p.len, p.cnt, qi, a.causal) : 0x7fffffff;
+            // rows past the block's see every token, so that only the last tile asks for a mask
+            const int lim = real ? visible_keys(p.len, p.cnt, qi, a.causal) : p.len;
             const size_t at = real ? (((size_t)p.u.b * a.Hkv * a.G + h) * a.Sq + qi) * D : 0;
             float cq = 0.f;
             if (p.live > 0) {
@@ -569,10 +569,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                         ptx::tmem_wait_ld();
                         reg_fence(s0);
                         reg_fence(s1);
-                        float mx, scale;
-                        auto largest = [&] {  // visible score, and the pages' largest scale
-                            mx = -INFINITY;
-                            scale = 0.f;
+                        // New references: the largest visible score, and the pages' scale unless what
+                        // O holds is larger by now.  A page whose weights are all 0 by now says
+                        // nothing of the second, and its share of O is 0 (or its scale's NaN).
+                        // Returned: what O is to be multiplied by
+                        auto refer = [&] {
+                            float mx = -INFINITY, mg[4];
 #pragma unroll
                             for (int g = 0; g < 4; ++g) {
                                 const uint32_t *s = (g < 2 ? s0 : s1) + (g & 1) * 16;
@@ -586,35 +588,41 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                                     for (int e = 0; e < 16; ++e)
                                         if (e < n[g]) m = fmaxf(m, __uint_as_float(s[e]));
                                 }
-                                if (m != -INFINITY) mx = fmaxf(mx, m * f[g]);
-                                scale = fmaxf(scale, sv[g]);
+                                mg[g] = m == -INFINITY ? m : m * f[g];
+                                mx = fmaxf(mx, mg[g]);
                             }
+                            const float nt = fmaxf(top, mx);
+                            const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
+                            float held = alpha * kBase / rv;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                if (mg[g] - nt >= -126.f) held = fmaxf(held, sv[g]);
+                                else if (sv[g] == sv[g]) sv[g] = 0.f;
+                            }
+                            const float nv = mx == -INFINITY ? rv : kBase / fmaxf(held, 0x1p-95f);
+                            const float to = alpha == 0.f ? 0.f : alpha * (nv / rv);
+                            l *= alpha;
+                            top = nt;
+                            rv = nv;
+                            return to;
                         };
-                        if (j < 2 && half == 0) {  // the unit's first references
-                            largest();
-                            top = fmaxf(top, mx);
-                            if (mx != -INFINITY) rv = kBase / fmaxf(scale, 0x1p-95f);
-                        }
+                        if (j < 2 && half == 0) refer();  // the unit's first references
                         weights();
+                        float c[4] = {sv[0] * rv, sv[1] * rv, sv[2] * rv, sv[3] * rv};
                         const float most = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
-                        const float heavy = fmaxf(fmaxf(all[0] * sv[0], all[1] * sv[1]), fmaxf(all[2] * sv[2], all[3] * sv[3]));
-                        if (__any_sync(0xffffffffu, most > kLargest || heavy * rv > kLargest * kBase)) {
-                            // new references: the scores' maximum, and the pages' scale unless what
-                            // O holds is larger by now
+                        constexpr float kHeavy = kLargest * kBase;
+                        // not <=: where c has overflowed beside weights of 0 the product is a NaN
+                        const bool fits = all[0] * c[0] <= kHeavy && all[1] * c[1] <= kHeavy &&
+                                          all[2] * c[2] <= kHeavy && all[3] * c[3] <= kHeavy;
+                        if (__any_sync(0xffffffffu, most > kLargest || !fits)) {
                             ptx::tmem_ld32(tH, s0);
                             ptx::tmem_ld32(tH + 32, s1);
                             ptx::tmem_wait_ld();
                             reg_fence(s0);
                             reg_fence(s1);
-                            largest();
-                            const float nt = fmaxf(top, mx);
-                            const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
-                            const float was = alpha * kBase / rv;
-                            const float nv = mx == -INFINITY ? rv : kBase / fmaxf(fmaxf(was, scale), 0x1p-95f);
-                            const float to = alpha * (nv / rv);
-                            l *= alpha;
-                            top = nt;
-                            rv = nv;
+                            const float to = refer();
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) c[g] = sv[g] * rv;
                             weights();
                             // O_t holds the tiles before and this one's first half
                             if (j > 1 || half == 1) {
@@ -639,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
                             const uint32_t *s = (g < 2 ? s0 : s1) + (g & 1) * 16;
-                            const float2 c2 = make_float2(sv[g] * rv, sv[g] * rv);
+                            const float2 c2 = make_float2(c[g], c[g]);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const float2 x = __fmul2_rn(

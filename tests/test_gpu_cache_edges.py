@@ -1,15 +1,85 @@
-"""The paged 8-bit cache at the edges of what a call may be given: sequences that take no part."""
+"""The paged 8-bit cache where a wrong number hides behind a large one: rows bounded by what they
+themselves weigh, page scales that span the type's range, sequences that take no part in a call,
+selections that many pages tie in.
+
+Attention is compared row by row and channel by channel.  With w_j the softmax weights of a row:
+
+  s     a score is off by e_s = 20 * 2^-23 * a, a the largest sum_c |q_c k_c| * scale (as in
+        test_gpu_cache.py), so a weight by 2 e_s of itself (numerator and sum);
+  p     exp2 and the products with the page scale: 2^-21 of a weight; rounded to fp16 for 16-bit
+        outputs: 2^-11 of it, half a step;
+  sums  n / 16 products of 16 keys and a few joins and rescalings one behind the other, 2^-23 of
+        what the sum has reached: (n / 16 + 16) * 2^-23 each for o and for the weights' sum;
+  low   a weight that leaves fp16's normal numbers is rounded to steps of 2^-24, half a step off;
+        one that the row weighs most, by weight times page scale, stands at no less than 2^5 (the
+        128-row kernel's reference; 2^11 in the other): 2^-30 * |code| * max_j w_j v_scale_j a key;
+  out   half a step of the output type (and of fp16's subnormals, 2^-25).
+"""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import cache_ref as ref
 import online_softmax_forward_gb300 as pkg
-from test_gpu_cache import check_pool, dev, f64, new_cache, rows, status
+from test_gpu_cache import HALF, check_pool, dev, f64, new_cache, rows, status, tables
 
 pytestmark = pytest.mark.gpu
 
 
+def check_rows(q, c, t, n, Sq, causal=True, scale=None, out_dtype=None):
+    """attention_cache of one sequence of n tokens, H_kv = 1, each row and channel within its own bound."""
+    o, lse = pkg.attention_cache(q.cuda(), c, dev(t), dev([n]), causal=causal, scale=scale, out_dtype=out_dtype)
+    assert status() == pkg.ATTN_OK
+    pool, page, d = ref.snapshot(c), c.page, c.d
+    k, v = (x[0, 0] for x in ref.read(pool, t, [n], n))
+    ids = [t[0][j // page] for j in range(n)]
+    vs = pool["v_scale"][ids, 0]
+    code = np.abs(np.stack([pool["v"][p, 0, j % page] for j, p in enumerate(ids)]))
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    got, glse = f64(o), f64(lse)
+    ep = 2.0 ** -21 + (2.0 ** -11 if o.dtype != torch.float32 else 0.0)
+    sums = 2 * (n / 16 + 16) * 2.0 ** -23
+    tight = 0.0
+    for h in range(q.shape[1]):
+        for i in range(Sq):
+            m = ref.visible(n, Sq, i, causal)
+            x = f64(q[0, h, i])
+            s = k[:m] @ x * scale
+            es = 20 * 2.0 ** -23 * (np.abs(k[:m]) @ np.abs(x) * scale).max()
+            w = np.exp(s - s.max())
+            o_, lse_ = w @ v[:m] / w.sum(), s.max() + math.log(w.sum())
+            own = w @ np.abs(v[:m]) / w.sum()
+            low = 2.0 ** -30 * (w * vs[:m]).max() * code[:m].sum(0) / w.sum()
+            bound = (2 * es + ep + sums) * own + low + HALF[o.dtype] * np.abs(o_) * 1.01
+            bound += 2.0 ** -25 if o.dtype == torch.float16 else 2.0 ** -149
+            err = np.abs(got[0, h, i] - o_)
+            worst = (err / bound).argmax()
+            assert np.all(err <= bound), "head %d query %d channel %d: %r, not %r, bound %.3e" % (
+                h, i, worst, got[0, h, i, worst], o_[worst], bound[worst])
+            assert abs(glse[0, h, i] - lse_) <= es + 2.0 ** -20 + 2.0 ** -22 * abs(lse_)
+            tight = max(tight, np.median(bound / np.maximum(own, 1e-300)))
+    assert tight < 2.0 ** -3  # the bound says something about o
+    return o
+
+
+def one_sequence(k, v, page, fmt, seed=0):
+    """(cache, table) of one sequence of one kv head; k and v [n, d]."""
+    n, d = k.shape
+    pages = -(-n // page)
+    c = new_cache(pages + 2, 1, page, d, fmt, junk=True)
+    t = tables([n], page, pages, pages + 2, seed=seed)
+    pkg.cache_append(c, k[None, None].cuda(), v[None, None].cuda(), dev(t), dev([0]))
+    assert status() == pkg.ATTN_OK
+    return c, t
+
+
+ROWS = [(1, torch.bfloat16), (4, torch.float16), (7, torch.bfloat16), (40, torch.bfloat16),  # 8 to 128 rows
+        (3, torch.float32)]
+
+
+# ------------------------------------------------------------------ sequences that take no part
 @pytest.mark.parametrize("page", [16, 64])
 def test_append_of_no_rows_touches_no_page(page):
     """A sequence with a count of 0 in the middle of a page: its table row may name pages that are
@@ -43,3 +113,41 @@ def test_append_of_no_rows_beside_the_pages_new_owner():
         pkg.cache_append(c, x.cuda(), x.cuda(), dev(t), dev(pos), dev(counts))
         assert status() == pkg.ATTN_OK
         check_pool(c, pool)
+
+
+# ------------------------------------------------------------------ page scales far apart
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Sq,dtype", ROWS)
+def test_a_large_page_of_no_weight_behind_pages_of_zeros(Sq, dtype, fmt):
+    """The first keys that a row weighs have zero values, then come pages of huge ones whose
+    weights underflow, then ordinary ones."""
+    n, d = 700, 64
+    k, v = rows((n, d), 1, torch.float32, 0.05), rows((n, d), 2, torch.float32)
+    k[:, 0] = 0.0
+    v[:448] = 0.0
+    k[448:512, 0] = -200.0
+    v[448:512] *= 1e25
+    c, t = one_sequence(k, v, 16, fmt)
+    q = rows((1, 4, Sq, d), 4, torch.float32, 0.1)
+    q[..., 0] = 8.0
+    check_rows(q.to(dtype), c, t, n, Sq, scale=1.0 / 8)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Sq,dtype", ROWS)
+@pytest.mark.parametrize("wide", [False, True])
+def test_large_values_that_scores_leave_behind_for_zeros(wide, Sq, dtype, fmt):
+    """Huge values first, then a score so much higher that nothing of them is left, on pages of
+    zeros, then ordinary values."""
+    n, d = 900, 64
+    k, v = rows((n, d), 1, torch.float32, 0.05), rows((n, d), 2, torch.float32)
+    k[:, 0] = 200.0
+    head = 64 if not wide else 32
+    for at in range(0, 512, 2 * head):
+        k[at: at + head, 0] = 0.0
+        v[at: at + head] *= 1e30
+        v[at + head: at + 2 * head] = 0.0
+    c, t = one_sequence(k, v, 16, fmt)
+    q = rows((1, 4, Sq, d), 4, torch.float32, 0.1)
+    q[..., 0] = 8.0
+    check_rows(q.to(dtype), c, t, n, Sq, scale=1.0 / 8)
