@@ -33,10 +33,13 @@
 // magnitude in [2^14, 2^15): any fp32 or bf16 exponent then fits fp16.
 //
 // Softmax.  The sums l and o are kept relative to a reference `top` of the
-// scores and, o, to a reference 2^11 / rv of the page scales, so the weight that
+// scores and, o, to a reference 2^11 / rv of weight times page scale, so the weight that
 // enters the second product is p * v_scale * rv.  Both references move only when
 // a step of 32 keys (a page of 16) would pass fp16's range or a weight 2^4: one vote, no
-// maximum across lanes and no rescaling in the others.
+// maximum across lanes and no rescaling in the others.  The second follows what the row
+// weighs most, not the largest page it sees: a page of huge values and no weight would
+// push the other weights under fp16's normal numbers.  What is below 2^-25 of the
+// largest weight times page scale keeps fewer bits, and nothing below 2^-36.
 //
 // Loads.  Each warp copies its own tiles into a ring of shared memory slots with
 // 16-byte cp.async (a slot holds the codes of one tile's keys and values), all
@@ -489,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                           !(most.x * c[nb].x <= 32768.f && most.y * c[nb].y <= 32768.f);
                 }
                 if (__any_sync(0xffffffffu, far)) {
-                    // new references: the scores' maximum, and the page scale unless what o
-                    // holds is larger by now.  Returned: what o is to be multiplied by
+                    // new references: the scores' maximum, and the largest weight times page scale
+                    // unless what o holds is larger by now.  Returned: what o is to be multiplied by
                     auto moved = [&](float f, float sv, int seen, const float (&x)[2 * MT], float &top, float &rv,
                                      float &l, float &c) {
                         float mx = -INFINITY;
@@ -502,15 +505,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                         const float nt = fmaxf(top, mx);
                         const float alpha = ex2(top - nt);  // 0 from kUnset
                         const float was = ratio(alpha * 2048.f, rv);
-                        // a page whose weights are all 0 by now says nothing of the reference, and its
-                        // share of o is 0 (or its scale's NaN)
-                        const bool weighs = mx - nt >= -126.f;
-                        const float nv = mx == -INFINITY ? rv : ratio(2048.f, fmaxf(fmaxf(was, weighs ? sv : 0.f), 0x1p-100f));
+                        // Nothing but what the row weighs moves the reference of o: the page's scale
+                        // times its largest weight.  Weights that are all 0 by now add nothing (but
+                        // their scale's NaN); below 2^-112 the scale counts that much, so that c stays
+                        // finite
+                        const float e = ex2(mx - nt);
+                        const float here = e > 0.f ? sv * fmaxf(e, 0x1p-112f) : 0.f;
+                        const float nv = mx == -INFINITY ? rv : ratio(2048.f, fmaxf(fmaxf(was, here), 0x1p-100f));
                         const float to = alpha == 0.f ? 0.f : alpha * ratio(nv, rv);
                         l *= alpha;
                         top = nt;
                         rv = nv;
-                        c = weighs || sv != sv ? sv * nv : 0.f;
+                        c = e > 0.f || sv != sv ? sv * nv : 0.f;
                         return to;
                     };
 #pragma unroll

@@ -16,10 +16,12 @@
 //   warps 14-15 issue the products of t = 0 and 1, S_t = Q K_j^T and O_t += P_t V_j.
 //
 // The two warpgroups keep states of their own (top, rv, l and O_t, references moved
-// only when 16 weights would pass 2^10 or fp16's range, as in attn_cache_fwd.cu),
-// so that one exponentiates while the other's products run; they are joined when
-// the unit ends.  P in fp16 is rounded by 2^-12, so this kernel serves the 16-bit
-// outputs.  A warp without a real row (few drafts, few heads) only keeps step.
+// only when 16 weights would pass 2^10 or fp16's range, as in attn_cache_fwd.cu), so
+// that one exponentiates while the other's products run; they are joined when the
+// unit ends.  P in fp16 is rounded by 2^-12, so this kernel serves the 16-bit
+// outputs; what is below 2^-19 of a row's largest weight times page scale keeps fewer
+// bits, and nothing below 2^-30.  A warp without a real row (few drafts, few heads)
+// only keeps step.
 //
 // A tile's S, P and products go in halves of 64 keys.  Tensor memory (512 columns)
 // is full with S_0 [0, 128), S_1 [128, 256), O_0 from 256 and O_1 from 256 + D, so
@@ -68,7 +70,7 @@ constexpr uint32_t kTmemCols = 512;
 // per CTA, 64 with equal ranges.
 constexpr int kSwitch = 6;
 constexpr float kLargest = 1024.f;  // of 16 keys' sum of weights; 32 * 1024 fits fp16
-constexpr float kBase = 32.f;       // page scale times rv, at its largest after a move
+constexpr float kBase = 32.f;       // weight times page scale times rv, at its largest after a move
 
 struct Bars {
     uint64_t q_full, q_empty;
@@ -569,9 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                         ptx::tmem_wait_ld();
                         reg_fence(s0);
                         reg_fence(s1);
-                        // New references: the largest visible score, and the pages' scale unless what
-                        // O holds is larger by now.  A page whose weights are all 0 by now says
-                        // nothing of the second, and its share of O is 0 (or its scale's NaN).
+                        // New references: the largest visible score, and the largest weight times page
+                        // scale unless what O holds is larger by now.  A page whose weights are all 0
+                        // by now says nothing of the second, and its share of O is 0 (or its scale's
+                        // NaN); below 2^-112 a weight counts as that much, so that c stays finite.
                         // Returned: what O is to be multiplied by
                         auto refer = [&] {
                             float mx = -INFINITY, mg[4];
@@ -596,7 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                             float held = alpha * kBase / rv;
 #pragma unroll
                             for (int g = 0; g < 4; ++g) {
-                                if (mg[g] - nt >= -126.f) held = fmaxf(held, sv[g]);
+                                const float e = ptx::ex2_approx(mg[g] - nt);
+                                if (e > 0.f) held = fmaxf(held, sv[g] * fmaxf(e, 0x1p-112f));
                                 else if (sv[g] == sv[g]) sv[g] = 0.f;
                             }
                             const float nv = mx == -INFINITY ? rv : kBase / fmaxf(held, 0x1p-95f);

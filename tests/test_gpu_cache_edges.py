@@ -151,3 +151,38 @@ def test_large_values_that_scores_leave_behind_for_zeros(wide, Sq, dtype, fmt):
     q = rows((1, 4, Sq, d), 4, torch.float32, 0.1)
     q[..., 0] = 8.0
     check_rows(q.to(dtype), c, t, n, Sq, scale=1.0 / 8)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Sq,dtype", ROWS)
+@pytest.mark.parametrize("at,far,low", [(0, 34, -19.0), (48, 34, -19.0), (304, 36, -20.0), (300, 20, -8.0)])
+def test_an_outweighed_page_costs_the_others_no_bits(at, far, low, Sq, dtype, fmt):
+    """One page whose scale is 2^far of the others' and whose keys weigh e^low of theirs, large in
+    channel 0 only: the other channels are sums of ordinary values."""
+    n, d = 600, 64
+    k, v = rows((n, d), 1, torch.float32, 0.05), rows((n, d), 2, torch.float32)
+    k[:, 0] = 0.0
+    k[at: at + 16, 0] = low
+    v[at + 3, 0] = 2.0 ** far
+    c, t = one_sequence(k, v, 16, fmt)
+    q = rows((1, 4, Sq, d), 4, torch.float32, 0.1)
+    q[..., 0] = 8.0
+    check_rows(q.to(dtype), c, t, n, Sq, causal=False, scale=1.0 / 8)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Sq,dtype", ROWS)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_moving_references_row_by_row(sign, Sq, dtype, fmt):
+    """Scores that rise (or fall) by 20 every 150 keys while the pages' scales go up and down by
+    many powers of two, among them outweighed pages of 2^25 more."""
+    page, d, n = 16, 64, 900
+    k, v = rows((n, d), 1, torch.float32, 0.05), rows((n, d), 2, torch.float32)
+    k[:, 0] = torch.arange(n) // 150 * 20.0
+    v *= torch.exp2(torch.tensor([0, 9, -12, 3, 14, -6, 1])[torch.arange(n) // 48 % 7])[:, None]
+    v[200:210] *= 2.0 ** 25
+    c, t = one_sequence(k, v, page, fmt, seed=2)
+    q = rows((1, 4, Sq, d), 4, torch.float32, 0.1)
+    q[..., 0] = 8.0
+    for causal in (True, False):
+        check_rows(sign * q.to(dtype), c, t, n, Sq, causal, scale=1.0 / 8)
