@@ -113,7 +113,7 @@ struct Tile {  // one key tile, held by one lane
     float ks, vs;
 };
 
-// Quotients of normal numbers below 2^126, to 2^-22.
+// Quotients of normal numbers, to 2^-22; the divisor is at most 2^126.
 __device__ __forceinline__ float ratio(float a, float b) { return __fdividef(a, b); }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {  // an 8 x 8 tile of 16-bit numbers
     uint32_t y;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             top[nb] = make_float2(kUnset, kUnset);
-            rv[nb] = make_float2(0x1p111f, 0x1p111f);
+            rv[nb] = make_float2(0x1p123f, 0x1p123f);
             l[nb] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int n = 0; n < VT; ++n) acc[nb][n][0] = acc[nb][n][1] = acc[nb][n][2] = acc[nb][n][3] = 0.f;
@@ -504,14 +504,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                         const float nt = fmaxf(top, mx);
                         const float alpha = ex2(top - nt);  // 0 from kUnset
-                        const float was = ratio(alpha * 2048.f, rv);
+                        const float was = ratio(alpha * 128.f, rv);  // a sixteenth, as `here`: finite for any scale
                         // Nothing but what the row weighs moves the reference of o: the page's scale
                         // times its largest weight.  Weights that are all 0 by now add nothing (but
                         // their scale's NaN); below 2^-112 the scale counts that much, so that c stays
                         // finite
                         const float e = ex2(mx - nt);
-                        const float here = e > 0.f ? sv * fmaxf(e, 0x1p-112f) : 0.f;
-                        const float nv = mx == -INFINITY ? rv : ratio(2048.f, fmaxf(fmaxf(was, here), 0x1p-100f));
+                        const float here = e > 0.f ? sv * fmaxf(e * 0x1p-4f, 0x1p-116f) : 0.f;
+                        const float nv = mx == -INFINITY ? rv : ratio(128.f, fmaxf(fmaxf(was, here), 0x1p-116f));
                         const float to = alpha == 0.f ? 0.f : alpha * ratio(nv, rv);
                         l *= alpha;
                         top = nt;
@@ -690,16 +690,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
             for (int o = 1; o < kWarps; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
             M = __shfl_sync(0xffffffffu, M, 0);
             L = __shfl_sync(0xffffffffu, L, 0);
-            float o[D / 32] = {};
+            float o[D / 32] = {};  // of 2^-3 times the weights: a sum that the largest values fit
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, wt, k);
+                const float wk = __shfl_sync(0xffffffffu, wt, k) * 0x1p-3f;
                 if (k >= n) continue;
                 const float *src = s_keep[first + k][k == 0 ? side : 0] + r * D + lane;
 #pragma unroll
                 for (int e = 0; e < D / 32; ++e) o[e] = fmaf(wk, src[32 * e], o[e]);
             }
-            const float inv = L == 0.f ? 0.f : ratio(1.f, L);
+            const float inv = L == 0.f ? 0.f : ratio(8.f, L);
             const float lse2 = L == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(L);
             if (earlier || open) {
                 if (!in_bounds(slot < 2 * (int)gridDim.x, a.status)) continue;
@@ -721,6 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
     }
     if (!over && threadIdx.x == 0) a.tail[blockIdx.x] = make_int4(0, 0, 0, 0);
 }
+
+static_assert(kCacheMaxCtas * kFits <= 1.f, "a sum of states that the largest values fit");
 
 // Joins the states of the unit that runs over the end of CTA blockIdx.x's
 // range: the CTA's own and those of the CTAs up to the one that holds the
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) 
     float acc[C] = {};
 #pragma unroll 4
     for (int p = warp; p < n; p += kWarps) {
-        const float wt = ex2(wts[p] - top);
+        const float wt = ex2(wts[p] - top) * kFits;
         const float *src = a.po + (slot(p) * R + r) * D + lane;
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[c] = fmaf(wt, src[32 * c], acc[c]);
@@ -772,7 +774,7 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) 
     for (int c = 0; c < C; ++c) part[warp][lane + 32 * c] = acc[c];
     __syncthreads();
     if (threadIdx.x < D) {
-        const float inv = L == 0.f ? 0.f : ratio(1.f, L);
+        const float inv = L == 0.f ? 0.f : ratio(1.f / kFits, L);
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) sum += part[k][threadIdx.x];
@@ -807,9 +809,9 @@ __global__ void __launch_bounds__(kThreads) cache_merge_rows_kernel(const FwdArg
         const float *src = a.po + (slot(p) * R + r) * D + lane;
         L += wt;
 #pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] = fmaf(wt, src[32 * c], acc[c]);
+        for (int c = 0; c < C; ++c) acc[c] = fmaf(wt * kFits, src[32 * c], acc[c]);
     }
-    const float inv = L == 0.f ? 0.f : ratio(1.f, L);
+    const float inv = L == 0.f ? 0.f : ratio(1.f / kFits, L);
 #pragma unroll
     for (int c = 0; c < C; ++c) store_o(a, row * D + lane + 32 * c, acc[c] * inv);
     if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (top + log2f(L)) * kLn2;

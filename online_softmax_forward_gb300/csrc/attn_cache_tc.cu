@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                 ++qn;
                 cq = a.sl2 * back[r];
             }
-            float top = kUnset, rv = 0x1p100f, l = 0.f;
+            float top = kUnset, rv = 0x1p123f, l = 0.f;
             for (int j = t; j < p.live; j += 2) {
                 const uint32_t ring = (slot + j) % kScaleRing, lap = (slot + j) / kScaleRing;
                 ok = wait_all(bar(bars->sc_full[ring]), lap & 1);
@@ -596,14 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                             }
                             const float nt = fmaxf(top, mx);
                             const float alpha = ptx::ex2_approx(top - nt);  // 0 from kUnset
-                            float held = alpha * kBase / rv;
+                            float held = fminf(alpha * kBase / rv, 3.402823466e38f);
 #pragma unroll
                             for (int g = 0; g < 4; ++g) {
                                 const float e = ptx::ex2_approx(mg[g] - nt);
                                 if (e > 0.f) held = fmaxf(held, sv[g] * fmaxf(e, 0x1p-112f));
                                 else if (sv[g] == sv[g]) sv[g] = 0.f;
                             }
-                            const float nv = mx == -INFINITY ? rv : kBase / fmaxf(held, 0x1p-95f);
+                            const float nv = mx == -INFINITY ? rv : kBase / fmaxf(held, 0x1p-118f);
                             const float to = alpha == 0.f ? 0.f : alpha * (nv / rv);
                             l *= alpha;
                             top = nt;
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                         ptx::tmem_wait_ld();
                         reg_fence(o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * u1 * c1;
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * c1 * u1;
                     }
                     if (has2) {
                         uint32_t o[32];
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                         ptx::tmem_wait_ld();
                         reg_fence(o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(o[e]) * u2 * c2;
+                        for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(o[e]) * c2 * u2;
                     }
                     if (real && whole) {
 #pragma unroll
@@ -778,15 +778,15 @@ __global__ void __launch_bounds__(8 * D / 4) cache_tc_merge_kernel(const FwdArgs
     float L = 0.f, acc[4] = {};
 #pragma unroll 4
     for (int p = 0; p < n; ++p) {
-        const float w = ptx::ex2_approx(a.pl[slot(p) * R + r] - base);
+        const float wt = ptx::ex2_approx(a.pl[slot(p) * R + r] - base), w = wt * kFits;
         const float4 x = reinterpret_cast<const float4 *>(a.po + slot(p) * R * D)[c4 * R + r];
-        L += w;
+        L += wt;
         acc[0] = fmaf(w, x.x, acc[0]);
         acc[1] = fmaf(w, x.y, acc[1]);
         acc[2] = fmaf(w, x.z, acc[2]);
         acc[3] = fmaf(w, x.w, acc[3]);
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = L == 0.f ? 0.f : 1.f / (kFits * L);
 #pragma unroll
     for (int e = 0; e < 4; ++e) store_o(a, row * D + c4 * 4 + e, acc[e] * inv);
     if (a.lse && c4 == 0) a.lse[row] = L == 0.f ? -INFINITY : (base + log2f(L)) * kLn2;

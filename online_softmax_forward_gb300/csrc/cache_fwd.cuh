@@ -185,6 +185,9 @@ __device__ __forceinline__ bool out_row(const FwdArgs &a, const Unit &u, int r, 
     row = ((size_t)u.b * a.Hkv * a.G + h) * a.Sq + i;
     return in_bounds(i < a.Sq && h < a.Hkv * a.G && u.b < a.B, a.status);
 }
+// Factor of the weights that join the states of kCacheMaxCtas CTAs: their sum of the largest
+// values is finite.
+constexpr float kFits = 0x1p-8f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 }  // namespace attn

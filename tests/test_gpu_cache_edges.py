@@ -186,3 +186,25 @@ def test_moving_references_row_by_row(sign, Sq, dtype, fmt):
     q[..., 0] = 8.0
     for causal in (True, False):
         check_rows(sign * q.to(dtype), c, t, n, Sq, causal, scale=1.0 / 8)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Sq,dtype", ROWS)
+@pytest.mark.parametrize("v_scale", [3.3e38, 2.0 ** 127, 2.0 ** 122, 2.0 ** -126])
+def test_any_finite_scale_of_values(v_scale, Sq, dtype, fmt):
+    """A pool filled by hand, codes of one and its neighbours under the largest and the smallest
+    scale."""
+    n, d, page = 200, 64, 16
+    k = rows((n, d), 1, torch.float32, 0.3)
+    v = torch.where(torch.arange(d) % 3 == 0, 1.0, 0.5 if fmt == "e4m3" else 0.0).expand(n, d).contiguous()
+    c, t = one_sequence(k, v, page, fmt)
+    c.v.copy_(torch.where(torch.arange(d) % 3 == 0, 1.0, 0.5 if fmt == "e4m3" else 0.0).to(c.v.dtype).cuda())
+    c.v_scale.fill_(v_scale)
+    q = rows((1, 4, Sq, d), 4, torch.float32).to(dtype)
+    o, _ = pkg.attention_cache(q.cuda(), c, dev(t), dev([n]), out_dtype=torch.float32)
+    assert status() == pkg.ATTN_OK
+    want = f64(c.v[0, 0, 0].float()) * v_scale  # every key has the same value
+    assert np.abs(f64(o) / v_scale - want / v_scale).max() <= 2.0 ** -18
+    if dtype == torch.bfloat16:
+        o, _ = pkg.attention_cache(q.cuda(), c, dev(t), dev([n]))
+        assert np.abs(f64(o) / v_scale - want / v_scale).max() <= 2.0 ** -8 + 2.0 ** -10
