@@ -343,9 +343,11 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     }
     // |error| of a score: 2 QS <= 16 sums of 16 products and 3 of sums, each off by at
     // most 2^-22 of what sum |q| * code has reached, two fp32 products and q's 22
-    // bits: below 2^-18 * sum |q| * largest code * scale
+    // bits: below 2^-18 * sum |q| * largest code * scale, twice that of a difference; where
+    // that is next to nothing, scores lose bits below fp32's normal numbers
     constexpr float kTop = FMT == ATTN_CACHE_E4M3 ? 448.f : 128.f;
-    const float eps = 2.f * 0x1p-18f * kTop * mass * __uint_as_float(top);  // of a difference
+    float eps = (kTop * mass) * (0x1p-17f * __uint_as_float(top));
+    if (eps < 0x1p-100f) eps = 0x1p-100f;
     const float least = unordered(low), per_bin = kBins / (unordered(high) - least);
     // pages whose score may be that of the last place: every one, or those of the
     // n-th score's bin and of the bins within eps of it
@@ -378,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     }
     static_assert(kBins == 4 * kThreads, "four bins a thread");
     int *near = reinterpret_cast<int *>(key + a.max_pages);
-    const bool equal = eps == 0.f;  // q or every scale is 0: all scores are
+    // q or every scale is 0: all scores are (no scale that is not finite among them)
+    const bool equal = top == 0 || (mass == 0.f && top < 0x7f800000u);
     int n_in = 0;
 #pragma unroll 4
     for (int p = t; p < m; p += kThreads) {

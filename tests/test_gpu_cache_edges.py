@@ -208,3 +208,23 @@ def test_any_finite_scale_of_values(v_scale, Sq, dtype, fmt):
     if dtype == torch.bfloat16:
         o, _ = pkg.attention_cache(q.cuda(), c, dev(t), dev([n]))
         assert np.abs(f64(o) / v_scale - want / v_scale).max() <= 2.0 ** -8 + 2.0 ** -10
+
+
+# ------------------------------------------------------------------ selection
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,small", [(torch.float32, 1e-8), (torch.bfloat16, 1e-8), (torch.float32, 1e-4),
+                                         (torch.float32, 1e-30)])
+def test_selection_of_scores_below_normal_numbers(dtype, small, fmt):
+    """Keys at the smallest scale under small queries: fp32 scores are subnormal or 0, the choice
+    is that of their exact values."""
+    n, d, page = 640, 64, 16
+    k = rows((n, d), 1, torch.float32, 2.0 ** -124)
+    c, t = one_sequence(k, k, page, fmt)
+    assert (c.k_scale[torch.from_numpy(t[0]).cuda()] == 2.0 ** -126).all()
+    q = (rows((1, 3, 2, d), 2, torch.float32) * small).to(dtype)
+    for m in (2, 7, 20):
+        pages = pkg.cache_select(q.cuda(), c, dev(t), dev([n]), m)
+        assert status() == pkg.ATTN_OK
+        want = ref.select(f64(q), ref.snapshot(c), t, [n], [2], m, True)
+        assert np.array_equal(pages.cpu().numpy(), want)
+        assert not np.array_equal(want[0, 0, 0, : m - 1], np.arange(m - 1))
