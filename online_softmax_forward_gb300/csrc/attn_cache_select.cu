@@ -20,7 +20,10 @@
 // fp64, where the products of a 16-bit q and an 8-bit code (at most 19 bits) add
 // up exactly unless they span more than 2^27, so the choice does not depend on
 // the order of a sum.  (fp64 for every page would cost more than the reading:
-// this GPU has 1/64 the fp64 rate.)
+// this GPU has 1/64 the fp64 rate.)  Pages marked by a NaN scale score infinity and do not
+// widen the bound.  More than 256 pages near the cut (equal keys, a q that is not finite) are
+// all summed in fp64 and cut by a radix search: 1.6 ms for 4095 pages that tie, 30 us for 4096
+// pages without such ties.
 //
 // Bound: by waits.  With the attention over the choice, 32 of 512 pages for 64 units
 // take 27 us and 96 of 4096 for 16 units 34 us, 12 and 23 us of it here, where the
@@ -65,6 +68,15 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 __device__ __forceinline__ float unordered(uint32_t u) {
     return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u);
+}
+
+// Score of a page whose scale is NaN, above all others whatever q is: it is attended to, so that
+// the NaN shows.  ordered(infinity).
+constexpr uint32_t kMarked = 0xff800000u;
+// The same order for doubles.
+__device__ __forceinline__ uint64_t ordered(double x) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);  // -0 as 0
+    return u >> 63 ? ~u : u | (uint64_t)1 << 63;
 }
 
 // `local` (a shared memory address) in the cluster's first CTA.
@@ -295,14 +307,17 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
                     const int p = base + 8 * j + 2 * t4 + c;
                     if (g == 0 && p < p1 && in_bounds(p < a.max_pages, a.status)) {
                         x *= s;
-                        // what is not finite leaves the decision to fp64; a page outside the
-                        // pool scores lowest
-                        if (!(fabsf(x) <= 3.402823466e38f)) odd = true;
-                        const uint32_t at = first_key + p * 4, y = ordered(x);
-                        if (ok < 0 || ok >= a.n_pages) x = -INFINITY;
-                        else high = max(high, y), low = min(low, y);
-                        if (g0 == 0) st_cluster(at, ordered(x));
-                        else asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(at), "r"(ordered(x)) : "memory");
+                        uint32_t y = s == s ? ordered(x) : kMarked;
+                        if (ok < 0 || ok >= a.n_pages) {  // outside the pool: scores lowest
+                            y = ordered(-INFINITY);
+                        } else if (s == s) {
+                            // what is not finite leaves the decision to fp64
+                            if (!(fabsf(x) <= 3.402823466e38f)) odd = true;
+                            high = max(high, y), low = min(low, y);
+                        }
+                        const uint32_t at = first_key + p * 4;
+                        if (g0 == 0) st_cluster(at, y);
+                        else asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(at), "r"(y) : "memory");
                     }
                 }
             }
@@ -380,8 +395,13 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     }
     static_assert(kBins == 4 * kThreads, "four bins a thread");
     int *near = reinterpret_cast<int *>(key + a.max_pages);
-    // q or every scale is 0: all scores are (no scale that is not finite among them)
-    const bool equal = top == 0 || (mass == 0.f && top < 0x7f800000u);
+    // q or every scale is 0: all scores are, but a marked page's
+    bool equal = top == 0 || (mass == 0.f && top < 0x7f800000u);
+    if (equal) {
+        int marked = 0;
+        for (int p = t; p < m; p += kThreads) marked |= key[p] == kMarked;
+        equal = !__syncthreads_or(marked);
+    }
     int n_in = 0;
 #pragma unroll 4
     for (int p = t; p < m; p += kThreads) {
@@ -394,54 +414,77 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     n_in = __reduce_add_sync(0xffffffffu, n_in);
     if (lane == 0) atomicAdd(&s_in, n_in);
     __syncthreads();
-    const int near_n = s_near, places = k - s_in;
-    // settle the near ones among themselves: `sure` beat a page whatever the errors,
-    // `may` might
-    double *exact = near_n <= kThreads ? s_exact : a.exact + unit * a.max_pages;
-    int settled = 0;
-    for (int base = 0; base < near_n; base += kThreads) {
-        const int j = base + t;
+    const int near_n = s_near, places = k - s_in;  // at least one place if there is a near page
+    // Up to kThreads of them are settled among themselves first: `sure` beat a page whatever the
+    // errors, `may` might.  More would take too long pair by pair (4095 pages that tie: 12 ms)
+    const bool pairs = near_n <= kThreads;
+    double *exact = pairs ? s_exact : a.exact + unit * a.max_pages;
+    constexpr uint32_t kOpen = 2, kTie = 4;
+    if (pairs) {
         int sure = 0, may = 0;
-        if (j < near_n) {
-            const float x = unordered(key[near[j]]);
+        if (t < near_n) {
+            const float x = unordered(key[near[t]]);
             for (int o = 0; o < near_n; ++o) {
                 const float y = unordered(key[near[o]]);
                 sure += y > x + eps;
                 may += !(y < x - eps);  // itself among them
             }
         }
-        // 1: in, 0: out, 2: open.  The scores are still read by others: kept aside
-        const int fate = may - 1 < places ? 1 : (sure >= places ? 0 : 2);
-        if (j < near_n) exact[j] = fate;
-        settled += j < near_n && fate == 1;
-        if (j < near_n && fate == 2) s_open = 1;
+        // 1: in, 0: out.  The scores are still read by others
+        const uint32_t fate = may - 1 < places ? 1 : sure >= places ? 0 : kOpen;
+        if (t < near_n && fate == kOpen) s_open = 1;
+        const int settled = __reduce_add_sync(0xffffffffu, t < near_n && fate == 1);
+        __syncthreads();
+        if (lane == 0) atomicAdd(&s_in, settled);
+        if (t < near_n) key[near[t]] = fate;
+        __syncthreads();
     }
-    settled = __reduce_add_sync(0xffffffffu, settled);
-    __syncthreads();
-    if (lane == 0) atomicAdd(&s_in, settled);
-    for (int j = t; j < near_n; j += kThreads) key[near[j]] = (uint32_t)exact[j];
-    __syncthreads();
-    if (s_open) {
-        const int left = k - s_in;
+    int want = k - s_in;  // places for the open ones
+    if (!pairs || s_open) {
 #pragma unroll 1
         for (int j = warp; j < near_n; j += kWarps) {
             const int p = near[j];
-            if (key[p] != 2) continue;  // the same for the whole warp
+            if (pairs && key[p] != kOpen) continue;  // the same for the whole warp
             const double x = exact_score<D, FMT, DT>(a, b, hk, i, table[p]);
             if (lane == 0) exact[j] = x;
         }
         __syncthreads();
-        for (int base = 0; base < near_n; base += kThreads) {
-            const int j = base + t;
+        if (pairs) {
             bool in = false;
-            if (j < near_n && (key[near[j]] & 2)) {
-                const double x = exact[j];
+            if (t < near_n && key[near[t]] == kOpen) {
+                const double x = s_exact[t];
                 int place = 0;
                 for (int o = 0; o < near_n; ++o)
-                    if (key[near[o]] & 2) place += exact[o] > x || (exact[o] == x && near[o] < near[j]);
-                in = place < left;
+                    if (key[near[o]] == kOpen) place += s_exact[o] > x || (s_exact[o] == x && near[o] < near[t]);
+                in = place < want;
             }
-            if (in) key[near[j]] = 3;
+            __syncthreads();
+            if (in) key[near[t]] = 1;
+        } else {  // the cut, by eight bits of the scores' order at a time
+            uint64_t cut = 0, known = 0;
+#pragma unroll 1
+            for (int shift = 56; shift >= 0; shift -= 8) {
+                hist[t] = 0;
+                __syncthreads();
+                for (int j = t; j < near_n; j += kThreads) {
+                    const uint64_t u = ordered(exact[j]);
+                    if ((u & known) == cut) atomicAdd(&hist[u >> shift & 255], 1);
+                }
+                __syncthreads();
+                const int c = hist[255 - t], above = block_scan(c, wsum);
+                if (above < want && want <= above + c) {
+                    s_bin = 255 - t;
+                    s_in = above;
+                }
+                __syncthreads();
+                cut |= (uint64_t)s_bin << shift;
+                known |= (uint64_t)255 << shift;
+                want -= s_in;  // of those that share the bits known so far
+            }
+            for (int j = t; j < near_n; j += kThreads) {
+                const uint64_t u = ordered(exact[j]);
+                key[near[j]] = u > cut ? 1 : u < cut ? 0 : kTie;  // the lowest `want` ties are in
+            }
         }
     }
     __syncthreads();
@@ -449,6 +492,14 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     // pages, of odd length so that the threads' reads fall into different banks
     const int per = (m + kThreads - 1) / kThreads | 1;
     const int p_end = min(m, (t + 1) * per);
+    if (!pairs) {
+        int ties = 0;
+        for (int p = t * per; p < p_end; ++p) ties += key[p] == kTie;
+        ties = block_scan(ties, wsum);
+        for (int p = t * per; p < p_end; ++p)
+            if (key[p] == kTie) key[p] = ties++ < want;
+        __syncthreads();
+    }
     int mine = 0;
     for (int p = t * per; p < p_end; ++p) mine += (int)(key[p] & 1);
     int at = block_scan(mine, wsum);

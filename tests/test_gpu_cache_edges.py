@@ -228,3 +228,112 @@ def test_selection_of_scores_below_normal_numbers(dtype, small, fmt):
         want = ref.select(f64(q), ref.snapshot(c), t, [n], [2], m, True)
         assert np.array_equal(pages.cpu().numpy(), want)
         assert not np.array_equal(want[0, 0, 0, : m - 1], np.arange(m - 1))
+
+
+def many_pages(pages, fmt="e4m3", page=16, seed=1, heads=1, d=64):
+    """(cache, table, k, v): one sequence of so many pages of random rows."""
+    n = pages * page
+    c = new_cache(pages, heads, page, d, fmt)
+    t = np.random.RandomState(seed).permutation(pages)[None]
+    k = rows((1, heads, n, d), seed, torch.float32)
+    return c, t, k
+
+
+def check_selection(q, c, t, lens, ns):
+    for n in ns:
+        pages = pkg.cache_select(q.cuda(), c, dev(t), dev(lens), n)
+        assert status() == pkg.ATTN_OK
+        want = ref.select(f64(q), ref.snapshot(c), t, lens, [q.shape[2]], n, True)
+        assert np.array_equal(pages.cpu().numpy(), want), n
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("pages", [200, 700, 2000])  # up to eight CTAs, few or many pages near the cut
+@pytest.mark.parametrize("marked", [1, 5, 400])
+def test_selection_among_marked_pages(marked, pages, fmt):
+    """Pages that hold a value which is not finite score highest, the lowest of them first, and
+    leave the others' order as it is."""
+    c, t, k = many_pages(pages, fmt)
+    at = np.random.RandomState(3).permutation(pages - 1)[: min(marked, pages // 2)]
+    for i, p in enumerate(at):
+        k[0, 0, 16 * p + i % 16, i % 64] = (math.nan, math.inf, -math.inf)[i % 3]
+    pkg.cache_append(c, k.cuda(), k.cuda(), dev(t), dev([0]))
+    for heads, dtype in ((2, torch.bfloat16), (9, torch.float32)):  # a block of eight heads, two
+        check_selection(rows((1, heads, 2, 64), 2, dtype), c, t, [16 * pages],
+                        (1, 2, len(at), len(at) + 1, len(at) + 2, len(at) + 40, pages - 1))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("pages", [300, 1500])
+def test_selection_where_many_pages_tie(pages, fmt):
+    """Equal scores, and scores that differ by less than fp32 tells, on more pages than are settled
+    pair by pair; some far above and below."""
+    c, t, k = many_pages(pages, fmt)
+    k[:] = 0
+    k[..., 0], k[..., 1] = 64.0, 0.5 if fmt == "e4m3" else 1.0
+    rng = np.random.RandomState(5)
+    for p in rng.permutation(pages)[: pages // 3]:
+        k[0, 0, 16 * p, 1] *= 1.125 if fmt == "e4m3" else 2.0
+    for i, p in enumerate(rng.permutation(pages)[:20]):
+        k[0, 0, 16 * p: 16 * p + 16, 0] = 8.0 if i % 2 else 128.0
+    pkg.cache_append(c, k.cuda(), k.cuda(), dev(t), dev([0]))
+    q = torch.zeros((1, 1, 1, 64))
+    q[..., 0], q[..., 1] = 1024.0, 2.0 ** -12
+    ns = (1, 2, 5, 30, pages // 3, pages // 2, pages - 7, pages - 1, pages)
+    check_selection(q, c, t, [16 * pages], ns)
+    check_selection(-q, c, t, [16 * pages], ns)
+    check_selection(q * 0, c, t, [16 * pages], ns)
+
+
+def test_selection_of_a_query_that_is_not_finite():
+    """Every page's score is NaN, infinite or, where codes are 0, as it may be."""
+    pages = 600
+    c, t, k = many_pages(pages)
+    k[..., 3] = 0
+    k[0, 0, 16 * 77: 16 * 78, 5] = 0
+    k[0, 0, 16 * 99: 16 * 100] = 0
+    pkg.cache_append(c, k.cuda(), k.cuda(), dev(t), dev([0]))
+    for value in (math.nan, math.inf, -math.inf):
+        for channel in (3, 5, 7):
+            q = rows((1, 1, 1, 64), 2, torch.float32)
+            q[0, 0, 0, channel] = value
+            with np.errstate(invalid="ignore"):
+                check_selection(q, c, t, [16 * pages], (2, 60, 300, 598))
+
+
+def test_selection_of_marked_pages_and_zeros():
+    """Scores of 0 wherever the page is not marked."""
+    pages = 400
+    c, t, k = many_pages(pages)
+    k[:] = 0
+    k[0, 0, 16 * 123] = math.nan
+    pkg.cache_append(c, k.cuda(), k.cuda(), dev(t), dev([0]))
+    for q in (rows((1, 1, 1, 64), 2, torch.float32), torch.zeros(1, 1, 1, 64)):
+        check_selection(q, c, t, [16 * pages], (1, 2, 3, 50, 399))
+
+
+def test_selection_takes_no_detour_for_marked_pages_or_ties():
+    """4096 pages: neither a marked page nor equal scores may cost a multiple of milliseconds."""
+    pages = 4096
+    times = []
+    for state in ("ordinary", "marked", "equal"):
+        c, t, k = many_pages(pages)
+        if state == "marked":
+            k[0, 0, 16 * 1000 + 3, 5] = math.nan
+        if state == "equal":
+            k[:] = 1.0
+        pkg.cache_append(c, k.cuda(), k.cuda(), dev(t), dev([0]))
+        q, tt, ll = rows((1, 4, 1, 64), 2, torch.bfloat16).cuda(), dev(t), dev([16 * pages])
+        best = math.inf
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            a.record()
+            pkg.cache_select(q, c, tt, ll, 96)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+    print("ordinary, marked, equal: %.3f %.3f %.3f ms" % tuple(times))
+    assert status() == pkg.ATTN_OK
+    assert times[1] < 4 * times[0] and times[2] < 2.0
