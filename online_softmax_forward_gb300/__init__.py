@@ -482,6 +482,13 @@ def merge(o_parts, lse_parts, out_dtype=None, stream=None):
 
 
 # ------------------------------------------------------------------ paged 8-bit cache
+class _Scratch(threading.local):
+    """A thread's workspaces of one cache, which end with the thread."""
+
+    def __init__(self):
+        self.kept = {}  # stream handle -> workspace of the calls on it
+
+
 class KVCache:
     """The pool of a paged 8-bit key/value cache (include/attn.h): five
     contiguous CUDA tensors the caller owns,
@@ -512,7 +519,7 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale, self.k_bounds = k, v, k_scale, v_scale, k_bounds
         self.n_pages, self.H_kv, self.page, self.d = n, h, page, d
         self.device = k.device
-        self._scratch = {}  # (thread, stream handle) -> workspace of its calls
+        self._scratch = _Scratch()
         self.c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                         k_bounds.data_ptr() if k_bounds is not None else None, n, h, page, d,
                         formats[k.dtype])
@@ -658,6 +665,9 @@ def _cache_q(cache, q):
     return shape[0], shape[1], shape[2]
 
 
+_KEPT_BYTES = 32 << 20  # of one kept workspace; attention needs 21 MB at most
+
+
 @functools.lru_cache(maxsize=4096)
 def _need(size, *args):
     """Bytes of a workspace: ``size`` depends on its arguments alone."""
@@ -670,22 +680,22 @@ def _workspace(workspace, need, cache, stream, handle):
     """(pointer, bytes, tensor) of the scratch of one call; the tensor has to outlive the launch.
     A thread's calls on one stream follow one another, so the cache keeps a workspace for each
     thread and stream (a call's two kernels need not be adjacent when two threads share a
-    stream); a call that is being captured, or on a stream that it names, gets one of its own,
-    which belongs to the graph or to that stream."""
+    stream), up to a size that every attention call fits; a call that is being captured, or on a
+    stream that it names, gets one of its own, which belongs to the graph or to that stream."""
     if workspace is not None:
         if not workspace.is_contiguous() or _device_of(workspace) != cache.device:
             raise ValueError("workspace must be a contiguous tensor on %s" % cache.device)
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    keep = stream is None and not _capturing()
+    keep = stream is None and need <= _KEPT_BYTES and not _capturing()
     if keep:
-        who = (threading.get_ident(), handle)
-        kept = cache._scratch.get(who)
+        scratch = cache._scratch.kept
+        kept = scratch.get(handle)
         if kept is not None and kept[1] >= need:
             return kept
     workspace = _new(stream, max(need, 16), _torch.uint8, cache.device)
     new = (workspace.data_ptr(), max(need, 16), workspace)
     if keep:
-        cache._scratch[who] = new
+        scratch[handle] = new
     return new
 
 

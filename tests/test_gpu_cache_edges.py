@@ -337,3 +337,36 @@ def test_selection_takes_no_detour_for_marked_pages_or_ties():
     print("ordinary, marked, equal: %.3f %.3f %.3f ms" % tuple(times))
     assert status() == pkg.ATTN_OK
     assert times[1] < 4 * times[0] and times[2] < 2.0
+
+
+# ------------------------------------------------------------------ memory and refusals
+def test_workspaces_end_with_their_use():
+    """Selecting for many queries among many pages leaves no workspace of its size behind, and a
+    thread's workspaces end with the thread."""
+    import threading
+    pages = 2000
+    c, t, k = many_pages(pages, heads=2)
+    tt, ll = dev(t), dev([16 * pages])
+    pkg.cache_append(c, k.cuda(), k.cuda(), tt, dev([0]))
+    q = rows((1, 2, 2000, 64), 3, torch.bfloat16).cuda()
+    one = q[:, :, :1].contiguous()
+    pkg.attention_cache(one, c, tt, ll)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    del_me = pkg.cache_select(q, c, tt, ll, 3)
+    del del_me
+    assert torch.cuda.memory_allocated() - before < 8 << 20  # the call's own is 64 MB
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(3):
+                pkg.attention_cache(one, c, tt, ll)
+            torch.cuda.synchronize()
+
+    before = torch.cuda.memory_allocated()
+    for _ in range(8):
+        x = threading.Thread(target=work)
+        x.start()
+        x.join()
+    assert torch.cuda.memory_allocated() == before
+    assert status() == pkg.ATTN_OK
