@@ -509,6 +509,8 @@ class KVCache:
         n, h, page, d = k.shape
         if page not in (16, 32, 64, 128) or d not in (64, 128):
             raise ValueError("page must be 16, 32, 64 or 128 and d 64 or 128, got %d and %d" % (page, d))
+        if n < 1 or h < 1:
+            raise ValueError("a pool has at least one page and one kv head, got %d and %d" % (n, h))
         dev = _device_of(k, v)
         for t, name in ((k, "k"), (v, "v")):
             _check_out(t, (n, h, page, d), k.dtype, dev, name)

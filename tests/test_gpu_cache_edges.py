@@ -370,3 +370,9 @@ def test_workspaces_end_with_their_use():
         x.join()
     assert torch.cuda.memory_allocated() == before
     assert status() == pkg.ATTN_OK
+
+
+def test_empty_pools_are_refused():
+    for n, h in ((0, 2), (4, 0)):
+        with pytest.raises(ValueError):
+            pkg.KVCache.empty(n, h, 16, 64)
