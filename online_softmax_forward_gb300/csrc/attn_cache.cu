@@ -77,6 +77,7 @@ __global__ void __launch_bounds__((kAppendThreads<D, MOST>), (kAppendCtas<D, DT,
     const int hk = (int)((blockIdx.x >> 1) - page_of * a.Hkv);
     const int b = (int)(page_of / a.by_touched);
     const int tp = (int)(page_of - (uint32_t)b * a.touched);
+    if (!in_bounds(b < a.B && hk < a.Hkv, a.status)) return;
     const int pos = a.pos[b];
     int cnt = a.counts ? a.counts[b] : a.S;
     if (cnt < 0 || cnt > a.S || pos < 0) {  // nothing of this sequence is written
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__((kAppendThreads<D, MOST>), (kAppendCtas<D, DT,
         return;
     }
     const int64_t ph = (int64_t)phys * a.Hkv + hk;
+    if (!in_bounds(ph < (int64_t)a.n_pages * a.Hkv && r1 <= a.page, a.status)) return;
     uint8_t *codes = (which ? a.codes[1] : a.codes[0]) + (ph << a.page_shift) * D;
     float *scale = (which ? a.scale[1] : a.scale[0]) + ph;
     const float before = r0 > 0 ? *scale : 0.f;
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__((kAppendThreads<D, MOST>), (kAppendCtas<D, DT,
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int r = rl + n * RL;
-        if (r < r0 || r >= r1) continue;
+        if (r < r0 || r >= r1 || !in_bounds(((size_t)rl * D + g * 8) + n * (RL * D) + 8 <= (size_t)a.page * D, a.status)) continue;
         uint2 c = make_uint2(0, 0);
         if (inv > 0.f) {
             float f[8];
@@ -176,6 +178,7 @@ __global__ void __launch_bounds__((kAppendThreads<D, MOST>), (kAppendCtas<D, DT,
     const float ratio = now > 0.f ? before * inv : 0.f;
     if (grew) {  // the older rows under the larger scale
         for (int i = threadIdx.x; i < r0 * (D / 8); i += T) {
+            if (!in_bounds((i + 1) * 8 <= a.page * D, a.status)) break;
             uint2 *p = reinterpret_cast<uint2 *>(codes) + i;
             uint2 c = *p;
             float f[8];
@@ -249,6 +252,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadArgs
     const int tile = (int)((blockIdx.x >> 1) - block_of * a.tiles);
     const int b = (int)(block_of / a.by_heads);
     const int hk = (int)(block_of - (uint32_t)b * a.Hkv);
+    if (!in_bounds(b < a.B && hk < a.Hkv, a.status)) return;
     const int len0 = a.lens[b];
     const int len = clamp_len(len0, a.max_pages, a.page);
     if (len != len0 && threadIdx.x == 0) atomicOr(a.status, kStatusTable);
@@ -258,10 +262,11 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadArgs
     if (threadIdx.x < 1u << (a.tile_shift - a.page_shift)) {
         int64_t block = -1;
         const int64_t lp = (first >> a.page_shift) + threadIdx.x;
-        if (((int)threadIdx.x << a.page_shift) < held) {
+        if (((int)threadIdx.x << a.page_shift) < held && in_bounds(lp < a.max_pages, a.status)) {
             const int phys = a.table[(int64_t)b * a.max_pages + lp];
             if (phys < 0 || phys >= a.n_pages) atomicOr(a.status, kStatusTable);  // read as zero, reported
             else block = (int64_t)phys * a.Hkv + hk;
+            if (!in_bounds(block < (int64_t)a.n_pages * a.Hkv, a.status)) block = -1;
         }
         s_block[threadIdx.x] = block;
         s_scale[threadIdx.x] = block < 0 ? 0.f : (which ? a.scale[1] : a.scale[0])[block];
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadArgs
         const int r = i / G, in_page = r & (a.page - 1);
         const int64_t block = s_block[r >> a.page_shift];
         float f[E];
-        if (r < held && block >= 0) {
+        if (r < held && block >= 0 && in_bounds(in_page * D + (i % G + 1) * E <= a.page * D, a.status)) {
             const float s = s_scale[r >> a.page_shift];
             const uint8_t *c = codes + ((block << a.page_shift) + in_page) * D + i % G * E;
             if constexpr (DT == 0) {

@@ -132,10 +132,12 @@ __device__ __forceinline__ Tile find_tile(const FwdArgs &a, const Place &p) {
     const Unit u = unit_at(a, p.b, p.unit);
     if (a.pages) {
         const int64_t list = ((int64_t)u.b * a.Hkv + u.hk) * a.nseg + u.seg;
+        if (!in_bounds(list < (int64_t)a.B * a.Hkv * a.nseg && lp < a.n_sel, a.status)) return d;
         lp = a.pages[list * a.n_sel + lp];
         if (lp < -1 || lp >= a.max_pages) atomicOr(a.status, kStatusTable);
         if (lp < 0 || lp >= a.max_pages) return d;
     }
+    if (!in_bounds(u.b < a.B && lp < a.max_pages, a.status)) return d;
     const int phys = a.table[(int64_t)u.b * a.max_pages + lp];
     const int len = clamp_len(a.lens[u.b], a.max_pages, a.page);
     const int cnt = a.counts ? min(max(a.counts[u.b], 0), a.Sq) : a.Sq;
@@ -153,6 +155,7 @@ __device__ __forceinline__ Tile find_tile(const FwdArgs &a, const Place &p) {
         return d;
     }
     const int64_t ph = (int64_t)phys * a.Hkv + u.hk;
+    if (!in_bounds(ph < (int64_t)a.n_pages * a.Hkv && sub < 1 << shift, a.status)) return d;
     d.at = (int)((ph << shift) + sub);
     d.ks = a.ks[ph];
     d.vs = a.vs[ph];
@@ -206,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
     if (a.one_each) {
         here.b = (int)((uint32_t)blockIdx.x / a.by_units);
         here.unit = blockIdx.x - here.b * a.units;
+        if (!in_bounds(here.b < a.B, a.status)) return;
         if (here.unit == 0 && threadIdx.x == 0) report(here.b);
         here.n = a.pages ? tpu : (clamp_len(a.lens[here.b], a.max_pages, a.page) + KT - 1) / KT;
         share_unit();
@@ -293,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
     int i = 0;  // tile of the range
     while (i < n_tiles) {
         const Unit u = unit_at(a, here.b, here.unit);
+        if (!in_bounds(u.b < a.B && here.unit < a.units, a.status)) break;
         const int left = min(here.n - here.t, n_tiles - i);  // tiles of this unit in the range
         const int len = clamp_len(a.lens[u.b], a.max_pages, a.page);
         const int cnt = a.counts ? min(max(a.counts[u.b], 0), a.Sq) : a.Sq;
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_fwd_kernel(const FwdArgs a)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             int qi, h;
-            const bool real = row_of<R>(a, u, nb * 8 + g, qi, h);
+            const bool real = row_of<R>(a, u, nb * 8 + g, qi, h) && q_row(a, u, h, qi);
             sees_all[nb] = real ? visible_keys(len, cnt, qi, a.causal) : 0;
             if (real) low = min(low, sees_all[nb]);
             const size_t at = real ? (((size_t)u.b * a.Hkv * a.G + h) * a.Sq + qi) * D + t * (D / 4) : 0;
@@ -740,7 +745,7 @@ __global__ void __launch_bounds__(kThreads) cache_merge_kernel(const FwdArgs a) 
     size_t row;
     if (!out_row<R>(a, u, r, row)) return;
     const int n = d0.y - (int)blockIdx.x + 1;
-    if (!in_bounds(n <= kCacheMaxCtas, a.status)) return;
+    if (!in_bounds(n >= 1 && n <= kCacheMaxCtas && blockIdx.x + n <= gridDim.x, a.status)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the owner's state lies in its second slot, the others' in their first
     auto slot = [&](int p) { return 2 * (int64_t)(blockIdx.x + p) + (p == 0 ? 1 : 0); };
@@ -794,7 +799,7 @@ __global__ void __launch_bounds__(kThreads) cache_merge_rows_kernel(const FwdArg
     size_t row;
     if (r >= R || !out_row<R>(a, u, r, row)) return;
     const int n = d0.y - (int)blockIdx.x + 1;
-    if (!in_bounds(n <= kCacheMaxCtas, a.status)) return;
+    if (!in_bounds(n >= 1 && n <= kCacheMaxCtas && blockIdx.x + n <= gridDim.x, a.status)) return;
     auto slot = [&](int p) { return 2 * (int64_t)(blockIdx.x + p) + (p == 0 ? 1 : 0); };
     float M = -INFINITY;
     for (int p = lane; p < n; p += 32) M = fmaxf(M, a.pl[slot(p) * R + r]);

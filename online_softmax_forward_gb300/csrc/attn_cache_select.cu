@@ -123,11 +123,12 @@ __device__ double exact_score(const SelectArgs &a, int b, int hk, int i, int phy
     for (int h0 = 0; h0 < a.G; h0 += 4) {
         const int h = min(h0 + sub, a.G - 1);  // a head twice changes no maximum
         const size_t qi = (((size_t)b * a.Hkv * a.G + hk * a.G + h) * a.Sq + i) * D + c0;
+        const bool there = in_bounds(qi + D / 8 <= (size_t)a.B * a.Hkv * a.G * a.Sq * D, a.status);
         double x[4] = {};
 #pragma unroll
         for (int c = 0; c < D / 8; c += 8) {
             float q8[8], l8[8], h8[8];
-            codec::load8<DT>(a.q, qi + c, q8);
+            codec::load8<DT>(a.q, there ? qi + c : 0, q8);
             const uint2 lw = *reinterpret_cast<const uint2 *>(lo + c);
             const uint2 hw = *reinterpret_cast<const uint2 *>(hi + c);
             codec::decode4<FMT>(lw.x, l8); codec::decode4<FMT>(lw.y, l8 + 4);
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
     const int b = (int)(head_of / a.by_heads);
     const int hk = (int)(head_of - (uint32_t)b * a.Hkv);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, t4 = lane & 3;
+    if (!in_bounds(b < a.B && hk < a.Hkv && i < a.Sq, a.status)) return;  // the whole cluster
     const int len0 = a.lens[b], cnt0 = a.counts ? a.counts[b] : a.Sq;
     const int len = clamp_len(len0, a.max_pages, a.page);
     const int cnt = min(max(cnt0, 0), a.Sq);
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 const int p = base + 8 * j + g;
-                next[j] = p < p1 ? table[p] : -1;
+                next[j] = p < p1 && in_bounds(p < a.max_pages, a.status) ? table[p] : -1;
             }
         };
         constexpr int kStride = kThreads / 4 * kGroups;
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_select_kernel(const SelectA
             const int p = near[j];
             if (pairs && key[p] != kOpen) continue;  // the same for the whole warp
             const double x = exact_score<D, FMT, DT>(a, b, hk, i, table[p]);
-            if (lane == 0) exact[j] = x;
+            if (lane == 0 && in_bounds(j < (pairs ? kThreads : a.max_pages), a.status)) exact[j] = x;
         }
         __syncthreads();
         if (pairs) {

@@ -344,10 +344,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
             at = -1;
             if (i >= n_tiles) return;
             const int tile = j + (lane >> 3), key = (p.t0 + tile) * KT + (lane & 7) * 16;
-            if (tile < p.live && key < p.len) {
+            if (tile < p.live && key < p.len && in_bounds(p.u.b < a.B && key >> page_shift < a.max_pages, a.status)) {
                 const int phys = a.table[(int64_t)p.u.b * a.max_pages + (key >> page_shift)];
                 if (phys < 0 || phys >= a.n_pages) atomicOr(a.status, kStatusTable);
                 else at = ((phys * a.Hkv + p.u.hk) << (page_shift - 4)) + ((key & (a.page - 1)) >> 4);
+                if (!in_bounds(at < ((int64_t)a.n_pages * a.Hkv) << (page_shift - 4), a.status)) at = -1;
             }
         };
         settle();
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                 for (int e = 0; e < 16 / PW; ++e) {
                     int ri, rh;
                     q[e].u[0] = make_uint4(0, 0, 0, 0);
-                    if (row_of<R>(a, p.u, warp * 16 + e * PW + sub, ri, rh))
+                    if (row_of<R>(a, p.u, warp * 16 + e * PW + sub, ri, rh) && q_row(a, p.u, rh, ri))
                         q[e].load(a.q, (((size_t)p.u.b * a.Hkv * a.G + rh) * a.Sq + ri) * D + piece * 8);
                 }
                 if (!__all_sync(0xffffffffu, watch.wait(bar(bars->q_empty), (qn & 1) ^ 1))) break;
@@ -736,8 +737,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tc_kernel(const __grid_cons
                     __syncwarp();  // the loads above are the whole warp's
                 }
                 if (t == 0 && real) {
-                    if (!whole) a.pl[sl * R + r] = lse2;
-                    else if (a.lse) a.lse[at / D] = lse2 * kLn2;
+                    if (!whole) {
+                        if (in_bounds(sl < 2 * (int)gridDim.x, a.status)) a.pl[sl * R + r] = lse2;
+                    }
+                    else if (a.lse && in_bounds(at / D < (size_t)a.B * a.Hkv * a.G * a.Sq, a.status)) a.lse[at / D] = lse2 * kLn2;
                 }
             }
             if (p.live > 0) {
@@ -770,7 +773,7 @@ __global__ void __launch_bounds__(8 * D / 4) cache_tc_merge_kernel(const FwdArgs
     size_t row;
     if (!out_row<R>(a, u, r, row)) return;
     const int n = d.y - (int)blockIdx.x + 1;
-    if (!in_bounds(n <= kCacheMaxCtas, a.status)) return;
+    if (!in_bounds(n >= 1 && n <= kCacheMaxCtas && blockIdx.x + n <= gridDim.x, a.status)) return;
     auto slot = [&](int p) { return 2 * (size_t)(blockIdx.x + p) + (p == 0 ? 1 : 0); };
     float M = -INFINITY;
     for (int p = 0; p < n; ++p) M = fmaxf(M, a.pl[slot(p) * R + r]);

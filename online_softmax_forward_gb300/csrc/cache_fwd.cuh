@@ -146,6 +146,11 @@ __device__ __forceinline__ void load_q(const FwdArgs &a, size_t i, float *f) {
     }
 }
 
+// The bounds-checking build: is the row of q of this head and query there?
+__device__ __forceinline__ bool q_row(const FwdArgs &a, const Unit &u, int h, int i) {
+    return in_bounds(u.b < a.B && h < a.Hkv * a.G && i < a.Sq, a.status);
+}
+
 // Eight consecutive outputs.
 __device__ __forceinline__ void store_o8(const FwdArgs &a, size_t i, const float *f) {
     if (a.dtype == ATTN_BF16) {

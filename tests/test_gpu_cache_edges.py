@@ -23,6 +23,8 @@ import torch
 
 import cache_ref as ref
 import online_softmax_forward_gb300 as pkg
+import test_gpu_cache as cache_tests
+from gpu_util import ensure_built
 from test_gpu_cache import HALF, check_pool, dev, f64, new_cache, rows, status, tables
 
 pytestmark = pytest.mark.gpu
@@ -376,3 +378,40 @@ def test_empty_pools_are_refused():
     for n, h in ((0, 2), (4, 0)):
         with pytest.raises(ValueError):
             pkg.KVCache.empty(n, h, 16, 64)
+
+
+# ------------------------------------------------------------------ the bounds-checking build
+@pytest.fixture
+def checked(monkeypatch):
+    """The wrappers on libattn_checked.so: status() then also reports an index out of bounds."""
+    ensure_built()
+    monkeypatch.setattr(pkg, "load_library", pkg.load_checked_library)
+
+
+@pytest.mark.parametrize("case", cache_tests.ATTEND, ids=lambda c: "L%s_q%d_H%dx%d_d%d_p%d" % (c[0], c[2], *c[3:]))
+def test_checked_wide_tables_and_lists(checked, case):
+    cache_tests.test_a_wide_table_gives_the_same_results(case)
+
+
+@pytest.mark.parametrize("d,fmt", [(64, "int8"), (128, "e4m3")])
+def test_checked_shared_ranges(checked, d, fmt):
+    cache_tests.test_many_rows_of_many_sequences(d, fmt)
+    cache_tests.test_every_key_of_a_large_split_call_counts()
+
+
+def test_checked_selection(checked):
+    test_selection_among_marked_pages(5, 2000, "int8")
+    test_selection_where_many_pages_tie(1500, "e4m3")
+    for case in cache_tests.SELECT:
+        cache_tests.test_selection_and_attention_over_it(case, True, torch.float32, "e4m3")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_checked_append_read_and_serving(checked, dtype):
+    for case in cache_tests.APPEND:
+        cache_tests.test_append_gives_the_definition(case, dtype, "int8")
+    cache_tests.test_append_of_special_values("e4m3")
+    for case in (([100, 7], 70, 3, 64, 64), ([129, 128, 1, 0], 140, 1, 128, 128)):
+        cache_tests.test_read_gives_what_the_codes_stand_for(case, dtype, "e4m3")
+    cache_tests.test_a_serving_loop_with_prompt_chunk_drafts_and_single_tokens("int8")
+    cache_tests.test_numbers_out_of_range_are_skipped_and_reported()
