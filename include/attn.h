@@ -399,7 +399,7 @@ ATTN_API int attn_cache_select(const attn_cache *cache, const void *q, const int
  *          argument.  Calls that may overlap on the GPU, replays of graphs
  *          among them, need workspaces of their own.
  * Arithmetic: exact products of codes and q (fp32 q: 22 bits of each row's
- * range), fp32 sums.  A weight times its page's v_scale keeps 22 bits for fp32
+ * range; 16-bit q: down to 2^-31 of it), fp32 sums.  A weight times its page's v_scale keeps 22 bits for fp32
  * outputs and 11 for 16-bit ones, or is kept to 2^-36 of the row's largest
  * such product (16-bit outputs of many rows: 2^-30) where that is coarser.  A
  * weight below 2^-126 of the row's largest counts as 0.

@@ -38,14 +38,14 @@ struct AppendArgs {
 };
 
 // Threads of a CTA: four rows each for pages up to 64.  With 256 threads for all, two
-// 8k prompts of 32 heads take 142 us in pages of 16 (so 56) and 80 in pages of 32 (53),
-// with d = 64 and int8 40 in pages of 64 (29).
+// prompts (8192 and 5462 tokens, 32 heads) take 142 us in pages of 16 (so 56) and 80 in
+// pages of 32 (53), with d = 64 and int8 40 in pages of 64 (29).
 template <int D, int MOST>
 constexpr int kAppendThreads = MOST <= 64 ? MOST * D / 32 : 256;
 
 // CTAs of an SM.  A CTA is a chain of waits (positions, rows, the block's maximum),
-// which others hide: as many as leave each thread the registers for its rows.  Two
-// 8k prompts of 32 heads, d = 128: bf16 52 us with eight of 32 registers (five: 71,
+// which others hide: as many as leave each thread the registers for its rows.  The two
+// prompts above, d = 128: bf16 52 us with eight of 32 registers (five: 71,
 // before the instructions were fewer); fp32 83 us with four (five spill: 92, three:
 // 112); fp32 with pages of 128 85 us with two, 94 with three.
 template <int D, int DT, int MOST>
@@ -57,7 +57,7 @@ constexpr int kAppendCtas = kAppendCtasOf256<D, DT, MOST> * (256 / kAppendThread
 
 // One CTA per (touched page of a sequence, kv head, keys or values).
 // MOST: rows of the page, which registers hold.
-// Bound by memory: 95 % of the copy rate in the case above.  It is also near the
+// Bound by memory: 95 to 97 % of the copy rate in the case above.  It is also near the
 // issue rate, so a page is found without divisions, and keys' ranges and values'
 // magnitudes are kept as packed pairs of 16 bits until a warp's rows are joined.
 template <int D, int FMT, int DT, int MOST>

@@ -52,11 +52,12 @@
 // pieces of a row are swizzled so that both reads are free of bank conflicts.
 //
 // Bound: by the reading of the codes where they are many (4 x 32 heads, 32k keys,
-// d = 128: 172 us, 6.2 TB/s, 92 % of the copy rate; the SMs do not get equal shares
+// d = 128: 170 us, 6.3 TB/s, 93 % of the copy rate; the SMs do not get equal shares
 // of the memory and the last ends 14 % after the mean), by waits in short calls
-// (one sequence of 1000 tokens, 8 kv heads: 9.7 us, of which 3 for eight steps of
+// (one sequence of 1000 tokens, 8 kv heads: 10 us, of which 3 for four steps of
 // keys; the rest finds the tiles, loads q, joins, each a chain of cold loads and
-// code).  8 warps of up to 240 registers; 12 warps, which one block's registers
+// code).  From the last key to the end of a CTA, its barrier and join, the 32k-key call
+// spends 10 000 clocks on average and the last CTA 5000.  8 warps of up to 240 registers; 12 warps, which one block's registers
 // allow, measured 169 us and 9.9 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -886,6 +887,7 @@ static int cache_blocks(int64_t rows, int dtype, int d) {
 //      48     24.0, 26.8 (22.1, 22.4) 74.3, 59.9 (58.4, 41.7) 43.7, 49.6 (35.0, 37.6)
 //      64     26.5, 27.4 (25.8, 22.7) 92.1, 60.1 (72.3, 42.0) 50.7, 50.0 (42.0, 38.4)
 //      96     30.8, 28.3 (28.5, 23.3) 126.9, 61.6 (90.7, 43.7) 67.3, 50.5 (49.4, 39.0)
+// One rule for both widths: d = 64 would change over a few rows earlier (32 rows of 16 x 4096).
 constexpr int64_t kTcRows = 33, kTcAlways = 65;
 static bool cache_tc(int64_t rows, int64_t units, int sms, int dtype, bool listed) {
     return !listed && !cache_fine(dtype) && (rows >= kTcAlways || (rows >= kTcRows && units > sms));

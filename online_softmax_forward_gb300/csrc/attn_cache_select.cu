@@ -26,7 +26,7 @@
 // pages without such ties.
 //
 // Bound: by waits.  With the attention over the choice, 32 of 512 pages for 64 units
-// take 27 us and 96 of 4096 for 16 units 34 us, 12 and 23 us of it here, where the
+// take 26 us and 96 of 4096 for 16 units 34 us, 13 and 22 us of it here, where the
 // bounds alone would be read in 1 to 3 us: lengths, table, bounds, scores, histogram
 // and list follow one another.  Three kernels in its place (scores, cut, list) took 50
 // and 75 us for the pair, a bisection in place of the histogram 49.

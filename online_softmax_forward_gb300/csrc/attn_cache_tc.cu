@@ -30,11 +30,12 @@
 // busy meanwhile, and 64 weights are what the registers of 16 warps hold.  Every
 // wait is bounded, as in attn_tc.cu.
 //
-// Bound: 1024 rows on 4096 keys, 2 sequences of 8 kv heads, d = 128: 57 us, 30 % of the
+// Bound: 1024 rows on 4096 keys, 2 sequences of 8 kv heads, d = 128: 54 us, 32 % of the
 // bf16 peak on 128 of the SMs, one unit each.  A tile takes 3400 clocks, of which the
-// products need 1300; by a clock trace the products wait for keys 20 to 30 % and for
-// weights 15 to 25 %, and the converters and the softmax warps are at work 80 % of the
-// time, each a chain of loads, conversions and stores that waits for itself.
+// products need 1300; by a clock trace the products wait for keys 17 to 26 % and for
+// weights 13 to 21 %, the converters are at work 80 % of the time (half of it converting,
+// half looking up and fetching) and the softmax warps half of it, each a chain of loads,
+// conversions and stores that waits for itself.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -66,8 +67,8 @@ constexpr int kScaleRing = 8;       // tiles whose page scales are kept
 constexpr int kScaleWords = 20;     // 8 of keys, 8 of values, the pieces that are missing; 16-byte steps
 constexpr uint32_t kTmemCols = 512;
 // What a second unit costs a CTA (its queries, the first scores, the join), in tiles:
-// about 20 000 clocks against 3 400 a tile.  The chunk of the header: 57 us with a unit
-// per CTA, 64 with equal ranges.
+// about 20 000 clocks against 3 400 a tile.  The chunk of the header, when it took 57 us
+// with a unit per CTA: 64 with equal ranges.
 constexpr int kSwitch = 6;
 constexpr float kLargest = 1024.f;  // of 16 keys' sum of weights; 32 * 1024 fits fp16
 constexpr float kBase = 32.f;       // weight times page scale times rv, at its largest after a move
