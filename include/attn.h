@@ -120,6 +120,97 @@ ATTN_API int attn_fwd(const void *q, const void *k, const void *v, void *o, floa
              int dtype, void *stream);
 
 /*
+ * attn_fwd_gqa -- attn_fwd with kv heads that several query heads share: k and
+ * v [B, H_kv, Skv, d], H_kv >= 1 and H >= 1 a multiple of it; query heads
+ * h * H / H_kv .. (h + 1) * H / H_kv - 1 read kv head h.  The result is that
+ * of attn_fwd on k and v with each head repeated, without the copies.
+ * Everything else as attn_fwd (which is the case H_kv = H).
+ */
+ATTN_API int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, float *lse,
+                 int B, int H, int H_kv, int Sq, int Skv, int d, int causal, float scale,
+                 int dtype, void *stream);
+
+/*
+ * Backward pass
+ * -------------
+ * attn_bwd -- the gradients of a loss in q, k and v, given its gradients do in o
+ * and (optionally) dlse in lse.  With the forward pass's o and lse,
+ *   P  = exp(scale q k^T - lse) on the visible keys (0 elsewhere),
+ *   dS = P * (do v^T - rowsum(o * do) + dlse),
+ *   dq = scale dS k,   dk = scale dS^T q,   dv = P^T do,
+ * dk and dv summed over the query heads that share a kv head.  The
+ * probabilities are recomputed tile by tile (not on the source pages, which
+ * stop at the forward pass; the tiles are theirs: aiml.sh
+ * "verify-tiled-attention", tiled_flash_attention).
+ *
+ *   q, do  [B, H, Sq, d], k, v [B, H_kv, Skv, d] in dtype's input type;
+ *   o      [B, H, Sq, d] in dtype's output type, lse [B, H, Sq] fp32: what
+ *          attn_fwd (or _gqa, _splitkv) wrote for the same q, k, v, causal,
+ *          scale and dtype.  Over a shard of the keys (causal = 0) they may be
+ *          the merged o and lse of all shards: dk and dv are then the shard's,
+ *          and the dq of the shards add up to the whole.
+ *   dlse   [B, H, Sq] fp32 or NULL (zero)
+ *   dq, dk, dv  as q, k, v, but in dtype's output type; all are written whole
+ *   H >= 1 a multiple of H_kv >= 1; d, dtype, causal, scale as attn_fwd
+ *   workspace  16-byte aligned scratch of attn_bwd_workspace_size bytes.  Calls
+ *          that may overlap on the GPU, replays of graphs among them, need
+ *          workspaces of their own.
+ * A row with lse = -inf (no visible key) contributes nothing and gets dq = 0,
+ * whatever its o, do and dlse hold, as long as they are finite.  Skv == 0
+ * writes dq = 0; Sq == 0 writes dk = dv = 0.  Infinities and NaN in a row of
+ * q, k, v or do may reach every gradient of its 128-row tile, masked or not.
+ * Arithmetic: fp32 sums; for 16-bit types P and dS are rounded to 16 bits as
+ * operands of the products (fp16: after scaling by powers of two that keep
+ * them in range).  Sums are made in a fixed order: equal calls give equal bits.
+ * All arrays must be distinct; q, k, v, o, do and gradients 16-byte aligned.
+ * Two kernels, three where few units share a long walk.
+ */
+ATTN_API int attn_bwd_workspace_size(int B, int H, int H_kv, int Sq, int Skv, int d, int causal,
+                            int dtype, size_t *bytes);
+ATTN_API int attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+             const void *do_, const float *dlse, void *dq, void *dk, void *dv, int B, int H,
+             int H_kv, int Sq, int Skv, int d, int causal, float scale, int dtype,
+             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions
+ * ----------------
+ * attn_rotary -- turns pair i of the first `width` channels of each row by the
+ * angle p * theta_i of its token's position p (before attn_fwd or
+ * attn_cache_append; not on the source pages):
+ *   (x, y) -> amplitude * (x cos a - y sin a, x sin a + y cos a);
+ * transpose = 1 multiplies with the transposed matrices instead (angle -a,
+ * the same amplitude): the gradient in the inputs, given the one in the outputs.
+ * Channels from `width` on are copied.
+ *
+ *   q, k   rows of one or two tensors (k may be NULL) of dtype ATTN_F32,
+ *          ATTN_BF16 or ATTN_F16: logically [B][H][S][d] with the strides (in
+ *          elements, >= 0) of batch, head and token; channels are contiguous.
+ *          `out` may be `in` with the same strides; otherwise no output may
+ *          overlap an input or the other output.  Outputs must not overlap
+ *          themselves.
+ *   interleaved  0: pairs (i, i + width / 2); 1: pairs (2i, 2i + 1)
+ *   turns  [width / 2] theta_i / (2 pi) as a 64-bit fraction of a turn per
+ *          position (rounded theta_i / (2 pi) * 2^64, modulo 2^64)
+ *   pos    int32: [B][S] if pos_per_token, else [B], the position of each
+ *          sequence's first row, the others following; any values (they wrap
+ *          at 32 bits)
+ *   width  even, 2 .. d;  d even, <= 1024;  H <= 65536
+ * fp32 arithmetic on the rows; the angle's error does not grow with the
+ * position beyond 2^-64 turns of each.  One kernel.
+ */
+typedef struct attn_heads {
+    const void *in;
+    void *out;
+    int H;
+    int64_t in_stride[3], out_stride[3];
+} attn_heads;
+
+ATTN_API int attn_rotary(const attn_heads *q, const attn_heads *k, const uint64_t *turns, int width,
+                int interleaved, float amplitude, int transpose, const int32_t *pos,
+                int pos_per_token, int B, int S, int d, int dtype, void *stream);
+
+/*
  * attn_validate -- the host-side argument check of attn_fwd, without any CUDA
  * call or launch.  Returns ATTN_OK or ATTN_ERR_INVALID_ARG.  Pointers are only
  * compared and tested for alignment, never dereferenced.

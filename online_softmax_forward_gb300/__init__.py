@@ -11,6 +11,7 @@ computing anything another way.
 from __future__ import annotations
 
 import ctypes
+import fractions
 import functools
 import math
 import os
@@ -25,14 +26,15 @@ __all__ = [
     "AttnError", "library_path", "load_library", "exported_symbols",
     "test_library_path", "load_test_library", "test_exported_symbols",
     "checked_library_path", "load_checked_library",
-    "attn_fwd", "attn_validate", "attn_fwd_f32_blocked", "attn_fwd_staged",
+    "attn_fwd", "attn_fwd_gqa", "attn_validate", "attn_fwd_f32_blocked", "attn_fwd_staged",
     "attn_check_status", "attn_strerror", "attn_abi_version", "attn_test_set_hook",
     "attn_splitkv_workspace_size", "attn_splitkv_plan", "attn_fwd_splitkv", "attn_merge",
     "attn_fwd_splitkv_noalloc", "attn_shutdown",
     "attn_cache_append", "attn_cache_read", "attn_cache_select_workspace_size",
     "attn_cache_select", "attn_fwd_cache_workspace_size", "attn_fwd_cache",
-    "attention", "attention_f32_blocked", "attention_splitkv", "merge", "dtype_code",
-    "KVCache", "cache_append", "cache_read", "cache_select", "attention_cache",
+    "attn_bwd_workspace_size", "attn_bwd", "attn_rotary",
+    "attention", "attention_bwd", "attention_f32_blocked", "attention_splitkv", "merge", "dtype_code",
+    "Rotary", "rotary", "KVCache", "cache_append", "cache_read", "cache_select", "attention_cache",
 ]
 
 ATTN_OK = 0
@@ -73,9 +75,20 @@ class _Cache(ctypes.Structure):  # attn_cache of include/attn.h
                 ("n_pages", _I), ("H_kv", _I), ("page", _I), ("d", _I), ("format", _I)]
 
 
+class _Heads(ctypes.Structure):  # attn_heads of include/attn.h
+    _fields_ = [("in_", _P), ("out", _P), ("H", _I), ("in_stride", ctypes.c_int64 * 3),
+                ("out_stride", ctypes.c_int64 * 3)]
+
+
 _C = ctypes.POINTER(_Cache)
+_R = ctypes.POINTER(_Heads)
 _SIGS = [
     ("attn_fwd", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    ("attn_fwd_gqa", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    ("attn_bwd_workspace_size", _I, [_I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_Z)]),
+    ("attn_bwd", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I,
+                      _P, _Z, _P]),
+    ("attn_rotary", _I, [_R, _R, _P, _I, _I, _F, _I, _P, _I, _I, _I, _I, _I, _P]),
     ("attn_validate", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I]),
     ("attn_fwd_staged", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                              _I, _I, _I, _I, _I, _I, _F, _I, _P]),
@@ -189,6 +202,34 @@ def _check(status: int, where: str):
 def attn_fwd(q, k, v, o, lse, B, H, Sq, Skv, d, causal, scale, dtype, stream):
     return load_library().attn_fwd(q, k, v, o, lse, B, H, Sq, Skv, d, int(causal),
                                    float(scale), dtype, stream)
+
+
+def attn_fwd_gqa(q, k, v, o, lse, B, H, H_kv, Sq, Skv, d, causal, scale, dtype, stream):
+    return load_library().attn_fwd_gqa(q, k, v, o, lse, B, H, H_kv, Sq, Skv, d, int(causal),
+                                       float(scale), dtype, stream)
+
+
+def attn_bwd_workspace_size(B, H, H_kv, Sq, Skv, d, causal, dtype):
+    """Returns (status, bytes)."""
+    n = _Z(0)
+    st = load_library().attn_bwd_workspace_size(B, H, H_kv, Sq, Skv, d, int(causal), dtype,
+                                                ctypes.byref(n))
+    return st, n.value
+
+
+def attn_bwd(q, k, v, o, lse, do, dlse, dq, dk, dv, B, H, H_kv, Sq, Skv, d, causal, scale, dtype,
+             workspace, workspace_bytes, stream):
+    return load_library().attn_bwd(q, k, v, o, lse, do, dlse, dq, dk, dv, B, H, H_kv, Sq, Skv, d,
+                                   int(causal), float(scale), dtype, workspace,
+                                   int(workspace_bytes), stream)
+
+
+def attn_rotary(q, k, turns, width, interleaved, amplitude, transpose, pos, pos_per_token, B, S, d,
+                dtype, stream):
+    """``q`` and ``k`` are _Heads structures; ``k`` may be None."""
+    return load_library().attn_rotary(q, k, turns, width, int(interleaved), float(amplitude),
+                                      int(transpose), pos, int(pos_per_token), B, S, d, dtype,
+                                      stream)
 
 
 def attn_validate(q, k, v, o, lse, B, H, Sq, Skv, d, causal, scale, dtype):
@@ -337,11 +378,14 @@ def _stream_handle(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _shapes(q, k, v):
+def _shapes(q, k, v, shared=False):
+    """(B, H, Sq, Skv, d); ``shared`` allows fewer kv heads, a divisor of H."""
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k, v must be [B, H, S, d]")
     B, H, Sq, d = q.shape
-    if k.shape != v.shape or k.shape[0] != B or k.shape[1] != H or k.shape[3] != d:
+    H_kv = k.shape[1]
+    fits = H_kv == H or (shared and 0 < H_kv < H and H % H_kv == 0)
+    if k.shape != v.shape or k.shape[0] != B or not fits or k.shape[3] != d:
         raise ValueError("shape mismatch q %s k %s v %s" % (tuple(q.shape), tuple(k.shape),
                                                             tuple(v.shape)))
     for t in (q, k, v):
@@ -375,13 +419,16 @@ def _check_out(t, shape, dtype, dev, name):
 
 def attention(q, k, v, causal: bool = False, scale: float | None = None, out_dtype=None,
               return_lse: bool = True, out=None, lse=None, stream=None):
-    """O (and LSE) for contiguous CUDA tensors q [B,H,Sq,d], k/v [B,H,Skv,d].
+    """O (and LSE) for contiguous CUDA tensors q [B,H,Sq,d], k/v [B,H,Skv,d]
+    (or [B,H_kv,Skv,d], H a multiple of H_kv: H / H_kv consecutive query heads
+    share a kv head).
 
     ``out_dtype`` = torch.float32 with bf16/fp16 inputs selects the fp32-output
     variant.  Outputs are allocated with torch unless ``out`` / ``lse`` are
     given."""
     import torch
-    B, H, Sq, Skv, d = _shapes(q, k, v)
+    B, H, Sq, Skv, d = _shapes(q, k, v, shared=True)
+    H_kv = k.shape[1]
     code = dtype_code(q.dtype, out_dtype)
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k, v must share a dtype")
@@ -396,11 +443,63 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out_dty
         _check_out(lse, (B, H, Sq), torch.float32, q.device, "lse")
     sc = 0.0 if scale is None else float(scale)
     with torch.cuda.device(q.device):
-        st = attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                      lse.data_ptr() if lse is not None else None, B, H, Sq, Skv, d, causal,
-                      sc, code, _stream_handle(stream))
-    _check(st, "attn_fwd")
+        if H_kv == H:
+            st = attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                          lse.data_ptr() if lse is not None else None, B, H, Sq, Skv, d, causal,
+                          sc, code, _stream_handle(stream))
+        else:
+            st = attn_fwd_gqa(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                              lse.data_ptr() if lse is not None else None, B, H, H_kv, Sq, Skv, d,
+                              causal, sc, code, _stream_handle(stream))
+    _check(st, "attn_fwd" if H_kv == H else "attn_fwd_gqa")
     return (out, lse) if return_lse else out
+
+
+def attention_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None = None,
+                  dlse=None, out=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of a loss, from its gradients ``do`` in o and ``dlse`` (default: zero)
+    in lse; q, k, v, causal and scale as given to ``attention``, o and lse as it returned them.
+
+    q, do [B,H,Sq,d] and k, v [B,H_kv,Skv,d] share a dtype; the gradients have o's dtype (fp32 if
+    the forward pass ran with ``out_dtype`` = torch.float32).  They are allocated with torch unless
+    ``out`` = (dq, dk, dv) is given, and so is the workspace (attn_bwd_workspace_size)."""
+    if _torch is None:
+        import torch
+        _bind(torch)
+    B, H, Sq, Skv, d = _shapes(q, k, v, shared=True)
+    H_kv = k.shape[1]
+    if H < 1:
+        raise ValueError("q has no head")
+    if k.dtype is not q.dtype or v.dtype is not q.dtype or do.dtype is not q.dtype:
+        raise ValueError("q, k, v and do must share a dtype")
+    code = dtype_code(q.dtype, o.dtype)
+    dev = q.device
+    _check_out(o, q.shape, o.dtype, dev, "o")
+    _check_out(do, q.shape, q.dtype, dev, "do")
+    rows = q.shape[:3]
+    _check_out(lse, rows, _torch.float32, dev, "lse")
+    if dlse is not None:
+        _check_out(dlse, rows, _torch.float32, dev, "dlse")
+    handle = _handle(dev, stream)
+    if out is None:
+        dq = _new(stream, q.shape, o.dtype, dev)
+        dk = _new(stream, k.shape, o.dtype, dev)
+        dv = _new(stream, k.shape, o.dtype, dev)
+    else:
+        dq, dk, dv = out
+        for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
+            _check_out(t, like.shape, o.dtype, dev, name)
+    need = _need(attn_bwd_workspace_size, B, H, H_kv, Sq, Skv, d, bool(causal), code)
+    if workspace is None:  # belongs to the call's stream, or to the graph that captures it
+        workspace = _new(stream, max(need, 16), _torch.uint8, dev)
+    elif not workspace.is_contiguous() or _device_of(workspace) != dev:
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    _call_on(dev, load_library().attn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+             lse.data_ptr(), do.data_ptr(), None if dlse is None else dlse.data_ptr(),
+             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, H_kv, Sq, Skv, d, 1 if causal else 0,
+             0.0 if scale is None else float(scale), code, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), handle)
+    return dq, dk, dv
 
 
 def attention_f32_blocked(q, k, v, block_q: int, block_kv: int, causal: bool = False,
@@ -479,6 +578,124 @@ def merge(o_parts, lse_parts, out_dtype=None, stream=None):
                         lse.data_ptr(), code, _stream_handle(stream))
     _check(st, "attn_merge")
     return out, lse
+
+
+# ------------------------------------------------------------------ rotary positions
+_PI = fractions.Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+
+
+class Rotary:
+    """The angles of rotary positions: pair i of the first ``width`` channels turns by theta_i per
+    position, theta_i = base ** (-2 i / width) unless ``frequencies`` gives them.
+
+    ``layout``: "half" (pairs i, i + width / 2) or "interleaved" (2i, 2i + 1).
+    ``scaling`` stretches positions for contexts ``factor`` times as long as trained:
+      "linear"  theta_i / factor;
+      "base"    a base of base * factor ** (width / (width - 2)): the fastest pair stays, the
+                slowest is stretched by factor;
+      "parts"   pairs that turn more than ``fast`` times within the trained ``context`` stay, those
+                that turn less than ``slow`` times are divided by factor, between them both are
+                blended linearly; the amplitude is then 1 + 0.1 ln(factor).
+    ``amplitude`` overrides the factor on both results.  The table of width / 2 angles is held on
+    ``device`` as 64-bit fractions of a turn (include/attn.h)."""
+
+    def __init__(self, width, base=10000.0, layout="half", scaling=None, factor=1.0, context=None,
+                 slow=1.0, fast=32.0, frequencies=None, amplitude=None, device="cuda"):
+        import torch
+        _bind(torch)
+        if width < 2 or width % 2 != 0:
+            raise ValueError("width must be even and at least 2, got %d" % width)
+        if layout not in ("half", "interleaved"):
+            raise ValueError("layout must be \"half\" or \"interleaved\", got %r" % (layout,))
+        if scaling not in (None, "linear", "base", "parts"):
+            raise ValueError("scaling must be None, \"linear\", \"base\" or \"parts\", got %r" % (scaling,))
+        if not (factor > 0 and math.isfinite(factor)) or not (base > 0 and math.isfinite(base)):
+            raise ValueError("base and factor must be positive and finite")
+        if frequencies is not None:
+            if scaling is not None:
+                raise ValueError("frequencies are given as they are: scaling must be None")
+            theta = [float(t) for t in frequencies]
+            if len(theta) != width // 2:
+                raise ValueError("width %d takes %d frequencies, got %d" % (width, width // 2, len(theta)))
+        else:
+            if scaling == "base":
+                if width < 4:
+                    raise ValueError("scaling \"base\" takes a width of at least 4")
+                base = base * factor ** (width / (width - 2))
+            theta = [base ** (-2.0 * i / width) for i in range(width // 2)]
+            if scaling == "linear":
+                theta = [t / factor for t in theta]
+            elif scaling == "parts":
+                if context is None or context < 1 or not fast > slow:
+                    raise ValueError("scaling \"parts\" takes the trained context and slow < fast")
+                for i, t in enumerate(theta):
+                    keep = (context * t / (2.0 * math.pi) - slow) / (fast - slow)
+                    keep = min(1.0, max(0.0, keep))
+                    theta[i] = t * (keep + (1.0 - keep) / factor)
+                if amplitude is None:
+                    amplitude = 1.0 + 0.1 * math.log(factor) if factor > 1.0 else 1.0
+        if not all(math.isfinite(t) for t in theta):
+            raise ValueError("frequencies must be finite")
+        self.width, self.layout, self.frequencies = width, layout, tuple(theta)
+        self.amplitude = 1.0 if amplitude is None else float(amplitude)
+        if not math.isfinite(self.amplitude):
+            raise ValueError("amplitude must be finite")
+        # theta / 2 pi of a turn, exactly, in units of 2^-64; as int64, which torch has everywhere
+        turns = [round(fractions.Fraction(t) * 2 ** 63 / _PI) % 2 ** 64 for t in theta]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns],
+                                  dtype=torch.int64, device=device)
+        self.device = self.turns.device
+        self._args = (self.turns.data_ptr(), width, 1 if layout == "interleaved" else 0, self.amplitude)
+
+
+def _heads(x, out, B, S, d, name):
+    """attn_heads of rows x [B, H, S, d] written to ``out``."""
+    xb, xh, xs, xc = x.stride()
+    ob, oh, os_, oc = out.stride()
+    if (xc != 1 or oc != 1) and d > 1:
+        raise ValueError("the channels of %s must be contiguous" % name)
+    return _Heads(x.data_ptr(), out.data_ptr(), x.shape[1], (xb, xh, xs), (ob, oh, os_))
+
+
+def rotary(q, k, rot, pos, transpose: bool = False, out=None, stream=None):
+    """Rows q [B,H,S,d] and k [B,H_kv,S,d] (or None) turned by the positions of their tokens.
+
+    ``rot`` is a Rotary; ``pos`` an int32 CUDA tensor, [B,S], or [B] with the position of each
+    sequence's first row.  q and k may be views of any strides with contiguous channels, for example
+    of a projection's [B,S,H,d].  ``transpose`` gives the gradient in q and k from the one in the
+    results.  New results are contiguous [B,H,S,d], as ``attention`` and ``cache_append`` take them;
+    ``out`` = (q', k') writes to other places, which may be q and k themselves.  Returns (q', k')."""
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [B, H, S, d]")
+    B, H, S, d = shape
+    dev, dtype = q.device, q.dtype
+    if dev != rot.device or not q.is_cuda:
+        raise ValueError("q is on %s, the angles on %s" % (dev, rot.device))
+    if rot.width > d:
+        raise ValueError("rows have %d channels, %d are turned" % (d, rot.width))
+    code = dtype_code(dtype)
+    if k is not None and (k.dtype is not dtype or k.device != dev or len(k.shape) != 4 or
+                          (k.shape[0], k.shape[2], k.shape[3]) != (B, S, d)):
+        raise ValueError("k must be [%d, H_kv, %d, %d] of q's dtype and device" % (B, S, d))
+    per_token = pos.dim() == 2
+    p = _int32_on(pos, (B, S) if per_token else (B,), dev, "pos")
+    handle = _handle(dev, stream)
+    if out is None:
+        qo = _new(stream, shape, dtype, dev)
+        ko = None if k is None else _new(stream, k.shape, dtype, dev)
+    else:
+        qo, ko = out
+        for t, like, name in ((qo, q, "out[0]"), (ko, k, "out[1]")):
+            if (t is None) != (like is None) or \
+                    (t is not None and (t.shape != like.shape or t.dtype is not dtype or t.device != dev)):
+                raise ValueError("%s must be of the shape, dtype and device of its input" % name)
+    hq = _heads(q, qo, B, S, d, "q")
+    hk = None if k is None else _heads(k, ko, B, S, d, "k")
+    turns, width, interleaved, amplitude = rot._args
+    _call_on(dev, load_library().attn_rotary, hq, hk, turns, width, interleaved, amplitude,
+             1 if transpose else 0, p, 1 if per_token else 0, B, S, d, code, handle)
+    return qo, ko
 
 
 # ------------------------------------------------------------------ paged 8-bit cache
@@ -587,7 +804,7 @@ def _handle(device, stream):
     if stream is None:
         return _raw_stream(device.index)
     if stream.device != device:
-        raise ValueError("the cache is on %s, the stream on %s" % (device, stream.device))
+        raise ValueError("the tensors are on %s, the stream on %s" % (device, stream.device))
     return stream.cuda_stream
 
 

@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include "attn.h"
+#include "attn_bwd.h"
 #include "attn_internal.h"
 #include "cache_index.h"
 #ifdef ATTN_TEST_EXPORTS
@@ -191,10 +192,11 @@ uint64_t watchdog_ns() { return g_watchdog_ns; }
 
 // Validation shared by attn_validate / attn_fwd / attn_fwd_staged /
 // attn_fwd_splitkv.  any_width: every head width of the fp32 path is allowed
-// for every dtype (the split-KV path).
+// for every dtype (the split-KV path).  group: query heads that share a kv head.
 static int validate(const void *q, const void *k, const void *v, const void *o,
                     const float *lse, int B, int H, int Sq, int Skv, int d,
-                    int causal, float scale, int dtype, Problem *out, bool any_width = false) {
+                    int causal, float scale, int dtype, Problem *out, bool any_width = false,
+                    int group = 1) {
     if (!dtype_known(dtype)) return ATTN_ERR_INVALID_ARG;
     if (B < 0 || H < 0 || Sq < 0 || Skv < 0 || d <= 0) return ATTN_ERR_INVALID_ARG;
     if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
@@ -204,7 +206,7 @@ static int validate(const void *q, const void *k, const void *v, const void *o,
     const int64_t bh = (int64_t)B * H;
     if (bh > INT32_MAX) return ATTN_ERR_INVALID_ARG;
     const size_t ein = elem_bytes_in(dtype), eout = elem_bytes_out(dtype);
-    const size_t nq = (size_t)bh * Sq * d, nkv = (size_t)bh * Skv * d;
+    const size_t nq = (size_t)bh * Sq * d, nkv = (size_t)(bh / group) * Skv * d;
     if (nq > 0) {
         if (!q || !o) return ATTN_ERR_INVALID_ARG;
         if (!aligned(q, 16) || !aligned(o, 16)) return ATTN_ERR_INVALID_ARG;
@@ -226,7 +228,7 @@ static int validate(const void *q, const void *k, const void *v, const void *o,
     }
     if (out) {
         out->B = B; out->H = H; out->Sq = Sq; out->Skv = Skv; out->d = d;
-        out->causal = causal; out->scale = sc; out->dtype = dtype;
+        out->causal = causal; out->scale = sc; out->dtype = dtype; out->group = group;
     }
     return ATTN_OK;
 }
@@ -367,6 +369,138 @@ int attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
     int st = validate(q, k, v, o, lse, B, H, Sq, Skv, d, causal, scale, dtype, &p);
     if (st != ATTN_OK) return st;
     return fwd_impl(q, k, v, o, lse, p, (cudaStream_t)stream);
+}
+
+int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H,
+                 int H_kv, int Sq, int Skv, int d, int causal, float scale, int dtype, void *stream) {
+    if (H < 1 || H_kv < 1 || H % H_kv != 0) return ATTN_ERR_INVALID_ARG;
+    Problem p;
+    int st = validate(q, k, v, o, lse, B, H, Sq, Skv, d, causal, scale, dtype, &p, false, H / H_kv);
+    if (st != ATTN_OK) return st;
+    return fwd_impl(q, k, v, o, lse, p, (cudaStream_t)stream);
+}
+
+// The sizes of a backward pass, without its pointers.
+static int bwd_problem(int B, int H, int H_kv, int Sq, int Skv, int d, int causal, float scale,
+                       int dtype, Problem *p, BwdPlan *plan) {
+    if (B < 0 || H < 1 || H_kv < 1 || H % H_kv != 0 || Sq < 0 || Skv < 0) return ATTN_ERR_INVALID_ARG;
+    const int st = validate(nullptr, nullptr, nullptr, nullptr, nullptr, 0, H, 0, 0, d, causal, scale,
+                            dtype, p, false, H / H_kv);
+    if (st != ATTN_OK) return st;
+    if ((int64_t)B * H > INT32_MAX) return ATTN_ERR_INVALID_ARG;
+    p->B = B;
+    p->Sq = Sq;
+    p->Skv = Skv;
+    return bwd_plan(*p, plan) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+int attn_bwd_workspace_size(int B, int H, int H_kv, int Sq, int Skv, int d, int causal, int dtype,
+                            size_t *bytes) {
+    if (!bytes) return ATTN_ERR_INVALID_ARG;
+    Problem p;
+    BwdPlan plan;
+    const int st = bwd_problem(B, H, H_kv, Sq, Skv, d, causal, 0.f, dtype, &p, &plan);
+    if (st != ATTN_OK) return st;
+    *bytes = (B == 0 || Sq == 0 || Skv == 0) ? 0 : plan.bytes;
+    return ATTN_OK;
+}
+
+int attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+             const void *do_, const float *dlse, void *dq, void *dk, void *dv, int B, int H,
+             int H_kv, int Sq, int Skv, int d, int causal, float scale, int dtype, void *workspace,
+             size_t workspace_bytes, void *stream) {
+    Problem p;
+    BwdPlan plan;
+    int st = bwd_problem(B, H, H_kv, Sq, Skv, d, causal, scale, dtype, &p, &plan);
+    if (st != ATTN_OK) return st;
+    const size_t nq = (size_t)p.bh() * Sq * d, nkv = (size_t)p.bh_kv() * Skv * d;
+    const size_t ein = elem_bytes_in(dtype), eout = elem_bytes_out(dtype);
+    const bool work = nq > 0 && nkv > 0;
+    const size_t rows = (size_t)p.bh() * Sq * 4;
+    struct Arg {
+        const void *ptr;
+        size_t bytes, align;
+        bool needed, written;
+    };
+    const Arg args[] = {{q, nq * ein, 16, work, false},       {do_, nq * ein, 16, work, false},
+                        {k, nkv * ein, 16, work, false},      {v, nkv * ein, 16, work, false},
+                        {o, nq * eout, 16, work, false},      {lse, rows, 4, work, false},
+                        {dlse, dlse ? rows : 0, 4, false, false},
+                        {dq, nq * eout, 16, nq > 0, true},    {dk, nkv * eout, 16, nkv > 0, true},
+                        {dv, nkv * eout, 16, nkv > 0, true},
+                        {workspace, work ? plan.bytes : 0, 16, work, true}};
+    const int n = (int)(sizeof(args) / sizeof(args[0]));
+    for (int i = 0; i < n; ++i) {
+        if (args[i].needed && !args[i].ptr) return ATTN_ERR_INVALID_ARG;
+        if (args[i].ptr && args[i].bytes > 0 && !aligned(args[i].ptr, args[i].align)) return ATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if ((args[i].written || args[j].written) &&
+                overlap(args[i].ptr, args[i].bytes, args[j].ptr, args[j].bytes))
+                return ATTN_ERR_INVALID_ARG;
+    }
+    if (work && workspace_bytes < plan.bytes) return ATTN_ERR_INVALID_ARG;
+    if (nq == 0 && nkv == 0) return ATTN_OK;
+    st = check_device();
+    if (st != ATTN_OK) return st;
+    if (!work) {  // no pair of a query and a key: what there is of the gradients is zero
+        if ((nq > 0 && cudaMemsetAsync(dq, 0, nq * eout, (cudaStream_t)stream) != cudaSuccess) ||
+            (nkv > 0 && (cudaMemsetAsync(dk, 0, nkv * eout, (cudaStream_t)stream) != cudaSuccess ||
+                         cudaMemsetAsync(dv, 0, nkv * eout, (cudaStream_t)stream) != cudaSuccess)))
+            return ATTN_ERR_LAUNCH;
+        return ATTN_OK;
+    }
+    const BwdArgs a{q, k, v, o, do_, lse, dlse, dq, dk, dv, workspace};
+    return launch_bwd(a, p, plan, (cudaStream_t)stream);
+}
+
+// Rows of attn_rotary: pointers, strides, and an output that does not overlap itself.
+static bool heads_ok(const attn_heads &w, int B, int S, int d, size_t elem) {
+    if (w.H < 0 || w.H > 65536) return false;
+    if (w.H == 0) return true;
+    if (!w.in || !w.out || !aligned(w.in, elem) || !aligned(w.out, elem)) return false;
+    const int64_t size[3] = {B, w.H, S};
+    int order[3] = {0, 1, 2};
+    bool same = true;
+    for (int i = 0; i < 3; ++i) {
+        // offsets of the rows fit 62 bits
+        if (w.in_stride[i] < 0 || w.out_stride[i] < 0 ||
+            (double)w.in_stride[i] * size[i] > 1e18 || (double)w.out_stride[i] * size[i] > 1e18)
+            return false;
+        if (size[i] > 1 && w.in_stride[i] != w.out_stride[i]) same = false;
+        for (int j = i; j > 0 && w.out_stride[order[j]] < w.out_stride[order[j - 1]]; --j) {
+            const int t = order[j];
+            order[j] = order[j - 1];
+            order[j - 1] = t;
+        }
+    }
+    int64_t span = d;  // elements of a row, then of all rows along the dimensions so far
+    for (int i = 0; i < 3; ++i) {
+        const int e = order[i];
+        if (size[e] <= 1) continue;
+        if (w.out_stride[e] < span) return false;
+        span += w.out_stride[e] * (size[e] - 1);
+    }
+    return w.in != w.out || same;
+}
+
+int attn_rotary(const attn_heads *q, const attn_heads *k, const uint64_t *turns, int width,
+                int interleaved, float amplitude, int transpose, const int32_t *pos,
+                int pos_per_token, int B, int S, int d, int dtype, void *stream) {
+    const int dt = plain_dtype(dtype);
+    if (!q || dt < 0 || B < 0 || S < 0 || d < 2 || d > 1024 || d % 2 != 0 || width < 2 || width > d ||
+        width % 2 != 0 || (interleaved != 0 && interleaved != 1) || (transpose != 0 && transpose != 1) ||
+        (pos_per_token != 0 && pos_per_token != 1) || isnan(amplitude) || isinf(amplitude))
+        return ATTN_ERR_INVALID_ARG;
+    if ((int64_t)B * S > (int64_t)INT32_MAX) return ATTN_ERR_INVALID_ARG;
+    if (B == 0 || S == 0) return ATTN_OK;
+    const size_t elem = dt == 0 ? 4 : 2;
+    if (!heads_ok(*q, B, S, d, elem) || (k && !heads_ok(*k, B, S, d, elem))) return ATTN_ERR_INVALID_ARG;
+    if (q->H + (k ? k->H : 0) == 0) return ATTN_OK;
+    if (!turns || !aligned(turns, 8) || !pos || !aligned(pos, 4)) return ATTN_ERR_INVALID_ARG;
+    const int st = check_device();
+    if (st != ATTN_OK) return st;
+    return launch_rotary(*q, k, turns, width, interleaved != 0, amplitude, transpose != 0, pos,
+                         pos_per_token, B, S, d, dt, (cudaStream_t)stream);
 }
 
 #ifdef ATTN_TEST_EXPORTS

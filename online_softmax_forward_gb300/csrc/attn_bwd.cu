@@ -1,0 +1,298 @@
+// attn_bwd.cu -- backward pass: the plan, the kernel of the row statistics and
+// the one that adds the splits (attn_bwd.h has the mathematics).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_bwd.h"
+
+namespace attn {
+
+bool bwd_plan(const Problem &p, BwdPlan *plan) {
+    const bool f32 = p.dtype == ATTN_F32;
+    const int64_t bh = p.bh(), bhk = p.bh_kv();
+    // the sizes below are products of these; anything near 2^62 bytes is refused first
+    const double est = 4.0 * 2 * kMaxBwdSplits * ((double)bh * (p.Sq + 128.0) + (double)bhk * (p.Skv + 128.0)) *
+                       (p.d + 2.0);
+    if (est > 4.0e18) return false;
+    plan->tile = f32 ? 64 : 128;
+    plan->nq = (p.Sq + plan->tile - 1) / plan->tile;
+    plan->nk = (p.Skv + plan->tile - 1) / plan->tile;
+    plan->ns_kv = plan->ns_q = 1;
+    // Costs in products of a tile: a kv unit makes four a step, a q unit three.  A unit
+    // longer than three quarters of an SM's share of everything would be what the
+    // launch waits for, so it is cut; but not below eight steps (fp32, whose
+    // steps are long: one), where the partial sums and their kernel cost more than they give.
+    const double len_kv = 4.0 * p.group * plan->nq, len_q = 3.0 * plan->nk;
+    const double share = ((double)bhk * plan->nk * len_kv + (double)bh * plan->nq * len_q) / kBwdSms *
+                         (p.causal && p.Sq == p.Skv ? 0.5 : 1.0);
+    const double least = f32 ? 4.0 : 32.0;
+    const double goal = share * 0.75 > least ? share * 0.75 : least;
+    auto cut = [&](double len) {
+        const double n = ceil(len / goal);
+        return n < 1 ? 1 : n > kMaxBwdSplits ? kMaxBwdSplits : (int)n;
+    };
+    plan->ns_kv = cut(len_kv);
+    plan->ns_q = cut(len_q);
+    const double units = (double)bhk * plan->nk * plan->ns_kv + (double)bh * plan->nq * plan->ns_q;
+    if (units > (double)(INT32_MAX / 2)) return false;
+    plan->n_units = (int64_t)units;
+    auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+    const size_t tiles = ((size_t)p.Sq + kStatTile - 1) / kStatTile;
+    plan->off_stats = 256;
+    plan->off_max = plan->off_stats + up((size_t)bh * tiles * 2 * kStatTile * 4);
+    plan->off_part_kv = plan->off_max + up(3 * (size_t)kPreBlocks * 4);
+    plan->off_part_q = plan->off_part_kv +
+                       (plan->ns_kv > 1 ? up((size_t)plan->ns_kv * bhk * p.Skv * p.d * 2 * 4) : 0);
+    plan->bytes = plan->off_part_q + (plan->ns_q > 1 ? up((size_t)plan->ns_q * bh * p.Sq * p.d * 4) : 0);
+    return true;
+}
+
+namespace {
+
+constexpr int kPreThreads = 256;
+constexpr int kSumThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x);
+template <>
+__device__ __forceinline__ float to_f(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+
+template <typename T, int N>
+struct alignas(16) Row {
+    T e[N];
+};
+
+struct PreParams {
+    const void *o, *dout, *v;
+    const float *lse, *dlse;
+    float *stats;
+    float *maxima;        // fp16: [3][gridDim.x], the CTAs' largest |do|, |D| and |v| rows
+    unsigned *counter;    // [2]: of the units, set to 0; how many CTAs left maxima
+    int64_t tiles, v_rows;  // blocks of statistics, rows of v
+    int Sq, tiles_per_head;
+    float add;            // to nl (fp16: P is kept times 2^add)
+    int *status;
+};
+
+// Row statistics.  D / E lanes share a row (E elements of do in 16 bytes); what
+// bounds it is reading o and do once.
+//
+// fp16 (kScale): dS is held in fp16 for the products with q and k, and its size
+// follows that of do, which a loss scale or its absence moves by orders of
+// magnitude.  |dS| <= |do| |v| + |D|, so the largest norms of the rows give a
+// power of two that keeps dS in range whatever the size of do; each CTA leaves
+// its maxima, which the next kernel joins.
+template <typename TD, typename TO, int D, bool kScale>
+__global__ void __launch_bounds__(kPreThreads) bwd_stats_kernel(const PreParams p) {
+    constexpr int E = 16 / sizeof(TD), L = D / E;  // elements of a lane, lanes of a row
+    constexpr int R = 32 / L;                      // rows of a warp
+    static_assert(L >= 1 && L <= 32 && kStatTile % R == 0, "lanes");
+    const int lane = threadIdx.x & 31, sub = lane % L, rw = lane / L;
+    const int64_t warp = ((int64_t)blockIdx.x * kPreThreads + threadIdx.x) >> 5;
+    const int64_t warps = (int64_t)gridDim.x * kPreThreads >> 5;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.counter[0] = 0u;
+        p.counter[1] = gridDim.x;
+    }
+    float big_do = 0.f, big_d = 0.f, big_v = 0.f;
+    const int64_t groups = p.tiles * (kStatTile / R);
+#pragma unroll 2
+    for (int64_t w = warp; w < groups; w += warps) {
+        const int64_t tile = w / (kStatTile / R);
+        const int in_tile = (int)(w % (kStatTile / R)) * R + rw;
+        const int64_t bh = tile / p.tiles_per_head;
+        const int row = (int)(tile - bh * p.tiles_per_head) * kStatTile + in_tile;
+        float dot = 0.f, sq = 0.f, nl = -INFINITY, nd = 0.f;
+        if (row < p.Sq) {
+            const size_t at = ((size_t)bh * p.Sq + row) * D + sub * E;
+            const auto x = *reinterpret_cast<const Row<TD, E> *>((const TD *)p.dout + at);
+            Row<TO, E> y;
+            constexpr int kWords = sizeof(y) / 16;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                reinterpret_cast<uint4 *>(&y)[i] = reinterpret_cast<const uint4 *>((const TO *)p.o + at)[i];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                dot = fmaf(to_f(x.e[i]), to_f(y.e[i]), dot);
+                if constexpr (kScale) sq = fmaf(to_f(x.e[i]), to_f(x.e[i]), sq);
+            }
+        }
+#pragma unroll
+        for (int s = L / 2; s > 0; s >>= 1) {
+            dot += __shfl_xor_sync(0xffffffffu, dot, s);
+            if constexpr (kScale) sq += __shfl_xor_sync(0xffffffffu, sq, s);
+        }
+        if (sub != 0) continue;
+        if (row < p.Sq) {
+            const size_t r = (size_t)bh * p.Sq + row;
+            const float l = p.lse[r];
+            nl = l == -INFINITY ? -INFINITY : fmaf(l, -1.4426950408889634f, p.add);
+            nd = (p.dlse ? p.dlse[r] : 0.f) - dot;
+            if (kScale && l != -INFINITY) {
+                big_do = fmaxf(big_do, sq);
+                big_d = fmaxf(big_d, fabsf(nd));
+            }
+        }
+        float *st = p.stats + (size_t)tile * 2 * kStatTile + in_tile;
+        if (in_bounds(tile < p.tiles && in_tile < kStatTile, p.status)) {
+            st[0] = nl;
+            st[kStatTile] = nd;
+        }
+    }
+    if constexpr (kScale) {
+        for (int64_t w = warp; w * R < p.v_rows; w += warps) {
+            const int64_t row = w * R + rw;
+            float sq = 0.f;
+            if (row < p.v_rows) {
+                const auto x = *reinterpret_cast<const Row<TD, E> *>((const TD *)p.v + (size_t)row * D + sub * E);
+#pragma unroll
+                for (int i = 0; i < E; ++i) sq = fmaf(to_f(x.e[i]), to_f(x.e[i]), sq);
+            }
+#pragma unroll
+            for (int s = L / 2; s > 0; s >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, s);
+            big_v = fmaxf(big_v, sq);
+        }
+        __shared__ float part[3][kPreThreads / 32];
+        float m[3] = {sqrtf(big_do), big_d, sqrtf(big_v)};
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], s));
+            if (lane == 0) part[j][threadIdx.x >> 5] = m[j];
+        }
+        __syncthreads();
+        if (threadIdx.x < 3) {
+            float x = 0.f;
+            for (int i = 0; i < kPreThreads / 32; ++i) x = fmaxf(x, part[threadIdx.x][i]);
+            p.maxima[threadIdx.x * kPreBlocks + blockIdx.x] = x;
+        }
+    }
+}
+
+struct SumParams {
+    const float *part[3];  // [splits][n] each; null: nothing to add
+    void *out[3];
+    int64_t n[3];          // elements
+    int splits[3];
+    int type;              // of the gradients: 0 fp32, 1 bf16, 2 fp16
+};
+
+// Adds the splits of dk, dv and dq in order; four elements a thread.
+__global__ void __launch_bounds__(kSumThreads) bwd_sum_kernel(const SumParams p) {
+    const int j = blockIdx.y;
+    if (!p.part[j]) return;
+    const int64_t n4 = p.n[j] / 4;
+    const int64_t stride = (int64_t)gridDim.x * kSumThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x; i < n4; i += stride) {
+        const float4 *src = reinterpret_cast<const float4 *>(p.part[j]) + i;
+        float4 a = *src;
+        for (int s = 1; s < p.splits[j]; ++s) {
+            const float4 b = src[s * n4];
+            a.x += b.x;
+            a.y += b.y;
+            a.z += b.z;
+            a.w += b.w;
+        }
+        if (p.type == 0) {
+            reinterpret_cast<float4 *>(p.out[j])[i] = a;
+        } else {
+            uint2 w;
+            if (p.type == 1) {
+                *reinterpret_cast<__nv_bfloat162 *>(&w.x) = __floats2bfloat162_rn(a.x, a.y);
+                *reinterpret_cast<__nv_bfloat162 *>(&w.y) = __floats2bfloat162_rn(a.z, a.w);
+            } else {
+                *reinterpret_cast<__half2 *>(&w.x) = __floats2half2_rn(a.x, a.y);
+                *reinterpret_cast<__half2 *>(&w.y) = __floats2half2_rn(a.z, a.w);
+            }
+            reinterpret_cast<uint2 *>(p.out[j])[i] = w;
+        }
+    }
+}
+
+template <typename TD, typename TO, int D, bool kScale>
+int launch_stats(const PreParams &p, cudaStream_t stream) {
+    constexpr int R = 32 / (D * (int)sizeof(TD) / 16);
+    const int64_t warps = p.tiles * (kStatTile / R) + (kScale ? (p.v_rows + R - 1) / R : 0);
+    int64_t grid = (warps + kPreThreads / 32 - 1) / (kPreThreads / 32);
+    if (grid > kPreBlocks) grid = kPreBlocks;
+    bwd_stats_kernel<TD, TO, D, kScale><<<(unsigned)grid, kPreThreads, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+template <int D>
+int stats_16(const PreParams &p, int dtype, cudaStream_t stream) {
+    switch (dtype) {
+    case ATTN_BF16: return launch_stats<__nv_bfloat16, __nv_bfloat16, D, false>(p, stream);
+    case ATTN_BF16_OUT_F32: return launch_stats<__nv_bfloat16, float, D, false>(p, stream);
+    case ATTN_F16: return launch_stats<__half, __half, D, true>(p, stream);
+    default: return launch_stats<__half, float, D, true>(p, stream);
+    }
+}
+
+}  // namespace
+
+int launch_bwd(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream) {
+    uint8_t *ws = (uint8_t *)a.workspace;
+    const bool f16 = p.dtype == ATTN_F16 || p.dtype == ATTN_F16_OUT_F32;
+    PreParams r{};
+    r.o = a.o;
+    r.dout = a.dout;
+    r.v = a.v;
+    r.lse = a.lse;
+    r.dlse = a.dlse;
+    r.counter = (unsigned *)ws;
+    r.stats = (float *)(ws + plan.off_stats);
+    r.maxima = (float *)(ws + plan.off_max);
+    r.tiles_per_head = (p.Sq + kStatTile - 1) / kStatTile;
+    r.tiles = p.bh() * r.tiles_per_head;
+    r.v_rows = p.bh_kv() * p.Skv;
+    r.Sq = p.Sq;
+    r.add = f16 ? (float)kBwdP16Log2 : 0.f;
+    r.status = status_word_device_ptr();
+    if (!r.status) return ATTN_ERR_CUDA;
+    int st = ATTN_ERR_INVALID_ARG;
+    if (p.dtype == ATTN_F32) {
+        switch (p.d) {
+        case 16: st = launch_stats<float, float, 16, false>(r, stream); break;
+        case 32: st = launch_stats<float, float, 32, false>(r, stream); break;
+        case 64: st = launch_stats<float, float, 64, false>(r, stream); break;
+        case 128: st = launch_stats<float, float, 128, false>(r, stream); break;
+        }
+    } else if (p.d == 64 || p.d == 128) {
+        st = p.d == 64 ? stats_16<64>(r, p.dtype, stream) : stats_16<128>(r, p.dtype, stream);
+    }
+    if (st != ATTN_OK) return st;
+    st = p.dtype == ATTN_F32 ? launch_bwd_f32(a, p, plan, stream) : launch_bwd_tc(a, p, plan, stream);
+    if (st != ATTN_OK || (plan.ns_kv == 1 && plan.ns_q == 1)) return st;
+    SumParams s{};
+    int64_t most = 0;
+    auto add = [&](int j, const float *part, void *out, int64_t n, int splits) {
+        s.part[j] = part;
+        s.out[j] = out;
+        s.n[j] = n;
+        s.splits[j] = splits;
+        if (n > most) most = n;
+    };
+    if (plan.ns_kv > 1) {
+        const int64_t n = p.bh_kv() * p.Skv * p.d;
+        const float *kv = (const float *)(ws + plan.off_part_kv);
+        add(0, kv, a.dk, n, plan.ns_kv);
+        add(1, kv + (size_t)plan.ns_kv * n, a.dv, n, plan.ns_kv);
+    }
+    if (plan.ns_q > 1)
+        add(2, (const float *)(ws + plan.off_part_q), a.dq, p.bh() * p.Sq * p.d, plan.ns_q);
+    s.type = elem_bytes_out(p.dtype) == 4 ? 0 : f16 ? 2 : 1;
+    int64_t grid = (most / 4 + kSumThreads - 1) / kSumThreads;
+    if (grid > 8 * kBwdSms) grid = 8 * kBwdSms;
+    bwd_sum_kernel<<<dim3((unsigned)grid, 3), kSumThreads, 0, stream>>>(s);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // namespace attn

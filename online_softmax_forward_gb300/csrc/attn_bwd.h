@@ -1,0 +1,64 @@
+// attn_bwd.h -- what the kernels of the backward pass share: the arguments, the
+// plan of the work, and the layout of the workspace.
+//
+// From q, do [B, H, Sq, d], k, v [B, H_kv, Skv, d], o, lse of the forward pass
+// and (optionally) the gradient of the lse:
+//     P  = exp(scale q k^T - lse)        on the visible keys, recomputed
+//     D  = rowsum(o * do) - dlse         (the softmax's and the lse's share)
+//     dS = P * (do v^T - D)
+//     dq = scale dS k,   dk = scale dS^T q,   dv = P^T do
+// with dk and dv summed over the query heads that share a kv head.
+//
+// No sum is made by atomics, so results do not depend on the order in which
+// CTAs run.  The work is cut into units of two kinds, each of which owns its
+// outputs: a kv unit holds one tile of keys (k and v) and walks over the query
+// tiles of all heads that share it; a q unit holds one tile of queries (q and
+// do) and walks over the key tiles.  P and dP are therefore computed twice
+// (seven products of a tile instead of five), which costs less than summing dq
+// in global memory in a fixed order.  Where units are few and long, their
+// walks are cut into splits that leave fp32 partial sums in the workspace,
+// and a last kernel adds those in order.
+//
+// A first kernel writes what both kinds need of each query row: nl = -lse
+// log2(e) (-inf for a row that sees no key, so that its P is 0) and nd = -D,
+// as [B * H][query tiles of 128][2][128], rows behind Sq with nl = -inf, nd = 0.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "attn_internal.h"
+
+namespace attn {
+
+constexpr int kStatTile = 128;   // query rows of one block of row statistics
+constexpr int kBwdSms = 152;     // the splits are planned for this many SMs
+constexpr int kMaxBwdSplits = 64;
+constexpr int kBwdP16Log2 = 14;  // fp16: P is kept times 2^14, so that small weights stay normal numbers
+constexpr int kPreBlocks = 1216; // CTAs of the first kernel at most
+
+struct BwdPlan {
+    int tile;           // rows of a tile
+    int nq, nk;         // query and key tiles
+    int ns_kv, ns_q;    // splits of a kv unit and of a q unit
+    int64_t n_units;
+    size_t off_stats, off_max, off_part_kv, off_part_q, bytes;
+};
+
+struct BwdArgs {
+    const void *q, *k, *v, *o, *dout;
+    const float *lse, *dlse;
+    void *dq, *dk, *dv;
+    void *workspace;
+};
+
+// The plan follows from the sizes alone, so that the workspace does too.
+// False if the problem is too large to number.
+bool bwd_plan(const Problem &p, BwdPlan *plan);
+
+// The kernels in order: row statistics, gradients, sum of the splits.
+int launch_bwd(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream);
+int launch_bwd_tc(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream);
+int launch_bwd_f32(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream);
+
+}  // namespace attn

@@ -1,0 +1,783 @@
+// attn_bwd_tc.cu -- bf16/fp16 backward pass of attention on the sm_103a tensor
+// cores (attn_bwd.h has the formulas and the two kinds of units).
+//
+// Both kinds of units run through the same kernel, because they have the same
+// shape.  A unit holds two tiles X1, X2 of 128 rows and streams pairs of tiles
+// Y1, Y2 of 128 rows:
+//     kv unit: X1 = k, X2 = v;  Y1 = q, Y2 = do, over the query tiles
+//     q unit:  X1 = q, X2 = do; Y1 = k, Y2 = v,  over the key tiles
+// and for each step
+//     T1 = X1 Y1^T   (scores: P = exp2(scale log2(e) T1 + nl))
+//     T2 = X2 Y2^T   (dP:     dS = P (T2 + nd))
+//     A2 += dS Y1    (dk of a kv unit, dq of a q unit)
+//     A1 += P Y2     (dv; kv units only)
+// In a kv unit rows are keys, so that T1 and T2 come out as S^T and dP^T: P and
+// dS are then already the left operands of the sums and go back into tensor
+// memory where they came from, without a transposition and without touching
+// shared memory.  Only the row statistics run along the columns there.
+//
+//  * Persistent grid, one CTA per SM, 12 warps; units are claimed from a
+//    counter in the workspace, kv units of a group of heads first, longest
+//    first, so that the CTAs running at any time share the tiles of a few heads
+//    through L2.
+//  * Warp 8 (producer) streams the tiles with TMA (128-byte swizzle) into a ring,
+//    Y1 and Y2 of a step in turn, and the statistics of a kv unit's query tile
+//    beside them.
+//  * Warp 9 issues the tcgen05.mma (kind::f16, fp32 accumulate).  A kv unit's step
+//    is A1(i), T1(i+1), A2(i), T2(i+1): while the first two run, the other
+//    warps turn T2(i) into dS, while the last two run, T1(i+1) into P.  A q
+//    unit has no A1, and its place in tensor memory is a second buffer of T2:
+//    T1(i+1), T2(i+1) run before A2(i).
+//  * Warps 0-3 and 4-7: columns 0-63 and 64-127 of T1 and T2, one thread per row
+//    and half.  P stays in fp32 registers between the two; it is rounded to 16
+//    bits for A1 alone, and dS for A2 (as the tensor core takes 16-bit
+//    operands; the sums are fp32).  fp16: P is kept times 2^14, and dS times a
+//    power of two from the norms of do and v (attn_bwd.cu), undone at the end.
+//  * Tensor memory (512 columns): T1 [0,128), T2 [128,256), A2 [256,256+D),
+//    A1 or the second T2 from 384.  P and dS overwrite the first 32 columns
+//    of each half of T1 and T2.
+//  * Every mbarrier wait is bounded, as in the forward kernel.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <atomic>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_bwd.h"
+#include "sm100_ptx.cuh"
+#include "tc_common.cuh"
+#include "tensor_map.h"
+
+namespace attn {
+namespace {
+
+constexpr int kRows = 128;  // rows of every tile
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kThreads = 12 * 32;
+constexpr int kComputeThreads = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSchedRing = 4;
+constexpr int kSchedReaders = 9;  // issuer and 8 computing warps
+constexpr int kStatStages = 2;
+constexpr int kLaunchRegs = 168;
+constexpr int kComputeRegs = 224;
+constexpr int kOtherRegs = 56;
+static_assert(2 * 128 * kComputeRegs + 128 * kOtherRegs == kThreads * kLaunchRegs, "register split");
+static_assert(kStatTile == kRows, "statistics of a tile");
+
+constexpr uint32_t kColT1 = 0, kColT2 = 128, kColA2 = 256, kColA1 = 384, kColT2b = 384;
+
+template <int D>
+struct Cfg {
+    static_assert(D == 64 || D == 128, "head width");
+    static constexpr int kChunks = D / 64;
+    static constexpr int kChunkBytes = kRows * 128;  // one 64-channel column of a tile: 16 KB
+    static constexpr int kTileBytes = kChunks * kChunkBytes;
+    static constexpr int kSlots = D == 128 ? 5 : 8;  // ring of Y tiles
+    static constexpr int kOffX = 0;                  // X1, X2
+    static constexpr int kOffY = 2 * kTileBytes;
+    static constexpr int kOffStat = kOffY + kSlots * kTileBytes;
+    static constexpr int kStatBytes = 2 * kStatTile * 4;
+    static constexpr int kOffBar = kOffStat + kStatStages * kStatBytes;
+    static constexpr int kSmemBytes = kOffBar + 896;
+};
+constexpr int kMaxSlots = 8;
+
+struct Unit {
+    int kind;   // 0: kv unit, 1: q unit, -2: no more units
+    int zx, zy; // slice (batch, head) of X; of the first Y
+    int x0;     // first row of X
+    int y, n;   // first tile of Y, steps
+    int first;  // kv unit: the first query tile of each head
+    int split;
+};
+
+struct Bars {
+    uint64_t x_full[2], x_empty[2];
+    uint64_t y_full[kMaxSlots], y_empty[kMaxSlots];
+    uint64_t st_full[kStatStages], st_empty[kStatStages];
+    uint64_t t1_full, p_full;      // T1 computed; T1 read (q unit) or P written (kv unit)
+    uint64_t t2_full[2], ds_full[2];  // T2 computed; dS written (of each buffer)
+    uint64_t acc_full, acc_empty;
+    uint64_t mma_done;
+    uint64_t sched_full[kSchedRing], sched_empty[kSchedRing];
+    Unit sched_unit[kSchedRing];
+    uint32_t tmem_base;
+    int abort_flag;
+    float ds_scale;  // fp16: 2^e of dS over that of P
+};
+static_assert(sizeof(Bars) <= 896, "barrier block");
+
+struct Params {
+    const float *stats;
+    const float *maxima;
+    unsigned *counter;
+    void *dk, *dv, *dq;               // gradients, or the splits' partial sums
+    int BH, BHk, group, Sq, Skv, causal;
+    int nq, nk, ns_kv, ns_q;
+    int hg;       // kv slices per schedule group
+    int n_units;
+    int kv_f32, q_f32;  // fp32 output of dk and dv, of dq
+    float scale_log2, scale;
+    int *status;
+    unsigned long long timeout_ns;
+};
+
+// Unit u of the schedule: groups of hg kv slices; in a group first the kv units,
+// then the q units, longest first (causal: first key tiles, last query tiles).
+__device__ __forceinline__ Unit decode_unit(int u, const Params &p) {
+    Unit r;
+    const int a_head = p.nk * p.ns_kv, b_head = p.group * p.nq * p.ns_q;
+    const int per_group = p.hg * (a_head + b_head);
+    const int g = u / per_group;
+    int rem = u - g * per_group;
+    const int heads = min(p.hg, p.BHk - g * p.hg);
+    const int off = p.Skv - p.Sq;
+    if (rem < heads * a_head) {
+        const int width = heads * p.ns_kv;
+        const int tile = rem / width;
+        rem -= tile * width;
+        const int head = rem / p.ns_kv;
+        r.split = rem - head * p.ns_kv;
+        r.kind = 0;
+        r.zx = g * p.hg + head;
+        r.x0 = tile * kRows;
+        r.first = p.causal ? max(0, r.x0 - off) / kRows : 0;
+        const int per = p.nq - r.first;  // query tiles of a head that see the tile
+        const int64_t steps = (int64_t)per * p.group;
+        const int t0 = (int)(steps * r.split / p.ns_kv), t1 = (int)(steps * (r.split + 1) / p.ns_kv);
+        r.n = t1 - t0;
+        const int skip = t0 / per;
+        r.zy = r.zx * p.group + skip;
+        r.y = r.first + t0 - skip * per;
+    } else {
+        rem -= heads * a_head;
+        const int width = heads * p.group * p.ns_q;
+        int tile = rem / width;
+        rem -= tile * width;
+        const int head = rem / p.ns_q;
+        r.split = rem - head * p.ns_q;
+        if (p.causal) tile = p.nq - 1 - tile;
+        r.kind = 1;
+        r.zx = g * p.hg * p.group + head;
+        r.zy = r.zx / p.group;
+        r.x0 = tile * kRows;
+        r.first = 0;
+        const int end = p.causal ? min(p.Skv, min(r.x0 + kRows, p.Sq) + off) : p.Skv;
+        const int steps = end > 0 ? (end + kRows - 1) / kRows : 0;
+        const int t0 = (int)((int64_t)steps * r.split / p.ns_q), t1 = (int)((int64_t)steps * (r.split + 1) / p.ns_q);
+        r.y = t0;
+        r.n = t1 - t0;
+    }
+    return r;
+}
+
+// The next step's tile: key tiles in order; query tiles in order, head by head.
+__device__ __forceinline__ void advance(const Unit &w, const Params &p, int &y, int &zy) {
+    ++y;
+    if (w.kind == 0 && y == p.nq) {
+        y = w.first;
+        ++zy;
+    }
+}
+
+template <bool kBF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (kBF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    } else {
+        __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+}
+
+__device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+// Untiled bulk copy into shared memory (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                   const Params p) {
+    using C = Cfg<D>;
+    constexpr int kSlots = C::kSlots;
+    // the tiles' swizzle needs 1024-byte alignment, which this declaration asks
+    // for: there is no room to align by hand at D = 128
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Bars *bars = reinterpret_cast<Bars *>(smem + C::kOffBar);
+    const uint32_t sX = ptx::smem_addr(smem + C::kOffX);
+    const uint32_t sY = ptx::smem_addr(smem + C::kOffY);
+    const uint32_t sStat = ptx::smem_addr(smem + C::kOffStat);
+    if (sX & 1023) {  // never taken: the address is the same for every thread
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+        return;
+    }
+
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
+    const Watch watch{&bars->abort_flag, p.status, p.timeout_ns};
+    auto bar = [&](uint64_t &b) { return ptx::smem_addr(&b); };
+
+    // ---------------------------------------------------------------- setup
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(bar(bars->x_full[t]), 1);
+            ptx::mbar_init(bar(bars->x_empty[t]), 1);
+            ptx::mbar_init(bar(bars->t2_full[t]), 1);
+            ptx::mbar_init(bar(bars->ds_full[t]), kComputeThreads);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            ptx::mbar_init(bar(bars->y_full[s]), 1);
+            ptx::mbar_init(bar(bars->y_empty[s]), 1);
+        }
+        for (int s = 0; s < kStatStages; ++s) {
+            ptx::mbar_init(bar(bars->st_full[s]), 1);
+            ptx::mbar_init(bar(bars->st_empty[s]), kComputeThreads);
+        }
+        ptx::mbar_init(bar(bars->t1_full), 1);
+        ptx::mbar_init(bar(bars->p_full), kComputeThreads);
+        ptx::mbar_init(bar(bars->acc_full), 1);
+        ptx::mbar_init(bar(bars->acc_empty), kComputeThreads);
+        ptx::mbar_init(bar(bars->mma_done), 1);
+        for (int s = 0; s < kSchedRing; ++s) {
+            ptx::mbar_init(bar(bars->sched_full[s]), 1);
+            ptx::mbar_init(bar(bars->sched_empty[s]), kSchedReaders);
+        }
+        bars->abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+        ptx::prefetch_tmap(&tm_v);
+        ptx::prefetch_tmap(&tm_do);
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(ptx::smem_addr(&bars->tmem_base), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    if constexpr (!kBF16) {
+        // |dS| <= max |do| max |v| + max |D|: the exponent that brings it to 2^14 at most
+        if (warp == 11) {
+            float m[3] = {0.f, 0.f, 0.f};
+            const int n = (int)p.counter[1];
+            for (int j = 0; j < 3; ++j) {
+                for (int i = lane; i < min(n, kPreBlocks); i += 32) m[j] = fmaxf(m[j], p.maxima[j * kPreBlocks + i]);
+                for (int s = 16; s > 0; s >>= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], s));
+            }
+            const float most = fmaf(m[0], m[2], m[1]);
+            int e = 0;
+            if (most > 0.f && most < INFINITY) e = max(-100, min(100, 13 - ilogbf(most)));
+            if (lane == 0) bars->ds_scale = ldexpf(1.f, e - kBwdP16Log2);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
+
+    // The producer's k-th claim for a consumer warp; false if the CTA is aborting.
+    auto next_unit = [&](uint32_t &k, Unit &w) {
+        const uint32_t s = k % kSchedRing;
+        if (!__all_sync(0xffffffffu, watch.wait(bar(bars->sched_full[s]), (k / kSchedRing) & 1)))
+            return false;
+        const volatile Unit *su = &bars->sched_unit[s];
+        w.kind = su->kind;
+        w.zx = su->zx;
+        w.zy = su->zy;
+        w.x0 = su->x0;
+        w.y = su->y;
+        w.n = su->n;
+        w.first = su->first;
+        w.split = su->split;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(bars->sched_empty[s]));
+        ++k;
+        return true;
+    };
+
+    if (warp == kProducerWarp) {
+        // ------------------------------------------------------------ producer
+        ptx::setmaxnreg_dec<kOtherRegs>();
+        if (lane == 0) {
+            uint32_t pos = 0, xn[2] = {0, 0}, sn = 0;  // tiles of Y, of each X, and statistics loaded
+            bool ok = true;
+            auto stop = [&]() {
+                *watch.abort_flag = 1;
+                return false;
+            };
+            auto tile = [&](uint32_t dst, uint64_t &full, const CUtensorMap *tm, int row, int z, int rows, int slices) {
+                if (!in_bounds(row >= 0 && row < rows && z >= 0 && z < slices, p.status)) return stop();
+                ptx::mbar_arrive_expect_tx(bar(full), C::kTileBytes);
+                for (int c = 0; c < C::kChunks; ++c)
+                    ptx::tma_load_3d(dst + c * C::kChunkBytes, tm, bar(full), c * 64, row, z);
+                return true;
+            };
+            auto load_x = [&](int t, const Unit &w) {
+                if (!watch.wait(bar(bars->x_empty[t]), (xn[t] & 1) ^ 1)) return false;
+                const CUtensorMap *tm = w.kind == 0 ? (t ? &tm_v : &tm_k) : (t ? &tm_do : &tm_q);
+                if (!tile(sX + t * C::kTileBytes, bars->x_full[t], tm, w.x0, w.zx,
+                          w.kind == 0 ? p.Skv : p.Sq, w.kind == 0 ? p.BHk : p.BH))
+                    return false;
+                ++xn[t];
+                return true;
+            };
+            auto load_y = [&](int t, const Unit &w, int y, int zy) {
+                const int s = pos % kSlots;
+                if (!watch.wait(bar(bars->y_empty[s]), ((pos / kSlots) & 1) ^ 1)) return false;
+                const CUtensorMap *tm = w.kind == 0 ? (t ? &tm_do : &tm_q) : (t ? &tm_v : &tm_k);
+                if (!tile(sY + s * C::kTileBytes, bars->y_full[s], tm, y * kRows, zy,
+                          w.kind == 0 ? p.Sq : p.Skv, w.kind == 0 ? p.BH : p.BHk))
+                    return false;
+                ++pos;
+                return true;
+            };
+            auto load_stat = [&](int y, int zy) {
+                const int s = sn % kStatStages;
+                if (!watch.wait(bar(bars->st_empty[s]), ((sn / kStatStages) & 1) ^ 1)) return false;
+                if (!in_bounds(y >= 0 && y < p.nq && zy >= 0 && zy < p.BH, p.status)) return stop();
+                ptx::mbar_arrive_expect_tx(bar(bars->st_full[s]), C::kStatBytes);
+                bulk_load(sStat + s * C::kStatBytes, p.stats + ((size_t)zy * p.nq + y) * 2 * kStatTile,
+                          C::kStatBytes, bar(bars->st_full[s]));
+                ++sn;
+                return true;
+            };
+            unsigned claim = atomicAdd(p.counter, 1u);
+            for (uint32_t k = 0; ok; ++k) {
+                const uint32_t slot = k % kSchedRing;
+                if (!watch.wait(bar(bars->sched_empty[slot]), ((k / kSchedRing) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                Unit w{-2, 0, 0, 0, 0, 0, 0, 0};
+                if (claim < (unsigned)p.n_units) w = decode_unit((int)claim, p);
+                volatile Unit *su = &bars->sched_unit[slot];
+                su->kind = w.kind;
+                su->zx = w.zx;
+                su->zy = w.zy;
+                su->x0 = w.x0;
+                su->y = w.y;
+                su->n = w.n;
+                su->first = w.first;
+                su->split = w.split;
+                ptx::mbar_arrive(bar(bars->sched_full[slot]));
+                if (w.kind < 0) break;
+                int y = w.y, zy = w.zy;
+                for (int i = 0; i < w.n && ok; ++i) {
+                    if (i == 0) ok = load_x(0, w);
+                    ok = ok && load_y(0, w, y, zy);
+                    if (w.kind == 0) ok = ok && load_stat(y, zy);
+                    if (i == 0) ok = ok && load_x(1, w);
+                    ok = ok && load_y(1, w, y, zy);
+                    advance(w, p, y, zy);
+                }
+                if (ok) claim = atomicAdd(p.counter, 1u);
+            }
+            // teardown: every load this thread issued has landed
+            for (uint32_t s = 0; s < (uint32_t)kSlots && s < pos; ++s) {
+                const uint32_t last = s + ((pos - 1 - s) / kSlots) * kSlots;
+                watch.drain(bar(bars->y_full[s]), (last / kSlots) & 1);
+            }
+            for (uint32_t s = 0; s < (uint32_t)kStatStages && s < sn; ++s) {
+                const uint32_t last = s + ((sn - 1 - s) / kStatStages) * kStatStages;
+                watch.drain(bar(bars->st_full[s]), (last / kStatStages) & 1);
+            }
+            for (int t = 0; t < 2; ++t)
+                if (xn[t] > 0) watch.drain(bar(bars->x_full[t]), (xn[t] - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        ptx::setmaxnreg_dec<kOtherRegs>();
+        auto wait_all = [&](uint64_t &b, uint32_t parity) {
+            return __all_sync(0xffffffffu, watch.wait(bar(b), parity));
+        };
+        constexpr uint32_t kIdescT = idesc_f16(kBF16, kRows, kRows, false);
+        constexpr uint32_t kIdescA = idesc_f16(kBF16, kRows, D, true);
+        const uint64_t dx = sdesc(sX, 16, 1024);
+        const uint64_t dyk = sdesc(sY, 16, 1024);              // Y as [rows of the result's columns][channels]
+        const uint64_t dyn = sdesc(sY, C::kChunkBytes, 1024);  // Y as [summed rows][channels of the result]
+        uint32_t pos = 0;             // ring position of the unit's Y1(0)
+        uint32_t xn = 0, un = 0;      // units begun, units whose sums were begun
+        uint32_t pn = 0, dn[2] = {0, 0};  // p_full and ds_full phases waited for
+        bool ok = true;
+        auto slot_full = [&](uint32_t at) { return wait_all(bars->y_full[at % kSlots], (at / kSlots) & 1); };
+        auto free_slot = [&](uint32_t at) { ptx::mma_commit_warp(bar(bars->y_empty[at % kSlots])); };
+        // T = X Y^T, Y at ring position `at`
+        auto issue_t = [&](uint32_t col, int x, uint32_t at) {
+            const uint64_t da = dx + (uint64_t)((x * C::kTileBytes) >> 4);
+            const uint64_t db = dyk + (uint64_t)(((at % kSlots) * C::kTileBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
+                ptx::mma_ss_warp(tmem + col, da + o, db + o, kIdescT, kk > 0 ? 1u : 0u);
+            }
+        };
+        // A += (16-bit rows at column `col`) Y
+        auto issue_a = [&](uint32_t acc, uint32_t col, uint32_t at, bool add) {
+            const uint64_t db = dyn + (uint64_t)(((at % kSlots) * C::kTileBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kRows / 16; ++kk)
+                ptx::mma_ts_warp(tmem + acc, tmem + col + (kk >> 2) * 64 + (kk & 3) * 8,
+                                 db + (uint64_t)((kk * 16 * 128) >> 4), kIdescA, (add || kk > 0) ? 1u : 0u);
+        };
+        for (uint32_t k = 0; ok;) {
+            Unit w;
+            if (!next_unit(k, w)) { ok = false; break; }
+            if (w.kind < 0) break;
+            const int n = w.n;
+            if (n == 0) continue;
+            const bool kv = w.kind == 0;
+            bool acc_free = false;
+            auto need_acc = [&]() {  // the previous unit's sums have been read
+                if (!acc_free && !wait_all(bars->acc_empty, (un & 1) ^ 1)) return false;
+                acc_free = true;
+                return true;
+            };
+            // T1 and T2 of step i
+            auto t1 = [&](int i) {
+                if (!slot_full(pos + 2 * i)) return false;
+                ptx::tc_fence_after();
+                issue_t(kColT1, 0, pos + 2 * i);
+                ptx::mma_commit_warp(bar(bars->t1_full));
+                if (i == n - 1) ptx::mma_commit_warp(bar(bars->x_empty[0]));
+                return true;
+            };
+            auto t2 = [&](int i) {
+                const int buf = kv ? 0 : i & 1;
+                if (!slot_full(pos + 2 * i + 1)) return false;
+                if (buf == 1 && !need_acc()) return false;
+                ptx::tc_fence_after();
+                issue_t(buf ? kColT2b : kColT2, 1, pos + 2 * i + 1);
+                ptx::mma_commit_warp(bar(bars->t2_full[buf]));
+                if (!kv) free_slot(pos + 2 * i + 1);
+                if (i == n - 1) ptx::mma_commit_warp(bar(bars->x_empty[1]));
+                return true;
+            };
+            ok = wait_all(bars->x_full[0], xn & 1) && t1(0) && wait_all(bars->x_full[1], xn & 1) && t2(0);
+            ++xn;
+            for (int i = 0; i < n && ok; ++i) {
+                // P(i) is written, or T1(i) read
+                if (!wait_all(bars->p_full, pn & 1)) { ok = false; break; }
+                ++pn;
+                if (kv) {
+                    if (!need_acc()) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    issue_a(kColA1, kColT1, pos + 2 * i + 1, i > 0);
+                    free_slot(pos + 2 * i + 1);
+                }
+                if (i + 1 < n) {
+                    ok = t1(i + 1);
+                    if (ok && !kv) ok = t2(i + 1);
+                    if (!ok) break;
+                }
+                const int buf = kv ? 0 : i & 1;
+                if (!wait_all(bars->ds_full[buf], (buf ? dn[1] : dn[0]) & 1) || !need_acc()) { ok = false; break; }
+                if (buf) ++dn[1]; else ++dn[0];
+                ptx::tc_fence_after();
+                issue_a(kColA2, buf ? kColT2b : kColT2, pos + 2 * i, i > 0);
+                free_slot(pos + 2 * i);
+                if (kv && i + 1 < n) ok = t2(i + 1);
+            }
+            if (!ok) break;
+            ptx::mma_commit_warp(bar(bars->acc_full));
+            ++un;
+            pos += 2 * n;
+        }
+        ptx::mma_commit_warp(bar(bars->mma_done));
+        watch.drain(bar(bars->mma_done), 0);
+        __syncwarp();
+    } else if (warp < kProducerWarp) {
+        // ------------------------------------------------------------ P, dS, sums out
+        ptx::setmaxnreg_inc<kComputeRegs>();
+        const int half = warp >> 2;  // columns [64 half, 64 half + 64) of T1 and T2
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tl = tmem + lane_base;
+        const float2 sc = make_float2(p.scale_log2, p.scale_log2);
+        const int off = p.Skv - p.Sq;
+        const float ds_scale = kBF16 ? 1.f : bars->ds_scale;
+        uint32_t n1 = 0, n2[2] = {0, 0}, sn = 0, an = 0;
+        bool ok = true;
+
+        for (uint32_t k = 0; ok;) {
+            Unit w;
+            if (!next_unit(k, w)) { ok = false; break; }
+            if (w.kind < 0) break;
+            const bool kv = w.kind == 0;
+            const int row = w.x0 + r;
+            float nl = 0.f, nd = 0.f;  // q unit: of this thread's row
+            if (!kv) {
+                const float *st = p.stats + ((size_t)w.zx * p.nq + w.x0 / kRows) * 2 * kStatTile + r;
+                if (in_bounds(w.zx < p.BH && w.x0 / kRows < p.nq, p.status)) {
+                    nl = st[0];
+                    nd = st[kStatTile];
+                }
+            }
+            int y = w.y;
+            int zy = w.zy;
+            for (int i = 0; i < w.n; ++i) {
+                const int y0 = y * kRows;
+                const int stage = sn % kStatStages;
+                const uint32_t st = sStat + stage * C::kStatBytes + half * 256;
+                bool got = watch.wait(bar(bars->t1_full), n1 & 1);
+                ++n1;
+                if (kv) got = got && watch.wait(bar(bars->st_full[stage]), (sn / kStatStages) & 1);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                ptx::tc_fence_after();
+                uint32_t a[32], b[32];
+                float pr[64];
+                const uint32_t tT1 = tl + kColT1 + half * 64;
+                ptx::tmem_ld32(tT1, a);
+                ptx::tmem_ld32(tT1 + 32, b);
+                ptx::tmem_wait_ld();
+                reg_fence(a);
+                reg_fence(b);
+                // columns visible to this row: [lo, hi)
+                const int lo = (kv && p.causal) ? row - off - y0 : 0;
+                const int hi = kv ? kRows : min(p.Skv, p.causal ? row + off + 1 : p.Skv) - y0;
+                const bool masked = kv ? (p.causal && w.x0 + kRows - 1 > y0 + off)
+                                       : y0 + kRows > min(p.Skv, p.causal ? w.x0 + off + 1 : p.Skv);
+                if (!kv) {  // T1 is read: the next one may be written
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(bar(bars->p_full));
+                }
+#pragma unroll
+                for (int j = 0; j < 64; j += 4) {
+                    const uint32_t *s = j < 32 ? a + j : b + (j - 32);
+                    float4 l = make_float4(nl, nl, nl, nl);
+                    if (kv) l = ld_shared_v4(st + j * 4);
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), sc, make_float2(l.x, l.y));
+                    const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), sc, make_float2(l.z, l.w));
+                    pr[j] = ptx::ex2_approx(x.x);
+                    pr[j + 1] = ptx::ex2_approx(x.y);
+                    pr[j + 2] = ptx::ex2_approx(z.x);
+                    pr[j + 3] = ptx::ex2_approx(z.y);
+                }
+                if (masked) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (half * 64 + j < lo || half * 64 + j >= hi) pr[j] = 0.f;
+                }
+                if (kv) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) pk[j] = pack2<kBF16>(pr[2 * j], pr[2 * j + 1]);
+                    ptx::tmem_st32(tT1, pk);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(bar(bars->p_full));
+                }
+                const int buf = kv ? 0 : i & 1;
+                got = watch.wait(bar(bars->t2_full[buf]), (buf ? n2[1] : n2[0]) & 1);
+                if (buf) ++n2[1]; else ++n2[0];
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                ptx::tc_fence_after();
+                const uint32_t tT2 = tl + (buf ? kColT2b : kColT2) + half * 64;
+                ptx::tmem_ld32(tT2, a);
+                ptx::tmem_ld32(tT2 + 32, b);
+                ptx::tmem_wait_ld();
+                reg_fence(a);
+                reg_fence(b);
+                uint32_t pk[32];
+#pragma unroll
+                for (int j = 0; j < 64; j += 4) {
+                    const uint32_t *s = j < 32 ? a + j : b + (j - 32);
+                    float4 l = make_float4(nd, nd, nd, nd);
+                    if (kv) l = ld_shared_v4(st + kStatTile * 4 + j * 4);
+                    float2 x = __fadd2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), make_float2(l.x, l.y));
+                    float2 z = __fadd2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), make_float2(l.z, l.w));
+                    if constexpr (!kBF16) {
+                        x = __fmul2_rn(x, make_float2(ds_scale, ds_scale));
+                        z = __fmul2_rn(z, make_float2(ds_scale, ds_scale));
+                    }
+                    x = __fmul2_rn(x, make_float2(pr[j], pr[j + 1]));
+                    z = __fmul2_rn(z, make_float2(pr[j + 2], pr[j + 3]));
+                    if (masked) {  // what a masked place holds does not matter
+                        const int c = half * 64 + j;
+                        if (c < lo || c >= hi) x.x = 0.f;
+                        if (c + 1 < lo || c + 1 >= hi) x.y = 0.f;
+                        if (c + 2 < lo || c + 2 >= hi) z.x = 0.f;
+                        if (c + 3 < lo || c + 3 >= hi) z.y = 0.f;
+                    }
+                    pk[j / 2] = pack2<kBF16>(x.x, x.y);
+                    pk[j / 2 + 1] = pack2<kBF16>(z.x, z.y);
+                }
+                ptx::tmem_st32(tT2, pk);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(bar(bars->ds_full[buf]));
+                if (kv) {
+                    ptx::mbar_arrive(bar(bars->st_empty[stage]));
+                    ++sn;
+                }
+                advance(w, p, y, zy);
+            }
+            if (!ok) break;
+
+            // ---- the unit's sums: dk and dv, or dq
+            if (w.n > 0) {
+                const bool got = watch.wait(bar(bars->acc_full), an & 1);
+                ++an;
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                ptx::tc_fence_after();
+            }
+            const int rows = kv ? p.Skv : p.Sq;
+            const int64_t slices = kv ? p.BHk : p.BH;
+            const bool f32 = kv ? p.kv_f32 : p.q_f32;
+            const size_t part = (size_t)w.split * slices * rows;  // rows of the splits before
+            const size_t extent = (size_t)slices * rows * (kv ? p.ns_kv : p.ns_q) * D;
+            const size_t at = (part + (size_t)w.zx * rows + row) * D + half * (D / 2);
+#pragma unroll 1
+            for (int m = kv ? 0 : 1; m < 2; ++m) {  // 0: A1 (dv), 1: A2 (dk or dq)
+                void *dst = m == 0 ? p.dv : kv ? p.dk : p.dq;
+                const float f = m == 0 ? (kBF16 ? 1.f : 1.f / (1 << kBwdP16Log2))
+                                       : (kBF16 ? p.scale : p.scale / (ds_scale * (1 << kBwdP16Log2)));
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    if (w.n > 0) {
+                        ptx::tmem_ld32(tl + (m == 0 ? kColA1 : kColA2) + half * (D / 2) + c * 32, o);
+                        ptx::tmem_wait_ld();
+                        reg_fence(o);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0u;
+                    }
+                    const size_t g = at + c * 32;
+                    if (row >= rows || !in_bounds(g + 32 <= extent, p.status)) continue;
+                    if (f32) {
+                        float4 *d4 = reinterpret_cast<float4 *>(reinterpret_cast<float *>(dst) + g);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            d4[i] = make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                                                __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+                    } else {
+                        uint4 *d4 = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(dst) + g);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint4 v;
+                            v.x = pack2<kBF16>(__uint_as_float(o[8 * i]) * f, __uint_as_float(o[8 * i + 1]) * f);
+                            v.y = pack2<kBF16>(__uint_as_float(o[8 * i + 2]) * f, __uint_as_float(o[8 * i + 3]) * f);
+                            v.z = pack2<kBF16>(__uint_as_float(o[8 * i + 4]) * f, __uint_as_float(o[8 * i + 5]) * f);
+                            v.w = pack2<kBF16>(__uint_as_float(o[8 * i + 6]) * f, __uint_as_float(o[8 * i + 7]) * f);
+                            d4[i] = v;
+                        }
+                    }
+                }
+            }
+            if (w.n > 0) {
+                __syncwarp();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(bar(bars->acc_empty));
+            }
+        }
+    } else {
+        // warps 10 and 11 only give up their registers
+        ptx::setmaxnreg_dec<kOtherRegs>();
+    }
+
+    // ---------------------------------------------------------------- teardown
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D, bool kBF16>
+int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
+    using C = Cfg<D>;
+    CUtensorMap tq, tk, tv, td;
+    if (!make_tile_map(&tq, a.q, kBF16, D, pr.Sq, pr.bh()) || !make_tile_map(&tk, a.k, kBF16, D, pr.Skv, pr.bh_kv()) ||
+        !make_tile_map(&tv, a.v, kBF16, D, pr.Skv, pr.bh_kv()) || !make_tile_map(&td, a.dout, kBF16, D, pr.Sq, pr.bh()))
+        return ATTN_ERR_CUDA;
+    uint8_t *ws = (uint8_t *)a.workspace;
+    Params p{};
+    p.stats = (const float *)(ws + plan.off_stats);
+    p.maxima = (const float *)(ws + plan.off_max);
+    p.counter = (unsigned *)ws;
+    p.BH = (int)pr.bh();
+    p.BHk = (int)pr.bh_kv();
+    p.group = pr.group;
+    p.Sq = pr.Sq;
+    p.Skv = pr.Skv;
+    p.causal = pr.causal;
+    p.nq = plan.nq;
+    p.nk = plan.nk;
+    p.ns_kv = plan.ns_kv;
+    p.ns_q = plan.ns_q;
+    p.n_units = (int)plan.n_units;
+    p.scale_log2 = pr.scale * 1.4426950408889634f;
+    p.scale = pr.scale;
+    const int out_f32 = elem_bytes_out(pr.dtype) == 4;
+    p.kv_f32 = out_f32 || plan.ns_kv > 1;
+    p.q_f32 = out_f32 || plan.ns_q > 1;
+    float *part_kv = (float *)(ws + plan.off_part_kv);
+    p.dk = plan.ns_kv > 1 ? part_kv : a.dk;
+    p.dv = plan.ns_kv > 1 ? part_kv + (size_t)plan.ns_kv * pr.bh_kv() * pr.Skv * D : a.dv;
+    p.dq = plan.ns_q > 1 ? (void *)(ws + plan.off_part_q) : a.dq;
+    const int sms = device_sm_count();
+    p.status = status_word_device_ptr();
+    if (sms <= 0 || !p.status) return ATTN_ERR_CUDA;
+    {
+        // kv slices per group: about one and a half rounds of units, as equal groups where
+        // that is possible; all slices otherwise, unless their tiles exceed what L2 holds
+        const int64_t units = (int64_t)plan.nk * plan.ns_kv + (int64_t)pr.group * plan.nq * plan.ns_q;
+        const int64_t h0 = (3 * sms / 2 + units - 1) / units;
+        int64_t hg = h0 < 1 ? 1 : h0;
+        while (hg < p.BHk && p.BHk % hg != 0) ++hg;
+        const int64_t bytes = 4LL * D * (pr.bh() * pr.Sq + pr.bh_kv() * pr.Skv);
+        if (hg >= p.BHk && bytes > (96LL << 20)) hg = h0;
+        if (hg > p.BHk) hg = p.BHk;
+        p.hg = (int)hg;
+    }
+    p.timeout_ns = watchdog_ns();
+    auto kern = attn_bwd_tc_kernel<D, kBF16>;
+    // setmaxnreg needs exactly the registers it was planned for (see the forward kernel)
+    static std::atomic<int> regs_ok{-1};
+    int ok = regs_ok.load(std::memory_order_relaxed);
+    if (ok < 0) {
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return ATTN_ERR_UNSUPPORTED_DEVICE;
+        ok = (fa.numRegs == kLaunchRegs && fa.maxThreadsPerBlock >= kThreads) ? 1 : 0;
+        regs_ok.store(ok, std::memory_order_relaxed);
+    }
+    if (!ok) return ATTN_ERR_LAUNCH;
+    if (!set_smem_limit_once(reinterpret_cast<const void *>(kern), C::kSmemBytes)) return ATTN_ERR_LAUNCH;
+    const int grid = (int)(plan.n_units < sms ? plan.n_units : sms);
+    kern<<<grid, kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, td, p);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaErrorNoKernelImageForDevice || e == cudaErrorInvalidDeviceFunction)
+        return ATTN_ERR_UNSUPPORTED_DEVICE;
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int launch_bwd_tc(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream) {
+    const bool bf16 = p.dtype == ATTN_BF16 || p.dtype == ATTN_BF16_OUT_F32;
+    if (p.d == 128)
+        return bf16 ? launch_typed<128, true>(a, p, plan, stream) : launch_typed<128, false>(a, p, plan, stream);
+    if (p.d == 64)
+        return bf16 ? launch_typed<64, true>(a, p, plan, stream) : launch_typed<64, false>(a, p, plan, stream);
+    return ATTN_ERR_INVALID_ARG;
+}
+
+}  // namespace attn

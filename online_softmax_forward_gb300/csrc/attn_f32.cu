@@ -289,7 +289,7 @@ template <int D, int KS, int NS>
 __global__ void __launch_bounds__(KS * kWG, 1)
 attn_f32_tiled_kernel(const float *__restrict__ q, const float *__restrict__ k,
                       const float *__restrict__ v, float *__restrict__ o,
-                      float *__restrict__ lse, int BH, int Sq, int Skv, int causal,
+                      float *__restrict__ lse, int BH, int group, int Sq, int Skv, int causal,
                       float scale_log2, int nqb, int *status) {
     using C = TiledCfg<D, KS, NS>;
     constexpr int LD = C::kLd, W = C::kW, NC = C::kNC;
@@ -308,8 +308,9 @@ attn_f32_tiled_kernel(const float *__restrict__ q, const float *__restrict__ k,
     const int off = Skv - Sq;  // causal: key j visible to query i iff j <= i + off
     if (!in_bounds(bh < BH, status)) return;  // the whole block: bh is block-uniform
     const float *qg = q + (size_t)bh * Sq * D;
-    const float *kg = k + (size_t)bh * Skv * D;
-    const float *vg = v + (size_t)bh * Skv * D;
+    const size_t head0 = (size_t)((unsigned)bh / (unsigned)group) * Skv * D;  // group query heads share a kv head
+    const float *kg = k + head0;
+    const float *vg = v + head0;
 
     // keys visible to each of this thread's rows: [0, lim[i])
     int lim[4];
@@ -607,7 +608,7 @@ static_assert(kSW * kSQ * 64 + 2 * kSW * kSQ <= kSW * kSWarpFloats, "state must 
 __global__ void __launch_bounds__(kSW * 32, 1)
 attn_f32_keysplit_kernel(const float *__restrict__ q, const float *__restrict__ k,
                          const float *__restrict__ v, float *__restrict__ o,
-                         float *__restrict__ lse, int BH, int Sq, int Skv, int causal,
+                         float *__restrict__ lse, int BH, int group, int Sq, int Skv, int causal,
                          float scale_log2, int nqb, int *status) {
     constexpr int D = 64;
     extern __shared__ __align__(16) float sm[];
@@ -624,8 +625,9 @@ attn_f32_keysplit_kernel(const float *__restrict__ q, const float *__restrict__ 
     const int off = Skv - Sq;  // causal: key j visible to query i iff j <= i + off
     if (!in_bounds(bh < BH, status)) return;  // block-uniform
     const float *qg = q + (size_t)bh * Sq * D;
-    const float *kgp = k + (size_t)bh * Skv * D;
-    const float *vg = v + (size_t)bh * Skv * D;
+    const size_t head0 = (size_t)((unsigned)bh / (unsigned)group) * Skv * D;  // group query heads share a kv head
+    const float *kgp = k + head0;
+    const float *vg = v + head0;
 
     int lim[8];  // keys visible to row rg + 4i: [0, lim[i])
 #pragma unroll
@@ -824,7 +826,7 @@ int launch_keysplit(const float *q, const float *k, const float *v, float *o, fl
     int *status = status_word_device_ptr();
     if (!status) return ATTN_ERR_CUDA;
     attn_f32_keysplit_kernel<<<(unsigned)grid, kSW * 32, kSSmemBytes, stream>>>(
-        q, k, v, o, lse, (int)p.bh(), p.Sq, p.Skv, p.causal, p.scale * 1.4426950408889634f, nqb,
+        q, k, v, o, lse, (int)p.bh(), p.group, p.Sq, p.Skv, p.causal, p.scale * 1.4426950408889634f, nqb,
         status);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
@@ -839,7 +841,7 @@ int launch_tiled_ks(const float *q, const float *k, const float *v, float *o, fl
     int *status = status_word_device_ptr();
     if (!status) return ATTN_ERR_CUDA;
     attn_f32_tiled_kernel<D, KS, NS><<<(unsigned)grid, KS * kWG, smem, stream>>>(
-        q, k, v, o, lse, (int)p.bh(), p.Sq, p.Skv, p.causal, p.scale * 1.4426950408889634f, nqb,
+        q, k, v, o, lse, (int)p.bh(), p.group, p.Sq, p.Skv, p.causal, p.scale * 1.4426950408889634f, nqb,
         status);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }

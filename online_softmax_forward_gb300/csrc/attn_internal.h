@@ -48,7 +48,9 @@ struct Problem {
     int B, H, Sq, Skv, d, causal;
     float scale;  // resolved (> 0)
     int dtype;
+    int group = 1;  // query heads that share a kv head (attn_fwd: 1)
     int64_t bh() const { return (int64_t)B * H; }
+    int64_t bh_kv() const { return bh() / group; }
 };
 
 size_t elem_bytes_in(int dtype);
@@ -90,6 +92,11 @@ int launch_merge(const float *po, const float *pl, int n_parts, int64_t rows, in
 constexpr size_t kNoAllocScratchBytes = (size_t)8 << 20;
 int noalloc_scratch_ptr(void **ptr);
 void forget_noalloc_scratch(int dev);  // attn_shutdown: look the address up again next time
+
+// Rotary positions (attn_rotary.cu); dtype 0 fp32, 1 bf16, 2 fp16.
+int launch_rotary(const attn_heads &q, const attn_heads *k, const uint64_t *turns, int width,
+                  bool interleaved, float amplitude, bool transpose, const int32_t *pos,
+                  int pos_tokens, int B, int S, int d, int dtype, cudaStream_t stream);
 
 // Paged 8-bit cache (attn_cache.cu, attn_cache_select.cu, attn_cache_fwd.cu).
 constexpr int kMaxCacheBatch = 4096;       // sequences of one attention call

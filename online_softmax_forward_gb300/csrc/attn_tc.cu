@@ -71,8 +71,41 @@
 #include "attn_internal.h"
 #include "sm100_ptx.cuh"
 #include "tc_common.cuh"
+#include "tensor_map.h"
 
 namespace attn {
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+}  // namespace
+
+bool make_tile_map(CUtensorMap *m, const void *base, bool bf16, int d, int S, int64_t slices) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)S, (cuuint64_t)slices};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)S * d * 2};
+    cuuint32_t box[3] = {64, 128, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                     3, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 namespace {
 
 constexpr int BM = 128;  // query rows per query tile (MMA M)
@@ -148,6 +181,7 @@ struct TcParams {
     int *status;
     unsigned int *sched;  // this launch's counter pair: next unit, CTAs done
     int BH, Sq, Skv, causal;
+    int group;    // query heads that share a kv head: slice bh reads the K and V of bh / group
     int nqb;      // units per (batch, head): ceil(Sq / 256)
     int hg;       // (batch, head) slices per schedule group (K/V of a group fit in L2)
     int n_units;  // BH * nqb
@@ -366,7 +400,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             auto load_kv = [&](const CUtensorMap *tm, int j, int bh) {
                 const int s = pos % kStages;
                 if (!watch.wait(bar(bars->kv_empty[s]), ((pos / kStages) & 1) ^ 1)) return false;
-                if (!in_bounds(j >= 0 && j * BN < p.Skv && bh >= 0 && bh < p.BH, p.status))
+                if (!in_bounds(j >= 0 && j * BN < p.Skv && bh >= 0 && bh * p.group < p.BH, p.status))
                     return stop();
                 ptx::mbar_arrive_expect_tx(bar(bars->kv_full[s]), C::kTileBytes);
                 for (int c = 0; c < C::kChunks; ++c)
@@ -425,9 +459,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     q_loaded[t] = true;
                     ++qn[t];
                 }
-                ok = ok && load_kv(&tm_k, 0, w.bh);
+                const int kvh = w.bh / p.group;
+                ok = ok && load_kv(&tm_k, 0, kvh);
                 for (int j = 0; j < nmax && ok; ++j)
-                    ok = (j + 1 >= nmax || load_kv(&tm_k, j + 1, w.bh)) && load_kv(&tm_v, j, w.bh);
+                    ok = (j + 1 >= nmax || load_kv(&tm_k, j + 1, kvh)) && load_kv(&tm_v, j, kvh);
                 if (ok) claim = atomicAdd(p.sched, 1u);
             }
             // teardown: wait until every load this thread issued has landed
@@ -868,35 +903,6 @@ unsigned int *next_sched_pair() {
     }
     return base + 2 * (g_sched_seq.fetch_add(1, std::memory_order_relaxed) % kSchedSlots);
 }
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
-// [BH, S, d] 16-bit tensor as a 3-D TMA map, box 64 (d) x 128 (rows) x 1,
-// 128-byte swizzle; rows past S read as zeros.
-bool make_map(CUtensorMap *m, const void *base, bool bf16, int d, int S, int64_t BH) {
-    auto enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)S, (cuuint64_t)BH};
-    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)S * d * 2};
-    cuuint32_t box[3] = {64, 128, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                     3, const_cast<void *>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
 
 template <int D, bool kBF16>
 int launch_typed(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -904,8 +910,8 @@ int launch_typed(const void *q, const void *k, const void *v, void *o, float *ls
     using C = Cfg<D>;
     CUtensorMap tq, tk, tv;
     const int64_t BH = pr.bh();
-    if (!make_map(&tq, q, kBF16, D, pr.Sq, BH) || !make_map(&tk, k, kBF16, D, pr.Skv, BH) ||
-        !make_map(&tv, v, kBF16, D, pr.Skv, BH))
+    if (!make_tile_map(&tq, q, kBF16, D, pr.Sq, BH) || !make_tile_map(&tk, k, kBF16, D, pr.Skv, pr.bh_kv()) ||
+        !make_tile_map(&tv, v, kBF16, D, pr.Skv, pr.bh_kv()))
         return ATTN_ERR_CUDA;
     int *status = status_word_device_ptr();
     unsigned int *sched = next_sched_pair();
@@ -919,6 +925,7 @@ int launch_typed(const void *q, const void *k, const void *v, void *o, float *ls
     p.Sq = pr.Sq;
     p.Skv = pr.Skv;
     p.causal = pr.causal;
+    p.group = pr.group;
     p.nqb = (pr.Sq + 2 * BM - 1) / (2 * BM);
     const int sms = device_sm_count();
     if (sms <= 0) return ATTN_ERR_CUDA;
@@ -935,7 +942,7 @@ int launch_typed(const void *q, const void *k, const void *v, void *o, float *ls
         if (h0 < 1) h0 = 1;
         int64_t hg = h0;
         while (hg < BH && BH % hg != 0) ++hg;
-        const int64_t kv_bytes = BH * 2LL * pr.Skv * D * 2;
+        const int64_t kv_bytes = pr.bh_kv() * 2LL * pr.Skv * D * 2;
         if (hg >= BH && kv_bytes > (96LL << 20)) hg = h0;
         if (hg > BH) hg = BH;
         p.hg = (int)hg;

@@ -1,0 +1,192 @@
+"""Host-only checks of the backward pass, of rotary positions and of shared kv
+heads: every refusal happens before any CUDA call (the addresses are never
+read), and the plan of the backward pass covers every pair of tiles once."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import online_softmax_forward_gb300 as pkg
+from online_softmax_forward_gb300 import build as lib_build
+
+GB = 1 << 30
+Q, K, V, O, L, DO, DL, DQ, DK, DV, W = (i * GB for i in range(1, 12))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    lib_build.build()
+    return pkg.load_library()
+
+
+def bwd(q=Q, k=K, v=V, o=O, lse=L, do=DO, dlse=DL, dq=DQ, dk=DK, dv=DV, B=2, H=8, H_kv=2, Sq=100,
+        Skv=200, d=64, causal=1, scale=0.0, dtype=pkg.ATTN_BF16, ws=W, ws_bytes=GB):
+    # raw: True and False are what they are for the caller of the C function
+    return pkg.load_library().attn_bwd(q, k, v, o, lse, do, dlse, dq, dk, dv, B, H, H_kv, Sq, Skv, d,
+                                       causal, scale, dtype, ws, ws_bytes, None)
+
+
+BAD = [
+    dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(lse=None), dict(do=None),
+    dict(dq=None), dict(dk=None), dict(dv=None), dict(ws=None),
+    dict(q=Q + 8), dict(do=DO + 2), dict(dk=DK + 8), dict(lse=L + 2), dict(dlse=DL + 1), dict(ws=W + 8),
+    dict(dq=Q), dict(dk=DV), dict(dv=K + 64), dict(ws=DO), dict(ws=DQ + 256), dict(dq=L), dict(dk=DL),
+    dict(ws_bytes=1000), dict(ws_bytes=0),
+    dict(H_kv=0), dict(H_kv=3), dict(H_kv=16), dict(H_kv=-2), dict(H=0), dict(H=-8), dict(B=-1),
+    dict(Sq=-1), dict(Skv=-1), dict(d=32), dict(d=96), dict(d=0), dict(dtype=pkg.ATTN_F32, d=24),
+    dict(dtype=5), dict(dtype=-1), dict(causal=2), dict(causal=-1), dict(scale=math.nan),
+    dict(scale=math.inf), dict(B=1 << 20, H=1 << 12, H_kv=1 << 12),
+    dict(B=1 << 15, H=1 << 15, H_kv=1 << 15, Sq=1 << 30, Skv=1 << 30),
+]
+
+
+@pytest.mark.parametrize("kw", BAD, ids=lambda kw: ",".join("%s=%s" % i for i in kw.items()))
+def test_bwd_refuses(kw):
+    assert bwd(**kw) == pkg.ATTN_ERR_INVALID_ARG
+
+
+def _no_gpu():
+    return not torch.cuda.is_available()
+
+
+def test_bwd_accepts_what_it_documents():
+    if not _no_gpu():
+        pytest.skip("valid calls with made-up addresses would launch on this host")
+    for dt in range(5):
+        for d in ((16, 32, 64, 128) if dt == pkg.ATTN_F32 else (64, 128)):
+            assert bwd(dtype=dt, d=d) == pkg.ATTN_ERR_UNSUPPORTED_DEVICE
+    assert bwd(dlse=None) == pkg.ATTN_ERR_UNSUPPORTED_DEVICE
+    assert bwd(H_kv=8) == bwd(H_kv=1) == pkg.ATTN_ERR_UNSUPPORTED_DEVICE
+    # one side empty: the other side's gradients are still written, nothing else is needed
+    assert bwd(Sq=0, q=None, o=None, lse=None, do=None, dlse=None, dq=None, ws=None, ws_bytes=0) == \
+        pkg.ATTN_ERR_UNSUPPORTED_DEVICE
+    assert bwd(Skv=0, k=None, v=None, dk=None, dv=None, ws=None, ws_bytes=0) == pkg.ATTN_ERR_UNSUPPORTED_DEVICE
+    assert bwd(B=0, q=None, k=None, v=None, o=None, lse=None, do=None, dq=None, dk=None, dv=None, ws=None) == \
+        pkg.ATTN_OK
+
+
+def test_bwd_workspace_size():
+    size = lambda *a: pkg.attn_bwd_workspace_size(*a)  # noqa: E731
+    st, n = size(2, 8, 2, 100, 200, 64, 1, pkg.ATTN_BF16)
+    assert st == pkg.ATTN_OK and n >= 2 * 8 * 128 * 8 and n % 256 == 0
+    assert bwd(ws_bytes=n - 1) == pkg.ATTN_ERR_INVALID_ARG
+    for empty in ((0, 8, 2, 100, 200), (2, 8, 2, 0, 200), (2, 8, 2, 100, 0)):
+        assert size(*empty, 64, 1, pkg.ATTN_BF16) == (pkg.ATTN_OK, 0)
+    for bad in ((2, 8, 3, 100, 200, 64, 1, 1), (2, 0, 1, 100, 200, 64, 1, 1), (2, 8, 2, 100, 200, 80, 1, 1),
+                (2, 8, 2, -1, 200, 64, 1, 1), (2, 8, 2, 100, 200, 64, 3, 1), (2, 8, 2, 100, 200, 64, 1, 9)):
+        assert size(*bad)[0] == pkg.ATTN_ERR_INVALID_ARG
+    assert pkg.load_library().attn_bwd_workspace_size(2, 8, 2, 1, 1, 64, 0, 1, None) == pkg.ATTN_ERR_INVALID_ARG
+
+
+def gqa(q=Q, k=K, v=V, o=O, lse=L, B=2, H=8, H_kv=2, Sq=100, Skv=200, d=64, causal=0, scale=0.0,
+        dtype=pkg.ATTN_BF16):
+    return pkg.attn_fwd_gqa(q, k, v, o, lse, B, H, H_kv, Sq, Skv, d, causal, scale, dtype, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(H_kv=0), dict(H_kv=3), dict(H_kv=-1), dict(H_kv=16), dict(H=0, H_kv=1), dict(q=None), dict(k=K + 8),
+    dict(o=Q), dict(lse=O + 16), dict(d=32), dict(causal=2), dict(scale=math.nan), dict(dtype=9),
+    # k and v are as large as their own heads make them, and no larger
+    dict(o=K + 2 * 2 * 200 * 64 * 2 - 16),
+], ids=lambda kw: ",".join("%s=%s" % i for i in kw.items()))
+def test_gqa_refuses(kw):
+    assert gqa(**kw) == pkg.ATTN_ERR_INVALID_ARG
+
+
+def test_gqa_accepts_what_it_documents():
+    if not _no_gpu():
+        pytest.skip("valid calls with made-up addresses would launch on this host")
+    assert gqa() == gqa(H_kv=8) == gqa(H_kv=1) == pkg.ATTN_ERR_UNSUPPORTED_DEVICE
+    assert gqa(o=K + 2 * 2 * 200 * 64 * 2) == pkg.ATTN_ERR_UNSUPPORTED_DEVICE
+    assert gqa(B=0, q=None, k=None, v=None, o=None, lse=None) == pkg.ATTN_OK
+
+
+def heads(in_=Q, out=O, H=4, in_stride=(4 * 10 * 64, 10 * 64, 64), out_stride=(4 * 10 * 64, 10 * 64, 64)):
+    i3 = ctypes.c_int64 * 3
+    return pkg._Heads(in_, out, H, i3(*in_stride), i3(*out_stride))
+
+
+def rot(q="default", k=None, turns=L, width=64, interleaved=0, amplitude=1.0, transpose=0, pos=W, per_token=1,
+        B=2, S=10, d=64, dtype=pkg.ATTN_BF16):
+    q = heads() if q == "default" else q
+    return pkg.load_library().attn_rotary(q, k, turns, width, interleaved, amplitude, transpose, pos, per_token,
+                                          B, S, d, dtype, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(turns=None), dict(pos=None), dict(turns=L + 4), dict(pos=W + 2), dict(width=0),
+    dict(width=63), dict(width=66), dict(d=63), dict(d=1026), dict(interleaved=2), dict(transpose=-1),
+    dict(amplitude=math.nan), dict(amplitude=math.inf), dict(per_token=2), dict(B=-1), dict(S=-1),
+    dict(dtype=pkg.ATTN_BF16_OUT_F32), dict(dtype=7), dict(B=1 << 16, S=1 << 15),
+    dict(q=heads(in_=None)), dict(q=heads(out=None)), dict(q=heads(in_=Q + 1)), dict(q=heads(H=-1)),
+    dict(q=heads(H=65537)), dict(q=heads(in_stride=(-1, 640, 64))),
+    dict(q=heads(out_stride=(2560, 640, 32))),      # rows of the output overlap
+    dict(q=heads(out_stride=(2560, 0, 64))),        # heads of the output are one
+    dict(q=heads(out_stride=(600, 640, 64))),       # sequences of the output overlap
+    dict(q=heads(out=Q, out_stride=(4 * 20 * 64, 20 * 64, 64))),  # in place, but elsewhere
+    dict(q=heads(in_stride=(1 << 61, 640, 64))),
+    dict(k=heads(in_=K, out=None)),
+], ids=str)
+def test_rotary_refuses(kw):
+    assert rot(**kw) == pkg.ATTN_ERR_INVALID_ARG
+
+
+def test_rotary_accepts_what_it_documents():
+    assert rot(B=0, q=heads(in_=None, out=None)) == rot(S=0, q=heads(in_=None)) == pkg.ATTN_OK
+    assert rot(q=heads(H=0, in_=None, out=None), turns=None) == pkg.ATTN_OK
+    if not _no_gpu():
+        pytest.skip("valid calls with made-up addresses would launch on this host")
+    ok = pkg.ATTN_ERR_UNSUPPORTED_DEVICE
+    assert rot() == rot(k=heads(K, V, 2)) == rot(width=2) == rot(q=heads(out=Q)) == ok
+    assert rot(q=heads(in_stride=(0, 0, 0))) == ok                       # a broadcast input
+    assert rot(q=heads(in_=Q + 2, in_stride=(2561, 641, 65))) == ok      # no vector fits
+    assert rot(q=heads(out_stride=(8 * 64 * 10, 64, 8 * 64))) == ok      # [B][S][heads][d]
+    # a dimension of one row has no stride that matters
+    assert rot(S=1, q=heads(out_stride=(4 * 64, 64, 0))) == ok
+
+
+def test_wrappers_refuse_before_any_call():
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t)  # noqa: E731
+    q, k, lse = z(1, 4, 8, 64), z(1, 2, 8, 64), z(1, 4, 8, t=torch.float32)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.attention_bwd(q, k, k, q, lse, q)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.attention(q, k, k)
+    with pytest.raises(ValueError, match="shape"):
+        pkg.attention(q, z(1, 3, 8, 64), z(1, 3, 8, 64))
+    with pytest.raises(ValueError, match="shape"):
+        pkg.attention_splitkv(q, k, k, n_splits=1)
+    r = pkg.Rotary(64, device="cpu")
+    pos = torch.zeros(1, 8, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        pkg.rotary(q, k, r, pos)  # not on a GPU
+    for bad in (dict(width=63), dict(width=0), dict(width=64, layout="other"), dict(width=64, scaling="more"),
+                dict(width=64, scaling="parts"), dict(width=64, scaling="parts", context=100, slow=3, fast=2),
+                dict(width=2, scaling="base"), dict(width=64, frequencies=[1.0]), dict(width=64, base=-1.0),
+                dict(width=2, frequencies=[math.nan]), dict(width=64, amplitude=math.inf),
+                dict(width=2, frequencies=[1.0], scaling="linear"), dict(width=64, factor=0.0)):
+        with pytest.raises(ValueError):
+            pkg.Rotary(**bad, device="cpu")
+
+
+def test_rotary_angles_are_exact_fractions_of_a_turn():
+    """turns / 2^64 of a turn per position is theta to 2^-65 turns (Machin's formula for pi, 200 bits)."""
+    one = 1 << 200
+
+    def arctan_inverse(n):
+        term, total, k = one // n, 0, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    r = pkg.Rotary(128, device="cpu")
+    for theta, t in zip(r.frequencies, r.turns.tolist()):
+        num, den = theta.as_integer_ratio()
+        want = num * one * 2 ** 63 // (den * pi)  # floor of theta / (2 pi) * 2^64
+        assert (t - want) % 2 ** 64 in (0, 1)
+    neg = pkg.Rotary(2, frequencies=[-1.0], device="cpu")
+    assert (neg.turns.item() + r.turns[0].item()) % 2 ** 64 == 0
