@@ -45,6 +45,7 @@
 #include <atomic>
 #include <math.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "attn_bwd.h"
 #include "sm100_ptx.cuh"
@@ -58,7 +59,7 @@ constexpr int kRows = 128;  // rows of every tile
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kThreads = 12 * 32;
-constexpr int kComputeThreads = 256;
+constexpr int kComputeWarps = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSchedRing = 4;
 constexpr int kSchedReaders = 9;  // issuer and 8 computing warps
@@ -196,11 +197,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
-__device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+__device__ __forceinline__ float2 ld_shared_v2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
     return v;
+}
+
+// One arrival for a whole warp, after what all its lanes did.
+__device__ __forceinline__ void arrive_warp(uint32_t bar, int lane) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar);
 }
 
 // Untiled bulk copy into shared memory (16-byte aligned, a multiple of 16 bytes).
@@ -240,7 +246,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ptx::mbar_init(bar(bars->x_full[t]), 1);
             ptx::mbar_init(bar(bars->x_empty[t]), 1);
             ptx::mbar_init(bar(bars->t2_full[t]), 1);
-            ptx::mbar_init(bar(bars->ds_full[t]), kComputeThreads);
+            ptx::mbar_init(bar(bars->ds_full[t]), kComputeWarps);
         }
         for (int s = 0; s < kSlots; ++s) {
             ptx::mbar_init(bar(bars->y_full[s]), 1);
@@ -248,12 +254,12 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int s = 0; s < kStatStages; ++s) {
             ptx::mbar_init(bar(bars->st_full[s]), 1);
-            ptx::mbar_init(bar(bars->st_empty[s]), kComputeThreads);
+            ptx::mbar_init(bar(bars->st_empty[s]), kComputeWarps);
         }
         ptx::mbar_init(bar(bars->t1_full), 1);
-        ptx::mbar_init(bar(bars->p_full), kComputeThreads);
+        ptx::mbar_init(bar(bars->p_full), kComputeWarps);
         ptx::mbar_init(bar(bars->acc_full), 1);
-        ptx::mbar_init(bar(bars->acc_empty), kComputeThreads);
+        ptx::mbar_init(bar(bars->acc_empty), kComputeWarps);
         ptx::mbar_init(bar(bars->mma_done), 1);
         for (int s = 0; s < kSchedRing; ++s) {
             ptx::mbar_init(bar(bars->sched_full[s]), 1);
@@ -508,13 +514,137 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         ptx::setmaxnreg_inc<kComputeRegs>();
         const int half = warp >> 2;  // columns [64 half, 64 half + 64) of T1 and T2
         const int r = (warp & 3) * 32 + lane;
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tl = tmem + lane_base;
-        const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-        const int off = p.Skv - p.Sq;
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float ds_scale = kBF16 ? 1.f : bars->ds_scale;
         uint32_t n1 = 0, n2[2] = {0, 0}, sn = 0, an = 0;
         bool ok = true;
+
+        // The steps of one unit.  T1 and T2 are read as 16 rows x 8 columns a register
+        // quad (16x256b): a thread holds columns 8 j + 2 t, + 1 (t = lane mod 4) of
+        // rows g, g + 8, g + 16, g + 24 (g = lane / 4) of its warp.  A kv unit's
+        // column statistics are then 32 numbers a thread, in registers for all four
+        // rows (one row a thread would read all 128 from shared memory, twice the
+        // time), and the 16-bit pairs go back as 16x128b without a shuffle.
+        auto steps = [&](auto kind, const Unit &w) {
+            constexpr bool KV = decltype(kind)::value;
+            const int g = lane >> 2, t = lane & 3;
+            const int row0 = w.x0 + (warp & 3) * 32 + g;  // this thread's rows: row0 + 8 m
+            const int col0 = half * 64 + 2 * t;           // its columns: col0 + 8 j, + 1
+            const int off = p.Skv - p.Sq;
+            const float2 sc = make_float2(p.scale_log2, p.scale_log2);
+            float2 nl[KV ? 8 : 4], nd[KV ? 8 : 4];  // of its columns, or of its rows (twice each)
+            if constexpr (!KV) {
+                const float *st = p.stats + ((size_t)w.zx * p.nq + w.x0 / kRows) * 2 * kStatTile + (row0 - w.x0);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    float a = 0.f, b = 0.f;
+                    if (in_bounds(w.zx < p.BH && w.x0 / kRows < p.nq, p.status)) {
+                        a = st[8 * m];
+                        b = st[kStatTile + 8 * m];
+                    }
+                    nl[m] = make_float2(a, a);
+                    nd[m] = make_float2(b, b);
+                }
+            }
+            int y = w.y, zy = w.zy;
+            for (int i = 0; i < w.n; ++i) {
+                const int y0 = y * kRows;
+                const int stage = sn % kStatStages;
+                const uint32_t st = sStat + stage * C::kStatBytes + col0 * 4;
+                bool got = true;
+                if constexpr (KV) {
+                    got = watch.wait(bar(bars->st_full[stage]), (sn / kStatStages) & 1);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) nl[j] = ld_shared_v2(st + j * 32);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) nd[j] = ld_shared_v2(st + kStatTile * 4 + j * 32);
+                }
+                got = watch.wait(bar(bars->t1_full), n1 & 1) && got;
+                ++n1;
+                if (!__all_sync(0xffffffffu, got)) return false;
+                ptx::tc_fence_after();
+                uint32_t a[2][32];
+                const uint32_t tT1 = tl + kColT1 + half * 64;
+                ptx::tmem_ld_16x256_x8(tT1, a[0]);
+                ptx::tmem_ld_16x256_x8(tT1 + (16u << 16), a[1]);
+                ptx::tmem_wait_ld();
+                reg_fence(a[0]);
+                reg_fence(a[1]);
+                if constexpr (!KV) {  // T1 is read: the next one may be written
+                    ptx::tc_fence_before();
+                    arrive_warp(bar(bars->p_full), lane);
+                }
+                const bool masked = KV ? (p.causal && w.x0 + kRows - 1 > y0 + off)
+                                       : y0 + kRows > min(p.Skv, p.causal ? w.x0 + off + 1 : p.Skv);
+                if (masked) {  // scores of pairs that do not see each other: -inf
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const int row = row0 + 8 * m;
+                        // columns visible to the row: [lo, hi)
+                        const int lo = KV ? row - off - y0 : 0;
+                        const int hi = KV ? kRows : min(p.Skv, p.causal ? row + off + 1 : p.Skv) - y0;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int c = col0 + 8 * j + e;
+                                if (KV ? c < lo : c >= hi) a[m >> 1][4 * j + 2 * (m & 1) + e] = __float_as_uint(-INFINITY);
+                            }
+                    }
+                }
+                float2 pr[2][16];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {  // columns of j / 2, rows g + 8 (j % 2) of the block
+                        const float2 l = KV ? nl[j >> 1] : nl[2 * b + (j & 1)];
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(a[b][2 * j]), __uint_as_float(a[b][2 * j + 1])), sc, l);
+                        pr[b][j] = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
+                        if constexpr (KV) pk[j] = pack2<kBF16>(pr[b][j].x, pr[b][j].y);
+                    }
+                    if constexpr (KV) ptx::tmem_st_16x128_x8(tT1 + ((uint32_t)(16 * b) << 16), pk);
+                }
+                if constexpr (KV) {
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    arrive_warp(bar(bars->p_full), lane);
+                }
+                const int buf = KV ? 0 : i & 1;
+                got = watch.wait(bar(bars->t2_full[buf]), (buf ? n2[1] : n2[0]) & 1);
+                if (buf) ++n2[1]; else ++n2[0];
+                if (!__all_sync(0xffffffffu, got)) return false;
+                ptx::tc_fence_after();
+                const uint32_t tT2 = tl + (buf ? kColT2b : kColT2) + half * 64;
+                ptx::tmem_ld_16x256_x8(tT2, a[0]);
+                ptx::tmem_ld_16x256_x8(tT2 + (16u << 16), a[1]);
+                ptx::tmem_wait_ld();
+                reg_fence(a[0]);
+                reg_fence(a[1]);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 l = KV ? nd[j >> 1] : nd[2 * b + (j & 1)];
+                        float2 x = __fadd2_rn(make_float2(__uint_as_float(a[b][2 * j]), __uint_as_float(a[b][2 * j + 1])), l);
+                        if constexpr (!kBF16) x = __fmul2_rn(x, make_float2(ds_scale, ds_scale));
+                        x = __fmul2_rn(x, pr[b][j]);
+                        pk[j] = pack2<kBF16>(x.x, x.y);
+                    }
+                    ptx::tmem_st_16x128_x8(tT2 + ((uint32_t)(16 * b) << 16), pk);
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                arrive_warp(bar(bars->ds_full[buf]), lane);
+                if constexpr (KV) {
+                    if (lane == 0) ptx::mbar_arrive(bar(bars->st_empty[stage]));
+                    ++sn;
+                }
+                advance(w, p, y, zy);
+            }
+            return true;
+        };
 
         for (uint32_t k = 0; ok;) {
             Unit w;
@@ -522,113 +652,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (w.kind < 0) break;
             const bool kv = w.kind == 0;
             const int row = w.x0 + r;
-            float nl = 0.f, nd = 0.f;  // q unit: of this thread's row
-            if (!kv) {
-                const float *st = p.stats + ((size_t)w.zx * p.nq + w.x0 / kRows) * 2 * kStatTile + r;
-                if (in_bounds(w.zx < p.BH && w.x0 / kRows < p.nq, p.status)) {
-                    nl = st[0];
-                    nd = st[kStatTile];
-                }
-            }
-            int y = w.y;
-            int zy = w.zy;
-            for (int i = 0; i < w.n; ++i) {
-                const int y0 = y * kRows;
-                const int stage = sn % kStatStages;
-                const uint32_t st = sStat + stage * C::kStatBytes + half * 256;
-                bool got = watch.wait(bar(bars->t1_full), n1 & 1);
-                ++n1;
-                if (kv) got = got && watch.wait(bar(bars->st_full[stage]), (sn / kStatStages) & 1);
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                ptx::tc_fence_after();
-                uint32_t a[32], b[32];
-                float pr[64];
-                const uint32_t tT1 = tl + kColT1 + half * 64;
-                ptx::tmem_ld32(tT1, a);
-                ptx::tmem_ld32(tT1 + 32, b);
-                ptx::tmem_wait_ld();
-                reg_fence(a);
-                reg_fence(b);
-                // columns visible to this row: [lo, hi)
-                const int lo = (kv && p.causal) ? row - off - y0 : 0;
-                const int hi = kv ? kRows : min(p.Skv, p.causal ? row + off + 1 : p.Skv) - y0;
-                const bool masked = kv ? (p.causal && w.x0 + kRows - 1 > y0 + off)
-                                       : y0 + kRows > min(p.Skv, p.causal ? w.x0 + off + 1 : p.Skv);
-                if (!kv) {  // T1 is read: the next one may be written
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(bar(bars->p_full));
-                }
-#pragma unroll
-                for (int j = 0; j < 64; j += 4) {
-                    const uint32_t *s = j < 32 ? a + j : b + (j - 32);
-                    float4 l = make_float4(nl, nl, nl, nl);
-                    if (kv) l = ld_shared_v4(st + j * 4);
-                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), sc, make_float2(l.x, l.y));
-                    const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), sc, make_float2(l.z, l.w));
-                    pr[j] = ptx::ex2_approx(x.x);
-                    pr[j + 1] = ptx::ex2_approx(x.y);
-                    pr[j + 2] = ptx::ex2_approx(z.x);
-                    pr[j + 3] = ptx::ex2_approx(z.y);
-                }
-                if (masked) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (half * 64 + j < lo || half * 64 + j >= hi) pr[j] = 0.f;
-                }
-                if (kv) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) pk[j] = pack2<kBF16>(pr[2 * j], pr[2 * j + 1]);
-                    ptx::tmem_st32(tT1, pk);
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(bar(bars->p_full));
-                }
-                const int buf = kv ? 0 : i & 1;
-                got = watch.wait(bar(bars->t2_full[buf]), (buf ? n2[1] : n2[0]) & 1);
-                if (buf) ++n2[1]; else ++n2[0];
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                ptx::tc_fence_after();
-                const uint32_t tT2 = tl + (buf ? kColT2b : kColT2) + half * 64;
-                ptx::tmem_ld32(tT2, a);
-                ptx::tmem_ld32(tT2 + 32, b);
-                ptx::tmem_wait_ld();
-                reg_fence(a);
-                reg_fence(b);
-                uint32_t pk[32];
-#pragma unroll
-                for (int j = 0; j < 64; j += 4) {
-                    const uint32_t *s = j < 32 ? a + j : b + (j - 32);
-                    float4 l = make_float4(nd, nd, nd, nd);
-                    if (kv) l = ld_shared_v4(st + kStatTile * 4 + j * 4);
-                    float2 x = __fadd2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), make_float2(l.x, l.y));
-                    float2 z = __fadd2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), make_float2(l.z, l.w));
-                    if constexpr (!kBF16) {
-                        x = __fmul2_rn(x, make_float2(ds_scale, ds_scale));
-                        z = __fmul2_rn(z, make_float2(ds_scale, ds_scale));
-                    }
-                    x = __fmul2_rn(x, make_float2(pr[j], pr[j + 1]));
-                    z = __fmul2_rn(z, make_float2(pr[j + 2], pr[j + 3]));
-                    if (masked) {  // what a masked place holds does not matter
-                        const int c = half * 64 + j;
-                        if (c < lo || c >= hi) x.x = 0.f;
-                        if (c + 1 < lo || c + 1 >= hi) x.y = 0.f;
-                        if (c + 2 < lo || c + 2 >= hi) z.x = 0.f;
-                        if (c + 3 < lo || c + 3 >= hi) z.y = 0.f;
-                    }
-                    pk[j / 2] = pack2<kBF16>(x.x, x.y);
-                    pk[j / 2 + 1] = pack2<kBF16>(z.x, z.y);
-                }
-                ptx::tmem_st32(tT2, pk);
-                ptx::tmem_wait_st();
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(bar(bars->ds_full[buf]));
-                if (kv) {
-                    ptx::mbar_arrive(bar(bars->st_empty[stage]));
-                    ++sn;
-                }
-                advance(w, p, y, zy);
-            }
+            ok = kv ? steps(std::true_type{}, w) : steps(std::false_type{}, w);
             if (!ok) break;
 
             // ---- the unit's sums: dk and dv, or dq
@@ -684,9 +708,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             if (w.n > 0) {
-                __syncwarp();
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(bar(bars->acc_empty));
+                arrive_warp(bar(bars->acc_empty), lane);
             }
         }
     } else {
