@@ -20,8 +20,8 @@
 //    counter in the workspace, kv units of a group of heads first, longest
 //    first, so that the CTAs running at any time share the tiles of a few heads
 //    through L2.
-//  * Warp 8 (producer) streams the tiles with TMA (128-byte swizzle) into a ring,
-//    Y1 and Y2 of a step in turn, and the statistics of a kv unit's query tile
+//  * Warp 8 (producer) streams the tiles with TMA (128-byte swizzle) into a ring of
+//    Y1 and one of Y2, and the statistics of a kv unit's query tile
 //    beside them.
 //  * Warp 9 issues the tcgen05.mma (kind::f16, fp32 accumulate).  A kv unit's step
 //    is A1(i), T1(i+1), A2(i), T2(i+1): while the first two run, the other
@@ -78,15 +78,26 @@ struct Cfg {
     static constexpr int kChunks = D / 64;
     static constexpr int kChunkBytes = kRows * 128;  // one 64-channel column of a tile: 16 KB
     static constexpr int kTileBytes = kChunks * kChunkBytes;
-    static constexpr int kSlots = D == 128 ? 5 : 8;  // ring of Y tiles
-    static constexpr int kOffX = 0;                  // X1, X2
+    // Rings of Y1 and of Y2.  A Y1 tile is held from T1 of its step until A2, six
+    // products in both kinds of units, a Y2 tile for one or two; a tile takes about
+    // three products' time to come (d = 128).  One ring of five made each wait for
+    // the longer-held of the two (2740 clocks a step of a q unit of d = 128).
+    static constexpr int kSlots1 = D == 128 ? 3 : 6;
+    static constexpr int kSlots2 = D == 128 ? 2 : 4;
+    static constexpr int kOffX = 0;  // X1, X2
     static constexpr int kOffY = 2 * kTileBytes;
-    static constexpr int kOffStat = kOffY + kSlots * kTileBytes;
+    static constexpr int kOffStat = kOffY + (kSlots1 + kSlots2) * kTileBytes;
+    __device__ static constexpr int slots(int t) { return t ? kSlots2 : kSlots1; }
+    // slot of the n-th tile of Y_t, among all
+    __device__ static __forceinline__ uint32_t slot(int t, uint32_t n) {
+        return t ? kSlots1 + n % kSlots2 : n % kSlots1;
+    }
+    __device__ static __forceinline__ uint32_t round(int t, uint32_t n) { return n / (t ? kSlots2 : kSlots1); }
     static constexpr int kStatBytes = 2 * kStatTile * 4;
     static constexpr int kOffBar = kOffStat + kStatStages * kStatBytes;
     static constexpr int kSmemBytes = kOffBar + 896;
 };
-constexpr int kMaxSlots = 8;
+constexpr int kMaxSlots = 10;
 
 struct Unit {
     int kind;   // 0: kv unit, 1: q unit, -2: no more units
@@ -222,7 +233,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                    const Params p) {
     using C = Cfg<D>;
-    constexpr int kSlots = C::kSlots;
+    constexpr int kSlots = C::kSlots1 + C::kSlots2;
     // the tiles' swizzle needs 1024-byte alignment, which this declaration asks
     // for: there is no room to align by hand at D = 128
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -322,7 +333,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ------------------------------------------------------------ producer
         ptx::setmaxnreg_dec<kOtherRegs>();
         if (lane == 0) {
-            uint32_t pos = 0, xn[2] = {0, 0}, sn = 0;  // tiles of Y, of each X, and statistics loaded
+            uint32_t yn[2] = {0, 0}, xn[2] = {0, 0}, sn = 0;  // tiles of each Y and X, statistics loaded
             bool ok = true;
             auto stop = [&]() {
                 *watch.abort_flag = 1;
@@ -345,13 +356,13 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 return true;
             };
             auto load_y = [&](int t, const Unit &w, int y, int zy) {
-                const int s = pos % kSlots;
-                if (!watch.wait(bar(bars->y_empty[s]), ((pos / kSlots) & 1) ^ 1)) return false;
+                const uint32_t s = C::slot(t, yn[t]);
+                if (!watch.wait(bar(bars->y_empty[s]), (C::round(t, yn[t]) & 1) ^ 1)) return false;
                 const CUtensorMap *tm = w.kind == 0 ? (t ? &tm_do : &tm_q) : (t ? &tm_v : &tm_k);
                 if (!tile(sY + s * C::kTileBytes, bars->y_full[s], tm, y * kRows, zy,
                           w.kind == 0 ? p.Sq : p.Skv, w.kind == 0 ? p.BH : p.BHk))
                     return false;
-                ++pos;
+                ++yn[t];
                 return true;
             };
             auto load_stat = [&](int y, int zy) {
@@ -396,10 +407,11 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (ok) claim = atomicAdd(p.counter, 1u);
             }
             // teardown: every load this thread issued has landed
-            for (uint32_t s = 0; s < (uint32_t)kSlots && s < pos; ++s) {
-                const uint32_t last = s + ((pos - 1 - s) / kSlots) * kSlots;
-                watch.drain(bar(bars->y_full[s]), (last / kSlots) & 1);
-            }
+            for (int t = 0; t < 2; ++t)
+                for (uint32_t s = 0; s < (uint32_t)C::slots(t) && s < yn[t]; ++s) {
+                    const uint32_t last = s + ((yn[t] - 1 - s) / C::slots(t)) * C::slots(t);
+                    watch.drain(bar(bars->y_full[C::slot(t, last)]), C::round(t, last) & 1);
+                }
             for (uint32_t s = 0; s < (uint32_t)kStatStages && s < sn; ++s) {
                 const uint32_t last = s + ((sn - 1 - s) / kStatStages) * kStatStages;
                 watch.drain(bar(bars->st_full[s]), (last / kStatStages) & 1);
@@ -419,25 +431,25 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint64_t dx = sdesc(sX, 16, 1024);
         const uint64_t dyk = sdesc(sY, 16, 1024);              // Y as [rows of the result's columns][channels]
         const uint64_t dyn = sdesc(sY, C::kChunkBytes, 1024);  // Y as [summed rows][channels of the result]
-        uint32_t pos = 0;             // ring position of the unit's Y1(0)
+        uint32_t pos = 0;             // steps of the units before: tiles of Y1 and of Y2
         uint32_t xn = 0, un = 0;      // units begun, units whose sums were begun
         uint32_t pn = 0, dn[2] = {0, 0};  // p_full and ds_full phases waited for
         bool ok = true;
-        auto slot_full = [&](uint32_t at) { return wait_all(bars->y_full[at % kSlots], (at / kSlots) & 1); };
-        auto free_slot = [&](uint32_t at) { ptx::mma_commit_warp(bar(bars->y_empty[at % kSlots])); };
-        // T = X Y^T, Y at ring position `at`
-        auto issue_t = [&](uint32_t col, int x, uint32_t at) {
-            const uint64_t da = dx + (uint64_t)((x * C::kTileBytes) >> 4);
-            const uint64_t db = dyk + (uint64_t)(((at % kSlots) * C::kTileBytes) >> 4);
+        auto slot_full = [&](int t, uint32_t n) { return wait_all(bars->y_full[C::slot(t, n)], C::round(t, n) & 1); };
+        auto free_slot = [&](int t, uint32_t n) { ptx::mma_commit_warp(bar(bars->y_empty[C::slot(t, n)])); };
+        // T = X_t Y_t^T, Y_t its n-th tile
+        auto issue_t = [&](uint32_t col, int t, uint32_t n) {
+            const uint64_t da = dx + (uint64_t)((t * C::kTileBytes) >> 4);
+            const uint64_t db = dyk + (uint64_t)((C::slot(t, n) * C::kTileBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t o = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
                 ptx::mma_ss_warp(tmem + col, da + o, db + o, kIdescT, kk > 0 ? 1u : 0u);
             }
         };
-        // A += (16-bit rows at column `col`) Y
-        auto issue_a = [&](uint32_t acc, uint32_t col, uint32_t at, bool add) {
-            const uint64_t db = dyn + (uint64_t)(((at % kSlots) * C::kTileBytes) >> 4);
+        // A += (16-bit rows at column `col`) Y_t
+        auto issue_a = [&](uint32_t acc, uint32_t col, int t, uint32_t n, bool add) {
+            const uint64_t db = dyn + (uint64_t)((C::slot(t, n) * C::kTileBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kRows / 16; ++kk)
                 ptx::mma_ts_warp(tmem + acc, tmem + col + (kk >> 2) * 64 + (kk & 3) * 8,
@@ -458,21 +470,21 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             // T1 and T2 of step i
             auto t1 = [&](int i) {
-                if (!slot_full(pos + 2 * i)) return false;
+                if (!slot_full(0, pos + i)) return false;
                 ptx::tc_fence_after();
-                issue_t(kColT1, 0, pos + 2 * i);
+                issue_t(kColT1, 0, pos + i);
                 ptx::mma_commit_warp(bar(bars->t1_full));
                 if (i == n - 1) ptx::mma_commit_warp(bar(bars->x_empty[0]));
                 return true;
             };
             auto t2 = [&](int i) {
                 const int buf = kv ? 0 : i & 1;
-                if (!slot_full(pos + 2 * i + 1)) return false;
+                if (!slot_full(1, pos + i)) return false;
                 if (buf == 1 && !need_acc()) return false;
                 ptx::tc_fence_after();
-                issue_t(buf ? kColT2b : kColT2, 1, pos + 2 * i + 1);
+                issue_t(buf ? kColT2b : kColT2, 1, pos + i);
                 ptx::mma_commit_warp(bar(bars->t2_full[buf]));
-                if (!kv) free_slot(pos + 2 * i + 1);
+                if (!kv) free_slot(1, pos + i);
                 if (i == n - 1) ptx::mma_commit_warp(bar(bars->x_empty[1]));
                 return true;
             };
@@ -485,8 +497,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (kv) {
                     if (!need_acc()) { ok = false; break; }
                     ptx::tc_fence_after();
-                    issue_a(kColA1, kColT1, pos + 2 * i + 1, i > 0);
-                    free_slot(pos + 2 * i + 1);
+                    issue_a(kColA1, kColT1, 1, pos + i, i > 0);
+                    free_slot(1, pos + i);
                 }
                 if (i + 1 < n) {
                     ok = t1(i + 1);
@@ -497,14 +509,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!wait_all(bars->ds_full[buf], (buf ? dn[1] : dn[0]) & 1) || !need_acc()) { ok = false; break; }
                 if (buf) ++dn[1]; else ++dn[0];
                 ptx::tc_fence_after();
-                issue_a(kColA2, buf ? kColT2b : kColT2, pos + 2 * i, i > 0);
-                free_slot(pos + 2 * i);
+                issue_a(kColA2, buf ? kColT2b : kColT2, 0, pos + i, i > 0);
+                free_slot(0, pos + i);
                 if (kv && i + 1 < n) ok = t2(i + 1);
             }
             if (!ok) break;
             ptx::mma_commit_warp(bar(bars->acc_full));
             ++un;
-            pos += 2 * n;
+            pos += n;
         }
         ptx::mma_commit_warp(bar(bars->mma_done));
         watch.drain(bar(bars->mma_done), 0);
