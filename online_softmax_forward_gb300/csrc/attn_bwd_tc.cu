@@ -208,9 +208,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
-__device__ __forceinline__ float2 ld_shared_v2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+__device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
 
@@ -531,54 +532,35 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint32_t n1 = 0, n2[2] = {0, 0}, sn = 0, an = 0;
         bool ok = true;
 
-        // The steps of one unit.  T1 and T2 are read as 16 rows x 8 columns a register
-        // quad (16x256b): a thread holds columns 8 j + 2 t, + 1 (t = lane mod 4) of
-        // rows g, g + 8, g + 16, g + 24 (g = lane / 4) of its warp.  A kv unit's
-        // column statistics are then 32 numbers a thread, in registers for all four
-        // rows (one row a thread would read all 128 from shared memory, twice the
-        // time), and the 16-bit pairs go back as 16x128b without a shuffle.
+        // The steps of one unit, one row and 64 columns a thread.
         auto steps = [&](auto kind, const Unit &w) {
             constexpr bool KV = decltype(kind)::value;
-            const int g = lane >> 2, t = lane & 3;
-            const int row0 = w.x0 + (warp & 3) * 32 + g;  // this thread's rows: row0 + 8 m
-            const int col0 = half * 64 + 2 * t;           // its columns: col0 + 8 j, + 1
+            const int row = w.x0 + r;
             const int off = p.Skv - p.Sq;
             const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-            float2 nl[KV ? 8 : 4], nd[KV ? 8 : 4];  // of its columns, or of its rows (twice each)
+            float rl = 0.f, rd = 0.f;  // q unit: nl and nd of this thread's row
             if constexpr (!KV) {
-                const float *st = p.stats + ((size_t)w.zx * p.nq + w.x0 / kRows) * 2 * kStatTile + (row0 - w.x0);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    float a = 0.f, b = 0.f;
-                    if (in_bounds(w.zx < p.BH && w.x0 / kRows < p.nq, p.status)) {
-                        a = st[8 * m];
-                        b = st[kStatTile + 8 * m];
-                    }
-                    nl[m] = make_float2(a, a);
-                    nd[m] = make_float2(b, b);
+                const float *st = p.stats + ((size_t)w.zx * p.nq + w.x0 / kRows) * 2 * kStatTile + r;
+                if (in_bounds(w.zx < p.BH && w.x0 / kRows < p.nq, p.status)) {
+                    rl = st[0];
+                    rd = st[kStatTile];
                 }
             }
             int y = w.y, zy = w.zy;
             for (int i = 0; i < w.n; ++i) {
                 const int y0 = y * kRows;
                 const int stage = sn % kStatStages;
-                const uint32_t st = sStat + stage * C::kStatBytes + col0 * 4;
+                const uint32_t st = sStat + stage * C::kStatBytes + half * 256;
                 bool got = true;
-                if constexpr (KV) {
-                    got = watch.wait(bar(bars->st_full[stage]), (sn / kStatStages) & 1);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) nl[j] = ld_shared_v2(st + j * 32);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) nd[j] = ld_shared_v2(st + kStatTile * 4 + j * 32);
-                }
+                if constexpr (KV) got = watch.wait(bar(bars->st_full[stage]), (sn / kStatStages) & 1);
                 got = watch.wait(bar(bars->t1_full), n1 & 1) && got;
                 ++n1;
                 if (!__all_sync(0xffffffffu, got)) return false;
                 ptx::tc_fence_after();
                 uint32_t a[2][32];
                 const uint32_t tT1 = tl + kColT1 + half * 64;
-                ptx::tmem_ld_16x256_x8(tT1, a[0]);
-                ptx::tmem_ld_16x256_x8(tT1 + (16u << 16), a[1]);
+                ptx::tmem_ld32(tT1, a[0]);
+                ptx::tmem_ld32(tT1 + 32, a[1]);
                 ptx::tmem_wait_ld();
                 reg_fence(a[0]);
                 reg_fence(a[1]);
@@ -589,35 +571,31 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const bool masked = KV ? (p.causal && w.x0 + kRows - 1 > y0 + off)
                                        : y0 + kRows > min(p.Skv, p.causal ? w.x0 + off + 1 : p.Skv);
                 if (masked) {  // scores of pairs that do not see each other: -inf
+                    // columns visible to the row: [lo, hi)
+                    const int lo = (KV ? row - off - y0 : 0) - half * 64;
+                    const int hi = (KV ? kRows : min(p.Skv, p.causal ? row + off + 1 : p.Skv) - y0) - half * 64;
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int row = row0 + 8 * m;
-                        // columns visible to the row: [lo, hi)
-                        const int lo = KV ? row - off - y0 : 0;
-                        const int hi = KV ? kRows : min(p.Skv, p.causal ? row + off + 1 : p.Skv) - y0;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int c = col0 + 8 * j + e;
-                                if (KV ? c < lo : c >= hi) a[m >> 1][4 * j + 2 * (m & 1) + e] = __float_as_uint(-INFINITY);
-                            }
-                    }
+                    for (int j = 0; j < 64; ++j)
+                        if (KV ? j < lo : j >= hi) a[j >> 5][j & 31] = __float_as_uint(-INFINITY);
                 }
-                float2 pr[2][16];
+                float2 pr[32];
+                uint32_t pk[32];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {  // columns of j / 2, rows g + 8 (j % 2) of the block
-                        const float2 l = KV ? nl[j >> 1] : nl[2 * b + (j & 1)];
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(a[b][2 * j]), __uint_as_float(a[b][2 * j + 1])), sc, l);
-                        pr[b][j] = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
-                        if constexpr (KV) pk[j] = pack2<kBF16>(pr[b][j].x, pr[b][j].y);
+                for (int j = 0; j < 32; j += 2) {
+                    const uint32_t *s = &a[j >> 4][(2 * j) & 31];
+                    float4 l = make_float4(rl, rl, rl, rl);
+                    if constexpr (KV) l = ld_shared_v4(st + j * 8);
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), sc, make_float2(l.x, l.y));
+                    const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), sc, make_float2(l.z, l.w));
+                    pr[j] = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
+                    pr[j + 1] = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
+                    if constexpr (KV) {
+                        pk[j] = pack2<kBF16>(pr[j].x, pr[j].y);
+                        pk[j + 1] = pack2<kBF16>(pr[j + 1].x, pr[j + 1].y);
                     }
-                    if constexpr (KV) ptx::tmem_st_16x128_x8(tT1 + ((uint32_t)(16 * b) << 16), pk);
                 }
                 if constexpr (KV) {
+                    ptx::tmem_st32(tT1, pk);
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
                     arrive_warp(bar(bars->p_full), lane);
@@ -628,24 +606,28 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!__all_sync(0xffffffffu, got)) return false;
                 ptx::tc_fence_after();
                 const uint32_t tT2 = tl + (buf ? kColT2b : kColT2) + half * 64;
-                ptx::tmem_ld_16x256_x8(tT2, a[0]);
-                ptx::tmem_ld_16x256_x8(tT2 + (16u << 16), a[1]);
+                ptx::tmem_ld32(tT2, a[0]);
+                ptx::tmem_ld32(tT2 + 32, a[1]);
                 ptx::tmem_wait_ld();
                 reg_fence(a[0]);
                 reg_fence(a[1]);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 l = KV ? nd[j >> 1] : nd[2 * b + (j & 1)];
-                        float2 x = __fadd2_rn(make_float2(__uint_as_float(a[b][2 * j]), __uint_as_float(a[b][2 * j + 1])), l);
-                        if constexpr (!kBF16) x = __fmul2_rn(x, make_float2(ds_scale, ds_scale));
-                        x = __fmul2_rn(x, pr[b][j]);
-                        pk[j] = pack2<kBF16>(x.x, x.y);
+                for (int j = 0; j < 32; j += 2) {
+                    const uint32_t *s = &a[j >> 4][(2 * j) & 31];
+                    float4 l = make_float4(rd, rd, rd, rd);
+                    if constexpr (KV) l = ld_shared_v4(st + kStatTile * 4 + j * 8);
+                    float2 x = __fadd2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), make_float2(l.x, l.y));
+                    float2 z = __fadd2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), make_float2(l.z, l.w));
+                    if constexpr (!kBF16) {
+                        x = __fmul2_rn(x, make_float2(ds_scale, ds_scale));
+                        z = __fmul2_rn(z, make_float2(ds_scale, ds_scale));
                     }
-                    ptx::tmem_st_16x128_x8(tT2 + ((uint32_t)(16 * b) << 16), pk);
+                    x = __fmul2_rn(x, pr[j]);
+                    z = __fmul2_rn(z, pr[j + 1]);
+                    pk[j] = pack2<kBF16>(x.x, x.y);
+                    pk[j + 1] = pack2<kBF16>(z.x, z.y);
                 }
+                ptx::tmem_st32(tT2, pk);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 arrive_warp(bar(bars->ds_full[buf]), lane);
