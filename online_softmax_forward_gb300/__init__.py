@@ -15,6 +15,7 @@ import fractions
 import functools
 import math
 import os
+import struct
 import threading
 
 __all__ = [
@@ -80,6 +81,7 @@ class _Heads(ctypes.Structure):  # attn_heads of include/attn.h
                 ("out_stride", ctypes.c_int64 * 3)]
 
 
+_HEADS = struct.Struct("PPi4x6q").pack  # the same as bytes, in a fifth of the time
 _C = ctypes.POINTER(_Cache)
 _R = ctypes.POINTER(_Heads)
 _SIGS = [
@@ -141,6 +143,9 @@ def _open(path, sigs, what):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    lib.rotary_packed = lib["attn_rotary"]  # takes its structures as bytes
+    lib.rotary_packed.restype = _I
+    lib.rotary_packed.argtypes = [ctypes.c_char_p, ctypes.c_char_p] + lib.attn_rotary.argtypes[2:]
     return lib
 
 
@@ -466,39 +471,46 @@ def attention_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None
     if _torch is None:
         import torch
         _bind(torch)
-    B, H, Sq, Skv, d = _shapes(q, k, v, shared=True)
-    H_kv = k.shape[1]
-    if H < 1:
-        raise ValueError("q has no head")
-    if k.dtype is not q.dtype or v.dtype is not q.dtype or do.dtype is not q.dtype:
+    shape, kshape, dtype, odt, dev = q.shape, k.shape, q.dtype, o.dtype, q.device
+    if len(shape) != 4 or len(kshape) != 4 or v.shape != kshape or o.shape != shape or do.shape != shape:
+        raise ValueError("q, o, do must be [B, H, Sq, d] of one shape and k, v [B, H_kv, Skv, d] of one")
+    B, H, Sq, d = shape
+    H_kv, Skv = kshape[1], kshape[2]
+    if kshape[0] != B or kshape[3] != d or H < 1 or H_kv < 1 or H % H_kv != 0:
+        raise ValueError("shape mismatch q %s k %s" % (tuple(shape), tuple(kshape)))
+    if k.dtype is not dtype or v.dtype is not dtype or do.dtype is not dtype:
         raise ValueError("q, k, v and do must share a dtype")
-    code = dtype_code(q.dtype, o.dtype)
-    dev = q.device
-    _check_out(o, q.shape, o.dtype, dev, "o")
-    _check_out(do, q.shape, q.dtype, dev, "do")
-    rows = q.shape[:3]
+    for t in (q, k, v, o, do):
+        if not t.is_cuda or t.device != dev:
+            raise ValueError("q, k, v, o and do must be CUDA tensors on one device")
+        if not t.is_contiguous():
+            raise ValueError("q, k, v, o and do must be contiguous")
+    code = dtype_code(dtype, odt)
+    rows = (B, H, Sq)
     _check_out(lse, rows, _torch.float32, dev, "lse")
     if dlse is not None:
         _check_out(dlse, rows, _torch.float32, dev, "dlse")
     handle = _handle(dev, stream)
-    if out is None:
-        dq = _new(stream, q.shape, o.dtype, dev)
-        dk = _new(stream, k.shape, o.dtype, dev)
-        dv = _new(stream, k.shape, o.dtype, dev)
-    else:
+    if out is not None:
         dq, dk, dv = out
         for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
-            _check_out(t, like.shape, o.dtype, dev, name)
+            _check_out(t, like.shape, odt, dev, name)
+    elif odt is dtype:
+        dq, dk, dv = _new_like(stream, q), _new_like(stream, k), _new_like(stream, k)
+    else:
+        dq, dk, dv = (_new(stream, s, odt, dev) for s in (shape, kshape, kshape))
     need = _need(attn_bwd_workspace_size, B, H, H_kv, Sq, Skv, d, bool(causal), code)
     if workspace is None:  # belongs to the call's stream, or to the graph that captures it
-        workspace = _new(stream, max(need, 16), _torch.uint8, dev)
+        workspace = _new(stream, need, _torch.uint8, dev)
+        wn = need
     elif not workspace.is_contiguous() or _device_of(workspace) != dev:
         raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    else:
+        wn = workspace.numel() * workspace.element_size()
     _call_on(dev, load_library().attn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
              lse.data_ptr(), do.data_ptr(), None if dlse is None else dlse.data_ptr(),
              dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, H_kv, Sq, Skv, d, 1 if causal else 0,
-             0.0 if scale is None else float(scale), code, workspace.data_ptr(),
-             workspace.numel() * workspace.element_size(), handle)
+             0.0 if scale is None else float(scale), code, workspace.data_ptr(), wn, handle)
     return dq, dk, dv
 
 
@@ -648,13 +660,20 @@ class Rotary:
         self._args = (self.turns.data_ptr(), width, 1 if layout == "interleaved" else 0, self.amplitude)
 
 
-def _heads(x, out, B, S, d, name):
-    """attn_heads of rows x [B, H, S, d] written to ``out``."""
+def _heads(x, out, name):
+    """attn_heads (packed) of rows x [B, H, S, d] written to ``out``."""
     xb, xh, xs, xc = x.stride()
     ob, oh, os_, oc = out.stride()
-    if (xc != 1 or oc != 1) and d > 1:
+    if xc != 1 or oc != 1:
         raise ValueError("the channels of %s must be contiguous" % name)
-    return _Heads(x.data_ptr(), out.data_ptr(), x.shape[1], (xb, xh, xs), (ob, oh, os_))
+    return _HEADS(x.data_ptr(), out.data_ptr(), x.shape[1], xb, xh, xs, ob, oh, os_)
+
+
+def _contiguous_like(stream, t):
+    """An uninitialised contiguous tensor of a strided one's shape, type and device."""
+    if stream is None:
+        return _torch.empty_like(t, memory_format=_contiguous)
+    return _new(stream, t.shape, t.dtype, t.device)
 
 
 def rotary(q, k, rot, pos, transpose: bool = False, out=None, stream=None):
@@ -665,35 +684,35 @@ def rotary(q, k, rot, pos, transpose: bool = False, out=None, stream=None):
     of a projection's [B,S,H,d].  ``transpose`` gives the gradient in q and k from the one in the
     results.  New results are contiguous [B,H,S,d], as ``attention`` and ``cache_append`` take them;
     ``out`` = (q', k') writes to other places, which may be q and k themselves.  Returns (q', k')."""
-    shape = q.shape
+    shape, dev, dtype = q.shape, q.device, q.dtype
     if len(shape) != 4:
         raise ValueError("q must be [B, H, S, d]")
-    B, H, S, d = shape
-    dev, dtype = q.device, q.dtype
+    B, _, S, d = shape
     if dev != rot.device or not q.is_cuda:
         raise ValueError("q is on %s, the angles on %s" % (dev, rot.device))
-    if rot.width > d:
-        raise ValueError("rows have %d channels, %d are turned" % (d, rot.width))
+    turns, width, interleaved, amplitude = rot._args
+    if width > d:
+        raise ValueError("rows have %d channels, %d are turned" % (d, width))
     code = dtype_code(dtype)
-    if k is not None and (k.dtype is not dtype or k.device != dev or len(k.shape) != 4 or
-                          (k.shape[0], k.shape[2], k.shape[3]) != (B, S, d)):
-        raise ValueError("k must be [%d, H_kv, %d, %d] of q's dtype and device" % (B, S, d))
+    if k is not None:
+        kshape = k.shape
+        if k.dtype is not dtype or k.device != dev or len(kshape) != 4 or kshape[0] != B or \
+                kshape[2] != S or kshape[3] != d:
+            raise ValueError("k must be [%d, H_kv, %d, %d] of q's dtype and device" % (B, S, d))
     per_token = pos.dim() == 2
     p = _int32_on(pos, (B, S) if per_token else (B,), dev, "pos")
     handle = _handle(dev, stream)
     if out is None:
-        qo = _new(stream, shape, dtype, dev)
-        ko = None if k is None else _new(stream, k.shape, dtype, dev)
+        qo = _contiguous_like(stream, q)
+        ko = None if k is None else _contiguous_like(stream, k)
     else:
         qo, ko = out
         for t, like, name in ((qo, q, "out[0]"), (ko, k, "out[1]")):
             if (t is None) != (like is None) or \
                     (t is not None and (t.shape != like.shape or t.dtype is not dtype or t.device != dev)):
                 raise ValueError("%s must be of the shape, dtype and device of its input" % name)
-    hq = _heads(q, qo, B, S, d, "q")
-    hk = None if k is None else _heads(k, ko, B, S, d, "k")
-    turns, width, interleaved, amplitude = rot._args
-    _call_on(dev, load_library().attn_rotary, hq, hk, turns, width, interleaved, amplitude,
+    _call_on(dev, load_library().rotary_packed, _heads(q, qo, "q"),
+             None if k is None else _heads(k, ko, "k"), turns, width, interleaved, amplitude,
              1 if transpose else 0, p, 1 if per_token else 0, B, S, d, code, handle)
     return qo, ko
 
@@ -776,12 +795,12 @@ def _sequence_args(cache, table, lens, counts, B):
 
 # What every call on a cache needs of torch, bound once a KVCache exists: looking it up in each
 # call takes as long as a small kernel.
-_torch = _int32 = _raw_stream = _current_device = _capturing = None
+_torch = _int32 = _contiguous = _raw_stream = _current_device = _capturing = None
 
 
 def _bind(torch):
-    global _torch, _int32, _raw_stream, _current_device, _capturing
-    _torch, _int32 = torch, torch.int32
+    global _torch, _int32, _contiguous, _raw_stream, _current_device, _capturing
+    _torch, _int32, _contiguous = torch, torch.int32, torch.contiguous_format
     _raw_stream = torch._C._cuda_getCurrentRawStream
     _current_device = torch._C._cuda_getDevice
     _capturing = torch._C._cuda_isCurrentStreamCapturing
