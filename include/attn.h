@@ -152,9 +152,9 @@ ATTN_API int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, 
  *   dlse   [B, H, Sq] fp32 or NULL (zero)
  *   dq, dk, dv  as q, k, v, but in dtype's output type; all are written whole
  *   H >= 1 a multiple of H_kv >= 1; d, dtype, causal, scale as attn_fwd
- *   workspace  16-byte aligned scratch of attn_bwd_workspace_size bytes.  Calls
- *          that may overlap on the GPU, replays of graphs among them, need
- *          workspaces of their own.
+ *   workspace  16-byte aligned scratch of attn_bwd_workspace_size bytes (NULL if
+ *          that is 0).  Calls that may overlap on the GPU, replays of graphs
+ *          among them, need workspaces of their own.
  * A row with lse = -inf (no visible key) contributes nothing and gets dq = 0,
  * whatever its o, do and dlse hold, as long as they are finite.  Skv == 0
  * writes dq = 0; Sq == 0 writes dk = dv = 0.  Infinities and NaN in a row of
@@ -163,7 +163,7 @@ ATTN_API int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, 
  * operands of the products (fp16: after scaling by powers of two that keep
  * them in range).  Sums are made in a fixed order: equal calls give equal bits.
  * All arrays must be distinct; q, k, v, o, do and gradients 16-byte aligned.
- * Two kernels, three where few units share a long walk.
+ * Two kernels (fp32: one), one more where few units share a long walk.
  */
 ATTN_API int attn_bwd_workspace_size(int B, int H, int H_kv, int Sq, int Skv, int d, int causal,
                             int dtype, size_t *bytes);

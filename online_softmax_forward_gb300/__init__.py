@@ -500,17 +500,19 @@ def attention_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None
     else:
         dq, dk, dv = (_new(stream, s, odt, dev) for s in (shape, kshape, kshape))
     need = _need(attn_bwd_workspace_size, B, H, H_kv, Sq, Skv, d, bool(causal), code)
-    if workspace is None:  # belongs to the call's stream, or to the graph that captures it
-        workspace = _new(stream, need, _torch.uint8, dev)
-        wn = need
+    wp, wn = None, 0
+    if workspace is None:
+        if need:  # belongs to the call's stream, or to the graph that captures it
+            workspace = _new(stream, need, _torch.uint8, dev)
+            wp, wn = workspace.data_ptr(), need
     elif not workspace.is_contiguous() or _device_of(workspace) != dev:
         raise ValueError("workspace must be a contiguous tensor on %s" % dev)
     else:
-        wn = workspace.numel() * workspace.element_size()
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call_on(dev, load_library().attn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
              lse.data_ptr(), do.data_ptr(), None if dlse is None else dlse.data_ptr(),
              dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, H_kv, Sq, Skv, d, 1 if causal else 0,
-             0.0 if scale is None else float(scale), code, workspace.data_ptr(), wn, handle)
+             0.0 if scale is None else float(scale), code, wp, wn, handle)
     return dq, dk, dv
 
 

@@ -428,7 +428,7 @@ int attn_bwd(const void *q, const void *k, const void *v, const void *o, const f
                         {dlse, dlse ? rows : 0, 4, false, false},
                         {dq, nq * eout, 16, nq > 0, true},    {dk, nkv * eout, 16, nkv > 0, true},
                         {dv, nkv * eout, 16, nkv > 0, true},
-                        {workspace, work ? plan.bytes : 0, 16, work, true}};
+                        {workspace, work ? plan.bytes : 0, 16, work && plan.bytes > 0, true}};
     const int n = (int)(sizeof(args) / sizeof(args[0]));
     for (int i = 0; i < n; ++i) {
         if (args[i].needed && !args[i].ptr) return ATTN_ERR_INVALID_ARG;

@@ -17,18 +17,25 @@ bool bwd_plan(const Problem &p, BwdPlan *plan) {
     const double est = 4.0 * 2 * kMaxBwdSplits * ((double)bh * (p.Sq + 128.0) + (double)bhk * (p.Skv + 128.0)) *
                        (p.d + 2.0);
     if (est > 4.0e18) return false;
-    plan->tile = f32 ? 64 : 128;
-    plan->nq = (p.Sq + plan->tile - 1) / plan->tile;
-    plan->nk = (p.Skv + plan->tile - 1) / plan->tile;
+    // rows of a unit's own tile and of the tiles it walks over
+    const int step = f32 ? 64 : 128;
+    auto tiles = [](int n, int tile) { return (n + tile - 1) / tile; };
+    auto units_of = [&](int tile) { return (double)bhk * tiles(p.Skv, tile) + (double)bh * tiles(p.Sq, tile); };
+    plan->tile = step;
+    // fp32: smaller units while they do not fill the places of two CTAs an SM
+    if (f32)
+        while (plan->tile > 16 && units_of(plan->tile) < 1.5 * kBwdSms) plan->tile /= 2;
+    plan->nq = tiles(p.Sq, plan->tile);
+    plan->nk = tiles(p.Skv, plan->tile);
     plan->ns_kv = plan->ns_q = 1;
-    // Costs in products of a tile: a kv unit makes four a step, a q unit three.  A unit
+    // Costs in products of a step: a kv unit makes four a step, a q unit three.  A unit
     // longer than three quarters of an SM's share of everything would be what the
-    // launch waits for, so it is cut; but not below eight steps (fp32, whose
-    // steps are long: one), where the partial sums and their kernel cost more than they give.
-    const double len_kv = 4.0 * p.group * plan->nq, len_q = 3.0 * plan->nk;
+    // launch waits for, so it is cut; but not below eight steps, where the partial sums
+    // and their kernel cost more than they give.
+    const double len_kv = 4.0 * p.group * tiles(p.Sq, step), len_q = 3.0 * tiles(p.Skv, step);
     const double share = ((double)bhk * plan->nk * len_kv + (double)bh * plan->nq * len_q) / kBwdSms *
                          (p.causal && p.Sq == p.Skv ? 0.5 : 1.0);
-    const double least = f32 ? 4.0 : 32.0;
+    const double least = 32.0;
     const double goal = share * 0.75 > least ? share * 0.75 : least;
     auto cut = [&](double len) {
         const double n = ceil(len / goal);
@@ -40,10 +47,9 @@ bool bwd_plan(const Problem &p, BwdPlan *plan) {
     if (units > (double)(INT32_MAX / 2)) return false;
     plan->n_units = (int64_t)units;
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
-    const size_t tiles = ((size_t)p.Sq + kStatTile - 1) / kStatTile;
-    plan->off_stats = 256;
-    plan->off_max = plan->off_stats + up((size_t)bh * tiles * 2 * kStatTile * 4);
-    plan->off_part_kv = plan->off_max + up(3 * (size_t)kPreBlocks * 4);
+    plan->off_stats = f32 ? 0 : 256;  // fp32 units compute the statistics themselves
+    plan->off_max = plan->off_stats + (f32 ? 0 : up((size_t)bh * tiles(p.Sq, kStatTile) * 2 * kStatTile * 4));
+    plan->off_part_kv = plan->off_max + (f32 ? 0 : up(3 * (size_t)kPreBlocks * 4));
     plan->off_part_q = plan->off_part_kv +
                        (plan->ns_kv > 1 ? up((size_t)plan->ns_kv * bhk * p.Skv * p.d * 2 * 4) : 0);
     plan->bytes = plan->off_part_q + (plan->ns_q > 1 ? up((size_t)plan->ns_q * bh * p.Sq * p.d * 4) : 0);
@@ -58,7 +64,7 @@ constexpr int kSumThreads = 256;
 template <typename T>
 __device__ __forceinline__ float to_f(T x);
 template <>
-__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(float x) { return x; }  // of o
 template <>
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <>
@@ -257,17 +263,9 @@ int launch_bwd(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStre
     r.add = f16 ? (float)kBwdP16Log2 : 0.f;
     r.status = status_word_device_ptr();
     if (!r.status) return ATTN_ERR_CUDA;
-    int st = ATTN_ERR_INVALID_ARG;
-    if (p.dtype == ATTN_F32) {
-        switch (p.d) {
-        case 16: st = launch_stats<float, float, 16, false>(r, stream); break;
-        case 32: st = launch_stats<float, float, 32, false>(r, stream); break;
-        case 64: st = launch_stats<float, float, 64, false>(r, stream); break;
-        case 128: st = launch_stats<float, float, 128, false>(r, stream); break;
-        }
-    } else if (p.d == 64 || p.d == 128) {
+    int st = ATTN_OK;
+    if (p.dtype != ATTN_F32)
         st = p.d == 64 ? stats_16<64>(r, p.dtype, stream) : stats_16<128>(r, p.dtype, stream);
-    }
     if (st != ATTN_OK) return st;
     st = p.dtype == ATTN_F32 ? launch_bwd_f32(a, p, plan, stream) : launch_bwd_tc(a, p, plan, stream);
     if (st != ATTN_OK || (plan.ns_kv == 1 && plan.ns_q == 1)) return st;

@@ -19,9 +19,10 @@
 // walks are cut into splits that leave fp32 partial sums in the workspace,
 // and a last kernel adds those in order.
 //
-// A first kernel writes what both kinds need of each query row: nl = -lse
-// log2(e) (-inf for a row that sees no key, so that its P is 0) and nd = -D,
-// as [B * H][query tiles of 128][2][128], rows behind Sq with nl = -inf, nd = 0.
+// Both kinds need of each query row: nl = -lse log2(e) (-inf for a row that sees
+// no key, so that its P is 0) and nd = -D.  For the 16-bit types a first kernel
+// writes them as [B * H][query tiles of 128][2][128], rows behind Sq with nl =
+// -inf, nd = 0; fp32 units compute them as they load do.
 #pragma once
 
 #include <stddef.h>
@@ -38,8 +39,8 @@ constexpr int kBwdP16Log2 = 14;  // fp16: P is kept times 2^14, so that small we
 constexpr int kPreBlocks = 1216; // CTAs of the first kernel at most
 
 struct BwdPlan {
-    int tile;           // rows of a tile
-    int nq, nk;         // query and key tiles
+    int tile;           // rows of a unit's own tile
+    int nq, nk;         // query and key tiles of that size
     int ns_kv, ns_q;    // splits of a kv unit and of a q unit
     int64_t n_units;
     size_t off_stats, off_max, off_part_kv, off_part_q, bytes;
@@ -56,7 +57,7 @@ struct BwdArgs {
 // False if the problem is too large to number.
 bool bwd_plan(const Problem &p, BwdPlan *plan);
 
-// The kernels in order: row statistics, gradients, sum of the splits.
+// The kernels in order: row statistics (16-bit types), gradients, sum of the splits.
 int launch_bwd(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream);
 int launch_bwd_tc(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream);
 int launch_bwd_f32(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream);

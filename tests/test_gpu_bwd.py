@@ -112,8 +112,8 @@ def test_gradients(c):
 ])
 def test_splits(dt, d, Sq, Skv, causal, H, Hkv):
     st, need = pkg.attn_bwd_workspace_size(1, H, Hkv, Sq, Skv, d, causal, pkg.dtype_code(dt))
-    rows = H * -(-Sq // 128) * 128 * 8
-    assert st == pkg.ATTN_OK and need > rows + 16384  # partial sums beside the rows and 15 KB of the rest
+    fixed = 0 if dt == F else H * -(-Sq // 128) * 128 * 8 + 16384  # row statistics and 15 KB of the rest
+    assert st == pkg.ATTN_OK and need > fixed  # partial sums are kept
     check(make(1, H, Hkv, Sq, Skv, d, dt, seed=5, causal=causal), causal)
 
 
