@@ -450,7 +450,7 @@ int attn_bwd(const void *q, const void *k, const void *v, const void *o, const f
         return ATTN_OK;
     }
     const BwdArgs a{q, k, v, o, do_, lse, dlse, dq, dk, dv, workspace};
-    return launch_bwd(a, p, plan, (cudaStream_t)stream);
+    return launch_bwd(a, plan, (cudaStream_t)stream);
 }
 
 // Rows of attn_rotary: pointers, strides, and an output that does not overlap itself.

@@ -10,7 +10,18 @@
 
 namespace attn {
 
-bool bwd_plan(const Problem &p, BwdPlan *plan) {
+bool bwd_plan(const Problem &call, BwdPlan *plan) {
+    Problem p = call;
+    plan->off = call.Skv - call.Sq;
+    plan->wrap = 0;
+    if (p.group > 1 && (!p.causal || p.Sq <= kStatTile) && (int64_t)p.group * p.Sq <= INT32_MAX - kStatTile) {
+        p.H /= p.group;
+        p.Sq *= p.group;
+        p.group = 1;
+        if (p.causal) plan->wrap = call.Sq;
+    }
+    plan->p = p;
+    if (p.Sq > INT32_MAX - 1024 || p.Skv > INT32_MAX - 1024) return false;  // ends of tiles fit 31 bits
     const bool f32 = p.dtype == ATTN_F32;
     const int64_t bh = p.bh(), bhk = p.bh_kv();
     // the sizes below are products of these; anything near 2^62 bytes is refused first
@@ -34,7 +45,7 @@ bool bwd_plan(const Problem &p, BwdPlan *plan) {
     // and their kernel cost more than they give.
     const double len_kv = 4.0 * p.group * tiles(p.Sq, step), len_q = 3.0 * tiles(p.Skv, step);
     const double share = ((double)bhk * plan->nk * len_kv + (double)bh * plan->nq * len_q) / kBwdSms *
-                         (p.causal && p.Sq == p.Skv ? 0.5 : 1.0);
+                         (p.causal && call.Sq == call.Skv ? 0.5 : 1.0);
     const double least = 32.0;
     const double goal = share * 0.75 > least ? share * 0.75 : least;
     auto cut = [&](double len) {
@@ -244,7 +255,8 @@ int stats_16(const PreParams &p, int dtype, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_bwd(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream) {
+int launch_bwd(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream) {
+    const Problem &p = plan.p;
     uint8_t *ws = (uint8_t *)a.workspace;
     const bool f16 = p.dtype == ATTN_F16 || p.dtype == ATTN_F16_OUT_F32;
     PreParams r{};
@@ -267,7 +279,7 @@ int launch_bwd(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStre
     if (p.dtype != ATTN_F32)
         st = p.d == 64 ? stats_16<64>(r, p.dtype, stream) : stats_16<128>(r, p.dtype, stream);
     if (st != ATTN_OK) return st;
-    st = p.dtype == ATTN_F32 ? launch_bwd_f32(a, p, plan, stream) : launch_bwd_tc(a, p, plan, stream);
+    st = p.dtype == ATTN_F32 ? launch_bwd_f32(a, plan, stream) : launch_bwd_tc(a, plan, stream);
     if (st != ATTN_OK || (plan.ns_kv == 1 && plan.ns_q == 1)) return st;
     SumParams s{};
     int64_t most = 0;

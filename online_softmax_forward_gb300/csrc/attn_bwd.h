@@ -39,6 +39,9 @@ constexpr int kBwdP16Log2 = 14;  // fp16: P is kept times 2^14, so that small we
 constexpr int kPreBlocks = 1216; // CTAs of the first kernel at most
 
 struct BwdPlan {
+    Problem p;          // the problem the kernels run, see below
+    int off;            // key j is visible to the query at position i iff j <= i + off
+    int wrap;           // 0, or query rows of a head, where p's rows are those of several heads
     int tile;           // rows of a unit's own tile
     int nq, nk;         // query and key tiles of that size
     int ns_kv, ns_q;    // splits of a kv unit and of a q unit
@@ -55,11 +58,18 @@ struct BwdArgs {
 
 // The plan follows from the sizes alone, so that the workspace does too.
 // False if the problem is too large to number.
+//
+// The query heads that share a kv head lie one behind the other, so that their
+// rows can be walked as the rows of one head (plan.p: H_kv heads of group * Sq
+// rows), with fewer tiles left partly empty.  Without a causal mask this is
+// always done; with one for up to a tile of queries, where a row's position is
+// its number modulo Sq (longer ones would lose the key tiles that the mask
+// leaves out).
 bool bwd_plan(const Problem &p, BwdPlan *plan);
 
 // The kernels in order: row statistics (16-bit types), gradients, sum of the splits.
-int launch_bwd(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream);
-int launch_bwd_tc(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream);
-int launch_bwd_f32(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream);
+int launch_bwd(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream);
+int launch_bwd_tc(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream);
+int launch_bwd_f32(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream);
 
 }  // namespace attn

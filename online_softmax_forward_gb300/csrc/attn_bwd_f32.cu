@@ -46,6 +46,7 @@ struct Params {
     const float *lse, *dlse;
     float *dk, *dv, *dq;  // gradients, or the splits' partial sums
     int BH, BHk, group, Sq, Skv, causal;
+    int off, wrap;   // of BwdPlan
     int nq, nk;      // X tiles of a slice: query rows, keys
     int yq;          // Y tiles of query rows of a slice
     int ns_kv, ns_q;
@@ -139,7 +140,6 @@ attn_bwd_f32_kernel(const Params p) {
     float *nls = sm + C::kOffStat, *nds = nls + kT;  // of the query rows of Y or of X
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tx = (warp & 1) * 8 + (lane & 7), ty = (warp >> 1) * 4 + (lane >> 3);
-    const int off = p.Skv - p.Sq;
 
     // the unit: kv units first, longest first where the call is causal
     const int n_kv = p.BHk * p.nk * p.ns_kv;
@@ -151,12 +151,13 @@ attn_bwd_f32_kernel(const Params p) {
     const int zx = u / ns, split = u - zx * ns;
     if (!kv && p.causal) tile = p.nq - 1 - tile;
     const int x0 = tile * X;
-    const int first = kv && p.causal ? max(0, x0 - off) / kT : 0;
+    const bool skips = p.causal && !p.wrap;  // whole tiles that the mask leaves out
+    const int first = kv && skips ? max(0, x0 - p.off) / kT : 0;
     int per;  // steps of a head
     if (kv) {
         per = p.yq - first;
     } else {
-        const int end = p.causal ? min(p.Skv, min(x0 + X, p.Sq) + off) : p.Skv;
+        const int end = skips ? min(p.Skv, min(x0 + X, p.Sq) + p.off) : p.Skv;
         per = end > 0 ? (end + kT - 1) / kT : 0;
     }
     const int64_t steps = (int64_t)per * (kv ? p.group : 1);
@@ -204,7 +205,8 @@ attn_bwd_f32_kernel(const Params p) {
             for (int j = 0; j < 4; ++j) {
                 const int xi = tx + 16 * i, yi = ty + 16 * j;
                 const int qi = kv ? y0 + yi : x0 + xi, kj = kv ? x0 + xi : y0 + yi;
-                const bool seen = kj < p.Skv && (!p.causal || kj <= qi + off);
+                const int pos = p.wrap ? qi % p.wrap : qi;
+                const bool seen = kj < p.Skv && (!p.causal || kj <= pos + p.off);
                 const float l = nls[kv ? yi : xi], d = nds[kv ? yi : xi];
                 const float pr = seen ? ptx::ex2_approx(fmaf(T1[i][j], p.scale_log2, l)) : 0.f;
                 if (kv) Ps[yi * LP + xi] = pr;
@@ -284,7 +286,8 @@ int launch_d(const Params &p, const BwdPlan &plan, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_bwd_f32(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
+int launch_bwd_f32(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream) {
+    const Problem &pr = plan.p;
     uint8_t *ws = (uint8_t *)a.workspace;
     Params p{};
     p.q = (const float *)a.q;
@@ -300,6 +303,8 @@ int launch_bwd_f32(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cud
     p.Sq = pr.Sq;
     p.Skv = pr.Skv;
     p.causal = pr.causal;
+    p.off = plan.off;
+    p.wrap = plan.wrap;
     p.nq = plan.nq;
     p.nk = plan.nk;
     p.ns_kv = plan.ns_kv;

@@ -114,7 +114,7 @@ struct Bars {
     uint64_t st_full[kStatStages], st_empty[kStatStages];
     uint64_t t1_full, p_full;      // T1 computed; T1 read (q unit) or P written (kv unit)
     uint64_t t2_full[2], ds_full[2];  // T2 computed; dS written (of each buffer)
-    uint64_t acc_full, acc_empty;
+    uint64_t acc_full[2], acc_empty;  // A1 and A2 of a unit complete; both read
     uint64_t mma_done;
     uint64_t sched_full[kSchedRing], sched_empty[kSchedRing];
     Unit sched_unit[kSchedRing];
@@ -130,10 +130,12 @@ struct Params {
     unsigned *counter;
     void *dk, *dv, *dq;               // gradients, or the splits' partial sums
     int BH, BHk, group, Sq, Skv, causal;
+    int off, wrap;  // of BwdPlan
     int nq, nk, ns_kv, ns_q;
     int hg;       // kv slices per schedule group
     int n_units;
     int kv_f32, q_f32;  // fp32 output of dk and dv, of dq
+    int wide;           // the outputs are 32-byte aligned
     float scale_log2, scale;
     int *status;
     unsigned long long timeout_ns;
@@ -148,7 +150,7 @@ __device__ __forceinline__ Unit decode_unit(int u, const Params &p) {
     const int g = u / per_group;
     int rem = u - g * per_group;
     const int heads = min(p.hg, p.BHk - g * p.hg);
-    const int off = p.Skv - p.Sq;
+    const bool skips = p.causal && !p.wrap;  // whole tiles that the mask leaves out
     if (rem < heads * a_head) {
         const int width = heads * p.ns_kv;
         const int tile = rem / width;
@@ -158,7 +160,7 @@ __device__ __forceinline__ Unit decode_unit(int u, const Params &p) {
         r.kind = 0;
         r.zx = g * p.hg + head;
         r.x0 = tile * kRows;
-        r.first = p.causal ? max(0, r.x0 - off) / kRows : 0;
+        r.first = skips ? max(0, r.x0 - p.off) / kRows : 0;
         const int per = p.nq - r.first;  // query tiles of a head that see the tile
         const int64_t steps = (int64_t)per * p.group;
         const int t0 = (int)(steps * r.split / p.ns_kv), t1 = (int)(steps * (r.split + 1) / p.ns_kv);
@@ -179,7 +181,7 @@ __device__ __forceinline__ Unit decode_unit(int u, const Params &p) {
         r.zy = r.zx / p.group;
         r.x0 = tile * kRows;
         r.first = 0;
-        const int end = p.causal ? min(p.Skv, min(r.x0 + kRows, p.Sq) + off) : p.Skv;
+        const int end = skips ? min(p.Skv, min(r.x0 + kRows, p.Sq) + p.off) : p.Skv;
         const int steps = end > 0 ? (end + kRows - 1) / kRows : 0;
         const int t0 = (int)((int64_t)steps * r.split / p.ns_q), t1 = (int)((int64_t)steps * (r.split + 1) / p.ns_q);
         r.y = t0;
@@ -213,6 +215,18 @@ __device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
+}
+
+// 32 bytes to global memory, as a whole sector where the address allows it.
+__device__ __forceinline__ void st_global_v8(uint32_t *dst, const uint32_t *v, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
 }
 
 // One arrival for a whole warp, after what all its lanes did.
@@ -270,7 +284,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         ptx::mbar_init(bar(bars->t1_full), 1);
         ptx::mbar_init(bar(bars->p_full), kComputeWarps);
-        ptx::mbar_init(bar(bars->acc_full), 1);
+        for (int t = 0; t < 2; ++t) ptx::mbar_init(bar(bars->acc_full[t]), 1);
         ptx::mbar_init(bar(bars->acc_empty), kComputeWarps);
         ptx::mbar_init(bar(bars->mma_done), 1);
         for (int s = 0; s < kSchedRing; ++s) {
@@ -500,6 +514,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ptx::tc_fence_after();
                     issue_a(kColA1, kColT1, 1, pos + i, i > 0);
                     free_slot(1, pos + i);
+                    if (i == n - 1) ptx::mma_commit_warp(bar(bars->acc_full[0]));
                 }
                 if (i + 1 < n) {
                     ok = t1(i + 1);
@@ -515,7 +530,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (kv && i + 1 < n) ok = t2(i + 1);
             }
             if (!ok) break;
-            ptx::mma_commit_warp(bar(bars->acc_full));
+            ptx::mma_commit_warp(bar(bars->acc_full[1]));
             ++un;
             pos += n;
         }
@@ -529,14 +544,18 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int r = (warp & 3) * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float ds_scale = kBF16 ? 1.f : bars->ds_scale;
-        uint32_t n1 = 0, n2[2] = {0, 0}, sn = 0, an = 0;
+        uint32_t n1 = 0, n2[2] = {0, 0}, sn = 0, an[2] = {0, 0};
         bool ok = true;
 
         // The steps of one unit, one row and 64 columns a thread.
         auto steps = [&](auto kind, const Unit &w) {
             constexpr bool KV = decltype(kind)::value;
             const int row = w.x0 + r;
-            const int off = p.Skv - p.Sq;
+            const int off = p.off;
+            // q unit: this row's position, and the first key that a row of the tile may not see
+            const int pos = p.wrap ? row % p.wrap : row;
+            const int sees = KV ? 0 : min(p.Skv, p.causal ? pos + off + 1 : p.Skv);
+            const int all_see = KV ? 0 : min(p.Skv, p.causal ? (p.wrap ? 0 : w.x0) + off + 1 : p.Skv);
             const float2 sc = make_float2(p.scale_log2, p.scale_log2);
             float rl = 0.f, rd = 0.f;  // q unit: nl and nd of this thread's row
             if constexpr (!KV) {
@@ -568,20 +587,27 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ptx::tc_fence_before();
                     arrive_warp(bar(bars->p_full), lane);
                 }
-                const bool masked = KV ? (p.causal && w.x0 + kRows - 1 > y0 + off)
-                                       : y0 + kRows > min(p.Skv, p.causal ? w.x0 + off + 1 : p.Skv);
+                const bool masked = KV ? p.causal && w.x0 + kRows - 1 > (p.wrap ? 0 : y0) + off : y0 + kRows > all_see;
                 if (masked) {  // scores of pairs that do not see each other: -inf
-                    // columns visible to the row: [lo, hi)
-                    const int lo = (KV ? row - off - y0 : 0) - half * 64;
-                    const int hi = (KV ? kRows : min(p.Skv, p.causal ? row + off + 1 : p.Skv) - y0) - half * 64;
+                    if (KV && p.wrap) {
+                        int at = (y0 + half * 64) % p.wrap;  // position of the query of column j
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (KV ? j < lo : j >= hi) a[j >> 5][j & 31] = __float_as_uint(-INFINITY);
+                        for (int j = 0; j < 64; ++j) {
+                            if (row > at + off) a[j >> 5][j & 31] = __float_as_uint(-INFINITY);
+                            if (++at == p.wrap) at = 0;
+                        }
+                    } else {
+                        // columns visible to the row: from lo on, or below hi
+                        const int lo = row - off - y0 - half * 64, hi = sees - y0 - half * 64;
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (KV ? j < lo : j >= hi) a[j >> 5][j & 31] = __float_as_uint(-INFINITY);
+                    }
                 }
                 float2 pr[32];
                 uint32_t pk[32];
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
+                // P = exp2(scores)
+                auto weights = [&](int j) {
                     const uint32_t *s = &a[j >> 4][(2 * j) & 31];
                     float4 l = make_float4(rl, rl, rl, rl);
                     if constexpr (KV) l = ld_shared_v4(st + j * 8);
@@ -589,12 +615,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), sc, make_float2(l.z, l.w));
                     pr[j] = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
                     pr[j + 1] = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
-                    if constexpr (KV) {
+                };
+                if constexpr (KV) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        weights(j);
                         pk[j] = pack2<kBF16>(pr[j].x, pr[j].y);
                         pk[j + 1] = pack2<kBF16>(pr[j + 1].x, pr[j + 1].y);
                     }
-                }
-                if constexpr (KV) {
                     ptx::tmem_st32(tT1, pk);
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
@@ -606,14 +634,16 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!__all_sync(0xffffffffu, got)) return false;
                 ptx::tc_fence_after();
                 const uint32_t tT2 = tl + (buf ? kColT2b : kColT2) + half * 64;
-                ptx::tmem_ld32(tT2, a[0]);
-                ptx::tmem_ld32(tT2 + 32, a[1]);
+                uint32_t b[2][32];
+                ptx::tmem_ld32(tT2, b[0]);
+                ptx::tmem_ld32(tT2 + 32, b[1]);
                 ptx::tmem_wait_ld();
-                reg_fence(a[0]);
-                reg_fence(a[1]);
+                reg_fence(b[0]);
+                reg_fence(b[1]);
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
-                    const uint32_t *s = &a[j >> 4][(2 * j) & 31];
+                    if constexpr (!KV) weights(j);  // both tiles are here: exponentials and products mixed
+                    const uint32_t *s = &b[j >> 4][(2 * j) & 31];
                     float4 l = make_float4(rd, rd, rd, rd);
                     if constexpr (KV) l = ld_shared_v4(st + kStatTile * 4 + j * 8);
                     float2 x = __fadd2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), make_float2(l.x, l.y));
@@ -649,13 +679,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = kv ? steps(std::true_type{}, w) : steps(std::false_type{}, w);
             if (!ok) break;
 
-            // ---- the unit's sums: dk and dv, or dq
-            if (w.n > 0) {
-                const bool got = watch.wait(bar(bars->acc_full), an & 1);
-                ++an;
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                ptx::tc_fence_after();
-            }
+            // ---- the unit's sums: dv (while A2 of the last step runs) and dk, or dq
             const int rows = kv ? p.Skv : p.Sq;
             const int64_t slices = kv ? p.BHk : p.BH;
             const bool f32 = kv ? p.kv_f32 : p.q_f32;
@@ -664,6 +688,12 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const size_t at = (part + (size_t)w.zx * rows + row) * D + half * (D / 2);
 #pragma unroll 1
             for (int m = kv ? 0 : 1; m < 2; ++m) {  // 0: A1 (dv), 1: A2 (dk or dq)
+                if (w.n > 0) {
+                    const bool got = watch.wait(bar(bars->acc_full[m]), (m ? an[1] : an[0]) & 1);
+                    if (m) ++an[1]; else ++an[0];
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                }
                 void *dst = m == 0 ? p.dv : kv ? p.dk : p.dq;
                 const float f = m == 0 ? (kBF16 ? 1.f : 1.f / (1 << kBwdP16Log2))
                                        : (kBF16 ? p.scale : p.scale / (ds_scale * (1 << kBwdP16Log2)));
@@ -675,35 +705,30 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         ptx::tmem_ld32(tl + (m == 0 ? kColA1 : kColA2) + half * (D / 2) + c * 32, o);
                         ptx::tmem_wait_ld();
                         reg_fence(o);
+                        if (m == 1 && c == D / 64 - 1) {  // read: the next unit's sums may begin
+                            ptx::tc_fence_before();
+                            arrive_warp(bar(bars->acc_empty), lane);
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0u;
                     }
                     const size_t g = at + c * 32;
                     if (row >= rows || !in_bounds(g + 32 <= extent, p.status)) continue;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                     if (f32) {
-                        float4 *d4 = reinterpret_cast<float4 *>(reinterpret_cast<float *>(dst) + g);
+                        uint32_t *d = reinterpret_cast<uint32_t *>(dst) + g;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            d4[i] = make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
-                                                __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+                        for (int i = 0; i < 32; i += 8) st_global_v8(d + i, o + i, p.wide);
                     } else {
-                        uint4 *d4 = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(dst) + g);
+                        uint32_t *d = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(dst) + g);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint4 v;
-                            v.x = pack2<kBF16>(__uint_as_float(o[8 * i]) * f, __uint_as_float(o[8 * i + 1]) * f);
-                            v.y = pack2<kBF16>(__uint_as_float(o[8 * i + 2]) * f, __uint_as_float(o[8 * i + 3]) * f);
-                            v.z = pack2<kBF16>(__uint_as_float(o[8 * i + 4]) * f, __uint_as_float(o[8 * i + 5]) * f);
-                            v.w = pack2<kBF16>(__uint_as_float(o[8 * i + 6]) * f, __uint_as_float(o[8 * i + 7]) * f);
-                            d4[i] = v;
-                        }
+                        for (int i = 0; i < 16; ++i) o[i] = pack2<kBF16>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+#pragma unroll
+                        for (int i = 0; i < 16; i += 8) st_global_v8(d + i, o + i, p.wide);
                     }
                 }
-            }
-            if (w.n > 0) {
-                ptx::tc_fence_before();
-                arrive_warp(bar(bars->acc_empty), lane);
             }
         }
     } else {
@@ -736,6 +761,8 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
     p.Sq = pr.Sq;
     p.Skv = pr.Skv;
     p.causal = pr.causal;
+    p.off = plan.off;
+    p.wrap = plan.wrap;
     p.nq = plan.nq;
     p.nk = plan.nk;
     p.ns_kv = plan.ns_kv;
@@ -750,6 +777,7 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
     p.dk = plan.ns_kv > 1 ? part_kv : a.dk;
     p.dv = plan.ns_kv > 1 ? part_kv + (size_t)plan.ns_kv * pr.bh_kv() * pr.Skv * D : a.dv;
     p.dq = plan.ns_q > 1 ? (void *)(ws + plan.off_part_q) : a.dq;
+    p.wide = ((uintptr_t)p.dk | (uintptr_t)p.dv | (uintptr_t)p.dq) % 32 == 0;
     const int sms = device_sm_count();
     p.status = status_word_device_ptr();
     if (sms <= 0 || !p.status) return ATTN_ERR_CUDA;
@@ -788,7 +816,8 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
 
 }  // namespace
 
-int launch_bwd_tc(const BwdArgs &a, const Problem &p, const BwdPlan &plan, cudaStream_t stream) {
+int launch_bwd_tc(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream) {
+    const Problem &p = plan.p;
     const bool bf16 = p.dtype == ATTN_BF16 || p.dtype == ATTN_BF16_OUT_F32;
     if (p.d == 128)
         return bf16 ? launch_typed<128, true>(a, p, plan, stream) : launch_typed<128, false>(a, p, plan, stream);

@@ -61,6 +61,12 @@ CASES = [
     (3, 2, 2, 127, 129, 64, False, BF),
     (1, 4, 4, 1000, 1000, 64, True, BF),
     (1, 40, 40, 300, 300, 128, True, BF),   # more units than SMs
+    (1, 8, 2, 77, 900, 128, True, BF),      # few queries: the heads of a kv head share tiles
+    (2, 16, 1, 100, 700, 64, True, HF),
+    (1, 6, 2, 100, 60, 64, True, BF),       # ... with rows without a key
+    (2, 5, 1, 128, 128, 128, True, BF),
+    (1, 4, 1, 3, 130, 64, True, F),
+    (1, 6, 3, 90, 50, 32, True, F),
     (2, 4, 4, 64, 64, 16, True, F),
     (1, 1, 1, 64, 64, 32, True, F),
     (1, 2, 2, 1, 1, 64, False, F),

@@ -38,6 +38,7 @@ BAD = [
     dict(dtype=5), dict(dtype=-1), dict(causal=2), dict(causal=-1), dict(scale=math.nan),
     dict(scale=math.inf), dict(B=1 << 20, H=1 << 12, H_kv=1 << 12),
     dict(B=1 << 15, H=1 << 15, H_kv=1 << 15, Sq=1 << 30, Skv=1 << 30),
+    dict(B=1, H=1, H_kv=1, Sq=(1 << 31) - 1, Skv=8), dict(B=1, H=1, H_kv=1, Sq=8, Skv=(1 << 31) - 1000),
 ]
 
 
