@@ -1,18 +1,32 @@
-// attn_bwd_f32.cu -- fp32 backward pass of attention on CUDA cores (attn_bwd.h
-// has the formulas and the two kinds of units).
+// attn_bwd_f32.cu -- fp32 backward pass of attention (attn_bwd.h has the
+// formulas and the two kinds of units).
 //
 // A CTA of 256 threads runs one unit: tiles X1, X2 of 16 R rows stay in shared
 // memory, tiles Y1, Y2 of 64 rows stream through it (kv unit: X = k, v and Y =
 // q, do; q unit: X = q, do and Y = k, v).  Each step makes
-//     T1 = X1 Y1^T, T2 = X2 Y2^T   (R x 4 results a thread, 16 bytes a load)
+//     T1 = X1 Y1^T, T2 = X2 Y2^T
 //     P = exp2(scale log2(e) T1 + nl), dS = P (T2 + nd)
-//     A2 += dS Y1, and in a kv unit A1 += P Y2   (R rows x D / 16 channels a thread)
-// with P and dS passed through shared memory between the two.  The row
-// statistics are computed where do is loaded (o is read once more for each kv
-// unit, which costs less than a kernel of its own), so that a small problem is
-// one launch.  What bounds it is the FP32 FMA rate: rows are padded so that
-// no load meets a bank twice.  R (attn_bwd.cu) is the largest of 4, 2 and 1
-// that gives enough units to fill the GPU: 4 has the most FMAs a load.
+//     A2 += dS Y1, and in a kv unit A1 += P Y2
+// A warp owns 16 rows of X and its share of the 64 columns.
+//
+//  * Products.  fp32 FMAs are bound by what shared memory delivers to registers
+//    (4 x 4 results a thread: 22 TFLOP/s of 74), so the products run on the tensor
+//    cores, each fp32 number as the sum of two tf32 ones, hi (rounded to 11
+//    bits) and lo = x - hi: x y = hi hi + hi lo + lo hi, wrong by 2^-21 of |x y| at
+//    most, over fp32's whole range.  mma.sync: its fragments come from plain
+//    fp32 tiles of any width and stay in registers; tcgen05 would want both
+//    parts of every tile in shared memory, which two tiles of 64 rows fill.
+//  * P and dS never leave registers: the accumulator of T holds columns 2 t, 2 t +
+//    1 where the left operand of A wants k = t, t + 4, which is only another
+//    order of the summed rows, so Y's rows are read in that order.
+//  * The tensor cores' sums round towards zero.  T adds its large products (hi hi)
+//    apart from the small ones, and A's sums of a step start at zero and are
+//    added to the unit's in fp32, so that no sum takes more than 16 such roundings.
+//  * The row statistics are computed where do is loaded (o is read once more for
+//    each kv unit, which costs less than a kernel of its own), so that a small
+//    problem is one launch.
+// R (attn_bwd.cu) is the largest of 4, 2 and 1 that gives enough units to fill the
+// GPU; the 8 / R warps that share rows add their sums at the end, in order.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -28,17 +42,16 @@ constexpr int kThreads = 256;
 
 template <int D, int R>
 struct Cfg {
-    static constexpr int kX = 16 * R;  // rows of an X tile
+    static constexpr int kX = 16 * R;      // rows of an X tile
+    static constexpr int kWY = 8 / R;      // warps that share rows of X
+    static constexpr int kN = kT / kWY / 8;  // 8-column tiles of T a warp
     static constexpr int kLd = D + 4;
-    static constexpr int kLdP = kX + 8;  // row stride of P and dS
     static constexpr int kOffY = 2 * kX * kLd;
-    static constexpr int kOffP = kOffY + 2 * kT * kLd;
-    static constexpr int kOffStat = kOffP + 2 * kT * kLdP;
+    static constexpr int kOffStat = kOffY + 2 * kT * kLd;
     static constexpr int kSmemBytes = (kOffStat + 2 * kT) * 4;
-    // CTAs an SM that shared memory allows, two at most
-    static constexpr int kCtas = 2 * kSmemBytes + 2048 <= 233472 ? 2 : 1;
-    static constexpr int kW = D >= 64 ? 4 : D / 16;  // channels of a load of the sums
-    static constexpr int kNC = D / (16 * kW);
+    // CTAs an SM: the sums of 128 channels take the registers of a whole one
+    static constexpr int kCtas = D <= 64 ? 2 : 1;
+    static_assert(8 * 16 * D <= 2 * kT * kLd, "the warps' sums fit where Y was");
 };
 
 struct Params {
@@ -54,10 +67,28 @@ struct Params {
     int *status;
 };
 
-template <int W>
-struct alignas(4 * W) Floats {
-    float e[W];
+// x = hi + lo, hi with 11 significant bits (to nearest), lo what is left
+struct Split {
+    uint32_t hi, lo;
 };
+__device__ __forceinline__ Split split(float x) {
+    Split r;
+    r.hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    r.lo = __float_as_uint(x - __uint_as_float(r.hi));
+    return r;
+}
+
+// c += a b on 16 x 8 by 8 x 8 tiles (tf32: the lower 13 bits of a and b are not read).
+// Thread l, g = l / 4, t = l mod 4: a at rows g, g + 8, k = t (a[0], a[1]) and t + 4 (a[2],
+// a[3]); b at k = t, t + 4, column g; c at rows g (c[0], c[1]), g + 8, columns 2 t, 2 t + 1.
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 // N rows of a [rows, D] slice from row r0 on; rows behind the last one are zero.
 template <int D, int N>
@@ -102,30 +133,66 @@ __device__ __forceinline__ void load_do(float *dst, float *nl, float *nd, const 
     }
 }
 
-// T[i][j] = X[tx + 16 i] . Y[ty + 16 j]
-template <int D, int R>
-__device__ __forceinline__ void product(const float *X, const float *Y, int tx, int ty, float (&T)[R][4]) {
+// T = X Y^T for 16 rows of X and 8 N rows of Y.
+template <int D, int N>
+__device__ __forceinline__ void product(const float *X, const float *Y, int g, int t, float (&T)[N][4]) {
     constexpr int LD = D + 4;
+    float small[N][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) T[i][j] = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < D; c += 4) {
-        float4 x[R], y[4];
+        for (int e = 0; e < 4; ++e) T[j][e] = small[j][e] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < D; k += 8) {
+        Split a[4];
 #pragma unroll
-        for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float4 *>(X + (tx + 16 * i) * LD + c);
+        for (int e = 0; e < 4; ++e) a[e] = split(X[(g + 8 * (e & 1)) * LD + k + t + 4 * (e >> 1)]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(Y + (ty + 16 * j) * LD + c);
+        for (int j = 0; j < N; ++j) {
+            const Split b0 = split(Y[(8 * j + g) * LD + k + t]), b1 = split(Y[(8 * j + g) * LD + k + t + 4]);
+            mma(small[j], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0.hi, b1.hi);
+            mma(T[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
+            mma(small[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
+        }
+    }
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                T[i][j] = fmaf(x[i].x, y[j].x, T[i][j]);
-                T[i][j] = fmaf(x[i].y, y[j].y, T[i][j]);
-                T[i][j] = fmaf(x[i].z, y[j].z, T[i][j]);
-                T[i][j] = fmaf(x[i].w, y[j].w, T[i][j]);
+        for (int e = 0; e < 4; ++e) T[j][e] += small[j][e];
+}
+
+// A += W Y for 16 rows of W (8 N columns, as `product` leaves them) and all channels of
+// 8 N rows of Y.
+template <int D, int N>
+__device__ __forceinline__ void accumulate(float (&A)[D / 8][4], const float (&W)[N][4], const float *Y, int g, int t) {
+    constexpr int LD = D + 4, M = D / 8 < 4 ? D / 8 : 4;  // channel tiles at a time
+    Split w[N][4];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[j][e] = split(W[j][e]);
+#pragma unroll
+    for (int m0 = 0; m0 < D / 8; m0 += M) {
+        float c[M][4];
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[m][e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                // columns 2 t and 2 t + 1 of W stand where k = t and t + 4 do
+                const float *y = Y + (8 * j + 2 * t) * LD + 8 * (m0 + m) + g;
+                const Split b0 = split(y[0]), b1 = split(y[LD]);
+                mma(c[m], w[j][0].lo, w[j][2].lo, w[j][1].lo, w[j][3].lo, b0.hi, b1.hi);
+                mma(c[m], w[j][0].hi, w[j][2].hi, w[j][1].hi, w[j][3].hi, b0.lo, b1.lo);
+                mma(c[m], w[j][0].hi, w[j][2].hi, w[j][1].hi, w[j][3].hi, b0.hi, b1.hi);
             }
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) A[m0 + m][e] += c[m][e];
     }
 }
 
@@ -133,13 +200,13 @@ template <int D, int R>
 __global__ void __launch_bounds__(kThreads, Cfg<D, R>::kCtas)
 attn_bwd_f32_kernel(const Params p) {
     using C = Cfg<D, R>;
-    constexpr int LD = C::kLd, LP = C::kLdP, W = C::kW, NC = C::kNC, X = C::kX;
+    constexpr int LD = C::kLd, X = C::kX, N = C::kN;
     extern __shared__ __align__(16) float sm[];
     float *X1 = sm, *X2 = sm + X * LD, *Y1 = sm + C::kOffY, *Y2 = Y1 + kT * LD;
-    float *Ps = sm + C::kOffP, *Ds = Ps + kT * LP;
     float *nls = sm + C::kOffStat, *nds = nls + kT;  // of the query rows of Y or of X
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tx = (warp & 1) * 8 + (lane & 7), ty = (warp >> 1) * 4 + (lane >> 3);
+    const int g = lane >> 2, t = lane & 3;
+    const int xw = warp % R * 16, yw = warp / R * (8 * N);  // first row and column of the warp
 
     // the unit: kv units first, longest first where the call is causal
     const int n_kv = p.BHk * p.nk * p.ns_kv;
@@ -148,7 +215,7 @@ attn_bwd_f32_kernel(const Params p) {
     const int slices = kv ? p.BHk : p.BH, ns = kv ? p.ns_kv : p.ns_q;
     int tile = u / (slices * ns);
     u -= tile * slices * ns;
-    const int zx = u / ns, split = u - zx * ns;
+    const int zx = u / ns, cut = u - zx * ns;
     if (!kv && p.causal) tile = p.nq - 1 - tile;
     const int x0 = tile * X;
     const bool skips = p.causal && !p.wrap;  // whole tiles that the mask leaves out
@@ -161,20 +228,18 @@ attn_bwd_f32_kernel(const Params p) {
         per = end > 0 ? (end + kT - 1) / kT : 0;
     }
     const int64_t steps = (int64_t)per * (kv ? p.group : 1);
-    const int t0 = (int)(steps * split / ns), n = (int)(steps * (split + 1) / ns) - t0;
+    const int t0 = (int)(steps * cut / ns), n = (int)(steps * (cut + 1) / ns) - t0;
     const int skip = per > 0 ? t0 / per : 0;
     int y = first + t0 - skip * per;
     int zy = kv ? zx * p.group + skip : zx / p.group;
     const int xrows = kv ? p.Skv : p.Sq, yrows = kv ? p.Sq : p.Skv;
     if (!in_bounds(zx < slices && x0 < xrows, p.status)) return;
 
-    float a1[R][NC][W], a2[R][NC][W];
+    float a1[D / 8][4], a2[D / 8][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int m = 0; m < D / 8; ++m)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int e = 0; e < W; ++e) a1[i][c][e] = a2[i][c][e] = 0.f;
+        for (int e = 0; e < 4; ++e) a1[m][e] = a2[m][e] = 0.f;
 
     if (n > 0) {
         const size_t s = (size_t)zx * xrows * D;
@@ -196,47 +261,24 @@ attn_bwd_f32_kernel(const Params p) {
                 load_tile<D, kT>(Y2, p.v + s, y0, yrows, p.status);
         }
         __syncthreads();
-        float T1[R][4], T2[R][4];
-        product<D, R>(X1, Y1, tx, ty, T1);
-        product<D, R>(X2, Y2, tx, ty, T2);
+        float T1[N][4], T2[N][4];
+        product<D, N>(X1 + xw * LD, Y1 + yw * LD, g, t, T1);
+        product<D, N>(X2 + xw * LD, Y2 + yw * LD, g, t, T2);
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int xi = tx + 16 * i, yi = ty + 16 * j;
+            for (int e = 0; e < 4; ++e) {
+                const int xi = xw + g + 8 * (e >> 1), yi = yw + 8 * j + 2 * t + (e & 1);
                 const int qi = kv ? y0 + yi : x0 + xi, kj = kv ? x0 + xi : y0 + yi;
                 const int pos = p.wrap ? qi % p.wrap : qi;
                 const bool seen = kj < p.Skv && (!p.causal || kj <= pos + p.off);
                 const float l = nls[kv ? yi : xi], d = nds[kv ? yi : xi];
-                const float pr = seen ? ptx::ex2_approx(fmaf(T1[i][j], p.scale_log2, l)) : 0.f;
-                if (kv) Ps[yi * LP + xi] = pr;
-                Ds[yi * LP + xi] = seen ? pr * (T2[i][j] + d) : 0.f;
+                const float pr = seen ? ptx::ex2_approx(fmaf(T1[j][e], p.scale_log2, l)) : 0.f;
+                T1[j][e] = pr;
+                T2[j][e] = seen ? pr * (T2[j][e] + d) : 0.f;
             }
-        __syncthreads();
-        // rows R ty .. of X, channels tx W + 16 W c
-#pragma unroll 4
-        for (int r = 0; r < kT; ++r) {
-            const Floats<R> ds = *reinterpret_cast<const Floats<R> *>(Ds + r * LP + R * ty);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const Floats<W> b = *reinterpret_cast<const Floats<W> *>(Y1 + r * LD + tx * W + 16 * W * c);
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-#pragma unroll
-                    for (int e = 0; e < W; ++e) a2[i][c][e] = fmaf(ds.e[i], b.e[e], a2[i][c][e]);
-            }
-            if (kv) {
-                const Floats<R> pr = *reinterpret_cast<const Floats<R> *>(Ps + r * LP + R * ty);
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const Floats<W> b = *reinterpret_cast<const Floats<W> *>(Y2 + r * LD + tx * W + 16 * W * c);
-#pragma unroll
-                    for (int i = 0; i < R; ++i)
-#pragma unroll
-                        for (int e = 0; e < W; ++e) a1[i][c][e] = fmaf(pr.e[i], b.e[e], a1[i][c][e]);
-                }
-            }
-        }
+        accumulate<D, N>(a2, T2, Y1 + yw * LD, g, t);
+        if (kv) accumulate<D, N>(a1, T1, Y2 + yw * LD, g, t);
         ++y;
         if (kv && y == p.yq) {
             y = first;
@@ -244,27 +286,34 @@ attn_bwd_f32_kernel(const Params p) {
         }
     }
 
-    const size_t part = (size_t)split * slices * xrows;
+    // The warps that share rows leave their sums where Y was, [warp's share][X][D], and
+    // all threads add them in order.
+    const size_t part = (size_t)cut * slices * xrows;
     const size_t extent = (size_t)ns * slices * xrows * D;
+    auto write = [&](float (&a)[D / 8][4], float *dst, float scale) {
+        __syncthreads();  // Y, or the sums before, are no longer read
+        float *mine = Y1 + ((warp / R) * X + xw + g) * D + 2 * t;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int row = x0 + R * ty + i;
-        if (row >= xrows) continue;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const size_t g = (part + (size_t)zx * xrows + row) * D + tx * W + 16 * W * c;
-            if (!in_bounds(g + W <= extent, p.status)) continue;
-            Floats<W> o;
-#pragma unroll
-            for (int e = 0; e < W; ++e) o.e[e] = a2[i][c][e] * p.scale;
-            *reinterpret_cast<Floats<W> *>((kv ? p.dk : p.dq) + g) = o;
-            if (kv) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) o.e[e] = a1[i][c][e];
-                *reinterpret_cast<Floats<W> *>(p.dv + g) = o;
-            }
+        for (int m = 0; m < D / 8; ++m) {
+            *reinterpret_cast<float2 *>(mine + 8 * m) = make_float2(a[m][0], a[m][1]);
+            *reinterpret_cast<float2 *>(mine + 8 * D + 8 * m) = make_float2(a[m][2], a[m][3]);
         }
-    }
+        __syncthreads();
+        for (int i = threadIdx.x; i < X * D / 4; i += kThreads) {
+            const int r = i / (D / 4), row = x0 + r;
+            float4 o = *reinterpret_cast<const float4 *>(Y1 + 4 * i);
+#pragma unroll
+            for (int w = 1; w < C::kWY; ++w) {
+                const float4 b = *reinterpret_cast<const float4 *>(Y1 + w * X * D + 4 * i);
+                o = make_float4(o.x + b.x, o.y + b.y, o.z + b.z, o.w + b.w);
+            }
+            const size_t at = (part + (size_t)zx * xrows + row) * D + 4 * (i % (D / 4));
+            if (row >= xrows || !in_bounds(at + 4 <= extent, p.status)) continue;
+            *reinterpret_cast<float4 *>(dst + at) = make_float4(o.x * scale, o.y * scale, o.z * scale, o.w * scale);
+        }
+    };
+    write(a2, kv ? p.dk : p.dq, p.scale);
+    if (kv) write(a1, p.dv, 1.f);
 }
 
 template <int D, int R>
