@@ -22,7 +22,8 @@
 //  * The tensor cores' sums round towards zero.  T adds its large products (hi hi)
 //    apart from the small ones, and A's sums of a step start at zero and are
 //    added to the unit's in fp32, so that no sum takes more than 16 such roundings.
-//  * The row statistics are computed where do is loaded (o is read once more for
+//  * The next step's tiles are copied while this one's are multiplied (two stages).
+//  * The row statistics are computed where do has come (o is read once more for
 //    each kv unit, which costs less than a kernel of its own), so that a small
 //    problem is one launch.
 // R (attn_bwd.cu) is the largest of 4, 2 and 1 that gives enough units to fill the
@@ -47,11 +48,12 @@ struct Cfg {
     static constexpr int kN = kT / kWY / 8;  // 8-column tiles of T a warp
     static constexpr int kLd = D + 4;
     static constexpr int kOffY = 2 * kX * kLd;
-    static constexpr int kOffStat = kOffY + 2 * kT * kLd;
-    static constexpr int kSmemBytes = (kOffStat + 2 * kT) * 4;
+    static constexpr int kStage = 2 * kT * kLd;  // Y1 and Y2; two stages
+    static constexpr int kOffStat = kOffY + 2 * kStage;
+    static constexpr int kSmemBytes = (kOffStat + 3 * kT) * 4;
     // CTAs an SM: the sums of 128 channels take the registers of a whole one
     static constexpr int kCtas = D <= 64 ? 2 : 1;
-    static_assert(8 * 16 * D <= 2 * kT * kLd, "the warps' sums fit where Y was");
+    static_assert(8 * 16 * D <= kStage, "the warps' sums fit where Y was");
 };
 
 struct Params {
@@ -90,48 +92,66 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// N rows of a [rows, D] slice from row r0 on; rows behind the last one are zero.
+// N rows of a [rows, D] slice from row r0 on, asynchronously; rows behind the last one
+// are zero.
 template <int D, int N>
 __device__ __forceinline__ void load_tile(float *dst, const float *src, int r0, int rows, int *status) {
     constexpr int V = D / 4;
 #pragma unroll
     for (int t = threadIdx.x; t < N * V; t += kThreads) {
         const int r = t / V, c = (t % V) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r0 + r < rows && in_bounds(r0 + r >= 0 && c + 4 <= D, status))
-            x = *reinterpret_cast<const float4 *>(src + (size_t)(r0 + r) * D + c);
-        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
+        const bool live = r0 + r < rows && in_bounds(r0 + r >= 0 && c + 4 <= D, status);
+        const float *from = live ? src + (size_t)(r0 + r) * D + c : src;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(dst + r * (D + 4) + c)),
+                     "l"(from), "r"(live ? 16 : 0)
+                     : "memory");
     }
 }
 
-// The same for rows of do, with their statistics: nl = -lse log2(e) (-inf for a row
-// without a key, and behind the last one) and nd = dlse - rowsum(o do).
+// What the statistics of N query rows need beside do, on its way in registers: o, and
+// (thread r, row r) lse and dlse.
 template <int D, int N>
-__device__ __forceinline__ void load_do(float *dst, float *nl, float *nd, const Params &p, int slice, int r0) {
-    constexpr int V = D / 4;  // lanes of a row
-    static_assert(N * V % 32 == 0, "whole warps");
-    const size_t s = (size_t)slice * p.Sq;
+struct StatRows {
+    static constexpr int V = D / 4, K = (N * V + kThreads - 1) / kThreads;
+    float4 o[K];
+    float lse, dlse;
+
+    __device__ __forceinline__ void load(const Params &p, int slice, int r0) {
+        const size_t s = (size_t)slice * p.Sq;
 #pragma unroll
-    for (int t = threadIdx.x; t < N * V; t += kThreads) {
-        const int r = t / V, c = (t % V) * 4, row = r0 + r;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        float dot = 0.f;
-        const bool live = row < p.Sq && in_bounds(slice < p.BH, p.status);
-        if (live) {
-            x = *reinterpret_cast<const float4 *>(p.dout + (s + row) * D + c);
-            const float4 y = *reinterpret_cast<const float4 *>(p.o + (s + row) * D + c);
-            dot = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
+        for (int i = 0; i < K; ++i) {
+            const int t = threadIdx.x + i * kThreads, row = r0 + t / V;
+            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t < N * V && row < p.Sq && in_bounds(slice < p.BH, p.status))
+                o[i] = *reinterpret_cast<const float4 *>(p.o + (s + row) * D + (t % V) * 4);
         }
-        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
-#pragma unroll
-        for (int m = V / 2; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-        if (t % V == 0) {
-            const float l = live ? p.lse[s + row] : -INFINITY;
-            nl[r] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
-            nd[r] = live ? (p.dlse ? p.dlse[s + row] : 0.f) - dot : 0.f;
+        const int row = r0 + threadIdx.x;
+        lse = -INFINITY;
+        dlse = 0.f;
+        if (threadIdx.x < N && row < p.Sq && in_bounds(slice < p.BH, p.status)) {
+            lse = p.lse[s + row];
+            if (p.dlse) dlse = p.dlse[s + row];
         }
     }
-}
+    // nl = -lse log2(e) (-inf for a row without a key, and behind the last one), nd =
+    // -rowsum(o do) and, apart, dlse; `dout` are the rows of do in shared memory
+    __device__ __forceinline__ void finish(const float *dout, float *nl, float *nd, float *dl) const {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int t = threadIdx.x + i * kThreads;
+            if (N * V % kThreads != 0 && t >= N * V) break;  // whole warps
+            const float4 x = *reinterpret_cast<const float4 *>(dout + t / V * (D + 4) + (t % V) * 4);
+            float dot = fmaf(x.x, o[i].x, fmaf(x.y, o[i].y, fmaf(x.z, o[i].z, x.w * o[i].w)));
+#pragma unroll
+            for (int m = V / 2; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+            if (t % V == 0) nd[t / V] = -dot;
+        }
+        if (threadIdx.x < N) {
+            nl[threadIdx.x] = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
+            dl[threadIdx.x] = dlse;
+        }
+    }
+};
 
 // T = X Y^T for 16 rows of X and 8 N rows of Y.
 template <int D, int N>
@@ -202,8 +222,8 @@ attn_bwd_f32_kernel(const Params p) {
     using C = Cfg<D, R>;
     constexpr int LD = C::kLd, X = C::kX, N = C::kN;
     extern __shared__ __align__(16) float sm[];
-    float *X1 = sm, *X2 = sm + X * LD, *Y1 = sm + C::kOffY, *Y2 = Y1 + kT * LD;
-    float *nls = sm + C::kOffStat, *nds = nls + kT;  // of the query rows of Y or of X
+    float *X1 = sm, *X2 = sm + X * LD, *Ys = sm + C::kOffY;
+    float *nls = sm + C::kOffStat, *nds = nls + kT, *dls = nds + kT;  // of the query rows of Y or of X
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int xw = warp % R * 16, yw = warp / R * (8 * N);  // first row and column of the warp
@@ -241,29 +261,47 @@ attn_bwd_f32_kernel(const Params p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) a1[m][e] = a2[m][e] = 0.f;
 
+    // Y1 and Y2 of a step into stage `st`, and what their statistics need
+    StatRows<D, kT> rows;
+    auto load_y = [&](int st, int zy, int y0) {
+        const size_t s = (size_t)zy * yrows * D;
+        float *Y = Ys + st * C::kStage;
+        if (in_bounds(zy < (kv ? p.BH : p.BHk) && y0 < yrows, p.status)) {
+            load_tile<D, kT>(Y, (kv ? p.q : p.k) + s, y0, yrows, p.status);
+            load_tile<D, kT>(Y + kT * LD, (kv ? p.dout : p.v) + s, y0, yrows, p.status);
+            if (kv) rows.load(p, zy, y0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     if (n > 0) {
         const size_t s = (size_t)zx * xrows * D;
         load_tile<D, X>(X1, (kv ? p.k : p.q) + s, x0, xrows, p.status);
-        if (kv)
-            load_tile<D, X>(X2, p.v + s, x0, xrows, p.status);
-        else
-            load_do<D, X>(X2, nls, nds, p, zx, x0);
+        load_tile<D, X>(X2, (kv ? p.v : p.dout) + s, x0, xrows, p.status);
+        load_y(0, zy, y * kT);
+        if (!kv) {
+            StatRows<D, X> mine;
+            mine.load(p, zx, x0);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();
+            mine.finish(X2, nls, nds, dls);
+        }
     }
     for (int step = 0; step < n; ++step) {
         const int y0 = y * kT;
-        if (step > 0) __syncthreads();  // the previous step's reads of Y, P and dS are done
-        const size_t s = (size_t)zy * yrows * D;
-        if (in_bounds(zy < (kv ? p.BH : p.BHk) && y0 < yrows, p.status)) {
-            load_tile<D, kT>(Y1, (kv ? p.q : p.k) + s, y0, yrows, p.status);
-            if (kv)
-                load_do<D, kT>(Y2, nls, nds, p, zy, y0);
-            else
-                load_tile<D, kT>(Y2, p.v + s, y0, yrows, p.status);
+        float *Y1 = Ys + (step & 1) * C::kStage, *Y2 = Y1 + kT * LD;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();  // this step's tiles are here, the other stage and the statistics are read
+        if (kv) rows.finish(Y2, nls, nds, dls);
+        ++y;
+        if (kv && y == p.yq) {
+            y = first;
+            ++zy;
         }
-        __syncthreads();
+        if (step + 1 < n) load_y((step + 1) & 1, zy, y * kT);
         float T1[N][4], T2[N][4];
         product<D, N>(X1 + xw * LD, Y1 + yw * LD, g, t, T1);
         product<D, N>(X2 + xw * LD, Y2 + yw * LD, g, t, T2);
+        if (kv) __syncthreads();  // the statistics are written
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
@@ -272,18 +310,14 @@ attn_bwd_f32_kernel(const Params p) {
                 const int qi = kv ? y0 + yi : x0 + xi, kj = kv ? x0 + xi : y0 + yi;
                 const int pos = p.wrap ? qi % p.wrap : qi;
                 const bool seen = kj < p.Skv && (!p.causal || kj <= pos + p.off);
-                const float l = nls[kv ? yi : xi], d = nds[kv ? yi : xi];
+                const int si = kv ? yi : xi;
+                const float l = nls[si], d = nds[si] + dls[si];
                 const float pr = seen ? ptx::ex2_approx(fmaf(T1[j][e], p.scale_log2, l)) : 0.f;
                 T1[j][e] = pr;
                 T2[j][e] = seen ? pr * (T2[j][e] + d) : 0.f;
             }
         accumulate<D, N>(a2, T2, Y1 + yw * LD, g, t);
         if (kv) accumulate<D, N>(a1, T1, Y2 + yw * LD, g, t);
-        ++y;
-        if (kv && y == p.yq) {
-            y = first;
-            ++zy;
-        }
     }
 
     // The warps that share rows leave their sums where Y was, [warp's share][X][D], and
@@ -292,7 +326,7 @@ attn_bwd_f32_kernel(const Params p) {
     const size_t extent = (size_t)ns * slices * xrows * D;
     auto write = [&](float (&a)[D / 8][4], float *dst, float scale) {
         __syncthreads();  // Y, or the sums before, are no longer read
-        float *mine = Y1 + ((warp / R) * X + xw + g) * D + 2 * t;
+        float *mine = Ys + ((warp / R) * X + xw + g) * D + 2 * t;
 #pragma unroll
         for (int m = 0; m < D / 8; ++m) {
             *reinterpret_cast<float2 *>(mine + 8 * m) = make_float2(a[m][0], a[m][1]);
@@ -301,10 +335,10 @@ attn_bwd_f32_kernel(const Params p) {
         __syncthreads();
         for (int i = threadIdx.x; i < X * D / 4; i += kThreads) {
             const int r = i / (D / 4), row = x0 + r;
-            float4 o = *reinterpret_cast<const float4 *>(Y1 + 4 * i);
+            float4 o = *reinterpret_cast<const float4 *>(Ys + 4 * i);
 #pragma unroll
             for (int w = 1; w < C::kWY; ++w) {
-                const float4 b = *reinterpret_cast<const float4 *>(Y1 + w * X * D + 4 * i);
+                const float4 b = *reinterpret_cast<const float4 *>(Ys + w * X * D + 4 * i);
                 o = make_float4(o.x + b.x, o.y + b.y, o.z + b.z, o.w + b.w);
             }
             const size_t at = (part + (size_t)zx * xrows + row) * D + 4 * (i % (D / 4));
