@@ -416,7 +416,7 @@ def _device_of(*tensors):
 
 def _check_out(t, shape, dtype, dev, name):
     """A caller-provided output must match exactly what the call writes."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
     if not t.is_cuda or t.device != dev:
         raise ValueError("%s must be on %s" % (name, dev))
@@ -431,32 +431,35 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out_dty
     ``out_dtype`` = torch.float32 with bf16/fp16 inputs selects the fp32-output
     variant.  Outputs are allocated with torch unless ``out`` / ``lse`` are
     given."""
-    import torch
+    if _torch is None:
+        import torch
+        _bind(torch)
     B, H, Sq, Skv, d = _shapes(q, k, v, shared=True)
     H_kv = k.shape[1]
-    code = dtype_code(q.dtype, out_dtype)
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    dtype, dev = q.dtype, q.device
+    code = dtype_code(dtype, out_dtype)
+    if k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("q, k, v must share a dtype")
-    odt = {ATTN_F32: torch.float32, ATTN_BF16: torch.bfloat16, ATTN_F16: torch.float16,
-           ATTN_BF16_OUT_F32: torch.float32, ATTN_F16_OUT_F32: torch.float32}[code]
-    if out is None:
-        out = torch.empty((B, H, Sq, d), dtype=odt, device=q.device)
-    _check_out(out, (B, H, Sq, d), odt, q.device, "out")
-    if return_lse and lse is None:
-        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+    odt = dtype if out_dtype is None else out_dtype
+    handle = _handle(dev, stream)
+    if out is not None:
+        _check_out(out, (B, H, Sq, d), odt, dev, "out")
+    elif odt is dtype:
+        out = _new_like(None, q)
+    else:
+        out = _new(None, (B, H, Sq, d), odt, dev)
     if lse is not None:
-        _check_out(lse, (B, H, Sq), torch.float32, q.device, "lse")
+        _check_out(lse, (B, H, Sq), _torch.float32, dev, "lse")
+    elif return_lse:
+        lse = _new(None, (B, H, Sq), _torch.float32, dev)
     sc = 0.0 if scale is None else float(scale)
-    with torch.cuda.device(q.device):
-        if H_kv == H:
-            st = attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                          lse.data_ptr() if lse is not None else None, B, H, Sq, Skv, d, causal,
-                          sc, code, _stream_handle(stream))
-        else:
-            st = attn_fwd_gqa(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                              lse.data_ptr() if lse is not None else None, B, H, H_kv, Sq, Skv, d,
-                              causal, sc, code, _stream_handle(stream))
-    _check(st, "attn_fwd" if H_kv == H else "attn_fwd_gqa")
+    lp = None if lse is None else lse.data_ptr()
+    if H_kv == H:
+        _call_on(dev, load_library().attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                 lp, B, H, Sq, Skv, d, 1 if causal else 0, sc, code, handle)
+    else:
+        _call_on(dev, load_library().attn_fwd_gqa, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                 lp, B, H, H_kv, Sq, Skv, d, 1 if causal else 0, sc, code, handle)
     return (out, lse) if return_lse else out
 
 
@@ -467,7 +470,8 @@ def attention_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None
 
     q, do [B,H,Sq,d] and k, v [B,H_kv,Skv,d] share a dtype; the gradients have o's dtype (fp32 if
     the forward pass ran with ``out_dtype`` = torch.float32).  They are allocated with torch unless
-    ``out`` = (dq, dk, dv) is given, and so is the workspace (attn_bwd_workspace_size)."""
+    ``out`` = (dq, dk, dv) is given; the workspace (attn_bwd_workspace_size) is one that this thread
+    keeps for the stream, or belongs to the call if it is large, names a stream or is captured."""
     if _torch is None:
         import torch
         _bind(torch)
@@ -480,16 +484,18 @@ def attention_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None
         raise ValueError("shape mismatch q %s k %s" % (tuple(shape), tuple(kshape)))
     if k.dtype is not dtype or v.dtype is not dtype or do.dtype is not dtype:
         raise ValueError("q, k, v and do must share a dtype")
-    for t in (q, k, v, o, do):
-        if not t.is_cuda or t.device != dev:
-            raise ValueError("q, k, v, o and do must be CUDA tensors on one device")
-        if not t.is_contiguous():
-            raise ValueError("q, k, v, o and do must be contiguous")
-    code = dtype_code(dtype, odt)
+    if not q.is_cuda or k.device != dev or v.device != dev or o.device != dev or do.device != dev:
+        raise ValueError("q, k, v, o and do must be CUDA tensors on one device")
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and o.is_contiguous()
+            and do.is_contiguous()):
+        raise ValueError("q, k, v, o and do must be contiguous")
+    code = _codes.get((dtype, odt))
+    if code is None:
+        code = dtype_code(dtype, odt)  # raises
     rows = (B, H, Sq)
-    _check_out(lse, rows, _torch.float32, dev, "lse")
+    _check_out(lse, rows, _float32, dev, "lse")
     if dlse is not None:
-        _check_out(dlse, rows, _torch.float32, dev, "dlse")
+        _check_out(dlse, rows, _float32, dev, "dlse")
     handle = _handle(dev, stream)
     if out is not None:
         dq, dk, dv = out
@@ -500,15 +506,9 @@ def attention_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None
     else:
         dq, dk, dv = (_new(stream, s, odt, dev) for s in (shape, kshape, kshape))
     need = _need(attn_bwd_workspace_size, B, H, H_kv, Sq, Skv, d, bool(causal), code)
-    wp, wn = None, 0
-    if workspace is None:
-        if need:  # belongs to the call's stream, or to the graph that captures it
-            workspace = _new(stream, need, _torch.uint8, dev)
-            wp, wn = workspace.data_ptr(), need
-    elif not workspace.is_contiguous() or _device_of(workspace) != dev:
-        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
-    else:
-        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    wp, wn, held = None, 0, None
+    if need or workspace is not None:
+        wp, wn, held = _workspace(workspace, need, _keeper(dev), stream, handle)
     _call_on(dev, load_library().attn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
              lse.data_ptr(), do.data_ptr(), None if dlse is None else dlse.data_ptr(),
              dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, H_kv, Sq, Skv, d, 1 if causal else 0,
@@ -695,7 +695,9 @@ def rotary(q, k, rot, pos, transpose: bool = False, out=None, stream=None):
     turns, width, interleaved, amplitude = rot._args
     if width > d:
         raise ValueError("rows have %d channels, %d are turned" % (d, width))
-    code = dtype_code(dtype)
+    code = _codes.get((dtype, dtype))
+    if code is None:
+        code = dtype_code(dtype)  # raises
     if k is not None:
         kshape = k.shape
         if k.dtype is not dtype or k.device != dev or len(kshape) != 4 or kshape[0] != B or \
@@ -721,10 +723,24 @@ def rotary(q, k, rot, pos, transpose: bool = False, out=None, stream=None):
 
 # ------------------------------------------------------------------ paged 8-bit cache
 class _Scratch(threading.local):
-    """A thread's workspaces of one cache, which end with the thread."""
+    """A thread's workspaces of one cache or device, which end with the thread."""
 
     def __init__(self):
         self.kept = {}  # stream handle -> workspace of the calls on it
+
+
+class _Keeper:
+    """What calls without an object of their own keep on a device."""
+
+    def __init__(self, device):
+        self.device, self._scratch = device, _Scratch()
+
+
+_keepers = {}  # torch.device -> _Keeper
+
+
+def _keeper(device):
+    return _keepers.get(device) or _keepers.setdefault(device, _Keeper(device))
 
 
 class KVCache:
@@ -797,12 +813,16 @@ def _sequence_args(cache, table, lens, counts, B):
 
 # What every call on a cache needs of torch, bound once a KVCache exists: looking it up in each
 # call takes as long as a small kernel.
-_torch = _int32 = _contiguous = _raw_stream = _current_device = _capturing = None
+_torch = _int32 = _float32 = _contiguous = _raw_stream = _current_device = _capturing = None
+_codes = {}  # (input dtype, output dtype) -> attn_dtype
 
 
 def _bind(torch):
-    global _torch, _int32, _contiguous, _raw_stream, _current_device, _capturing
-    _torch, _int32, _contiguous = torch, torch.int32, torch.contiguous_format
+    global _torch, _int32, _float32, _contiguous, _raw_stream, _current_device, _capturing
+    _torch, _int32, _float32, _contiguous = torch, torch.int32, torch.float32, torch.contiguous_format
+    for t in (torch.float32, torch.bfloat16, torch.float16):
+        for u in {t, torch.float32}:
+            _codes[t, u] = dtype_code(t, u)
     _raw_stream = torch._C._cuda_getCurrentRawStream
     _current_device = torch._C._cuda_getDevice
     _capturing = torch._C._cuda_isCurrentStreamCapturing
