@@ -309,3 +309,92 @@ def test_shared_heads_equal_repeated_ones(c):
     assert (o.cpu().double() - o64).abs().max() <= (1e-5 if dt == F else 2e-2)
     assert (lse.cpu().double() - lse64)[live].abs().max() <= 1e-4
     assert pkg.attn_check_status(None) == pkg.ATTN_OK
+
+
+# ------------------------------------------------------------------ what callers may do
+@pytest.mark.parametrize("dt,d", [(BF, 128), (HF, 64), (F, 64), (F, 16)], ids=str)
+def test_sixteen_byte_alignment_and_nothing_beside_the_outputs(dt, d):
+    """Inputs and outputs that start 16 bytes behind a 32-byte boundary, outputs with marked
+    memory on both sides."""
+    x = make(2, 4, 2, 150, 270, d, dt, seed=20, causal=True)
+    want, errors = backward64(**x, causal=True)
+    pad = 16 // x["q"].element_size()
+
+    def offset(t):
+        buf = torch.full((t.numel() + 3 * pad,), 7.0, dtype=t.dtype, device="cuda")
+        view = buf[pad:pad + t.numel()].view(t.shape)
+        assert view.data_ptr() % 32 == 16
+        return buf, view
+
+    y = {}
+    for n in ("q", "k", "v", "o", "do"):
+        y[n] = offset(x[n])[1].copy_(x[n])
+    outs = [offset(x[n]) for n in "qkv"]
+    ws = torch.full((pkg.attn_bwd_workspace_size(2, 4, 2, 150, 270, d, 1, pkg.dtype_code(dt))[1] + 32,), 9,
+                    dtype=torch.uint8, device="cuda")
+    got = pkg.attention_bwd(y["q"], y["k"], y["v"], y["o"], x["lse"].cuda(), y["do"], causal=True,
+                            out=[v for _, v in outs], workspace=ws[16:-16])
+    assert_gradients(got, want, errors)
+    for buf, view in outs:
+        assert (buf[:pad] == 7.0).all() and (buf[pad + view.numel():] == 7.0).all()
+    assert (ws[:16] == 9).all() and (ws[-16:] == 9).all()
+    assert pkg.attn_check_status(None) == pkg.ATTN_OK
+
+
+def test_two_streams_and_threads_at_once():
+    import threading
+    xs = [{n: t.cuda() if t is not None else None
+           for n, t in make(1, 8, 2, 900, 1100, 128, BF, seed=s, causal=True).items()} for s in range(4)]
+    args = [(x["q"], x["k"], x["v"], x["o"], x["lse"], x["do"]) for x in xs]
+    want = [pkg.attention_bwd(*a, causal=True) for a in args]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(10):
+                got[i] = pkg.attention_bwd(*args[i], causal=True)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(want, got):
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
+    assert pkg.attn_check_status(None) == pkg.ATTN_OK
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(seed):
+    import random
+    r = random.Random(seed)
+    dt = r.choice([BF, HF, F])
+    d = r.choice([16, 32, 64, 128] if dt == F else [64, 128])
+    Hkv, G, B = r.choice([1, 2, 3]), r.choice([1, 2, 3, 7]), r.choice([1, 1, 2])
+    Sq = r.choice([1, 2, 63, 64, 65, 127, 128, 129, r.randint(1, 700)])
+    Skv = r.choice([Sq, 1, 64, 128, 255, r.randint(1, 900)])
+    causal = r.random() < 0.6
+    check(make(B, Hkv * G, Hkv, Sq, Skv, d, dt, seed=seed, causal=causal, dlse=r.random() < 0.4,
+               o32=dt != F and r.random() < 0.3), causal)
+
+
+def test_wrapper_refusals():
+    x = {n: t.cuda() if t is not None else None for n, t in make(1, 4, 2, 40, 50, 64, BF, seed=21).items()}
+    base = dict(q=x["q"], k=x["k"], v=x["v"], o=x["o"], lse=x["lse"], do=x["do"])
+    pkg.attention_bwd(**base)
+    for change in (dict(k=x["k"][:, :, :49]), dict(v=x["v"].half()), dict(do=x["do"].float()), dict(o=x["o"].half()),
+                   dict(lse=x["lse"].double()), dict(lse=x["lse"][:, :, :39]), dict(q=x["q"].cpu()),
+                   dict(q=x["q"].transpose(1, 2).contiguous().transpose(1, 2)), dict(dlse=x["lse"][:, :3]),
+                   dict(out=(x["q"].float(), x["k"].clone(), x["v"].clone())),
+                   dict(k=x["k"][:, :1].expand(1, 3, 50, 64).contiguous(), v=x["v"][:, :1].expand(1, 3, 50, 64).contiguous()),
+                   dict(workspace=torch.empty(100, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            pkg.attention_bwd(**{**base, **change})
+    for change in (dict(out=(x["q"], torch.empty_like(x["k"]), torch.empty_like(x["v"]))),
+                   dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), dict(scale=math.nan)):
+        with pytest.raises(pkg.AttnError):
+            pkg.attention_bwd(**{**base, **change})
+    assert pkg.attn_check_status(None) == pkg.ATTN_OK
