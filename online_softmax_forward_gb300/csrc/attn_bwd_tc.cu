@@ -70,8 +70,6 @@ constexpr int kOtherRegs = 56;
 static_assert(2 * 128 * kComputeRegs + 128 * kOtherRegs == kThreads * kLaunchRegs, "register split");
 static_assert(kStatTile == kRows, "statistics of a tile");
 
-constexpr uint32_t kColT1 = 0, kColT2 = 128, kColA2 = 256, kColA1 = 384, kColT2b = 384;
-
 template <int D>
 struct Cfg {
     static_assert(D == 64 || D == 128, "head width");
@@ -82,6 +80,14 @@ struct Cfg {
     // products in both kinds of units, a Y2 tile for one or two; a tile takes about
     // three products' time to come (d = 128).  One ring of five made each wait for
     // the longer-held of the two (2740 clocks a step of a q unit of d = 128).
+    // Tensor-memory columns.  At D = 64 the sums leave room for two T1, so that a kv
+    // unit's next scores need not wait for P to be consumed; a q unit has two T2, the
+    // second one in place of A1 (D = 128) or of the second T1.
+    static constexpr bool kTwoT1 = D == 64;
+    static constexpr uint32_t kColT1b = 128, kColT2 = kTwoT1 ? 256 : 128, kColT2b = kTwoT1 ? 128 : 384;
+    static constexpr uint32_t kColA2 = kTwoT1 ? 384 : 256, kColA1 = kTwoT1 ? 448 : 384;
+    __device__ static constexpr uint32_t col_t1(int b) { return b ? kColT1b : 0u; }
+    __device__ static constexpr uint32_t col_t2(int b) { return b ? kColT2b : kColT2; }
     static constexpr int kSlots1 = D == 128 ? 3 : 6;
     static constexpr int kSlots2 = D == 128 ? 2 : 4;
     static constexpr int kOffX = 0;  // X1, X2
@@ -112,7 +118,7 @@ struct Bars {
     uint64_t x_full[2], x_empty[2];
     uint64_t y_full[kMaxSlots], y_empty[kMaxSlots];
     uint64_t st_full[kStatStages], st_empty[kStatStages];
-    uint64_t t1_full, p_full;      // T1 computed; T1 read (q unit) or P written (kv unit)
+    uint64_t t1_full[2], p_full[2];   // T1 computed; T1 read (q unit) or P written (kv unit)
     uint64_t t2_full[2], ds_full[2];  // T2 computed; dS written (of each buffer)
     uint64_t acc_full[2], acc_empty;  // A1 and A2 of a unit complete; both read
     uint64_t mma_done;
@@ -273,6 +279,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ptx::mbar_init(bar(bars->x_empty[t]), 1);
             ptx::mbar_init(bar(bars->t2_full[t]), 1);
             ptx::mbar_init(bar(bars->ds_full[t]), kComputeWarps);
+            ptx::mbar_init(bar(bars->t1_full[t]), 1);
+            ptx::mbar_init(bar(bars->p_full[t]), kComputeWarps);
         }
         for (int s = 0; s < kSlots; ++s) {
             ptx::mbar_init(bar(bars->y_full[s]), 1);
@@ -282,8 +290,6 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ptx::mbar_init(bar(bars->st_full[s]), 1);
             ptx::mbar_init(bar(bars->st_empty[s]), kComputeWarps);
         }
-        ptx::mbar_init(bar(bars->t1_full), 1);
-        ptx::mbar_init(bar(bars->p_full), kComputeWarps);
         for (int t = 0; t < 2; ++t) ptx::mbar_init(bar(bars->acc_full[t]), 1);
         ptx::mbar_init(bar(bars->acc_empty), kComputeWarps);
         ptx::mbar_init(bar(bars->mma_done), 1);
@@ -448,7 +454,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint64_t dyn = sdesc(sY, C::kChunkBytes, 1024);  // Y as [summed rows][channels of the result]
         uint32_t pos = 0;             // steps of the units before: tiles of Y1 and of Y2
         uint32_t xn = 0, un = 0;      // units begun, units whose sums were begun
-        uint32_t pn = 0, dn[2] = {0, 0};  // p_full and ds_full phases waited for
+        uint32_t pn[2] = {0, 0}, dn[2] = {0, 0};  // p_full and ds_full phases waited for
         bool ok = true;
         auto slot_full = [&](int t, uint32_t n) { return wait_all(bars->y_full[C::slot(t, n)], C::round(t, n) & 1); };
         auto free_slot = [&](int t, uint32_t n) { ptx::mma_commit_warp(bar(bars->y_empty[C::slot(t, n)])); };
@@ -487,17 +493,18 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             auto t1 = [&](int i) {
                 if (!slot_full(0, pos + i)) return false;
                 ptx::tc_fence_after();
-                issue_t(kColT1, 0, pos + i);
-                ptx::mma_commit_warp(bar(bars->t1_full));
+                const int b = C::kTwoT1 && kv ? i & 1 : 0;
+                issue_t(C::col_t1(b), 0, pos + i);
+                ptx::mma_commit_warp(bar(bars->t1_full[b]));
                 if (i == n - 1) ptx::mma_commit_warp(bar(bars->x_empty[0]));
                 return true;
             };
             auto t2 = [&](int i) {
                 const int buf = kv ? 0 : i & 1;
                 if (!slot_full(1, pos + i)) return false;
-                if (buf == 1 && !need_acc()) return false;
+                if (!C::kTwoT1 && buf == 1 && !need_acc()) return false;
                 ptx::tc_fence_after();
-                issue_t(buf ? kColT2b : kColT2, 1, pos + i);
+                issue_t(C::col_t2(buf), 1, pos + i);
                 ptx::mma_commit_warp(bar(bars->t2_full[buf]));
                 if (!kv) free_slot(1, pos + i);
                 if (i == n - 1) ptx::mma_commit_warp(bar(bars->x_empty[1]));
@@ -506,18 +513,20 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = wait_all(bars->x_full[0], xn & 1) && t1(0) && wait_all(bars->x_full[1], xn & 1) && t2(0);
             ++xn;
             for (int i = 0; i < n && ok; ++i) {
+                const int b1 = C::kTwoT1 && kv ? i & 1 : 0;
+                if (C::kTwoT1 && kv && i + 1 < n && !t1(i + 1)) { ok = false; break; }
                 // P(i) is written, or T1(i) read
-                if (!wait_all(bars->p_full, pn & 1)) { ok = false; break; }
-                ++pn;
+                if (!wait_all(bars->p_full[b1], (b1 ? pn[1] : pn[0]) & 1)) { ok = false; break; }
+                if (b1) ++pn[1]; else ++pn[0];
                 if (kv) {
                     if (!need_acc()) { ok = false; break; }
                     ptx::tc_fence_after();
-                    issue_a(kColA1, kColT1, 1, pos + i, i > 0);
+                    issue_a(C::kColA1, C::col_t1(b1), 1, pos + i, i > 0);
                     free_slot(1, pos + i);
                     if (i == n - 1) ptx::mma_commit_warp(bar(bars->acc_full[0]));
                 }
                 if (i + 1 < n) {
-                    ok = t1(i + 1);
+                    if (!C::kTwoT1 || !kv) ok = t1(i + 1);
                     if (ok && !kv) ok = t2(i + 1);
                     if (!ok) break;
                 }
@@ -525,7 +534,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!wait_all(bars->ds_full[buf], (buf ? dn[1] : dn[0]) & 1) || !need_acc()) { ok = false; break; }
                 if (buf) ++dn[1]; else ++dn[0];
                 ptx::tc_fence_after();
-                issue_a(kColA2, buf ? kColT2b : kColT2, 0, pos + i, i > 0);
+                issue_a(C::kColA2, C::col_t2(buf), 0, pos + i, i > 0);
                 free_slot(0, pos + i);
                 if (kv && i + 1 < n) ok = t2(i + 1);
             }
@@ -544,7 +553,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int r = (warp & 3) * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float ds_scale = kBF16 ? 1.f : bars->ds_scale;
-        uint32_t n1 = 0, n2[2] = {0, 0}, sn = 0, an[2] = {0, 0};
+        uint32_t n1[2] = {0, 0}, n2[2] = {0, 0}, sn = 0, an[2] = {0, 0};
         bool ok = true;
 
         // The steps of one unit, one row and 64 columns a thread.
@@ -572,12 +581,13 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const uint32_t st = sStat + stage * C::kStatBytes + half * 256;
                 bool got = true;
                 if constexpr (KV) got = watch.wait(bar(bars->st_full[stage]), (sn / kStatStages) & 1);
-                got = watch.wait(bar(bars->t1_full), n1 & 1) && got;
-                ++n1;
+                const int b1 = C::kTwoT1 && KV ? i & 1 : 0;
+                got = watch.wait(bar(bars->t1_full[b1]), (b1 ? n1[1] : n1[0]) & 1) && got;
+                if (b1) ++n1[1]; else ++n1[0];
                 if (!__all_sync(0xffffffffu, got)) return false;
                 ptx::tc_fence_after();
                 uint32_t a[2][32];
-                const uint32_t tT1 = tl + kColT1 + half * 64;
+                const uint32_t tT1 = tl + C::col_t1(b1) + half * 64;
                 ptx::tmem_ld32(tT1, a[0]);
                 ptx::tmem_ld32(tT1 + 32, a[1]);
                 ptx::tmem_wait_ld();
@@ -585,7 +595,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 reg_fence(a[1]);
                 if constexpr (!KV) {  // T1 is read: the next one may be written
                     ptx::tc_fence_before();
-                    arrive_warp(bar(bars->p_full), lane);
+                    arrive_warp(bar(bars->p_full[b1]), lane);
                 }
                 const bool masked = KV ? p.causal && w.x0 + kRows - 1 > (p.wrap ? 0 : y0) + off : y0 + kRows > all_see;
                 if (masked) {  // scores of pairs that do not see each other: -inf
@@ -626,14 +636,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ptx::tmem_st32(tT1, pk);
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
-                    arrive_warp(bar(bars->p_full), lane);
+                    arrive_warp(bar(bars->p_full[b1]), lane);
                 }
                 const int buf = KV ? 0 : i & 1;
                 got = watch.wait(bar(bars->t2_full[buf]), (buf ? n2[1] : n2[0]) & 1);
                 if (buf) ++n2[1]; else ++n2[0];
                 if (!__all_sync(0xffffffffu, got)) return false;
                 ptx::tc_fence_after();
-                const uint32_t tT2 = tl + (buf ? kColT2b : kColT2) + half * 64;
+                const uint32_t tT2 = tl + C::col_t2(buf) + half * 64;
                 uint32_t b[2][32];
                 ptx::tmem_ld32(tT2, b[0]);
                 ptx::tmem_ld32(tT2 + 32, b[1]);
@@ -702,7 +712,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     uint32_t o[32];
                     __syncwarp();
                     if (w.n > 0) {
-                        ptx::tmem_ld32(tl + (m == 0 ? kColA1 : kColA2) + half * (D / 2) + c * 32, o);
+                        ptx::tmem_ld32(tl + (m == 0 ? C::kColA1 : C::kColA2) + half * (D / 2) + c * 32, o);
                         ptx::tmem_wait_ld();
                         reg_fence(o);
                         if (m == 1 && c == D / 64 - 1) {  // read: the next unit's sums may begin
