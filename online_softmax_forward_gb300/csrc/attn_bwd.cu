@@ -119,6 +119,8 @@ __global__ void __launch_bounds__(kPreThreads) bwd_stats_kernel(const PreParams 
         p.counter[1] = gridDim.x;
     }
     float big_do = 0.f, big_d = 0.f, big_v = 0.f;
+    // the next kernel may be set up on SMs that this one leaves free; it waits for the results
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t groups = p.tiles * (kStatTile / R);
 #pragma unroll 2
     for (int64_t w = warp; w < groups; w += warps) {

@@ -310,6 +310,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         ptx::tmem_alloc(ptx::smem_addr(&bars->tmem_base), kTmemCols);
         ptx::tmem_relinquish();
     }
+    // Launched while the kernel of the row statistics still runs: nothing of it, or of
+    // what came before it, is read above.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if constexpr (!kBF16) {
         // |dS| <= max |do| max |v| + max |D|: the exponent that brings it to 2^14 at most
         if (warp == 11) {
@@ -817,7 +820,18 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
     if (!ok) return ATTN_ERR_LAUNCH;
     if (!set_smem_limit_once(reinterpret_cast<const void *>(kern), C::kSmemBytes)) return ATTN_ERR_LAUNCH;
     const int grid = (int)(plan.n_units < sms ? plan.n_units : sms);
-    kern<<<grid, kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, td, p);
+    // starts its set-up before the row statistics are complete (see the kernel)
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    (void)cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, td, p);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaErrorNoKernelImageForDevice || e == cudaErrorInvalidDeviceFunction)
         return ATTN_ERR_UNSUPPORTED_DEVICE;
