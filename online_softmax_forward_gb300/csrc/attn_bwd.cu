@@ -98,8 +98,9 @@ struct PreParams {
     int *status;
 };
 
-// Row statistics.  D / E lanes share a row (E elements of do in 16 bytes); what
-// bounds it is reading o and do once.
+// Row statistics.  D / E lanes share a row (E elements of do in 16 bytes), four rows at
+// a time with all loads first; what bounds it is reading o and do once (32 heads of
+// 8192 rows of 128 in bf16, 135 MB: 24 us, 5.6 TB/s).
 //
 // fp16 (kScale): dS is held in fp16 for the products with q and k, and its size
 // follows that of do, which a loss scale or its absence moves by orders of
@@ -121,48 +122,64 @@ __global__ void __launch_bounds__(kPreThreads) bwd_stats_kernel(const PreParams 
     float big_do = 0.f, big_d = 0.f, big_v = 0.f;
     // the next kernel may be set up on SMs that this one leaves free; it waits for the results
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t groups = p.tiles * (kStatTile / R);
-#pragma unroll 2
+    // U rows a lane group at a time, all loads first
+    constexpr int U = kStatTile / R < 4 ? kStatTile / R : 4;
+    const int64_t groups = p.tiles * (kStatTile / R / U);
     for (int64_t w = warp; w < groups; w += warps) {
-        const int64_t tile = w / (kStatTile / R);
-        const int in_tile = (int)(w % (kStatTile / R)) * R + rw;
+        const int64_t tile = w / (kStatTile / R / U);
+        const int in_tile = (int)(w % (kStatTile / R / U)) * (R * U) + rw;
         const int64_t bh = tile / p.tiles_per_head;
-        const int row = (int)(tile - bh * p.tiles_per_head) * kStatTile + in_tile;
-        float dot = 0.f, sq = 0.f, nl = -INFINITY, nd = 0.f;
-        if (row < p.Sq) {
-            const size_t at = ((size_t)bh * p.Sq + row) * D + sub * E;
-            const auto x = *reinterpret_cast<const Row<TD, E> *>((const TD *)p.dout + at);
-            Row<TO, E> y;
-            constexpr int kWords = sizeof(y) / 16;
+        const int row0 = (int)(tile - bh * p.tiles_per_head) * kStatTile + in_tile;
+        Row<TD, E> x[U];
+        Row<TO, E> y[U];
+        float l[U], dl[U];
+        constexpr int kWords = sizeof(y[0]) / 16;
 #pragma unroll
-            for (int i = 0; i < kWords; ++i)
-                reinterpret_cast<uint4 *>(&y)[i] = reinterpret_cast<const uint4 *>((const TO *)p.o + at)[i];
+        for (int u = 0; u < U; ++u) {
+            const size_t r = (size_t)bh * p.Sq + row0 + u * R, at = r * D + sub * E;
+            l[u] = -INFINITY;
+            dl[u] = 0.f;
+            if (row0 + u * R < p.Sq) {
+                if (sub == 0) {
+                    l[u] = p.lse[r];
+                    if (p.dlse) dl[u] = p.dlse[r];
+                }
+                *reinterpret_cast<uint4 *>(&x[u]) = *reinterpret_cast<const uint4 *>((const TD *)p.dout + at);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                dot = fmaf(to_f(x.e[i]), to_f(y.e[i]), dot);
-                if constexpr (kScale) sq = fmaf(to_f(x.e[i]), to_f(x.e[i]), sq);
+                for (int i = 0; i < kWords; ++i)
+                    reinterpret_cast<uint4 *>(&y[u])[i] = reinterpret_cast<const uint4 *>((const TO *)p.o + at)[i];
             }
         }
 #pragma unroll
-        for (int s = L / 2; s > 0; s >>= 1) {
-            dot += __shfl_xor_sync(0xffffffffu, dot, s);
-            if constexpr (kScale) sq += __shfl_xor_sync(0xffffffffu, sq, s);
-        }
-        if (sub != 0) continue;
-        if (row < p.Sq) {
-            const size_t r = (size_t)bh * p.Sq + row;
-            const float l = p.lse[r];
-            nl = l == -INFINITY ? -INFINITY : fmaf(l, -1.4426950408889634f, p.add);
-            nd = (p.dlse ? p.dlse[r] : 0.f) - dot;
-            if (kScale && l != -INFINITY) {
-                big_do = fmaxf(big_do, sq);
-                big_d = fmaxf(big_d, fabsf(nd));
+        for (int u = 0; u < U; ++u) {
+            const int row = row0 + u * R;
+            float dot = 0.f, sq = 0.f, nl = -INFINITY, nd = 0.f;
+            if (row < p.Sq) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    dot = fmaf(to_f(x[u].e[i]), to_f(y[u].e[i]), dot);
+                    if constexpr (kScale) sq = fmaf(to_f(x[u].e[i]), to_f(x[u].e[i]), sq);
+                }
             }
-        }
-        float *st = p.stats + (size_t)tile * 2 * kStatTile + in_tile;
-        if (in_bounds(tile < p.tiles && in_tile < kStatTile, p.status)) {
-            st[0] = nl;
-            st[kStatTile] = nd;
+#pragma unroll
+            for (int s = L / 2; s > 0; s >>= 1) {
+                dot += __shfl_xor_sync(0xffffffffu, dot, s);
+                if constexpr (kScale) sq += __shfl_xor_sync(0xffffffffu, sq, s);
+            }
+            if (sub != 0) continue;
+            if (row < p.Sq) {
+                nl = l[u] == -INFINITY ? -INFINITY : fmaf(l[u], -1.4426950408889634f, p.add);
+                nd = dl[u] - dot;
+                if (kScale && l[u] != -INFINITY) {
+                    big_do = fmaxf(big_do, sq);
+                    big_d = fmaxf(big_d, fabsf(nd));
+                }
+            }
+            float *st = p.stats + (size_t)tile * 2 * kStatTile + in_tile + u * R;
+            if (in_bounds(tile < p.tiles && in_tile + u * R < kStatTile, p.status)) {
+                st[0] = nl;
+                st[kStatTile] = nd;
+            }
         }
     }
     if constexpr (kScale) {
@@ -238,7 +255,7 @@ __global__ void __launch_bounds__(kSumThreads) bwd_sum_kernel(const SumParams p)
 template <typename TD, typename TO, int D, bool kScale>
 int launch_stats(const PreParams &p, cudaStream_t stream) {
     constexpr int R = 32 / (D * (int)sizeof(TD) / 16);
-    const int64_t warps = p.tiles * (kStatTile / R) + (kScale ? (p.v_rows + R - 1) / R : 0);
+    const int64_t warps = p.tiles * (kStatTile / R / 4) + (kScale ? (p.v_rows + R - 1) / R : 0);
     int64_t grid = (warps + kPreThreads / 32 - 1) / (kPreThreads / 32);
     if (grid > kPreBlocks) grid = kPreBlocks;
     bwd_stats_kernel<TD, TO, D, kScale><<<(unsigned)grid, kPreThreads, 0, stream>>>(p);
