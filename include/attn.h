@@ -159,10 +159,14 @@ ATTN_API int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, 
  * whatever its o, do and dlse hold, as long as they are finite.  Skv == 0
  * writes dq = 0; Sq == 0 writes dk = dv = 0.  Infinities and NaN in a row of
  * q, k, v or do may reach every gradient of its 128-row tile, masked or not.
- * Arithmetic: fp32 sums; for 16-bit types P and dS are rounded to 16 bits as
+ * Arithmetic: fp32 sums.  16-bit types: P and dS are rounded to 16 bits as
  * operands of the products (fp16: after scaling by powers of two that keep
- * them in range).  Sums are made in a fixed order: equal calls give equal bits.
+ * them in range; up to 128 keys: dS to twice as many bits).  fp32: each product
+ * of two numbers is wrong by 2^-21 of itself at most.  Sums are made in a fixed
+ * order: equal calls give equal bits.
  * All arrays must be distinct; q, k, v, o, do and gradients 16-byte aligned.
+ * Sq and Skv <= 2^31 - 1024.  CUDA graphs: as attn_fwd, without its limit on
+ * launches in flight.
  * Two kernels (fp32: one), one more where few units share a long walk.
  */
 ATTN_API int attn_bwd_workspace_size(int B, int H, int H_kv, int Sq, int Skv, int d, int causal,

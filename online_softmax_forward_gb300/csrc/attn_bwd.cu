@@ -46,6 +46,12 @@ bool bwd_plan(const Problem &call, BwdPlan *plan) {
     const double len_kv = 4.0 * p.group * tiles(p.Sq, step), len_q = 3.0 * tiles(p.Skv, step);
     const double share = ((double)bhk * plan->nk * len_kv + (double)bh * plan->nq * len_q) / kBwdSms *
                          (p.causal && call.Sq == call.Skv ? 0.5 : 1.0);
+    // dS sums to zero over a row's keys, so that its rounding to 16 bits weighs most in
+    // dq and dk where those are few.  A second part of dS costs one product more in four
+    // (kv units) or three: 28 % of a long walk, less where a q unit is one step (2 heads of
+    // 128 keys 7.0 -> 7.3 us, 1024 heads of 100 keys 43.6 -> 48.9 us; error of dq in bf16
+    // 2.4e-3 -> 1.7e-3, which is the rounding of dq itself).
+    plan->fine = !f32 && p.Skv <= kStatTile;
     const double least = 32.0;
     const double goal = share * 0.75 > least ? share * 0.75 : least;
     auto cut = [&](double len) {

@@ -45,6 +45,7 @@ struct BwdPlan {
     int tile;           // rows of a unit's own tile
     int nq, nk;         // query and key tiles of that size
     int ns_kv, ns_q;    // splits of a kv unit and of a q unit
+    bool fine;          // 16-bit types: dS enters its products as the sum of two 16-bit numbers
     int64_t n_units;
     size_t off_stats, off_max, off_part_kv, off_part_q, bytes;
 };

@@ -28,6 +28,11 @@
 //    problem is one launch.
 // R (attn_bwd.cu) is the largest of 4, 2 and 1 that gives enough units to fill the
 // GPU; the 8 / R warps that share rows add their sums at the end, in order.
+//
+// What bounds it: the tensor cores' tf32 rate (300 TFLOP/s measured for mma.sync, 100
+// for three products), 54 % busy, and the loads and splits between their
+// instructions.  8 heads of 512 x 512, d = 64: 50 us (as FP32 FMAs 90); 64 heads of
+// 1000 x 1000, 16 kv heads, causal: 613 us, 33 TFLOP/s of the five products.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -19,24 +19,33 @@
 //  * Persistent grid, one CTA per SM, 12 warps; units are claimed from a
 //    counter in the workspace, kv units of a group of heads first, longest
 //    first, so that the CTAs running at any time share the tiles of a few heads
-//    through L2.
+//    through L2 (32 heads of 8192 rows: 1.01 times the inputs read from DRAM).
 //  * Warp 8 (producer) streams the tiles with TMA (128-byte swizzle) into a ring of
-//    Y1 and one of Y2, and the statistics of a kv unit's query tile
-//    beside them.
+//    Y1 and one of Y2, and the statistics of a kv unit's query tile beside them.
 //  * Warp 9 issues the tcgen05.mma (kind::f16, fp32 accumulate).  A kv unit's step
 //    is A1(i), T1(i+1), A2(i), T2(i+1): while the first two run, the other
 //    warps turn T2(i) into dS, while the last two run, T1(i+1) into P.  A q
-//    unit has no A1, and its place in tensor memory is a second buffer of T2:
-//    T1(i+1), T2(i+1) run before A2(i).
+//    unit has no A1, and T2 has two buffers: T1(i+1), T2(i+1) run before A2(i).
 //  * Warps 0-3 and 4-7: columns 0-63 and 64-127 of T1 and T2, one thread per row
-//    and half.  P stays in fp32 registers between the two; it is rounded to 16
-//    bits for A1 alone, and dS for A2 (as the tensor core takes 16-bit
+//    and half (32x32b loads; a 16x256b fragment would spare a kv unit's column
+//    statistics their way through shared memory, but holds the read port of tensor
+//    memory four times as long).  P stays in fp32 registers between the two; it is
+//    rounded to 16 bits for A1 alone, and dS for A2 (as the tensor core takes 16-bit
 //    operands; the sums are fp32).  fp16: P is kept times 2^14, and dS times a
 //    power of two from the norms of do and v (attn_bwd.cu), undone at the end.
-//  * Tensor memory (512 columns): T1 [0,128), T2 [128,256), A2 [256,256+D),
-//    A1 or the second T2 from 384.  P and dS overwrite the first 32 columns
-//    of each half of T1 and T2.
+//    They also write a unit's sums: dv while the last A2 runs, then dk or dq.
+//  * Tensor memory (512 columns): Cfg.  P and dS overwrite the first 32 columns of
+//    each half of T1 and T2, the second part of dS (kFine) the next 32.
 //  * Every mbarrier wait is bounded, as in the forward kernel.
+//
+// What bounds it: at D = 128 and long walks the tensor cores.  32 heads of 8192
+// tokens, causal, take 1060 us: the seven products run at 1.87 PFLOP/s, the rate
+// that cuBLAS reaches on this GPU (the tensor pipe is busy 79 % of the clocks), 1.30
+// PFLOP/s of the five that a backward pass cannot do without.  A step takes 2740
+// (kv) and 2060 (q) clocks in long walks, a unit's start and end about 4000 more,
+// which is what 2 x 4001 tokens (619 us, 1.06 PFLOP/s) and shorter calls lose.  At D
+// = 64 the chain of exponentials and conversions is longer than the products:
+// 1840 and 1400 clocks a step of 1024 and 768.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -76,10 +85,6 @@ struct Cfg {
     static constexpr int kChunks = D / 64;
     static constexpr int kChunkBytes = kRows * 128;  // one 64-channel column of a tile: 16 KB
     static constexpr int kTileBytes = kChunks * kChunkBytes;
-    // Rings of Y1 and of Y2.  A Y1 tile is held from T1 of its step until A2, six
-    // products in both kinds of units, a Y2 tile for one or two; a tile takes about
-    // three products' time to come (d = 128).  One ring of five made each wait for
-    // the longer-held of the two (2740 clocks a step of a q unit of d = 128).
     // Tensor-memory columns.  At D = 64 the sums leave room for two T1, so that a kv
     // unit's next scores need not wait for P to be consumed; a q unit has two T2, the
     // second one in place of A1 (D = 128) or of the second T1.
@@ -88,6 +93,10 @@ struct Cfg {
     static constexpr uint32_t kColA2 = kTwoT1 ? 384 : 256, kColA1 = kTwoT1 ? 448 : 384;
     __device__ static constexpr uint32_t col_t1(int b) { return b ? kColT1b : 0u; }
     __device__ static constexpr uint32_t col_t2(int b) { return b ? kColT2b : kColT2; }
+    // Rings of Y1 and of Y2.  A Y1 tile is held from T1 of its step until A2, six
+    // products in both kinds of units, a Y2 tile for one or two; a tile takes about
+    // three products' time to come (D = 128).  One ring of five made each wait for
+    // the longer-held of the two (a q unit's step 2740 clocks, now 2060).
     static constexpr int kSlots1 = D == 128 ? 3 : 6;
     static constexpr int kSlots2 = D == 128 ? 2 : 4;
     static constexpr int kOffX = 0;  // X1, X2
@@ -248,7 +257,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-template <int D, bool kBF16>
+template <bool kBF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// kFine: dS as the sum of two 16-bit numbers (BwdPlan::fine).
+template <int D, bool kBF16, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -538,6 +554,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (buf) ++dn[1]; else ++dn[0];
                 ptx::tc_fence_after();
                 issue_a(C::kColA2, C::col_t2(buf), 0, pos + i, i > 0);
+                if constexpr (kFine) issue_a(C::kColA2, C::col_t2(buf) + 32, 0, pos + i, true);
                 free_slot(0, pos + i);
                 if (kv && i + 1 < n) ok = t2(i + 1);
             }
@@ -618,7 +635,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 }
                 float2 pr[32];
-                uint32_t pk[32];
+                uint32_t pk[32], rest[kFine ? 32 : 1];
                 // P = exp2(scores)
                 auto weights = [&](int j) {
                     const uint32_t *s = &a[j >> 4][(2 * j) & 31];
@@ -669,8 +686,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     z = __fmul2_rn(z, pr[j + 1]);
                     pk[j] = pack2<kBF16>(x.x, x.y);
                     pk[j + 1] = pack2<kBF16>(z.x, z.y);
+                    if constexpr (kFine) {  // what the rounding leaves
+                        const float2 hx = unpack2<kBF16>(pk[j]), hz = unpack2<kBF16>(pk[j + 1]);
+                        rest[j] = pack2<kBF16>(x.x - hx.x, x.y - hx.y);
+                        rest[j + 1] = pack2<kBF16>(z.x - hz.x, z.y - hz.y);
+                    }
                 }
                 ptx::tmem_st32(tT2, pk);
+                if constexpr (kFine) ptx::tmem_st32(tT2 + 32, rest);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 arrive_warp(bar(bars->ds_full[buf]), lane);
@@ -756,7 +779,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, bool kFine>
 int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
     using C = Cfg<D>;
     CUtensorMap tq, tk, tv, td;
@@ -807,7 +830,7 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
         p.hg = (int)hg;
     }
     p.timeout_ns = watchdog_ns();
-    auto kern = attn_bwd_tc_kernel<D, kBF16>;
+    auto kern = attn_bwd_tc_kernel<D, kBF16, kFine>;
     // setmaxnreg needs exactly the registers it was planned for (see the forward kernel)
     static std::atomic<int> regs_ok{-1};
     int ok = regs_ok.load(std::memory_order_relaxed);
@@ -838,15 +861,20 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
+template <int D, bool kBF16>
+int launch_fine(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
+    return plan.fine ? launch_typed<D, kBF16, true>(a, pr, plan, stream) : launch_typed<D, kBF16, false>(a, pr, plan, stream);
+}
+
 }  // namespace
 
 int launch_bwd_tc(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream) {
     const Problem &p = plan.p;
     const bool bf16 = p.dtype == ATTN_BF16 || p.dtype == ATTN_BF16_OUT_F32;
     if (p.d == 128)
-        return bf16 ? launch_typed<128, true>(a, p, plan, stream) : launch_typed<128, false>(a, p, plan, stream);
+        return bf16 ? launch_fine<128, true>(a, p, plan, stream) : launch_fine<128, false>(a, p, plan, stream);
     if (p.d == 64)
-        return bf16 ? launch_typed<64, true>(a, p, plan, stream) : launch_typed<64, false>(a, p, plan, stream);
+        return bf16 ? launch_fine<64, true>(a, p, plan, stream) : launch_fine<64, false>(a, p, plan, stream);
     return ATTN_ERR_INVALID_ARG;
 }
 
