@@ -26,13 +26,17 @@
 //  * The row statistics are computed where do has come (o is read once more for
 //    each kv unit, which costs less than a kernel of its own), so that a small
 //    problem is one launch.
+//  * The loads of T's products are ldmatrix, and up to 32 rows X is split into its parts
+//    once, beside itself (8 heads of 512: 49.7 -> 46.3 us; 64 rows would leave room for
+//    one CTA an SM). Products of one part follow each other over the column tiles, so
+//    that none waits for the one before it.
 // R (attn_bwd.cu) is the largest of 4, 2 and 1 that gives enough units to fill the
 // GPU; the 8 / R warps that share rows add their sums at the end, in order.
 //
 // What bounds it: the tensor cores' tf32 rate (300 TFLOP/s measured for mma.sync, 100
-// for three products), 54 % busy, and the loads and splits between their
-// instructions.  8 heads of 512 x 512, d = 64: 50 us (as FP32 FMAs 90); 64 heads of
-// 1000 x 1000, 16 kv heads, causal: 613 us, 33 TFLOP/s of the five products.
+// for three products), 54 to 58 % busy, and the loads and splits between
+// their instructions.  8 heads of 512 x 512, d = 64: 46 us (as FP32 FMAs 90); 64 heads of
+// 1000 x 1000, 16 kv heads, causal: 578 us, 35 TFLOP/s of the five products.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -52,7 +56,9 @@ struct Cfg {
     static constexpr int kWY = 8 / R;      // warps that share rows of X
     static constexpr int kN = kT / kWY / 8;  // 8-column tiles of T a warp
     static constexpr int kLd = D + 4;
-    static constexpr int kOffY = 2 * kX * kLd;
+    // X is held as its two parts, X1, X2 (hi) and behind them their lo
+    static constexpr bool kParts = R <= 2;
+    static constexpr int kOffY = (kParts ? 4 : 2) * kX * kLd;
     static constexpr int kStage = 2 * kT * kLd;  // Y1 and Y2; two stages
     static constexpr int kOffStat = kOffY + 2 * kStage;
     static constexpr int kSmemBytes = (kOffStat + 3 * kT) * 4;
@@ -158,10 +164,23 @@ struct StatRows {
     }
 };
 
-// T = X Y^T for 16 rows of X and 8 N rows of Y.
-template <int D, int N>
-__device__ __forceinline__ void product(const float *X, const float *Y, int g, int t, float (&T)[N][4]) {
-    constexpr int LD = D + 4;
+// 8 x 4 blocks of 32-bit numbers: thread l gets row l / 4, column l mod 4 of each; thread l
+// names row l mod 8 of block l / 8.
+__device__ __forceinline__ void load_blocks(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void load_blocks(uint32_t (&r)[2], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+
+// T = X Y^T for 16 rows of X and 8 N rows of Y; kLo: how far behind X's hi its lo is, or
+// 0 where X is whole.
+template <int D, int N, int kLo>
+__device__ __forceinline__ void product(const float *X, const float *Y, int lane, float (&T)[N][4]) {
+    constexpr int LD = D + 4, J = N > 1 ? 2 : 1;  // column tiles of one load
+    const uint32_t xa = ptx::smem_addr(X + (lane & 15) * LD + (lane >> 4) * 4);
+    const uint32_t ya = ptx::smem_addr(Y + ((lane & 7) + (N > 1 ? lane >> 4 << 3 : 0)) * LD + (lane >> 3 & 1) * 4);
     float small[N][4];
 #pragma unroll
     for (int j = 0; j < N; ++j)
@@ -169,16 +188,28 @@ __device__ __forceinline__ void product(const float *X, const float *Y, int g, i
         for (int e = 0; e < 4; ++e) T[j][e] = small[j][e] = 0.f;
 #pragma unroll 2
     for (int k = 0; k < D; k += 8) {
-        Split a[4];
+        Split a[4], b[N][2];
+        uint32_t x[4], xl[4];
+        load_blocks(x, xa + k * 4);
+        if constexpr (kLo > 0) load_blocks(xl, xa + (kLo + k) * 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[e] = split(X[(g + 8 * (e & 1)) * LD + k + t + 4 * (e >> 1)]);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const Split b0 = split(Y[(8 * j + g) * LD + k + t]), b1 = split(Y[(8 * j + g) * LD + k + t + 4]);
-            mma(small[j], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0.hi, b1.hi);
-            mma(T[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
-            mma(small[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (kLo > 0) a[e] = Split{x[e], xl[e]};
+            else a[e] = split(__uint_as_float(x[e]));
         }
+#pragma unroll
+        for (int j = 0; j < N; j += J) {
+            uint32_t y[2 * J];
+            load_blocks(y, ya + (8 * j * LD + k) * 4);
+#pragma unroll
+            for (int e = 0; e < 2 * J; ++e) b[j + e / 2][e & 1] = split(__uint_as_float(y[e]));
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) mma(small[j], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[j][0].hi, b[j][1].hi);
+#pragma unroll
+        for (int j = 0; j < N; ++j) mma(T[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[j][0].hi, b[j][1].hi);
+#pragma unroll
+        for (int j = 0; j < N; ++j) mma(small[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[j][0].lo, b[j][1].lo);
     }
 #pragma unroll
     for (int j = 0; j < N; ++j)
@@ -204,16 +235,25 @@ __device__ __forceinline__ void accumulate(float (&A)[D / 8][4], const float (&W
 #pragma unroll
             for (int e = 0; e < 4; ++e) c[m][e] = 0.f;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+        for (int j = 0; j < N; ++j) {
+            Split b[M][2];
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 // columns 2 t and 2 t + 1 of W stand where k = t and t + 4 do
                 const float *y = Y + (8 * j + 2 * t) * LD + 8 * (m0 + m) + g;
-                const Split b0 = split(y[0]), b1 = split(y[LD]);
-                mma(c[m], w[j][0].lo, w[j][2].lo, w[j][1].lo, w[j][3].lo, b0.hi, b1.hi);
-                mma(c[m], w[j][0].hi, w[j][2].hi, w[j][1].hi, w[j][3].hi, b0.lo, b1.lo);
-                mma(c[m], w[j][0].hi, w[j][2].hi, w[j][1].hi, w[j][3].hi, b0.hi, b1.hi);
+                b[m][0] = split(y[0]);
+                b[m][1] = split(y[LD]);
             }
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                mma(c[m], w[j][0].lo, w[j][2].lo, w[j][1].lo, w[j][3].lo, b[m][0].hi, b[m][1].hi);
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                mma(c[m], w[j][0].hi, w[j][2].hi, w[j][1].hi, w[j][3].hi, b[m][0].lo, b[m][1].lo);
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                mma(c[m], w[j][0].hi, w[j][2].hi, w[j][1].hi, w[j][3].hi, b[m][0].hi, b[m][1].hi);
+        }
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -290,6 +330,18 @@ attn_bwd_f32_kernel(const Params p) {
             __syncthreads();
             mine.finish(X2, nls, nds, dls);
         }
+        if constexpr (C::kParts) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * X * (D / 4); i += kThreads) {
+                uint4 *at = reinterpret_cast<uint4 *>(X1 + i / (D / 4) * LD + i % (D / 4) * 4);
+                const uint4 x = *at;
+                const Split a = split(__uint_as_float(x.x)), b = split(__uint_as_float(x.y)),
+                            c = split(__uint_as_float(x.z)), d = split(__uint_as_float(x.w));
+                *at = make_uint4(a.hi, b.hi, c.hi, d.hi);
+                at[2 * X * LD / 4] = make_uint4(a.lo, b.lo, c.lo, d.lo);
+            }
+        }
     }
     for (int step = 0; step < n; ++step) {
         const int y0 = y * kT;
@@ -304,8 +356,8 @@ attn_bwd_f32_kernel(const Params p) {
         }
         if (step + 1 < n) load_y((step + 1) & 1, zy, y * kT);
         float T1[N][4], T2[N][4];
-        product<D, N>(X1 + xw * LD, Y1 + yw * LD, g, t, T1);
-        product<D, N>(X2 + xw * LD, Y2 + yw * LD, g, t, T2);
+        product<D, N, C::kParts ? 2 * X * LD : 0>(X1 + xw * LD, Y1 + yw * LD, lane, T1);
+        product<D, N, C::kParts ? 2 * X * LD : 0>(X2 + xw * LD, Y2 + yw * LD, lane, T2);
         if (kv) __syncthreads();  // the statistics are written
 #pragma unroll
         for (int j = 0; j < N; ++j)
