@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <algorithm>
 
 #include "attn_bwd.h"
 
@@ -46,12 +47,18 @@ bool bwd_plan(const Problem &call, BwdPlan *plan) {
     const double len_kv = 4.0 * p.group * tiles(p.Sq, step), len_q = 3.0 * tiles(p.Skv, step);
     const double share = ((double)bhk * plan->nk * len_kv + (double)bh * plan->nq * len_q) / kBwdSms *
                          (p.causal && call.Sq == call.Skv ? 0.5 : 1.0);
-    // dS sums to zero over a row's keys, so that its rounding to 16 bits weighs most in
-    // dq and dk where those are few.  A second part of dS costs one product more in four
-    // (kv units) or three: 28 % of a long walk, less where a q unit is one step (2 heads of
-    // 128 keys 7.0 -> 7.3 us, 1024 heads of 100 keys 43.6 -> 48.9 us; error of dq in bf16
-    // 2.4e-3 -> 1.7e-3, which is the rounding of dq itself).
-    plan->fine = !f32 && p.Skv <= kStatTile;
+    // dS sums to zero over a row's keys and is largest where these are few, so that there its
+    // rounding to 16 bits is most of what dq and dk are wrong by, and in a causal call it is
+    // large beside the gradients of the later rows (8192 tokens in bf16: one element of dq
+    // wrong by 0.44 of dq's root mean square, now 0.17).  Steps of query tiles whose first row
+    // sees at most kFewKeys keys therefore take dS in two parts, with one product more (2 heads
+    // of 128 keys 7.0 us in either form; 1024 heads of 100 keys 43.6 -> 48.9 us).  The rule goes
+    // by positions alone, so that a result does not depend on what else is in the batch.
+    plan->few = 0;
+    if (p.Skv <= kFewKeys) plan->few = plan->nq;
+    else if (plan->wrap) plan->few = plan->off < kFewKeys ? plan->nq : 0;  // every tile may hold a first position
+    else if (p.causal && plan->off < kFewKeys) plan->few = std::min(plan->nq, (kFewKeys - 1 - plan->off) / kStatTile + 1);
+    if (f32) plan->few = 0;
     const double least = 32.0;
     const double goal = share * 0.75 > least ? share * 0.75 : least;
     auto cut = [&](double len) {

@@ -35,6 +35,7 @@ namespace attn {
 constexpr int kStatTile = 128;   // query rows of one block of row statistics
 constexpr int kBwdSms = 152;     // the splits are planned for this many SMs
 constexpr int kMaxBwdSplits = 64;
+constexpr int kFewKeys = 128;    // see BwdPlan::few
 constexpr int kBwdP16Log2 = 14;  // fp16: P is kept times 2^14, so that small weights stay normal numbers
 constexpr int kPreBlocks = 1216; // CTAs of the first kernel at most
 
@@ -45,7 +46,7 @@ struct BwdPlan {
     int tile;           // rows of a unit's own tile
     int nq, nk;         // query and key tiles of that size
     int ns_kv, ns_q;    // splits of a kv unit and of a q unit
-    bool fine;          // 16-bit types: dS enters its products as the sum of two 16-bit numbers
+    int few;            // 16-bit types: query tiles of a head, from the first on, with dS in two parts
     int64_t n_units;
     size_t off_stats, off_max, off_part_kv, off_part_q, bytes;
 };

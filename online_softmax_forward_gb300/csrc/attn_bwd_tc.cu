@@ -35,15 +35,16 @@
 //    power of two from the norms of do and v (attn_bwd.cu), undone at the end.
 //    They also write a unit's sums: dv while the last A2 runs, then dk or dq.
 //  * Tensor memory (512 columns): Cfg.  P and dS overwrite the first 32 columns of
-//    each half of T1 and T2, the second part of dS (kFine) the next 32.
+//    each half of T1 and T2, the second part of dS (kFew) the next 32.
 //  * Every mbarrier wait is bounded, as in the forward kernel.
 //
 // What bounds it: at D = 128 and long walks the tensor cores.  32 heads of 8192
-// tokens, causal, take 1060 us: the seven products run at 1.87 PFLOP/s, the rate
-// that cuBLAS reaches on this GPU (the tensor pipe is busy 79 % of the clocks), 1.30
-// PFLOP/s of the five that a backward pass cannot do without.  A step takes 2740
+// tokens, causal, take 1085 us: the seven products of whole tiles run at 1.80 PFLOP/s, near the rate
+// that cuBLAS reaches on this GPU (the tensor pipe is busy 79 % of the clocks), 1.27
+// PFLOP/s of the five that a backward pass cannot do without.  1060 us without kFew: the
+// issuing warp's test stands between a wait and the product that others wait for.  A step takes 2740
 // (kv) and 2060 (q) clocks in long walks, a unit's start and end about 4000 more,
-// which is what 2 x 4001 tokens (619 us, 1.06 PFLOP/s) and shorter calls lose.  At D
+// which is what 2 x 4001 tokens (630 us, 1.04 PFLOP/s) and shorter calls lose.  At D
 // = 64 the chain of exponentials and conversions is longer than the products:
 // 1840 and 1400 clocks a step of 1024 and 768.
 #include <cuda.h>
@@ -145,7 +146,7 @@ struct Params {
     unsigned *counter;
     void *dk, *dv, *dq;               // gradients, or the splits' partial sums
     int BH, BHk, group, Sq, Skv, causal;
-    int off, wrap;  // of BwdPlan
+    int off, wrap, few;  // of BwdPlan
     int nq, nk, ns_kv, ns_q;
     int hg;       // kv slices per schedule group
     int n_units;
@@ -263,8 +264,9 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     else return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// kFine: dS as the sum of two 16-bit numbers (BwdPlan::fine).
-template <int D, bool kBF16, bool kFine>
+// kFew: there are query tiles, the first p.few of each head, whose first query sees at most
+// kFewKeys keys; dS of those is held as the sum of two 16-bit numbers (BwdPlan::few).
+template <int D, bool kBF16, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -531,7 +533,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             ok = wait_all(bars->x_full[0], xn & 1) && t1(0) && wait_all(bars->x_full[1], xn & 1) && t2(0);
             ++xn;
+            int y = kv ? w.y : w.x0 / kRows, zy = w.zy;  // the step's query tile (kFew)
             for (int i = 0; i < n && ok; ++i) {
+                const bool few = kFew && y < p.few;
                 const int b1 = C::kTwoT1 && kv ? i & 1 : 0;
                 if (C::kTwoT1 && kv && i + 1 < n && !t1(i + 1)) { ok = false; break; }
                 // P(i) is written, or T1(i) read
@@ -554,9 +558,10 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (buf) ++dn[1]; else ++dn[0];
                 ptx::tc_fence_after();
                 issue_a(C::kColA2, C::col_t2(buf), 0, pos + i, i > 0);
-                if constexpr (kFine) issue_a(C::kColA2, C::col_t2(buf) + 32, 0, pos + i, true);
+                if (kFew && few) issue_a(C::kColA2, C::col_t2(buf) + 32, 0, pos + i, true);
                 free_slot(0, pos + i);
                 if (kv && i + 1 < n) ok = t2(i + 1);
+                if (kFew && kv) advance(w, p, y, zy);
             }
             if (!ok) break;
             ptx::mma_commit_warp(bar(bars->acc_full[1]));
@@ -595,10 +600,11 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             int y = w.y, zy = w.zy;
-            for (int i = 0; i < w.n; ++i) {
+            auto one = [&](auto few, int i) {
+                constexpr bool kTwo = decltype(few)::value;
                 const int y0 = y * kRows;
                 const int stage = sn % kStatStages;
-                const uint32_t st = sStat + stage * C::kStatBytes + half * 256;
+                [[maybe_unused]] const uint32_t st = sStat + stage * C::kStatBytes + half * 256;
                 bool got = true;
                 if constexpr (KV) got = watch.wait(bar(bars->st_full[stage]), (sn / kStatStages) & 1);
                 const int b1 = C::kTwoT1 && KV ? i & 1 : 0;
@@ -635,7 +641,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 }
                 float2 pr[32];
-                uint32_t pk[32], rest[kFine ? 32 : 1];
+                uint32_t pk[32], rest[kTwo ? 32 : 1];
                 // P = exp2(scores)
                 auto weights = [&](int j) {
                     const uint32_t *s = &a[j >> 4][(2 * j) & 31];
@@ -686,14 +692,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     z = __fmul2_rn(z, pr[j + 1]);
                     pk[j] = pack2<kBF16>(x.x, x.y);
                     pk[j + 1] = pack2<kBF16>(z.x, z.y);
-                    if constexpr (kFine) {  // what the rounding leaves
+                    if constexpr (kTwo) {  // what the rounding leaves
                         const float2 hx = unpack2<kBF16>(pk[j]), hz = unpack2<kBF16>(pk[j + 1]);
                         rest[j] = pack2<kBF16>(x.x - hx.x, x.y - hx.y);
                         rest[j + 1] = pack2<kBF16>(z.x - hz.x, z.y - hz.y);
                     }
                 }
                 ptx::tmem_st32(tT2, pk);
-                if constexpr (kFine) ptx::tmem_st32(tT2 + 32, rest);
+                if constexpr (kTwo) ptx::tmem_st32(tT2 + 32, rest);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 arrive_warp(bar(bars->ds_full[buf]), lane);
@@ -702,6 +708,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ++sn;
                 }
                 advance(w, p, y, zy);
+                return true;
+            };
+            for (int i = 0; i < w.n; ++i) {
+                if (kFew && (KV ? y : w.x0 / kRows) < p.few) {
+                    if (!one(std::bool_constant<kFew>{}, i)) return false;
+                } else if (!one(std::false_type{}, i)) {
+                    return false;
+                }
             }
             return true;
         };
@@ -779,7 +793,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool kBF16, bool kFine>
+template <int D, bool kBF16, bool kFew>
 int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
     using C = Cfg<D>;
     CUtensorMap tq, tk, tv, td;
@@ -799,6 +813,7 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
     p.causal = pr.causal;
     p.off = plan.off;
     p.wrap = plan.wrap;
+    p.few = plan.few;
     p.nq = plan.nq;
     p.nk = plan.nk;
     p.ns_kv = plan.ns_kv;
@@ -830,7 +845,7 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
         p.hg = (int)hg;
     }
     p.timeout_ns = watchdog_ns();
-    auto kern = attn_bwd_tc_kernel<D, kBF16, kFine>;
+    auto kern = attn_bwd_tc_kernel<D, kBF16, kFew>;
     // setmaxnreg needs exactly the registers it was planned for (see the forward kernel)
     static std::atomic<int> regs_ok{-1};
     int ok = regs_ok.load(std::memory_order_relaxed);
@@ -862,8 +877,8 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
 }
 
 template <int D, bool kBF16>
-int launch_fine(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
-    return plan.fine ? launch_typed<D, kBF16, true>(a, pr, plan, stream) : launch_typed<D, kBF16, false>(a, pr, plan, stream);
+int launch_few(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
+    return plan.few ? launch_typed<D, kBF16, true>(a, pr, plan, stream) : launch_typed<D, kBF16, false>(a, pr, plan, stream);
 }
 
 }  // namespace
@@ -872,9 +887,9 @@ int launch_bwd_tc(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream) {
     const Problem &p = plan.p;
     const bool bf16 = p.dtype == ATTN_BF16 || p.dtype == ATTN_BF16_OUT_F32;
     if (p.d == 128)
-        return bf16 ? launch_fine<128, true>(a, p, plan, stream) : launch_fine<128, false>(a, p, plan, stream);
+        return bf16 ? launch_few<128, true>(a, p, plan, stream) : launch_few<128, false>(a, p, plan, stream);
     if (p.d == 64)
-        return bf16 ? launch_fine<64, true>(a, p, plan, stream) : launch_fine<64, false>(a, p, plan, stream);
+        return bf16 ? launch_few<64, true>(a, p, plan, stream) : launch_few<64, false>(a, p, plan, stream);
     return ATTN_ERR_INVALID_ARG;
 }
 

@@ -27,7 +27,8 @@ def forward64(q, k, v, causal, scale=None):
 def backward64(q, k, v, o, lse, do, dlse=None, causal=False, scale=None):
     """dq, dk, dv and, for each, the largest error that the kernels' roundings allow.
 
-    u is half a step of the operands of the products (P and dS), 0 for fp32 inputs.  The other
+    u is half a step of the operands of the products (P and dS), 0 for fp32 inputs; dS of queries
+    that see at most 128 keys is held in two such parts, which leaves u * u.  The other
     terms are fp32 arithmetic: a product's sum over d channels in any order and an exponent of a
     few units in the last place of its largest term, and the sums over rows, all taken as 2^-20 of
     the sum of the terms' magnitudes (16 units; sums of n terms grow with sqrt(n) and stay far
@@ -51,12 +52,14 @@ def backward64(q, k, v, o, lse, do, dlse=None, causal=False, scale=None):
         D = D - dlse.double()[..., None]
     dp = do @ V.mT
     ds = p * (dp - D)
-    # errors of P and dS
-    ep = p * (u + f * (1 + l0.abs() + scale * (q.abs() @ K.abs().mT)))
+    # errors of P (in fp32, and as an operand) and dS, which is made of P in fp32
+    e32 = p * f * (1 + l0.abs() + scale * (q.abs() @ K.abs().mT))
+    ep = p * u + e32
+    us = torch.where(seen.sum(-1, keepdim=True) <= 128, u * u, u)
     mag = do.abs() @ V.abs().mT + (o.abs() * do.abs()).sum(-1, keepdim=True)
     if dlse is not None:
         mag = mag + dlse.double().abs()[..., None]
-    es = ds.abs() * u + p * f * mag + ep * (dp - D).abs()
+    es = ds.abs() * us + p * f * mag + e32 * (dp - D).abs()
     if dt == torch.float16:
         # floors of fp16 under the scales: P times 2^14; dS brought to at least 2^12 of its bound
         bound = do.norm(dim=-1).amax() * v.norm(dim=-1).amax() + D.abs().amax()

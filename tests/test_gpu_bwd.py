@@ -140,6 +140,20 @@ def test_fp32_gradients_of_16_bit_inputs(dt):
     assert got[0].dtype == F
 
 
+@pytest.mark.parametrize("H,Hkv,Sq,Skv", [(2, 2, 400, 400), (2, 1, 300, 420), (2, 2, 300, 427), (4, 1, 100, 140),
+                                           (3, 1, 128, 129), (2, 2, 600, 300), (2, 1, 140, 128)])
+@pytest.mark.parametrize("dt,d", [(BF, 128), (HF, 64), (BF, 64), (HF, 128)])
+def test_queries_with_few_keys(dt, d, H, Hkv, Sq, Skv):
+    """dS is held to twice 16 bits for queries that see up to 128 keys: without the outputs' rounding
+    their dq, and the dk of the keys that only they see, come out that close."""
+    x = make(1, H, Hkv, Sq, Skv, d, dt, seed=Sq + Skv, o32=True, causal=True)
+    check(x, True)
+    seen = torch.arange(Sq) + 1 + Skv - Sq
+    few = int((seen <= 128).sum())
+    want, errors = backward64(**x, causal=True)
+    assert few > 0 and (errors[0][:, :, :few] <= 2.0 ** -13 * want[0].abs().amax()).all()
+
+
 @pytest.mark.parametrize("size", [1e-7, 1e-4, 300.0])
 def test_fp16_follows_the_size_of_do(size):
     """Gradients of a loss that was scaled down or up: dS would leave fp16's range unscaled."""
