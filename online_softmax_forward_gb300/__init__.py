@@ -470,11 +470,17 @@ def attention_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None
 
     q, do [B,H,Sq,d] and k, v [B,H_kv,Skv,d] share a dtype; the gradients have o's dtype (fp32 if
     the forward pass ran with ``out_dtype`` = torch.float32).  They are allocated with torch unless
-    ``out`` = (dq, dk, dv) is given; the workspace (attn_bwd_workspace_size) is one that this thread
-    keeps for the stream, or belongs to the call if it is large, names a stream or is captured."""
+    ``out`` = (dq, dk, dv) is given; the workspace (attn_bwd_workspace_size) belongs to the call, or is
+    one that this thread keeps for the stream where ``out`` is given and the call is not captured."""
     if _torch is None:
         import torch
         _bind(torch)
+    if out is None and workspace is None and stream is None:
+        r = _fast().attention_bwd(q, k, v, o, lse, do, dlse, causal, 0.0 if scale is None else scale)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            raise AttnError(r, "attn_bwd")
     shape, kshape, dtype, odt, dev = q.shape, k.shape, q.dtype, o.dtype, q.device
     if len(shape) != 4 or len(kshape) != 4 or v.shape != kshape or o.shape != shape or do.shape != shape:
         raise ValueError("q, o, do must be [B, H, Sq, d] of one shape and k, v [B, H_kv, Skv, d] of one")
@@ -659,7 +665,8 @@ class Rotary:
         self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns],
                                   dtype=torch.int64, device=device)
         self.device = self.turns.device
-        self._args = (self.turns.data_ptr(), width, 1 if layout == "interleaved" else 0, self.amplitude)
+        self._args = (self.turns.data_ptr(), width, 1 if layout == "interleaved" else 0, self.amplitude,
+                      self.device.index if self.turns.is_cuda else -1)
 
 
 def _heads(x, out, name):
@@ -686,13 +693,19 @@ def rotary(q, k, rot, pos, transpose: bool = False, out=None, stream=None):
     of a projection's [B,S,H,d].  ``transpose`` gives the gradient in q and k from the one in the
     results.  New results are contiguous [B,H,S,d], as ``attention`` and ``cache_append`` take them;
     ``out`` = (q', k') writes to other places, which may be q and k themselves.  Returns (q', k')."""
+    if out is None and stream is None:
+        r = _fast().rotary(q, k, pos, transpose, *rot._args)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            raise AttnError(r, "attn_rotary")
     shape, dev, dtype = q.shape, q.device, q.dtype
     if len(shape) != 4:
         raise ValueError("q must be [B, H, S, d]")
     B, _, S, d = shape
     if dev != rot.device or not q.is_cuda:
         raise ValueError("q is on %s, the angles on %s" % (dev, rot.device))
-    turns, width, interleaved, amplitude = rot._args
+    turns, width, interleaved, amplitude, _ = rot._args
     if width > d:
         raise ValueError("rows have %d channels, %d are turned" % (d, width))
     code = _codes.get((dtype, dtype))
@@ -813,8 +826,26 @@ def _sequence_args(cache, table, lens, counts, B):
 
 # What every call on a cache needs of torch, bound once a KVCache exists: looking it up in each
 # call takes as long as a small kernel.
+_calls = None  # module of csrc/torch_calls.cpp
 _torch = _int32 = _float32 = _contiguous = _raw_stream = _current_device = _capturing = None
 _codes = {}  # (input dtype, output dtype) -> attn_dtype
+
+
+def _fast():
+    """The wrappers' host side in C++, for calls with nothing out of the ordinary: each of its
+    functions answers None to any other, for the Python code behind it to do or to refuse."""
+    global _calls
+    if _calls is None:
+        import torch
+        try:
+            from . import _torch_calls
+        except ImportError as e:
+            raise RuntimeError("_torch_calls.so is missing or of another PyTorch: run %s/build.py (%s)" % (_HERE, e))
+        if torch.__version__.split("+")[0] != _torch_calls.torch_version:
+            raise RuntimeError("_torch_calls.so was built for PyTorch %s, this is %s: run %s/build.py"
+                               % (_torch_calls.torch_version, torch.__version__, _HERE))
+        _calls = _torch_calls
+    return _calls
 
 
 def _bind(torch):

@@ -1,6 +1,6 @@
 """Build libattn.so in-tree with nvcc for sm_103a (GB300).
 
-Each .cu file compiles in parallel to an object under _build/, then two
+Each .cu file compiles in parallel to an object under _build/, then the
 shared libraries are linked next to this file:
 
 * libattn.so -- the product: exports the functions of include/attn.h only
@@ -11,7 +11,10 @@ shared libraries are linked next to this file:
 * libattn_checked.so -- the bounds-checking build: every source compiled
   with ATTN_BOUNDS_CHECK (and the test exports), so that the kernels test
   each global index and TMA coordinate before using it and report a failed
-  test through the status word instead of touching memory out of bounds.
+  test through the status word instead of touching memory out of bounds;
+* _torch_calls.so -- the host side of the Python wrappers whose calls are
+  short, against PyTorch's headers (csrc/torch_calls.cpp, by the host
+  compiler).
 
 The CUDA runtime is linked statically (nvcc's default), so the libraries
 need only the driver at run time; the tensor-map encoder is fetched from the
@@ -20,9 +23,12 @@ driver at first use.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -32,6 +38,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn.so")
 TEST_LIB = os.path.join(HERE, "libattn_test.so")
 CHECKED_LIB = os.path.join(HERE, "libattn_checked.so")
+CALLS_LIB = os.path.join(HERE, "_torch_calls.so")
 SOURCES = ["attn_api.cu", "attn_bwd.cu", "attn_bwd_f32.cu", "attn_bwd_tc.cu", "attn_cache.cu", "attn_cache_fwd.cu", "attn_cache_select.cu",
            "attn_cache_tc.cu", "attn_f32.cu", "attn_rotary.cu", "attn_splitkv.cu", "attn_tc.cu"]
 # (source, object name, extra flags) of the test library's own objects
@@ -73,9 +80,38 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    """PyTorch's folder, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _cxx() -> str:
+    return os.environ.get("CXX") or shutil.which("g++") or "c++"
+
+
+def _calls_compile(src: str, obj: str):
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    dirs = [INCLUDE, sysconfig.get_paths()["include"], inc,
+            os.path.join(inc, "torch", "csrc", "api", "include"), cuda]
+    return ([_cxx(), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w"]
+            + [f for d in dirs for f in ("-I", d)] + ["-c", src, "-o", obj])
+
+
+def _calls_link(lib: str, obj: str):
+    return [_cxx(), "-shared", "-o", lib, obj, "-L", HERE, "-l:libattn.so", "-Wl,-rpath,$ORIGIN",
+            "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
 def _link(lib: str, objs) -> None:
     tmp = lib + ".tmp%d" % os.getpid()
-    cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + list(objs)
+    if lib == CALLS_LIB:
+        cmd = _calls_link(tmp, *objs)
+    else:
+        cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + list(objs)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         print(r.stdout + r.stderr)
@@ -84,7 +120,7 @@ def _link(lib: str, objs) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Builds the three libraries (only what is stale); returns the product's path."""
+    """Builds the libraries (only what is stale); returns the product's path."""
     os.makedirs(BUILD, exist_ok=True)
     objs, jobs = {}, []
     units = ([(src, src.replace(".cu", ".o"), []) for src in SOURCES] + TEST_SOURCES
@@ -95,6 +131,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         objs[oname] = o
         if force or _stale(o, s):
             jobs.append([nvcc()] + _flags(list(extra_flags) + fl) + ["-c", s, "-o", o])
+    # one object for each version of PyTorch, whose headers it is made of
+    calls_src = os.path.join(CSRC, "torch_calls.cpp")
+    calls_obj = os.path.join(BUILD, "torch_calls-%s.o" % importlib.metadata.version("torch"))
+    calls = force or _stale(calls_obj, calls_src)
+    if calls:
+        jobs.append(_calls_compile(calls_src, calls_obj))
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -103,7 +145,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 print(" ".join(cmd))
                 print(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("nvcc failed for %s" % cmd[-3])
+                raise RuntimeError("compiling %s failed" % cmd[-3])
     product = [objs[src.replace(".cu", ".o")] for src in SOURCES]
     test_set = product[:]
     for src, oname, _ in TEST_SOURCES:  # the test build replaces the product object
@@ -114,6 +156,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         _link(TEST_LIB, test_set)
     if jobs or not os.path.exists(CHECKED_LIB) or force:
         _link(CHECKED_LIB, [objs[t[1]] for t in CHECKED_SOURCES])
+    if calls or not os.path.exists(CALLS_LIB) or os.path.getmtime(CALLS_LIB) < os.path.getmtime(calls_obj):
+        _link(CALLS_LIB, [calls_obj])
     return LIB
 
 

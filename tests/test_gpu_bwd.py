@@ -412,3 +412,24 @@ def test_wrapper_refusals():
         with pytest.raises(pkg.AttnError):
             pkg.attention_bwd(**{**base, **change})
     assert pkg.attn_check_status(None) == pkg.ATTN_OK
+
+
+@pytest.mark.parametrize("dt,o32,Sq,Skv", [(BF, False, 300, 300), (HF, True, 40, 7000), (F, False, 65, 64)], ids=str)
+def test_both_ways_through_the_wrapper(dt, o32, Sq, Skv):
+    """The host side in C++ takes ordinary calls and gives the bits of the Python one; what it does
+    not take, it leaves alone."""
+    x = {n: t.cuda() for n, t in make(1, 4, 2, Sq, Skv, 64, dt, seed=22, o32=o32, dlse=True).items()}
+    order = ("q", "k", "v", "o", "lse", "do", "dlse")
+    fast = lambda **change: pkg._fast().attention_bwd(*({**x, **change}[n] for n in order), True, 0.0)  # noqa: E731
+    for dlse in (x["dlse"], None):
+        a = fast(dlse=dlse)
+        out = tuple(torch.empty_like(x[n], dtype=x["o"].dtype) for n in "qkv")
+        b = pkg.attention_bwd(**{**x, "dlse": dlse}, causal=True, out=out)
+        assert type(a) is tuple and all(torch.equal(s, t) for s, t in zip(a, b))
+    other = HF if dt == F else F
+    for change in (dict(q=x["q"].cpu()), dict(k=x["k"][:, :, 1:]), dict(v=x["v"].to(other)), dict(do=x["do"].to(other)),
+                   dict(o=x["o"].to(torch.float64)), dict(lse=x["lse"].double()), dict(lse=x["lse"][:, :, 1:]),
+                   dict(dlse=x["lse"][:, 1:]), dict(dlse=x["lse"].cpu()), dict(q=x["q"].transpose(1, 2)),
+                   dict(lse=None), dict(k=x["k"][:, :1].repeat(1, 3, 1, 1), v=x["v"][:, :1].repeat(1, 3, 1, 1))):
+        assert fast(**change) is None
+    assert pkg._fast().attention_bwd(*(x[n] for n in order), True, math.nan) == pkg.ATTN_ERR_INVALID_ARG

@@ -68,7 +68,8 @@ def test_bounds_checking_build(dt, width, layout, monkeypatch):
     rot, pos = pkg.Rotary(width, layout=layout), positions(3, 41, 5000)
     lib = pkg.load_checked_library()
     monkeypatch.setattr(pkg, "load_library", lambda: lib)
-    q2, k2 = pkg.rotary(q, k, rot, pos)
+    # with outputs given the call goes through load_library()
+    q2, k2 = pkg.rotary(q, k, rot, pos, out=(torch.empty_like(q), torch.empty_like(k)))
     assert lib.attn_check_status(None) == pkg.ATTN_OK
     compare(q2, q, pos, rot)
     compare(k2, k, pos, rot)
@@ -223,3 +224,32 @@ def test_a_layer_there_and_back(dt, layout):
     o2, _ = pkg.attention(q1, kc, vc, causal=True)
     assert (o1.float() - o2.float()).abs().max() <= 2e-2
     assert pkg.attn_check_status(None) == pkg.ATTN_OK
+
+
+@pytest.mark.parametrize("dt", [BF, HF, F], ids=str)
+def test_both_ways_through_the_wrapper(dt):
+    """The host side in C++ takes ordinary calls and gives the bits of the Python one; what it does
+    not take, it leaves alone."""
+    x = rows(3, 41, 9, 64, dt=dt)
+    q, k = x[:, :, :6].transpose(1, 2), x[:, :, 6:].transpose(1, 2)
+    rot, pos = pkg.Rotary(48, layout="interleaved"), positions(3, 41, 5000)
+    fast = lambda *a: pkg._fast().rotary(*a, *rot._args)  # noqa: E731
+    for transpose in (False, True):
+        for kk, p in ((k, pos), (None, pos[:, 0].contiguous())):
+            a = fast(q, kk, p, transpose)
+            out = (torch.empty(q.shape, dtype=dt, device="cuda"),
+                   None if kk is None else torch.empty(k.shape, dtype=dt, device="cuda"))
+            b = pkg.rotary(q, kk, rot, p, transpose=transpose, out=out)
+            assert type(a) is tuple and a[0].is_contiguous() and torch.equal(a[0], b[0])
+            assert a[1] is None if kk is None else torch.equal(a[1], b[1])
+    class Rows(torch.Tensor):
+        pass
+    for args in ((q.cpu(), k, pos), (q, k.cpu(), pos), (q, k, pos.cpu()), (q, k, pos.long()), (q, k, pos[:2]),
+                 (q, k, pos.t()), (q, k[:, :, :5], pos), (q.double(), None, pos), (q[0], None, pos),
+                 (q[..., ::2], None, pos), (q[..., :32], None, pos), (q.as_subclass(Rows), None, pos), (q, 3, pos),
+                 (q, k, pos[:, :, None])):
+        assert fast(*args, False) is None
+    host = pkg.Rotary(48, device="cpu")
+    assert pkg._fast().rotary(q, k, pos, False, *host._args) is None
+    with pytest.raises(ValueError):
+        pkg.rotary(q, k, host, pos)

@@ -191,3 +191,15 @@ def test_rotary_angles_are_exact_fractions_of_a_turn():
         assert (t - want) % 2 ** 64 in (0, 1)
     neg = pkg.Rotary(2, frequencies=[-1.0], device="cpu")
     assert (neg.turns.item() + r.turns[0].item()) % 2 ** 64 == 0
+
+
+def test_calls_on_host_tensors_are_left_to_the_wrapper():
+    q, k, pos = torch.zeros(1, 2, 3, 64), torch.zeros(1, 1, 3, 64), torch.zeros(1, 3, dtype=torch.int32)
+    lse, rot = torch.zeros(1, 2, 3), pkg.Rotary(64, device="cpu")
+    assert pkg._fast().rotary(q, k, pos, False, *rot._args) is None
+    assert pkg._fast().rotary(q, None, pos, False) is None
+    assert pkg._fast().attention_bwd(q, k, k, q, lse, q, None, False, 0.0) is None
+    with pytest.raises(ValueError):
+        pkg.rotary(q, k, rot, pos)
+    with pytest.raises(ValueError):
+        pkg.attention_bwd(q, k, k, q, lse, q)
