@@ -20,8 +20,9 @@
 //    1 where the left operand of A wants k = t, t + 4, which is only another
 //    order of the summed rows, so Y's rows are read in that order.
 //  * The tensor cores' sums round towards zero.  T adds its large products (hi hi)
-//    apart from the small ones, and A's sums of a step start at zero and are
-//    added to the unit's in fp32, so that no sum takes more than 16 such roundings.
+//    apart from the small ones, 64 channels at a time (one sum over 128: error 1.06e-6 in
+//    place of 0.85e-6, 186 us in place of 190), and A's sums of a step start at zero and are
+//    added to the unit's in fp32, so that no sum takes more than 8 such roundings.
 //  * The next step's tiles are copied while this one's are multiplied (two stages).
 //  * The row statistics are computed where do has come (o is read once more for
 //    each kv unit, which costs less than a kernel of its own), so that a small
@@ -179,6 +180,8 @@ __device__ __forceinline__ void load_blocks(uint32_t (&r)[2], uint32_t addr) {
 template <int D, int N, int kLo>
 __device__ __forceinline__ void product(const float *X, const float *Y, int lane, float (&T)[N][4]) {
     constexpr int LD = D + 4, J = N > 1 ? 2 : 1;  // column tiles of one load
+    constexpr int kSum = D < 64 ? D : 64;         // channels of one sum of the tensor cores
+    static_assert(D <= 2 * kSum, "two sums at most");
     const uint32_t xa = ptx::smem_addr(X + (lane & 15) * LD + (lane >> 4) * 4);
     const uint32_t ya = ptx::smem_addr(Y + ((lane & 7) + (N > 1 ? lane >> 4 << 3 : 0)) * LD + (lane >> 3 & 1) * 4);
     float small[N][4];
@@ -186,30 +189,45 @@ __device__ __forceinline__ void product(const float *X, const float *Y, int lane
     for (int j = 0; j < N; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) T[j][e] = small[j][e] = 0.f;
+    auto channels = [&](float (&big)[N][4], int k0) {  // kSum of them from k0 on
 #pragma unroll 2
-    for (int k = 0; k < D; k += 8) {
-        Split a[4], b[N][2];
-        uint32_t x[4], xl[4];
-        load_blocks(x, xa + k * 4);
-        if constexpr (kLo > 0) load_blocks(xl, xa + (kLo + k) * 4);
+        for (int k = k0; k < k0 + kSum; k += 8) {
+            Split a[4], b[N][2];
+            uint32_t x[4], xl[4];
+            load_blocks(x, xa + k * 4);
+            if constexpr (kLo > 0) load_blocks(xl, xa + (kLo + k) * 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if constexpr (kLo > 0) a[e] = Split{x[e], xl[e]};
-            else a[e] = split(__uint_as_float(x[e]));
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (kLo > 0) a[e] = Split{x[e], xl[e]};
+                else a[e] = split(__uint_as_float(x[e]));
+            }
+#pragma unroll
+            for (int j = 0; j < N; j += J) {
+                uint32_t y[2 * J];
+                load_blocks(y, ya + (8 * j * LD + k) * 4);
+#pragma unroll
+                for (int e = 0; e < 2 * J; ++e) b[j + e / 2][e & 1] = split(__uint_as_float(y[e]));
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) mma(small[j], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[j][0].hi, b[j][1].hi);
+#pragma unroll
+            for (int j = 0; j < N; ++j) mma(big[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[j][0].hi, b[j][1].hi);
+#pragma unroll
+            for (int j = 0; j < N; ++j) mma(small[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[j][0].lo, b[j][1].lo);
         }
+    };
+    channels(T, 0);
+    if constexpr (D > kSum) {
+        float big[N][4];
 #pragma unroll
-        for (int j = 0; j < N; j += J) {
-            uint32_t y[2 * J];
-            load_blocks(y, ya + (8 * j * LD + k) * 4);
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int e = 0; e < 2 * J; ++e) b[j + e / 2][e & 1] = split(__uint_as_float(y[e]));
-        }
+            for (int e = 0; e < 4; ++e) big[j][e] = 0.f;
+        channels(big, kSum);
 #pragma unroll
-        for (int j = 0; j < N; ++j) mma(small[j], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[j][0].hi, b[j][1].hi);
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-        for (int j = 0; j < N; ++j) mma(T[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[j][0].hi, b[j][1].hi);
-#pragma unroll
-        for (int j = 0; j < N; ++j) mma(small[j], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[j][0].lo, b[j][1].lo);
+            for (int e = 0; e < 4; ++e) T[j][e] += big[j][e];
     }
 #pragma unroll
     for (int j = 0; j < N; ++j)
