@@ -161,7 +161,7 @@ ATTN_API int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, 
  * q, k, v or do may reach every gradient of its 128-row tile, masked or not.
  * Arithmetic: fp32 sums.  16-bit types: P and dS are rounded to 16 bits as
  * operands of the products (fp16: after scaling by powers of two that keep
- * them in range; dS of queries that see up to 128 keys: to twice as many bits).  fp32: each product
+ * them in range; dS of queries that see up to 128 keys, and P if Skv <= 128, to twice as many bits).  fp32: each product
  * of two numbers is wrong by 2^-21 of itself at most.  Sums are made in a fixed
  * order: equal calls give equal bits.
  * All arrays must be distinct; q, k, v, o, do and gradients 16-byte aligned.

@@ -51,8 +51,10 @@ bool bwd_plan(const Problem &call, BwdPlan *plan) {
     // rounding to 16 bits is most of what dq and dk are wrong by, and in a causal call it is
     // large beside the gradients of the later rows (8192 tokens in bf16: one element of dq
     // wrong by 0.44 of dq's root mean square, now 0.17).  Steps of query tiles whose first row
-    // sees at most kFewKeys keys therefore take dS in two parts, with one product more (2 heads
-    // of 128 keys 7.0 us in either form; 1024 heads of 100 keys 43.6 -> 48.9 us).  The rule goes
+    // sees at most kFewKeys keys therefore take dS in two parts, with one product more.  Where
+    // there are no more keys in all, P is in two parts too (2 heads of 128 keys 7.0 us in
+    // any form; 1024 heads of 100 keys 43.6 -> 51 us); in the first tile of a causal call that
+    // would cost the issuing warp of all steps another test (8192 tokens 5 %).  The rule goes
     // by positions alone, so that a result does not depend on what else is in the batch.
     plan->few = 0;
     if (p.Skv <= kFewKeys) plan->few = plan->nq;

@@ -35,13 +35,13 @@
 //    power of two from the norms of do and v (attn_bwd.cu), undone at the end.
 //    They also write a unit's sums: dv while the last A2 runs, then dk or dq.
 //  * Tensor memory (512 columns): Cfg.  P and dS overwrite the first 32 columns of
-//    each half of T1 and T2, the second part of dS (kFew) the next 32.
+//    each half of T1 and T2, the second parts (kTwo) the next 32.
 //  * Every mbarrier wait is bounded, as in the forward kernel.
 //
 // What bounds it: at D = 128 and long walks the tensor cores.  32 heads of 8192
 // tokens, causal, take 1085 us: the seven products of whole tiles run at 1.80 PFLOP/s, near the rate
 // that cuBLAS reaches on this GPU (the tensor pipe is busy 79 % of the clocks), 1.27
-// PFLOP/s of the five that a backward pass cannot do without.  1060 us without kFew: the
+// PFLOP/s of the five that a backward pass cannot do without.  1060 us without kTwo: the
 // issuing warp's test stands between a wait and the product that others wait for.  A step takes 2740
 // (kv) and 2060 (q) clocks in long walks, a unit's start and end about 4000 more,
 // which is what 2 x 4001 tokens (630 us, 1.04 PFLOP/s) and shorter calls lose.  At D
@@ -258,15 +258,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// What the rounding of x to `w` left, rounded itself.
 template <bool kBF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if constexpr (kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    else return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+__device__ __forceinline__ uint32_t pack_rest(float2 x, uint32_t w) {
+    float2 h;
+    if constexpr (kBF16) h = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else h = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return pack2<kBF16>(x.x - h.x, x.y - h.y);
 }
 
-// kFew: there are query tiles, the first p.few of each head, whose first query sees at most
-// kFewKeys keys; dS of those is held as the sum of two 16-bit numbers (BwdPlan::few).
-template <int D, bool kBF16, bool kFew>
+// kTwo: what is held as the sum of two 16-bit numbers (BwdPlan::few).  0: nothing; 1: dS of the
+// first p.few query tiles of each head; 2: P and dS throughout.
+template <int D, bool kBF16, int kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -533,9 +536,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             ok = wait_all(bars->x_full[0], xn & 1) && t1(0) && wait_all(bars->x_full[1], xn & 1) && t2(0);
             ++xn;
-            int y = kv ? w.y : w.x0 / kRows, zy = w.zy;  // the step's query tile (kFew)
+            int y = kv ? w.y : w.x0 / kRows, zy = w.zy;  // the step's query tile (kTwo 1)
             for (int i = 0; i < n && ok; ++i) {
-                const bool few = kFew && y < p.few;
+                const bool two = kTwo == 2 || (kTwo == 1 && y < p.few);
                 const int b1 = C::kTwoT1 && kv ? i & 1 : 0;
                 if (C::kTwoT1 && kv && i + 1 < n && !t1(i + 1)) { ok = false; break; }
                 // P(i) is written, or T1(i) read
@@ -545,6 +548,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (!need_acc()) { ok = false; break; }
                     ptx::tc_fence_after();
                     issue_a(C::kColA1, C::col_t1(b1), 1, pos + i, i > 0);
+                    if constexpr (kTwo == 2) issue_a(C::kColA1, C::col_t1(b1) + 32, 1, pos + i, true);
                     free_slot(1, pos + i);
                     if (i == n - 1) ptx::mma_commit_warp(bar(bars->acc_full[0]));
                 }
@@ -558,10 +562,10 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (buf) ++dn[1]; else ++dn[0];
                 ptx::tc_fence_after();
                 issue_a(C::kColA2, C::col_t2(buf), 0, pos + i, i > 0);
-                if (kFew && few) issue_a(C::kColA2, C::col_t2(buf) + 32, 0, pos + i, true);
+                if (two) issue_a(C::kColA2, C::col_t2(buf) + 32, 0, pos + i, true);
                 free_slot(0, pos + i);
                 if (kv && i + 1 < n) ok = t2(i + 1);
-                if (kFew && kv) advance(w, p, y, zy);
+                if (kTwo == 1 && kv) advance(w, p, y, zy);
             }
             if (!ok) break;
             ptx::mma_commit_warp(bar(bars->acc_full[1]));
@@ -600,8 +604,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             int y = w.y, zy = w.zy;
-            auto one = [&](auto few, int i) {
-                constexpr bool kTwo = decltype(few)::value;
+            auto one = [&](auto two, int i) {
+                constexpr bool kRest = decltype(two)::value;  // dS in two parts
                 const int y0 = y * kRows;
                 const int stage = sn % kStatStages;
                 [[maybe_unused]] const uint32_t st = sStat + stage * C::kStatBytes + half * 256;
@@ -641,7 +645,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 }
                 float2 pr[32];
-                uint32_t pk[32], rest[kTwo ? 32 : 1];
+                uint32_t pk[32], rest[kRest ? 32 : 1];
                 // P = exp2(scores)
                 auto weights = [&](int j) {
                     const uint32_t *s = &a[j >> 4][(2 * j) & 31];
@@ -658,8 +662,13 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         weights(j);
                         pk[j] = pack2<kBF16>(pr[j].x, pr[j].y);
                         pk[j + 1] = pack2<kBF16>(pr[j + 1].x, pr[j + 1].y);
+                        if constexpr (kTwo == 2) {
+                            rest[j] = pack_rest<kBF16>(pr[j], pk[j]);
+                            rest[j + 1] = pack_rest<kBF16>(pr[j + 1], pk[j + 1]);
+                        }
                     }
                     ptx::tmem_st32(tT1, pk);
+                    if constexpr (kTwo == 2) ptx::tmem_st32(tT1 + 32, rest);
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
                     arrive_warp(bar(bars->p_full[b1]), lane);
@@ -692,14 +701,13 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     z = __fmul2_rn(z, pr[j + 1]);
                     pk[j] = pack2<kBF16>(x.x, x.y);
                     pk[j + 1] = pack2<kBF16>(z.x, z.y);
-                    if constexpr (kTwo) {  // what the rounding leaves
-                        const float2 hx = unpack2<kBF16>(pk[j]), hz = unpack2<kBF16>(pk[j + 1]);
-                        rest[j] = pack2<kBF16>(x.x - hx.x, x.y - hx.y);
-                        rest[j + 1] = pack2<kBF16>(z.x - hz.x, z.y - hz.y);
+                    if constexpr (kRest) {
+                        rest[j] = pack_rest<kBF16>(x, pk[j]);
+                        rest[j + 1] = pack_rest<kBF16>(z, pk[j + 1]);
                     }
                 }
                 ptx::tmem_st32(tT2, pk);
-                if constexpr (kTwo) ptx::tmem_st32(tT2 + 32, rest);
+                if constexpr (kRest) ptx::tmem_st32(tT2 + 32, rest);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 arrive_warp(bar(bars->ds_full[buf]), lane);
@@ -711,9 +719,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 return true;
             };
             for (int i = 0; i < w.n; ++i) {
-                if (kFew && (KV ? y : w.x0 / kRows) < p.few) {
-                    if (!one(std::bool_constant<kFew>{}, i)) return false;
-                } else if (!one(std::false_type{}, i)) {
+                if (kTwo == 1 && (KV ? y : w.x0 / kRows) < p.few) {
+                    if (!one(std::bool_constant<(kTwo > 0)>{}, i)) return false;
+                } else if (!one(std::bool_constant<kTwo == 2>{}, i)) {
                     return false;
                 }
             }
@@ -793,7 +801,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool kBF16, bool kFew>
+template <int D, bool kBF16, int kTwo>
 int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
     using C = Cfg<D>;
     CUtensorMap tq, tk, tv, td;
@@ -845,7 +853,7 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
         p.hg = (int)hg;
     }
     p.timeout_ns = watchdog_ns();
-    auto kern = attn_bwd_tc_kernel<D, kBF16, kFew>;
+    auto kern = attn_bwd_tc_kernel<D, kBF16, kTwo>;
     // setmaxnreg needs exactly the registers it was planned for (see the forward kernel)
     static std::atomic<int> regs_ok{-1};
     int ok = regs_ok.load(std::memory_order_relaxed);
@@ -877,8 +885,10 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
 }
 
 template <int D, bool kBF16>
-int launch_few(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
-    return plan.few ? launch_typed<D, kBF16, true>(a, pr, plan, stream) : launch_typed<D, kBF16, false>(a, pr, plan, stream);
+int launch_two(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
+    if (pr.Skv <= kFewKeys) return launch_typed<D, kBF16, 2>(a, pr, plan, stream);
+    if (plan.few) return launch_typed<D, kBF16, 1>(a, pr, plan, stream);
+    return launch_typed<D, kBF16, 0>(a, pr, plan, stream);
 }
 
 }  // namespace
@@ -887,9 +897,9 @@ int launch_bwd_tc(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream) {
     const Problem &p = plan.p;
     const bool bf16 = p.dtype == ATTN_BF16 || p.dtype == ATTN_BF16_OUT_F32;
     if (p.d == 128)
-        return bf16 ? launch_few<128, true>(a, p, plan, stream) : launch_few<128, false>(a, p, plan, stream);
+        return bf16 ? launch_two<128, true>(a, p, plan, stream) : launch_two<128, false>(a, p, plan, stream);
     if (p.d == 64)
-        return bf16 ? launch_few<64, true>(a, p, plan, stream) : launch_few<64, false>(a, p, plan, stream);
+        return bf16 ? launch_two<64, true>(a, p, plan, stream) : launch_two<64, false>(a, p, plan, stream);
     return ATTN_ERR_INVALID_ARG;
 }
 

@@ -28,7 +28,8 @@ def backward64(q, k, v, o, lse, do, dlse=None, causal=False, scale=None):
     """dq, dk, dv and, for each, the largest error that the kernels' roundings allow.
 
     u is half a step of the operands of the products (P and dS), 0 for fp32 inputs; dS of queries
-    that see at most 128 keys is held in two such parts, which leaves u * u.  The other
+    that see at most 128 keys, and P if there are no more, are held in two such parts, which leaves
+    u * u.  The other
     terms are fp32 arithmetic: a product's sum over d channels in any order and an exponent of a
     few units in the last place of its largest term, and the sums over rows, all taken as 2^-20 of
     the sum of the terms' magnitudes (16 units; sums of n terms grow with sqrt(n) and stay far
@@ -54,8 +55,8 @@ def backward64(q, k, v, o, lse, do, dlse=None, causal=False, scale=None):
     ds = p * (dp - D)
     # errors of P (in fp32, and as an operand) and dS, which is made of P in fp32
     e32 = p * f * (1 + l0.abs() + scale * (q.abs() @ K.abs().mT))
-    ep = p * u + e32
     us = torch.where(seen.sum(-1, keepdim=True) <= 128, u * u, u)
+    ep = p * (u * u if Skv <= 128 else u) + e32
     mag = do.abs() @ V.abs().mT + (o.abs() * do.abs()).sum(-1, keepdim=True)
     if dlse is not None:
         mag = mag + dlse.double().abs()[..., None]

@@ -144,14 +144,16 @@ def test_fp32_gradients_of_16_bit_inputs(dt):
                                            (3, 1, 128, 129), (2, 2, 600, 300), (2, 1, 140, 128)])
 @pytest.mark.parametrize("dt,d", [(BF, 128), (HF, 64), (BF, 64), (HF, 128)])
 def test_queries_with_few_keys(dt, d, H, Hkv, Sq, Skv):
-    """dS is held to twice 16 bits for queries that see up to 128 keys: without the outputs' rounding
-    their dq, and the dk of the keys that only they see, come out that close."""
+    """dS of queries that see up to 128 keys is held to twice 16 bits, and P where there are no more:
+    without the outputs' rounding their dq, and dk and dv of calls with no other, come out that close."""
     x = make(1, H, Hkv, Sq, Skv, d, dt, seed=Sq + Skv, o32=True, causal=True)
     check(x, True)
     seen = torch.arange(Sq) + 1 + Skv - Sq
     few = int((seen <= 128).sum())
     want, errors = backward64(**x, causal=True)
     assert few > 0 and (errors[0][:, :, :few] <= 2.0 ** -13 * want[0].abs().amax()).all()
+    if Skv <= 128:
+        assert all((e <= 2.0 ** -13 * w.abs().amax()).all() for e, w in zip(errors, want))
 
 
 @pytest.mark.parametrize("size", [1e-7, 1e-4, 300.0])
