@@ -46,7 +46,8 @@
 // the product that others wait for.)  A step takes 2740 (kv) and 2060 (q) clocks in
 // long walks, a unit's start and end about 4000 more, which is what 2 x 4001
 // tokens (635 us, 1.03 PFLOP/s) and shorter calls lose.  At D = 64 the
-// chain of exponentials and conversions is longer than the products: 1840 and 1400 clocks a step of 1024 and 768.
+// chain of exponentials and conversions is longer than the products: 1840 and 1400
+// clocks a step of 1024 and 768.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
