@@ -69,6 +69,10 @@ bool bwd_plan(const Problem &call, BwdPlan *plan) {
     };
     plan->ns_kv = cut(len_kv);
     plan->ns_q = cut(len_q);
+    // The units with the longer walks start first, so that the last ones are short (fp32, 2 x
+    // 8 heads of 40 queries to 2000 keys, d = 64: 70 -> 45 us; 77 queries of 32768 keys, 32
+    // heads in bf16: 178 -> 167 us).
+    plan->q_first = len_q / plan->ns_q > len_kv / plan->ns_kv;
     const double units = (double)bhk * plan->nk * plan->ns_kv + (double)bh * plan->nq * plan->ns_q;
     if (units > (double)(INT32_MAX / 2)) return false;
     plan->n_units = (int64_t)units;

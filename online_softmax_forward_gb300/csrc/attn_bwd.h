@@ -46,6 +46,7 @@ struct BwdPlan {
     int tile;           // rows of a unit's own tile
     int nq, nk;         // query and key tiles of that size
     int ns_kv, ns_q;    // splits of a kv unit and of a q unit
+    bool q_first;       // q units come before kv units
     int few;            // 16-bit types: query tiles of a head, from the first on, with dS in two parts
     int64_t n_units;
     size_t off_stats, off_max, off_part_kv, off_part_q, bytes;

@@ -76,7 +76,7 @@ struct Params {
     int off, wrap;   // of BwdPlan
     int nq, nk;      // X tiles of a slice: query rows, keys
     int yq;          // Y tiles of query rows of a slice
-    int ns_kv, ns_q;
+    int ns_kv, ns_q, q_first;
     float scale_log2, scale;
     int *status;
 };
@@ -291,10 +291,10 @@ attn_bwd_f32_kernel(const Params p) {
     const int g = lane >> 2, t = lane & 3;
     const int xw = warp % R * 16, yw = warp / R * (8 * N);  // first row and column of the warp
 
-    // the unit: kv units first, longest first where the call is causal
-    const int n_kv = p.BHk * p.nk * p.ns_kv;
-    const bool kv = (int)blockIdx.x < n_kv;
-    int u = kv ? (int)blockIdx.x : (int)blockIdx.x - n_kv;
+    // the unit: the kind of BwdPlan::q_first first, longest first where the call is causal
+    const int n_kv = p.BHk * p.nk * p.ns_kv, n_q = p.BH * p.nq * p.ns_q;
+    const bool kv = p.q_first ? (int)blockIdx.x >= n_q : (int)blockIdx.x < n_kv;
+    int u = (int)blockIdx.x - (kv ? (p.q_first ? n_q : 0) : (p.q_first ? 0 : n_kv));
     const int slices = kv ? p.BHk : p.BH, ns = kv ? p.ns_kv : p.ns_q;
     int tile = u / (slices * ns);
     u -= tile * slices * ns;
@@ -467,6 +467,7 @@ int launch_bwd_f32(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream) {
     p.nk = plan.nk;
     p.ns_kv = plan.ns_kv;
     p.ns_q = plan.ns_q;
+    p.q_first = plan.q_first;
     p.yq = (pr.Sq + kT - 1) / kT;
     p.scale_log2 = pr.scale * 1.4426950408889634f;
     p.scale = pr.scale;

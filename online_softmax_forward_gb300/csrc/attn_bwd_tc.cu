@@ -148,7 +148,7 @@ struct Params {
     void *dk, *dv, *dq;               // gradients, or the splits' partial sums
     int BH, BHk, group, Sq, Skv, causal;
     int off, wrap, few;  // of BwdPlan
-    int nq, nk, ns_kv, ns_q;
+    int nq, nk, ns_kv, ns_q, q_first;
     int hg;       // kv slices per schedule group
     int n_units;
     int kv_f32, q_f32;  // fp32 output of dk and dv, of dq
@@ -158,8 +158,8 @@ struct Params {
     unsigned long long timeout_ns;
 };
 
-// Unit u of the schedule: groups of hg kv slices; in a group first the kv units,
-// then the q units, longest first (causal: first key tiles, last query tiles).
+// Unit u of the schedule: groups of hg kv slices; in a group first the kv units, then
+// the q units (or the other way round, BwdPlan::q_first), longest first (causal: first key tiles, last query tiles).
 __device__ __forceinline__ Unit decode_unit(int u, const Params &p) {
     Unit r;
     const int a_head = p.nk * p.ns_kv, b_head = p.group * p.nq * p.ns_q;
@@ -168,7 +168,10 @@ __device__ __forceinline__ Unit decode_unit(int u, const Params &p) {
     int rem = u - g * per_group;
     const int heads = min(p.hg, p.BHk - g * p.hg);
     const bool skips = p.causal && !p.wrap;  // whole tiles that the mask leaves out
-    if (rem < heads * a_head) {
+    const int n_first = heads * (p.q_first ? b_head : a_head);  // units of the kind that comes first
+    const bool kv = p.q_first ? rem >= n_first : rem < n_first;
+    if (rem >= n_first) rem -= n_first;
+    if (kv) {
         const int width = heads * p.ns_kv;
         const int tile = rem / width;
         rem -= tile * width;
@@ -186,7 +189,6 @@ __device__ __forceinline__ Unit decode_unit(int u, const Params &p) {
         r.zy = r.zx * p.group + skip;
         r.y = r.first + t0 - skip * per;
     } else {
-        rem -= heads * a_head;
         const int width = heads * p.group * p.ns_q;
         int tile = rem / width;
         rem -= tile * width;
@@ -827,6 +829,7 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
     p.nk = plan.nk;
     p.ns_kv = plan.ns_kv;
     p.ns_q = plan.ns_q;
+    p.q_first = plan.q_first;
     p.n_units = (int)plan.n_units;
     p.scale_log2 = pr.scale * 1.4426950408889634f;
     p.scale = pr.scale;
