@@ -160,8 +160,12 @@ ATTN_API int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, 
  * writes dq = 0; Sq == 0 writes dk = dv = 0.  Infinities and NaN in a row of
  * q, k, v or do may reach every gradient of its 128-row tile, masked or not.
  * Arithmetic: fp32 sums.  16-bit types: P and dS are rounded to 16 bits as
- * operands of the products (fp16: after scaling by powers of two that keep
- * them in range; dS of queries that see up to 128 keys, and P if Skv <= 128, to twice as many bits).  fp32: each product
+ * operands of the products (dS of queries that see up to 128 keys, and P if
+ * Skv <= 128, to twice as many bits).  fp16: after scaling by powers of two, P by
+ * one for all, dS by one for each row of dq and one for each 128 rows of dk, from
+ * the norms of what makes it, so that heads and sequences of very different do
+ * share a call without loss; in a row of dk, terms of queries whose do is less
+ * than 2^-26 of the largest one of the same kv head lose bits.  fp32: each product
  * of two numbers is wrong by 2^-21 of itself at most.  Sums are made in a fixed
  * order: equal calls give equal bits.
  * All arrays must be distinct; q, k, v, o, do and gradients 16-byte aligned.

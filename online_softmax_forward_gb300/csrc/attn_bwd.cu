@@ -23,10 +23,10 @@ bool bwd_plan(const Problem &call, BwdPlan *plan) {
     }
     plan->p = p;
     if (p.Sq > INT32_MAX - 1024 || p.Skv > INT32_MAX - 1024) return false;  // ends of tiles fit 31 bits
-    const bool f32 = p.dtype == ATTN_F32;
+    const bool f32 = p.dtype == ATTN_F32, f16 = p.dtype == ATTN_F16 || p.dtype == ATTN_F16_OUT_F32;
     const int64_t bh = p.bh(), bhk = p.bh_kv();
     // the sizes below are products of these; anything near 2^62 bytes is refused first
-    const double est = 4.0 * 2 * kMaxBwdSplits * ((double)bh * (p.Sq + 128.0) + (double)bhk * (p.Skv + 128.0)) *
+    const double est = 4.0 * kScaleRows * kMaxBwdSplits * ((double)bh * (p.Sq + 128.0) + (double)bhk * (p.Skv + 128.0)) *
                        (p.d + 2.0);
     if (est > 4.0e18) return false;
     // rows of a unit's own tile and of the tiles it walks over
@@ -78,8 +78,12 @@ bool bwd_plan(const Problem &call, BwdPlan *plan) {
     plan->n_units = (int64_t)units;
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     plan->off_stats = f32 ? 0 : 256;  // fp32 units compute the statistics themselves
-    plan->off_max = plan->off_stats + (f32 ? 0 : up((size_t)bh * tiles(p.Sq, kStatTile) * 2 * kStatTile * 4));
-    plan->off_part_kv = plan->off_max + (f32 ? 0 : up(3 * (size_t)kPreBlocks * 4));
+    const size_t stat_tiles = (size_t)bh * tiles(p.Sq, kStatTile);
+    plan->off_max = plan->off_stats + (f32 ? 0 : up(stat_tiles * (f16 ? kScaleRows : 2) * kStatTile * 4));
+    plan->off_max_v = plan->off_max + (f16 ? up(stat_tiles * 2 * 4) : 0);
+    const size_t maxima = (f16 ? up(stat_tiles * 2 * 4) + up((size_t)bhk * tiles(p.Skv, kStatTile) * 4) : 0);
+    // bf16 leaves this room unused; workspaces keep their least size
+    plan->off_part_kv = plan->off_max + (f32 ? 0 : std::max(maxima, up(kMaximaBytes)));
     plan->off_part_q = plan->off_part_kv +
                        (plan->ns_kv > 1 ? up((size_t)plan->ns_kv * bhk * p.Skv * p.d * 2 * 4) : 0);
     plan->bytes = plan->off_part_q + (plan->ns_q > 1 ? up((size_t)plan->ns_q * bh * p.Sq * p.d * 4) : 0);
@@ -109,44 +113,42 @@ struct PreParams {
     const void *o, *dout, *v;
     const float *lse, *dlse;
     float *stats;
-    float *maxima;        // fp16: [3][gridDim.x], the CTAs' largest |do|, |D| and |v| rows
-    unsigned *counter;    // [2]: of the units, set to 0; how many CTAs left maxima
-    int64_t tiles, v_rows;  // blocks of statistics, rows of v
-    int Sq, tiles_per_head;
-    float add;            // to nl (fp16: P is kept times 2^add)
+    float *max_q, *max_v;   // fp16: [tiles][2] largest |do| and |D|, [v_tiles] largest |v|
+    unsigned *counter;      // of the units, set to 0
+    int64_t tiles, v_tiles; // blocks of statistics, tiles of v
+    int Sq, tiles_per_head, Skv, v_tiles_per_head;
+    float add;              // to nl (fp16: P is kept times 2^add)
     int *status;
 };
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
+    return x;
+}
 
 // Row statistics.  D / E lanes share a row (E elements of do in 16 bytes), four rows at
 // a time with all loads first; what bounds it is reading o and do once (32 heads of
 // 8192 rows of 128 in bf16, 135 MB: 24 us, 5.6 TB/s).
 //
-// fp16 (kScale): dS is held in fp16 for the products with q and k, and its size
-// follows that of do, which a loss scale or its absence moves by orders of
-// magnitude.  |dS| <= |do| |v| + |D|, so the largest norms of the rows give a
-// power of two that keeps dS in range whatever the size of do; each CTA leaves
-// its maxima, which the next kernel joins.
+// fp16 (kScale): a CTA takes whole tiles, so that it can join their largest norms (attn_bwd.h),
+// and then tiles of v.
 template <typename TD, typename TO, int D, bool kScale>
 __global__ void __launch_bounds__(kPreThreads) bwd_stats_kernel(const PreParams p) {
     constexpr int E = 16 / sizeof(TD), L = D / E;  // elements of a lane, lanes of a row
     constexpr int R = 32 / L;                      // rows of a warp
-    static_assert(L >= 1 && L <= 32 && kStatTile % R == 0, "lanes");
+    constexpr int U = 4;                           // rows of a lane group, all loads first
+    constexpr int kGroups = kStatTile / (R * U);   // times a warp reads, in a tile
+    constexpr int kWarps = kPreThreads / 32;
+    constexpr int kPer = kScale ? kScaleRows : 2;
+    static_assert(L >= 1 && L <= 32 && kStatTile % (R * U) == 0, "lanes");
     const int lane = threadIdx.x & 31, sub = lane % L, rw = lane / L;
-    const int64_t warp = ((int64_t)blockIdx.x * kPreThreads + threadIdx.x) >> 5;
-    const int64_t warps = (int64_t)gridDim.x * kPreThreads >> 5;
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        p.counter[0] = 0u;
-        p.counter[1] = gridDim.x;
-    }
-    float big_do = 0.f, big_d = 0.f, big_v = 0.f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.counter[0] = 0u;
     // the next kernel may be set up on SMs that this one leaves free; it waits for the results
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // U rows a lane group at a time, all loads first
-    constexpr int U = kStatTile / R < 4 ? kStatTile / R : 4;
-    const int64_t groups = p.tiles * (kStatTile / R / U);
-    for (int64_t w = warp; w < groups; w += warps) {
-        const int64_t tile = w / (kStatTile / R / U);
-        const int in_tile = (int)(w % (kStatTile / R / U)) * (R * U) + rw;
+    [[maybe_unused]] float big_do = 0.f, big_d = 0.f;
+    auto group = [&](int64_t tile, int g) {
+        const int in_tile = g * (R * U) + rw;
         const int64_t bh = tile / p.tiles_per_head;
         const int row0 = (int)(tile - bh * p.tiles_per_head) * kStatTile + in_tile;
         Row<TD, E> x[U];
@@ -186,47 +188,73 @@ __global__ void __launch_bounds__(kPreThreads) bwd_stats_kernel(const PreParams 
                 if constexpr (kScale) sq += __shfl_xor_sync(0xffffffffu, sq, s);
             }
             if (sub != 0) continue;
+            float norm = 0.f;
             if (row < p.Sq) {
                 nl = l[u] == -INFINITY ? -INFINITY : fmaf(l[u], -1.4426950408889634f, p.add);
                 nd = dl[u] - dot;
                 if (kScale && l[u] != -INFINITY) {
-                    big_do = fmaxf(big_do, sq);
-                    big_d = fmaxf(big_d, fabsf(nd));
+                    norm = sqrtf(sq);
+                    if (norm < INFINITY && fabsf(nd) < INFINITY) {  // false for NaN, too
+                        big_do = fmaxf(big_do, norm);
+                        big_d = fmaxf(big_d, fabsf(nd));
+                    }
                 }
             }
-            float *st = p.stats + (size_t)tile * 2 * kStatTile + in_tile + u * R;
+            float *st = p.stats + (size_t)tile * kPer * kStatTile + in_tile + u * R;
             if (in_bounds(tile < p.tiles && in_tile + u * R < kStatTile, p.status)) {
                 st[0] = nl;
                 st[kStatTile] = nd;
+                if constexpr (kScale) st[2 * kStatTile] = norm;
             }
         }
-    }
-    if constexpr (kScale) {
-        for (int64_t w = warp; w * R < p.v_rows; w += warps) {
-            const int64_t row = w * R + rw;
-            float sq = 0.f;
-            if (row < p.v_rows) {
-                const auto x = *reinterpret_cast<const Row<TD, E> *>((const TD *)p.v + (size_t)row * D + sub * E);
+    };
+    if constexpr (!kScale) {
+        const int64_t warp = ((int64_t)blockIdx.x * kPreThreads + threadIdx.x) >> 5;
+        const int64_t warps = (int64_t)gridDim.x * kPreThreads >> 5;
+        for (int64_t w = warp; w < p.tiles * kGroups; w += warps) group(w / kGroups, (int)(w % kGroups));
+    } else {
+        __shared__ float part[2][kWarps];
+        const int warp = threadIdx.x >> 5;
+        for (int64_t item = blockIdx.x; item < p.tiles + p.v_tiles; item += gridDim.x) {
+            big_do = big_d = 0.f;
+            const bool of_v = item >= p.tiles;
+            if (!of_v) {
+                for (int g = warp; g < kGroups; g += kWarps) group(item, g);
+            } else {
+                const int64_t tile = item - p.tiles, slice = tile / p.v_tiles_per_head;
+                const int row0 = (int)(tile - slice * p.v_tiles_per_head) * kStatTile;
+#pragma unroll 4
+                for (int i = warp * R + rw; i < kStatTile; i += kWarps * R) {
+                    float sq = 0.f;
+                    if (row0 + i < p.Skv) {
+                        const auto x = *reinterpret_cast<const Row<TD, E> *>(
+                            (const TD *)p.v + ((size_t)slice * p.Skv + row0 + i) * D + sub * E);
 #pragma unroll
-                for (int i = 0; i < E; ++i) sq = fmaf(to_f(x.e[i]), to_f(x.e[i]), sq);
+                        for (int e = 0; e < E; ++e) sq = fmaf(to_f(x.e[e]), to_f(x.e[e]), sq);
+                    }
+#pragma unroll
+                    for (int s = L / 2; s > 0; s >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, s);
+                    if (sq < INFINITY) big_do = fmaxf(big_do, sqrtf(sq));
+                }
             }
+            big_do = warp_max(big_do);
+            big_d = warp_max(big_d);
+            if (lane == 0) {
+                part[0][warp] = big_do;
+                part[1][warp] = big_d;
+            }
+            __syncthreads();
+            if (threadIdx.x < 2) {
+                float x = 0.f;
 #pragma unroll
-            for (int s = L / 2; s > 0; s >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, s);
-            big_v = fmaxf(big_v, sq);
-        }
-        __shared__ float part[3][kPreThreads / 32];
-        float m[3] = {sqrtf(big_do), big_d, sqrtf(big_v)};
-#pragma unroll
-        for (int j = 0; j < 3; ++j) {
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], s));
-            if (lane == 0) part[j][threadIdx.x >> 5] = m[j];
-        }
-        __syncthreads();
-        if (threadIdx.x < 3) {
-            float x = 0.f;
-            for (int i = 0; i < kPreThreads / 32; ++i) x = fmaxf(x, part[threadIdx.x][i]);
-            p.maxima[threadIdx.x * kPreBlocks + blockIdx.x] = x;
+                for (int i = 0; i < kWarps; ++i) x = fmaxf(x, part[threadIdx.x][i]);
+                if (!of_v) {
+                    p.max_q[2 * item + threadIdx.x] = x;
+                } else if (threadIdx.x == 0) {
+                    p.max_v[item - p.tiles] = x;
+                }
+            }
+            __syncthreads();
         }
     }
 }
@@ -274,8 +302,12 @@ __global__ void __launch_bounds__(kSumThreads) bwd_sum_kernel(const SumParams p)
 template <typename TD, typename TO, int D, bool kScale>
 int launch_stats(const PreParams &p, cudaStream_t stream) {
     constexpr int R = 32 / (D * (int)sizeof(TD) / 16);
-    const int64_t warps = p.tiles * (kStatTile / R / 4) + (kScale ? (p.v_rows + R - 1) / R : 0);
-    int64_t grid = (warps + kPreThreads / 32 - 1) / (kPreThreads / 32);
+    const int64_t warps = p.tiles * (kStatTile / R / 4);
+    int64_t grid = kScale ? p.tiles + p.v_tiles : (warps + kPreThreads / 32 - 1) / (kPreThreads / 32);
+    if (kScale && grid > kPreBlocks) {  // equal shares of whole tiles
+        const int64_t rounds = (grid + kPreBlocks - 1) / kPreBlocks;
+        grid = (grid + rounds - 1) / rounds;
+    }
     if (grid > kPreBlocks) grid = kPreBlocks;
     bwd_stats_kernel<TD, TO, D, kScale><<<(unsigned)grid, kPreThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
@@ -305,11 +337,14 @@ int launch_bwd(const BwdArgs &a, const BwdPlan &plan, cudaStream_t stream) {
     r.dlse = a.dlse;
     r.counter = (unsigned *)ws;
     r.stats = (float *)(ws + plan.off_stats);
-    r.maxima = (float *)(ws + plan.off_max);
+    r.max_q = (float *)(ws + plan.off_max);
+    r.max_v = (float *)(ws + plan.off_max_v);
     r.tiles_per_head = (p.Sq + kStatTile - 1) / kStatTile;
     r.tiles = p.bh() * r.tiles_per_head;
-    r.v_rows = p.bh_kv() * p.Skv;
+    r.v_tiles_per_head = (p.Skv + kStatTile - 1) / kStatTile;
+    r.v_tiles = p.bh_kv() * r.v_tiles_per_head;
     r.Sq = p.Sq;
+    r.Skv = p.Skv;
     r.add = f16 ? (float)kBwdP16Log2 : 0.f;
     r.status = status_word_device_ptr();
     if (!r.status) return ATTN_ERR_CUDA;

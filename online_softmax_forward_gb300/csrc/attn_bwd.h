@@ -23,6 +23,17 @@
 // no key, so that its P is 0) and nd = -D.  For the 16-bit types a first kernel
 // writes them as [B * H][query tiles of 128][2][128], rows behind Sq with nl =
 // -inf, nd = 0; fp32 units compute them as they load do.
+//
+// fp16: dS is held in fp16 for the products with q and k, and its size follows that of
+// do, which a loss scale or its absence, and the weight of a sequence or a token in the
+// loss, move by orders of magnitude.  |dS| <= |do| |v| + |D|, so norms of the rows give a
+// power of two that brings dS to 2^14 at most; it has to be one for all terms of a sum:
+//     dq: one for each query row, from its |do| and |D| and the largest |v| of its kv head;
+//     dk: one for each kv unit, from the largest |do| and |D| of the query tiles it walks
+//         over and the largest |v| of its keys.
+// So no head's precision depends on another's do.  The first kernel writes |do| of each row
+// as a third number beside nl and nd (kScaleRows), and the largest values of each query tile
+// and of each tile of v, which the units join.  Rows with an infinity or a NaN do not count.
 #pragma once
 
 #include <stddef.h>
@@ -38,6 +49,8 @@ constexpr int kMaxBwdSplits = 64;
 constexpr int kFewKeys = 128;    // see BwdPlan::few
 constexpr int kBwdP16Log2 = 14;  // fp16: P is kept times 2^14, so that small weights stay normal numbers
 constexpr int kPreBlocks = 1216; // CTAs of the first kernel at most
+constexpr size_t kMaximaBytes = 3 * kPreBlocks * 4;
+constexpr int kScaleRows = 3;    // fp16: numbers of a query row that the first kernel writes (bf16: 2)
 
 struct BwdPlan {
     Problem p;          // the problem the kernels run, see below
@@ -49,7 +62,8 @@ struct BwdPlan {
     bool q_first;       // q units come before kv units
     int few;            // 16-bit types: query tiles of a head, from the first on, with dS in two parts
     int64_t n_units;
-    size_t off_stats, off_max, off_part_kv, off_part_q, bytes;
+    // fp16: off_max [B * H][query tiles][2] largest |do| and |D|, off_max_v [B * H_kv][key tiles] largest |v|
+    size_t off_stats, off_max, off_max_v, off_part_kv, off_part_q, bytes;
 };
 
 struct BwdArgs {

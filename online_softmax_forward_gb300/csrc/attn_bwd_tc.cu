@@ -32,7 +32,8 @@
 //    memory four times as long).  P stays in fp32 registers between the two; it is
 //    rounded to 16 bits for A1 alone, and dS for A2 (as the tensor core takes 16-bit
 //    operands; the sums are fp32).  fp16: P is kept times 2^14, and dS times a
-//    power of two from the norms of do and v (attn_bwd.cu), undone at the end.
+//    power of two from the norms of do and v (attn_bwd.h), undone at the end; warp 10
+//    joins a unit's norms from their tiles while its first products are on their way.
 //    They also write a unit's sums: dv while the last A2 runs, then dk or dq.
 //  * Tensor memory (512 columns): Cfg.  P and dS overwrite the first 32 columns of
 //    each half of T1 and T2, the second parts (kTwo) the next 32.
@@ -69,11 +70,12 @@ namespace {
 constexpr int kRows = 128;  // rows of every tile
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kScaleWarp = 10;  // fp16
 constexpr int kThreads = 12 * 32;
 constexpr int kComputeWarps = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSchedRing = 4;
-constexpr int kSchedReaders = 9;  // issuer and 8 computing warps
+constexpr int kSchedReaders = 9;  // issuer and 8 computing warps; fp16: and the warp of the scales
 constexpr int kStatStages = 2;
 constexpr int kLaunchRegs = 168;
 constexpr int kComputeRegs = 224;
@@ -134,16 +136,17 @@ struct Bars {
     uint64_t acc_full[2], acc_empty;  // A1 and A2 of a unit complete; both read
     uint64_t mma_done;
     uint64_t sched_full[kSchedRing], sched_empty[kSchedRing];
+    uint64_t norm_full[kSchedRing];
     Unit sched_unit[kSchedRing];
+    float norm[kSchedRing];  // fp16: a bound of the unit's |dS| (kv unit), the largest |v| (q unit)
     uint32_t tmem_base;
     int abort_flag;
-    float ds_scale;  // fp16: 2^e of dS over that of P
 };
 static_assert(sizeof(Bars) <= 896, "barrier block");
 
 struct Params {
     const float *stats;
-    const float *maxima;
+    const float *max_q, *max_v;  // fp16, of BwdPlan
     unsigned *counter;
     void *dk, *dv, *dq;               // gradients, or the splits' partial sums
     int BH, BHk, group, Sq, Skv, causal;
@@ -218,6 +221,13 @@ __device__ __forceinline__ void advance(const Unit &w, const Params &p, int &y, 
     }
 }
 
+// fp16: what brings P dS' (P is kept times 2^14) to 2^14 at most where |dS'| <= most.
+__device__ __forceinline__ float ds_scale_of(float most) {
+    int e = 0;
+    if (most > 0.f && most < INFINITY) e = max(-100, min(100, 13 - ilogbf(most)));
+    return ldexpf(1.f, e - kBwdP16Log2);
+}
+
 template <bool kBF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (kBF16) {
@@ -279,6 +289,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                    const Params p) {
     using C = Cfg<D>;
     constexpr int kSlots = C::kSlots1 + C::kSlots2;
+    constexpr int kPer = kBF16 ? 2 : kScaleRows;  // numbers of a row's statistics
     // the tiles' swizzle needs 1024-byte alignment, which this declaration asks
     // for: there is no room to align by hand at D = 128
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -319,7 +330,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         ptx::mbar_init(bar(bars->mma_done), 1);
         for (int s = 0; s < kSchedRing; ++s) {
             ptx::mbar_init(bar(bars->sched_full[s]), 1);
-            ptx::mbar_init(bar(bars->sched_empty[s]), kSchedReaders);
+            ptx::mbar_init(bar(bars->sched_empty[s]), kSchedReaders + (kBF16 ? 0 : 1));
+            ptx::mbar_init(bar(bars->norm_full[s]), 1);
         }
         bars->abort_flag = 0;
         ptx::fence_mbar_init();
@@ -337,28 +349,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // Launched while the kernel of the row statistics still runs: nothing of it, or of
     // what came before it, is read above.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if constexpr (!kBF16) {
-        // |dS| <= max |do| max |v| + max |D|: the exponent that brings it to 2^14 at most
-        if (warp == 11) {
-            float m[3] = {0.f, 0.f, 0.f};
-            const int n = (int)p.counter[1];
-            for (int j = 0; j < 3; ++j) {
-                for (int i = lane; i < min(n, kPreBlocks); i += 32) m[j] = fmaxf(m[j], p.maxima[j * kPreBlocks + i]);
-                for (int s = 16; s > 0; s >>= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], s));
-            }
-            const float most = fmaf(m[0], m[2], m[1]);
-            int e = 0;
-            if (most > 0.f && most < INFINITY) e = max(-100, min(100, 13 - ilogbf(most)));
-            if (lane == 0) bars->ds_scale = ldexpf(1.f, e - kBwdP16Log2);
-        }
-    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
-    // The producer's k-th claim for a consumer warp; false if the CTA is aborting.
-    auto next_unit = [&](uint32_t &k, Unit &w) {
+    // The producer's k-th claim for a consumer warp, and the unit's norm where one is asked
+    // for; false if the CTA is aborting.
+    auto next_unit = [&](uint32_t &k, Unit &w, float *norm = nullptr) {
         const uint32_t s = k % kSchedRing;
         if (!__all_sync(0xffffffffu, watch.wait(bar(bars->sched_full[s]), (k / kSchedRing) & 1)))
             return false;
@@ -371,6 +369,10 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         w.n = su->n;
         w.first = su->first;
         w.split = su->split;
+        if (norm && w.kind >= 0) {
+            if (!__all_sync(0xffffffffu, watch.wait(bar(bars->norm_full[s]), (k / kSchedRing) & 1))) return false;
+            *norm = *(const volatile float *)&bars->norm[s];
+        }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(bars->sched_empty[s]));
         ++k;
@@ -418,7 +420,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!watch.wait(bar(bars->st_empty[s]), ((sn / kStatStages) & 1) ^ 1)) return false;
                 if (!in_bounds(y >= 0 && y < p.nq && zy >= 0 && zy < p.BH, p.status)) return stop();
                 ptx::mbar_arrive_expect_tx(bar(bars->st_full[s]), C::kStatBytes);
-                bulk_load(sStat + s * C::kStatBytes, p.stats + ((size_t)zy * p.nq + y) * 2 * kStatTile,
+                bulk_load(sStat + s * C::kStatBytes, p.stats + ((size_t)zy * p.nq + y) * kPer * kStatTile,
                           C::kStatBytes, bar(bars->st_full[s]));
                 ++sn;
                 return true;
@@ -584,7 +586,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int half = warp >> 2;  // columns [64 half, 64 half + 64) of T1 and T2
         const int r = (warp & 3) * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const float ds_scale = kBF16 ? 1.f : bars->ds_scale;
+        float norm = 0.f, ds_scale = 1.f;  // fp16: of the unit, of this thread's row
         uint32_t n1[2] = {0, 0}, n2[2] = {0, 0}, sn = 0, an[2] = {0, 0};
         bool ok = true;
 
@@ -600,11 +602,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const float2 sc = make_float2(p.scale_log2, p.scale_log2);
             float rl = 0.f, rd = 0.f;  // q unit: nl and nd of this thread's row
             if constexpr (!KV) {
-                const float *st = p.stats + ((size_t)w.zx * p.nq + w.x0 / kRows) * 2 * kStatTile + r;
+                const float *st = p.stats + ((size_t)w.zx * p.nq + w.x0 / kRows) * kPer * kStatTile + r;
                 if (in_bounds(w.zx < p.BH && w.x0 / kRows < p.nq, p.status)) {
                     rl = st[0];
                     rd = st[kStatTile];
+                    if constexpr (!kBF16) ds_scale = ds_scale_of(fmaf(st[2 * kStatTile], norm, fabsf(rd)));
                 }
+            } else if constexpr (!kBF16) {
+                ds_scale = ds_scale_of(norm);
             }
             int y = w.y, zy = w.zy;
             auto one = [&](auto two, int i) {
@@ -733,7 +738,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
         for (uint32_t k = 0; ok;) {
             Unit w;
-            if (!next_unit(k, w)) { ok = false; break; }
+            if (!next_unit(k, w, kBF16 ? nullptr : &norm)) { ok = false; break; }
             if (w.kind < 0) break;
             const bool kv = w.kind == 0;
             const int row = w.x0 + r;
@@ -793,8 +798,38 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
     } else {
-        // warps 10 and 11 only give up their registers
+        // the other warps only give up their registers, but for fp16's norms
         ptx::setmaxnreg_dec<kOtherRegs>();
+        if (!kBF16 && warp == kScaleWarp) {
+            for (uint32_t k = 0;;) {
+                const uint32_t s = k % kSchedRing;
+                Unit w;
+                if (!next_unit(k, w) || w.kind < 0) break;
+                float a = 0.f, d = 0.f, v = 0.f;
+                if (w.kind == 0) {
+                    const int per = p.nq - w.first;
+                    for (int i = lane; i < w.n; i += 32) {
+                        const int t = w.y - w.first + i, head = w.zy + t / per, y = w.first + t % per;
+                        if (!in_bounds(head < p.BH && y < p.nq, p.status)) break;
+                        const float2 m = reinterpret_cast<const float2 *>(p.max_q)[(size_t)head * p.nq + y];
+                        a = fmaxf(a, m.x);
+                        d = fmaxf(d, m.y);
+                    }
+                    v = p.max_v[(size_t)w.zx * p.nk + w.x0 / kRows];
+                } else {
+                    for (int i = lane; i < p.nk; i += 32) v = fmaxf(v, p.max_v[(size_t)w.zy * p.nk + i]);
+                }
+                for (int m = 16; m > 0; m >>= 1) {
+                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
+                    d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, m));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+                }
+                if (lane == 0) {
+                    *(volatile float *)&bars->norm[s] = w.kind == 0 ? fmaf(a, v, d) : v;
+                    ptx::mbar_arrive(bar(bars->norm_full[s]));
+                }
+            }
+        }
     }
 
     // ---------------------------------------------------------------- teardown
@@ -814,7 +849,8 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
     uint8_t *ws = (uint8_t *)a.workspace;
     Params p{};
     p.stats = (const float *)(ws + plan.off_stats);
-    p.maxima = (const float *)(ws + plan.off_max);
+    p.max_q = (const float *)(ws + plan.off_max);
+    p.max_v = (const float *)(ws + plan.off_max_v);
     p.counter = (unsigned *)ws;
     p.BH = (int)pr.bh();
     p.BHk = (int)pr.bh_kv();
