@@ -17,6 +17,7 @@ import math
 import os
 import struct
 import threading
+import warnings
 
 __all__ = [
     "ATTN_OK", "ATTN_ERR_INVALID_ARG", "ATTN_ERR_UNSUPPORTED_DEVICE", "ATTN_ERR_LAUNCH",
@@ -831,16 +832,31 @@ _torch = _int32 = _float32 = _contiguous = _raw_stream = _current_device = _capt
 _codes = {}  # (input dtype, output dtype) -> attn_dtype
 
 
+class _NoCalls:
+    """In place of _torch_calls where it was not built (build.py): the wrappers' Python code does it all."""
+
+    @staticmethod
+    def rotary(*args):
+        return None
+
+    attention_bwd = rotary
+
+
 def _fast():
     """The wrappers' host side in C++, for calls with nothing out of the ordinary: each of its
     functions answers None to any other, for the Python code behind it to do or to refuse."""
     global _calls
     if _calls is None:
         import torch
+        if not os.path.exists(os.path.join(_HERE, "_torch_calls.so")):
+            warnings.warn("_torch_calls.so was not built: small calls take about 10 us longer on the host",
+                          RuntimeWarning)
+            _calls = _NoCalls
+            return _calls
         try:
             from . import _torch_calls
         except ImportError as e:
-            raise RuntimeError("_torch_calls.so is missing or of another PyTorch: run %s/build.py (%s)" % (_HERE, e))
+            raise RuntimeError("_torch_calls.so is of another PyTorch: run %s/build.py (%s)" % (_HERE, e))
         if torch.__version__.split("+")[0] != _torch_calls.torch_version:
             raise RuntimeError("_torch_calls.so was built for PyTorch %s, this is %s: run %s/build.py"
                                % (_torch_calls.torch_version, torch.__version__, _HERE))

@@ -14,7 +14,7 @@ shared libraries are linked next to this file:
   test through the status word instead of touching memory out of bounds;
 * _torch_calls.so -- the host side of the Python wrappers whose calls are
   short, against PyTorch's headers (csrc/torch_calls.cpp, by the host
-  compiler).
+  compiler).  Left out where either is missing: the wrappers then do without.
 
 The CUDA runtime is linked statically (nvcc's default), so the libraries
 need only the driver at run time; the tensor-map encoder is fetched from the
@@ -88,8 +88,17 @@ def _torch_dir() -> str:
     return list(spec.submodule_search_locations)[0]
 
 
-def _cxx() -> str:
-    return os.environ.get("CXX") or shutil.which("g++") or "c++"
+def _torch_version():
+    """Version of the PyTorch that is installed, or None."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _cxx():
+    """The C++ compiler, or None."""
+    return os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
 
 
 def _calls_compile(src: str, obj: str):
@@ -132,20 +141,30 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(o, s):
             jobs.append([nvcc()] + _flags(list(extra_flags) + fl) + ["-c", s, "-o", o])
     # one object for each version of PyTorch, whose headers it is made of
+    version = _torch_version()
     calls_src = os.path.join(CSRC, "torch_calls.cpp")
-    calls_obj = os.path.join(BUILD, "torch_calls-%s.o" % importlib.metadata.version("torch"))
-    calls = force or _stale(calls_obj, calls_src)
-    if calls:
-        jobs.append(_calls_compile(calls_src, calls_obj))
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
-        for cmd, r in zip(jobs, results):
-            if verbose or r.returncode != 0:
-                print(" ".join(cmd))
-                print(r.stdout + r.stderr)
-            if r.returncode != 0:
-                raise RuntimeError("compiling %s failed" % cmd[-3])
+    calls_obj = os.path.join(BUILD, "torch_calls-%s.o" % version)
+    calls_job = None
+    if version is None or _cxx() is None:
+        print("%s is left out: %s not found" % (os.path.basename(CALLS_LIB),
+                                                "PyTorch" if version is None else "a C++ compiler"))
+    elif force or _stale(calls_obj, calls_src):
+        calls_job = _calls_compile(calls_src, calls_obj)
+    todo = jobs + ([calls_job] if calls_job else [])
+    done = []
+    if todo:
+        with cf.ThreadPoolExecutor(max_workers=len(todo)) as ex:
+            done = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), todo))
+
+    def check(cmd, r):
+        if verbose or r.returncode != 0:
+            print(" ".join(cmd))
+            print(r.stdout + r.stderr)
+        if r.returncode != 0:
+            raise RuntimeError("compiling %s failed" % cmd[-3])
+
+    for cmd, r in zip(jobs, done):
+        check(cmd, r)
     product = [objs[src.replace(".cu", ".o")] for src in SOURCES]
     test_set = product[:]
     for src, oname, _ in TEST_SOURCES:  # the test build replaces the product object
@@ -156,7 +175,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         _link(TEST_LIB, test_set)
     if jobs or not os.path.exists(CHECKED_LIB) or force:
         _link(CHECKED_LIB, [objs[t[1]] for t in CHECKED_SOURCES])
-    if calls or not os.path.exists(CALLS_LIB) or os.path.getmtime(CALLS_LIB) < os.path.getmtime(calls_obj):
+    if calls_job:
+        check(calls_job, done[-1])
+    if version is not None and _cxx() is not None and \
+            (calls_job or not os.path.exists(CALLS_LIB) or os.path.getmtime(CALLS_LIB) < os.path.getmtime(calls_obj)):
         _link(CALLS_LIB, [calls_obj])
     return LIB
 
