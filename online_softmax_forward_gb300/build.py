@@ -177,9 +177,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         _link(CHECKED_LIB, [objs[t[1]] for t in CHECKED_SOURCES])
     if calls_job:
         check(calls_job, done[-1])
-    if version is not None and _cxx() is not None and \
-            (calls_job or not os.path.exists(CALLS_LIB) or os.path.getmtime(CALLS_LIB) < os.path.getmtime(calls_obj)):
-        _link(CALLS_LIB, [calls_obj])
+    if version is not None and _cxx() is not None:
+        stamp = os.path.join(BUILD, "torch_calls.version")  # of the PyTorch the library was linked for
+        linked = open(stamp).read() if os.path.exists(stamp) else None
+        if (calls_job or linked != version or not os.path.exists(CALLS_LIB)
+                or os.path.getmtime(CALLS_LIB) < os.path.getmtime(calls_obj)):
+            _link(CALLS_LIB, [calls_obj])
+            with open(stamp, "w") as f:
+                f.write(version)
     return LIB
 
 

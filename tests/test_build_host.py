@@ -55,3 +55,22 @@ def test_wrappers_do_without_the_host_side(monkeypatch, tmp_path):
     assert calls.rotary(q, None, pos, False) is None and calls.attention_bwd(q, q, q, q, q, q, None, False, 0.0) is None
     with pytest.raises(ValueError, match="CUDA"):
         pkg.attention_bwd(q, q, q, q, torch.zeros(1, 2, 3), q)
+
+
+def test_the_host_side_follows_the_version_of_torch(elsewhere, monkeypatch):
+    """Built for one PyTorch, then for another, then for the first again: each time that one's object."""
+    links = []
+    monkeypatch.setattr(lib_build, "_link", lambda lib, objs: (links.append(list(objs)), open(lib, "w").close()))
+    objects = {v: os.path.join(lib_build.BUILD, "torch_calls-%s.o" % v) for v in ("0.0.1", "0.0.2")}
+    monkeypatch.setattr(lib_build, "_stale", lambda obj, src: src.endswith(".cpp") and not os.path.exists(obj))
+    monkeypatch.setattr(lib_build, "_calls_compile", lambda src, obj: ["cp", src, obj])
+    try:
+        for v in ("0.0.1", "0.0.2", "0.0.1", "0.0.1"):
+            monkeypatch.setattr(lib_build, "_torch_version", lambda v=v: v)
+            lib_build.build()
+        calls = [objs[0] for objs in links if "torch_calls" in objs[0]]
+        assert calls == [objects["0.0.1"], objects["0.0.2"], objects["0.0.1"]]
+    finally:
+        for path in objects.values():
+            if os.path.exists(path):
+                os.remove(path)
