@@ -860,6 +860,9 @@ def _fast():
         if torch.__version__.split("+")[0] != _torch_calls.torch_version:
             raise RuntimeError("_torch_calls.so was built for PyTorch %s, this is %s: run %s/build.py"
                                % (_torch_calls.torch_version, torch.__version__, _HERE))
+        lib = load_library()
+        _torch_calls.bind(*(ctypes.cast(getattr(lib, name), _P).value
+                            for name in ("attn_rotary", "attn_bwd_workspace_size", "attn_bwd")))
         _calls = _torch_calls
     return _calls
 

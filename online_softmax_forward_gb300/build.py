@@ -111,8 +111,8 @@ def _calls_compile(src: str, obj: str):
 
 
 def _calls_link(lib: str, obj: str):
-    return [_cxx(), "-shared", "-o", lib, obj, "-L", HERE, "-l:libattn.so", "-Wl,-rpath,$ORIGIN",
-            "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    # without libattn.so: it is handed the addresses of the one that is loaded
+    return [_cxx(), "-shared", "-o", lib, obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def _link(lib: str, objs) -> None:

@@ -8,6 +8,8 @@
 // error, a tensor on a device that is not the current one, a subclass of Tensor) is
 // answered with None, and the wrapper goes its own way, which says what is wrong.
 //
+// bind(address of attn_rotary, of attn_bwd_workspace_size, of attn_bwd): first, once; the
+//     functions of the libattn.so that the process uses
 // rotary(q, k, pos, transpose, turns, width, interleaved, amplitude, device index of turns)
 //     -> (q', k')
 // attention_bwd(q, k, v, o, lse, do, dlse, causal, scale) -> (dq, dk, dv)
@@ -27,6 +29,11 @@
 #include "attn.h"
 
 namespace {
+
+// what `bind` was given
+decltype(&attn_rotary) call_rotary;
+decltype(&attn_bwd_workspace_size) call_bwd_workspace_size;
+decltype(&attn_bwd) call_bwd;
 
 struct WithoutGil {  // allocations and launches may wait; other threads run meanwhile
     PyThreadState *state = PyEval_SaveThread();
@@ -67,9 +74,23 @@ attn_heads heads(const at::Tensor &in, const at::Tensor &out) {
     return h;
 }
 
+PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 3) {
+        PyErr_SetString(PyExc_TypeError, "three addresses expected");
+        return nullptr;
+    }
+    void *at[3];
+    for (int i = 0; i < 3; ++i) at[i] = PyLong_AsVoidPtr(args[i]);
+    if (PyErr_Occurred()) return nullptr;
+    call_rotary = (decltype(call_rotary))at[0];
+    call_bwd_workspace_size = (decltype(call_bwd_workspace_size))at[1];
+    call_bwd = (decltype(call_bwd))at[2];
+    Py_RETURN_NONE;
+}
+
 PyObject *rotary(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 9) Py_RETURN_NONE;
+    if (n != 9 || !call_rotary) Py_RETURN_NONE;
     const at::Tensor *q = tensor(args[0]), *k = args[1] == Py_None ? nullptr : tensor(args[1]), *pos = tensor(args[2]);
     if (!q || !pos || (!k && args[1] != Py_None) || q->dim() != 4 || !q->is_cuda()) Py_RETURN_NONE;
     const c10::Device dev = q->device();
@@ -97,7 +118,7 @@ PyObject *rotary(PyObject *, PyObject *const *args, Py_ssize_t n) {
         qo = at::empty(q->sizes(), q->options());
         if (k) ko = at::empty(k->sizes(), k->options());
         const attn_heads hq = heads(*q, qo), hk = k ? heads(*k, ko) : attn_heads{};
-        st = attn_rotary(&hq, k ? &hk : nullptr, turns, (int)width, (int)interleaved, (float)amplitude, transpose,
+        st = call_rotary(&hq, k ? &hk : nullptr, turns, (int)width, (int)interleaved, (float)amplitude, transpose,
                          (const int32_t *)pos->data_ptr(), per_token, (int)B, (int)S, (int)d, code, stream_of(dev));
     }
     if (st != ATTN_OK) return PyLong_FromLong(st);
@@ -108,7 +129,7 @@ PyObject *rotary(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 PyObject *attention_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 9) Py_RETURN_NONE;
+    if (n != 9 || !call_bwd || !call_bwd_workspace_size) Py_RETURN_NONE;
     const at::Tensor *t[7];  // q, k, v, o, lse, do, dlse
     for (int i = 0; i < 7; ++i) {
         t[i] = args[i] == Py_None && i == 6 ? nullptr : tensor(args[i]);
@@ -136,7 +157,7 @@ PyObject *attention_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     {
         WithoutGil free;
         size_t need = 0;
-        st = attn_bwd_workspace_size((int)B, (int)H, (int)H_kv, (int)Sq, (int)Skv, (int)d, causal, code, &need);
+        st = call_bwd_workspace_size((int)B, (int)H, (int)H_kv, (int)Sq, (int)Skv, (int)d, causal, code, &need);
         if (st == ATTN_OK) {
             const auto like = q.options().dtype(out);
             dq = at::empty(q.sizes(), like);
@@ -145,7 +166,7 @@ PyObject *attention_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
             // returned to the allocator behind the launch, for later work on this stream
             at::Tensor work;
             if (need) work = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
-            st = attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), (const float *)lse.data_ptr(),
+            st = call_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), (const float *)lse.data_ptr(),
                           dout.data_ptr(), t[6] ? (const float *)t[6]->data_ptr() : nullptr, dq.data_ptr(),
                           dk.data_ptr(), dv.data_ptr(), (int)B, (int)H, (int)H_kv, (int)Sq, (int)Skv, (int)d, causal,
                           (float)scale, code, need ? work.data_ptr() : nullptr, need, stream_of(dev));
@@ -157,7 +178,8 @@ PyObject *attention_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-PyMethodDef methods[] = {{"rotary", (PyCFunction)(void (*)())rotary, METH_FASTCALL, nullptr},
+PyMethodDef methods[] = {{"bind", (PyCFunction)(void (*)())bind, METH_FASTCALL, nullptr},
+                         {"rotary", (PyCFunction)(void (*)())rotary, METH_FASTCALL, nullptr},
                          {"attention_bwd", (PyCFunction)(void (*)())attention_bwd, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -203,3 +203,24 @@ def test_calls_on_host_tensors_are_left_to_the_wrapper():
         pkg.rotary(q, k, rot, pos)
     with pytest.raises(ValueError):
         pkg.attention_bwd(q, k, k, q, lse, q)
+
+
+def test_one_library_serves_every_call(tmp_path):
+    """ATTN_GB300_LIB names the library of all functions, those that the wrappers' host side calls among
+    them: a second one in the process would have a status word of its own, which nobody reads."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    named = str(tmp_path / "libnamed.so")
+    shutil.copy(os.path.join(os.path.dirname(pkg.__file__), "libattn.so"), named)
+    code = ("import torch, online_softmax_forward_gb300 as pkg\n"
+            "assert pkg.attn_abi_version() == pkg.load_library().attn_abi_version()\n"
+            "q = torch.zeros(1, 2, 3, 64)\n"
+            "assert pkg._fast().rotary(q, None, torch.zeros(1, 3).int(), False, 0, 64, 0, 1.0, -1) is None\n"
+            "print(*sorted({l.split()[-1] for l in open('/proc/self/maps') if 'libattn' in l or 'libnamed' in l}))\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       env={**os.environ, "ATTN_GB300_LIB": named},
+                       cwd=os.path.dirname(os.path.dirname(pkg.__file__)))
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == [named]
