@@ -431,7 +431,7 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out_dty
 
     ``out_dtype`` = torch.float32 with bf16/fp16 inputs selects the fp32-output
     variant.  Outputs are allocated with torch unless ``out`` / ``lse`` are
-    given."""
+    given; those of a call that names a ``stream`` belong to that stream."""
     if _torch is None:
         import torch
         _bind(torch)
@@ -446,13 +446,13 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out_dty
     if out is not None:
         _check_out(out, (B, H, Sq, d), odt, dev, "out")
     elif odt is dtype:
-        out = _new_like(None, q)
+        out = _new_like(stream, q)
     else:
-        out = _new(None, (B, H, Sq, d), odt, dev)
+        out = _new(stream, (B, H, Sq, d), odt, dev)
     if lse is not None:
         _check_out(lse, (B, H, Sq), _torch.float32, dev, "lse")
     elif return_lse:
-        lse = _new(None, (B, H, Sq), _torch.float32, dev)
+        lse = _new(stream, (B, H, Sq), _torch.float32, dev)
     sc = 0.0 if scale is None else float(scale)
     lp = None if lse is None else lse.data_ptr()
     if H_kv == H:
@@ -528,9 +528,11 @@ def attention_f32_blocked(q, k, v, block_q: int, block_kv: int, causal: bool = F
     """fp32 path with explicit tile sizes (block-size invariance tests;
     runs in the test library, include/attn_test.h)."""
     import torch
+    if _torch is None:
+        _bind(torch)
     B, H, Sq, Skv, d = _shapes(q, k, v)
-    out = torch.empty((B, H, Sq, d), dtype=torch.float32, device=q.device)
-    lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+    out = _new(stream, (B, H, Sq, d), torch.float32, q.device)
+    lse = _new(stream, (B, H, Sq), torch.float32, q.device)
     sc = 0.0 if scale is None else float(scale)
     with torch.cuda.device(q.device):
         st = attn_fwd_f32_blocked(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -551,6 +553,8 @@ def attention_splitkv(q, k, v, causal: bool = False, scale: float | None = None,
     a torch uint8 CUDA tensor, allocated here unless given; ``n_splits`` is
     the library's choice unless given.  Returns (o, lse)."""
     import torch
+    if _torch is None:
+        _bind(torch)
     B, H, Sq, Skv, d = _shapes(q, k, v)
     code = dtype_code(q.dtype, out_dtype)
     if k.dtype != q.dtype or v.dtype != q.dtype:
@@ -562,13 +566,13 @@ def attention_splitkv(q, k, v, causal: bool = False, scale: float | None = None,
     st, need = attn_splitkv_workspace_size(B, H, Sq, d, n_splits)
     _check(st, "attn_splitkv_workspace_size")
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, max(need, 16), torch.uint8, q.device)
     if not workspace.is_contiguous() or _device_of(workspace) != q.device:
         raise ValueError("workspace must be a contiguous tensor on %s" % q.device)
     odt = {ATTN_F32: torch.float32, ATTN_BF16: torch.bfloat16, ATTN_F16: torch.float16,
            ATTN_BF16_OUT_F32: torch.float32, ATTN_F16_OUT_F32: torch.float32}[code]
-    out = torch.empty((B, H, Sq, d), dtype=odt, device=q.device)
-    lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+    out = _new(stream, (B, H, Sq, d), odt, q.device)
+    lse = _new(stream, (B, H, Sq), torch.float32, q.device)
     sc = 0.0 if scale is None else float(scale)
     with torch.cuda.device(q.device):
         st = attn_fwd_splitkv(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -583,18 +587,21 @@ def merge(o_parts, lse_parts, out_dtype=None, stream=None):
     """attn_merge on torch tensors: o_parts [n, rows, d] fp32, lse_parts
     [n, rows] fp32 -> (o [rows, d], lse [rows])."""
     import torch
+    if _torch is None:
+        _bind(torch)
     if o_parts.dim() != 3 or lse_parts.shape != o_parts.shape[:2]:
         raise ValueError("o_parts [n, rows, d] and lse_parts [n, rows] expected")
     if o_parts.dtype != torch.float32 or lse_parts.dtype != torch.float32:
         raise ValueError("partial results are fp32")
-    o_parts, lse_parts = o_parts.contiguous(), lse_parts.contiguous()
-    _device_of(o_parts, lse_parts)
+    dev = _device_of(o_parts, lse_parts)
+    with _on(stream, dev):
+        o_parts, lse_parts = o_parts.contiguous(), lse_parts.contiguous()
     n, rows, d = o_parts.shape
     odt = torch.float32 if out_dtype is None else out_dtype
     code = {torch.float32: ATTN_F32, torch.bfloat16: ATTN_BF16, torch.float16: ATTN_F16}[odt]
-    out = torch.empty((rows, d), dtype=odt, device=o_parts.device)
-    lse = torch.empty((rows,), dtype=torch.float32, device=o_parts.device)
-    with torch.cuda.device(o_parts.device):
+    out = _new(stream, (rows, d), odt, dev)
+    lse = _new(stream, (rows,), torch.float32, dev)
+    with torch.cuda.device(dev):
         st = attn_merge(o_parts.data_ptr(), lse_parts.data_ptr(), n, rows, d, out.data_ptr(),
                         lse.data_ptr(), code, _stream_handle(stream))
     _check(st, "attn_merge")
@@ -894,9 +901,16 @@ def _handle(device, stream):
     making a Stream object, which takes longer than a launch."""
     if stream is None:
         return _raw_stream(device.index)
-    if stream.device != device:
+    if getattr(stream, "device", device) != device:
         raise ValueError("the tensors are on %s, the stream on %s" % (device, stream.device))
     return stream.cuda_stream
+
+
+def _on(stream, device):
+    """The context in which torch's work and allocations are ``stream``'s, if one is given."""
+    if stream is not None and not isinstance(stream, _torch.cuda.Stream):
+        stream = _torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return _torch.cuda.stream(stream)
 
 
 def _new(stream, shape, dtype, device):
@@ -904,7 +918,7 @@ def _new(stream, shape, dtype, device):
     current stream's work still uses is then not handed to another stream's."""
     if stream is None:
         return _torch.empty(shape, dtype=dtype, device=device)
-    with _torch.cuda.stream(stream):
+    with _on(stream, device):
         return _torch.empty(shape, dtype=dtype, device=device)
 
 
