@@ -876,13 +876,14 @@ def _fast():
 
 def _bind(torch):
     global _torch, _int32, _float32, _contiguous, _raw_stream, _current_device, _capturing
-    _torch, _int32, _float32, _contiguous = torch, torch.int32, torch.float32, torch.contiguous_format
+    _int32, _float32, _contiguous = torch.int32, torch.float32, torch.contiguous_format
     for t in (torch.float32, torch.bfloat16, torch.float16):
         for u in {t, torch.float32}:
             _codes[t, u] = dtype_code(t, u)
     _raw_stream = torch._C._cuda_getCurrentRawStream
     _current_device = torch._C._cuda_getDevice
     _capturing = torch._C._cuda_isCurrentStreamCapturing
+    _torch = torch  # last: the other names are there for a thread that sees this one
 
 
 def _call_on(device, fn, *args):

@@ -224,3 +224,29 @@ def test_one_library_serves_every_call(tmp_path):
                        cwd=os.path.dirname(os.path.dirname(pkg.__file__)))
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == [named]
+
+
+def test_binding_torch_is_seen_whole(monkeypatch):
+    """A thread that finds torch bound finds all of it: the name that callers look at comes last."""
+    import threading
+    names = ("_torch", "_int32", "_float32", "_contiguous", "_raw_stream", "_current_device", "_capturing")
+    for name in names:
+        monkeypatch.setattr(pkg, name, None)
+    monkeypatch.setattr(pkg, "_codes", {})
+    inside, go = threading.Event(), threading.Event()
+    code = pkg.dtype_code
+
+    def slow(*a):
+        inside.set()
+        assert go.wait(10)
+        return code(*a)
+
+    monkeypatch.setattr(pkg, "dtype_code", slow)
+    binding = threading.Thread(target=pkg._bind, args=(torch,))
+    binding.start()
+    assert inside.wait(10)
+    early = pkg._torch  # what another thread's call looks at meanwhile
+    go.set()
+    binding.join()
+    assert early is None
+    assert all(getattr(pkg, name) is not None for name in names) and len(pkg._codes) == 5
