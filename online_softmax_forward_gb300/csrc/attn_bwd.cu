@@ -15,7 +15,7 @@ bool bwd_plan(const Problem &call, BwdPlan *plan) {
     Problem p = call;
     plan->off = call.Skv - call.Sq;
     plan->wrap = 0;
-    if (p.group > 1 && (!p.causal || p.Sq <= kStatTile) && (int64_t)p.group * p.Sq <= INT32_MAX - kStatTile) {
+    if (p.group > 1 && (!p.causal || (p.Sq <= kStatTile && plan->off >= 0)) && (int64_t)p.group * p.Sq <= INT32_MAX - kStatTile) {
         p.H /= p.group;
         p.Sq *= p.group;
         p.group = 1;
@@ -190,8 +190,9 @@ __global__ void __launch_bounds__(kPreThreads) bwd_stats_kernel(const PreParams 
             if (sub != 0) continue;
             float norm = 0.f;
             if (row < p.Sq) {
+                // a row that sees no key has P = 0, and no D that P would be multiplied with
                 nl = l[u] == -INFINITY ? -INFINITY : fmaf(l[u], -1.4426950408889634f, p.add);
-                nd = dl[u] - dot;
+                nd = l[u] == -INFINITY ? 0.f : dl[u] - dot;
                 if (kScale && l[u] != -INFINITY) {
                     norm = sqrtf(sq);
                     if (norm < INFINITY && fabsf(nd) < INFINITY) {  // false for NaN, too

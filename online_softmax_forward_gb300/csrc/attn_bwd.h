@@ -79,9 +79,9 @@ struct BwdArgs {
 // The query heads that share a kv head lie one behind the other, so that their
 // rows can be walked as the rows of one head (plan.p: H_kv heads of group * Sq
 // rows), with fewer tiles left partly empty.  Without a causal mask this is
-// always done; with one for up to a tile of queries, where a row's position is
-// its number modulo Sq (longer ones would lose the key tiles that the mask
-// leaves out).
+// always done; with one for up to a tile of queries and no more than there are keys,
+// where a row's position is its number modulo Sq (longer ones would lose the key
+// tiles that the mask leaves out; rows that see no key are the first of a head).
 bool bwd_plan(const Problem &p, BwdPlan *plan);
 
 // The kernels in order: row statistics (16-bit types), gradients, sum of the splits.

@@ -151,6 +151,7 @@ struct Params {
     void *dk, *dv, *dq;               // gradients, or the splits' partial sums
     int BH, BHk, group, Sq, Skv, causal;
     int off, wrap, few;  // of BwdPlan
+    int blind;           // first query rows of a head that see no key: behind tm_q's and tm_do's start
     int nq, nk, ns_kv, ns_q, q_first;
     int hg;       // kv slices per schedule group
     int n_units;
@@ -389,19 +390,19 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 *watch.abort_flag = 1;
                 return false;
             };
-            auto tile = [&](uint32_t dst, uint64_t &full, const CUtensorMap *tm, int row, int z, int rows, int slices) {
-                if (!in_bounds(row >= 0 && row < rows && z >= 0 && z < slices, p.status)) return stop();
+            // rows from `row` on of slice z of q or do, or of k or v
+            auto tile = [&](uint32_t dst, uint64_t &full, const CUtensorMap *tm, int row, int z, bool of_q) {
+                if (!in_bounds(row >= 0 && row < (of_q ? p.Sq : p.Skv) && z >= 0 && z < (of_q ? p.BH : p.BHk), p.status))
+                    return stop();
                 ptx::mbar_arrive_expect_tx(bar(full), C::kTileBytes);
                 for (int c = 0; c < C::kChunks; ++c)
-                    ptx::tma_load_3d(dst + c * C::kChunkBytes, tm, bar(full), c * 64, row, z);
+                    ptx::tma_load_3d(dst + c * C::kChunkBytes, tm, bar(full), c * 64, of_q ? row - p.blind : row, z);
                 return true;
             };
             auto load_x = [&](int t, const Unit &w) {
                 if (!watch.wait(bar(bars->x_empty[t]), (xn[t] & 1) ^ 1)) return false;
                 const CUtensorMap *tm = w.kind == 0 ? (t ? &tm_v : &tm_k) : (t ? &tm_do : &tm_q);
-                if (!tile(sX + t * C::kTileBytes, bars->x_full[t], tm, w.x0, w.zx,
-                          w.kind == 0 ? p.Skv : p.Sq, w.kind == 0 ? p.BHk : p.BH))
-                    return false;
+                if (!tile(sX + t * C::kTileBytes, bars->x_full[t], tm, w.x0, w.zx, w.kind != 0)) return false;
                 ++xn[t];
                 return true;
             };
@@ -409,9 +410,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const uint32_t s = C::slot(t, yn[t]);
                 if (!watch.wait(bar(bars->y_empty[s]), (C::round(t, yn[t]) & 1) ^ 1)) return false;
                 const CUtensorMap *tm = w.kind == 0 ? (t ? &tm_do : &tm_q) : (t ? &tm_v : &tm_k);
-                if (!tile(sY + s * C::kTileBytes, bars->y_full[s], tm, y * kRows, zy,
-                          w.kind == 0 ? p.Sq : p.Skv, w.kind == 0 ? p.BH : p.BHk))
-                    return false;
+                if (!tile(sY + s * C::kTileBytes, bars->y_full[s], tm, y * kRows, zy, w.kind == 0)) return false;
                 ++yn[t];
                 return true;
             };
@@ -842,9 +841,16 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 template <int D, bool kBF16, int kTwo>
 int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaStream_t stream) {
     using C = Cfg<D>;
+    // Rows that see no key have P = 0, which makes no 0 of an infinity that their do leaves in
+    // dP: the maps of q and do start behind them, so that they read as zeros.  (Clearing dP
+    // where it is read cost 4 % of every call.)
+    const int blind = pr.causal && plan.off < 0 ? -plan.off : 0;
+    const size_t skip = (size_t)blind * D * 2;
     CUtensorMap tq, tk, tv, td;
-    if (!make_tile_map(&tq, a.q, kBF16, D, pr.Sq, pr.bh()) || !make_tile_map(&tk, a.k, kBF16, D, pr.Skv, pr.bh_kv()) ||
-        !make_tile_map(&tv, a.v, kBF16, D, pr.Skv, pr.bh_kv()) || !make_tile_map(&td, a.dout, kBF16, D, pr.Sq, pr.bh()))
+    if (!make_tile_map(&tq, (const uint8_t *)a.q + skip, kBF16, D, pr.Sq, pr.Sq - blind, pr.bh()) ||
+        !make_tile_map(&tk, a.k, kBF16, D, pr.Skv, pr.Skv, pr.bh_kv()) ||
+        !make_tile_map(&tv, a.v, kBF16, D, pr.Skv, pr.Skv, pr.bh_kv()) ||
+        !make_tile_map(&td, (const uint8_t *)a.dout + skip, kBF16, D, pr.Sq, pr.Sq - blind, pr.bh()))
         return ATTN_ERR_CUDA;
     uint8_t *ws = (uint8_t *)a.workspace;
     Params p{};
@@ -861,6 +867,7 @@ int launch_typed(const BwdArgs &a, const Problem &pr, const BwdPlan &plan, cudaS
     p.off = plan.off;
     p.wrap = plan.wrap;
     p.few = plan.few;
+    p.blind = blind;
     p.nq = plan.nq;
     p.nk = plan.nk;
     p.ns_kv = plan.ns_kv;

@@ -92,10 +92,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 }  // namespace
 
-bool make_tile_map(CUtensorMap *m, const void *base, bool bf16, int d, int S, int64_t slices) {
+bool make_tile_map(CUtensorMap *m, const void *base, bool bf16, int d, int S, int rows, int64_t slices) {
     auto enc = encode_fn();
     if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)S, (cuuint64_t)slices};
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)slices};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)S * d * 2};
     cuuint32_t box[3] = {64, 128, 1};
     cuuint32_t estr[3] = {1, 1, 1};
@@ -910,8 +910,9 @@ int launch_typed(const void *q, const void *k, const void *v, void *o, float *ls
     using C = Cfg<D>;
     CUtensorMap tq, tk, tv;
     const int64_t BH = pr.bh();
-    if (!make_tile_map(&tq, q, kBF16, D, pr.Sq, BH) || !make_tile_map(&tk, k, kBF16, D, pr.Skv, pr.bh_kv()) ||
-        !make_tile_map(&tv, v, kBF16, D, pr.Skv, pr.bh_kv()))
+    if (!make_tile_map(&tq, q, kBF16, D, pr.Sq, pr.Sq, BH) ||
+        !make_tile_map(&tk, k, kBF16, D, pr.Skv, pr.Skv, pr.bh_kv()) ||
+        !make_tile_map(&tv, v, kBF16, D, pr.Skv, pr.Skv, pr.bh_kv()))
         return ATTN_ERR_CUDA;
     int *status = status_word_device_ptr();
     unsigned int *sched = next_sched_pair();

@@ -6,8 +6,9 @@
 
 namespace attn {
 
-// [slices, S, d] 16-bit tensor as a 3-D TMA map, box 64 (d) x 128 (rows) x 1,
-// 128-byte swizzle; rows past S read as zeros.  False if the driver refuses it.
-bool make_tile_map(CUtensorMap *m, const void *base, bool bf16, int d, int S, int64_t slices);
+// The first `rows` rows of each slice of a [slices, S, d] 16-bit tensor as a 3-D TMA map, box
+// 64 (d) x 128 (rows) x 1, 128-byte swizzle; rows outside read as zeros.  False if the driver
+// refuses it.
+bool make_tile_map(CUtensorMap *m, const void *base, bool bf16, int d, int S, int rows, int64_t slices);
 
 }  // namespace attn
