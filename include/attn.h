@@ -166,7 +166,9 @@ ATTN_API int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, 
  * the norms of what makes it, so that heads and sequences of very different do
  * share a call without loss; in a row of dk, terms whose P |do| is less than
  * 2^-27 of the largest |do| of the same kv head lose bits.  fp32: each product
- * of two numbers is wrong by 2^-21 of itself at most.  Sums are made in a fixed
+ * of two numbers is wrong by 2^-21 of itself at most; numbers from 2^128 - 2^116 on
+ * count as infinite, and what numbers below 2^-112 hold beyond their first 11 bits
+ * may be lost.  Sums are made in a fixed
  * order: equal calls give equal bits.
  * All arrays must be distinct; q, k, v, o, do and gradients 16-byte aligned.
  * Sq and Skv <= 2^31 - 1024.  CUDA graphs: as attn_fwd, without its limit on

@@ -13,9 +13,11 @@
 //    (4 x 4 results a thread: 22 TFLOP/s of 74), so the products run on the tensor
 //    cores, each fp32 number as the sum of two tf32 ones, hi (rounded to 11
 //    bits) and lo = x - hi: x y = hi hi + hi lo + lo hi, wrong by 2^-21 of |x y| at
-//    most, over fp32's whole range.  mma.sync: its fragments come from plain
-//    fp32 tiles of any width and stay in registers; tcgen05 would want both
-//    parts of every tile in shared memory, which two tiles of 64 rows fill.
+//    most for numbers of 2^-112 to 2^128 - 2^116.  (Larger ones round to an infinity, and
+//    of smaller ones lo is no normal number and counts as 0.  Bounding hi by the largest
+//    tf32 number, one more instruction a split, cost 5 to 10 %.)  mma.sync: its
+//    fragments come from plain fp32 tiles of any width and stay in registers; tcgen05
+//    would want both parts of every tile in shared memory, which two tiles of 64 rows fill.
 //  * P and dS never leave registers: the accumulator of T holds columns 2 t, 2 t +
 //    1 where the left operand of A wants k = t, t + 4, which is only another
 //    order of the summed rows, so Y's rows are read in that order.
@@ -104,15 +106,15 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// N rows of a [rows, D] slice from row r0 on, asynchronously; rows behind the last one
-// are zero.
+// N rows of a [rows, D] slice from row r0 on, asynchronously; rows before `from_row` and
+// behind the last one are zero.
 template <int D, int N>
-__device__ __forceinline__ void load_tile(float *dst, const float *src, int r0, int rows, int *status) {
+__device__ __forceinline__ void load_tile(float *dst, const float *src, int r0, int from_row, int rows, int *status) {
     constexpr int V = D / 4;
 #pragma unroll
     for (int t = threadIdx.x; t < N * V; t += kThreads) {
         const int r = t / V, c = (t % V) * 4;
-        const bool live = r0 + r < rows && in_bounds(r0 + r >= 0 && c + 4 <= D, status);
+        const bool live = r0 + r >= from_row && r0 + r < rows && in_bounds(r0 + r >= 0 && c + 4 <= D, status);
         const float *from = live ? src + (size_t)(r0 + r) * D + c : src;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(dst + r * (D + 4) + c)),
                      "l"(from), "r"(live ? 16 : 0)
@@ -316,6 +318,8 @@ attn_bwd_f32_kernel(const Params p) {
     int y = first + t0 - skip * per;
     int zy = kv ? zx * p.group + skip : zx / p.group;
     const int xrows = kv ? p.Skv : p.Sq, yrows = kv ? p.Sq : p.Skv;
+    // query rows that see no key read as zeros: their P is 0, which would not make 0 of an infinity
+    const int blind = p.causal && p.off < 0 ? -p.off : 0, x_from = kv ? 0 : blind, y_from = kv ? blind : 0;
     if (!in_bounds(zx < slices && x0 < xrows, p.status)) return;
 
     float a1[D / 8][4], a2[D / 8][4];
@@ -330,16 +334,16 @@ attn_bwd_f32_kernel(const Params p) {
         const size_t s = (size_t)zy * yrows * D;
         float *Y = Ys + st * C::kStage;
         if (in_bounds(zy < (kv ? p.BH : p.BHk) && y0 < yrows, p.status)) {
-            load_tile<D, kT>(Y, (kv ? p.q : p.k) + s, y0, yrows, p.status);
-            load_tile<D, kT>(Y + kT * LD, (kv ? p.dout : p.v) + s, y0, yrows, p.status);
+            load_tile<D, kT>(Y, (kv ? p.q : p.k) + s, y0, y_from, yrows, p.status);
+            load_tile<D, kT>(Y + kT * LD, (kv ? p.dout : p.v) + s, y0, y_from, yrows, p.status);
             if (kv) rows.load(p, zy, y0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (n > 0) {
         const size_t s = (size_t)zx * xrows * D;
-        load_tile<D, X>(X1, (kv ? p.k : p.q) + s, x0, xrows, p.status);
-        load_tile<D, X>(X2, (kv ? p.v : p.dout) + s, x0, xrows, p.status);
+        load_tile<D, X>(X1, (kv ? p.k : p.q) + s, x0, x_from, xrows, p.status);
+        load_tile<D, X>(X2, (kv ? p.v : p.dout) + s, x0, x_from, xrows, p.status);
         load_y(0, zy, y * kT);
         if (!kv) {
             StatRows<D, X> mine;
