@@ -197,15 +197,16 @@ ATTN_API int attn_bwd(const void *q, const void *k, const void *v, const void *o
  *          ATTN_BF16 or ATTN_F16: logically [B][H][S][d] with the strides (in
  *          elements, >= 0) of batch, head and token; channels are contiguous.
  *          `out` may be `in` with the same strides; otherwise no output may
- *          overlap an input or the other output.  Outputs must not overlap
- *          themselves.
+ *          overlap an input (the positions and the angles too), the other output
+ *          or itself: refused, but that strides with no order in common are tested
+ *          for a few thousand combinations only.
  *   interleaved  0: pairs (i, i + width / 2); 1: pairs (2i, 2i + 1)
  *   turns  [width / 2] theta_i / (2 pi) as a 64-bit fraction of a turn per
  *          position (rounded theta_i / (2 pi) * 2^64, modulo 2^64)
  *   pos    int32: [B][S] if pos_per_token, else [B], the position of each
  *          sequence's first row, the others following; any values (they wrap
  *          at 32 bits)
- *   width  even, 2 .. d;  d even, <= 1024;  H <= 65536
+ *   width  even, 2 .. d;  d even, <= 1024;  H <= 65536;  B * S < 2^31
  * fp32 arithmetic on the rows; the angle's error does not grow with the
  * position beyond 2^-64 turns of each.  One kernel.
  */

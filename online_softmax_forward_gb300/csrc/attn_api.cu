@@ -483,6 +483,103 @@ static bool heads_ok(const attn_heads &w, int B, int S, int d, size_t elem) {
     return w.in != w.out || same;
 }
 
+// Rows of `row` bytes at base + sum of stride * index.
+struct RowSet {
+    const void *base;
+    int64_t row;
+    int64_t size[3], stride[3];  // stride in bytes
+};
+static RowSet row_set(const void *base, const int64_t *stride, int B, int H, int S, int d, size_t elem) {
+    RowSet r{base, (int64_t)(d * elem), {B, H, S}, {}};
+    for (int i = 0; i < 3; ++i) r.stride[i] = r.size[i] > 1 ? stride[i] : 0;
+    for (int i = 0; i < 3; ++i) r.stride[i] *= (int64_t)elem;  // fits: heads_ok
+    return r;
+}
+
+// Do two sets of rows share a byte?  Their rows do where the difference of two rows' starts,
+// base + sum over both sets' dimensions of stride * index, is smaller than the row that comes
+// first.  Dimensions of one stride are one of both; the widest is tried first, and of its
+// indices only those that the others can make up for: for the views of one packed tensor two
+// at most.  Strides that fit nothing may leave more; after kTries the sets count as apart.
+struct Reach {
+    static constexpr int kTries = 4096;
+    typedef __int128 i128;
+    i128 stride[6], first[6], last[6], least[7], most[7];  // least, most: of the sums from a term on
+    int n = 0, tries = kTries;
+
+    void add(const RowSet &r, int sign) {
+        for (int i = 0; i < 3; ++i) {
+            const int64_t s = r.stride[i], top = r.size[i] - 1;
+            if (s == 0 || top <= 0) continue;
+            int j = 0;
+            while (j < n && stride[j] > s) ++j;
+            if (j == n || stride[j] != s) {
+                for (int m = n; m > j; --m) {
+                    stride[m] = stride[m - 1];
+                    first[m] = first[m - 1];
+                    last[m] = last[m - 1];
+                }
+                stride[j] = s;
+                first[j] = last[j] = 0;
+                ++n;
+            }
+            (sign > 0 ? last[j] : first[j]) += sign * top;
+        }
+    }
+    void sums() {
+        least[n] = most[n] = 0;
+        for (int i = n - 1; i >= 0; --i) {
+            least[i] = least[i + 1] + stride[i] * first[i];
+            most[i] = most[i + 1] + stride[i] * last[i];
+        }
+    }
+    // is there a sum of the terms from k on in [lo, hi]?
+    bool hits(int k, i128 lo, i128 hi) {
+        if (most[k] < lo || least[k] > hi) return false;
+        if (least[k] >= lo || most[k] <= hi) return true;
+        i128 a = lo - most[k + 1], b = hi - least[k + 1];  // k < n: both sums of no term are 0
+        a = a > 0 ? (a + stride[k] - 1) / stride[k] : -(-a / stride[k]);
+        b = b >= 0 ? b / stride[k] : -((-b + stride[k] - 1) / stride[k]);
+        if (a < first[k]) a = first[k];
+        if (b > last[k]) b = last[k];
+        for (i128 t = a; t <= b; ++t) {
+            if (--tries < 0) return false;
+            if (hits(k + 1, lo - stride[k] * t, hi - stride[k] * t)) return true;
+        }
+        return false;
+    }
+};
+static bool share_bytes(const RowSet &a, const RowSet &b) {
+    Reach r;
+    r.add(a, 1);
+    r.add(b, -1);
+    r.sums();
+    const __int128 apart = (__int128)(uintptr_t)b.base - (__int128)(uintptr_t)a.base;
+    return r.hits(0, apart - a.row + 1, apart + b.row - 1);
+}
+
+// No output of attn_rotary overlaps an input, the angles, the positions or the other output;
+// but rows may be turned where they are (heads_ok).
+static bool rotary_apart(const attn_heads *const (&w)[2], const uint64_t *turns, int width, const int32_t *pos,
+                         int pos_per_token, int B, int S, int d, size_t elem) {
+    const RowSet arrays[2] = {{turns, (int64_t)width / 2 * 8, {1, 1, 1}, {}},
+                              {pos, (int64_t)B * (pos_per_token ? S : 1) * 4, {1, 1, 1}, {}}};
+    for (int i = 0; i < 2; ++i) {
+        if (!w[i] || w[i]->H == 0) continue;
+        const RowSet out = row_set(w[i]->out, w[i]->out_stride, B, w[i]->H, S, d, elem);
+        for (const RowSet &a : arrays)
+            if (share_bytes(out, a)) return false;
+        for (int j = 0; j < 2; ++j) {
+            if (!w[j] || w[j]->H == 0) continue;
+            if ((j != i || w[j]->in != w[j]->out) &&
+                share_bytes(out, row_set(w[j]->in, w[j]->in_stride, B, w[j]->H, S, d, elem)))
+                return false;
+            if (j > i && share_bytes(out, row_set(w[j]->out, w[j]->out_stride, B, w[j]->H, S, d, elem))) return false;
+        }
+    }
+    return true;
+}
+
 int attn_rotary(const attn_heads *q, const attn_heads *k, const uint64_t *turns, int width,
                 int interleaved, float amplitude, int transpose, const int32_t *pos,
                 int pos_per_token, int B, int S, int d, int dtype, void *stream) {
@@ -497,6 +594,7 @@ int attn_rotary(const attn_heads *q, const attn_heads *k, const uint64_t *turns,
     if (!heads_ok(*q, B, S, d, elem) || (k && !heads_ok(*k, B, S, d, elem))) return ATTN_ERR_INVALID_ARG;
     if (q->H + (k ? k->H : 0) == 0) return ATTN_OK;
     if (!turns || !aligned(turns, 8) || !pos || !aligned(pos, 4)) return ATTN_ERR_INVALID_ARG;
+    if (!rotary_apart({q, k}, turns, width, pos, pos_per_token, B, S, d, elem)) return ATTN_ERR_INVALID_ARG;
     const int st = check_device();
     if (st != ATTN_OK) return st;
     return launch_rotary(*q, k, turns, width, interleaved != 0, amplitude, transpose != 0, pos,

@@ -250,3 +250,106 @@ def test_binding_torch_is_seen_whole(monkeypatch):
     binding.join()
     assert early is None
     assert all(getattr(pkg, name) is not None for name in names) and len(pkg._codes) == 5
+
+
+def many(in_, out, H, row=64, **kw):
+    """Heads of a packed [B][S][14 heads][64] tensor, in and out."""
+    packed = (10 * 14 * 64, 64, 14 * 64)
+    return heads(in_, out, H, in_stride=packed, out_stride=packed)
+
+
+HEAD = 64 * 2  # bytes of a bf16 head
+ROWS = 2 * 4 * 10 * 64 * 2  # of the default tensor
+
+
+@pytest.mark.parametrize("kw", [
+    # one output, two tensors
+    dict(q=heads(out=O), k=heads(K, O)),
+    dict(q=heads(out=O), k=heads(K, O + ROWS - HEAD)),
+    dict(q=heads(out=O), k=heads(K, O - ROWS + HEAD)),
+    # packed rows: the other's heads begin one too early, or lie where the next token's do
+    dict(q=many(Q, O, 8), k=many(Q + 8 * HEAD, O + 7 * HEAD, 4)),
+    dict(q=many(Q, O, 8), k=many(Q + 8 * HEAD, O + 11 * HEAD, 4)),
+    dict(q=many(Q, O, 8), k=many(Q + 8 * HEAD, O + 8 * HEAD - 2, 4)),
+    # an output over the other tensor's input, or over its own elsewhere
+    dict(q=many(Q, Q + 8 * HEAD, 8), k=many(Q + 8 * HEAD, O, 4)),
+    dict(q=heads(out=K), k=heads(K, V)),
+    dict(q=heads(out=O), k=heads(K, Q)),
+    dict(q=heads(out=Q + HEAD)),
+    dict(q=many(Q, Q + 2 * HEAD, 8)),
+    # contiguous rows over packed ones, either way
+    dict(q=many(Q, Q, 8), k=heads(K, Q + 64 * HEAD)),
+    dict(q=heads(out=Q + HEAD, in_stride=(10 * 14 * 64, 64, 14 * 64))),
+    # other strides in the same place: every second head of one, every third of the other
+    dict(q=heads(out=O, out_stride=(10 * 64 * 64, 2 * 64, 64 * 64)),
+         k=heads(K, O, out_stride=(10 * 64 * 64, 3 * 64, 64 * 64))),
+    # a broadcast input under an output
+    dict(q=heads(out=O), k=heads(O + ROWS // 2, V, in_stride=(0, 0, 0))),
+    # the positions and the angles
+    dict(q=heads(out=W)), dict(q=heads(out=W - ROWS + HEAD)), dict(q=heads(out=L)), dict(q=heads(), k=heads(K, W)),
+], ids=str)
+def test_rotary_refuses_overlap(kw):
+    assert rot(**kw) == pkg.ATTN_ERR_INVALID_ARG
+
+
+def test_rotary_accepts_neighbours():
+    """Outputs and inputs that share a buffer and no element of it."""
+    if not _no_gpu():
+        pytest.skip("valid calls with made-up addresses would launch on this host")
+    ok = pkg.ATTN_ERR_UNSUPPORTED_DEVICE
+    for kw in (
+        dict(q=heads(out=O), k=heads(K, O + ROWS)), dict(q=heads(out=O), k=heads(K, O - ROWS)),
+        dict(q=many(Q, O, 8), k=many(Q + 8 * HEAD, O + 8 * HEAD, 4)),
+        dict(q=many(Q, Q, 8), k=many(Q + 8 * HEAD, Q + 8 * HEAD, 4)),        # in place
+        dict(q=many(Q, Q + 8 * HEAD, 4), k=many(Q, Q + 12 * HEAD, 2)),       # one input for both
+        dict(q=many(Q, O, 8), k=many(Q + 8 * HEAD, O + 10 * HEAD, 4)),
+        dict(q=heads(out=O, out_stride=(10 * 64 * 64, 2 * 64, 64 * 64)),     # even and odd heads
+             k=heads(K, O + HEAD, out_stride=(10 * 64 * 64, 4 * 64, 64 * 64))),
+        dict(q=heads(out=Q, H=1, in_stride=(640, 1, 64), out_stride=(640, 9, 64))),  # one head: its stride does not matter
+        dict(q=heads(), k=heads(Q, V)),
+        dict(q=heads(), k=heads(V, K, in_stride=(0, 0, 0))),
+        dict(q=heads(out=W + 80)), dict(q=heads(out=W - ROWS)), dict(q=heads(out=L + 256)),
+    ):
+        assert rot(**kw) == ok, kw
+    assert rot(q=heads(out=O), k=heads(K, O, H=0)) == ok
+    assert rot(q=heads(out=W + 8), per_token=0) == ok  # two positions
+
+
+def test_rotary_overlap_of_random_layouts():
+    """The answer is that of the elements counted one by one."""
+    if not _no_gpu():
+        pytest.skip("valid calls with made-up addresses would launch on this host")
+    import itertools
+    import random
+    r = random.Random(7)
+    B, S, d, answers = 2, 3, 4, []
+    base = 3 * GB
+
+    def layout(H, nested):
+        """Strides of the dimensions in some order, each at least the span of those inside it."""
+        strides, span = [0, 0, 0], d
+        for i in r.sample(range(3), 3):
+            strides[i] = span + r.choice([0, 0, 0, 1, 4, 8, 20]) if nested else r.choice([0, 1, 4, 8, 12, 24, 40])
+            span = strides[i] * ((B, H, S)[i] - 1) + span
+        return tuple(strides)
+
+    def elements(start, H, strides):
+        return {start + b * strides[0] + h * strides[1] + s * strides[2] + c
+                for b, h, s, c in itertools.product(range(B), range(H), range(S), range(d))}
+
+    for _ in range(3000):
+        Hq, Hk = r.randint(1, 4), r.randint(1, 3)
+        strides = [layout(Hq, False), layout(Hq, True), layout(Hk, False), layout(Hk, True)]
+        if r.random() < 0.5:
+            strides[1] = strides[3] = layout(max(Hq, Hk), True)  # views of one packed tensor
+        starts = [r.randint(0, 30), r.randint(100, 400), r.randint(0, 500), r.randint(0, 400)]
+        qi, qo, ki, ko = (elements(s, H, t) for s, H, t in zip(starts, (Hq, Hq, Hk, Hk), strides))
+        if len(qo) < Hq * B * S * d or len(ko) < Hk * B * S * d:
+            continue
+        free = not (qo & (qi | ki | ko) or ko & (qi | ki))
+        at = [base + 2 * s for s in starts]
+        got = rot(q=heads(at[0], at[1], Hq, strides[0], strides[1]), k=heads(at[2], at[3], Hk, strides[2], strides[3]),
+                  width=d, d=d, B=B, S=S)
+        assert got == (pkg.ATTN_ERR_UNSUPPORTED_DEVICE if free else pkg.ATTN_ERR_INVALID_ARG), (starts, strides, Hq, Hk)
+        answers.append(free)
+    assert 200 < sum(answers) < len(answers) - 200
