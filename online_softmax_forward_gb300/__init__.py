@@ -423,6 +423,16 @@ def _check_out(t, shape, dtype, dev, name):
         raise ValueError("%s must be on %s" % (name, dev))
 
 
+def _no_graph(name, *tensors):
+    """Says that autograd will not see what it would be expected to; ``name`` is the caller's."""
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            if _torch.is_grad_enabled():
+                warnings.warn("%s records no gradient for tensors that require one: attention_bwd and rotary(..., "
+                              "transpose=True) compute them; call it under torch.no_grad()" % name, stacklevel=3)
+            return
+
+
 def attention(q, k, v, causal: bool = False, scale: float | None = None, out_dtype=None,
               return_lse: bool = True, out=None, lse=None, stream=None):
     """O (and LSE) for contiguous CUDA tensors q [B,H,Sq,d], k/v [B,H,Skv,d]
@@ -431,7 +441,8 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out_dty
 
     ``out_dtype`` = torch.float32 with bf16/fp16 inputs selects the fp32-output
     variant.  Outputs are allocated with torch unless ``out`` / ``lse`` are
-    given; those of a call that names a ``stream`` belong to that stream."""
+    given; those of a call that names a ``stream`` belong to that stream.
+    Nothing is recorded for autograd (``attention_bwd`` has the gradients)."""
     if _torch is None:
         import torch
         _bind(torch)
@@ -441,6 +452,7 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, out_dty
     code = dtype_code(dtype, out_dtype)
     if k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("q, k, v must share a dtype")
+    _no_graph("attention", q, k, v)
     odt = dtype if out_dtype is None else out_dtype
     handle = _handle(dev, stream)
     if out is not None:
@@ -472,7 +484,8 @@ def attention_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None
     q, do [B,H,Sq,d] and k, v [B,H_kv,Skv,d] share a dtype; the gradients have o's dtype (fp32 if
     the forward pass ran with ``out_dtype`` = torch.float32).  They are allocated with torch unless
     ``out`` = (dq, dk, dv) is given; the workspace (attn_bwd_workspace_size) belongs to the call, or is
-    one that this thread keeps for the stream where ``out`` is given and the call is not captured."""
+    one that this thread keeps for the stream where ``out`` is given and the call is not captured.
+    Nothing is recorded for autograd."""
     if _torch is None:
         import torch
         _bind(torch)
@@ -503,6 +516,7 @@ def attention_bwd(q, k, v, o, lse, do, causal: bool = False, scale: float | None
     _check_out(lse, rows, _float32, dev, "lse")
     if dlse is not None:
         _check_out(dlse, rows, _float32, dev, "dlse")
+    _no_graph("attention_bwd", q, k, v, o, lse, do, dlse)
     handle = _handle(dev, stream)
     if out is not None:
         dq, dk, dv = out
@@ -700,7 +714,8 @@ def rotary(q, k, rot, pos, transpose: bool = False, out=None, stream=None):
     sequence's first row.  q and k may be views of any strides with contiguous channels, for example
     of a projection's [B,S,H,d].  ``transpose`` gives the gradient in q and k from the one in the
     results.  New results are contiguous [B,H,S,d], as ``attention`` and ``cache_append`` take them;
-    ``out`` = (q', k') writes to other places, which may be q and k themselves.  Returns (q', k')."""
+    ``out`` = (q', k') writes to other places, which may be q and k themselves.  Returns (q', k').
+    Nothing is recorded for autograd."""
     if out is None and stream is None:
         r = _fast().rotary(q, k, pos, transpose, *rot._args)
         if type(r) is tuple:
@@ -724,6 +739,7 @@ def rotary(q, k, rot, pos, transpose: bool = False, out=None, stream=None):
         if k.dtype is not dtype or k.device != dev or len(kshape) != 4 or kshape[0] != B or \
                 kshape[2] != S or kshape[3] != d:
             raise ValueError("k must be [%d, H_kv, %d, %d] of q's dtype and device" % (B, S, d))
+    _no_graph("rotary", q, k)
     per_token = pos.dim() == 2
     p = _int32_on(pos, (B, S) if per_token else (B,), dev, "pos")
     handle = _handle(dev, stream)

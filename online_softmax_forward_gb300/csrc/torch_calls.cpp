@@ -5,7 +5,8 @@
 // rotary positions takes 13.8 us for a kernel of 2.7: 5.9 for two allocations between
 // other work, 1.4 for the foreign-function interface, 4 for checks.  Here the checks that
 // an ordinary call passes are made on the tensors themselves.  What does not pass them (an
-// error, a tensor on a device that is not the current one, a subclass of Tensor) is
+// error, a tensor on a device that is not the current one, a subclass of Tensor, one whose
+// gradient autograd would record) is
 // answered with None, and the wrapper goes its own way, which says what is wrong.
 //
 // bind(address of attn_rotary, of attn_bwd_workspace_size, of attn_bwd): first, once; the
@@ -19,6 +20,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <limits.h>
@@ -41,6 +43,8 @@ struct WithoutGil {  // allocations and launches may wait; other threads run mea
 };
 
 const at::Tensor *tensor(PyObject *x) { return THPVariable_CheckExact(x) ? &THPVariable_Unpack(x) : nullptr; }
+
+bool recorded(const at::Tensor *t) { return t && t->requires_grad() && c10::GradMode::is_enabled(); }
 
 bool whole(const at::Tensor &t, at::ScalarType type, c10::Device dev) {
     return t.scalar_type() == type && t.device() == dev && t.is_contiguous();
@@ -92,7 +96,9 @@ PyObject *rotary(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (n != 9 || !call_rotary) Py_RETURN_NONE;
     const at::Tensor *q = tensor(args[0]), *k = args[1] == Py_None ? nullptr : tensor(args[1]), *pos = tensor(args[2]);
-    if (!q || !pos || (!k && args[1] != Py_None) || q->dim() != 4 || !q->is_cuda()) Py_RETURN_NONE;
+    if (!q || !pos || (!k && args[1] != Py_None) || q->dim() != 4 || !q->is_cuda() ||
+        recorded(q) || recorded(k))
+        Py_RETURN_NONE;
     const c10::Device dev = q->device();
     const int64_t B = q->size(0), S = q->size(2), d = q->size(3);
     const int code = type_code(q->scalar_type(), q->scalar_type());
@@ -133,7 +139,7 @@ PyObject *attention_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const at::Tensor *t[7];  // q, k, v, o, lse, do, dlse
     for (int i = 0; i < 7; ++i) {
         t[i] = args[i] == Py_None && i == 6 ? nullptr : tensor(args[i]);
-        if (!t[i] && !(args[i] == Py_None && i == 6)) Py_RETURN_NONE;
+        if ((!t[i] && !(args[i] == Py_None && i == 6)) || recorded(t[i])) Py_RETURN_NONE;
     }
     const at::Tensor &q = *t[0], &k = *t[1], &v = *t[2], &o = *t[3], &lse = *t[4], &dout = *t[5];
     if (q.dim() != 4 || k.dim() != 4 || !q.is_cuda()) Py_RETURN_NONE;
