@@ -15,14 +15,14 @@ bool bwd_plan(const Problem &call, BwdPlan *plan) {
     Problem p = call;
     plan->off = call.Skv - call.Sq;
     plan->wrap = 0;
-    if (p.group > 1 && (!p.causal || (p.Sq <= kStatTile && plan->off >= 0)) && (int64_t)p.group * p.Sq <= INT32_MAX - kStatTile) {
+    if (p.group > 1 && (!p.causal || (p.Sq <= kStatTile && plan->off >= 0)) && (int64_t)p.group * p.Sq <= kMaxBwdRows) {
         p.H /= p.group;
         p.Sq *= p.group;
         p.group = 1;
         if (p.causal) plan->wrap = call.Sq;
     }
     plan->p = p;
-    if (p.Sq > INT32_MAX - 1024 || p.Skv > INT32_MAX - 1024) return false;  // ends of tiles fit 31 bits
+    if (p.Sq > kMaxBwdRows || p.Skv > kMaxBwdRows) return false;
     const bool f32 = p.dtype == ATTN_F32, f16 = p.dtype == ATTN_F16 || p.dtype == ATTN_F16_OUT_F32;
     const int64_t bh = p.bh(), bhk = p.bh_kv();
     // the sizes below are products of these; anything near 2^62 bytes is refused first

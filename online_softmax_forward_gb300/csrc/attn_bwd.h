@@ -46,6 +46,7 @@ namespace attn {
 constexpr int kStatTile = 128;   // query rows of one block of row statistics
 constexpr int kBwdSms = 152;     // the splits are planned for this many SMs
 constexpr int kMaxBwdSplits = 64;
+constexpr int kMaxBwdRows = INT32_MAX - 1023;  // of a head: ends of tiles fit 31 bits
 constexpr int kFewKeys = 128;    // see BwdPlan::few
 constexpr int kBwdP16Log2 = 14;  // fp16: P is kept times 2^14, so that small weights stay normal numbers
 constexpr int kPreBlocks = 1216; // CTAs of the first kernel at most

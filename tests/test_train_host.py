@@ -353,3 +353,16 @@ def test_rotary_overlap_of_random_layouts():
         assert got == (pkg.ATTN_ERR_UNSUPPORTED_DEVICE if free else pkg.ATTN_ERR_INVALID_ARG), (starts, strides, Hq, Hk)
         answers.append(free)
     assert 200 < sum(answers) < len(answers) - 200
+
+
+def test_bwd_takes_the_lengths_it_documents():
+    """Sq and Skv up to 2^31 - 1024, and shared heads whose rows together pass that."""
+    top = 2 ** 31 - 1024
+    size = lambda **kw: pkg.attn_bwd_workspace_size(*{**dict(B=1, H=1, H_kv=1, Sq=8, Skv=8, d=16, causal=0,  # noqa: E731
+                                                             dtype=pkg.ATTN_F32), **kw}.values())[0]
+    for kw in (dict(Sq=top), dict(Skv=top), dict(Sq=top, Skv=top, H=2, H_kv=2), dict(Sq=top, d=128, dtype=pkg.ATTN_BF16),
+               dict(Skv=top, d=64, dtype=pkg.ATTN_F16, causal=1), dict(H=4, Sq=2 ** 29 - 256), dict(H=4, Sq=2 ** 29 - 200),
+               dict(H=4, Sq=2 ** 29 - 33), dict(H=4, Sq=2 ** 29)):
+        assert size(**kw) == pkg.ATTN_OK, kw
+    for kw in (dict(Sq=top + 1), dict(Skv=top + 1), dict(H=4, Sq=top + 1)):
+        assert size(**kw) == pkg.ATTN_ERR_INVALID_ARG, kw
