@@ -23,8 +23,9 @@
 //    order of the summed rows, so Y's rows are read in that order.
 //  * The tensor cores' sums round towards zero.  T adds its large products (hi hi)
 //    apart from the small ones, 64 channels at a time (one sum over 128: error 1.06e-6 in
-//    place of 0.85e-6, 186 us in place of 190), and A's sums of a step start at zero and are
-//    added to the unit's in fp32, so that no sum takes more than 12 such roundings.
+//    place of 0.85e-6, 186 us in place of 190): 8 such roundings at most; the small ones' sum
+//    takes 2 for each 8 channels, of numbers 2^-11 as large.  A's sums of a step start at
+//    zero and are added to the unit's in fp32: 12 roundings at most.
 //  * The next step's tiles are copied while this one's are multiplied (two stages).
 //  * The row statistics are computed where do has come (o is read once more for
 //    each kv unit, which costs less than a kernel of its own), so that a small
