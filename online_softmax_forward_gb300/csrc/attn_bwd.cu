@@ -224,15 +224,21 @@ __global__ void __launch_bounds__(kPreThreads) bwd_stats_kernel(const PreParams 
             } else {
                 const int64_t tile = item - p.tiles, slice = tile / p.v_tiles_per_head;
                 const int row0 = (int)(tile - slice * p.v_tiles_per_head) * kStatTile;
-#pragma unroll 4
-                for (int i = warp * R + rw; i < kStatTile; i += kWarps * R) {
-                    float sq = 0.f;
-                    if (row0 + i < p.Skv) {
-                        const auto x = *reinterpret_cast<const Row<TD, E> *>(
-                            (const TD *)p.v + ((size_t)slice * p.Skv + row0 + i) * D + sub * E);
+                constexpr int kTimes = kStatTile / (kWarps * R);
+                Row<TD, E> x[kTimes];
 #pragma unroll
-                        for (int e = 0; e < E; ++e) sq = fmaf(to_f(x.e[e]), to_f(x.e[e]), sq);
-                    }
+                for (int i = 0; i < kTimes; ++i) {
+                    const int row = row0 + (i * kWarps + warp) * R + rw;
+                    *reinterpret_cast<uint4 *>(&x[i]) = make_uint4(0, 0, 0, 0);
+                    if (row < p.Skv)
+                        *reinterpret_cast<uint4 *>(&x[i]) = *reinterpret_cast<const uint4 *>(
+                            (const TD *)p.v + ((size_t)slice * p.Skv + row) * D + sub * E);
+                }
+#pragma unroll
+                for (int i = 0; i < kTimes; ++i) {
+                    float sq = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sq = fmaf(to_f(x[i].e[e]), to_f(x[i].e[e]), sq);
 #pragma unroll
                     for (int s = L / 2; s > 0; s >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, s);
                     if (sq < INFINITY) big_do = fmaxf(big_do, sqrtf(sq));
@@ -305,11 +311,8 @@ int launch_stats(const PreParams &p, cudaStream_t stream) {
     constexpr int R = 32 / (D * (int)sizeof(TD) / 16);
     const int64_t warps = p.tiles * (kStatTile / R / 4);
     int64_t grid = kScale ? p.tiles + p.v_tiles : (warps + kPreThreads / 32 - 1) / (kPreThreads / 32);
-    if (kScale && grid > kPreBlocks) {  // equal shares of whole tiles
-        const int64_t rounds = (grid + kPreBlocks - 1) / kPreBlocks;
-        grid = (grid + rounds - 1) / rounds;
-    }
-    if (grid > kPreBlocks) grid = kPreBlocks;
+    const int64_t most = kScale ? 1 << 20 : kPreBlocks;
+    if (grid > most) grid = most;
     bwd_stats_kernel<TD, TO, D, kScale><<<(unsigned)grid, kPreThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }

@@ -49,7 +49,7 @@ constexpr int kMaxBwdSplits = 64;
 constexpr int kMaxBwdRows = INT32_MAX - 1023;  // of a head: ends of tiles fit 31 bits
 constexpr int kFewKeys = 128;    // see BwdPlan::few
 constexpr int kBwdP16Log2 = 14;  // fp16: P is kept times 2^14, so that small weights stay normal numbers
-constexpr int kPreBlocks = 1216; // CTAs of the first kernel at most
+constexpr int kPreBlocks = 1216; // CTAs of the first kernel at most (bf16)
 constexpr size_t kMaximaBytes = 3 * kPreBlocks * 4;
 constexpr int kScaleRows = 3;    // fp16: numbers of a query row that the first kernel writes (bf16: 2)
 
