@@ -40,11 +40,11 @@
 //  * Every mbarrier wait is bounded, as in the forward kernel.
 //
 // What bounds it: at D = 128 and long walks the tensor cores.  32 heads of 8192
-// tokens, causal, take 1092 us: the seven products of whole tiles run at 1.79
-// PFLOP/s, near the rate that cuBLAS reaches on this GPU (the tensor pipe is busy
-// 79 % of the clocks), 1.26 PFLOP/s of the five that a backward pass cannot do
-// without.  (1063 us with kTwo = 0: the issuing warp's test stands between a wait and
-// the product that others wait for.)  A step takes 2740 (kv) and 2060 (q) clocks in
+// tokens, causal, take 1053 us alone (tensor pipe busy 80 % of the clocks) and 1073 to
+// 1098 us in a replayed graph with the row statistics: the seven products of whole tiles
+// run at 1.78 to 1.86 PFLOP/s, near the rate that cuBLAS reaches on this GPU, 1.26 PFLOP/s
+// of the five that a backward pass cannot do without.  (2.5 % less with kTwo = 0: the
+// issuing warp's test stands between a wait and the product that others wait for.)  A step takes 2740 (kv) and 2060 (q) clocks in
 // long walks, a unit's start and end about 4000 more, which is what 2 x 4001
 // tokens (635 us, 1.03 PFLOP/s) and shorter calls lose.  At D = 64 the
 // chain of exponentials and conversions is longer than the products: 1840 and 1400
