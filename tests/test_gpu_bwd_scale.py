@@ -112,3 +112,41 @@ def test_large_walks_and_splits(dt_o):
     x = make(2, 2, 2, 5, 9000, 128, torch.tensor([1e-2, 2000.0]).view(1, 2, 1, 1), 6, False)
     x["o"] = x["o"].to(dt_o)
     check(x, False)
+
+
+def test_replays_go_by_what_they_are_given():
+    """Captured with small gradients, replayed with large ones in another head."""
+    names = ("q", "k", "v", "o", "lse", "do")
+    first, second = (make(2, 4, 2, 150, 700, 64, torch.tensor(s).view(1, 4, 1, 1), 8 + i, True)
+                     for i, s in enumerate(((1e-3, 1e-3, 1e-5, 1e-5), (0.1, 0.1, 3000.0, 3000.0))))
+    held = {n: first[n].cuda() for n in names}
+    g = torch.cuda.CUDAGraph()
+    pkg.attention_bwd(*(held[n] for n in names), causal=True)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        got = pkg.attention_bwd(*(held[n] for n in names), causal=True)
+    for x in (second, first, second):
+        for n in names:
+            held[n].copy_(x[n])
+        g.replay()
+        want = call(x, True)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("c", SHAPES, ids=str)
+def test_bounds_checking_build(c):
+    B, H, Hkv, Sq, Skv, d, causal = c
+    x = make(B, H, Hkv, Sq, Skv, d, torch.tensor([1e-3, 100.0]).repeat(H)[:H].view(1, H, 1, 1), 9, causal)
+    want = call(x, causal)
+    y = {n: t.cuda() for n, t in x.items()}
+    lib, code = pkg.load_checked_library(), pkg.dtype_code(HF, F)
+    out = [torch.full(y[n].shape, 7.0, device="cuda") for n in "qkv"]
+    st, need = pkg.attn_bwd_workspace_size(B, H, Hkv, Sq, Skv, d, causal, code)
+    ws = torch.full((need + 64,), 9, dtype=torch.uint8, device="cuda")
+    st = lib.attn_bwd(*(y[n].data_ptr() for n in ("q", "k", "v", "o", "lse", "do")), None,
+                      *(t.data_ptr() for t in out), B, H, Hkv, Sq, Skv, d, int(causal), 0.0, code,
+                      ws.data_ptr() + 32, need, None)
+    assert st == pkg.ATTN_OK and lib.attn_check_status(None) == pkg.ATTN_OK
+    assert all(torch.equal(a.cpu(), b) for a, b in zip(out, want))
+    assert (ws[:32] == 9).all() and (ws[-32:] == 9).all()

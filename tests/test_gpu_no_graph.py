@@ -1,4 +1,5 @@
-"""The wrappers record nothing for autograd, and say so where it would be missed."""
+"""The wrappers record nothing for autograd, and say so where it would be missed; they give the same bits
+without their host side in C++."""
 import warnings
 
 import pytest
@@ -43,3 +44,13 @@ def test_a_gradient_that_is_not_recorded_is_announced(name):
                 again = call(**{arg: leaf})
             call(**{arg: leaf.detach()})
         assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(want, got, again))
+
+
+@pytest.mark.parametrize("name", ["attention_bwd", "rotary"])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=str)
+def test_without_their_host_side_in_c(name, dt, monkeypatch):
+    """The wrappers' Python code alone, as where _torch_calls.so was not built: the same bits."""
+    call = calls(dt)[0][name][0]
+    want = call()
+    monkeypatch.setattr(pkg, "_calls", pkg._NoCalls)
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
