@@ -164,12 +164,11 @@ ATTN_API int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, 
  * Skv <= 128, to twice as many bits).  fp16: after scaling by powers of two, P by
  * one for all, dS by one for each row of dq and one for each 128 rows of dk, from
  * the norms of what makes it, so that heads and sequences of very different do
- * share a call without loss; in a row of dk, terms whose P |do| is less than
- * 2^-27 of the largest |do| of the same kv head lose bits.  fp32: each product
- * of two numbers is wrong by 2^-21 of itself at most; numbers from 2^128 - 2^116 on
- * count as infinite, and what numbers below 2^-112 hold beyond their first 11 bits
- * may be lost.  Sums are made in a fixed
- * order: equal calls give equal bits.
+ * share a call without loss; terms P (|do| |v| + |D|) of one sum that are less than
+ * 2^-27 of the largest |do| |v| + |D| among the 128-row tiles it goes over lose bits.
+ * fp32: each product of two numbers is wrong by 2^-21 of itself at most; numbers from
+ * 2^128 - 2^116 on count as infinite, and what numbers below 2^-112 hold beyond their
+ * first 11 bits may be lost.  Sums are made in a fixed order: equal calls give equal bits.
  * All arrays must be distinct; q, k, v, o, do and gradients 16-byte aligned.
  * Sq and Skv <= 2^31 - 1024.  CUDA graphs: as attn_fwd, without its limit on
  * launches in flight.

@@ -28,7 +28,8 @@
 // do, which a loss scale or its absence, and the weight of a sequence or a token in the
 // loss, move by orders of magnitude.  |dS| <= |do| |v| + |D|, so norms of the rows give a
 // power of two that brings dS to 2^14 at most; it has to be one for all terms of a sum:
-//     dq: one for each query row, from its |do| and |D| and the largest |v| of its kv head;
+//     dq: one for each query row, from its |do| and |D| and the largest |v| of the key tiles
+//         its unit walks over;
 //     dk: one for each kv unit, from the largest |do| and |D| of the query tiles it walks
 //         over and the largest |v| of its keys.
 // So no head's precision depends on another's do.  The first kernel writes |do| of each row

@@ -816,7 +816,10 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     v = p.max_v[(size_t)w.zx * p.nk + w.x0 / kRows];
                 } else {
-                    for (int i = lane; i < p.nk; i += 32) v = fmaxf(v, p.max_v[(size_t)w.zy * p.nk + i]);
+                    for (int i = lane; i < w.n; i += 32) {
+                        if (!in_bounds(w.zy < p.BHk && w.y + i < p.nk, p.status)) break;
+                        v = fmaxf(v, p.max_v[(size_t)w.zy * p.nk + w.y + i]);
+                    }
                 }
                 for (int m = 16; m > 0; m >>= 1) {
                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));

@@ -150,3 +150,20 @@ def test_bounds_checking_build(c):
     assert st == pkg.ATTN_OK and lib.attn_check_status(None) == pkg.ATTN_OK
     assert all(torch.equal(a.cpu(), b) for a, b in zip(out, want))
     assert (ws[:32] == 9).all() and (ws[-32:] == 9).all()
+
+
+@pytest.mark.parametrize("B,H,Hkv,S,d", [(1, 2, 2, 700, 64), (2, 4, 2, 520, 128)])
+def test_keys_that_are_not_seen_do_not_count(B, H, Hkv, S, d):
+    """Large values behind a row, in tiles its walk leaves out, cost its dq no precision."""
+    x = make(B, H, Hkv, S, S, d, torch.full((1, 1, 1, 1), 1e-2), 11, True)
+    x["v"][:, :, 512:] = 6e4
+    o, lse = forward64(x["q"], x["k"], x["v"], True)
+    x["o"] = o.float()
+    dq = call(x, True)[0][:, :, :512]
+    seen = {n: t[:, :, :512] for n, t in x.items()}
+    for b in range(B):
+        for h in range(H):
+            one = {n: t[b:b + 1, h * Hkv // H:h * Hkv // H + 1] if n in "kv" else t[b:b + 1, h:h + 1]
+                   for n, t in seen.items()}
+            want, errors = backward64(**one, causal=True)
+            assert_gradients([dq[b:b + 1, h:h + 1]], want[:1], errors[:1], ("dq",))
