@@ -55,7 +55,7 @@ bool bwd_plan(const Problem &call, BwdPlan *plan) {
     // there are no more keys in all, P is in two parts too (2 heads of 128 keys 7.0 us in
     // any form; 1024 heads of 100 keys 43.6 -> 51 us); in the first tile of a causal call that
     // would cost the issuing warp of all steps another test (8192 tokens 5 %).  The rule goes
-    // by positions alone, so that a result does not depend on what else is in the batch.
+    // by positions alone, so that no row's precision depends on what else is in the batch.
     plan->few = 0;
     if (p.Skv <= kFewKeys) plan->few = plan->nq;
     else if (plan->wrap) plan->few = plan->off < kFewKeys ? plan->nq : 0;  // every tile may hold a first position
